@@ -105,6 +105,9 @@ typedef enum snack_status {
 
 typedef enum snack_dtype { SNACK_F32 = 0, SNACK_BF16 = 1 } snack_dtype;
 
+/* Type of token ids and targets. */
+typedef enum snack_index { SNACK_I32 = 0, SNACK_I64 = 1 } snack_index;
+
 /*
  * Sizes of the caller-allocated buffers for a layer.
  *   plan_bytes       persistent plan, alive as long as the handle;
@@ -341,6 +344,59 @@ const char *snack_status_string(snack_status st);
 
 /* SNACK_VERSION of the built library. */
 int snack_version(void);
+
+/*
+ * Operators at the two ends of a language model of sparse layers, and at the
+ * end of its training step.  They take no handle: every size, stride and
+ * buffer is an argument, they run on the CUDA device current at the call (the
+ * stream's), and they keep nothing between calls.  A matrix is row-major with
+ * its rows `ld` >= width elements apart, aligned to its element; 16-byte
+ * aligned rows run fastest.  Workspaces are 256-byte aligned.  Sums are fp32,
+ * each output is rounded once to its type, and results repeat bit for bit.
+ */
+
+/*
+ * Embedding lookup: out[i, :] = scale * table[ids[i], :], for n ids.  An id
+ * outside [0, vocab) (a padding token) gives a row of zeros; no address is
+ * formed from it.  table [vocab, width] and out [n, width] in type t; out must
+ * not overlap the other arguments.  n >= 0; n, vocab < 2^31 - 1.
+ */
+snack_status snack_embed_fwd(const void *ids, snack_index ids_t, int64_t n, const void *table, int64_t table_ld,
+                             int64_t vocab, int32_t width, snack_dtype t, float scale, void *out, int64_t out_ld,
+                             snack_stream_t stream);
+
+/*
+ * The lookup's gradient: dtable[v, :] = scale * sum_{i : ids[i] = v} dout[i, :],
+ * summed in fp32 in the order of i.  With accumulate == 0 every row of dtable
+ * is written (zeros where no id names it); otherwise the sums are added to
+ * dtable (in fp32, then rounded), whose other rows are not touched: a table
+ * shared with the projection to the vocabulary takes its second gradient so.
+ * dtable must not overlap the other arguments.
+ */
+snack_status snack_embed_grad_workspace_size(int64_t n, int64_t vocab, int32_t width, size_t *bytes);
+snack_status snack_embed_grad(const void *ids, snack_index ids_t, int64_t n, const void *dout, int64_t dout_ld,
+                              int64_t vocab, int32_t width, snack_dtype t, float scale, int accumulate, void *dtable,
+                              int64_t dtable_ld, void *ws, size_t ws_bytes, snack_stream_t stream);
+
+/*
+ * Global norm of a model's gradients, and clipping:
+ *   norm   = sqrt(sum over all tensors and elements of g^2)
+ *   out[k] = g[k] * min(1, max_norm / (norm + 1e-6))
+ * grads, outs, numel and types are host arrays of n_tensors entries (read
+ * during the call): device pointers, element counts (0 allowed) and element
+ * types; out[k] has its gradient's type and count, and is the gradient itself
+ * (in place) or overlaps no gradient.  outs may be NULL: only the norm is
+ * computed.  norm (device, fp32) may be NULL.  In place nothing is written
+ * when the factor is 1.  The squares are summed at three scales, so the norm
+ * is right (to fp32) also where squares over- or underflow fp32.  An infinite
+ * norm gives the factor 0 (an infinite element becomes NaN), a NaN norm makes
+ * every output NaN.  0 <= max_norm.
+ */
+snack_status snack_clip_workspace_size(int32_t n_tensors, const int64_t *numel, const snack_dtype *types,
+                                       size_t *bytes);
+snack_status snack_clip_grad_norm(int32_t n_tensors, const void *const *grads, void *const *outs,
+                                  const int64_t *numel, const snack_dtype *types, float max_norm, float *norm,
+                                  void *ws, size_t ws_bytes, snack_stream_t stream);
 
 /*
  * Kernel trace of the calling host thread (a profiling aid).  While a trace

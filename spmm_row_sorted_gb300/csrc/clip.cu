@@ -1,0 +1,354 @@
+// Global gradient norm over many tensors, and clipping.
+//
+//   norm = sqrt(sum g^2),   out = g * min(1, max_norm / (norm + 1e-6))
+//
+// Bound by memory: the norm has to be known before the first output, so the
+// gradients are read twice and written once; the second pass walks the pieces
+// from the last to the first, so that what the first pass read last is still
+// in L2.  The tensors' addresses travel as kernel arguments (no table is laid
+// out on the device).  The work is cut into pieces of kPiece bytes of one
+// tensor, and a block finds a piece's tensor by a search in the pieces' prefix.
+//
+// Each thread adds its squares in fp32; blocks leave their sums in the
+// workspace and every block of the second pass adds them in the same order, in
+// fp64, so no atomics are needed and results repeat.  Squares are summed at
+// three scales (g, 2^-80 g and 2^100 g), which costs arithmetic that hides
+// behind the loads: the plain sum is used unless it left fp32's range.
+#include <stdint.h>
+
+#include "internal.hpp"
+#include "lm.hpp"
+
+namespace snack {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int64_t kPiece = 64 * 1024;  // bytes of one tensor per piece
+constexpr int kBlocksPerSm = 6;
+constexpr float kDown = 8.271806125530277e-25f;   // 2^-80
+constexpr float kUp = 1.2676506002282294e30f;     // 2^100
+constexpr float kTiny = 7.888609052210118e-31f;   // 2^-100
+
+// A launch's tensors, in kernel arguments: at most kMost of them.
+template <int kMost>
+struct ClipTable {
+  const void *in[kMost];
+  void *out[kMost];
+  int64_t n[kMost];          // elements; bf16 tensors as -n - 1
+  uint32_t first[kMost + 1];  // pieces before the tensor
+  int count;
+};
+constexpr int kSmallTable = 16, kMidTable = 128, kBigTable = 768;
+static_assert(sizeof(ClipTable<kBigTable>) < 32000, "kernel arguments hold 32764 bytes");
+
+struct Sum3 {
+  float mid, low, high;  // sums of g^2, (2^-80 g)^2, (2^100 g)^2
+};
+
+__device__ __forceinline__ void add_square(Sum3 &s, float v) {
+  s.mid = fmaf(v, v, s.mid);
+  const float a = v * kDown, b = v * kUp;
+  s.low = fmaf(a, a, s.low);
+  s.high = fmaf(b, b, s.high);
+}
+
+template <int kMost>
+__device__ __forceinline__ int find_tensor(const ClipTable<kMost> &t, uint32_t piece) {
+  int lo = 0, hi = t.count;  // first[lo] <= piece < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (t.first[mid] <= piece)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+template <typename T>
+__device__ __forceinline__ void sum_piece(const T *__restrict__ p, int64_t m, Sum3 &s) {
+  constexpr int kN = 16 / (int)sizeof(T);
+  typedef Pack<T, 16> V;
+  // elements before the first 16-byte boundary, 16-byte accesses, and the rest
+  int64_t lead = (int64_t)((16 - ((uintptr_t)p & 15)) & 15) / (int64_t)sizeof(T);
+  if (lead > m) lead = m;
+  const int64_t vecs = (m - lead) / kN;
+  const uint4 *v = reinterpret_cast<const uint4 *>(p + lead);
+  int64_t i = threadIdx.x;
+  for (; i + 3 * kThreads < vecs; i += 4 * kThreads) {
+    V a[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) a[u].raw = __ldg(v + i + u * kThreads);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int e = 0; e < kN; ++e) add_square(s, a[u].get(e));
+  }
+  for (; i < vecs; i += kThreads) {
+    V a;
+    a.raw = __ldg(v + i);
+#pragma unroll
+    for (int e = 0; e < kN; ++e) add_square(s, a.get(e));
+  }
+  for (int64_t j = threadIdx.x; j < lead; j += kThreads) add_square(s, to_f32(p[j]));
+  for (int64_t j = lead + vecs * kN + threadIdx.x; j < m; j += kThreads) add_square(s, to_f32(p[j]));
+}
+
+__device__ __forceinline__ Sum3 block_sum(Sum3 s) {
+  __shared__ Sum3 part[kThreads / 32];
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    s.mid += __shfl_xor_sync(0xffffffffu, s.mid, d);
+    s.low += __shfl_xor_sync(0xffffffffu, s.low, d);
+    s.high += __shfl_xor_sync(0xffffffffu, s.high, d);
+  }
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+  __syncthreads();
+  Sum3 t = {0.f, 0.f, 0.f};
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    t.mid += part[w].mid;
+    t.low += part[w].low;
+    t.high += part[w].high;
+  }
+  return t;
+}
+
+// sums[base + block] = this block's share of the launch's pieces
+template <int kMost>
+__global__ void __launch_bounds__(kThreads) k_clip_norm(const __grid_constant__ ClipTable<kMost> t, uint32_t pieces,
+                                                        Sum3 *__restrict__ sums) {
+  pdl_wait();
+  Sum3 s = {0.f, 0.f, 0.f};
+  for (uint32_t q = blockIdx.x; q < pieces; q += gridDim.x) {
+    const int k = find_tensor(t, q);
+    const int64_t at = (int64_t)(q - t.first[k]) * kPiece;
+    const int64_t n = t.n[k];
+    if (n >= 0) {
+      const int64_t e = at / 4;
+      sum_piece(reinterpret_cast<const float *>(t.in[k]) + e, min(kPiece / 4, n - e), s);
+    } else {
+      const int64_t e = at / 2;
+      sum_piece(reinterpret_cast<const bf16 *>(t.in[k]) + e, min(kPiece / 2, -n - 1 - e), s);
+    }
+  }
+  const Sum3 b = block_sum(s);
+  if (threadIdx.x == 0) sums[blockIdx.x] = b;
+}
+
+// the norm from all blocks' sums, the same in every block
+__device__ __forceinline__ float total_norm(const Sum3 *__restrict__ sums, int n_sums) {
+  __shared__ double red[3][kThreads / 32];
+  double m = 0, l = 0, h = 0;
+  for (int i = threadIdx.x; i < n_sums; i += kThreads) {
+    m += (double)sums[i].mid;
+    l += (double)sums[i].low;
+    h += (double)sums[i].high;
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    m += __shfl_xor_sync(0xffffffffu, m, d);
+    l += __shfl_xor_sync(0xffffffffu, l, d);
+    h += __shfl_xor_sync(0xffffffffu, h, d);
+  }
+  if ((threadIdx.x & 31) == 0) {
+    red[0][threadIdx.x >> 5] = m;
+    red[1][threadIdx.x >> 5] = l;
+    red[2][threadIdx.x >> 5] = h;
+  }
+  __syncthreads();
+  m = l = h = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    m += red[0][w];
+    l += red[1][w];
+    h += red[2][w];
+  }
+  if (isnan(m)) return (float)m;
+  if (isinf(m)) return (float)(sqrt(l) * 0x1p80);
+  if (m < (double)kTiny) return (float)(sqrt(h) * 0x1p-100);
+  return (float)sqrt(m);
+}
+
+template <typename T>
+__device__ __forceinline__ void scale_piece(const T *p, T *o, int64_t m, float f) {
+  constexpr int kN = 16 / (int)sizeof(T);
+  typedef Pack<T, 16> V;
+  if ((((uintptr_t)p ^ (uintptr_t)o) & 15) == 0) {
+    int64_t lead = (int64_t)((16 - ((uintptr_t)p & 15)) & 15) / (int64_t)sizeof(T);
+    if (lead > m) lead = m;
+    const int64_t vecs = (m - lead) / kN;
+    const uint4 *v = reinterpret_cast<const uint4 *>(p + lead);
+    uint4 *w = reinterpret_cast<uint4 *>(o + lead);
+    int64_t i = threadIdx.x;
+    for (; i + 3 * kThreads < vecs; i += 4 * kThreads) {
+      V a[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) a[u].raw = __ldcs(v + i + u * kThreads);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+#pragma unroll
+        for (int e = 0; e < kN; ++e) a[u].set(e, a[u].get(e) * f);
+        __stcs(w + i + u * kThreads, a[u].raw);
+      }
+    }
+    for (; i < vecs; i += kThreads) {
+      V a;
+      a.raw = __ldcs(v + i);
+#pragma unroll
+      for (int e = 0; e < kN; ++e) a.set(e, a.get(e) * f);
+      __stcs(w + i, a.raw);
+    }
+    for (int64_t j = threadIdx.x; j < lead; j += kThreads) o[j] = from_f32<T>(to_f32(p[j]) * f);
+    for (int64_t j = lead + vecs * kN + threadIdx.x; j < m; j += kThreads) o[j] = from_f32<T>(to_f32(p[j]) * f);
+  } else {  // the two lie at different offsets from a 16-byte boundary
+    int64_t j = threadIdx.x;
+    for (; j + 7 * kThreads < m; j += 8 * kThreads) {
+      T a[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) a[u] = p[j + u * kThreads];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) o[j + u * kThreads] = from_f32<T>(to_f32(a[u]) * f);
+    }
+    for (; j < m; j += kThreads) o[j] = from_f32<T>(to_f32(p[j]) * f);
+  }
+}
+
+template <int kMost>
+__global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__ ClipTable<kMost> t, uint32_t pieces,
+                                                         const Sum3 *__restrict__ sums, int n_sums, float max_norm,
+                                                         float *norm) {
+  pdl_wait();
+  const float nrm = total_norm(sums, n_sums);
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = nrm;
+  float f = max_norm / (nrm + 1e-6f);
+  if (f > 1.f) f = 1.f;  // a NaN stays
+  for (uint32_t q = blockIdx.x; q < pieces; q += gridDim.x) {
+    const uint32_t r = pieces - 1 - q;
+    const int k = find_tensor(t, r);
+    if (f == 1.f && t.out[k] == t.in[k]) continue;
+    const int64_t at = (int64_t)(r - t.first[k]) * kPiece;
+    const int64_t n = t.n[k];
+    if (n >= 0) {
+      const int64_t e = at / 4;
+      scale_piece(reinterpret_cast<const float *>(t.in[k]) + e, reinterpret_cast<float *>(t.out[k]) + e,
+                  min(kPiece / 4, n - e), f);
+    } else {
+      const int64_t e = at / 2;
+      scale_piece(reinterpret_cast<const bf16 *>(t.in[k]) + e, reinterpret_cast<bf16 *>(t.out[k]) + e,
+                  min(kPiece / 2, -n - 1 - e), f);
+    }
+  }
+}
+
+inline int64_t pieces_of(int64_t n, snack_dtype t) { return ceil_div(n * (int64_t)dtype_size(t), kPiece); }
+
+struct ClipCall {
+  int32_t n;
+  const void *const *grads;
+  void *const *outs;
+  const int64_t *numel;
+  const snack_dtype *types;
+  float max_norm;
+  float *norm;
+  Sum3 *sums;
+  int sms;
+};
+
+int64_t groups_of(int32_t n, int most) { return ceil_div((int64_t)n, (int64_t)most); }
+int table_for(int32_t n) { return n <= kSmallTable ? kSmallTable : n <= kMidTable ? kMidTable : kBigTable; }
+
+template <int kMost>
+snack_status run_clip(const ClipCall &c, cudaStream_t s) {
+  const int64_t groups = c.n > 0 ? groups_of(c.n, kMost) : 1;
+  const int most_blocks = c.sms * kBlocksPerSm;
+  int n_sums = 0;
+  for (int pass = 0; pass < 2; ++pass)
+    for (int64_t g0 = 0; g0 < groups; ++g0) {
+      const int64_t g = pass == 0 ? g0 : groups - 1 - g0;
+      ClipTable<kMost> t;
+      t.count = 0;
+      int64_t pieces = 0;
+      for (int64_t k = g * kMost; k < c.n && k < (g + 1) * kMost; ++k) {
+        if (c.numel[k] == 0) continue;
+        t.in[t.count] = c.grads[k];
+        t.out[t.count] = c.outs ? c.outs[k] : nullptr;
+        t.n[t.count] = c.types[k] == SNACK_F32 ? c.numel[k] : -c.numel[k] - 1;
+        t.first[t.count++] = (uint32_t)pieces;
+        pieces += pieces_of(c.numel[k], c.types[k]);
+        if (pieces > INT32_MAX) return SNACK_ERR_UNSUPPORTED;
+      }
+      t.first[t.count] = (uint32_t)pieces;
+      const int blocks = pieces < 1 ? 1 : (int)(pieces < most_blocks ? pieces : most_blocks);
+      cudaError_t e = cudaSuccess;
+      if (pass == 0) {
+        e = launch_pdl(k_clip_norm<kMost>, (unsigned)blocks, kThreads, 0, s, t, (uint32_t)pieces, c.sums + n_sums);
+        n_sums += blocks;
+      } else if (c.outs || g0 == 0) {
+        e = launch_pdl(k_clip_scale<kMost>, c.outs ? (unsigned)blocks : 1u, kThreads, 0, s, t,
+                       c.outs ? (uint32_t)pieces : 0u, (const Sum3 *)c.sums, n_sums, c.max_norm,
+                       g0 == 0 ? c.norm : (float *)nullptr);
+      }
+      if (e != cudaSuccess) return SNACK_ERR_CUDA;
+    }
+  return SNACK_OK;
+}
+
+bool clip_sizes_ok(int32_t n, const int64_t *numel, const snack_dtype *types) {
+  if (n < 0 || (n > 0 && (!numel || !types))) return false;
+  for (int32_t k = 0; k < n; ++k)
+    if (numel[k] < 0 || numel[k] > ((int64_t)1 << 45) || !lm_dtype_ok(types[k])) return false;
+  return true;
+}
+
+// the sums of every launch's blocks, on any device of up to 1024 multiprocessors
+size_t clip_ws(int32_t n) {
+  const int64_t groups = n > 0 ? groups_of(n, table_for(n)) : 1;
+  return align_up((size_t)groups * 1024 * kBlocksPerSm * sizeof(Sum3), kAlign);
+}
+
+}  // namespace
+}  // namespace snack
+
+using namespace snack;
+
+extern "C" {
+
+snack_status snack_clip_workspace_size(int32_t n_tensors, const int64_t *numel, const snack_dtype *types,
+                                       size_t *bytes) {
+  if (!bytes || !clip_sizes_ok(n_tensors, numel, types)) return SNACK_ERR_INVALID_ARG;
+  *bytes = clip_ws(n_tensors);
+  return SNACK_OK;
+}
+
+snack_status snack_clip_grad_norm(int32_t n_tensors, const void *const *grads, void *const *outs,
+                                  const int64_t *numel, const snack_dtype *types, float max_norm, float *norm,
+                                  void *ws, size_t ws_bytes, snack_stream_t stream) {
+  if (!clip_sizes_ok(n_tensors, numel, types) || !(max_norm >= 0.f)) return SNACK_ERR_INVALID_ARG;
+  if (n_tensors > 0 && !grads) return SNACK_ERR_INVALID_ARG;
+  for (int32_t k = 0; k < n_tensors; ++k) {
+    if (numel[k] == 0) continue;
+    const size_t es = dtype_size(types[k]), bytes = (size_t)numel[k] * es;
+    if (!grads[k] || !ptr_aligned(grads[k], es)) return SNACK_ERR_INVALID_ARG;
+    if (!outs) continue;
+    if (!outs[k] || !ptr_aligned(outs[k], es)) return SNACK_ERR_INVALID_ARG;
+    if (outs[k] != grads[k] && spans_overlap(outs[k], bytes, grads[k], bytes)) return SNACK_ERR_INVALID_ARG;
+  }
+  if (norm && !ptr_aligned(norm, 4)) return SNACK_ERR_INVALID_ARG;
+  if (!ws || !ptr_aligned(ws, kAlign)) return SNACK_ERR_INVALID_ARG;
+  if (ws_bytes < clip_ws(n_tensors)) return SNACK_ERR_WORKSPACE;
+  ClipCall c = {n_tensors, grads, outs, numel, types, max_norm, norm, reinterpret_cast<Sum3 *>(ws), current_sms()};
+  if (c.sms < 1) return SNACK_ERR_CUDA;
+  if (c.sms > 1024) c.sms = 1024;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  switch (table_for(n_tensors)) {
+    case kSmallTable:
+      return run_clip<kSmallTable>(c, s);
+    case kMidTable:
+      return run_clip<kMidTable>(c, s);
+    default:
+      return run_clip<kBigTable>(c, s);
+  }
+}
+
+}  // extern "C"

@@ -1,0 +1,501 @@
+// Embedding lookup and its gradient.
+//
+//   forward   out[i] = scale * table[id_i]            (zeros for an id outside [0, vocab))
+//   gradient  dtable[v] = scale * sum_{i : id_i = v} dout[i]
+//
+// Both are bound by memory: the lookup reads each distinct row once and writes
+// every output row; the gradient reads every dout row once and writes every
+// row of the table's gradient, most of them zeros for a large vocabulary.
+//
+// The gradient sorts the (id, position) pairs, stably, so that each row's
+// terms lie together in the order of their positions: one sum per row in that
+// order, in fp32, with no atomics on values, so results repeat bit for bit.
+// Up to kRankMax tokens one kernel finds each token's place by counting the
+// pairs before it (n^2 comparisons, no passes); above that an LSD radix sort.
+// The sorted list is cut into chunks of equal length, one warp per chunk and
+// column segment, so that a frequent token's many rows are shared by many
+// warps: a run that crosses a chunk's border leaves fp32 partial sums, which a
+// second kernel adds in order.  The blocks after those of the sums fill the
+// rows that no token names (found by a search in the sorted list) with zeros.
+#include <stdint.h>
+
+#include "internal.hpp"
+#include "lm.hpp"
+#include "prims.cuh"
+
+namespace snack {
+namespace {
+
+constexpr int kFwdUnroll = 4;  // accesses per lane and row segment
+
+template <typename T, int B>
+__global__ void __launch_bounds__(256) k_embed_fwd(TokenSrc ids, int64_t n, const T *__restrict__ table,
+                                                   int64_t table_ld, int32_t width, float scale, T *__restrict__ out,
+                                                   int64_t out_ld) {
+  pdl_wait();
+  typedef Pack<T, B> P;
+  const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.y;
+  if (row >= n) return;
+  const uint32_t id = ids.key(row);
+  const int acc = width / P::kN;
+  const int a0 = blockIdx.y * (32 * kFwdUnroll) + threadIdx.x;
+  T *o = out + row * out_ld;
+  const T *t = table + (int64_t)id * table_ld;
+  P v[kFwdUnroll];
+#pragma unroll
+  for (int u = 0; u < kFwdUnroll; ++u) {
+    const int a = a0 + u * 32;
+    if (a < acc && id < ids.vocab) v[u].raw = __ldg(reinterpret_cast<const typename P::R *>(t) + a);
+  }
+#pragma unroll
+  for (int u = 0; u < kFwdUnroll; ++u) {
+    const int a = a0 + u * 32;
+    if (a >= acc) continue;
+#pragma unroll
+    for (int i = 0; i < P::kN; ++i) v[u].set(i, id < ids.vocab ? scale * v[u].get(i) : 0.f);
+    reinterpret_cast<typename P::R *>(o)[a] = v[u].raw;
+  }
+}
+
+// ------------------------------------------------------------ sorted order
+
+constexpr int kRankMax = 8192;
+constexpr int kRankRows = 32;  // tokens per block
+constexpr int kRankThreads = 256;
+
+// Place of token i among all: the number of (id, position) pairs before its
+// own.  Lane l of every warp holds token 32 blockIdx.x + l; the eight warps
+// count over interleaved groups of 32 tokens, whose ids they read from shared
+// memory (every lane the same word).
+__global__ void __launch_bounds__(kRankThreads) k_rank(TokenSrc ids, int n, uint32_t *__restrict__ keys,
+                                                       uint32_t *__restrict__ pos) {
+  pdl_wait();
+  extern __shared__ __align__(16) uint32_t s_ids[];
+  __shared__ int cnt[kRankThreads / 32][kRankRows];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = (n + 31) / 32;
+  for (int i = threadIdx.x; i < groups * 32; i += kRankThreads) s_ids[i] = i < n ? ids.key(i) : 0xFFFFFFFFu;
+  __syncthreads();
+  const int own = blockIdx.x;
+  const int i = own * 32 + lane;
+  const uint32_t mine = s_ids[i];
+  int c = 0;
+  for (int g = warp; g < groups; g += kRankThreads / 32) {
+    const uint4 *q = reinterpret_cast<const uint4 *>(s_ids + g * 32);
+    if (g == own) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const uint32_t k = s_ids[g * 32 + j];
+        c += (k < mine || (k == mine && j < lane)) ? 1 : 0;
+      }
+    } else {
+      const uint32_t lim = g < own ? mine + 1u : mine;  // an earlier token of the same id comes first
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint4 k = q[j];
+        c += (k.x < lim) + (k.y < lim) + (k.z < lim) + (k.w < lim);
+      }
+    }
+  }
+  cnt[warp][lane] = c;
+  __syncthreads();
+  if (warp == 0 && i < n) {
+    int r = 0;
+#pragma unroll
+    for (int w = 0; w < kRankThreads / 32; ++w) r += cnt[w][lane];
+    keys[r] = mine;
+    pos[r] = (uint32_t)i;
+  }
+}
+
+// ------------------------------------------------------------ gradient
+
+struct EmbedGrad {
+  const uint32_t *keys, *pos;  // [n] sorted ids (vocab: none) and their positions
+  int64_t n;
+  const void *dout;
+  int64_t dout_ld;
+  void *dtable;
+  int64_t table_ld;
+  uint32_t vocab;
+  int32_t width;
+  float scale;
+  int accumulate;
+  float *part;      // [chunks][2][part_ld] sums of the runs that a chunk begins with (0) and ends with (1);
+                    //  element i of a lane's access a at i * accesses + a, so a warp's stores are whole lines
+  int64_t part_ld;
+  int chunk;        // sorted entries per chunk
+  int64_t n_chunks;
+  int n_seg;        // column segments
+  int64_t sum_blocks;
+};
+
+constexpr int kGradWarps = 8;
+constexpr int kGradVecs = 2;   // accesses per lane
+constexpr int kGradBatch = 4;  // rows in flight per lane
+constexpr int kZeroRows = 8;   // rows per warp of the zero fill
+
+__device__ __forceinline__ int64_t lower_bound(const uint32_t *__restrict__ k, int64_t n, uint32_t v) {
+  int64_t lo = 0, hi = n;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (__ldg(k + mid) < v)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// this lane's accesses of one row of the gradient: scale * acc (+ what is there)
+template <typename T, int B>
+__device__ __forceinline__ void put_row(const EmbedGrad &g, uint32_t row, int a0, int acc_n,
+                                        const float (&acc)[kGradVecs][Pack<T, B>::kN]) {
+  typedef Pack<T, B> P;
+  typename P::R *o = reinterpret_cast<typename P::R *>(reinterpret_cast<T *>(g.dtable) + (int64_t)row * g.table_ld);
+#pragma unroll
+  for (int u = 0; u < kGradVecs; ++u) {
+    const int a = a0 + 32 * u;
+    if (a >= acc_n) continue;
+    P v;
+    if (g.accumulate) v.raw = o[a];
+#pragma unroll
+    for (int i = 0; i < P::kN; ++i) {
+      const float t = g.scale * acc[u][i];
+      v.set(i, g.accumulate ? v.get(i) + t : t);
+    }
+    o[a] = v.raw;
+  }
+}
+
+template <typename T, int B>
+__global__ void __launch_bounds__(kGradWarps * 32) k_embed_sum(const EmbedGrad g) {
+  pdl_wait();
+  typedef Pack<T, B> P;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int acc_n = g.width / P::kN;
+  if ((int64_t)blockIdx.x >= g.sum_blocks) {  // ---- rows that no token names
+    const int64_t v0 = (((int64_t)blockIdx.x - g.sum_blocks) * kGradWarps + warp) * kZeroRows;
+    bool absent = false;
+    if (lane < kZeroRows && v0 + lane < (int64_t)g.vocab) {
+      const uint32_t v = (uint32_t)(v0 + lane);
+      const int64_t at = lower_bound(g.keys, g.n, v);
+      absent = at >= g.n || __ldg(g.keys + at) != v;
+    }
+    const unsigned rows = __ballot_sync(0xffffffffu, absent);
+    P z;
+#pragma unroll
+    for (int i = 0; i < P::kN; ++i) z.set(i, 0.f);
+    for (int r = 0; r < kZeroRows; ++r) {
+      if (!((rows >> r) & 1u)) continue;
+      typename P::R *o = reinterpret_cast<typename P::R *>(reinterpret_cast<T *>(g.dtable) + (v0 + r) * g.table_ld);
+      for (int a = lane; a < acc_n; a += 32) __stcs(o + a, z.raw);
+    }
+    return;
+  }
+  const int64_t gw = (int64_t)blockIdx.x * kGradWarps + warp;
+  const int64_t c = gw / g.n_seg;
+  if (c >= g.n_chunks) return;
+  const int seg = (int)(gw - c * g.n_seg);
+  const int a0 = seg * (32 * kGradVecs) + lane;
+  const int64_t j0 = c * g.chunk, j1 = min(j0 + (int64_t)g.chunk, g.n);
+  const uint32_t first = __ldg(g.keys + j0);
+  if (first >= g.vocab) return;  // only tokens outside the vocabulary from here on
+  const bool from_before = j0 > 0 && __ldg(g.keys + j0 - 1) == first;
+  const uint32_t after = j1 < g.n ? __ldg(g.keys + j1) : 0xFFFFFFFFu;
+  const T *dout = reinterpret_cast<const T *>(g.dout);
+  float acc[kGradVecs][P::kN];
+#pragma unroll
+  for (int u = 0; u < kGradVecs; ++u)
+#pragma unroll
+    for (int i = 0; i < P::kN; ++i) acc[u][i] = 0.f;
+  uint32_t cur = first;
+  bool head = from_before;  // the current run began in an earlier chunk
+  auto keep_part = [&](int which) {
+    float *p = g.part + (c * 2 + which) * g.part_ld;
+#pragma unroll
+    for (int u = 0; u < kGradVecs; ++u)
+      if (a0 + 32 * u < acc_n)
+#pragma unroll
+        for (int i = 0; i < P::kN; ++i) p[(int64_t)i * acc_n + a0 + 32 * u] = acc[u][i];
+  };
+  for (int64_t b = j0; b < j1 && cur < g.vocab; b += 32) {
+    const uint32_t my_key = b + lane < j1 ? __ldg(g.keys + b + lane) : 0xFFFFFFFFu;
+    const uint32_t my_pos = b + lane < j1 ? __ldg(g.pos + b + lane) : 0u;
+    const int m = (int)min((int64_t)32, j1 - b);
+    for (int e0 = 0; e0 < m && cur < g.vocab; e0 += kGradBatch) {
+      P v[kGradBatch][kGradVecs];
+#pragma unroll
+      for (int e = 0; e < kGradBatch; ++e) {
+        const uint32_t k = __shfl_sync(0xffffffffu, my_key, e0 + e), p = __shfl_sync(0xffffffffu, my_pos, e0 + e);
+        const typename P::R *src = reinterpret_cast<const typename P::R *>(dout + (int64_t)p * g.dout_ld);
+#pragma unroll
+        for (int u = 0; u < kGradVecs; ++u)
+          if (k < g.vocab && a0 + 32 * u < acc_n) v[e][u].raw = __ldcs(src + a0 + 32 * u);
+      }
+#pragma unroll
+      for (int e = 0; e < kGradBatch; ++e) {
+        const uint32_t k = __shfl_sync(0xffffffffu, my_key, e0 + e);
+        if (k != cur) {
+          if (cur >= g.vocab) break;
+          if (e0 + e >= m) break;  // the chunk's end: its last run is finished below
+          if (head)
+            keep_part(0);
+          else
+            put_row<T, B>(g, cur, a0, acc_n, acc);
+          head = false;
+          cur = k;
+          if (cur >= g.vocab) break;
+#pragma unroll
+          for (int u = 0; u < kGradVecs; ++u)
+#pragma unroll
+            for (int i = 0; i < P::kN; ++i) acc[u][i] = 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < kGradVecs; ++u)
+          if (a0 + 32 * u < acc_n)
+#pragma unroll
+            for (int i = 0; i < P::kN; ++i) acc[u][i] += v[e][u].get(i);
+      }
+    }
+  }
+  if (cur >= g.vocab) return;
+  if (head)
+    keep_part(0);
+  else if (after == cur)
+    keep_part(1);
+  else
+    put_row<T, B>(g, cur, a0, acc_n, acc);
+}
+
+// A run that crosses chunk borders: the chunk it begins in adds the partial
+// sums of the chunks it covers, in order.
+template <typename T, int B>
+__global__ void __launch_bounds__(kGradWarps * 32) k_embed_join(const EmbedGrad g) {
+  pdl_wait();
+  typedef Pack<T, B> P;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t gw = (int64_t)blockIdx.x * kGradWarps + warp;
+  const int64_t c = gw / g.n_seg;
+  if (c + 1 >= g.n_chunks) return;
+  const int64_t j0 = c * g.chunk, j1 = j0 + g.chunk;
+  const uint32_t cur = __ldg(g.keys + j1 - 1);
+  if (cur >= g.vocab || __ldg(g.keys + j1) != cur) return;
+  if (__ldg(g.keys + j0) == cur && j0 > 0 && __ldg(g.keys + j0 - 1) == cur) return;  // it began earlier
+  const int64_t end = j1 + lower_bound(g.keys + j1, g.n - j1, cur + 1u);
+  const int64_t last = (end - 1) / g.chunk;  // the chunk it ends in
+  const int seg = (int)(gw - c * g.n_seg);
+  const int acc_n = g.width / P::kN;
+  const int a0 = seg * (32 * kGradVecs) + lane;
+  float acc[kGradVecs][P::kN];
+#pragma unroll
+  for (int u = 0; u < kGradVecs; ++u)
+#pragma unroll
+    for (int i = 0; i < P::kN; ++i)
+      acc[u][i] = a0 + 32 * u < acc_n ? g.part[(c * 2 + 1) * g.part_ld + (int64_t)i * acc_n + a0 + 32 * u] : 0.f;
+  for (int64_t q = c + 1; q <= last; ++q) {
+    const float *p = g.part + q * 2 * g.part_ld;
+#pragma unroll
+    for (int u = 0; u < kGradVecs; ++u)
+      if (a0 + 32 * u < acc_n)
+#pragma unroll
+        for (int i = 0; i < P::kN; ++i) acc[u][i] += p[(int64_t)i * acc_n + a0 + 32 * u];
+  }
+  put_row<T, B>(g, cur, a0, acc_n, acc);
+}
+
+// ------------------------------------------------------------ host side
+
+int key_bits(uint32_t vocab) {
+  int b = 0;
+  while (b < 32 && (vocab >> b)) ++b;
+  return b;  // keys are 0 .. vocab
+}
+
+constexpr int kSegElems = 32 * kGradVecs;  // accesses per segment
+
+struct GradWs {
+  size_t keys, pos, k0, v0, k1, v1, temp, part, total;
+  int chunk;
+  int64_t n_chunks, part_ld;
+};
+
+// Chunks short enough that a small call still has a few thousand warps, at
+// most kMaxChunk entries; the partial sums of a run that covers many chunks
+// are added by one warp per segment, so long calls get longer chunks.
+GradWs grad_ws(int64_t n, int32_t width) {
+  GradWs w;
+  int64_t chunk = 8;
+  while (chunk < 4096 && n / chunk > 2048) chunk *= 2;
+  w.chunk = (int)chunk;
+  w.n_chunks = n > 0 ? (n + chunk - 1) / chunk : 0;
+  w.part_ld = (int64_t)align_up((size_t)width, 4);
+  size_t o = 0;
+  w.keys = o;
+  o += align_up((size_t)n * 4, kAlign);
+  w.pos = o;
+  o += align_up((size_t)n * 4, kAlign);
+  const bool radix = n > kRankMax;
+  w.k0 = o;
+  if (radix) o += align_up((size_t)n * 4, kAlign);
+  w.v0 = o;
+  if (radix) o += align_up((size_t)n * 4, kAlign);
+  w.k1 = o;
+  if (radix) o += align_up((size_t)n * 4, kAlign);
+  w.v1 = o;
+  if (radix) o += align_up((size_t)n * 4, kAlign);
+  w.temp = o;
+  if (radix) o += align_up(radix_temp_bytes(n), kAlign);
+  w.part = o;
+  o += align_up((size_t)w.n_chunks * 2 * (size_t)w.part_ld * 4, kAlign);
+  w.total = o;
+  return w;
+}
+
+bool embed_sizes_ok(int64_t n, int64_t vocab, int32_t width) {
+  return n >= 0 && n < INT32_MAX && vocab >= 1 && vocab < INT32_MAX && width >= 1;
+}
+
+template <typename T, int B>
+cudaError_t launch_fwd(TokenSrc ids, int64_t n, const void *table, int64_t table_ld, int32_t width, float scale,
+                       void *out, int64_t out_ld, cudaStream_t s) {
+  const int acc = width / Pack<T, B>::kN;
+  const dim3 grid((unsigned)ceil_div(n, 8), (unsigned)ceil_div(acc, 32 * kFwdUnroll));
+  return launch_pdl(k_embed_fwd<T, B>, grid, dim3(32, 8), 0, s, ids, n, reinterpret_cast<const T *>(table), table_ld,
+                    width, scale, reinterpret_cast<T *>(out), out_ld);
+}
+
+template <typename T, int B>
+cudaError_t launch_grad(EmbedGrad g, cudaStream_t s) {
+  const int acc = g.width / Pack<T, B>::kN;
+  g.n_seg = (int)ceil_div(acc, kSegElems);
+  g.sum_blocks = ceil_div(g.n_chunks * g.n_seg, kGradWarps);
+  const int64_t zero_blocks = g.accumulate ? 0 : ceil_div((int64_t)g.vocab, (int64_t)kGradWarps * kZeroRows);
+  const int64_t blocks = g.sum_blocks + zero_blocks;
+  if (blocks == 0) return cudaSuccess;
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  cudaError_t e = launch_pdl(k_embed_sum<T, B>, (unsigned)blocks, kGradWarps * 32, 0, s, (const EmbedGrad)g);
+  if (e != cudaSuccess || g.n_chunks < 2) return e;
+  return launch_pdl(k_embed_join<T, B>, (unsigned)g.sum_blocks, kGradWarps * 32, 0, s, (const EmbedGrad)g);
+}
+
+}  // namespace
+}  // namespace snack
+
+using namespace snack;
+
+extern "C" {
+
+snack_status snack_embed_fwd(const void *ids, snack_index ids_t, int64_t n, const void *table, int64_t table_ld,
+                             int64_t vocab, int32_t width, snack_dtype t, float scale, void *out, int64_t out_ld,
+                             snack_stream_t stream) {
+  if (!lm_dtype_ok(t) || !lm_index_ok(ids_t) || !embed_sizes_ok(n, vocab, width)) return SNACK_ERR_INVALID_ARG;
+  if (table_ld < width || out_ld < width) return SNACK_ERR_INVALID_ARG;
+  if (n == 0) return SNACK_OK;
+  const size_t es = dtype_size(t);
+  if (!ids || !table || !out || !ptr_aligned(ids, index_size(ids_t)) || !ptr_aligned(table, es) || !ptr_aligned(out, es))
+    return SNACK_ERR_INVALID_ARG;
+  if (spans_overlap(out, span_bytes(n, width, out_ld, es), table, span_bytes(vocab, width, table_ld, es)) ||
+      spans_overlap(out, span_bytes(n, width, out_ld, es), ids, (size_t)n * index_size(ids_t)))
+    return SNACK_ERR_INVALID_ARG;
+  const TokenSrc src{ids, ids_t == SNACK_I64, (uint32_t)vocab};
+  const int b = access_bytes((uintptr_t)table | (uintptr_t)out | (uintptr_t)(table_ld * es) | (uintptr_t)(out_ld * es) |
+                             (uintptr_t)((size_t)width * es));
+  if (ceil_div((int64_t)width * (int64_t)es, (int64_t)b * 32 * kFwdUnroll) > 65535) return SNACK_ERR_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+#define SNACK_FWD(T, B) e = launch_fwd<T, B>(src, n, table, table_ld, width, scale, out, out_ld, s)
+  if (t == SNACK_F32) {
+    if (b == 16)
+      SNACK_FWD(float, 16);
+    else if (b == 8)
+      SNACK_FWD(float, 8);
+    else
+      SNACK_FWD(float, 4);
+  } else {
+    if (b == 16)
+      SNACK_FWD(bf16, 16);
+    else if (b == 8)
+      SNACK_FWD(bf16, 8);
+    else if (b == 4)
+      SNACK_FWD(bf16, 4);
+    else
+      SNACK_FWD(bf16, 2);
+  }
+#undef SNACK_FWD
+  return e == cudaSuccess ? SNACK_OK : SNACK_ERR_CUDA;
+}
+
+snack_status snack_embed_grad_workspace_size(int64_t n, int64_t vocab, int32_t width, size_t *bytes) {
+  if (!bytes || !embed_sizes_ok(n, vocab, width)) return SNACK_ERR_INVALID_ARG;
+  *bytes = grad_ws(n, width).total;
+  return SNACK_OK;
+}
+
+snack_status snack_embed_grad(const void *ids, snack_index ids_t, int64_t n, const void *dout, int64_t dout_ld,
+                              int64_t vocab, int32_t width, snack_dtype t, float scale, int accumulate, void *dtable,
+                              int64_t dtable_ld, void *ws, size_t ws_bytes, snack_stream_t stream) {
+  if (!lm_dtype_ok(t) || !lm_index_ok(ids_t) || !embed_sizes_ok(n, vocab, width)) return SNACK_ERR_INVALID_ARG;
+  if (dout_ld < width || dtable_ld < width || !dtable) return SNACK_ERR_INVALID_ARG;
+  const size_t es = dtype_size(t);
+  if (!ptr_aligned(dtable, es)) return SNACK_ERR_INVALID_ARG;
+  const GradWs W = grad_ws(n, width);
+  if (n > 0) {
+    if (!ids || !dout || !ws || !ptr_aligned(ids, index_size(ids_t)) || !ptr_aligned(dout, es) || !ptr_aligned(ws, kAlign))
+      return SNACK_ERR_INVALID_ARG;
+    const size_t nd = span_bytes(vocab, width, dtable_ld, es);
+    if (spans_overlap(dtable, nd, dout, span_bytes(n, width, dout_ld, es)) ||
+        spans_overlap(dtable, nd, ids, (size_t)n * index_size(ids_t)) || spans_overlap(dtable, nd, ws, ws_bytes))
+      return SNACK_ERR_INVALID_ARG;
+    if (ws_bytes < W.total) return SNACK_ERR_WORKSPACE;
+  }
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t *w = reinterpret_cast<uint8_t *>(ws);
+  EmbedGrad g = {};
+  g.n = n;
+  g.dout = dout;
+  g.dout_ld = dout_ld;
+  g.dtable = dtable;
+  g.table_ld = dtable_ld;
+  g.vocab = (uint32_t)vocab;
+  g.width = width;
+  g.scale = scale;
+  g.accumulate = accumulate != 0;
+  g.chunk = W.chunk;
+  g.n_chunks = W.n_chunks;
+  g.part_ld = W.part_ld;
+  cudaError_t e = cudaSuccess;
+  if (n > 0) {
+    uint32_t *keys = reinterpret_cast<uint32_t *>(w + W.keys), *pos = reinterpret_cast<uint32_t *>(w + W.pos);
+    g.keys = keys;
+    g.pos = pos;
+    g.part = reinterpret_cast<float *>(w + W.part);
+    const TokenSrc src{ids, ids_t == SNACK_I64, (uint32_t)vocab};
+    if (n <= kRankMax) {
+      const size_t smem = align_up((size_t)n, 32) * 4;
+      e = launch_pdl(k_rank, (unsigned)ceil_div(n, kRankRows), kRankThreads, smem, s, src, (int)n, keys, pos);
+    } else {
+      try {
+        e = radix_sort_custom<uint32_t>(src, ArrayDst<uint32_t>{keys, pos}, n, key_bits((uint32_t)vocab),
+                                        reinterpret_cast<uint32_t *>(w + W.k0), reinterpret_cast<uint32_t *>(w + W.v0),
+                                        reinterpret_cast<uint32_t *>(w + W.k1), reinterpret_cast<uint32_t *>(w + W.v1),
+                                        w + W.temp, s);
+      } catch (...) {  // the shared-memory table could not grow
+        return SNACK_ERR_CUDA;
+      }
+    }
+    if (e != cudaSuccess) return SNACK_ERR_CUDA;
+  }
+  const int b = access_bytes((uintptr_t)dtable | (n > 0 ? (uintptr_t)dout : 0) | (uintptr_t)(dtable_ld * es) |
+                             (uintptr_t)(dout_ld * es) | (uintptr_t)((size_t)width * es));
+  if (t == SNACK_F32)
+    e = b == 16 ? launch_grad<float, 16>(g, s) : b == 8 ? launch_grad<float, 8>(g, s) : launch_grad<float, 4>(g, s);
+  else
+    e = b == 16  ? launch_grad<bf16, 16>(g, s)
+        : b == 8 ? launch_grad<bf16, 8>(g, s)
+        : b == 4 ? launch_grad<bf16, 4>(g, s)
+                 : launch_grad<bf16, 2>(g, s);
+  return e == cudaSuccess ? SNACK_OK : SNACK_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -27,12 +27,15 @@ STATUS_NAMES = {0: "SNACK_OK", 1: "SNACK_ERR_INVALID_ARG", 2: "SNACK_ERR_UNSORTE
                 4: "SNACK_ERR_WORKSPACE", 5: "SNACK_ERR_CUDA", 6: "SNACK_ERR_TIMEOUT", 7: "SNACK_ERR_UNSUPPORTED",
                 8: "SNACK_ERR_NO_SPACE"}
 SNACK_F32, SNACK_BF16 = 0, 1
+SNACK_I32, SNACK_I64 = 0, 1
 
 EXPORTED = ("snack_query_sizes", "snack_create", "snack_spmm_fwd", "snack_spmm_fwd_noalloc", "snack_spmm_dx",
             "snack_spmm_fwd_gelu", "snack_spmm_dx_gelu", "snack_sddmm_dw", "snack_backward",
             "snack_restructure_workspace_size", "snack_restructure", "snack_restructure_rows_workspace_size",
             "snack_restructure_rows", "snack_wait_plan", "snack_destroy", "snack_status_string", "snack_version",
-            "snack_trace_start", "snack_trace_read", "snack_trace_stop")
+            "snack_trace_start", "snack_trace_read", "snack_trace_stop", "snack_embed_fwd",
+            "snack_embed_grad_workspace_size", "snack_embed_grad", "snack_clip_workspace_size",
+            "snack_clip_grad_norm")
 
 
 class SnackLibraryMissing(RuntimeError):
@@ -107,6 +110,18 @@ def load(path: Optional[str] = None):
         lib.snack_trace_read.restype = st
         lib.snack_trace_stop.argtypes = []
         lib.snack_trace_stop.restype = st
+        f32 = ctypes.c_float
+        lib.snack_embed_fwd.argtypes = [vp, st, i64, vp, i64, i64, i32, st, f32, vp, i64, vp]
+        lib.snack_embed_fwd.restype = st
+        lib.snack_embed_grad_workspace_size.argtypes = [i64, i64, i32, ctypes.POINTER(sz)]
+        lib.snack_embed_grad_workspace_size.restype = st
+        lib.snack_embed_grad.argtypes = [vp, st, i64, vp, i64, i64, i32, st, f32, ctypes.c_int, vp, i64, vp, sz, vp]
+        lib.snack_embed_grad.restype = st
+        lib.snack_clip_workspace_size.argtypes = [i32, ctypes.POINTER(i64), ctypes.POINTER(st), ctypes.POINTER(sz)]
+        lib.snack_clip_workspace_size.restype = st
+        lib.snack_clip_grad_norm.argtypes = [i32, ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(i64),
+                                             ctypes.POINTER(st), f32, vp, vp, sz, vp]
+        lib.snack_clip_grad_norm.restype = st
         _lib = lib
         return lib
 
@@ -268,6 +283,55 @@ def snack_version() -> int:
     return int(load().snack_version())
 
 
+def index_code(dt: torch.dtype) -> int:
+    if dt == torch.int32:
+        return SNACK_I32
+    if dt == torch.int64:
+        return SNACK_I64
+    raise ValueError(f"unsupported index dtype {dt}")
+
+
+def snack_embed_fwd(ids, table, scale: float, out, stream=None) -> None:
+    _check("snack_embed_fwd",
+           load().snack_embed_fwd(_ptr(ids), index_code(ids.dtype), ids.numel(), _ptr(table), table.stride(0),
+                                  table.shape[0], table.shape[1], dtype_code(table.dtype), scale, _ptr(out),
+                                  out.stride(0), _stream(stream)))
+
+
+def snack_embed_grad_workspace_size(n: int, vocab: int, width: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check("snack_embed_grad_workspace_size",
+           load().snack_embed_grad_workspace_size(n, vocab, width, ctypes.byref(b)))
+    return b.value
+
+
+def snack_embed_grad(ids, dout, scale: float, accumulate: bool, dtable, ws, stream=None) -> None:
+    _check("snack_embed_grad",
+           load().snack_embed_grad(_ptr(ids), index_code(ids.dtype), ids.numel(), _ptr(dout), dout.stride(0),
+                                   dtable.shape[0], dtable.shape[1], dtype_code(dtable.dtype), scale,
+                                   1 if accumulate else 0, _ptr(dtable), dtable.stride(0), _ptr(ws), _nbytes(ws),
+                                   _stream(stream)))
+
+
+def snack_clip_workspace_size(numel, types) -> int:
+    n = len(numel)
+    b = ctypes.c_size_t(0)
+    _check("snack_clip_workspace_size",
+           load().snack_clip_workspace_size(n, (ctypes.c_int64 * n)(*numel), (ctypes.c_int * n)(*types),
+                                            ctypes.byref(b)))
+    return b.value
+
+
+def snack_clip_grad_norm(grads, outs, numel, types, max_norm: float, norm, ws, stream=None) -> None:
+    """grads and outs: lists of device addresses (outs None: the norm alone); numel, types: lists of their sizes."""
+    n = len(grads)
+    _check("snack_clip_grad_norm",
+           load().snack_clip_grad_norm(n, (ctypes.c_void_p * n)(*grads),
+                                       None if outs is None else (ctypes.c_void_p * n)(*outs),
+                                       (ctypes.c_int64 * n)(*numel), (ctypes.c_int * n)(*types), max_norm, _ptr(norm),
+                                       _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
 # ------------------------------------------------------------- layer owner
 
 
@@ -406,3 +470,142 @@ class _SparseLinearFn(torch.autograd.Function):
 def sparse_linear(x: torch.Tensor, layer: SparseLinear) -> torch.Tensor:
     """Autograd-aware Y = X W^T + b; gradients flow to x and to layer.val."""
     return _SparseLinearFn.apply(x, layer.val, layer)
+
+
+# ------------------------------------------------------------- language-model operators
+#
+# Plain functions on CUDA tensors (float32 or bfloat16; ids and targets int32 or
+# int64).  Outputs and workspaces come from torch's allocator, on the stream
+# that the kernels run on: torch's current one, or `stream`.
+
+
+class _Place:
+    """The device and the stream of a call: enters both where they are not the current ones."""
+
+    def __init__(self, t: torch.Tensor, stream):
+        if not t.is_cuda:
+            raise ValueError("expected CUDA tensors")
+        self.device = t.device
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+        if stream is not None and stream.device != t.device:
+            raise ValueError("the stream belongs to another device than the tensors")
+        self.stream = stream
+        self.outer = None
+
+    def __enter__(self):
+        if self.stream is not None:
+            self.outer = torch.cuda.stream(self.stream)
+        elif self.device.index != torch.cuda.current_device():
+            self.outer = torch.cuda.device(self.device)
+        if self.outer is not None:
+            self.outer.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.outer is not None:
+            self.outer.__exit__(*exc)
+
+
+def _same_device(*tensors) -> None:
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors must be on one CUDA device")
+
+
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    """t as a matrix whose rows are contiguous (their distance may exceed their length)."""
+    if t.dim() != 2:
+        raise ValueError("expected a matrix")
+    if (t.stride(1) == 1 or t.shape[1] == 1) and t.stride(0) >= t.shape[1]:
+        return t
+    return t.contiguous()
+
+
+def _out_rows(out: torch.Tensor, rows: int, width: int, dtype) -> torch.Tensor:
+    if tuple(out.shape) != (rows, width) or out.dtype != dtype or (width > 1 and out.stride(1) != 1) \
+            or (rows > 1 and out.stride(0) < width):
+        raise ValueError(f"out must be a {dtype} matrix [{rows}, {width}] with contiguous rows")
+    return out
+
+
+def _workspace(nbytes: int, device) -> torch.Tensor:
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+
+def embed(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out: Optional[torch.Tensor] = None,
+          stream=None) -> torch.Tensor:
+    """scale * table[ids]; zeros for an id outside the table.  ids of any shape; the result has that shape plus the width."""
+    _same_device(table, ids, out)
+    with _Place(table, stream):
+        tab, flat = _rows(table), ids.contiguous()
+        n, width = flat.numel(), tab.shape[1]
+        y = torch.empty((n, width), dtype=tab.dtype, device=tab.device) if out is None \
+            else _out_rows(out, n, width, tab.dtype)
+        snack_embed_fwd(flat, tab, float(scale), y)
+        return y.view(*ids.shape, width) if out is None and ids.dim() != 1 else y
+
+
+def embed_grad(ids: torch.Tensor, dout: torch.Tensor, vocab: int, scale: float = 1.0,
+               out: Optional[torch.Tensor] = None, accumulate: bool = False, stream=None) -> torch.Tensor:
+    """The gradient of embed's table, [vocab, width] in dout's type.  With accumulate the sums are added to `out`."""
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    _same_device(dout, ids, out)
+    with _Place(dout, stream):
+        width = dout.shape[-1]
+        d, flat = _rows(dout if dout.dim() == 2 else dout.reshape(-1, width)), ids.contiguous()
+        if d.shape[0] != flat.numel():
+            raise ValueError("dout needs one row per id")
+        g = torch.empty((vocab, width), dtype=d.dtype, device=d.device) if out is None \
+            else _out_rows(out, vocab, width, d.dtype)
+        ws = _workspace(snack_embed_grad_workspace_size(flat.numel(), vocab, width), d.device)
+        snack_embed_grad(flat, d, float(scale), accumulate, g, ws)
+        return g
+
+
+class _EmbedFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, table, ids, scale):
+        ctx.save_for_backward(ids)
+        ctx.vocab, ctx.scale = table.shape[0], scale
+        return embed(ids, table, scale)
+
+    @staticmethod
+    def backward(ctx, dy):
+        (ids,) = ctx.saved_tensors
+        return embed_grad(ids, dy, ctx.vocab, ctx.scale), None, None
+
+
+def embedding(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
+    """Autograd-aware embed; the gradient flows to table."""
+    return _EmbedFn.apply(table, ids, scale)
+
+
+def clip_grad_norm(grads, max_norm: float, out=None, stream=None) -> torch.Tensor:
+    """The 2-norm over all gradients (a float32 CUDA scalar); scales them so that it is at most max_norm.
+
+    grads: a sequence of contiguous CUDA tensors, float32 and bfloat16 as they
+    come.  The clipped gradients go to `out` (tensors of the same types and
+    sizes), or in place when it is None.
+    """
+    grads = list(grads)
+    if not grads:
+        raise ValueError("no gradients")
+    outs = grads if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError("out needs one tensor per gradient")
+    dev = grads[0].device
+    for g, o in zip(grads, outs):
+        if g.device != dev or not g.is_contiguous():
+            raise ValueError("gradients must be contiguous tensors on one CUDA device")
+        if o is not g and (o.device != dev or o.dtype != g.dtype or o.numel() != g.numel() or not o.is_contiguous()):
+            raise ValueError("out must hold contiguous tensors of the gradients' types and sizes")
+    with _Place(grads[0], stream):
+        numel, types = [g.numel() for g in grads], [dtype_code(g.dtype) for g in grads]
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        ws = _workspace(snack_clip_workspace_size(numel, types), dev)
+        snack_clip_grad_norm([g.data_ptr() for g in grads], [o.data_ptr() for o in outs], numel, types,
+                             float(max_norm), norm, ws)
+        return norm

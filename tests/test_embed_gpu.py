@@ -1,0 +1,228 @@
+"""Embedding lookup and its gradient against the definitions in 64 bits.
+
+Tolerances.  Forward: one product of the scale (rounded to fp32) and a stored
+value, rounded once more: |err| <= 2^-23 |y| in fp32 (two roundings of half an
+ulp), and half a bf16 ulp more in bf16.  Gradient: a row of m terms summed in
+fp32, in any grouping, is within m 2^-24 of the sum of its terms' magnitudes
+T (one rounding per addition), plus two roundings for the scale: (m + 2) 2^-24
+T; a bf16 result adds half a bf16 ulp.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from spmm_row_sorted_gb300 import snack
+
+from gpu_util import assert_close_T, bf16_half_ulp, f64
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+U = 2.0 ** -24
+
+
+def make_ids(n, vocab, kind, seed, itype):
+    rng = np.random.default_rng(seed)
+    if kind == "uniform":
+        ids = rng.integers(0, vocab, n)
+    elif kind == "skewed":  # a few ids take most tokens
+        ids = np.minimum((vocab * rng.random(n) ** 6).astype(np.int64), vocab - 1)
+    elif kind == "one":
+        ids = np.full(n, vocab // 2)
+    elif kind == "outside":  # no token names a row
+        ids = np.where(rng.random(n) < 0.5, -1, vocab)
+    else:  # "padded": some ids outside, at both ends
+        ids = rng.integers(0, vocab, n)
+        ids[rng.random(n) < 0.3] = -1
+        ids[rng.random(n) < 0.1] = vocab
+        ids[rng.random(n) < 0.05] = -100
+    return torch.from_numpy(ids.astype(np.int64)).to(itype).cuda()
+
+
+def strided(n, width, gap, lead, dtype, seed, std=1.0):
+    """[n, width] whose rows lie width + gap apart and start `lead` elements into their buffer."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    buf = torch.full((n * (width + gap) + lead,), float("nan"), device="cuda", dtype=DTYPES[dtype])
+    v = buf[lead:].view(n, width + gap)[:, :width]
+    v.copy_(torch.empty(n, width, device="cuda").normal_(0, std, generator=g))
+    return v
+
+
+LOOKUPS = [
+    # n, vocab, width, dtype, kind, gap, lead
+    (1, 7, 8, "f32", "uniform", 0, 0),
+    (1, 1, 1, "bf16", "uniform", 0, 0),
+    (5, 100, 64, "bf16", "padded", 0, 0),
+    (33, 1000, 4096, "bf16", "uniform", 0, 0),
+    (257, 1000, 1001, "f32", "padded", 0, 0),
+    (257, 1000, 1001, "bf16", "padded", 0, 0),
+    (100, 333, 770, "bf16", "skewed", 0, 0),     # 4-byte accesses
+    (100, 333, 772, "bf16", "skewed", 0, 0),     # 8-byte accesses
+    (100, 333, 770, "f32", "skewed", 2, 0),      # 8-byte accesses
+    (100, 333, 768, "f32", "padded", 3, 1),      # rows off every boundary
+    (64, 50, 128, "bf16", "outside", 8, 8),
+]
+
+
+@pytest.mark.parametrize("itype", [torch.int32, torch.int64], ids=["i32", "i64"])
+@pytest.mark.parametrize("n,vocab,width,dtype,kind,gap,lead", LOOKUPS)
+def test_embed_matches_definition(n, vocab, width, dtype, kind, gap, lead, itype):
+    table = strided(vocab, width, gap, lead, dtype, seed=n)
+    ids = make_ids(n, vocab, kind, n, itype)
+    scale = 1.7
+    y = snack.embed(ids, table, scale)
+    t, i = f64(table), ids.cpu().numpy().astype(np.int64)
+    inside = (i >= 0) & (i < vocab)
+    ref = np.where(inside[:, None], scale * t[np.where(inside, i, 0)], 0.0)
+    assert y.shape == (n, width)
+    err = np.abs(f64(y) - ref)
+    bound = 2.0 ** -23 * np.abs(ref)
+    if dtype == "bf16":
+        bound = bound + bf16_half_ulp(np.abs(ref) * (1 + 2.0 ** -23))
+    assert np.all(err <= bound)
+    assert not np.any(f64(y)[~inside])
+
+
+def test_embed_scale_one_copies_bits_and_shapes():
+    table = strided(50, 96, 0, 0, "bf16", seed=3)
+    ids = make_ids(24, 50, "uniform", 1, torch.int64).view(2, 3, 4)
+    y = snack.embed(ids, table)
+    assert y.shape == (2, 3, 4, 96)
+    assert torch.equal(y, table[ids])
+    assert snack.embed(ids[:0], table).shape == (0, 3, 4, 96)
+
+
+def test_embed_leaves_the_gaps_of_its_output():
+    table = strided(20, 30, 0, 0, "f32", seed=5)
+    ids = make_ids(9, 20, "padded", 2, torch.int64)
+    buf = torch.full((9, 37), 7.0, device="cuda")
+    snack.embed(ids, table, 2.0, out=buf[:, 4:34])
+    assert torch.all(buf[:, :4] == 7.0) and torch.all(buf[:, 34:] == 7.0)
+    assert torch.equal(buf[:, 4:34].contiguous(), snack.embed(ids, table, 2.0))
+
+
+GRADS = [
+    # n, vocab, width, dtype, kind, gap, lead
+    (0, 10, 16, "f32", "uniform", 0, 0),
+    (1, 5, 8, "f32", "uniform", 0, 0),
+    (1, 1, 1, "bf16", "uniform", 0, 0),
+    (7, 3, 40, "bf16", "uniform", 0, 0),
+    (8, 1000, 64, "f32", "outside", 0, 0),
+    (31, 100, 1001, "f32", "padded", 0, 0),
+    (32, 100, 1001, "bf16", "padded", 0, 0),
+    (1023, 500, 768, "f32", "skewed", 5, 0),
+    (1024, 500, 770, "bf16", "skewed", 0, 0),
+    (1025, 500, 772, "bf16", "skewed", 0, 0),
+    (4097, 37, 128, "bf16", "uniform", 0, 0),
+    (3000, 100, 256, "f32", "one", 0, 0),        # one run over every chunk
+    (8192, 4000, 512, "bf16", "padded", 0, 0),   # the last size that counts places
+    (8193, 4000, 512, "bf16", "padded", 0, 0),   # the first that sorts by digits
+    (20001, 255, 130, "f32", "skewed", 0, 1),    # one digit
+    (20000, 256, 136, "bf16", "uniform", 0, 0),  # keys of nine bits
+    (50000, 70000, 33, "f32", "skewed", 0, 0),   # three digits
+    (70001, 300, 64, "f32", "one", 0, 0),
+]
+
+
+def grad_ref(ids, dout, vocab, scale):
+    i = ids.cpu().numpy().astype(np.int64)
+    inside = (i >= 0) & (i < vocab)
+    d = f64(dout)
+    out, mag, m = np.zeros((vocab, d.shape[1])), np.zeros((vocab, d.shape[1])), np.zeros(vocab)
+    np.add.at(out, i[inside], d[inside])
+    np.add.at(mag, i[inside], np.abs(d[inside]))
+    np.add.at(m, i[inside], 1.0)
+    return scale * out, abs(scale) * mag, m
+
+
+def check_grad(got, ref, mag, m, dtype):
+    bound = (m[:, None] + 2) * U * mag
+    if dtype == "bf16":
+        bound = bound + bf16_half_ulp(np.abs(ref) + bound)
+    assert np.all(np.abs(f64(got) - ref) <= bound)
+    assert not np.any(f64(got)[m == 0])
+
+
+@pytest.mark.parametrize("n,vocab,width,dtype,kind,gap,lead", GRADS)
+def test_embed_grad_matches_definition(n, vocab, width, dtype, kind, gap, lead):
+    ids = make_ids(n, vocab, kind, n + 1, torch.int64 if n % 2 else torch.int32)
+    dout = strided(n, width, gap, lead, dtype, seed=n)
+    out = torch.full((vocab, width), float("nan"), device="cuda", dtype=DTYPES[dtype])
+    g = snack.embed_grad(ids, dout, vocab, 0.7, out=out)
+    ref, mag, m = grad_ref(ids, dout, vocab, 0.7)
+    check_grad(g, ref, mag, m, dtype)
+    assert torch.equal(g, snack.embed_grad(ids, dout, vocab, 0.7))  # repeats bit for bit
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_embed_grad_accumulates(dtype):
+    n, vocab, width = 500, 90, 200
+    ids = make_ids(n, vocab, "skewed", 3, torch.int32)
+    ids[ids > 60] = -1  # rows that no token names
+    dout = strided(n, width, 0, 0, dtype, seed=4)
+    start = strided(vocab, width, 0, 0, dtype, seed=5)
+    out = start.clone()
+    snack.embed_grad(ids, dout, vocab, 0.5, out=out, accumulate=True)
+    ref, mag, m = grad_ref(ids, dout, vocab, 0.5)
+    check = f64(out)
+    s = f64(start)
+    bound = (m[:, None] + 3) * U * (mag + np.abs(s))
+    if dtype == "bf16":
+        bound = bound + bf16_half_ulp(np.abs(ref + s) + bound)
+    assert np.all(np.abs(check - (ref + s)) <= bound)
+    assert torch.equal(out[torch.from_numpy(m == 0).cuda()], start[torch.from_numpy(m == 0).cuda()])
+
+
+def test_embedding_autograd_matches_differences():
+    vocab, width = 12, 6
+    table = strided(vocab, width, 0, 0, "f32", seed=8).contiguous().requires_grad_()
+    ids = make_ids(40, vocab, "padded", 9, torch.int64).view(4, 10)
+    weight = torch.randn(4, 10, width, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    (snack.embedding(ids, table, 1.5) * weight).sum().backward()
+    # linear in the table: central differences are exact but for rounding (values below 16, sums of 240 terms)
+    base = table.detach()
+    for r, c in [(0, 0), (5, 3), (11, 5)]:
+        lo, hi = base.clone(), base.clone()
+        lo[r, c] -= 0.5
+        hi[r, c] += 0.5
+        diff = (snack.embed(ids, hi, 1.5).double() * weight).sum() - (snack.embed(ids, lo, 1.5).double() * weight).sum()
+        assert abs(float(diff) - float(table.grad[r, c])) < 1e-4
+
+
+def test_embed_on_another_stream():
+    n, vocab, width = 2000, 700, 256
+    ids = make_ids(n, vocab, "skewed", 1, torch.int64)
+    table, dout = strided(vocab, width, 0, 0, "bf16", 1), strided(n, width, 0, 0, "bf16", 2)
+    want = snack.embed(ids, table), snack.embed_grad(ids, dout, vocab)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = snack.embed(ids, table, stream=side), snack.embed_grad(ids, dout, vocab, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+def test_embed_refusals():
+    table = torch.zeros(10, 8, device="cuda")
+    ids = torch.zeros(4, dtype=torch.int64, device="cuda")
+    with pytest.raises(ValueError):
+        snack.embed(ids.float(), table)
+    with pytest.raises(ValueError):
+        snack.embed(ids, table.half())
+    with pytest.raises(ValueError):
+        snack.embed(ids.cpu(), table)
+    with pytest.raises(ValueError):
+        snack.embed(ids, table, out=torch.zeros(4, 7, device="cuda"))
+    with pytest.raises(snack.SnackError):
+        snack.embed(ids, table, out=table[:4])  # overlaps its table
+    with pytest.raises(ValueError):
+        snack.embed_grad(ids, torch.zeros(3, 8, device="cuda"), 10)
+    with pytest.raises(ValueError):
+        snack.embed_grad(ids, torch.zeros(4, 8, device="cuda"), 10, accumulate=True)
+    with pytest.raises(snack.SnackError):
+        snack.embed_grad(ids, torch.zeros(4, 8, device="cuda"), 0)
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    d = torch.zeros(4000, 8, device="cuda")
+    with pytest.raises(snack.SnackError) as e:
+        snack.snack_embed_grad(torch.zeros(4000, dtype=torch.int64, device="cuda"), d, 1.0, False, table, ws)
+    assert e.value.status == 4
