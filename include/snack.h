@@ -379,6 +379,52 @@ snack_status snack_embed_grad(const void *ids, snack_index ids_t, int64_t n, con
                               int64_t dtable_ld, void *ws, size_t ws_bytes, snack_stream_t stream);
 
 /*
+ * Softmax cross entropy of a projection to a vocabulary, without its logits:
+ *   z[i, v] = sum_d x[i, d] * w[v, d]
+ *   lse[i]  = log sum_v exp(z[i, v])
+ *   loss[i] = lse[i] - z[i, targets[i]]
+ * x [n, width] and w [vocab, width] in type t.  A target outside [0, vocab)
+ * (such as -100) marks a position that is not trained on: its loss is 0, and
+ * so is its row of the gradient; its row of x is still read and has to be
+ * finite when dw is wanted.  loss receives n values (SNACK_NONE), their sum
+ * over the trained positions (SNACK_SUM), or that divided by their count
+ * (SNACK_MEAN; 0 when there are none).  state (n + 1 fp32 values) keeps each
+ * row's lse, and 1 / count for the mean, for the gradient.
+ */
+typedef enum snack_reduction { SNACK_NONE = 0, SNACK_SUM = 1, SNACK_MEAN = 2 } snack_reduction;
+
+/*
+ * Workspace of snack_xent_fwd (grad == 0) or snack_xent_bwd (grad != 0); of x
+ * and w only the alignment is looked at, and has to be that of the call's
+ * (rows of bf16 matrices that are not 16-byte aligned are laid out again in
+ * the workspace, as are the bf16 parts of fp32 matrices).  It grows with n *
+ * vocab / 32 for the forward and holds at most about 256 MB of dz at a time
+ * for the gradient (1024 rows of the vocabulary at least).
+ * vocab < 2^30, n < 2^24, width < 2^20.
+ */
+snack_status snack_xent_workspace_size(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld,
+                                       int64_t vocab, int32_t width, snack_dtype t, int grad, size_t *bytes);
+
+snack_status snack_xent_fwd(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld, int64_t vocab,
+                            int32_t width, snack_dtype t, const void *targets, snack_index targets_t,
+                            snack_reduction reduction, float *loss, float *state, void *ws, size_t ws_bytes,
+                            snack_stream_t stream);
+
+/*
+ * The loss's gradients, from the same x, w and targets and the state that
+ * snack_xent_fwd left:
+ *   dz[i, v] = g_i * (exp(z[i, v] - lse[i]) - [v == targets[i]])
+ *   dx = dz w   [n, width],     dw = dz^T x   [vocab, width]      in type t
+ * with g_i = dloss[i] (SNACK_NONE), or *dloss (1 when dloss is NULL) times 1
+ * (SNACK_SUM) or 1 / count (SNACK_MEAN).  dx or dw may be NULL.  dz is rounded
+ * to bf16 for bf16 operands and kept to fp32 precision for fp32 ones.
+ */
+snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld, int64_t vocab,
+                            int32_t width, snack_dtype t, const void *targets, snack_index targets_t,
+                            snack_reduction reduction, const float *state, const float *dloss, void *dx, int64_t dx_ld,
+                            void *dw, int64_t dw_ld, void *ws, size_t ws_bytes, snack_stream_t stream);
+
+/*
  * Global norm of a model's gradients, and clipping:
  *   norm   = sqrt(sum over all tensors and elements of g^2)
  *   out[k] = g[k] * min(1, max_norm / (norm + 1e-6))

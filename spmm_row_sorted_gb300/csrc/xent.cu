@@ -1,0 +1,1106 @@
+// Softmax cross entropy of a projection to a vocabulary, and its gradient,
+// in pieces of the vocabulary; the logits are never kept.
+//
+//   z[i, v]  = sum_d x[i, d] w[v, d]
+//   lse[i]   = log sum_v exp z[i, v],   loss[i] = lse[i] - z[i, t_i]
+//   dz[i, v] = g_i (exp(z[i, v] - lse[i]) - [v = t_i])
+//   dx = dz w,   dw = dz^T x
+//
+// Four matrix products of 2 n V D operations each on the tensor cores (the
+// forward's logits, the same again for the gradient, dx and dw), all by one
+// kernel with four epilogues:
+//   stats  keeps of a logits tile only each row's maximum and sum of
+//          exponentials, per half tile, and the target's logit;
+//   dlog   turns a logits tile into dz, stored as bf16 for one piece of the
+//          vocabulary;
+//   dx     adds dz w of the piece to fp32 sums (a TMA reduction: one addition
+//          per element and piece, in the pieces' order);
+//   dw     writes the piece's rows of dw.
+// Bound by the tensor cores; for a few tokens by reading w once.
+//
+// One CTA per SM works through 128 x (64, 128 or 256) output tiles: a warp
+// loads operand tiles by TMA into a ring of stages, a warp issues the
+// tcgen05.mma, eight warps run the epilogue of one tile from one half of the
+// tensor memory while the next tile accumulates in the other.  Operands whose
+// rows run along K are K-major tiles (128-byte swizzle), the others (w for dx,
+// dz^T and x for dw) are read as they lie, as MN-major tiles: no transposes.
+//
+// fp32 operands are cut into three bf16 parts each (8 significant bits at a
+// time, 24 in all), and a product is the sum of the six part products down to
+// 2^-16 of the leading one, smallest first; what is left out is below 2^-24.
+// The parts, and bf16 operands whose rows are not 16-byte aligned, are laid
+// out in the workspace, w's by pieces of the vocabulary.
+//
+// Every wait on an mbarrier is bounded; when one runs out the CTA marks its
+// error word, waits (bounded) for what it has in flight, frees its tensor
+// memory and returns, and the kernel that finishes a call makes the losses, dx and the first row
+// of dw NaN.
+#include <cuda.h>
+#include <math.h>
+
+#include "internal.hpp"
+#include "lm.hpp"
+
+namespace snack {
+namespace {
+
+// ------------------------------------------------------------ PTX wrappers
+
+__device__ __forceinline__ uint32_t su32(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(bar)) : "memory");
+}
+constexpr int kSpinLimit = 1 << 20;  // try_wait rounds before a wait is declared stuck (far above any real wait)
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
+  const uint32_t a = su32(bar);
+  for (int i = 0; i < kSpinLimit; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(a), "r"(parity)
+        : "memory");
+    if (done) return true;
+  }
+  return false;
+}
+__device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(su32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(su32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap *map, const void *src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(su32(src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+__device__ __forceinline__ void tma_add(const CUtensorMap *map, const void *src, int x, int y, int z) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(su32(src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(dst)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// D (TMEM) (+)= A (smem) * B (smem)^T, bf16 with fp32 accumulation
+__device__ __forceinline__ void umma(uint32_t taddr, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                     uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(taddr),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(bar))
+               : "memory");
+}
+// 32 consecutive fp32 columns of this thread's TMEM lane
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Shared-memory descriptor of an operand tile with the 128-byte swizzle:
+// start (16-byte units), leading and stride byte offsets, version 1, layout
+// type 2.  K-major: 128-byte rows of 64 K elements, 8 rows to a 1024-byte
+// atom, stride 1024 from atom to atom (the leading offset is not used).
+// MN-major: boxes of 64 K rows of 64 MN elements (128 bytes each); 8 K rows
+// to an atom, stride 1024 from one to the next along K, and the leading
+// offset is the 8192 bytes from one box of 64 MN elements to the next.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t saddr, bool mn_major) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFF) >> 4);
+  d |= (uint64_t)(mn_major ? (8192 >> 4) : 1) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+// Instruction descriptor of kind::f16: fp32 accumulator (bit 4), A and B bf16
+// (bits 7 and 10), MN-major A and B (bits 15 and 16), N / 8 at bit 17, M / 16 at bit 24.
+__device__ __forceinline__ uint32_t inst_desc(int m, int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// ------------------------------------------------------------------ kernel
+
+constexpr int kM = 128;           // rows of an output tile, TMEM lanes
+constexpr int kNMax = 256;        // columns of the widest output tile
+constexpr int kKb = 64;           // K per stage
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = (kEpiWarps + 2) * 32;
+constexpr int kStageA = kM * kKb * 2;
+constexpr int kRing = 4 * (kStageA + kNMax * kKb * 2);  // bytes of the ring of stages
+constexpr int kMaxStages = 8;
+constexpr int kStaging = 4096;    // an epilogue warp's 32 rows x 128 bytes on their way out
+constexpr int kSmem = 1024 + kRing + kEpiWarps * kStaging + 256;
+static_assert(kSmem <= 232448, "shared memory of one CTA");
+static_assert(kStageA + 64 * kKb * 2 <= kRing / kMaxStages, "eight stages of the narrowest tile fit the ring");
+
+enum { kStats = 0, kDlog = 1, kDx = 2, kDw = 3 };
+
+struct GemmArgs {
+  int32_t m, n;             // rows and columns of the product
+  int32_t nt;               // columns of a tile
+  int32_t m_tiles, n_tiles, n_split;
+  int32_t k_blocks;         // of 64
+  int32_t products;         // part products per element (1: bf16, 6: fp32)
+  uint32_t a_part, b_part;  // 4 bits per product: its parts
+  int32_t stages;
+  uint32_t *err;            // [256] error words, one per CTA
+  int32_t first;            // the call's first launch writes every error word
+  // stats
+  float2 *part;             // [slots][m] (maximum, sum of exp(z - maximum)) per half tile
+  int32_t slot0;
+  float *zt;                // [m] the target's logit
+  // stats, dlog
+  TokenSrc targets;
+  int32_t v0;               // first vocabulary row of the piece
+  // dlog
+  const float *lse;         // [m], and 1 / count at [m]
+  const float *dloss;       // upstream gradient: [m], one value, or null (1)
+  int32_t per_row;          // dloss has a value per row
+  int32_t out_parts;        // bf16 parts of dz
+  // dx
+  int32_t add;              // add to the sums (else write them)
+  // dw
+  void *out;                // first row of the piece; used where TMA cannot store
+  int64_t out_ld;
+  int32_t out_wide;         // fp32 (else bf16)
+  int32_t out_tma;
+};
+
+// the six part products, smallest first: parts (2,0) (1,1) (0,2) (1,0) (0,1) (0,0)
+constexpr uint32_t kPartA = 0x001012u, kPartB = 0x010210u;
+
+// Byte offset of 16-byte chunk c of row r in a warp's staging tile (32 rows
+// of 128 bytes, 128-byte swizzle: what the store's tensor map undoes).
+__device__ __forceinline__ uint32_t stage_off(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int kMode>
+__global__ void __launch_bounds__(kThreads, 1) k_xent(const __grid_constant__ CUtensorMap map_a,
+                                                      const __grid_constant__ CUtensorMap map_b,
+                                                      const __grid_constant__ CUtensorMap map_o, const GemmArgs P) {
+  pdl_wait();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  constexpr bool kAmn = kMode == kDw, kBmn = kMode == kDx || kMode == kDw;
+  const uint32_t stage_bytes = (uint32_t)(kStageA + P.nt * kKb * 2);
+  uint8_t *staging = smem + kRing;
+  uint64_t *full = reinterpret_cast<uint64_t *>(staging + kEpiWarps * kStaging);
+  uint64_t *empty = full + kMaxStages;
+  uint64_t *acc_full = empty + kMaxStages;  // [2]
+  uint64_t *acc_free = acc_full + 2;        // [2]
+  uint64_t *drained = acc_free + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
+  int *bad = reinterpret_cast<int *>(tmem_slot + 1);
+  int *loads = bad + 1;  // stages loaded so far
+  static_assert(8 * (2 * kMaxStages + 5) + 16 <= 256, "barriers and flags fit their 256 bytes");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_free[b], kEpiWarps);
+    }
+    mbar_init(drained, 1);
+    *bad = 0;
+    *loads = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int tiles = P.m_tiles * P.n_tiles * P.n_split;
+  const int per_split = (P.k_blocks + P.n_split - 1) / P.n_split;
+  bool ok = true;
+  // a tile: its row and column of tiles, its share of K; neighbours in the
+  // order share the operand that the other dimension re-reads
+  struct Tile {
+    int m0, n0, split, k0, nk;
+  };
+  auto tile_at = [&](int t) {
+    Tile r;
+    r.split = t / (P.m_tiles * P.n_tiles);
+    const int mn = t - r.split * (P.m_tiles * P.n_tiles);
+    if (kMode == kDw) {  // columns (D) run fastest: a row of tiles shares the piece's dz^T
+      r.m0 = mn / P.n_tiles * kM;
+      r.n0 = mn % P.n_tiles * P.nt;
+    } else {
+      r.m0 = mn % P.m_tiles * kM;
+      r.n0 = mn / P.m_tiles * P.nt;
+    }
+    r.k0 = r.split * per_split;
+    r.nk = max(0, min(P.k_blocks, r.k0 + per_split) - r.k0);
+    return r;
+  };
+
+  if (warp == kEpiWarps) {  // ------------------------------------------- loads
+    if (lane == 0) {
+      uint32_t it = 0;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        const Tile q = tile_at(t);
+        for (int c = 0; c < P.products && ok; ++c) {
+          const int za = (P.a_part >> (4 * c)) & 15, zb = (P.b_part >> (4 * c)) & 15;
+          for (int kb = q.k0; kb < q.k0 + q.nk; ++kb, ++it) {
+            const int s = (int)(it % P.stages);
+            if (!mbar_wait(&empty[s], ((it / P.stages) & 1) ^ 1)) {
+              ok = false;
+              break;
+            }
+            uint8_t *a = smem + (uint32_t)s * stage_bytes, *b = a + kStageA;
+            mbar_expect_tx(&full[s], stage_bytes);
+            if (kAmn) {
+              tma_load(a, &map_a, q.m0, kb * kKb, za, &full[s]);
+              tma_load(a + 8192, &map_a, q.m0 + 64, kb * kKb, za, &full[s]);
+            } else {
+              tma_load(a, &map_a, kb * kKb, q.m0, za, &full[s]);
+            }
+            if (kBmn) {
+              for (int j = 0; j < P.nt; j += 64) tma_load(b + j * 128, &map_b, q.n0 + j, kb * kKb, zb, &full[s]);
+            } else {
+              tma_load(b, &map_b, kb * kKb, q.n0, zb, &full[s]);
+            }
+            *loads = (int)it + 1;
+          }
+        }
+      }
+    }
+  } else if (warp == kEpiWarps + 1) {  // -------------------------------- MMAs
+    if (lane == 0) {
+      const uint32_t idesc = inst_desc(kM, P.nt, kAmn, kBmn);
+      uint32_t it = 0;
+      int n_acc = 0;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        const Tile q = tile_at(t);
+        if (q.nk == 0) continue;
+        const int buf = n_acc & 1;
+        if (!mbar_wait(&acc_free[buf], ((n_acc >> 1) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(buf * kNMax);
+        const int steps = P.products * q.nk;
+        for (int i = 0; i < steps; ++i, ++it) {
+          const int s = (int)(it % P.stages);
+          if (!mbar_wait(&full[s], (it / P.stages) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = su32(smem) + (uint32_t)s * stage_bytes, b = a + kStageA;
+#pragma unroll
+          for (int k = 0; k < kKb / 16; ++k) {
+            // 16 K elements: 32 bytes within the swizzled row, or 16 rows of 128 bytes
+            const uint64_t da = tile_desc(a + (kAmn ? k * 2048 : k * 32), kAmn);
+            const uint64_t db = tile_desc(b + (kBmn ? k * 2048 : k * 32), kBmn);
+            umma(d, da, db, idesc, (i | k) != 0);
+          }
+          umma_commit(&empty[s]);
+        }
+        if (!ok) break;
+        umma_commit(&acc_full[buf]);
+        ++n_acc;
+      }
+      umma_commit(drained);
+    }
+  } else {  // -------------------------------------------------------- epilogue
+    const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter .. +31; half of the columns
+    uint8_t *stage = staging + warp * kStaging;
+    constexpr float kLog2e = 1.4426950408889634f;
+    int n_acc = 0;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const Tile q = tile_at(t);
+      if (q.nk == 0) continue;
+      const int buf = n_acc & 1;
+      const int row = q.m0 + quarter * 32 + lane;
+      const bool row_ok = row < P.m;
+      const int c_end = P.nt / 2;  // columns of this half
+      const int col0 = q.n0 + half * c_end;
+      const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * kNMax + half * c_end);
+      // the target's column of this tile's half, or below zero
+      int tcol = -1;
+      float lse = 0.f, g = 0.f;
+      if (kMode == kStats || kMode == kDlog) {
+        if (row_ok) {
+          const uint32_t id = P.targets.key(row);
+          if (id < P.targets.vocab) {
+            tcol = (int)id - P.v0 - col0;
+            if (kMode == kDlog) {
+              lse = P.lse[row];
+              g = (P.dloss ? P.dloss[P.per_row ? row : 0] : 1.f) * P.lse[P.m];
+            }
+          }
+        }
+      }
+      if (!mbar_wait(&acc_full[buf], (n_acc >> 1) & 1)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      if (kMode == kStats) {
+        float mx = -INFINITY, sum = 0.f;
+        for (int c = 0; c < c_end; c += 32) {
+          float v[32];
+          tmem_ld32(acc + (uint32_t)c, v);
+          const int valid = P.n - col0 - c;
+          if (valid < 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j >= valid) v[j] = -INFINITY;
+          }
+          if (tcol >= c && tcol < c + 32) {
+            float z = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (tcol == c + j) z = v[j];
+            P.zt[row] = z;
+          }
+          float m4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+          for (int j = 4; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], v[j]);
+          const float nm = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+          const float base = nm == -INFINITY ? 0.f : nm;  // a row of -inf so far: every term is 0
+          float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 32; ++j) s4[j & 3] += ex2((v[j] - base) * kLog2e);
+          sum = sum * ex2((mx - base) * kLog2e) + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
+          mx = nm;
+        }
+        if (row_ok)
+          P.part[(size_t)(P.slot0 + 2 * (q.n0 / P.nt) + half) * (size_t)P.m + row] = make_float2(mx, sum);
+      } else if (kMode == kDlog) {
+        for (int c = 0; c < c_end; c += 32) {
+          float v[32];
+          tmem_ld32(acc + (uint32_t)c, v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float p = ex2((v[j] - lse) * kLog2e);
+            v[j] = g == 0.f ? 0.f : g * (tcol == c + j ? p - 1.f : p);
+          }
+          // 32 rows x 64 bytes per store
+          for (int part = 0; part < P.out_parts; ++part) {
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+              uint4 u;
+              u.x = pack_bf16(v[8 * ch], v[8 * ch + 1]);
+              u.y = pack_bf16(v[8 * ch + 2], v[8 * ch + 3]);
+              u.z = pack_bf16(v[8 * ch + 4], v[8 * ch + 5]);
+              u.w = pack_bf16(v[8 * ch + 6], v[8 * ch + 7]);
+              *reinterpret_cast<uint4 *>(stage + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) = u;
+              if (P.out_parts > 1) {  // what the part leaves over
+                v[8 * ch] -= bf16_lo(u.x);
+                v[8 * ch + 1] -= bf16_hi(u.x);
+                v[8 * ch + 2] -= bf16_lo(u.y);
+                v[8 * ch + 3] -= bf16_hi(u.y);
+                v[8 * ch + 4] -= bf16_lo(u.z);
+                v[8 * ch + 5] -= bf16_hi(u.z);
+                v[8 * ch + 6] -= bf16_lo(u.w);
+                v[8 * ch + 7] -= bf16_hi(u.w);
+              }
+            }
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0 && col0 + c < P.n && q.m0 + quarter * 32 < P.m) {
+              tma_store(&map_o, stage, col0 + c, q.m0 + quarter * 32, part);
+              bulk_commit();
+            }
+          }
+        }
+      } else {
+        const bool wide = kMode == kDx || P.out_wide;
+        const int step = wide ? 32 : 64;  // columns of 128 bytes
+        for (int c = 0; c < c_end; c += 32) {
+          float v[32];
+          tmem_ld32(acc + (uint32_t)c, v);
+          if (lane == 0 && (c % step) == 0) bulk_wait_read();
+          __syncwarp();
+          if (wide) {
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch)
+              *reinterpret_cast<float4 *>(stage + stage_off(lane, ch)) =
+                  make_float4(v[4 * ch], v[4 * ch + 1], v[4 * ch + 2], v[4 * ch + 3]);
+          } else {
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+              uint4 u;
+              u.x = pack_bf16(v[8 * ch], v[8 * ch + 1]);
+              u.y = pack_bf16(v[8 * ch + 2], v[8 * ch + 3]);
+              u.z = pack_bf16(v[8 * ch + 4], v[8 * ch + 5]);
+              u.w = pack_bf16(v[8 * ch + 6], v[8 * ch + 7]);
+              *reinterpret_cast<uint4 *>(stage + stage_off(lane, ch + ((c & 32) >> 3))) = u;
+            }
+          }
+          if ((c + 32) % step != 0 && c + 32 < c_end) continue;  // the row's other half first
+          const int x0 = col0 + c / step * step;
+          if (kMode == kDx || P.out_tma) {
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0 && x0 < P.n && q.m0 + quarter * 32 < P.m) {
+              if (kMode == kDx && P.add)
+                tma_add(&map_o, stage, x0, q.m0 + quarter * 32, q.split);
+              else
+                tma_store(&map_o, stage, x0, q.m0 + quarter * 32, kMode == kDx ? q.split : 0);
+              bulk_commit();
+            }
+          } else {  // rows that TMA cannot address: a warp writes one after the other
+            __syncwarp();
+            const int have = min(step, c_end - c / step * step);  // a 64-wide tile's half has 32 columns
+            for (int r = 0; r < 32; ++r) {
+              const int orow = q.m0 + quarter * 32 + r;
+              if (orow >= P.m) break;
+              for (int j = lane; j < have && x0 + j < P.n; j += 32) {
+                if (wide)
+                  reinterpret_cast<float *>(P.out)[(int64_t)orow * P.out_ld + x0 + j] =
+                      *reinterpret_cast<const float *>(stage + stage_off(r, j >> 2) + (j & 3) * 4);
+                else
+                  reinterpret_cast<uint16_t *>(P.out)[(int64_t)orow * P.out_ld + x0 + j] =
+                      *reinterpret_cast<const uint16_t *>(stage + stage_off(r, j >> 3) + (j & 7) * 2);
+              }
+            }
+            __syncwarp();
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_free[buf]);
+      ++n_acc;
+    }
+    if (lane == 0) bulk_wait();
+  }
+  if (!ok) *bad = 1;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const bool failed = *bad != 0;
+    if (failed) {  // every load and MMA issued has completed (bounded) before the tensor memory is given back
+      const int n = *loads;
+      for (int g = n - 1; g >= 0 && g >= n - P.stages; --g) mbar_wait(&full[g % P.stages], (g / P.stages) & 1);
+      mbar_wait(drained, 0);
+    }
+    if (P.first) {
+      for (int e = blockIdx.x; e < 256; e += gridDim.x) P.err[e] = failed ? 1u : 0u;
+    } else if (failed) {
+      P.err[blockIdx.x & 255] = 1u;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+__device__ __forceinline__ bool any_error(const uint32_t *err) {
+  uint32_t e = 0;
+  for (int i = threadIdx.x; i < 256; i += blockDim.x) e |= err[i];
+  return __syncthreads_or((int)e) != 0;
+}
+
+// Per row: the maximum and sum over all slots, the loss, the kept state.
+// Eight rows per block, 32 threads per row, each over every 32nd slot.
+__global__ void __launch_bounds__(256) k_xent_join(const float2 *__restrict__ part, int slots, int m,
+                                                   const float *__restrict__ zt, TokenSrc targets,
+                                                   float *__restrict__ loss, float *__restrict__ state,
+                                                   const uint32_t *__restrict__ err) {
+  pdl_wait();
+  const bool bad = any_error(err);
+  __shared__ float2 red[32][9];
+  const int r = threadIdx.x & 7, q = threadIdx.x >> 3;
+  const int row = blockIdx.x * 8 + r;
+  float mx = -INFINITY, sum = 0.f;
+  if (row < m) {
+    for (int s = q; s < slots; s += 32) {
+      const float2 p = part[(size_t)s * (size_t)m + row];
+      const float nm = fmaxf(mx, p.x);
+      if (nm != -INFINITY) {
+        sum = sum * expf(mx - nm) + p.y * expf(p.x - nm);
+        mx = nm;
+      } else {
+        sum += p.y;  // zero, or a NaN to keep
+      }
+    }
+  }
+  red[q][r] = make_float2(mx, sum);
+  __syncthreads();
+  if (threadIdx.x < 8 && row < m) {
+    mx = -INFINITY;
+    sum = 0.f;
+    for (int s = 0; s < 32; ++s) {
+      const float2 p = red[s][threadIdx.x];
+      const float nm = fmaxf(mx, p.x);
+      if (nm != -INFINITY) {
+        sum = sum * expf(mx - nm) + p.y * expf(p.x - nm);
+        mx = nm;
+      } else {
+        sum += p.y;
+      }
+    }
+    float lse = mx + logf(sum);
+    if (bad) lse = NAN;
+    state[row] = lse;
+    loss[row] = targets.key(row) < targets.vocab ? lse - zt[row] : 0.f;
+    if (row == 0) state[m] = 1.f;
+  }
+}
+
+// The sum or mean of the losses, and 1 / count beside the rows' state.
+__global__ void __launch_bounds__(1024) k_xent_total(const float *__restrict__ row_loss, int m, TokenSrc targets,
+                                                     int mean, float *__restrict__ loss, float *__restrict__ state) {
+  pdl_wait();
+  __shared__ double sl[32];
+  __shared__ int sc[32];
+  double s = 0;
+  int c = 0;
+  for (int i = threadIdx.x; i < m; i += 1024) {
+    s += (double)row_loss[i];
+    c += targets.key(i) < targets.vocab ? 1 : 0;
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, d);
+    c += __shfl_xor_sync(0xffffffffu, c, d);
+  }
+  if ((threadIdx.x & 31) == 0) {
+    sl[threadIdx.x >> 5] = s;
+    sc[threadIdx.x >> 5] = c;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0;
+    c = 0;
+    for (int w = 0; w < 32; ++w) {
+      s += sl[w];
+      c += sc[w];
+    }
+    const int n = c > 0 ? c : 1;
+    *loss = (float)(mean ? s / n : s);
+    state[m] = mean ? 1.f / (float)n : 1.f;
+  }
+}
+
+// [rows][width] into `parts` planes of bf16 [rows][out_ld]: the value, what
+// its rounding to bf16 leaves over, and what that leaves over.
+template <typename T>
+__global__ void __launch_bounds__(256) k_xent_pack(const T *__restrict__ in, int64_t ld, int64_t rows, int32_t width,
+                                                   int parts, bf16 *__restrict__ out, int32_t out_ld, int64_t plane) {
+  pdl_wait();
+  const int groups = out_ld / 8;
+  const int64_t total = rows * groups;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / groups;
+    const int c = (int)(i - r * groups) * 8;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < width ? to_f32(in[r * ld + c + j]) : 0.f;
+    for (int p = 0; p < parts; ++p) {
+      Pack<bf16, 16> o;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float h = __bfloat162float(__float2bfloat16_rn(v[j]));
+        if (isinf(h) && !isinf(v[j])) h = __uint_as_float(__float_as_uint(v[j]) & 0xFFFF0000u);  // rounded past the largest
+        o.set(j, h);
+        v[j] = isfinite(v[j]) ? v[j] - h : 0.f;
+      }
+      reinterpret_cast<uint4 *>(out + p * plane + r * out_ld + c)[0] = o.raw;
+    }
+  }
+}
+
+// dx = the splits' sums, added in order and rounded once.  The last kernel of a
+// gradient: after an error it makes dx and the first row of dw NaN.
+template <typename T>
+__global__ void __launch_bounds__(256) k_xent_dx(const float *__restrict__ acc, int splits, int64_t plane, int32_t acc_ld,
+                                                 int32_t m, int32_t width, T *__restrict__ dx, int64_t ld,
+                                                 T *__restrict__ dw, const uint32_t *__restrict__ err) {
+  pdl_wait();
+  const bool bad = any_error(err);
+  if (bad && dw && blockIdx.x == 0)
+    for (int i = threadIdx.x; i < width; i += 256) dw[i] = from_f32<T>(NAN);
+  const int groups = acc_ld / 4;
+  const int64_t total = (int64_t)m * groups;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / groups;
+    const int c = (int)(i - r * groups) * 4;
+    float4 s = *reinterpret_cast<const float4 *>(acc + r * acc_ld + c);
+    for (int k = 1; k < splits; ++k) {
+      const float4 b = *reinterpret_cast<const float4 *>(acc + k * plane + r * acc_ld + c);
+      s.x += b.x;
+      s.y += b.y;
+      s.z += b.z;
+      s.w += b.w;
+    }
+    if (bad) s = make_float4(NAN, NAN, NAN, NAN);
+    T *o = dx + r * ld + c;
+    const float e[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c + j < width) o[j] = from_f32<T>(e[j]);
+  }
+}
+
+// ------------------------------------------------------------ host side
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+  static const EncodeTiled fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// planes x rows x cols (cols contiguous, rows ld elements apart) in boxes of
+// box_rows rows of box_cols columns; zero fill outside
+bool make_map(CUtensorMap *m, const void *base, bool wide, uint64_t cols, uint64_t rows, uint64_t ld, uint64_t planes,
+              uint64_t plane, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+  EncodeTiled enc = encoder();
+  if (!enc) return false;
+  const uint64_t es = wide ? 4 : 2;
+  const cuuint64_t dims[3] = {cols, rows, planes};
+  const cuuint64_t strides[2] = {ld * es, plane * es};
+  const cuuint32_t box[3] = {box_cols, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A matrix as the products read it: bf16, 16-byte aligned rows, one or three planes.
+struct Operand {
+  const void *p;
+  int64_t rows, ld, plane;
+  int32_t cols, planes;
+};
+bool load_map(CUtensorMap *m, const Operand &o, bool mn_major, uint32_t box_rows) {
+  return make_map(m, o.p, false, (uint64_t)o.cols, (uint64_t)o.rows, (uint64_t)o.ld, (uint64_t)o.planes,
+                  (uint64_t)(o.plane > 0 ? o.plane : o.rows * o.ld), 64, mn_major ? 64 : box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+constexpr size_t kPieceBytes = (size_t)256 << 20;  // of dz, or of w's parts, at a time
+
+int sms_of() {
+  const int n = current_sms();
+  return n < 1 ? 152 : n > 256 ? 256 : n;
+}
+
+// The widest tile that still gives every SM one; narrower tiles share a small
+// product among more SMs.
+int tile_cols(int64_t m_tiles, int64_t n, int sms) {
+  for (int nt = 256; nt > 64; nt /= 2)
+    if (m_tiles * ceil_div(n, nt) >= sms) return nt;
+  return 64;
+}
+
+// Equal pieces of the vocabulary, multiples of 256 rows, of at most `bytes` each.
+int64_t piece_rows(int64_t vocab, int64_t row_bytes) {
+  int64_t most = (int64_t)(kPieceBytes / (size_t)row_bytes) / 256 * 256;
+  if (most < 1024) most = 1024;
+  const int64_t pieces = ceil_div(vocab, most);
+  return ceil_div(ceil_div(vocab, pieces), 256) * 256;
+}
+
+// How many ways the K of a product is split: the choice whose last wave of
+// tiles wastes least, each tile counted as its K blocks and the fixed cost of
+// eight more.
+int pick_split(int64_t tiles, int64_t k_steps, int sms) {
+  int best = 1;
+  int64_t best_cost = INT64_MAX;
+  for (int s = 1; s <= 8; ++s) {
+    const int64_t per = ceil_div(k_steps, s);
+    if (s > 1 && (per < 8 || (s - 1) * per >= k_steps)) break;
+    const int64_t cost = ceil_div(tiles * s, sms) * (per + 8);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+struct XentShape {
+  int32_t n, width;
+  int64_t vocab;
+  snack_dtype t;
+  bool pack_x, pack_w;
+  int parts;
+  int32_t ld;  // row length of packed planes
+  int sms;
+};
+
+struct XentWs {
+  size_t err, zt, row_loss, part, xp, wp, dz, acc, total;
+  int nt;             // forward tile
+  int64_t piece;      // vocabulary rows at a time (forward: of packed w; gradient: of dz)
+  int64_t slots;
+  int64_t dz_ld;
+  int32_t acc_ld;
+  int nt_d, split;    // dx, dw tile columns; K splits of dx
+};
+
+XentWs xent_ws(const XentShape &s, bool grad) {
+  XentWs w = {};
+  size_t o = 0;
+  const int64_t m_tiles = ceil_div(s.n, kM);
+  w.err = o;
+  o += align_up(256 * 4, kAlign);
+  const int64_t w_row = (int64_t)s.parts * s.ld * 2;
+  w.nt = tile_cols(m_tiles, s.vocab, s.sms);
+  w.xp = o;
+  if (s.pack_x) o += align_up((size_t)s.parts * (size_t)s.n * (size_t)s.ld * 2, kAlign);
+  if (!grad) {
+    w.piece = s.pack_w ? piece_rows(s.vocab, w_row) : s.vocab;
+    if (w.piece > s.vocab) w.piece = s.vocab;
+    w.slots = 2 * (ceil_div(s.vocab, w.piece) * ceil_div(w.piece, w.nt));
+    w.zt = o;
+    o += align_up((size_t)s.n * 4, kAlign);
+    w.row_loss = o;
+    o += align_up((size_t)s.n * 4, kAlign);
+    w.part = o;
+    o += align_up((size_t)w.slots * (size_t)s.n * 8, kAlign);
+  } else {
+    const int64_t dz_row = (int64_t)s.parts * s.n * 2;
+    w.piece = piece_rows(s.vocab, s.pack_w && w_row > dz_row ? w_row : dz_row);
+    if (w.piece > s.vocab) w.piece = s.vocab;
+    w.dz_ld = ceil_div(w.piece, 64) * 64;
+    w.nt_d = s.width > 128 ? 256 : s.width > 64 ? 128 : 64;
+    w.acc_ld = (int32_t)align_up((size_t)s.width, 4);
+    w.split = pick_split(m_tiles * ceil_div(s.width, w.nt_d), ceil_div(w.piece, kKb), s.sms);
+    w.dz = o;
+    o += align_up((size_t)s.parts * (size_t)s.n * (size_t)w.dz_ld * 2, kAlign);
+    w.acc = o;
+    o += align_up((size_t)w.split * (size_t)s.n * (size_t)w.acc_ld * 4, kAlign);
+  }
+  w.wp = o;
+  if (s.pack_w) o += align_up((size_t)s.parts * (size_t)w.piece * (size_t)s.ld * 2, kAlign);
+  w.total = o;
+  return w;
+}
+
+bool rows_ready(const void *p, int64_t ld) { return ptr_aligned(p, 16) && ld % 8 == 0; }
+
+XentShape xent_shape(const void *x, int64_t x_ld, int32_t n, const void *wt, int64_t w_ld, int64_t vocab, int32_t width,
+                     snack_dtype t) {
+  XentShape s;
+  s.n = n;
+  s.width = width;
+  s.vocab = vocab;
+  s.t = t;
+  s.parts = t == SNACK_F32 ? 3 : 1;
+  s.pack_x = t == SNACK_F32 || !rows_ready(x, x_ld);
+  s.pack_w = t == SNACK_F32 || !rows_ready(wt, w_ld);
+  s.ld = (int32_t)align_up((size_t)width, 8);
+  s.sms = sms_of();
+  return s;
+}
+
+template <int kMode>
+cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o, GemmArgs &g, int sms,
+                        cudaStream_t s) {
+  cudaError_t e = raise_smem_limit(k_xent<kMode>, kSmem);
+  if (e != cudaSuccess) return e;
+  g.m_tiles = (int32_t)ceil_div(g.m, kM);
+  g.n_tiles = (int32_t)ceil_div(g.n, g.nt);
+  g.stages = kRing / (kStageA + g.nt * kKb * 2);
+  if (g.stages > kMaxStages) g.stages = kMaxStages;
+  const int64_t tiles = (int64_t)g.m_tiles * g.n_tiles * g.n_split;
+  if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+  e = launch_pdl(k_xent<kMode>, (unsigned)(tiles < sms ? tiles : sms), kThreads, kSmem, s, a, b, o, (const GemmArgs)g);
+  g.first = 0;
+  return e;
+}
+
+cudaError_t pack(const XentShape &s, const void *in, int64_t ld, int64_t rows, void *out, cudaStream_t st) {
+  const int64_t total = rows * (s.ld / 8);
+  int64_t blocks = ceil_div(total, 256);
+  if (blocks > (int64_t)s.sms * 32) blocks = (int64_t)s.sms * 32;
+  if (s.t == SNACK_F32)
+    return launch_pdl(k_xent_pack<float>, (unsigned)blocks, 256, 0, st, reinterpret_cast<const float *>(in), ld, rows,
+                      s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld);
+  return launch_pdl(k_xent_pack<bf16>, (unsigned)blocks, 256, 0, st, reinterpret_cast<const bf16 *>(in), ld, rows,
+                    s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld);
+}
+
+// x, or a piece of w from row v0 on, as the products read it
+cudaError_t operand(const XentShape &s, bool packed, const void *p, int64_t ld, int64_t v0, int64_t rows, void *buf,
+                    Operand *o, cudaStream_t st) {
+  const size_t es = dtype_size(s.t);
+  const uint8_t *at = reinterpret_cast<const uint8_t *>(p) + (size_t)v0 * (size_t)ld * es;
+  o->rows = rows;
+  o->cols = s.width;
+  if (!packed) {
+    o->p = at;
+    o->ld = ld;
+    o->planes = 1;
+    o->plane = 0;
+    return cudaSuccess;
+  }
+  o->p = buf;
+  o->ld = s.ld;
+  o->planes = s.parts;
+  o->plane = rows * s.ld;
+  return pack(s, at, ld, rows, buf, st);
+}
+
+GemmArgs gemm_args(const XentShape &s, uint8_t *ws, const XentWs &W, int first) {
+  GemmArgs g = {};
+  g.n_split = 1;
+  g.products = s.parts == 3 ? 6 : 1;
+  g.a_part = s.parts == 3 ? kPartA : 0;
+  g.b_part = s.parts == 3 ? kPartB : 0;
+  g.err = reinterpret_cast<uint32_t *>(ws + W.err);
+  g.first = first;
+  return g;
+}
+
+snack_status xent_check(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld, int64_t vocab, int32_t width,
+                        snack_dtype t) {
+  if (!lm_dtype_ok(t) || n < 0 || vocab < 1 || width < 1 || x_ld < width || w_ld < width) return SNACK_ERR_INVALID_ARG;
+  const size_t es = dtype_size(t);
+  if (!ptr_aligned(x, es) || !ptr_aligned(w, es)) return SNACK_ERR_INVALID_ARG;
+  // tile counts and the row steps of tensor maps stay within 31 and 40 bits
+  if (vocab >= ((int64_t)1 << 30) || n >= (1 << 24) || width >= (1 << 20) || x_ld >= ((int64_t)1 << 36) ||
+      w_ld >= ((int64_t)1 << 36))
+    return SNACK_ERR_UNSUPPORTED;
+  return SNACK_OK;
+}
+
+}  // namespace
+}  // namespace snack
+
+using namespace snack;
+
+#define XENT_CUDA(x)                               \
+  do {                                             \
+    if ((x) != cudaSuccess) return SNACK_ERR_CUDA; \
+  } while (0)
+
+extern "C" {
+
+snack_status snack_xent_workspace_size(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld,
+                                       int64_t vocab, int32_t width, snack_dtype t, int grad, size_t *bytes) {
+  if (!bytes) return SNACK_ERR_INVALID_ARG;
+  const snack_status st = xent_check(x, x_ld, n, w, w_ld, vocab, width, t);
+  if (st != SNACK_OK) return st;
+  *bytes = n == 0 ? 0 : xent_ws(xent_shape(x, x_ld, n, w, w_ld, vocab, width, t), grad != 0).total;
+  return SNACK_OK;
+}
+
+snack_status snack_xent_fwd(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld, int64_t vocab,
+                            int32_t width, snack_dtype t, const void *targets, snack_index targets_t,
+                            snack_reduction reduction, float *loss, float *state, void *ws, size_t ws_bytes,
+                            snack_stream_t stream) try {
+  const snack_status ck = xent_check(x, x_ld, n, w, w_ld, vocab, width, t);
+  if (ck != SNACK_OK) return ck;
+  if (!lm_index_ok(targets_t) || reduction < SNACK_NONE || reduction > SNACK_MEAN) return SNACK_ERR_INVALID_ARG;
+  if (!loss || !state || !ptr_aligned(loss, 4) || !ptr_aligned(state, 4)) return SNACK_ERR_INVALID_ARG;
+  if (n > 0 && (!x || !w || !targets || !ws || !ptr_aligned(targets, index_size(targets_t)) || !ptr_aligned(ws, kAlign)))
+    return SNACK_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const TokenSrc tg{targets, targets_t == SNACK_I64, (uint32_t)vocab};
+  if (n == 0) {
+    if (reduction != SNACK_NONE)
+      XENT_CUDA(launch_pdl(k_xent_total, 1, 1024, 0, s, (const float *)nullptr, 0, tg, reduction == SNACK_MEAN, loss, state));
+    return SNACK_OK;
+  }
+  const XentShape S = xent_shape(x, x_ld, n, w, w_ld, vocab, width, t);
+  const XentWs W = xent_ws(S, false);
+  if (ws_bytes < W.total) return SNACK_ERR_WORKSPACE;
+  uint8_t *b = reinterpret_cast<uint8_t *>(ws);
+  Operand ox, ow;
+  XENT_CUDA(operand(S, S.pack_x, x, x_ld, 0, n, b + W.xp, &ox, s));
+  CUtensorMap mx, mw;
+  if (!load_map(&mx, ox, false, kM)) return SNACK_ERR_CUDA;
+  GemmArgs g = gemm_args(S, b, W, 1);
+  g.m = n;
+  g.nt = W.nt;
+  g.k_blocks = (int32_t)ceil_div(width, kKb);
+  g.part = reinterpret_cast<float2 *>(b + W.part);
+  g.zt = reinterpret_cast<float *>(b + W.zt);
+  g.targets = tg;
+  for (int64_t v0 = 0; v0 < vocab; v0 += W.piece) {
+    const int64_t rows = vocab - v0 < W.piece ? vocab - v0 : W.piece;
+    XENT_CUDA(operand(S, S.pack_w, w, w_ld, v0, rows, b + W.wp, &ow, s));
+    if (!load_map(&mw, ow, false, (uint32_t)W.nt)) return SNACK_ERR_CUDA;
+    g.n = (int32_t)rows;
+    g.v0 = (int32_t)v0;
+    XENT_CUDA(launch_gemm<kStats>(mx, mw, mx, g, S.sms, s));
+    g.slot0 += 2 * g.n_tiles;
+  }
+  float *row_loss = reduction == SNACK_NONE ? loss : reinterpret_cast<float *>(b + W.row_loss);
+  XENT_CUDA(launch_pdl(k_xent_join, (unsigned)ceil_div(n, 8), 256, 0, s, (const float2 *)g.part, g.slot0, n,
+                       (const float *)g.zt, tg, row_loss, state, (const uint32_t *)g.err));
+  if (reduction != SNACK_NONE)
+    XENT_CUDA(launch_pdl(k_xent_total, 1, 1024, 0, s, (const float *)row_loss, n, tg, reduction == SNACK_MEAN, loss, state));
+  return SNACK_OK;
+} catch (...) {  // a host allocation failed
+  return SNACK_ERR_CUDA;
+}
+
+snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld, int64_t vocab,
+                            int32_t width, snack_dtype t, const void *targets, snack_index targets_t,
+                            snack_reduction reduction, const float *state, const float *dloss, void *dx, int64_t dx_ld,
+                            void *dw, int64_t dw_ld, void *ws, size_t ws_bytes, snack_stream_t stream) try {
+  const snack_status ck = xent_check(x, x_ld, n, w, w_ld, vocab, width, t);
+  if (ck != SNACK_OK) return ck;
+  const size_t es = dtype_size(t);
+  if (!lm_index_ok(targets_t) || reduction < SNACK_NONE || reduction > SNACK_MEAN) return SNACK_ERR_INVALID_ARG;
+  if ((dx && (dx_ld < width || !ptr_aligned(dx, es))) || (dw && (dw_ld < width || !ptr_aligned(dw, es))))
+    return SNACK_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (n == 0) {
+    if (dw) XENT_CUDA(cudaMemset2DAsync(dw, (size_t)dw_ld * es, 0, (size_t)width * es, (size_t)vocab, s));
+    return SNACK_OK;
+  }
+  if (!x || !w || !targets || !state || !ws || !ptr_aligned(targets, index_size(targets_t)) || !ptr_aligned(state, 4) ||
+      !ptr_aligned(ws, kAlign) || (dloss && !ptr_aligned(dloss, 4)) || (reduction == SNACK_NONE && !dloss))
+    return SNACK_ERR_INVALID_ARG;
+  const size_t nx = span_bytes(n, width, x_ld, es), nw = span_bytes(vocab, width, w_ld, es);
+  const size_t ndx = dx ? span_bytes(n, width, dx_ld, es) : 0, ndw = dw ? span_bytes(vocab, width, dw_ld, es) : 0;
+  if (spans_overlap(dx, ndx, x, nx) || spans_overlap(dx, ndx, w, nw) || spans_overlap(dw, ndw, x, nx) ||
+      spans_overlap(dw, ndw, w, nw) || spans_overlap(dx, ndx, dw, ndw))
+    return SNACK_ERR_INVALID_ARG;
+  const XentShape S = xent_shape(x, x_ld, n, w, w_ld, vocab, width, t);
+  const XentWs W = xent_ws(S, true);
+  if (ws_bytes < W.total) return SNACK_ERR_WORKSPACE;
+  if (!dx && !dw) return SNACK_OK;
+  uint8_t *b = reinterpret_cast<uint8_t *>(ws);
+  const bool wide = t == SNACK_F32;
+  Operand ox, ow;
+  XENT_CUDA(operand(S, S.pack_x, x, x_ld, 0, n, b + W.xp, &ox, s));
+  CUtensorMap mx, mw, mxt, mwt, mdz, mdzt, mdz_out, macc, mdw;
+  if (!load_map(&mx, ox, false, kM) || !load_map(&mxt, ox, true, 0)) return SNACK_ERR_CUDA;
+  if (!make_map(&macc, b + W.acc, true, (uint64_t)width, (uint64_t)n, (uint64_t)W.acc_ld, (uint64_t)W.split,
+                (uint64_t)n * (uint64_t)W.acc_ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+    return SNACK_ERR_CUDA;
+  int first = 1;
+  for (int64_t v0 = 0; v0 < vocab; v0 += W.piece) {
+    const int64_t rows = vocab - v0 < W.piece ? vocab - v0 : W.piece;
+    XENT_CUDA(operand(S, S.pack_w, w, w_ld, v0, rows, b + W.wp, &ow, s));
+    const Operand dz = {b + W.dz, n, W.dz_ld, (int64_t)n * W.dz_ld, (int32_t)rows, S.parts};
+    const int nt = tile_cols(ceil_div(n, kM), rows, S.sms);
+    if (!load_map(&mw, ow, false, (uint32_t)nt) || !load_map(&mwt, ow, true, 0) || !load_map(&mdz, dz, false, kM) ||
+        !load_map(&mdzt, dz, true, 0) ||
+        !make_map(&mdz_out, dz.p, false, (uint64_t)rows, (uint64_t)n, (uint64_t)W.dz_ld, (uint64_t)S.parts,
+                  (uint64_t)dz.plane, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+      return SNACK_ERR_CUDA;
+    GemmArgs g = gemm_args(S, b, W, first);
+    g.m = n;
+    g.n = (int32_t)rows;
+    g.nt = nt;
+    g.k_blocks = (int32_t)ceil_div(width, kKb);
+    g.targets = TokenSrc{targets, targets_t == SNACK_I64, (uint32_t)vocab};
+    g.v0 = (int32_t)v0;
+    g.lse = state;
+    g.dloss = dloss;
+    g.per_row = reduction == SNACK_NONE;
+    g.out_parts = S.parts;
+    XENT_CUDA(launch_gemm<kDlog>(mx, mw, mdz_out, g, S.sms, s));
+    first = 0;
+    if (dx) {
+      GemmArgs h = gemm_args(S, b, W, 0);
+      h.m = n;
+      h.n = width;
+      h.nt = W.nt_d;
+      h.n_split = W.split;
+      h.k_blocks = (int32_t)ceil_div(rows, kKb);
+      h.add = v0 > 0;
+      XENT_CUDA(launch_gemm<kDx>(mdz, mwt, macc, h, S.sms, s));
+    }
+    if (dw) {
+      GemmArgs h = gemm_args(S, b, W, 0);
+      h.m = (int32_t)rows;
+      h.n = width;
+      h.nt = W.nt_d;
+      h.k_blocks = (int32_t)ceil_div(n, kKb);
+      uint8_t *to = reinterpret_cast<uint8_t *>(dw) + (size_t)v0 * (size_t)dw_ld * es;
+      h.out = to;
+      h.out_ld = dw_ld;
+      h.out_wide = wide;
+      h.out_tma = ptr_aligned(to, 16) && (size_t)dw_ld * es % 16 == 0 && (wide || W.nt_d >= 128);
+      if (h.out_tma && !make_map(&mdw, to, wide, (uint64_t)width, (uint64_t)rows, (uint64_t)dw_ld, 1,
+                                 (uint64_t)rows * (uint64_t)dw_ld, wide ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+        return SNACK_ERR_CUDA;
+      XENT_CUDA(launch_gemm<kDw>(mdzt, mxt, h.out_tma ? mdw : mxt, h, S.sms, s));
+    }
+  }
+  const int64_t total = dx ? (int64_t)n * (W.acc_ld / 4) : 0;
+  int64_t blocks = ceil_div(total, 256);
+  if (blocks > (int64_t)S.sms * 16) blocks = (int64_t)S.sms * 16;
+  if (blocks < 1) blocks = 1;
+  const float *acc = reinterpret_cast<const float *>(b + W.acc);
+  const uint32_t *err = reinterpret_cast<const uint32_t *>(b + W.err);
+  if (wide)
+    XENT_CUDA(launch_pdl(k_xent_dx<float>, (unsigned)blocks, 256, 0, s, acc, W.split, (int64_t)n * W.acc_ld, W.acc_ld,
+                         dx ? n : 0, width, reinterpret_cast<float *>(dx), dx_ld, reinterpret_cast<float *>(dw), err));
+  else
+    XENT_CUDA(launch_pdl(k_xent_dx<bf16>, (unsigned)blocks, 256, 0, s, acc, W.split, (int64_t)n * W.acc_ld, W.acc_ld,
+                         dx ? n : 0, width, reinterpret_cast<bf16 *>(dx), dx_ld, reinterpret_cast<bf16 *>(dw), err));
+  return SNACK_OK;
+} catch (...) {  // a host allocation failed
+  return SNACK_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -28,6 +28,7 @@ STATUS_NAMES = {0: "SNACK_OK", 1: "SNACK_ERR_INVALID_ARG", 2: "SNACK_ERR_UNSORTE
                 8: "SNACK_ERR_NO_SPACE"}
 SNACK_F32, SNACK_BF16 = 0, 1
 SNACK_I32, SNACK_I64 = 0, 1
+REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
 
 EXPORTED = ("snack_query_sizes", "snack_create", "snack_spmm_fwd", "snack_spmm_fwd_noalloc", "snack_spmm_dx",
             "snack_spmm_fwd_gelu", "snack_spmm_dx_gelu", "snack_sddmm_dw", "snack_backward",
@@ -35,7 +36,7 @@ EXPORTED = ("snack_query_sizes", "snack_create", "snack_spmm_fwd", "snack_spmm_f
             "snack_restructure_rows", "snack_wait_plan", "snack_destroy", "snack_status_string", "snack_version",
             "snack_trace_start", "snack_trace_read", "snack_trace_stop", "snack_embed_fwd",
             "snack_embed_grad_workspace_size", "snack_embed_grad", "snack_clip_workspace_size",
-            "snack_clip_grad_norm")
+            "snack_clip_grad_norm", "snack_xent_workspace_size", "snack_xent_fwd", "snack_xent_bwd")
 
 
 class SnackLibraryMissing(RuntimeError):
@@ -122,6 +123,13 @@ def load(path: Optional[str] = None):
         lib.snack_clip_grad_norm.argtypes = [i32, ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(i64),
                                              ctypes.POINTER(st), f32, vp, vp, sz, vp]
         lib.snack_clip_grad_norm.restype = st
+        lib.snack_xent_workspace_size.argtypes = [vp, i64, i32, vp, i64, i64, i32, st, ctypes.c_int, ctypes.POINTER(sz)]
+        lib.snack_xent_workspace_size.restype = st
+        lib.snack_xent_fwd.argtypes = [vp, i64, i32, vp, i64, i64, i32, st, vp, st, st, vp, vp, vp, sz, vp]
+        lib.snack_xent_fwd.restype = st
+        lib.snack_xent_bwd.argtypes = [vp, i64, i32, vp, i64, i64, i32, st, vp, st, st, vp, vp, vp, i64, vp, i64, vp, sz,
+                                       vp]
+        lib.snack_xent_bwd.restype = st
         _lib = lib
         return lib
 
@@ -330,6 +338,29 @@ def snack_clip_grad_norm(grads, outs, numel, types, max_norm: float, norm, ws, s
                                        None if outs is None else (ctypes.c_void_p * n)(*outs),
                                        (ctypes.c_int64 * n)(*numel), (ctypes.c_int * n)(*types), max_norm, _ptr(norm),
                                        _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def snack_xent_workspace_size(x, w, grad: bool) -> int:
+    b = ctypes.c_size_t(0)
+    _check("snack_xent_workspace_size",
+           load().snack_xent_workspace_size(_ptr(x), x.stride(0), x.shape[0], _ptr(w), w.stride(0), w.shape[0],
+                                            w.shape[1], dtype_code(w.dtype), 1 if grad else 0, ctypes.byref(b)))
+    return b.value
+
+
+def snack_xent_fwd(x, w, targets, reduction: int, loss, state, ws, stream=None) -> None:
+    _check("snack_xent_fwd",
+           load().snack_xent_fwd(_ptr(x), x.stride(0), x.shape[0], _ptr(w), w.stride(0), w.shape[0], w.shape[1],
+                                 dtype_code(w.dtype), _ptr(targets), index_code(targets.dtype), reduction, _ptr(loss),
+                                 _ptr(state), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def snack_xent_bwd(x, w, targets, reduction: int, state, dloss, dx, dw, ws, stream=None) -> None:
+    _check("snack_xent_bwd",
+           load().snack_xent_bwd(_ptr(x), x.stride(0), x.shape[0], _ptr(w), w.stride(0), w.shape[0], w.shape[1],
+                                 dtype_code(w.dtype), _ptr(targets), index_code(targets.dtype), reduction, _ptr(state),
+                                 _ptr(dloss), _ptr(dx), 0 if dx is None else dx.stride(0), _ptr(dw),
+                                 0 if dw is None else dw.stride(0), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 # ------------------------------------------------------------- layer owner
@@ -609,3 +640,73 @@ def clip_grad_norm(grads, max_norm: float, out=None, stream=None) -> torch.Tenso
         snack_clip_grad_norm([g.data_ptr() for g in grads], [o.data_ptr() for o in outs], numel, types,
                              float(max_norm), norm, ws)
         return norm
+
+
+def _xent_args(x, w, targets, reduction):
+    if reduction not in REDUCTIONS:
+        raise ValueError(f"reduction must be one of {sorted(REDUCTIONS)}")
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1] or x.dtype != w.dtype:
+        raise ValueError("x [n, width] and w [vocab, width] must have one type and width")
+    if targets.numel() != x.shape[0]:
+        raise ValueError("targets needs one entry per row of x")
+    return _rows(x), _rows(w), targets.contiguous(), REDUCTIONS[reduction]
+
+
+def xent(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, reduction: str = "mean", stream=None):
+    """Softmax cross entropy of x w^T against targets, without the logits: (loss, state).
+
+    A target outside the vocabulary (such as -100) is not trained on.  state
+    (float32, n + 1) is what xent_grad needs beside the same arguments.
+    """
+    _same_device(x, w, targets)
+    with _Place(x, stream):
+        x, w, targets, red = _xent_args(x, w, targets, reduction)
+        n = x.shape[0]
+        loss = torch.empty((n,) if reduction == "none" else (), dtype=torch.float32, device=x.device)
+        state = torch.empty(n + 1, dtype=torch.float32, device=x.device)
+        ws = _workspace(snack_xent_workspace_size(x, w, False), x.device)
+        if n or reduction != "none":
+            snack_xent_fwd(x, w, targets, red, loss, state, ws)
+        return loss, state
+
+
+def xent_grad(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, state: torch.Tensor,
+              dloss: Optional[torch.Tensor] = None, reduction: str = "mean", want_dx: bool = True,
+              want_dw: bool = True, stream=None):
+    """(dx, dw) of xent for an upstream gradient dloss (1 when None; one value per row for "none")."""
+    _same_device(x, w, targets, state, dloss)
+    with _Place(x, stream):
+        x, w, targets, red = _xent_args(x, w, targets, reduction)
+        if state.dtype != torch.float32 or state.numel() != x.shape[0] + 1 or not state.is_contiguous():
+            raise ValueError("state must be what xent returned for these arguments")
+        if dloss is not None:
+            if dloss.numel() != (x.shape[0] if reduction == "none" else 1):
+                raise ValueError("dloss has the loss's shape")
+            dloss = dloss.contiguous().float()
+        elif reduction == "none":
+            raise ValueError('reduction "none" needs dloss')
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_dx else None
+        dw = torch.empty(w.shape, dtype=w.dtype, device=w.device) if want_dw else None
+        ws = _workspace(snack_xent_workspace_size(x, w, True), x.device)
+        snack_xent_bwd(x, w, targets, red, state, dloss, dx, dw, ws)
+        return dx, dw
+
+
+class _XentFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, targets, reduction):
+        loss, state = xent(x, w, targets, reduction)
+        ctx.save_for_backward(x, w, targets, state)
+        ctx.reduction = reduction
+        return loss
+
+    @staticmethod
+    def backward(ctx, dloss):
+        x, w, targets, state = ctx.saved_tensors
+        dx, dw = xent_grad(x, w, targets, state, dloss, ctx.reduction, ctx.needs_input_grad[0], ctx.needs_input_grad[1])
+        return dx, dw, None, None
+
+
+def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, reduction: str = "mean"):
+    """Autograd-aware xent: the loss alone; gradients flow to x and w."""
+    return _XentFn.apply(x, w, targets, reduction)

@@ -1,0 +1,283 @@
+"""Softmax cross entropy of a vocabulary projection, and its gradient, against
+the definitions in 64 bits.
+
+Tolerances, from the kernels' arithmetic.  A logit is a sum in fp32 of exact
+products (bf16 operands; fp32 ones as parts that leave out less than 2^-23 of
+a product): |err z| <= A T with A = 1e-5, the bound of every fp32 sum of this
+library, and T the largest sum of magnitudes of the row.  The log of the sum
+moves by at most the largest err z, plus the errors of 2^x (2^-21) and of the
+sums (2^-17 over thousands of terms): |err loss| <= 2 A T + 2^-16 + 2^-22 |lse|.
+With e = 2 A T + 2^-16 the relative error of a probability, dz is within
+g (p e + the rounding to bf16, 2^-8 (p + [v = t])) for bf16 operands and within
+g (e p + 2^-22 (p + [v = t])) for fp32 ones.  A product's sum adds A of its
+magnitudes, and a bf16 output half an ulp.  E below is the sum over the
+magnitudes g (p + [v = t]) |w| (or |x|).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from spmm_row_sorted_gb300 import snack
+
+from gpu_util import bf16_half_ulp, f64
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+A = 1e-5
+
+
+def make(n, vocab, width, dtype, seed, gap=0, lead=0, ignored=0.1, itype=torch.int64, spread=3.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def matrix(rows, std):
+        buf = torch.full((rows * (width + gap) + lead,), float("nan"), device="cuda", dtype=DTYPES[dtype])
+        m = buf[lead:].view(rows, width + gap)[:, :width]
+        m.copy_(torch.empty(rows, width, device="cuda").normal_(0, std, generator=g))
+        return m
+
+    x, w = matrix(n, 1.0), matrix(vocab, spread / width ** 0.5)
+    rng = np.random.default_rng(seed)
+    t = rng.integers(0, vocab, n)
+    t[rng.random(n) < ignored] = -100
+    t[rng.random(n) < ignored / 4] = vocab
+    if n > 1:
+        t[0], t[-1] = 0, vocab - 1
+    return x, w, torch.from_numpy(t).to(itype).cuda()
+
+
+def reference(x, w, t, g):
+    """loss per row, dx, dw and their magnitudes for per-row weights g (zero where not trained on)."""
+    x, w, t = f64(x), f64(w), t.cpu().numpy().astype(np.int64)
+    inside = (t >= 0) & (t < w.shape[0])
+    z = x @ w.T
+    T = (np.abs(x) @ np.abs(w).T).max(1)
+    top = z.max(1)
+    lse = top + np.log(np.exp(z - top[:, None]).sum(1))
+    at = np.where(inside, t, 0)
+    rows = np.arange(len(t))
+    loss = np.where(inside, lse - z[rows, at], 0.0)
+    p = np.exp(z - lse[:, None])
+    g = np.where(inside, g, 0.0)[:, None]
+    hot = np.zeros_like(z)
+    hot[rows[inside], at[inside]] = 1.0
+    dz, mag = g * (p - hot), np.abs(g) * (p + hot)
+    return dict(loss=loss, lse=lse, T=T, inside=inside, dx=dz @ w, dw=dz.T @ x,
+                # magnitudes, and the same weighted by each row's relative error of a probability
+                ex=mag @ np.abs(w), ew=mag.T @ np.abs(x), e=2 * A * T + 2.0 ** -16,
+                eew=(mag * (2 * A * T + 2.0 ** -16)[:, None]).T @ np.abs(x))
+
+
+def check_loss(loss, r):
+    assert np.all(np.abs(f64(loss) - r["loss"]) <= 2 * A * r["T"] + 2.0 ** -16 + 2.0 ** -22 * np.abs(r["lse"]))
+    assert not np.any(f64(loss)[~r["inside"]])
+
+
+def check_grads(dx, dw, r, dtype):
+    round_dz = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -22
+    for got, ref, bound in ((dx, r["dx"], (r["e"][:, None] + round_dz + A) * r["ex"]),
+                            (dw, r["dw"], r["eew"] + (round_dz + A) * r["ew"])):
+        if got is None:
+            continue
+        if dtype == "bf16":
+            bound = bound + bf16_half_ulp(np.abs(ref) + bound)
+        assert np.all(np.abs(f64(got) - ref) <= bound + 1e-300)
+
+
+SHAPES = [
+    # n, vocab, width, gap, lead
+    (1, 1, 1, 0, 0),
+    (1, 2, 8, 0, 0),
+    (1, 5000, 64, 0, 0),
+    (3, 257, 16, 0, 0),
+    (16, 1000, 128, 0, 0),
+    (31, 129, 72, 0, 0),
+    (127, 513, 65, 0, 0),      # rows that are laid out again
+    (128, 512, 64, 0, 0),      # whole tiles
+    (129, 511, 192, 0, 0),
+    (200, 700, 100, 4, 0),     # 16-byte aligned rows with gaps for fp32, not for bf16
+    (200, 700, 96, 8, 8),
+    (200, 700, 96, 0, 1),      # off a 16-byte boundary
+    (300, 4000, 320, 0, 0),
+    (64, 40000, 40, 0, 0),     # wide tiles
+    (1030, 3001, 259, 0, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,vocab,width,gap,lead", SHAPES)
+def test_xent_matches_definition(n, vocab, width, gap, lead, dtype):
+    x, w, t = make(n, vocab, width, dtype, seed=n + vocab, gap=gap, lead=lead, itype=torch.int32 if n % 2 else torch.int64)
+    rng = np.random.default_rng(n)
+    dloss = torch.from_numpy(rng.normal(size=n).astype(np.float32)).cuda()
+    r = reference(x, w, t, dloss.cpu().numpy().astype(np.float64))
+    loss, state = snack.xent(x, w, t, reduction="none")
+    check_loss(loss, r)
+    dx, dw = snack.xent_grad(x, w, t, state, dloss, reduction="none")
+    check_grads(dx, dw, r, dtype)
+    assert not np.any(f64(dx)[~r["inside"]])
+    again = snack.xent_grad(x, w, t, snack.xent(x, w, t, reduction="none")[1], dloss, reduction="none")
+    assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])  # repeats bit for bit
+    only_x, none_w = snack.xent_grad(x, w, t, state, dloss, reduction="none", want_dw=False)
+    none_x, only_w = snack.xent_grad(x, w, t, state, dloss, reduction="none", want_dx=False)
+    assert none_w is None and none_x is None and torch.equal(only_x, dx) and torch.equal(only_w, dw)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("reduction", ["sum", "mean"])
+def test_xent_reductions(reduction, dtype):
+    x, w, t = make(150, 900, 128, dtype, seed=4)
+    inside = ((t >= 0) & (t < 900)).cpu().numpy()
+    scale = 1.0 if reduction == "sum" else 1.0 / inside.sum()
+    up = torch.tensor(0.3, device="cuda")
+    r = reference(x, w, t, np.full(150, 0.3 * scale))
+    loss, state = snack.xent(x, w, t, reduction=reduction)
+    tol = (2 * A * r["T"] + 2.0 ** -16 + 2.0 ** -22 * np.abs(r["lse"]))[inside].sum() * scale
+    want = r["loss"].sum() * scale
+    assert loss.shape == () and abs(float(loss) - want) <= tol + 2.0 ** -23 * abs(want)
+    dx, dw = snack.xent_grad(x, w, t, state, up, reduction=reduction)
+    check_grads(dx, dw, r, dtype)
+    if reduction == "mean":  # no upstream gradient: 1
+        r1 = reference(x, w, t, np.full(150, scale))
+        check_grads(*snack.xent_grad(x, w, t, state, reduction=reduction), r1, dtype)
+
+
+def test_xent_nothing_to_train_on():
+    x, w, t = make(40, 300, 64, "bf16", seed=6)
+    t[:] = -100
+    loss, state = snack.xent(x, w, t)
+    assert float(loss) == 0.0
+    dx, dw = snack.xent_grad(x, w, t, state)
+    assert not dx.any() and not dw.any()
+    loss, state = snack.xent(x[:0], w, t[:0])
+    assert float(loss) == 0.0
+    dx, dw = snack.xent_grad(x[:0], w, t[:0], state)
+    assert dx.shape == (0, 64) and not dw.any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_xent_large_logits(dtype):
+    """Logits of several hundred, of both signs: exponentials of the differences only."""
+    x, w, t = make(70, 800, 64, dtype, seed=8, spread=200.0)
+    r = reference(x, w, t, np.ones(70))
+    loss, state = snack.xent(x, w, t, reduction="none")
+    check_loss(loss, r)
+    assert np.isfinite(f64(loss)).all()
+    dx, dw = snack.xent_grad(x, w, t, state, reduction="sum")
+    assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
+    w32 = w.clone()
+    w32[:] = w[0]  # equal logits
+    loss, _ = snack.xent(x, w32, t, reduction="none")
+    inside = r["inside"]
+    assert np.allclose(f64(loss)[inside], np.log(800.0), rtol=0, atol=2e-4)
+
+
+def test_xent_not_finite_rows_stay_apart():
+    x, w, t = make(140, 600, 64, "bf16", seed=9, ignored=0.0)
+    clean, _ = snack.xent(x, w, t, reduction="none")
+    bad = x.clone()
+    bad[5, 3] = float("nan")
+    bad[77, 0] = float("inf")
+    loss, state = snack.xent(bad, w, t, reduction="none")
+    assert torch.isnan(loss[5]) and torch.isnan(loss[77])
+    keep = torch.ones(140, dtype=torch.bool, device="cuda")
+    keep[5] = keep[77] = False
+    assert torch.equal(loss[keep], clean[keep])
+    t2 = t.clone()
+    t2[5] = t2[77] = -100  # not trained on: their dx is zero, the other rows' as before
+    loss, state = snack.xent(bad, w, t2, reduction="none")
+    assert float(loss[5]) == 0.0 and float(loss[77]) == 0.0
+    ones = torch.ones(140, device="cuda")
+    dx, _ = snack.xent_grad(bad, w, t2, state, ones, reduction="none", want_dw=False)
+    want, _ = snack.xent_grad(x, w, t2, snack.xent(x, w, t2, reduction="none")[1], ones, reduction="none", want_dw=False)
+    assert torch.equal(dx, want)
+
+
+def test_xent_in_pieces_of_the_vocabulary():
+    """A workspace-bounded gradient: n * vocab large enough for several pieces of dz and of w's parts."""
+    n, vocab, width = 8300, 40100, 64
+    x, w, t = make(n, vocab, width, "bf16", seed=10)
+    loss, state = snack.xent(x, w, t)
+    dx, dw = snack.xent_grad(x, w, t, state)
+    assert snack.snack_xent_workspace_size(x, w, True) < 2 * n * vocab  # less than dz whole
+    # the first and last rows of x, and blocks of the vocabulary in every piece, against the definition
+    inside = ((t >= 0) & (t < vocab)).cpu().numpy()
+    scale = 1.0 / inside.sum()
+    rows = np.r_[0:40, n - 40:n]
+    r = reference(x[rows], w, t[rows], np.full(80, scale))
+    check_grads(dx[rows], None, r, "bf16")
+    zs = (x.float() @ w.float().T).double()
+    lse = torch.logsumexp(zs, 1)
+    p = torch.exp(zs - lse[:, None])
+    del zs
+    ok = torch.from_numpy(inside).cuda()
+    p[ok, t[ok].long()] -= 1.0
+    p *= ok[:, None] * scale
+    ref = p.T @ x.double()
+    mag = p.abs().T @ x.double().abs()
+    T = float((x[:512].double().abs() @ w.double().abs().T).max()) * 1.5
+    # p - 1 stands for p + 1 in the magnitudes: a factor of 1 + 2 p / (1 - p) <= 2 for p <= 1/3
+    bound = 2 * (2 * A * T + 2.0 ** -16 + 2.0 ** -8 + 2 * A) * mag + 2.0 ** -8 * ref.abs() + 1e-12
+    assert bool(((dw.double() - ref).abs() <= bound).all())
+
+
+def test_linear_cross_entropy_autograd_matches_differences():
+    n, vocab, width = 6, 11, 5
+    x, w, t = make(n, vocab, width, "f32", seed=12)
+    x, w = x.contiguous().requires_grad_(), w.contiguous().requires_grad_()
+    (snack.linear_cross_entropy(x, w, t, reduction="sum") * 1.5).backward()
+    h = 2.0 ** -6
+
+    def loss(a, b):
+        return 1.5 * float(snack.xent(a.detach(), b.detach(), t, reduction="sum")[0])
+
+    # central differences: h^2 / 6 of a third derivative below 10 (softmax of logits with |x|, |w| < 4), and
+    # 2^-22 of a loss below 64 over h
+    for which in (x, w):
+        for i in (0, which.numel() // 2, which.numel() - 1):
+            lo, hi = which.detach().clone(), which.detach().clone()
+            lo.view(-1)[i] -= h
+            hi.view(-1)[i] += h
+            pair = (loss(hi, w) - loss(lo, w)) if which is x else (loss(x, hi) - loss(x, lo))
+            assert abs(pair / (2 * h) - float(which.grad.view(-1)[i])) < 10 * h * h / 6 * 1.5 + 64 * 2.0 ** -22 / h
+
+
+def test_xent_on_another_stream():
+    x, w, t = make(300, 2000, 128, "bf16", seed=14)
+    loss, state = snack.xent(x, w, t)
+    want = snack.xent_grad(x, w, t, state)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    l2, s2 = snack.xent(x, w, t, stream=side)
+    got = snack.xent_grad(x, w, t, s2, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(loss, l2) and torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+def test_xent_refusals():
+    x, w = torch.zeros(4, 8, device="cuda"), torch.zeros(10, 8, device="cuda")
+    t = torch.zeros(4, dtype=torch.int64, device="cuda")
+    for args in ((x, w.bfloat16(), t), (x[:, :7], w, t), (x, w, t[:3]), (x.half(), w.half(), t), (x, w, t.float()),
+                 (x.cpu(), w.cpu(), t.cpu()), (x, w, t.cpu())):
+        with pytest.raises(ValueError):
+            snack.xent(*args)
+    with pytest.raises(ValueError):
+        snack.xent(x, w, t, reduction="max")
+    loss, state = snack.xent(x, w, t, reduction="none")
+    with pytest.raises(ValueError):
+        snack.xent_grad(x, w, t, state, reduction="none")  # no upstream gradient
+    with pytest.raises(ValueError):
+        snack.xent_grad(x, w, t, state[:4])
+    with pytest.raises(ValueError):
+        snack.xent_grad(x, w, t, state, torch.zeros(3, device="cuda"), reduction="none")
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    with pytest.raises(snack.SnackError) as e:
+        snack.snack_xent_fwd(x, w, t, 0, loss, state, ws)
+    assert e.value.status == 4
+    with pytest.raises(snack.SnackError) as e:  # dx on x
+        snack.snack_xent_bwd(x, w, t, 1, state, None, x, None, torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 1
+    with pytest.raises(snack.SnackError) as e:
+        snack.snack_xent_fwd(x, w, t, 7, loss, state, ws)
+    assert e.value.status == 1
