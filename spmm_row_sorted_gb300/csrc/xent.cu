@@ -18,12 +18,20 @@
 //   dw     writes the piece's rows of dw.
 // Bound by the tensor cores; for a few tokens by reading w once.
 //
-// One CTA per SM works through 128 x (64, 128 or 256) output tiles: a warp
-// loads operand tiles by TMA into a ring of stages, a warp issues the
-// tcgen05.mma, eight warps run the epilogue of one tile from one half of the
-// tensor memory while the next tile accumulates in the other.  Operands whose
+// A pair of CTAs, one per SM, works through 256 x (64, 128 or 256) output tiles,
+// 128 rows each: in each a warp loads its rows of A and its half of B by TMA
+// into a ring of stages; one thread of the pair issues the tcgen05.mma, which
+// read both halves of B (a third fewer bytes from L2 than a tile per CTA, which
+// L2 held to 71 % of the tensor cores' cycles); in each eight warps run the epilogue of one tile from one half of the
+// tensor memory while the next one forms in the other.  Operands whose
 // rows run along K are K-major tiles (128-byte swizzle), the others (w for dx,
 // dz^T and x for dw) are read as they lie, as MN-major tiles: no transposes.
+//
+// The tensor core's fp32 accumulation rounds towards zero, which over a long K
+// is a bias: a sum of 4096 products came out 1e-5 of itself too small.  So an
+// accumulator takes 256 of K at a time (16 instructions) where that counts,
+// and the epilogue's warps add the partial sums in registers, rounding to
+// nearest, while the next one forms in the other half of the tensor memory.
 //
 // fp32 operands are cut into three bf16 parts each (8 significant bits at a
 // time, 24 in all), and a product is the sum of the six part products down to
@@ -53,8 +61,22 @@ __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
 __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(bar)), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(bar)) : "memory");
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// the address, in the cluster's shared memory, of the pair leader's copy of `p`
+__device__ __forceinline__ uint32_t at_leader(const void *p) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(su32(p)));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 constexpr int kSpinLimit = 1 << 20;  // try_wait rounds before a wait is declared stuck (far above any real wait)
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
@@ -70,11 +92,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
   }
   return false;
 }
-__device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+// into this CTA's shared memory; the bytes count on the barrier at `bar`, in either CTA of the pair
+__device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-      "[%5];" ::"r"(su32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(su32(bar))
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3, %4}], [%5];" ::"r"(su32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void tma_store(const CUtensorMap *map, const void *src, int x, int y, int z) {
@@ -96,25 +119,29 @@ __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(dst)), "r"(ncols)
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(dst)), "r"(ncols)
                : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-// D (TMEM) (+)= A (smem) * B (smem)^T, bf16 with fp32 accumulation
+// D (TMEM) (+)= A (smem) * B (smem)^T, bf16 with fp32 accumulation, over the
+// pair of CTAs: 256 rows, 128 of A and of D in each; half of B's rows in each
 __device__ __forceinline__ void umma(uint32_t taddr, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                      uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(taddr),
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(taddr),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// arrive on both CTAs' *bar once every MMA issued so far by this thread has completed
 __device__ __forceinline__ void umma_commit(uint64_t *bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(bar))
-               : "memory");
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(su32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
 }
 // 32 consecutive fp32 columns of this thread's TMEM lane
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
@@ -164,20 +191,34 @@ __device__ __forceinline__ uint32_t inst_desc(int m, int n, bool a_mn, bool b_mn
 
 // ------------------------------------------------------------------ kernel
 
-constexpr int kM = 128;           // rows of an output tile, TMEM lanes
+constexpr int kM = 256;           // rows of an output tile: 128 (the TMEM lanes) in each CTA of the pair
+constexpr int kMCta = kM / 2;
 constexpr int kNMax = 256;        // columns of the widest output tile
 constexpr int kKb = 64;           // K per stage
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = (kEpiWarps + 2) * 32;
-constexpr int kStageA = kM * kKb * 2;
-constexpr int kRing = 4 * (kStageA + kNMax * kKb * 2);  // bytes of the ring of stages
+constexpr int kChunks = kNMax / 2 / 32;  // 32-column chunks of an epilogue warp's half tile
+constexpr int kThreads = (kEpiWarps + 4) * 32;  // and a warpgroup for the loads and the MMAs (two of its warps idle)
+// An epilogue thread keeps 128 sums; launched with 168 registers each, the
+// third warpgroup gives most of its own to the other two (384 * 168 in all).
+constexpr int kEpiRegs = 232, kIssueRegs = 40;
+static_assert(256 * kEpiRegs + 128 * kIssueRegs <= kThreads * 168, "the split stays within the launch's registers");
+constexpr int kStageA = kMCta * kKb * 2;
+constexpr int kRing = 6 * (kStageA + kNMax / 2 * kKb * 2);  // bytes of the ring of stages
 constexpr int kMaxStages = 8;
 constexpr int kStaging = 4096;    // an epilogue warp's 32 rows x 128 bytes on their way out
 constexpr int kSmem = 1024 + kRing + kEpiWarps * kStaging + 256;
 static_assert(kSmem <= 232448, "shared memory of one CTA");
-static_assert(kStageA + 64 * kKb * 2 <= kRing / kMaxStages, "eight stages of the narrowest tile fit the ring");
+static_assert(kStageA + 128 / 2 * kKb * 2 <= kRing / kMaxStages, "eight stages of the narrower tiles fit the ring");
 
 enum { kStats = 0, kDlog = 1, kDx = 2, kDw = 3 };
+
+// The factor common to all rows of dz (sum and mean): a product of up to two
+// device values.  It is applied to the finished sums, so dz itself lies in
+// [-1, 1] and its rounding to bf16 is not the same for every row.
+struct Factor {
+  const float *a, *b;  // null: 1
+  __device__ __forceinline__ float get() const { return (a ? *a : 1.f) * (b ? *b : 1.f); }
+};
 
 struct GemmArgs {
   int32_t m, n;             // rows and columns of the product
@@ -186,6 +227,7 @@ struct GemmArgs {
   int32_t k_blocks;         // of 64
   int32_t products;         // part products per element (1: bf16, 6: fp32)
   uint32_t a_part, b_part;  // 4 bits per product: its parts
+  int32_t unit;             // K stages summed on the tensor core before the sum moves to registers
   int32_t stages;
   uint32_t *err;            // [256] error words, one per CTA
   int32_t first;            // the call's first launch writes every error word
@@ -197,13 +239,13 @@ struct GemmArgs {
   TokenSrc targets;
   int32_t v0;               // first vocabulary row of the piece
   // dlog
-  const float *lse;         // [m], and 1 / count at [m]
-  const float *dloss;       // upstream gradient: [m], one value, or null (1)
-  int32_t per_row;          // dloss has a value per row
+  const float *lse;         // [m]
+  const float *dloss;       // upstream gradient of each row, or null (1: a common factor is applied to the sums)
   int32_t out_parts;        // bf16 parts of dz
   // dx
   int32_t add;              // add to the sums (else write them)
   // dw
+  Factor factor;
   void *out;                // first row of the piece; used where TMA cannot store
   int64_t out_ld;
   int32_t out_wide;         // fp32 (else bf16)
@@ -224,14 +266,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 template <int kMode>
-__global__ void __launch_bounds__(kThreads, 1) k_xent(const __grid_constant__ CUtensorMap map_a,
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(const __grid_constant__ CUtensorMap map_a,
                                                       const __grid_constant__ CUtensorMap map_b,
                                                       const __grid_constant__ CUtensorMap map_o, const GemmArgs P) {
   pdl_wait();
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   constexpr bool kAmn = kMode == kDw, kBmn = kMode == kDx || kMode == kDw;
-  const uint32_t stage_bytes = (uint32_t)(kStageA + P.nt * kKb * 2);
+  const uint32_t rank = cta_rank();  // 0: the leader, which issues the pair's MMAs
+  const int nb = P.nt / 2;           // rows of B in each CTA
+  const uint32_t stage_bytes = (uint32_t)(kStageA + nb * kKb * 2);
   uint8_t *staging = smem + kRing;
   uint64_t *full = reinterpret_cast<uint64_t *>(staging + kEpiWarps * kStaging);
   uint64_t *empty = full + kMaxStages;
@@ -240,7 +284,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_xent(const __grid_constant__ CU
   uint64_t *drained = acc_free + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
   int *bad = reinterpret_cast<int *>(tmem_slot + 1);
-  int *loads = bad + 1;  // stages loaded so far
   static_assert(8 * (2 * kMaxStages + 5) + 16 <= 256, "barriers and flags fit their 256 bytes");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -251,16 +294,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_xent(const __grid_constant__ CU
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_free[b], kEpiWarps);
+      mbar_init(&acc_free[b], 2 * kEpiWarps);
     }
     mbar_init(drained, 1);
     *bad = 0;
-    *loads = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
+  pair_sync();  // both CTAs' barriers are ready
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -288,10 +331,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_xent(const __grid_constant__ CU
     return r;
   };
 
+  if (warp >= kEpiWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
   if (warp == kEpiWarps) {  // ------------------------------------------- loads
     if (lane == 0) {
       uint32_t it = 0;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
         const Tile q = tile_at(t);
         for (int c = 0; c < P.products && ok; ++c) {
           const int za = (P.a_part >> (4 * c)) & 15, zb = (P.b_part >> (4 * c)) & 15;
@@ -302,76 +347,79 @@ __global__ void __launch_bounds__(kThreads, 1) k_xent(const __grid_constant__ CU
               break;
             }
             uint8_t *a = smem + (uint32_t)s * stage_bytes, *b = a + kStageA;
-            mbar_expect_tx(&full[s], stage_bytes);
+            const uint32_t bar = at_leader(&full[s]);  // the leader's barrier counts both CTAs' bytes
+            if (rank == 0) mbar_expect_tx(&full[s], 2 * stage_bytes);
+            const int am = q.m0 + (int)rank * kMCta, bn = q.n0 + (int)rank * nb;
             if (kAmn) {
-              tma_load(a, &map_a, q.m0, kb * kKb, za, &full[s]);
-              tma_load(a + 8192, &map_a, q.m0 + 64, kb * kKb, za, &full[s]);
+              tma_load(a, &map_a, am, kb * kKb, za, bar);
+              tma_load(a + 8192, &map_a, am + 64, kb * kKb, za, bar);
             } else {
-              tma_load(a, &map_a, kb * kKb, q.m0, za, &full[s]);
+              tma_load(a, &map_a, kb * kKb, am, za, bar);
             }
             if (kBmn) {
-              for (int j = 0; j < P.nt; j += 64) tma_load(b + j * 128, &map_b, q.n0 + j, kb * kKb, zb, &full[s]);
+              for (int j = 0; j < nb; j += 64) tma_load(b + j * 128, &map_b, bn + j, kb * kKb, zb, bar);
             } else {
-              tma_load(b, &map_b, kb * kKb, q.n0, zb, &full[s]);
+              tma_load(b, &map_b, kb * kKb, bn, zb, bar);
             }
-            *loads = (int)it + 1;
           }
         }
       }
     }
   } else if (warp == kEpiWarps + 1) {  // -------------------------------- MMAs
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       const uint32_t idesc = inst_desc(kM, P.nt, kAmn, kBmn);
       uint32_t it = 0;
       int n_acc = 0;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
         const Tile q = tile_at(t);
         if (q.nk == 0) continue;
-        const int buf = n_acc & 1;
-        if (!mbar_wait(&acc_free[buf], ((n_acc >> 1) & 1) ^ 1)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(buf * kNMax);
         const int steps = P.products * q.nk;
-        for (int i = 0; i < steps; ++i, ++it) {
-          const int s = (int)(it % P.stages);
-          if (!mbar_wait(&full[s], (it / P.stages) & 1)) {
+        for (int i = 0; i < steps && ok; ++n_acc) {  // a unit of steps per accumulator
+          const int buf = n_acc & 1;
+          if (!mbar_wait(&acc_free[buf], ((n_acc >> 1) & 1) ^ 1)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a = su32(smem) + (uint32_t)s * stage_bytes, b = a + kStageA;
+          const uint32_t d = tmem + (uint32_t)(buf * kNMax);
+          const int end = min(steps, i + P.unit);
+          for (int u = 0; i < end; ++i, ++it, ++u) {
+            const int s = (int)(it % P.stages);
+            if (!mbar_wait(&full[s], (it / P.stages) & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a = su32(smem) + (uint32_t)s * stage_bytes, b = a + kStageA;
 #pragma unroll
-          for (int k = 0; k < kKb / 16; ++k) {
-            // 16 K elements: 32 bytes within the swizzled row, or 16 rows of 128 bytes
-            const uint64_t da = tile_desc(a + (kAmn ? k * 2048 : k * 32), kAmn);
-            const uint64_t db = tile_desc(b + (kBmn ? k * 2048 : k * 32), kBmn);
-            umma(d, da, db, idesc, (i | k) != 0);
+            for (int k = 0; k < kKb / 16; ++k) {
+              // 16 K elements: 32 bytes within the swizzled row, or 16 rows of 128 bytes
+              const uint64_t da = tile_desc(a + (kAmn ? k * 2048 : k * 32), kAmn);
+              const uint64_t db = tile_desc(b + (kBmn ? k * 2048 : k * 32), kBmn);
+              umma(d, da, db, idesc, (u | k) != 0);
+            }
+            umma_commit(&empty[s]);
           }
-          umma_commit(&empty[s]);
+          if (ok) umma_commit(&acc_full[buf]);
         }
-        if (!ok) break;
-        umma_commit(&acc_full[buf]);
-        ++n_acc;
       }
       umma_commit(drained);
     }
+  }
   } else {  // -------------------------------------------------------- epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter .. +31; half of the columns
     uint8_t *stage = staging + warp * kStaging;
     constexpr float kLog2e = 1.4426950408889634f;
     int n_acc = 0;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+    for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
       const Tile q = tile_at(t);
       if (q.nk == 0) continue;
-      const int buf = n_acc & 1;
-      const int row = q.m0 + quarter * 32 + lane;
+      const int m0 = q.m0 + (int)rank * kMCta;  // this CTA's rows
+      const int row = m0 + quarter * 32 + lane;
       const bool row_ok = row < P.m;
       const int c_end = P.nt / 2;  // columns of this half
       const int col0 = q.n0 + half * c_end;
-      const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * kNMax + half * c_end);
       // the target's column of this tile's half, or below zero
       int tcol = -1;
       float lse = 0.f, g = 0.f;
@@ -382,21 +430,46 @@ __global__ void __launch_bounds__(kThreads, 1) k_xent(const __grid_constant__ CU
             tcol = (int)id - P.v0 - col0;
             if (kMode == kDlog) {
               lse = P.lse[row];
-              g = (P.dloss ? P.dloss[P.per_row ? row : 0] : 1.f) * P.lse[P.m];
+              g = P.dloss ? P.dloss[row] : 1.f;
             }
           }
         }
       }
-      if (!mbar_wait(&acc_full[buf], (n_acc >> 1) & 1)) {
-        ok = false;
-        break;
+      // the tile's sums: one unit after the other, added in fp32
+      float acc[kChunks][32];
+      const int units = (P.products * q.nk + P.unit - 1) / P.unit;
+      for (int u = 0; u < units; ++u, ++n_acc) {
+        const int buf = n_acc & 1;
+        if (!mbar_wait(&acc_full[buf], (n_acc >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * kNMax + half * c_end);
+#pragma unroll
+        for (int h = 0; h < kChunks; ++h)
+          if (32 * h < c_end) {
+            if (u == 0) {
+              tmem_ld32(from + 32u * h, acc[h]);
+            } else {
+              float v[32];
+              tmem_ld32(from + 32u * h, v);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) acc[h][j] += v[j];
+            }
+          }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(at_leader(&acc_free[buf]));
       }
-      tc_fence_after();
+      if (!ok) break;
       if (kMode == kStats) {
         float mx = -INFINITY, sum = 0.f;
-        for (int c = 0; c < c_end; c += 32) {
-          float v[32];
-          tmem_ld32(acc + (uint32_t)c, v);
+#pragma unroll
+        for (int h = 0; h < kChunks; ++h) {
+          const int c = 32 * h;
+          if (c >= c_end) break;
+          float(&v)[32] = acc[h];
           const int valid = P.n - col0 - c;
           if (valid < 32) {
 #pragma unroll
@@ -424,9 +497,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_xent(const __grid_constant__ CU
         if (row_ok)
           P.part[(size_t)(P.slot0 + 2 * (q.n0 / P.nt) + half) * (size_t)P.m + row] = make_float2(mx, sum);
       } else if (kMode == kDlog) {
-        for (int c = 0; c < c_end; c += 32) {
-          float v[32];
-          tmem_ld32(acc + (uint32_t)c, v);
+#pragma unroll
+        for (int h = 0; h < kChunks; ++h) {
+          const int c = 32 * h;
+          if (c >= c_end) break;
+          float(&v)[32] = acc[h];
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             const float p = ex2((v[j] - lse) * kLog2e);
@@ -457,18 +532,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_xent(const __grid_constant__ CU
             }
             fence_async_shared();
             __syncwarp();
-            if (lane == 0 && col0 + c < P.n && q.m0 + quarter * 32 < P.m) {
-              tma_store(&map_o, stage, col0 + c, q.m0 + quarter * 32, part);
+            if (lane == 0 && col0 + c < P.n && m0 + quarter * 32 < P.m) {
+              tma_store(&map_o, stage, col0 + c, m0 + quarter * 32, part);
               bulk_commit();
             }
           }
         }
       } else {
         const bool wide = kMode == kDx || P.out_wide;
+        if (kMode == kDw) {
+          const float f = P.factor.get();
+#pragma unroll
+          for (int h = 0; h < kChunks; ++h)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[h][j] *= f;
+        }
         const int step = wide ? 32 : 64;  // columns of 128 bytes
-        for (int c = 0; c < c_end; c += 32) {
-          float v[32];
-          tmem_ld32(acc + (uint32_t)c, v);
+#pragma unroll
+        for (int h = 0; h < kChunks; ++h) {
+          const int c = 32 * h;
+          if (c >= c_end) break;
+          float(&v)[32] = acc[h];
           if (lane == 0 && (c % step) == 0) bulk_wait_read();
           __syncwarp();
           if (wide) {
@@ -487,25 +571,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_xent(const __grid_constant__ CU
               *reinterpret_cast<uint4 *>(stage + stage_off(lane, ch + ((c & 32) >> 3))) = u;
             }
           }
-          if ((c + 32) % step != 0 && c + 32 < c_end) continue;  // the row's other half first
+          if ((c + 32) % step != 0) continue;  // the row's other half first
           const int x0 = col0 + c / step * step;
           if (kMode == kDx || P.out_tma) {
             fence_async_shared();
             __syncwarp();
-            if (lane == 0 && x0 < P.n && q.m0 + quarter * 32 < P.m) {
+            if (lane == 0 && x0 < P.n && m0 + quarter * 32 < P.m) {
               if (kMode == kDx && P.add)
-                tma_add(&map_o, stage, x0, q.m0 + quarter * 32, q.split);
+                tma_add(&map_o, stage, x0, m0 + quarter * 32, q.split);
               else
-                tma_store(&map_o, stage, x0, q.m0 + quarter * 32, kMode == kDx ? q.split : 0);
+                tma_store(&map_o, stage, x0, m0 + quarter * 32, kMode == kDx ? q.split : 0);
               bulk_commit();
             }
           } else {  // rows that TMA cannot address: a warp writes one after the other
             __syncwarp();
-            const int have = min(step, c_end - c / step * step);  // a 64-wide tile's half has 32 columns
             for (int r = 0; r < 32; ++r) {
-              const int orow = q.m0 + quarter * 32 + r;
+              const int orow = m0 + quarter * 32 + r;
               if (orow >= P.m) break;
-              for (int j = lane; j < have && x0 + j < P.n; j += 32) {
+              for (int j = lane; j < step && x0 + j < P.n; j += 32) {
                 if (wide)
                   reinterpret_cast<float *>(P.out)[(int64_t)orow * P.out_ld + x0 + j] =
                       *reinterpret_cast<const float *>(stage + stage_off(r, j >> 2) + (j & 3) * 4);
@@ -518,22 +601,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_xent(const __grid_constant__ CU
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_free[buf]);
-      ++n_acc;
     }
     if (lane == 0) bulk_wait();
   }
   if (!ok) *bad = 1;
   __syncthreads();
   if (threadIdx.x == 0) {
-    const bool failed = *bad != 0;
-    if (failed) {  // every load and MMA issued has completed (bounded) before the tensor memory is given back
-      const int n = *loads;
-      for (int g = n - 1; g >= 0 && g >= n - P.stages; --g) mbar_wait(&full[g % P.stages], (g / P.stages) & 1);
-      mbar_wait(drained, 0);
-    }
+    bool failed = *bad != 0;
+    // the leader's last commit: every MMA of the pair and every arrival on this
+    // CTA's barriers is done (bounded; after a failure, a millisecond more for
+    // loads that are still in flight)
+    const bool rest = mbar_wait(drained, 0);
+    failed = failed || !rest;
+    if (failed)
+      for (int i = 0; i < 1000; ++i) __nanosleep(1000);
     if (P.first) {
       for (int e = blockIdx.x; e < 256; e += gridDim.x) P.err[e] = failed ? 1u : 0u;
     } else if (failed) {
@@ -542,6 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_xent(const __grid_constant__ CU
   }
   tc_fence_before();
   __syncthreads();
+  pair_sync();  // nothing of either CTA is still at work in the other's memory
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
@@ -667,9 +749,11 @@ __global__ void __launch_bounds__(256) k_xent_pack(const T *__restrict__ in, int
 template <typename T>
 __global__ void __launch_bounds__(256) k_xent_dx(const float *__restrict__ acc, int splits, int64_t plane, int32_t acc_ld,
                                                  int32_t m, int32_t width, T *__restrict__ dx, int64_t ld,
-                                                 T *__restrict__ dw, const uint32_t *__restrict__ err) {
+                                                 T *__restrict__ dw, Factor factor,
+                                                 const uint32_t *__restrict__ err) {
   pdl_wait();
   const bool bad = any_error(err);
+  const float f = bad ? NAN : factor.get();
   if (bad && dw && blockIdx.x == 0)
     for (int i = threadIdx.x; i < width; i += 256) dw[i] = from_f32<T>(NAN);
   const int groups = acc_ld / 4;
@@ -685,9 +769,8 @@ __global__ void __launch_bounds__(256) k_xent_dx(const float *__restrict__ acc, 
       s.z += b.z;
       s.w += b.w;
     }
-    if (bad) s = make_float4(NAN, NAN, NAN, NAN);
     T *o = dx + r * ld + c;
-    const float e[4] = {s.x, s.y, s.z, s.w};
+    const float e[4] = {s.x * f, s.y * f, s.z * f, s.w * f};
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (c + j < width) o[j] = from_f32<T>(e[j]);
@@ -743,14 +826,14 @@ constexpr size_t kPieceBytes = (size_t)256 << 20;  // of dz, or of w's parts, at
 
 int sms_of() {
   const int n = current_sms();
-  return n < 1 ? 152 : n > 256 ? 256 : n;
+  return n < 2 ? 152 : n > 256 ? 256 : n;
 }
 
-// The widest tile that still gives every SM one; narrower tiles share a small
+// The widest tile that still gives every pair of SMs one; narrower tiles share a small
 // product among more SMs.
 int tile_cols(int64_t m_tiles, int64_t n, int sms) {
   for (int nt = 256; nt > 64; nt /= 2)
-    if (m_tiles * ceil_div(n, nt) >= sms) return nt;
+    if (m_tiles * ceil_div(n, nt) >= sms / 2) return nt;
   return 64;
 }
 
@@ -771,7 +854,7 @@ int pick_split(int64_t tiles, int64_t k_steps, int sms) {
   for (int s = 1; s <= 8; ++s) {
     const int64_t per = ceil_div(k_steps, s);
     if (s > 1 && (per < 8 || (s - 1) * per >= k_steps)) break;
-    const int64_t cost = ceil_div(tiles * s, sms) * (per + 8);
+    const int64_t cost = ceil_div(tiles * s, sms / 2) * (per + 8);
     if (cost < best_cost) {
       best_cost = cost;
       best = s;
@@ -825,7 +908,7 @@ XentWs xent_ws(const XentShape &s, bool grad) {
     w.piece = piece_rows(s.vocab, s.pack_w && w_row > dz_row ? w_row : dz_row);
     if (w.piece > s.vocab) w.piece = s.vocab;
     w.dz_ld = ceil_div(w.piece, 64) * 64;
-    w.nt_d = s.width > 128 ? 256 : s.width > 64 ? 128 : 64;
+    w.nt_d = s.width > 128 ? 256 : 128;  // a CTA's half of B is 64 columns at least
     w.acc_ld = (int32_t)align_up((size_t)s.width, 4);
     w.split = pick_split(m_tiles * ceil_div(s.width, w.nt_d), ceil_div(w.piece, kKb), s.sms);
     w.dz = o;
@@ -863,11 +946,11 @@ cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtens
   if (e != cudaSuccess) return e;
   g.m_tiles = (int32_t)ceil_div(g.m, kM);
   g.n_tiles = (int32_t)ceil_div(g.n, g.nt);
-  g.stages = kRing / (kStageA + g.nt * kKb * 2);
+  g.stages = kRing / (kStageA + g.nt / 2 * kKb * 2);
   if (g.stages > kMaxStages) g.stages = kMaxStages;
   const int64_t tiles = (int64_t)g.m_tiles * g.n_tiles * g.n_split;
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
-  e = launch_pdl(k_xent<kMode>, (unsigned)(tiles < sms ? tiles : sms), kThreads, kSmem, s, a, b, o, (const GemmArgs)g);
+  e = launch_pdl(k_xent<kMode>, 2 * (unsigned)(tiles < sms / 2 ? tiles : sms / 2), kThreads, kSmem, s, a, b, o, (const GemmArgs)g);
   g.first = 0;
   return e;
 }
@@ -904,8 +987,19 @@ cudaError_t operand(const XentShape &s, bool packed, const void *p, int64_t ld, 
   return pack(s, at, ld, rows, buf, st);
 }
 
+// Units of K stages (64 each): see the note on rounding at the top.  Sums that
+// become fp32 results, or the logits, take short ones; those that are rounded
+// to bf16 (dx and dw of bf16 operands) are far below half its ulp with long ones.
+#ifndef SNACK_XENT_UNIT
+#define SNACK_XENT_UNIT 4
+#endif
+#ifndef SNACK_XENT_UNIT_BF16
+#define SNACK_XENT_UNIT_BF16 64
+#endif
+
 GemmArgs gemm_args(const XentShape &s, uint8_t *ws, const XentWs &W, int first) {
   GemmArgs g = {};
+  g.unit = SNACK_XENT_UNIT;
   g.n_split = 1;
   g.products = s.parts == 3 ? 6 : 1;
   g.a_part = s.parts == 3 ? kPartA : 0;
@@ -972,7 +1066,7 @@ snack_status snack_xent_fwd(const void *x, int64_t x_ld, int32_t n, const void *
   Operand ox, ow;
   XENT_CUDA(operand(S, S.pack_x, x, x_ld, 0, n, b + W.xp, &ox, s));
   CUtensorMap mx, mw;
-  if (!load_map(&mx, ox, false, kM)) return SNACK_ERR_CUDA;
+  if (!load_map(&mx, ox, false, kMCta)) return SNACK_ERR_CUDA;
   GemmArgs g = gemm_args(S, b, W, 1);
   g.m = n;
   g.nt = W.nt;
@@ -983,7 +1077,7 @@ snack_status snack_xent_fwd(const void *x, int64_t x_ld, int32_t n, const void *
   for (int64_t v0 = 0; v0 < vocab; v0 += W.piece) {
     const int64_t rows = vocab - v0 < W.piece ? vocab - v0 : W.piece;
     XENT_CUDA(operand(S, S.pack_w, w, w_ld, v0, rows, b + W.wp, &ow, s));
-    if (!load_map(&mw, ow, false, (uint32_t)W.nt)) return SNACK_ERR_CUDA;
+    if (!load_map(&mw, ow, false, (uint32_t)W.nt / 2)) return SNACK_ERR_CUDA;
     g.n = (int32_t)rows;
     g.v0 = (int32_t)v0;
     XENT_CUDA(launch_gemm<kStats>(mx, mw, mx, g, S.sms, s));
@@ -1031,17 +1125,18 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
   Operand ox, ow;
   XENT_CUDA(operand(S, S.pack_x, x, x_ld, 0, n, b + W.xp, &ox, s));
   CUtensorMap mx, mw, mxt, mwt, mdz, mdzt, mdz_out, macc, mdw;
-  if (!load_map(&mx, ox, false, kM) || !load_map(&mxt, ox, true, 0)) return SNACK_ERR_CUDA;
+  if (!load_map(&mx, ox, false, kMCta) || !load_map(&mxt, ox, true, 0)) return SNACK_ERR_CUDA;
   if (!make_map(&macc, b + W.acc, true, (uint64_t)width, (uint64_t)n, (uint64_t)W.acc_ld, (uint64_t)W.split,
                 (uint64_t)n * (uint64_t)W.acc_ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B))
     return SNACK_ERR_CUDA;
+  const Factor factor = {reduction == SNACK_NONE ? nullptr : dloss, reduction == SNACK_MEAN ? state + n : nullptr};
   int first = 1;
   for (int64_t v0 = 0; v0 < vocab; v0 += W.piece) {
     const int64_t rows = vocab - v0 < W.piece ? vocab - v0 : W.piece;
     XENT_CUDA(operand(S, S.pack_w, w, w_ld, v0, rows, b + W.wp, &ow, s));
     const Operand dz = {b + W.dz, n, W.dz_ld, (int64_t)n * W.dz_ld, (int32_t)rows, S.parts};
     const int nt = tile_cols(ceil_div(n, kM), rows, S.sms);
-    if (!load_map(&mw, ow, false, (uint32_t)nt) || !load_map(&mwt, ow, true, 0) || !load_map(&mdz, dz, false, kM) ||
+    if (!load_map(&mw, ow, false, (uint32_t)nt / 2) || !load_map(&mwt, ow, true, 0) || !load_map(&mdz, dz, false, kMCta) ||
         !load_map(&mdzt, dz, true, 0) ||
         !make_map(&mdz_out, dz.p, false, (uint64_t)rows, (uint64_t)n, (uint64_t)W.dz_ld, (uint64_t)S.parts,
                   (uint64_t)dz.plane, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
@@ -1054,13 +1149,13 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
     g.targets = TokenSrc{targets, targets_t == SNACK_I64, (uint32_t)vocab};
     g.v0 = (int32_t)v0;
     g.lse = state;
-    g.dloss = dloss;
-    g.per_row = reduction == SNACK_NONE;
+    g.dloss = reduction == SNACK_NONE ? dloss : nullptr;
     g.out_parts = S.parts;
     XENT_CUDA(launch_gemm<kDlog>(mx, mw, mdz_out, g, S.sms, s));
     first = 0;
     if (dx) {
       GemmArgs h = gemm_args(S, b, W, 0);
+      if (!wide) h.unit = SNACK_XENT_UNIT_BF16;
       h.m = n;
       h.n = width;
       h.nt = W.nt_d;
@@ -1071,15 +1166,17 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
     }
     if (dw) {
       GemmArgs h = gemm_args(S, b, W, 0);
+      if (!wide) h.unit = SNACK_XENT_UNIT_BF16;
       h.m = (int32_t)rows;
       h.n = width;
       h.nt = W.nt_d;
       h.k_blocks = (int32_t)ceil_div(n, kKb);
       uint8_t *to = reinterpret_cast<uint8_t *>(dw) + (size_t)v0 * (size_t)dw_ld * es;
       h.out = to;
+      h.factor = factor;
       h.out_ld = dw_ld;
       h.out_wide = wide;
-      h.out_tma = ptr_aligned(to, 16) && (size_t)dw_ld * es % 16 == 0 && (wide || W.nt_d >= 128);
+      h.out_tma = ptr_aligned(to, 16) && (size_t)dw_ld * es % 16 == 0;
       if (h.out_tma && !make_map(&mdw, to, wide, (uint64_t)width, (uint64_t)rows, (uint64_t)dw_ld, 1,
                                  (uint64_t)rows * (uint64_t)dw_ld, wide ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
         return SNACK_ERR_CUDA;
@@ -1094,10 +1191,12 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
   const uint32_t *err = reinterpret_cast<const uint32_t *>(b + W.err);
   if (wide)
     XENT_CUDA(launch_pdl(k_xent_dx<float>, (unsigned)blocks, 256, 0, s, acc, W.split, (int64_t)n * W.acc_ld, W.acc_ld,
-                         dx ? n : 0, width, reinterpret_cast<float *>(dx), dx_ld, reinterpret_cast<float *>(dw), err));
+                         dx ? n : 0, width, reinterpret_cast<float *>(dx), dx_ld, reinterpret_cast<float *>(dw), factor,
+                         err));
   else
     XENT_CUDA(launch_pdl(k_xent_dx<bf16>, (unsigned)blocks, 256, 0, s, acc, W.split, (int64_t)n * W.acc_ld, W.acc_ld,
-                         dx ? n : 0, width, reinterpret_cast<bf16 *>(dx), dx_ld, reinterpret_cast<bf16 *>(dw), err));
+                         dx ? n : 0, width, reinterpret_cast<bf16 *>(dx), dx_ld, reinterpret_cast<bf16 *>(dw), factor,
+                         err));
   return SNACK_OK;
 } catch (...) {  // a host allocation failed
   return SNACK_ERR_CUDA;
