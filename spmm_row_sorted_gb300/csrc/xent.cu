@@ -79,18 +79,25 @@ __device__ __forceinline__ void pair_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 constexpr int kSpinLimit = 1 << 20;  // try_wait rounds before a wait is declared stuck (far above any real wait)
+__device__ __forceinline__ bool mbar_try(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done)
+      : "r"(su32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
-  const uint32_t a = su32(bar);
-  for (int i = 0; i < kSpinLimit; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(done)
-        : "r"(a), "r"(parity)
-        : "memory");
-    if (done) return true;
-  }
+  for (int i = 0; i < kSpinLimit; ++i)
+    if (mbar_try(bar, parity)) return true;
   return false;
+}
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+  return p != 0;
 }
 // into this CTA's shared memory; the bytes count on the barrier at `bar`, in either CTA of the pair
 __device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
@@ -126,14 +133,24 @@ __device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t ncols) {
 __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
+// Shared-memory descriptor of an operand tile with the 128-byte swizzle:
+// start (16-byte units), leading and stride byte offsets, version 1, layout
+// type 2.  K-major: 128-byte rows of 64 K elements, 8 rows to a 1024-byte
+// atom, stride 1024 from atom to atom (the leading offset is not used).
+// MN-major: boxes of 64 K rows of 64 MN elements (128 bytes each); 8 K rows
+// to an atom, stride 1024 from one to the next along K, and the leading
+// offset is the 8192 bytes from one box of 64 MN elements to the next.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride, version, layout
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, bool mn_major) {
+  return ((saddr & 0x3FFFF) >> 4) | ((mn_major ? (8192u >> 4) : 1u) << 16);
+}
 // D (TMEM) (+)= A (smem) * B (smem)^T, bf16 with fp32 accumulation, over the
 // pair of CTAs: 256 rows, 128 of A and of D in each; half of B's rows in each
-__device__ __forceinline__ void umma(uint32_t taddr, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                     uint32_t accumulate) {
+__device__ __forceinline__ void umma(uint32_t taddr, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(taddr),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n}" ::"r"(taddr),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
       : "memory");
 }
 // arrive on both CTAs' *bar once every MMA issued so far by this thread has completed
@@ -166,22 +183,6 @@ __device__ __forceinline__ float ex2(float v) {
   return r;
 }
 
-// Shared-memory descriptor of an operand tile with the 128-byte swizzle:
-// start (16-byte units), leading and stride byte offsets, version 1, layout
-// type 2.  K-major: 128-byte rows of 64 K elements, 8 rows to a 1024-byte
-// atom, stride 1024 from atom to atom (the leading offset is not used).
-// MN-major: boxes of 64 K rows of 64 MN elements (128 bytes each); 8 K rows
-// to an atom, stride 1024 from one to the next along K, and the leading
-// offset is the 8192 bytes from one box of 64 MN elements to the next.
-__device__ __forceinline__ uint64_t tile_desc(uint32_t saddr, bool mn_major) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFF) >> 4);
-  d |= (uint64_t)(mn_major ? (8192 >> 4) : 1) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
 // Instruction descriptor of kind::f16: fp32 accumulator (bit 4), A and B bf16
 // (bits 7 and 10), MN-major A and B (bits 15 and 16), N / 8 at bit 17, M / 16 at bit 24.
 __device__ __forceinline__ uint32_t inst_desc(int m, int n, bool a_mn, bool b_mn) {
@@ -287,7 +288,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
   int *bad = reinterpret_cast<int *>(tmem_slot + 1);
   static_assert(8 * (2 * kMaxStages + 5) + 16 <= 256, "barriers and flags fit their 256 bytes");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&full[s], 1);
@@ -334,78 +335,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
 
   if (warp >= kEpiWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    // The whole warp runs each loop, so that addresses and descriptors stay in
+    // uniform registers, and one lane issues: with the loops inside a one-lane
+    // branch the MMA warp needed 730 cycles for a stage's 512 of MMAs.
+    const bool one = elect_one();
+    int s = 0;           // stage
+    uint32_t phase = 0;  // of its barriers
     if (warp == kEpiWarps) {  // ------------------------------------------- loads
-      if (lane == 0) {
-        uint32_t it = 0;
-        for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
-          const Tile q = tile_at(t);
-          for (int c = 0; c < P.products && ok; ++c) {
-            const int za = (P.a_part >> (4 * c)) & 15, zb = (P.b_part >> (4 * c)) & 15;
-            for (int kb = q.k0; kb < q.k0 + q.nk; ++kb, ++it) {
-              const int s = (int)(it % P.stages);
-              if (!mbar_wait(&empty[s], ((it / P.stages) & 1) ^ 1)) {
-                ok = false;
-                break;
-              }
-              uint8_t *a = smem + (uint32_t)s * stage_bytes, *b = a + kStageA;
-              const uint32_t bar = at_leader(&full[s]);  // the leader's barrier counts both CTAs' bytes
-              if (rank == 0) mbar_expect_tx(&full[s], 2 * stage_bytes);
-              const int am = q.m0 + (int)rank * kMCta, bn = q.n0 + (int)rank * nb;
-              if (kAmn) {
-                tma_load(a, &map_a, am, kb * kKb, za, bar);
-                tma_load(a + 8192, &map_a, am + 64, kb * kKb, za, bar);
-              } else {
-                tma_load(a, &map_a, kb * kKb, am, za, bar);
-              }
-              if (kBmn) {
-                for (int j = 0; j < nb; j += 64) tma_load(b + j * 128, &map_b, bn + j, kb * kKb, zb, bar);
-              } else {
-                tma_load(b, &map_b, kb * kKb, bn, zb, bar);
-              }
-            }
-          }
-        }
-      }
-    } else if (warp == kEpiWarps + 1) {  // -------------------------------- MMAs
-      if (lane == 0 && rank == 0) {
-        const uint32_t idesc = inst_desc(kM, P.nt, kAmn, kBmn);
-        uint32_t it = 0;
-        int n_acc = 0;
-        for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
-          const Tile q = tile_at(t);
-          if (q.nk == 0) continue;
-          const int steps = P.products * q.nk, lead = steps - q.nk;
-          for (int i = 0; i < steps && ok; ++n_acc) {  // a unit of steps per accumulator
-            const int buf = n_acc & 1;
-            if (!mbar_wait(&acc_free[buf], ((n_acc >> 1) & 1) ^ 1)) {
+      const uint32_t bar0 = at_leader(full);  // the leader's barriers count both CTAs' bytes
+      for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
+        const Tile q = tile_at(t);
+        const int am = q.m0 + (int)rank * kMCta, bn = q.n0 + (int)rank * nb;
+        for (int c = 0; c < P.products && ok; ++c) {
+          const int za = (P.a_part >> (4 * c)) & 15, zb = (P.b_part >> (4 * c)) & 15;
+          for (int k = q.k0 * kKb; k < (q.k0 + q.nk) * kKb; k += kKb) {
+            if (!mbar_wait(&empty[s], phase ^ 1)) {
               ok = false;
               break;
             }
-            tc_fence_after();
-            const uint32_t d = tmem + (uint32_t)(buf * kNMax);
-            const int end = i < lead ? lead : min(steps, i + P.unit);
-            for (int u = 0; i < end; ++i, ++it, ++u) {
-              const int s = (int)(it % P.stages);
-              if (!mbar_wait(&full[s], (it / P.stages) & 1)) {
-                ok = false;
-                break;
+            if (one) {
+              uint8_t *a = smem + (uint32_t)s * stage_bytes, *b = a + kStageA;
+              const uint32_t bar = bar0 + 8u * s;
+              if (rank == 0) mbar_expect_tx(&full[s], 2 * stage_bytes);
+              if (kAmn) {
+                tma_load(a, &map_a, am, k, za, bar);
+                tma_load(a + 8192, &map_a, am + 64, k, za, bar);
+              } else {
+                tma_load(a, &map_a, k, am, za, bar);
               }
-              tc_fence_after();
-              const uint32_t a = su32(smem) + (uint32_t)s * stage_bytes, b = a + kStageA;
-#pragma unroll
-              for (int k = 0; k < kKb / 16; ++k) {
-                // 16 K elements: 32 bytes within the swizzled row, or 16 rows of 128 bytes
-                const uint64_t da = tile_desc(a + (kAmn ? k * 2048 : k * 32), kAmn);
-                const uint64_t db = tile_desc(b + (kBmn ? k * 2048 : k * 32), kBmn);
-                umma(d, da, db, idesc, (u | k) != 0);
+              if (kBmn) {
+                tma_load(b, &map_b, bn, k, zb, bar);
+                if (nb > 64) tma_load(b + 8192, &map_b, bn + 64, k, zb, bar);
+              } else {
+                tma_load(b, &map_b, k, bn, zb, bar);
               }
-              umma_commit(&empty[s]);
             }
-            if (ok) umma_commit(&acc_full[buf]);
+            __syncwarp();
+            if (++s == P.stages) {
+              s = 0;
+              phase ^= 1;
+            }
           }
         }
-        umma_commit(drained);
       }
+    } else if (warp == kEpiWarps + 1 && rank == 0) {  // ------------------- MMAs
+      const uint32_t idesc = inst_desc(kM, P.nt, kAmn, kBmn);
+      const uint32_t a_lo = desc_lo(su32(smem), kAmn), b_lo = desc_lo(su32(smem) + kStageA, kBmn);
+      constexpr uint32_t kA16 = kAmn ? 128 : 2, kB16 = kBmn ? 128 : 2;  // 16 of K in 16-byte units: 16 rows, or 32 bytes
+      int n_acc = 0;
+      for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
+        const Tile q = tile_at(t);
+        const int steps = P.products * q.nk, lead = steps - q.nk;
+        bool ready = false;  // the next stage's bytes have been seen
+        for (int i = 0; i < steps && ok; ++n_acc) {  // a unit of steps per accumulator
+          const int buf = n_acc & 1;
+          if (!mbar_wait(&acc_free[buf], ((n_acc >> 1) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem + (uint32_t)(buf * kNMax);
+          const int end = i < lead ? lead : min(steps, i + P.unit);
+          uint32_t more = 0;  // the unit's first MMA overwrites
+          for (; i < end; ++i) {
+            if (!ready && !mbar_wait(&full[s], phase)) {
+              ok = false;
+              break;
+            }
+            const uint32_t off = (uint32_t)s * (stage_bytes >> 4);
+            const int cur = s;
+            if (++s == P.stages) {
+              s = 0;
+              phase ^= 1;
+            }
+            ready = i + 1 < steps && mbar_try(&full[s], phase);  // answered while the MMAs below are issued
+            if (one) {
+#pragma unroll
+              for (int k = 0; k < kKb / 16; ++k)
+                umma(d, a_lo + off + k * kA16, b_lo + off + k * kB16, idesc, k == 0 ? more : 1u);
+              umma_commit(&empty[cur]);
+            }
+            __syncwarp();
+            more = 1;
+          }
+          if (ok && one) umma_commit(&acc_full[buf]);
+          __syncwarp();
+        }
+      }
+      if (one) umma_commit(drained);
+      __syncwarp();
     }
   } else {  // -------------------------------------------------------- epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
