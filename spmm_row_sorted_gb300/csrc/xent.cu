@@ -120,7 +120,11 @@ __device__ __forceinline__ void tma_add(const CUtensorMap *map, const void *src,
                : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// all but the newest `kLeft` stores have read their shared memory
+template <int kLeft>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
+}
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -160,22 +164,25 @@ __device__ __forceinline__ void umma_commit(uint64_t *bar) {
       "h"((uint16_t)3)
       : "memory");
 }
-// 32 consecutive fp32 columns of this thread's TMEM lane
+// 32 consecutive fp32 columns of this thread's TMEM lane; not there before tmem_wait and tmem_ready
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
-  __syncwarp();
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(taddr)
       : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// ties a load's registers to the wait before it: no use of them moves above
+__device__ __forceinline__ void tmem_ready(float (&v)[32]) {
+  asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+        "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]),
+        "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
+        "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
 }
 __device__ __forceinline__ float ex2(float v) {
   float r;
@@ -431,6 +438,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
     uint8_t *stage = staging + warp * kStaging;
     constexpr float kLog2e = 1.4426950408889634f;
     int n_acc = 0;
+    uint32_t n_store = 0;
     for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
       const Tile q = tile_at(t);
       if (q.nk == 0) continue;
@@ -465,21 +473,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
         }
         tc_fence_after();
         const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * kNMax + half * c_end);
+        const int chunks = c_end / 32;
+        auto release = [&] {  // the accumulator has been read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(at_leader(&acc_free[buf]));
+        };
+        __syncwarp();
+        if (u == 0) {  // all loads in flight at once; later units two at a time (their sums need registers too)
 #pragma unroll
-        for (int h = 0; h < kChunks; ++h)
-          if (32 * h < c_end) {
-            if (u == 0) {
-              tmem_ld32(from + 32u * h, acc[h]);
-            } else {
-              float v[32];
-              tmem_ld32(from + 32u * h, v);
+          for (int h = 0; h < kChunks; ++h)
+            if (h < chunks) tmem_ld32(from + 32u * h, acc[h]);
+          tmem_wait();
+          release();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) acc[h][j] += v[j];
+          for (int h = 0; h < kChunks; ++h) tmem_ready(acc[h]);
+        } else {
+#pragma unroll
+          for (int h = 0; h < kChunks; h += 2) {
+            if (h >= chunks) break;
+            float v[2][32];
+            tmem_ld32(from + 32u * h, v[0]);
+            if (h + 1 < chunks) tmem_ld32(from + 32u * (h + 1), v[1]);
+            tmem_wait();
+            if (h + 2 >= chunks) release();
+            tmem_ready(v[0]);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[h][j] += v[0][j];
+            if (h + 1 < chunks) {
+              tmem_ready(v[1]);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) acc[h + 1][j] += v[1][j];
             }
           }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_at(at_leader(&acc_free[buf]));
+        }
       }
       if (!ok) break;
       if (kMode == kStats) {
@@ -522,13 +549,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
           if (c >= c_end) break;
           float(&v)[32] = acc[h];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float p = ex2((v[j] - lse) * kLog2e);
-            v[j] = g == 0.f ? 0.f : g * (tcol == c + j ? p - 1.f : p);
+          for (int j = 0; j < 32; ++j) v[j] = g * ex2((v[j] - lse) * kLog2e);
+          if (tcol >= c && tcol < c + 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (tcol == c + j) v[j] -= g;
           }
-          // 32 rows x 64 bytes per store
+          if (g == 0.f) {  // not trained on, whatever its logits
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+          }
+          // 32 rows x 64 bytes per store, from two buffers in turn
           for (int part = 0; part < P.out_parts; ++part) {
-            if (lane == 0) bulk_wait_read();
+            uint8_t *to = stage + (n_store++ & 1) * (kStaging / 2);
+            if (lane == 0) bulk_wait_read<1>();
             __syncwarp();
 #pragma unroll
             for (int ch = 0; ch < 4; ++ch) {
@@ -537,7 +571,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
               u.y = pack_bf16(v[8 * ch + 2], v[8 * ch + 3]);
               u.z = pack_bf16(v[8 * ch + 4], v[8 * ch + 5]);
               u.w = pack_bf16(v[8 * ch + 6], v[8 * ch + 7]);
-              *reinterpret_cast<uint4 *>(stage + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) = u;
+              *reinterpret_cast<uint4 *>(to + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) = u;
               if (P.out_parts > 1) {  // what the part leaves over
                 v[8 * ch] -= bf16_lo(u.x);
                 v[8 * ch + 1] -= bf16_hi(u.x);
@@ -552,9 +586,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
             fence_async_shared();
             __syncwarp();
             if (lane == 0 && col0 + c < P.n && m0 + quarter * 32 < P.m) {
-              tma_store(&map_o, stage, col0 + c, m0 + quarter * 32, part);
-              bulk_commit();
+              tma_store(&map_o, to, col0 + c, m0 + quarter * 32, part);
             }
+            if (lane == 0) bulk_commit();  // an empty group where nothing was stored keeps the buffers' turns
           }
         }
       } else {
@@ -572,7 +606,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
           const int c = 32 * h;
           if (c >= c_end) break;
           float(&v)[32] = acc[h];
-          if (lane == 0 && (c % step) == 0) bulk_wait_read();
+          if (lane == 0 && (c % step) == 0) bulk_wait_read<0>();
           __syncwarp();
           if (wide) {
 #pragma unroll
