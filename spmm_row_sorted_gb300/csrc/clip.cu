@@ -9,6 +9,9 @@
 // out on the device).  The work is cut into pieces of kPiece bytes of one
 // tensor, and a block finds a piece's tensor by a search in the pieces' prefix.
 //
+// Up to 65,536 elements in at most 16 tensors, one cluster of blocks does both
+// passes in one launch, its elements in registers.
+//
 // Each thread adds its squares in fp32; blocks leave their sums in the
 // workspace and every block of the second pass adds them in the same order, in
 // fp64, so no atomics are needed and results repeat.  Squares are summed at
@@ -136,57 +139,69 @@ __global__ void __launch_bounds__(kThreads) k_clip_norm(const __grid_constant__ 
   if (threadIdx.x == 0) sums[blockIdx.x] = b;
 }
 
-// the norm from all blocks' sums, the same in every block
-__device__ __forceinline__ float total_norm(const Sum3 *__restrict__ sums, int n_sums) {
-  __shared__ double red[3][kThreads / 32];
-  double m = 0, l = 0, h = 0;
-  for (int i = threadIdx.x; i < n_sums; i += kThreads) {
-    m += (double)sums[i].mid;
-    l += (double)sums[i].low;
-    h += (double)sums[i].high;
-  }
+// The norm from all blocks' sums, the same in every block: one warp adds them
+// in fp64 (which is slow here), the scaled sums only where they are needed.
+__device__ __forceinline__ double warp_total(const float *p, int n_sums) {
+  double m = 0;
+  for (int i = threadIdx.x; i < n_sums; i += 32) m += (double)__ldg(p + 3 * i);
 #pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    m += __shfl_xor_sync(0xffffffffu, m, d);
-    l += __shfl_xor_sync(0xffffffffu, l, d);
-    h += __shfl_xor_sync(0xffffffffu, h, d);
+  for (int d = 16; d; d >>= 1) m += __shfl_xor_sync(0xffffffffu, m, d);
+  return m;
+}
+__device__ __forceinline__ float root(double sum, float back) {
+  // sqrt in fp32 of a value scaled into its range by an even power of two
+  int e;
+  double f = frexp(sum, &e);
+  if (e & 1) {
+    f *= 2.0;
+    e -= 1;
   }
-  if ((threadIdx.x & 31) == 0) {
-    red[0][threadIdx.x >> 5] = m;
-    red[1][threadIdx.x >> 5] = l;
-    red[2][threadIdx.x >> 5] = h;
+  return ldexpf(sqrtf((float)f), e / 2) * back;
+}
+__device__ __forceinline__ float norm_of(double mid, double low, double high) {
+  if (isnan(mid)) return (float)mid;
+  if (isinf(mid)) return isinf(low) ? INFINITY : root(low, 1.f / kDown);
+  if (mid < (double)kTiny) return high > 0 ? root(high, 1.f / kUp) : 0.f;
+  return root(mid, 1.f);
+}
+__device__ __forceinline__ float total_norm(const Sum3 *__restrict__ sums, int n_sums) {
+  __shared__ float result;
+  if (threadIdx.x < 32) {
+    const float *p = reinterpret_cast<const float *>(sums);
+    const double mid = warp_total(p, n_sums);
+    double low = 0, high = 0;
+    if (isinf(mid)) low = warp_total(p + 1, n_sums);
+    if (mid < (double)kTiny) high = warp_total(p + 2, n_sums);
+    if (threadIdx.x == 0) result = norm_of(mid, low, high);
   }
   __syncthreads();
-  m = l = h = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    m += red[0][w];
-    l += red[1][w];
-    h += red[2][w];
-  }
-  if (isnan(m)) return (float)m;
-  if (isinf(m)) return (float)(sqrt(l) * 0x1p80);
-  if (m < (double)kTiny) return (float)(sqrt(h) * 0x1p-100);
-  return (float)sqrt(m);
+  return result;
 }
 
+// o[0 .. m) = p[0 .. m) * f, in 16-byte accesses on both sides also where the
+// two lie at different offsets from a 16-byte boundary: the eight (fp32: four)
+// elements of an aligned piece of o then lie in two neighbouring aligned pieces
+// of p, the second of which is the next lane's first (so it comes from L1), and
+// a funnel shift by the offset, the same for the whole tensor, joins them.
 template <typename T>
 __device__ __forceinline__ void scale_piece(const T *p, T *o, int64_t m, float f) {
   constexpr int kN = 16 / (int)sizeof(T);
+  constexpr int kU = 4;
   typedef Pack<T, 16> V;
-  if ((((uintptr_t)p ^ (uintptr_t)o) & 15) == 0) {
-    int64_t lead = (int64_t)((16 - ((uintptr_t)p & 15)) & 15) / (int64_t)sizeof(T);
-    if (lead > m) lead = m;
-    const int64_t vecs = (m - lead) / kN;
-    const uint4 *v = reinterpret_cast<const uint4 *>(p + lead);
-    uint4 *w = reinterpret_cast<uint4 *>(o + lead);
+  int64_t lead = (int64_t)((16 - ((uintptr_t)o & 15)) & 15) / (int64_t)sizeof(T);
+  if (lead > m) lead = m;
+  int64_t vecs = (m - lead) / kN;
+  const uint32_t off = (uint32_t)((uintptr_t)(p + lead) & 15);  // bytes that p's elements lie past a boundary
+  const uint4 *v = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p + lead) & ~(uintptr_t)15);
+  uint4 *w = reinterpret_cast<uint4 *>(o + lead);
+  if (off == 0) {
     int64_t i = threadIdx.x;
-    for (; i + 3 * kThreads < vecs; i += 4 * kThreads) {
-      V a[4];
+    for (; i + (kU - 1) * kThreads < vecs; i += kU * kThreads) {
+      V a[kU];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) a[u].raw = __ldcs(v + i + u * kThreads);
+      for (int u = 0; u < kU; ++u) a[u].raw = __ldcs(v + i + u * kThreads);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kU; ++u) {
 #pragma unroll
         for (int e = 0; e < kN; ++e) a[u].set(e, a[u].get(e) * f);
         __stcs(w + i + u * kThreads, a[u].raw);
@@ -199,19 +214,52 @@ __device__ __forceinline__ void scale_piece(const T *p, T *o, int64_t m, float f
       for (int e = 0; e < kN; ++e) a.set(e, a.get(e) * f);
       __stcs(w + i, a.raw);
     }
-    for (int64_t j = threadIdx.x; j < lead; j += kThreads) o[j] = from_f32<T>(to_f32(p[j]) * f);
-    for (int64_t j = lead + vecs * kN + threadIdx.x; j < m; j += kThreads) o[j] = from_f32<T>(to_f32(p[j]) * f);
-  } else {  // the two lie at different offsets from a 16-byte boundary
-    int64_t j = threadIdx.x;
-    for (; j + 7 * kThreads < m; j += 8 * kThreads) {
-      T a[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) a[u] = p[j + u * kThreads];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) o[j + u * kThreads] = from_f32<T>(to_f32(a[u]) * f);
+  } else {
+    // the first and the last piece are read by element: their aligned neighbours may lie outside the tensor
+    if (vecs > 0) {
+      lead += kN;
+      --vecs;
+      ++v;
+      ++w;
     }
-    for (; j < m; j += kThreads) o[j] = from_f32<T>(to_f32(p[j]) * f);
+    if (vecs > 0) --vecs;
+    const int words = (int)(off >> 2);
+    const bool half = (off & 2) != 0;
+    auto join = [&](const uint4 &x, const uint4 &y) {
+      uint32_t t[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      if (words & 2) {
+#pragma unroll
+        for (int k = 0; k < 6; ++k) t[k] = t[k + 2];
+      }
+      if (words & 1) {
+#pragma unroll
+        for (int k = 0; k < 5; ++k) t[k] = t[k + 1];
+      }
+      if (half) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) t[k] = __funnelshift_r(t[k], t[k + 1], 16);
+      }
+      V a;
+      a.raw = make_uint4(t[0], t[1], t[2], t[3]);
+#pragma unroll
+      for (int e = 0; e < kN; ++e) a.set(e, a.get(e) * f);
+      return a.raw;
+    };
+    int64_t i = threadIdx.x;
+    for (; i + (kU - 1) * kThreads < vecs; i += kU * kThreads) {
+      uint4 x[kU], y[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        x[u] = __ldg(v + i + u * kThreads);
+        y[u] = __ldg(v + i + u * kThreads + 1);
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) __stcs(w + i + u * kThreads, join(x[u], y[u]));
+    }
+    for (; i < vecs; i += kThreads) __stcs(w + i, join(__ldg(v + i), __ldg(v + i + 1)));
   }
+  for (int64_t j = threadIdx.x; j < lead; j += kThreads) o[j] = from_f32<T>(to_f32(p[j]) * f);
+  for (int64_t j = lead + vecs * kN + threadIdx.x; j < m; j += kThreads) o[j] = from_f32<T>(to_f32(p[j]) * f);
 }
 
 template <int kMost>
@@ -241,6 +289,101 @@ __global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__
   }
 }
 
+// A few small tensors: one cluster of kCluster blocks does it all in one
+// launch.  Its threads keep their elements in registers between the norm and
+// the scaling; the blocks' sums meet in the first block's shared memory.
+constexpr int kCluster = 8;
+constexpr int kClusterThreads = 1024;
+constexpr int kKeep = 8;  // elements per thread
+constexpr int64_t kSmallMost = (int64_t)kCluster * kClusterThreads * kKeep;
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kClusterThreads)
+    k_clip_small(const __grid_constant__ ClipTable<kSmallTable> t, int scale, float max_norm, float *norm) {
+  pdl_wait();
+  __shared__ Sum3 part[kClusterThreads / 32];
+  __shared__ Sum3 all[kCluster];  // of the first block
+  __shared__ float result;
+  uint32_t rank;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this block runs: its shared memory is there
+  // first[k]: elements before tensor k
+  const uint32_t total = t.first[t.count];
+  const uint32_t i0 = rank * kClusterThreads + threadIdx.x;
+  float v[kKeep];
+  int owner[kKeep];
+  Sum3 s = {0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < kKeep; ++j) {
+    const uint32_t i = i0 + (uint32_t)j * (kCluster * kClusterThreads);
+    v[j] = 0.f;
+    owner[j] = 0;
+    if (i < total) {
+      int k = 0;
+      while (k + 1 < t.count && t.first[k + 1] <= i) ++k;
+      owner[j] = k;
+      const uint32_t e = i - t.first[k];
+      v[j] = t.n[k] >= 0 ? reinterpret_cast<const float *>(t.in[k])[e] : to_f32(reinterpret_cast<const bf16 *>(t.in[k])[e]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kKeep; ++j) add_square(s, v[j]);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    s.mid += __shfl_xor_sync(0xffffffffu, s.mid, d);
+    s.low += __shfl_xor_sync(0xffffffffu, s.low, d);
+    s.high += __shfl_xor_sync(0xffffffffu, s.high, d);
+  }
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+  __syncthreads();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (threadIdx.x < 32) {
+    s = part[threadIdx.x];
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+      s.mid += __shfl_xor_sync(0xffffffffu, s.mid, d);
+      s.low += __shfl_xor_sync(0xffffffffu, s.low, d);
+      s.high += __shfl_xor_sync(0xffffffffu, s.high, d);
+    }
+    if (threadIdx.x < kCluster) {  // into every block's copy of `all`, at this block's place
+      uint32_t to;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;"
+          : "=r"(to)
+          : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(&all[rank]))), "r"(threadIdx.x));
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(s.mid) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4), "f"(s.low) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 8), "f"(s.high) : "memory");
+    }
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (threadIdx.x == 0) {
+    double m = 0, l = 0, h = 0;
+    for (int b = 0; b < kCluster; ++b) {
+      m += (double)all[b].mid;
+      l += (double)all[b].low;
+      h += (double)all[b].high;
+    }
+    result = norm_of(m, l, h);
+    if (norm && rank == 0) *norm = result;
+  }
+  __syncthreads();
+  if (!scale) return;
+  float f = max_norm / (result + 1e-6f);
+  if (f > 1.f) f = 1.f;
+#pragma unroll
+  for (int j = 0; j < kKeep; ++j) {
+    const uint32_t i = i0 + (uint32_t)j * (kCluster * kClusterThreads);
+    if (i >= total) continue;
+    const int k = owner[j];
+    if (f == 1.f && t.out[k] == t.in[k]) continue;
+    const uint32_t e = i - t.first[k];
+    if (t.n[k] >= 0)
+      reinterpret_cast<float *>(t.out[k])[e] = v[j] * f;
+    else
+      reinterpret_cast<bf16 *>(t.out[k])[e] = from_f32<bf16>(v[j] * f);
+  }
+}
+
 inline int64_t pieces_of(int64_t n, snack_dtype t) { return ceil_div(n * (int64_t)dtype_size(t), kPiece); }
 
 struct ClipCall {
@@ -260,6 +403,28 @@ int table_for(int32_t n) { return n <= kSmallTable ? kSmallTable : n <= kMidTabl
 
 template <int kMost>
 snack_status run_clip(const ClipCall &c, cudaStream_t s) {
+  if (kMost == kSmallTable) {  // few enough to stay in one cluster's registers
+    int64_t total = 0;
+    for (int32_t k = 0; k < c.n && total <= kSmallMost; ++k) total += c.numel[k];
+    if (total <= kSmallMost) {
+      ClipTable<kSmallTable> t;
+      t.count = 0;
+      uint32_t at = 0;
+      for (int32_t k = 0; k < c.n; ++k) {
+        if (c.numel[k] == 0) continue;
+        t.in[t.count] = c.grads[k];
+        t.out[t.count] = c.outs ? c.outs[k] : nullptr;
+        t.n[t.count] = c.types[k] == SNACK_F32 ? c.numel[k] : -c.numel[k] - 1;
+        t.first[t.count++] = at;
+        at += (uint32_t)c.numel[k];
+      }
+      t.first[t.count] = at;
+      return launch_pdl(k_clip_small, kCluster, kClusterThreads, 0, s, t, c.outs ? 1 : 0, c.max_norm, c.norm) ==
+                     cudaSuccess
+                 ? SNACK_OK
+                 : SNACK_ERR_CUDA;
+    }
+  }
   const int64_t groups = c.n > 0 ? groups_of(c.n, kMost) : 1;
   const int most_blocks = c.sms * kBlocksPerSm;
   int n_sums = 0;

@@ -10,13 +10,13 @@
 // The gradient sorts the (id, position) pairs, stably, so that each row's
 // terms lie together in the order of their positions: one sum per row in that
 // order, in fp32, with no atomics on values, so results repeat bit for bit.
-// Up to kRankMax tokens one kernel finds each token's place by counting the
-// pairs before it (n^2 comparisons, no passes); above that an LSD radix sort.
-// The sorted list is cut into chunks of equal length, one warp per chunk and
-// column segment, so that a frequent token's many rows are shared by many
-// warps: a run that crosses a chunk's border leaves fp32 partial sums, which a
-// second kernel adds in order.  The blocks after those of the sums fill the
-// rows that no token names (found by a search in the sorted list) with zeros.
+// One kernel finds each token's place by counting the pairs before it (n^2
+// comparisons, no passes) while its other blocks clear the table's gradient;
+// where that would take longer than the clearing, an LSD radix sort does.  The
+// sorted list is cut into chunks of equal length, one warp per chunk and column
+// segment, so that a frequent token's many rows are shared by many warps: a run
+// that crosses a chunk's border leaves fp32 partial sums, which a second kernel
+// adds in order.
 #include <stdint.h>
 
 #include "internal.hpp"
@@ -59,41 +59,77 @@ __global__ void __launch_bounds__(256) k_embed_fwd(TokenSrc ids, int64_t n, cons
 
 // ------------------------------------------------------------ sorted order
 
-constexpr int kRankMax = 8192;
 constexpr int kRankRows = 32;  // tokens per block
 constexpr int kRankThreads = 256;
+constexpr int kRankTile = 4096;  // ids in shared memory at a time
+
+// The rows of a table to clear: accesses of 16 bytes where its rows allow it.
+struct ZeroFill {
+  uint8_t *base;
+  int64_t row_bytes, ld_bytes, rows;  // rows 0: nothing to clear
+  int wide;                           // 16-byte accesses, else 2-byte ones
+};
+
+// Row groups of kZeroRows per block: a warp clears one row after the other.
+constexpr int kZeroRows = 64;
+__device__ __forceinline__ void zero_rows(const ZeroFill &z, int64_t block) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t r1 = min(z.rows, (block + 1) * kZeroRows);
+  for (int64_t r = block * kZeroRows + warp; r < r1; r += kRankThreads / 32) {
+    uint8_t *row = z.base + r * z.ld_bytes;
+    if (z.wide) {
+      uint4 *o = reinterpret_cast<uint4 *>(row);
+      const int64_t n = z.row_bytes / 16;
+      for (int64_t i = lane; i < n; i += 32) __stcs(o + i, make_uint4(0, 0, 0, 0));
+    } else {
+      uint16_t *o = reinterpret_cast<uint16_t *>(row);
+      const int64_t n = z.row_bytes / 2;
+      for (int64_t i = lane; i < n; i += 32) o[i] = 0;
+    }
+  }
+}
 
 // Place of token i among all: the number of (id, position) pairs before its
-// own.  Lane l of every warp holds token 32 blockIdx.x + l; the eight warps
-// count over interleaved groups of 32 tokens, whose ids they read from shared
-// memory (every lane the same word).
+// own.  Lane l of every warp holds token 32 b + l; the eight warps count over
+// interleaved groups of 32 tokens, whose ids they read from shared memory
+// (every lane the same word).  The blocks after the first `rank_blocks` clear
+// the table meanwhile: the counting is arithmetic, the clearing stores.
 __global__ void __launch_bounds__(kRankThreads) k_rank(TokenSrc ids, int n, uint32_t *__restrict__ keys,
-                                                       uint32_t *__restrict__ pos) {
+                                                       uint32_t *__restrict__ pos, int rank_blocks, ZeroFill zero) {
   pdl_wait();
-  extern __shared__ __align__(16) uint32_t s_ids[];
+  if ((int)blockIdx.x >= rank_blocks) {
+    zero_rows(zero, (int64_t)blockIdx.x - rank_blocks);
+    return;
+  }
+  __shared__ __align__(16) uint32_t s_ids[kRankTile];
   __shared__ int cnt[kRankThreads / 32][kRankRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int groups = (n + 31) / 32;
-  for (int i = threadIdx.x; i < groups * 32; i += kRankThreads) s_ids[i] = i < n ? ids.key(i) : 0xFFFFFFFFu;
-  __syncthreads();
   const int own = blockIdx.x;
   const int i = own * 32 + lane;
-  const uint32_t mine = s_ids[i];
+  const uint32_t mine = i < n ? ids.key(i) : 0u;
   int c = 0;
-  for (int g = warp; g < groups; g += kRankThreads / 32) {
-    const uint4 *q = reinterpret_cast<const uint4 *>(s_ids + g * 32);
-    if (g == own) {
+  for (int t0 = 0; t0 < n; t0 += kRankTile) {
+    const int m = min(kRankTile, n - t0);
+    const int groups = (m + 31) / 32;
+    __syncthreads();
+    for (int k = threadIdx.x; k < groups * 32; k += kRankThreads) s_ids[k] = k < m ? ids.key(t0 + k) : 0xFFFFFFFFu;
+    __syncthreads();
+    for (int g = warp; g < groups; g += kRankThreads / 32) {
+      const int at = t0 / 32 + g;
+      if (at == own) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const uint32_t k = s_ids[g * 32 + j];
-        c += (k < mine || (k == mine && j < lane)) ? 1 : 0;
-      }
-    } else {
-      const uint32_t lim = g < own ? mine + 1u : mine;  // an earlier token of the same id comes first
+        for (int j = 0; j < 32; ++j) {
+          const uint32_t k = s_ids[g * 32 + j];
+          c += (k < mine || (k == mine && j < lane)) ? 1 : 0;
+        }
+      } else {
+        const uint4 *q = reinterpret_cast<const uint4 *>(s_ids + g * 32);
+        const uint32_t lim = at < own ? mine + 1u : mine;  // an earlier token of the same id comes first
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint4 k = q[j];
-        c += (k.x < lim) + (k.y < lim) + (k.z < lim) + (k.w < lim);
+        for (int j = 0; j < 8; ++j) {
+          const uint4 k = q[j];
+          c += (k.x < lim) + (k.y < lim) + (k.z < lim) + (k.w < lim);
+        }
       }
     }
   }
@@ -106,6 +142,12 @@ __global__ void __launch_bounds__(kRankThreads) k_rank(TokenSrc ids, int n, uint
     keys[r] = mine;
     pos[r] = (uint32_t)i;
   }
+}
+
+// the clearing alone, beside the radix sort's kernels (or with no tokens at all)
+__global__ void __launch_bounds__(kRankThreads) k_zero(ZeroFill zero) {
+  pdl_wait();
+  zero_rows(zero, blockIdx.x);
 }
 
 // ------------------------------------------------------------ gradient
@@ -127,13 +169,12 @@ struct EmbedGrad {
   int chunk;        // sorted entries per chunk
   int64_t n_chunks;
   int n_seg;        // column segments
-  int64_t sum_blocks;
 };
 
 constexpr int kGradWarps = 8;
 constexpr int kGradVecs = 2;   // accesses per lane
 constexpr int kGradBatch = 4;  // rows in flight per lane
-constexpr int kZeroRows = 8;   // rows per warp of the zero fill
+constexpr int kJoinBatch = 4;  // chunks whose partial sums are in flight
 
 __device__ __forceinline__ int64_t lower_bound(const uint32_t *__restrict__ k, int64_t n, uint32_t v) {
   int64_t lo = 0, hi = n;
@@ -174,25 +215,6 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_embed_sum(const EmbedGrad g
   typedef Pack<T, B> P;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int acc_n = g.width / P::kN;
-  if ((int64_t)blockIdx.x >= g.sum_blocks) {  // ---- rows that no token names
-    const int64_t v0 = (((int64_t)blockIdx.x - g.sum_blocks) * kGradWarps + warp) * kZeroRows;
-    bool absent = false;
-    if (lane < kZeroRows && v0 + lane < (int64_t)g.vocab) {
-      const uint32_t v = (uint32_t)(v0 + lane);
-      const int64_t at = lower_bound(g.keys, g.n, v);
-      absent = at >= g.n || __ldg(g.keys + at) != v;
-    }
-    const unsigned rows = __ballot_sync(0xffffffffu, absent);
-    P z;
-#pragma unroll
-    for (int i = 0; i < P::kN; ++i) z.set(i, 0.f);
-    for (int r = 0; r < kZeroRows; ++r) {
-      if (!((rows >> r) & 1u)) continue;
-      typename P::R *o = reinterpret_cast<typename P::R *>(reinterpret_cast<T *>(g.dtable) + (v0 + r) * g.table_ld);
-      for (int a = lane; a < acc_n; a += 32) __stcs(o + a, z.raw);
-    }
-    return;
-  }
   const int64_t gw = (int64_t)blockIdx.x * kGradWarps + warp;
   const int64_t c = gw / g.n_seg;
   if (c >= g.n_chunks) return;
@@ -293,13 +315,24 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_embed_join(const EmbedGrad 
 #pragma unroll
     for (int i = 0; i < P::kN; ++i)
       acc[u][i] = a0 + 32 * u < acc_n ? g.part[(c * 2 + 1) * g.part_ld + (int64_t)i * acc_n + a0 + 32 * u] : 0.f;
-  for (int64_t q = c + 1; q <= last; ++q) {
-    const float *p = g.part + q * 2 * g.part_ld;
+  for (int64_t q0 = c + 1; q0 <= last; q0 += kJoinBatch) {  // loads of several chunks in flight, added in order
+    float v[kJoinBatch][kGradVecs][P::kN];
 #pragma unroll
-    for (int u = 0; u < kGradVecs; ++u)
-      if (a0 + 32 * u < acc_n)
+    for (int e = 0; e < kJoinBatch; ++e) {
+      const float *p = g.part + (q0 + e) * 2 * g.part_ld;
 #pragma unroll
-        for (int i = 0; i < P::kN; ++i) acc[u][i] += p[(int64_t)i * acc_n + a0 + 32 * u];
+      for (int u = 0; u < kGradVecs; ++u)
+#pragma unroll
+        for (int i = 0; i < P::kN; ++i)
+          v[e][u][i] = q0 + e <= last && a0 + 32 * u < acc_n ? __ldcg(p + (int64_t)i * acc_n + a0 + 32 * u) : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < kJoinBatch; ++e)
+#pragma unroll
+      for (int u = 0; u < kGradVecs; ++u)
+#pragma unroll
+        for (int i = 0; i < P::kN; ++i)
+          if (q0 + e <= last) acc[u][i] += v[e][u][i];
   }
   put_row<T, B>(g, cur, a0, acc_n, acc);
 }
@@ -314,19 +347,29 @@ int key_bits(uint32_t vocab) {
 
 constexpr int kSegElems = 32 * kGradVecs;  // accesses per segment
 
+// Whether the places are found by counting (n^2 comparisons, one kernel, beside
+// the clearing) or by a radix sort (three or four passes of four kernels).
+// Measured on GB300: the counting takes n^2 * 0.06 ns beside other work, the
+// sort about 55 us at 32768 tokens, in which memory idles.
+bool by_counting(int64_t n, int64_t clear_bytes) {
+  const double count_us = (double)n * (double)n * 6e-8, clear_us = (double)clear_bytes / 6.5e6;
+  return n <= 65536 && count_us <= (clear_us > 25.0 ? clear_us : 25.0);
+}
+
 struct GradWs {
   size_t keys, pos, k0, v0, k1, v1, temp, part, total;
   int chunk;
   int64_t n_chunks, part_ld;
 };
 
-// Chunks short enough that a small call still has a few thousand warps, at
-// most kMaxChunk entries; the partial sums of a run that covers many chunks
-// are added by one warp per segment, so long calls get longer chunks.
+// Chunks short enough that a small call still has some thousand warps; the
+// partial sums of a run that covers many chunks are added by one warp per
+// segment, so long calls get longer chunks.
 GradWs grad_ws(int64_t n, int32_t width) {
   GradWs w;
+  const int64_t segs = ceil_div(width, 512);  // at 16-byte accesses; narrower ones have more
   int64_t chunk = 8;
-  while (chunk < 4096 && n / chunk > 2048) chunk *= 2;
+  while (chunk < 4096 && n / chunk * segs > 8192) chunk *= 2;
   w.chunk = (int)chunk;
   w.n_chunks = n > 0 ? (n + chunk - 1) / chunk : 0;
   w.part_ld = (int64_t)align_up((size_t)width, 4);
@@ -335,7 +378,7 @@ GradWs grad_ws(int64_t n, int32_t width) {
   o += align_up((size_t)n * 4, kAlign);
   w.pos = o;
   o += align_up((size_t)n * 4, kAlign);
-  const bool radix = n > kRankMax;
+  const bool radix = n > 4096;  // it may be wanted
   w.k0 = o;
   if (radix) o += align_up((size_t)n * 4, kAlign);
   w.v0 = o;
@@ -369,14 +412,11 @@ template <typename T, int B>
 cudaError_t launch_grad(EmbedGrad g, cudaStream_t s) {
   const int acc = g.width / Pack<T, B>::kN;
   g.n_seg = (int)ceil_div(acc, kSegElems);
-  g.sum_blocks = ceil_div(g.n_chunks * g.n_seg, kGradWarps);
-  const int64_t zero_blocks = g.accumulate ? 0 : ceil_div((int64_t)g.vocab, (int64_t)kGradWarps * kZeroRows);
-  const int64_t blocks = g.sum_blocks + zero_blocks;
-  if (blocks == 0) return cudaSuccess;
+  const int64_t blocks = ceil_div(g.n_chunks * g.n_seg, kGradWarps);
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaError_t e = launch_pdl(k_embed_sum<T, B>, (unsigned)blocks, kGradWarps * 32, 0, s, (const EmbedGrad)g);
   if (e != cudaSuccess || g.n_chunks < 2) return e;
-  return launch_pdl(k_embed_join<T, B>, (unsigned)g.sum_blocks, kGradWarps * 32, 0, s, (const EmbedGrad)g);
+  return launch_pdl(k_embed_join<T, B>, (unsigned)blocks, kGradWarps * 32, 0, s, (const EmbedGrad)g);
 }
 
 }  // namespace
@@ -464,29 +504,41 @@ snack_status snack_embed_grad(const void *ids, snack_index ids_t, int64_t n, con
   g.chunk = W.chunk;
   g.n_chunks = W.n_chunks;
   g.part_ld = W.part_ld;
-  cudaError_t e = cudaSuccess;
-  if (n > 0) {
-    uint32_t *keys = reinterpret_cast<uint32_t *>(w + W.keys), *pos = reinterpret_cast<uint32_t *>(w + W.pos);
-    g.keys = keys;
-    g.pos = pos;
-    g.part = reinterpret_cast<float *>(w + W.part);
-    const TokenSrc src{ids, ids_t == SNACK_I64, (uint32_t)vocab};
-    if (n <= kRankMax) {
-      const size_t smem = align_up((size_t)n, 32) * 4;
-      e = launch_pdl(k_rank, (unsigned)ceil_div(n, kRankRows), kRankThreads, smem, s, src, (int)n, keys, pos);
-    } else {
-      try {
-        e = radix_sort_custom<uint32_t>(src, ArrayDst<uint32_t>{keys, pos}, n, key_bits((uint32_t)vocab),
-                                        reinterpret_cast<uint32_t *>(w + W.k0), reinterpret_cast<uint32_t *>(w + W.v0),
-                                        reinterpret_cast<uint32_t *>(w + W.k1), reinterpret_cast<uint32_t *>(w + W.v1),
-                                        w + W.temp, s);
-      } catch (...) {  // the shared-memory table could not grow
-        return SNACK_ERR_CUDA;
-      }
-    }
-    if (e != cudaSuccess) return SNACK_ERR_CUDA;
+  ZeroFill z = {};
+  if (!accumulate) {
+    z.base = reinterpret_cast<uint8_t *>(dtable);
+    z.row_bytes = (int64_t)width * (int64_t)es;
+    z.ld_bytes = dtable_ld * (int64_t)es;
+    z.rows = vocab;
+    z.wide = access_bytes((uintptr_t)dtable | (uintptr_t)z.ld_bytes | (uintptr_t)z.row_bytes) == 16;
   }
-  const int b = access_bytes((uintptr_t)dtable | (n > 0 ? (uintptr_t)dout : 0) | (uintptr_t)(dtable_ld * es) |
+  const int64_t zero_blocks = ceil_div(z.rows, (int64_t)kZeroRows);
+  const bool counting = n > 0 && by_counting(n, z.rows * z.row_bytes);
+  cudaError_t e = cudaSuccess;
+  if (!counting && zero_blocks > 0) e = launch_pdl(k_zero, (unsigned)zero_blocks, kRankThreads, 0, s, z);
+  if (e != cudaSuccess) return SNACK_ERR_CUDA;
+  if (n == 0) return SNACK_OK;
+  uint32_t *keys = reinterpret_cast<uint32_t *>(w + W.keys), *pos = reinterpret_cast<uint32_t *>(w + W.pos);
+  g.keys = keys;
+  g.pos = pos;
+  g.part = reinterpret_cast<float *>(w + W.part);
+  const TokenSrc src{ids, ids_t == SNACK_I64, (uint32_t)vocab};
+  if (counting) {
+    const int rank_blocks = (int)ceil_div(n, kRankRows);
+    e = launch_pdl(k_rank, (unsigned)(rank_blocks + zero_blocks), kRankThreads, 0, s, src, (int)n, keys, pos, rank_blocks,
+                   z);
+  } else {
+    try {
+      e = radix_sort_custom<uint32_t>(src, ArrayDst<uint32_t>{keys, pos}, n, key_bits((uint32_t)vocab),
+                                      reinterpret_cast<uint32_t *>(w + W.k0), reinterpret_cast<uint32_t *>(w + W.v0),
+                                      reinterpret_cast<uint32_t *>(w + W.k1), reinterpret_cast<uint32_t *>(w + W.v1),
+                                      w + W.temp, s);
+    } catch (...) {  // the shared-memory table could not grow
+      return SNACK_ERR_CUDA;
+    }
+  }
+  if (e != cudaSuccess) return SNACK_ERR_CUDA;
+  const int b = access_bytes((uintptr_t)dtable | (uintptr_t)dout | (uintptr_t)(dtable_ld * es) |
                              (uintptr_t)(dout_ld * es) | (uintptr_t)((size_t)width * es));
   if (t == SNACK_F32)
     e = b == 16 ? launch_grad<float, 16>(g, s) : b == 8 ? launch_grad<float, 8>(g, s) : launch_grad<float, 4>(g, s);

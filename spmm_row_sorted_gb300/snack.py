@@ -13,7 +13,9 @@ autograd function over it.
 
 from __future__ import annotations
 
+import array
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -118,10 +120,9 @@ def load(path: Optional[str] = None):
         lib.snack_embed_grad_workspace_size.restype = st
         lib.snack_embed_grad.argtypes = [vp, st, i64, vp, i64, i64, i32, st, f32, ctypes.c_int, vp, i64, vp, sz, vp]
         lib.snack_embed_grad.restype = st
-        lib.snack_clip_workspace_size.argtypes = [i32, ctypes.POINTER(i64), ctypes.POINTER(st), ctypes.POINTER(sz)]
+        lib.snack_clip_workspace_size.argtypes = [i32, vp, vp, ctypes.POINTER(sz)]
         lib.snack_clip_workspace_size.restype = st
-        lib.snack_clip_grad_norm.argtypes = [i32, ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(i64),
-                                             ctypes.POINTER(st), f32, vp, vp, sz, vp]
+        lib.snack_clip_grad_norm.argtypes = [i32, vp, vp, vp, vp, f32, vp, vp, sz, vp]
         lib.snack_clip_grad_norm.restype = st
         lib.snack_xent_workspace_size.argtypes = [vp, i64, i32, vp, i64, i64, i32, st, ctypes.c_int, ctypes.POINTER(sz)]
         lib.snack_xent_workspace_size.restype = st
@@ -137,6 +138,17 @@ def load(path: Optional[str] = None):
 def _check(fn: str, status: int) -> None:
     if status != SNACK_OK:
         raise SnackError(fn, status, load().snack_status_string(status).decode())
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    """The cudaStream_t of `stream`, or of torch's current one, as an integer."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -301,66 +313,73 @@ def index_code(dt: torch.dtype) -> int:
 
 def snack_embed_fwd(ids, table, scale: float, out, stream=None) -> None:
     _check("snack_embed_fwd",
-           load().snack_embed_fwd(_ptr(ids), index_code(ids.dtype), ids.numel(), _ptr(table), table.stride(0),
-                                  table.shape[0], table.shape[1], dtype_code(table.dtype), scale, _ptr(out),
-                                  out.stride(0), _stream(stream)))
+           (_lib or load()).snack_embed_fwd(_addr(ids), index_code(ids.dtype), ids.numel(), _addr(table), table.stride(0),
+                                  table.shape[0], table.shape[1], dtype_code(table.dtype), scale, _addr(out),
+                                  out.stride(0), _raw_stream(stream)))
 
 
 def snack_embed_grad_workspace_size(n: int, vocab: int, width: int) -> int:
     b = ctypes.c_size_t(0)
     _check("snack_embed_grad_workspace_size",
-           load().snack_embed_grad_workspace_size(n, vocab, width, ctypes.byref(b)))
+           (_lib or load()).snack_embed_grad_workspace_size(n, vocab, width, ctypes.byref(b)))
     return b.value
 
 
 def snack_embed_grad(ids, dout, scale: float, accumulate: bool, dtable, ws, stream=None) -> None:
     _check("snack_embed_grad",
-           load().snack_embed_grad(_ptr(ids), index_code(ids.dtype), ids.numel(), _ptr(dout), dout.stride(0),
+           (_lib or load()).snack_embed_grad(_addr(ids), index_code(ids.dtype), ids.numel(), _addr(dout), dout.stride(0),
                                    dtable.shape[0], dtable.shape[1], dtype_code(dtable.dtype), scale,
-                                   1 if accumulate else 0, _ptr(dtable), dtable.stride(0), _ptr(ws), _nbytes(ws),
-                                   _stream(stream)))
+                                   1 if accumulate else 0, _addr(dtable), dtable.stride(0), _addr(ws), _nbytes(ws),
+                                   _raw_stream(stream)))
 
 
 def snack_clip_workspace_size(numel, types) -> int:
-    n = len(numel)
     b = ctypes.c_size_t(0)
     _check("snack_clip_workspace_size",
-           load().snack_clip_workspace_size(n, (ctypes.c_int64 * n)(*numel), (ctypes.c_int * n)(*types),
-                                            ctypes.byref(b)))
+           load().snack_clip_workspace_size(len(numel), _array("q", numel), _array("i", types), ctypes.byref(b)))
     return b.value
+
+
+def _array(code: str, values):
+    """A C array of `values` ("Q" addresses, "q" int64, "i" int) and its address, kept alive with it."""
+    a = array.array(code, values)
+    p = ctypes.c_void_p(a.buffer_info()[0] if values else None)
+    p.owner = a
+    return p
 
 
 def snack_clip_grad_norm(grads, outs, numel, types, max_norm: float, norm, ws, stream=None) -> None:
     """grads and outs: lists of device addresses (outs None: the norm alone); numel, types: lists of their sizes."""
-    n = len(grads)
+    if not len(grads) == len(numel) == len(types) or (outs is not None and len(outs) != len(grads)):
+        raise ValueError("one address, size and type per tensor")
     _check("snack_clip_grad_norm",
-           load().snack_clip_grad_norm(n, (ctypes.c_void_p * n)(*grads),
-                                       None if outs is None else (ctypes.c_void_p * n)(*outs),
-                                       (ctypes.c_int64 * n)(*numel), (ctypes.c_int * n)(*types), max_norm, _ptr(norm),
-                                       _ptr(ws), _nbytes(ws), _stream(stream)))
+           (_lib or load()).snack_clip_grad_norm(len(grads), _array("Q", grads),
+                                                 None if outs is None else _array("Q", outs), _array("q", numel),
+                                                 _array("i", types), max_norm, _addr(norm), _addr(ws), _nbytes(ws),
+                                                 _raw_stream(stream)))
 
 
 def snack_xent_workspace_size(x, w, grad: bool) -> int:
     b = ctypes.c_size_t(0)
     _check("snack_xent_workspace_size",
-           load().snack_xent_workspace_size(_ptr(x), x.stride(0), x.shape[0], _ptr(w), w.stride(0), w.shape[0],
+           (_lib or load()).snack_xent_workspace_size(_addr(x), x.stride(0), x.shape[0], _addr(w), w.stride(0), w.shape[0],
                                             w.shape[1], dtype_code(w.dtype), 1 if grad else 0, ctypes.byref(b)))
     return b.value
 
 
 def snack_xent_fwd(x, w, targets, reduction: int, loss, state, ws, stream=None) -> None:
     _check("snack_xent_fwd",
-           load().snack_xent_fwd(_ptr(x), x.stride(0), x.shape[0], _ptr(w), w.stride(0), w.shape[0], w.shape[1],
-                                 dtype_code(w.dtype), _ptr(targets), index_code(targets.dtype), reduction, _ptr(loss),
-                                 _ptr(state), _ptr(ws), _nbytes(ws), _stream(stream)))
+           (_lib or load()).snack_xent_fwd(_addr(x), x.stride(0), x.shape[0], _addr(w), w.stride(0), w.shape[0], w.shape[1],
+                                 dtype_code(w.dtype), _addr(targets), index_code(targets.dtype), reduction, _addr(loss),
+                                 _addr(state), _addr(ws), _nbytes(ws), _raw_stream(stream)))
 
 
 def snack_xent_bwd(x, w, targets, reduction: int, state, dloss, dx, dw, ws, stream=None) -> None:
     _check("snack_xent_bwd",
-           load().snack_xent_bwd(_ptr(x), x.stride(0), x.shape[0], _ptr(w), w.stride(0), w.shape[0], w.shape[1],
-                                 dtype_code(w.dtype), _ptr(targets), index_code(targets.dtype), reduction, _ptr(state),
-                                 _ptr(dloss), _ptr(dx), 0 if dx is None else dx.stride(0), _ptr(dw),
-                                 0 if dw is None else dw.stride(0), _ptr(ws), _nbytes(ws), _stream(stream)))
+           (_lib or load()).snack_xent_bwd(_addr(x), x.stride(0), x.shape[0], _addr(w), w.stride(0), w.shape[0], w.shape[1],
+                                 dtype_code(w.dtype), _addr(targets), index_code(targets.dtype), reduction, _addr(state),
+                                 _addr(dloss), _addr(dx), 0 if dx is None else dx.stride(0), _addr(dw),
+                                 0 if dw is None else dw.stride(0), _addr(ws), _nbytes(ws), _raw_stream(stream)))
 
 
 # ------------------------------------------------------------- layer owner
@@ -510,38 +529,34 @@ def sparse_linear(x: torch.Tensor, layer: SparseLinear) -> torch.Tensor:
 # that the kernels run on: torch's current one, or `stream`.
 
 
-class _Place:
-    """The device and the stream of a call: enters both where they are not the current ones."""
+class _On:
+    """The stream of a call, entered as torch's current one where it is not (and its device with it)."""
 
-    def __init__(self, t: torch.Tensor, stream):
-        if not t.is_cuda:
-            raise ValueError("expected CUDA tensors")
-        self.device = t.device
+    def __init__(self, device: torch.device, stream):
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=t.device)
-        if stream is not None and stream.device != t.device:
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        if stream is not None and stream.device != device:
             raise ValueError("the stream belongs to another device than the tensors")
-        self.stream = stream
-        self.outer = None
+        self.outer = torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
-        if self.stream is not None:
-            self.outer = torch.cuda.stream(self.stream)
-        elif self.device.index != torch.cuda.current_device():
-            self.outer = torch.cuda.device(self.device)
-        if self.outer is not None:
-            self.outer.__enter__()
-        return self
+        self.outer.__enter__()
 
     def __exit__(self, *exc):
-        if self.outer is not None:
-            self.outer.__exit__(*exc)
+        self.outer.__exit__(*exc)
 
 
-def _same_device(*tensors) -> None:
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
+def _elsewhere(t: torch.Tensor, stream) -> bool:
+    """Whether a call on t has to enter a stream or a device first; refuses what is not on a GPU."""
+    if not t.is_cuda:
+        raise ValueError("expected CUDA tensors")
+    return stream is not None or t.get_device() != torch.cuda.current_device()
+
+
+def _same_device(first: torch.Tensor, *others) -> None:
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
             raise ValueError("all tensors must be on one CUDA device")
 
 
@@ -549,7 +564,8 @@ def _rows(t: torch.Tensor) -> torch.Tensor:
     """t as a matrix whose rows are contiguous (their distance may exceed their length)."""
     if t.dim() != 2:
         raise ValueError("expected a matrix")
-    if (t.stride(1) == 1 or t.shape[1] == 1) and t.stride(0) >= t.shape[1]:
+    step, one = t.stride()
+    if (one == 1 or t.shape[1] == 1) and step >= t.shape[1]:
         return t
     return t.contiguous()
 
@@ -565,17 +581,43 @@ def _workspace(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
+# Workspace sizes are functions of the shapes alone (and, for xent, of the rows' alignment).
+_embed_grad_ws = functools.lru_cache(maxsize=256)(snack_embed_grad_workspace_size)
+
+
+@functools.lru_cache(maxsize=256)
+def _clip_ws(n: int) -> int:
+    return snack_clip_workspace_size([0] * n, [SNACK_F32] * n)
+
+
+@functools.lru_cache(maxsize=256)
+def _xent_ws(device: int, x_bits: int, x_ld: int, n: int, w_bits: int, w_ld: int, vocab: int, width: int, t: int,
+             grad: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check("snack_xent_workspace_size",
+           load().snack_xent_workspace_size(x_bits, x_ld, n, w_bits, w_ld, vocab, width, t, grad, ctypes.byref(b)))
+    return b.value
+
+
+def _xent_workspace(x, w, grad: int) -> torch.Tensor:
+    # of the addresses, their place within 256 bytes
+    nbytes = _xent_ws(x.get_device(), x.data_ptr() % 256, x.stride(0), x.shape[0], w.data_ptr() % 256, w.stride(0),
+                      w.shape[0], w.shape[1], dtype_code(w.dtype), grad)
+    return _workspace(nbytes, x.device)
+
+
 def embed(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out: Optional[torch.Tensor] = None,
           stream=None) -> torch.Tensor:
     """scale * table[ids]; zeros for an id outside the table.  ids of any shape; the result has that shape plus the width."""
+    if _elsewhere(table, stream):
+        with _On(table.device, stream):
+            return embed(ids, table, scale, out)
     _same_device(table, ids, out)
-    with _Place(table, stream):
-        tab, flat = _rows(table), ids.contiguous()
-        n, width = flat.numel(), tab.shape[1]
-        y = torch.empty((n, width), dtype=tab.dtype, device=tab.device) if out is None \
-            else _out_rows(out, n, width, tab.dtype)
-        snack_embed_fwd(flat, tab, float(scale), y)
-        return y.view(*ids.shape, width) if out is None and ids.dim() != 1 else y
+    tab, flat = _rows(table), ids.contiguous()
+    n, width = flat.numel(), tab.shape[1]
+    y = tab.new_empty((n, width)) if out is None else _out_rows(out, n, width, tab.dtype)
+    snack_embed_fwd(flat, tab, float(scale), y)
+    return y.view(*ids.shape, width) if out is None and ids.dim() != 1 else y
 
 
 def embed_grad(ids: torch.Tensor, dout: torch.Tensor, vocab: int, scale: float = 1.0,
@@ -583,17 +625,18 @@ def embed_grad(ids: torch.Tensor, dout: torch.Tensor, vocab: int, scale: float =
     """The gradient of embed's table, [vocab, width] in dout's type.  With accumulate the sums are added to `out`."""
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
+    if _elsewhere(dout, stream):
+        with _On(dout.device, stream):
+            return embed_grad(ids, dout, vocab, scale, out, accumulate)
     _same_device(dout, ids, out)
-    with _Place(dout, stream):
-        width = dout.shape[-1]
-        d, flat = _rows(dout if dout.dim() == 2 else dout.reshape(-1, width)), ids.contiguous()
-        if d.shape[0] != flat.numel():
-            raise ValueError("dout needs one row per id")
-        g = torch.empty((vocab, width), dtype=d.dtype, device=d.device) if out is None \
-            else _out_rows(out, vocab, width, d.dtype)
-        ws = _workspace(snack_embed_grad_workspace_size(flat.numel(), vocab, width), d.device)
-        snack_embed_grad(flat, d, float(scale), accumulate, g, ws)
-        return g
+    width = dout.shape[-1]
+    d, flat = _rows(dout if dout.dim() == 2 else dout.reshape(-1, width)), ids.contiguous()
+    n = flat.numel()
+    if d.shape[0] != n:
+        raise ValueError("dout needs one row per id")
+    g = d.new_empty((vocab, width)) if out is None else _out_rows(out, vocab, width, d.dtype)
+    snack_embed_grad(flat, d, float(scale), accumulate, g, _workspace(_embed_grad_ws(n, vocab, width), d.device))
+    return g
 
 
 class _EmbedFn(torch.autograd.Function):
@@ -624,22 +667,28 @@ def clip_grad_norm(grads, max_norm: float, out=None, stream=None) -> torch.Tenso
     grads = list(grads)
     if not grads:
         raise ValueError("no gradients")
-    outs = grads if out is None else list(out)
-    if len(outs) != len(grads):
-        raise ValueError("out needs one tensor per gradient")
-    dev = grads[0].device
-    for g, o in zip(grads, outs):
-        if g.device != dev or not g.is_contiguous():
-            raise ValueError("gradients must be contiguous tensors on one CUDA device")
-        if o is not g and (o.device != dev or o.dtype != g.dtype or o.numel() != g.numel() or not o.is_contiguous()):
-            raise ValueError("out must hold contiguous tensors of the gradients' types and sizes")
-    with _Place(grads[0], stream):
-        numel, types = [g.numel() for g in grads], [dtype_code(g.dtype) for g in grads]
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-        ws = _workspace(snack_clip_workspace_size(numel, types), dev)
-        snack_clip_grad_norm([g.data_ptr() for g in grads], [o.data_ptr() for o in outs], numel, types,
-                             float(max_norm), norm, ws)
-        return norm
+    first = grads[0]
+    if _elsewhere(first, stream):
+        with _On(first.device, stream):
+            return clip_grad_norm(grads, max_norm, out)
+    # one call over all tensors per property: a model has hundreds of gradients
+    T = torch.Tensor
+    numel, dtypes = list(map(T.numel, grads)), [g.dtype for g in grads]
+    addr = list(map(T.data_ptr, grads))
+    if not all(map(T.is_contiguous, grads)) or set(map(T.get_device, grads)) != {first.get_device()}:
+        raise ValueError("gradients must be contiguous tensors on one CUDA device")
+    to = addr
+    if out is not None:
+        outs = list(out)
+        if list(map(T.numel, outs)) != numel or [o.dtype for o in outs] != dtypes \
+                or not all(map(T.is_contiguous, outs)) or set(map(T.get_device, outs)) != {first.get_device()}:
+            raise ValueError("out must hold contiguous tensors of the gradients' types and sizes, on their device")
+        to = list(map(T.data_ptr, outs))
+    norm = torch.empty((), dtype=torch.float32, device=first.device)
+    types = [dtype_code(d) for d in dtypes] if len(grads) < 8 else list(map({d: dtype_code(d) for d in set(dtypes)}.get, dtypes))
+    ws = _workspace(_clip_ws(len(grads)), first.device)
+    snack_clip_grad_norm(addr, to, numel, types, float(max_norm), norm, ws)
+    return norm
 
 
 def _xent_args(x, w, targets, reduction):
@@ -658,38 +707,40 @@ def xent(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, reduction: str
     A target outside the vocabulary (such as -100) is not trained on.  state
     (float32, n + 1) is what xent_grad needs beside the same arguments.
     """
+    if _elsewhere(x, stream):
+        with _On(x.device, stream):
+            return xent(x, w, targets, reduction)
     _same_device(x, w, targets)
-    with _Place(x, stream):
-        x, w, targets, red = _xent_args(x, w, targets, reduction)
-        n = x.shape[0]
-        loss = torch.empty((n,) if reduction == "none" else (), dtype=torch.float32, device=x.device)
-        state = torch.empty(n + 1, dtype=torch.float32, device=x.device)
-        ws = _workspace(snack_xent_workspace_size(x, w, False), x.device)
-        if n or reduction != "none":
-            snack_xent_fwd(x, w, targets, red, loss, state, ws)
-        return loss, state
+    x, w, targets, red = _xent_args(x, w, targets, reduction)
+    n = x.shape[0]
+    loss = torch.empty((n,) if reduction == "none" else (), dtype=torch.float32, device=x.device)
+    state = torch.empty(n + 1, dtype=torch.float32, device=x.device)
+    if n or reduction != "none":
+        snack_xent_fwd(x, w, targets, red, loss, state, _xent_workspace(x, w, 0))
+    return loss, state
 
 
 def xent_grad(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, state: torch.Tensor,
               dloss: Optional[torch.Tensor] = None, reduction: str = "mean", want_dx: bool = True,
               want_dw: bool = True, stream=None):
     """(dx, dw) of xent for an upstream gradient dloss (1 when None; one value per row for "none")."""
+    if _elsewhere(x, stream):
+        with _On(x.device, stream):
+            return xent_grad(x, w, targets, state, dloss, reduction, want_dx, want_dw)
     _same_device(x, w, targets, state, dloss)
-    with _Place(x, stream):
-        x, w, targets, red = _xent_args(x, w, targets, reduction)
-        if state.dtype != torch.float32 or state.numel() != x.shape[0] + 1 or not state.is_contiguous():
-            raise ValueError("state must be what xent returned for these arguments")
-        if dloss is not None:
-            if dloss.numel() != (x.shape[0] if reduction == "none" else 1):
-                raise ValueError("dloss has the loss's shape")
-            dloss = dloss.contiguous().float()
-        elif reduction == "none":
-            raise ValueError('reduction "none" needs dloss')
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_dx else None
-        dw = torch.empty(w.shape, dtype=w.dtype, device=w.device) if want_dw else None
-        ws = _workspace(snack_xent_workspace_size(x, w, True), x.device)
-        snack_xent_bwd(x, w, targets, red, state, dloss, dx, dw, ws)
-        return dx, dw
+    x, w, targets, red = _xent_args(x, w, targets, reduction)
+    if state.dtype != torch.float32 or state.numel() != x.shape[0] + 1 or not state.is_contiguous():
+        raise ValueError("state must be what xent returned for these arguments")
+    if dloss is not None:
+        if dloss.numel() != (x.shape[0] if reduction == "none" else 1):
+            raise ValueError("dloss has the loss's shape")
+        dloss = dloss.contiguous().float()
+    elif reduction == "none":
+        raise ValueError('reduction "none" needs dloss')
+    dx = x.new_empty(x.shape) if want_dx else None
+    dw = w.new_empty(w.shape) if want_dw else None
+    snack_xent_bwd(x, w, targets, red, state, dloss, dx, dw, _xent_workspace(x, w, 1))
+    return dx, dw
 
 
 class _XentFn(torch.autograd.Function):
