@@ -55,6 +55,13 @@ __device__ __forceinline__ void add_square(Sum3 &s, float v) {
   s.high = fmaf(b, b, s.high);
 }
 
+// A load that is issued where it stands: the batches below keep several in flight.
+__device__ __forceinline__ uint4 load16(const uint4 *p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 template <int kMost>
 __device__ __forceinline__ int find_tensor(const ClipTable<kMost> &t, uint32_t piece) {
   int lo = 0, hi = t.count;  // first[lo] <= piece < first[hi]
@@ -81,7 +88,7 @@ __device__ __forceinline__ void sum_piece(const T *__restrict__ p, int64_t m, Su
   for (; i + 3 * kThreads < vecs; i += 4 * kThreads) {
     V a[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) a[u].raw = __ldg(v + i + u * kThreads);
+    for (int u = 0; u < 4; ++u) a[u].raw = load16(v + i + u * kThreads);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
@@ -199,7 +206,7 @@ __device__ __forceinline__ void scale_piece(const T *p, T *o, int64_t m, float f
     for (; i + (kU - 1) * kThreads < vecs; i += kU * kThreads) {
       V a[kU];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) a[u].raw = __ldcs(v + i + u * kThreads);
+      for (int u = 0; u < kU; ++u) a[u].raw = load16(v + i + u * kThreads);
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
 #pragma unroll
@@ -250,8 +257,8 @@ __device__ __forceinline__ void scale_piece(const T *p, T *o, int64_t m, float f
       uint4 x[kU], y[kU];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        x[u] = __ldg(v + i + u * kThreads);
-        y[u] = __ldg(v + i + u * kThreads + 1);
+        x[u] = load16(v + i + u * kThreads);
+        y[u] = load16(v + i + u * kThreads + 1);
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u) __stcs(w + i + u * kThreads, join(x[u], y[u]));

@@ -90,21 +90,25 @@ __device__ __forceinline__ void zero_rows(const ZeroFill &z, int64_t block) {
 }
 
 // Place of token i among all: the number of (id, position) pairs before its
-// own.  Lane l of every warp holds token 32 b + l; the eight warps count over
+// own.  Lane l of every warp holds token 32 own + l; the eight warps count over
 // interleaved groups of 32 tokens, whose ids they read from shared memory
-// (every lane the same word).  The blocks after the first `rank_blocks` clear
-// the table meanwhile: the counting is arithmetic, the clearing stores.
+// (every lane the same word).  Every other block clears rows of the table
+// meanwhile: the counting is arithmetic, the clearing stores.
 __global__ void __launch_bounds__(kRankThreads) k_rank(TokenSrc ids, int n, uint32_t *__restrict__ keys,
                                                        uint32_t *__restrict__ pos, int rank_blocks, ZeroFill zero) {
   pdl_wait();
-  if ((int)blockIdx.x >= rank_blocks) {
-    zero_rows(zero, (int64_t)blockIdx.x - rank_blocks);
+  // the two kinds of block alternate while both last
+  const int zero_blocks = (int)gridDim.x - rank_blocks, both = 2 * min(rank_blocks, zero_blocks);
+  const int b = (int)blockIdx.x;
+  const bool counts = b < both ? (b & 1) == 0 : rank_blocks > zero_blocks;
+  const int own = b < both ? b >> 1 : b - both / 2;
+  if (!counts) {
+    zero_rows(zero, own);
     return;
   }
   __shared__ __align__(16) uint32_t s_ids[kRankTile];
   __shared__ int cnt[kRankThreads / 32][kRankRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int own = blockIdx.x;
   const int i = own * 32 + lane;
   const uint32_t mine = i < n ? ids.key(i) : 0u;
   int c = 0;
@@ -291,50 +295,109 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_embed_sum(const EmbedGrad g
 }
 
 // A run that crosses chunk borders: the chunk it begins in adds the partial
-// sums of the chunks it covers, in order.
+// sums of the chunks it covers, in order.  A warp does so for a run of up to
+// kJoinShort chunks; for a longer one the block's warps take an equal stretch
+// of it each, and their sums are added in the stretches' order.
+constexpr int kJoinShort = 8;
+
 template <typename T, int B>
-__global__ void __launch_bounds__(kGradWarps * 32) k_embed_join(const EmbedGrad g) {
-  pdl_wait();
-  typedef Pack<T, B> P;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t gw = (int64_t)blockIdx.x * kGradWarps + warp;
-  const int64_t c = gw / g.n_seg;
-  if (c + 1 >= g.n_chunks) return;
-  const int64_t j0 = c * g.chunk, j1 = j0 + g.chunk;
-  const uint32_t cur = __ldg(g.keys + j1 - 1);
-  if (cur >= g.vocab || __ldg(g.keys + j1) != cur) return;
-  if (__ldg(g.keys + j0) == cur && j0 > 0 && __ldg(g.keys + j0 - 1) == cur) return;  // it began earlier
-  const int64_t end = j1 + lower_bound(g.keys + j1, g.n - j1, cur + 1u);
-  const int64_t last = (end - 1) / g.chunk;  // the chunk it ends in
-  const int seg = (int)(gw - c * g.n_seg);
-  const int acc_n = g.width / P::kN;
-  const int a0 = seg * (32 * kGradVecs) + lane;
-  float acc[kGradVecs][P::kN];
-#pragma unroll
-  for (int u = 0; u < kGradVecs; ++u)
-#pragma unroll
-    for (int i = 0; i < P::kN; ++i)
-      acc[u][i] = a0 + 32 * u < acc_n ? g.part[(c * 2 + 1) * g.part_ld + (int64_t)i * acc_n + a0 + 32 * u] : 0.f;
-  for (int64_t q0 = c + 1; q0 <= last; q0 += kJoinBatch) {  // loads of several chunks in flight, added in order
-    float v[kJoinBatch][kGradVecs][P::kN];
+__device__ __forceinline__ void add_parts(const EmbedGrad &g, int64_t q0, int64_t q1, int a0, int acc_n,
+                                          float (&acc)[kGradVecs][Pack<T, B>::kN]) {
+  constexpr int kN = Pack<T, B>::kN;
+  for (; q0 < q1; q0 += kJoinBatch) {  // loads of several chunks in flight
+    float v[kJoinBatch][kGradVecs][kN];
 #pragma unroll
     for (int e = 0; e < kJoinBatch; ++e) {
       const float *p = g.part + (q0 + e) * 2 * g.part_ld;
 #pragma unroll
       for (int u = 0; u < kGradVecs; ++u)
 #pragma unroll
-        for (int i = 0; i < P::kN; ++i)
-          v[e][u][i] = q0 + e <= last && a0 + 32 * u < acc_n ? __ldcg(p + (int64_t)i * acc_n + a0 + 32 * u) : 0.f;
+        for (int i = 0; i < kN; ++i)
+          v[e][u][i] = q0 + e < q1 && a0 + 32 * u < acc_n ? __ldcg(p + (int64_t)i * acc_n + a0 + 32 * u) : 0.f;
     }
 #pragma unroll
     for (int e = 0; e < kJoinBatch; ++e)
 #pragma unroll
       for (int u = 0; u < kGradVecs; ++u)
 #pragma unroll
-        for (int i = 0; i < P::kN; ++i)
-          if (q0 + e <= last) acc[u][i] += v[e][u][i];
+        for (int i = 0; i < kN; ++i)
+          if (q0 + e < q1) acc[u][i] += v[e][u][i];
   }
-  put_row<T, B>(g, cur, a0, acc_n, acc);
+}
+
+template <typename T, int B>
+__global__ void __launch_bounds__(kGradWarps * 32) k_embed_join(const EmbedGrad g) {
+  pdl_wait();
+  constexpr int kN = Pack<T, B>::kN;
+  __shared__ int64_t s_last[kGradWarps];  // a long run's last chunk, else -1
+  __shared__ uint32_t s_key[kGradWarps];
+  __shared__ float s_sum[kGradWarps][32 * kGradVecs * kN];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int acc_n = g.width / kN;
+  float acc[kGradVecs][kN];
+  auto clear = [&] {
+#pragma unroll
+    for (int u = 0; u < kGradVecs; ++u)
+#pragma unroll
+      for (int i = 0; i < kN; ++i) acc[u][i] = 0.f;
+  };
+  auto tail = [&](int64_t c, int a0) {  // what the chunk the run begins in left over
+#pragma unroll
+    for (int u = 0; u < kGradVecs; ++u)
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (a0 + 32 * u < acc_n) acc[u][i] = g.part[(c * 2 + 1) * g.part_ld + (int64_t)i * acc_n + a0 + 32 * u];
+  };
+  const int64_t w0 = (int64_t)blockIdx.x * kGradWarps;
+  int64_t last_long = -1;
+  {
+    const int64_t gw = w0 + warp, c = gw / g.n_seg;
+    if (c + 1 < g.n_chunks) {
+      const int64_t j0 = c * g.chunk, j1 = j0 + g.chunk;
+      const uint32_t cur = __ldg(g.keys + j1 - 1);
+      const bool crosses = cur < g.vocab && __ldg(g.keys + j1) == cur;
+      const bool earlier = j0 > 0 && __ldg(g.keys + j0) == cur && __ldg(g.keys + j0 - 1) == cur;
+      if (crosses && !earlier) {
+        const int64_t end = j1 + lower_bound(g.keys + j1, g.n - j1, cur + 1u);
+        const int64_t last = (end - 1) / g.chunk;  // the chunk it ends in
+        if (last - c > kJoinShort) {
+          last_long = last;
+          if (lane == 0) s_key[warp] = cur;
+        } else {
+          const int a0 = (int)(gw - c * g.n_seg) * (32 * kGradVecs) + lane;
+          clear();
+          tail(c, a0);
+          add_parts<T, B>(g, c + 1, last + 1, a0, acc_n, acc);
+          put_row<T, B>(g, cur, a0, acc_n, acc);
+        }
+      }
+    }
+  }
+  if (lane == 0) s_last[warp] = last_long;
+  if (!__syncthreads_or(last_long >= 0)) return;
+  for (int k = 0; k < kGradWarps; ++k) {
+    const int64_t last = s_last[k];
+    if (last < 0) continue;
+    const int64_t gw = w0 + k, c = gw / g.n_seg, n = last - c;
+    const int a0 = (int)(gw - c * g.n_seg) * (32 * kGradVecs) + lane;
+    clear();
+    if (warp == 0) tail(c, a0);
+    add_parts<T, B>(g, c + 1 + n * warp / kGradWarps, c + 1 + n * (warp + 1) / kGradWarps, a0, acc_n, acc);
+#pragma unroll
+    for (int u = 0; u < kGradVecs; ++u)
+#pragma unroll
+      for (int i = 0; i < kN; ++i) s_sum[warp][(u * kN + i) * 32 + lane] = acc[u][i];
+    __syncthreads();
+    if (warp == 0) {
+      for (int q = 1; q < kGradWarps; ++q)
+#pragma unroll
+        for (int u = 0; u < kGradVecs; ++u)
+#pragma unroll
+          for (int i = 0; i < kN; ++i) acc[u][i] += s_sum[q][(u * kN + i) * 32 + lane];
+      put_row<T, B>(g, s_key[k], a0, acc_n, acc);
+    }
+    __syncthreads();
+  }
 }
 
 // ------------------------------------------------------------ host side

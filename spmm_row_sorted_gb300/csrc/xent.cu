@@ -18,7 +18,7 @@
 //   dw     writes the piece's rows of dw.
 // Bound by the tensor cores; for a few tokens by reading w once.
 //
-// A pair of CTAs, one per SM, works through 256 x (64, 128 or 256) output tiles,
+// A pair of CTAs, one per SM, works through output tiles of 256 x up to 256,
 // 128 rows each: in each a warp loads its rows of A and its half of B by TMA
 // into a ring of stages; one thread of the pair issues the tcgen05.mma, which
 // read both halves of B (a third fewer bytes from L2 than a tile per CTA, which
@@ -212,11 +212,12 @@ constexpr int kEpiRegs = 232, kIssueRegs = 40;
 static_assert(256 * kEpiRegs + 128 * kIssueRegs <= kThreads * 168, "the split stays within the launch's registers");
 constexpr int kStageA = kMCta * kKb * 2;
 constexpr int kRing = 6 * (kStageA + kNMax / 2 * kKb * 2);  // bytes of the ring of stages
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 16;
 constexpr int kStaging = 4096;    // an epilogue warp's 32 rows x 128 bytes on their way out
-constexpr int kSmem = 1024 + kRing + kEpiWarps * kStaging + 256;
+constexpr int kBarBytes = 512;
+constexpr int kSmem = 1024 + kRing + kEpiWarps * kStaging + kBarBytes;
 static_assert(kSmem <= 232448, "shared memory of one CTA");
-static_assert(kStageA + 128 / 2 * kKb * 2 <= kRing / kMaxStages, "eight stages of the narrower tiles fit the ring");
+static_assert(kStageA <= kEpiWarps * kStaging, "a short A tile's reads end within the CTA's shared memory");
 
 enum { kStats = 0, kDlog = 1, kDx = 2, kDw = 3 };
 
@@ -230,7 +231,8 @@ struct Factor {
 
 struct GemmArgs {
   int32_t m, n;             // rows and columns of the product
-  int32_t nt;               // columns of a tile
+  int32_t nt;               // columns of a tile: a multiple of 32 (128 or 256 where B is MN-major)
+  int32_t a_rows;           // rows of A loaded per CTA: 128, or fewer where m has fewer (K-major A)
   int32_t m_tiles, n_tiles, n_split;
   int32_t k_blocks;         // of 64
   int32_t products;         // part products per element (1: bf16, 6: fp32)
@@ -284,7 +286,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
   constexpr bool kAmn = kMode == kDw, kBmn = kMode == kDx || kMode == kDw;
   const uint32_t rank = cta_rank();  // 0: the leader, which issues the pair's MMAs
   const int nb = P.nt / 2;           // rows of B in each CTA
-  const uint32_t stage_bytes = (uint32_t)(kStageA + nb * kKb * 2);
+  // With few rows a stage holds only those of A: the MMAs read 128 rows all the
+  // same, whatever lies in the others' place, and those rows are never used.
+  const uint32_t a_bytes = (uint32_t)(P.a_rows * kKb * 2);
+  const uint32_t stage_bytes = a_bytes + (uint32_t)(nb * kKb * 2);
   uint8_t *staging = smem + kRing;
   uint64_t *full = reinterpret_cast<uint64_t *>(staging + kEpiWarps * kStaging);
   uint64_t *empty = full + kMaxStages;
@@ -293,7 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
   uint64_t *drained = acc_free + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
   int *bad = reinterpret_cast<int *>(tmem_slot + 1);
-  static_assert(8 * (2 * kMaxStages + 5) + 16 <= 256, "barriers and flags fit their 256 bytes");
+  static_assert(8 * (2 * kMaxStages + 5) + 16 <= kBarBytes, "barriers and flags fit their bytes");
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -361,7 +366,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
               break;
             }
             if (one) {
-              uint8_t *a = smem + (uint32_t)s * stage_bytes, *b = a + kStageA;
+              uint8_t *a = smem + (uint32_t)s * stage_bytes, *b = a + a_bytes;
               const uint32_t bar = bar0 + 8u * s;
               if (rank == 0) mbar_expect_tx(&full[s], 2 * stage_bytes);
               if (kAmn) {
@@ -387,7 +392,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
       }
     } else if (warp == kEpiWarps + 1 && rank == 0) {  // ------------------- MMAs
       const uint32_t idesc = inst_desc(kM, P.nt, kAmn, kBmn);
-      const uint32_t a_lo = desc_lo(su32(smem), kAmn), b_lo = desc_lo(su32(smem) + kStageA, kBmn);
+      const uint32_t a_lo = desc_lo(su32(smem), kAmn), b_lo = desc_lo(su32(smem) + a_bytes, kBmn);
       constexpr uint32_t kA16 = kAmn ? 128 : 2, kB16 = kBmn ? 128 : 2;  // 16 of K in 16-byte units: 16 rows, or 32 bytes
       int n_acc = 0;
       for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
@@ -445,8 +450,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
       const int m0 = q.m0 + (int)rank * kMCta;  // this CTA's rows
       const int row = m0 + quarter * 32 + lane;
       const bool row_ok = row < P.m;
-      const int c_end = P.nt / 2;  // columns of this half
-      const int col0 = q.n0 + half * c_end;
+      const int width0 = (P.nt / 32 + 1) / 2 * 32;  // columns of the first half
+      const int c_end = half ? P.nt - width0 : width0;
+      const int col0 = q.n0 + half * width0;
       // the target's column of this tile's half, or below zero
       int tcol = -1;
       float lse = 0.f, g = 0.f;
@@ -454,7 +460,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
         if (row_ok) {
           const uint32_t id = P.targets.key(row);
           if (id < P.targets.vocab) {
-            tcol = (int)id - P.v0 - col0;
+            tcol = (int)id - P.v0 - col0;  // beyond c_end: another half's
             if (kMode == kDlog) {
               lse = P.lse[row];
               g = P.dloss ? P.dloss[row] : 1.f;
@@ -472,7 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
           break;
         }
         tc_fence_after();
-        const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * kNMax + half * c_end);
+        const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * kNMax + half * width0);
         const int chunks = c_end / 32;
         auto release = [&] {  // the accumulator has been read
           tc_fence_before();
@@ -522,7 +528,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
             for (int j = 0; j < 32; ++j)
               if (j >= valid) v[j] = -INFINITY;
           }
-          if (tcol >= c && tcol < c + 32) {
+          if (tcol >= c && tcol < c + 32 && tcol < P.n - col0) {
             float z = 0.f;
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -713,24 +719,20 @@ __global__ void __launch_bounds__(256) k_xent_join(const float2 *__restrict__ pa
   }
   red[q][r] = make_float2(mx, sum);
   __syncthreads();
-  if (threadIdx.x < 8 && row < m) {
-    mx = -INFINITY;
-    sum = 0.f;
-    for (int s = 0; s < 32; ++s) {
-      const float2 p = red[s][threadIdx.x];
-      const float nm = fmaxf(mx, p.x);
-      if (nm != -INFINITY) {
-        sum = sum * expf(mx - nm) + p.y * expf(p.x - nm);
-        mx = nm;
-      } else {
-        sum += p.y;
-      }
-    }
-    float lse = mx + logf(sum);
+  const int own = blockIdx.x * 8 + (threadIdx.x >> 5);  // a warp for each row
+  const float2 p = red[threadIdx.x & 31][threadIdx.x >> 5];
+  float nm = p.x;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, d));
+  sum = nm == -INFINITY ? p.y : p.y * expf(p.x - nm);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if ((threadIdx.x & 31) == 0 && own < m) {
+    float lse = nm + logf(sum);
     if (bad) lse = NAN;
-    state[row] = lse;
-    loss[row] = targets.key(row) < targets.vocab ? lse - zt[row] : 0.f;
-    if (row == 0) state[m] = 1.f;
+    state[own] = lse;
+    loss[own] = targets.key(own) < targets.vocab ? lse - zt[own] : 0.f;
+    if (own == 0) state[m] = 1.f;
   }
 }
 
@@ -773,7 +775,7 @@ __global__ void __launch_bounds__(1024) k_xent_total(const float *__restrict__ r
 // its rounding to bf16 leaves over, and what that leaves over.
 template <typename T>
 __global__ void __launch_bounds__(256) k_xent_pack(const T *__restrict__ in, int64_t ld, int64_t rows, int32_t width,
-                                                   int parts, bf16 *__restrict__ out, int32_t out_ld, int64_t plane) {
+                                                   int parts, bf16 *__restrict__ out, int32_t out_ld, int64_t plane, int vec) {
   pdl_wait();
   const int groups = out_ld / 8;
   const int64_t total = rows * groups;
@@ -781,8 +783,20 @@ __global__ void __launch_bounds__(256) k_xent_pack(const T *__restrict__ in, int
     const int64_t r = i / groups;
     const int c = (int)(i - r * groups) * 8;
     float v[8];
+    const T *at = in + r * ld + c;
+    if (vec && c + 8 <= width) {
+      constexpr int kB = 16 / (int)sizeof(T);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < width ? to_f32(in[r * ld + c + j]) : 0.f;
+      for (int h = 0; h < 8 / kB; ++h) {
+        Pack<T, 16> q;
+        q.raw = __ldg(reinterpret_cast<const uint4 *>(at) + h);
+#pragma unroll
+        for (int j = 0; j < kB; ++j) v[h * kB + j] = q.get(j);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = c + j < width ? to_f32(at[j]) : 0.f;
+    }
     for (int p = 0; p < parts; ++p) {
       Pack<bf16, 16> o;
 #pragma unroll
@@ -882,12 +896,20 @@ int sms_of() {
   return n < 2 ? 152 : n > 256 ? 256 : n;
 }
 
-// The widest tile that still gives every pair of SMs one; narrower tiles share a small
-// product among more SMs.
+// Columns of a tile of a product with a K-major B: the width whose last wave of
+// tiles wastes least, each tile counted as its columns and the fixed cost of 16
+// more; the widest of equals.
 int tile_cols(int64_t m_tiles, int64_t n, int sms) {
-  for (int nt = 256; nt > 64; nt /= 2)
-    if (m_tiles * ceil_div(n, nt) >= sms / 2) return nt;
-  return 64;
+  int best = 256;
+  int64_t best_cost = INT64_MAX;
+  for (int nt = 256; nt >= 64; nt -= 32) {
+    const int64_t cost = ceil_div(m_tiles * ceil_div(n, nt), sms / 2) * (nt + 16);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = nt;
+    }
+  }
+  return best;
 }
 
 // Equal pieces of the vocabulary, multiples of 256 rows, of at most `bytes` each.
@@ -975,19 +997,28 @@ XentWs xent_ws(const XentShape &s, bool grad) {
   return w;
 }
 
-bool rows_ready(const void *p, int64_t ld) { return ptr_aligned(p, 16) && ld % 8 == 0; }
+// Whether a bf16 matrix can be read as it lies.  TMA asks for 16-byte aligned
+// rows; off a 128-byte line every box row costs it one line more, and the
+// products run a fifth to a quarter slower (1999 x 50001 x 1000: gradient 499
+// against 402 us, forward 235 against 199 us), so large products lay it out
+// again first: the gradient reads an operand three times, the forward once.
+bool rows_ready(const void *p, int64_t ld, int32_t n, bool grad) {
+  if (!ptr_aligned(p, 16) || ld % 8 != 0) return false;
+  const bool on_lines = ptr_aligned(p, 128) && ld % 64 == 0;
+  return on_lines || n < (grad ? 1024 : 4096);
+}
 
 XentShape xent_shape(const void *x, int64_t x_ld, int32_t n, const void *wt, int64_t w_ld, int64_t vocab, int32_t width,
-                     snack_dtype t) {
+                     snack_dtype t, bool grad) {
   XentShape s;
   s.n = n;
   s.width = width;
   s.vocab = vocab;
   s.t = t;
   s.parts = t == SNACK_F32 ? 3 : 1;
-  s.pack_x = t == SNACK_F32 || !rows_ready(x, x_ld);
-  s.pack_w = t == SNACK_F32 || !rows_ready(wt, w_ld);
-  s.ld = (int32_t)align_up((size_t)width, 8);
+  s.pack_x = t == SNACK_F32 || !rows_ready(x, x_ld, n, grad);
+  s.pack_w = t == SNACK_F32 || !rows_ready(wt, w_ld, n, grad);
+  s.ld = (int32_t)align_up((size_t)width, 64);
   s.sms = sms_of();
   return s;
 }
@@ -1015,7 +1046,8 @@ cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtens
   g.m_tiles = (int32_t)ceil_div(g.m, kM);
   g.n_tiles = (int32_t)ceil_div(g.n, g.nt);
   g.unit = unit_of((int)ceil_div(g.k_blocks, g.n_split), kMode == kStats || g.products > 1);
-  g.stages = kRing / (kStageA + g.nt / 2 * kKb * 2);
+  g.a_rows = kMode == kDw || g.m >= kMCta ? kMCta : (int32_t)align_up((size_t)g.m, 8);
+  g.stages = kRing / ((g.a_rows + g.nt / 2) * kKb * 2);
   if (g.stages > kMaxStages) g.stages = kMaxStages;
   const int64_t tiles = (int64_t)g.m_tiles * g.n_tiles * g.n_split;
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
@@ -1028,11 +1060,12 @@ cudaError_t pack(const XentShape &s, const void *in, int64_t ld, int64_t rows, v
   const int64_t total = rows * (s.ld / 8);
   int64_t blocks = ceil_div(total, 256);
   if (blocks > (int64_t)s.sms * 32) blocks = (int64_t)s.sms * 32;
+  const int vec = ptr_aligned(in, 16) && (size_t)ld * dtype_size(s.t) % 16 == 0;
   if (s.t == SNACK_F32)
     return launch_pdl(k_xent_pack<float>, (unsigned)blocks, 256, 0, st, reinterpret_cast<const float *>(in), ld, rows,
-                      s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld);
+                      s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld, vec);
   return launch_pdl(k_xent_pack<bf16>, (unsigned)blocks, 256, 0, st, reinterpret_cast<const bf16 *>(in), ld, rows,
-                    s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld);
+                    s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld, vec);
 }
 
 // x, or a piece of w from row v0 on, as the products read it
@@ -1096,7 +1129,7 @@ snack_status snack_xent_workspace_size(const void *x, int64_t x_ld, int32_t n, c
   if (!bytes) return SNACK_ERR_INVALID_ARG;
   const snack_status st = xent_check(x, x_ld, n, w, w_ld, vocab, width, t);
   if (st != SNACK_OK) return st;
-  *bytes = n == 0 ? 0 : xent_ws(xent_shape(x, x_ld, n, w, w_ld, vocab, width, t), grad != 0).total;
+  *bytes = n == 0 ? 0 : xent_ws(xent_shape(x, x_ld, n, w, w_ld, vocab, width, t, grad != 0), grad != 0).total;
   return SNACK_OK;
 }
 
@@ -1117,14 +1150,15 @@ snack_status snack_xent_fwd(const void *x, int64_t x_ld, int32_t n, const void *
       XENT_CUDA(launch_pdl(k_xent_total, 1, 1024, 0, s, (const float *)nullptr, 0, tg, reduction == SNACK_MEAN, loss, state));
     return SNACK_OK;
   }
-  const XentShape S = xent_shape(x, x_ld, n, w, w_ld, vocab, width, t);
+  const XentShape S = xent_shape(x, x_ld, n, w, w_ld, vocab, width, t, false);
   const XentWs W = xent_ws(S, false);
   if (ws_bytes < W.total) return SNACK_ERR_WORKSPACE;
   uint8_t *b = reinterpret_cast<uint8_t *>(ws);
+  const uint32_t a_rows = n >= kMCta ? kMCta : (uint32_t)align_up((size_t)n, 8);
   Operand ox, ow;
   XENT_CUDA(operand(S, S.pack_x, x, x_ld, 0, n, b + W.xp, &ox, s));
   CUtensorMap mx, mw;
-  if (!load_map(&mx, ox, false, kMCta)) return SNACK_ERR_CUDA;
+  if (!load_map(&mx, ox, false, a_rows)) return SNACK_ERR_CUDA;
   GemmArgs g = gemm_args(S, b, W, 1);
   g.m = n;
   g.nt = W.nt;
@@ -1174,16 +1208,17 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
   if (spans_overlap(dx, ndx, x, nx) || spans_overlap(dx, ndx, w, nw) || spans_overlap(dw, ndw, x, nx) ||
       spans_overlap(dw, ndw, w, nw) || spans_overlap(dx, ndx, dw, ndw))
     return SNACK_ERR_INVALID_ARG;
-  const XentShape S = xent_shape(x, x_ld, n, w, w_ld, vocab, width, t);
+  const XentShape S = xent_shape(x, x_ld, n, w, w_ld, vocab, width, t, true);
   const XentWs W = xent_ws(S, true);
   if (ws_bytes < W.total) return SNACK_ERR_WORKSPACE;
   if (!dx && !dw) return SNACK_OK;
   uint8_t *b = reinterpret_cast<uint8_t *>(ws);
   const bool wide = t == SNACK_F32;
+  const uint32_t a_rows = n >= kMCta ? kMCta : (uint32_t)align_up((size_t)n, 8);
   Operand ox, ow;
   XENT_CUDA(operand(S, S.pack_x, x, x_ld, 0, n, b + W.xp, &ox, s));
   CUtensorMap mx, mw, mxt, mwt, mdz, mdzt, mdz_out, macc, mdw;
-  if (!load_map(&mx, ox, false, kMCta) || !load_map(&mxt, ox, true, 0)) return SNACK_ERR_CUDA;
+  if (!load_map(&mx, ox, false, a_rows) || !load_map(&mxt, ox, true, 0)) return SNACK_ERR_CUDA;
   if (!make_map(&macc, b + W.acc, true, (uint64_t)width, (uint64_t)n, (uint64_t)W.acc_ld, (uint64_t)W.split,
                 (uint64_t)n * (uint64_t)W.acc_ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B))
     return SNACK_ERR_CUDA;
@@ -1194,7 +1229,7 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
     XENT_CUDA(operand(S, S.pack_w, w, w_ld, v0, rows, b + W.wp, &ow, s));
     const Operand dz = {b + W.dz, n, W.dz_ld, (int64_t)n * W.dz_ld, (int32_t)rows, S.parts};
     const int nt = tile_cols(ceil_div(n, kM), rows, S.sms);
-    if (!load_map(&mw, ow, false, (uint32_t)nt / 2) || !load_map(&mwt, ow, true, 0) || !load_map(&mdz, dz, false, kMCta) ||
+    if (!load_map(&mw, ow, false, (uint32_t)nt / 2) || !load_map(&mwt, ow, true, 0) || !load_map(&mdz, dz, false, a_rows) ||
         !load_map(&mdzt, dz, true, 0) ||
         !make_map(&mdz_out, dz.p, false, (uint64_t)rows, (uint64_t)n, (uint64_t)W.dz_ld, (uint64_t)S.parts,
                   (uint64_t)dz.plane, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
