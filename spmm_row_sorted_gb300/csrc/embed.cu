@@ -10,13 +10,14 @@
 // The gradient sorts the (id, position) pairs, stably, so that each row's
 // terms lie together in the order of their positions: one sum per row in that
 // order, in fp32, with no atomics on values, so results repeat bit for bit.
-// One kernel finds each token's place by counting the pairs before it (n^2
-// comparisons, no passes) while its other blocks clear the table's gradient;
-// where that would take longer than the clearing, an LSD radix sort does.  The
-// sorted list is cut into chunks of equal length, one warp per chunk and column
-// segment, so that a frequent token's many rows are shared by many warps: a run
-// that crosses a chunk's border leaves fp32 partial sums, which a second kernel
-// adds in order.
+// The order comes from one kernel up to 65,536 tokens: by counting the pairs
+// before each (n^2 comparisons, no passes), or a radix sort by one cluster of
+// blocks; above that from a device-wide radix sort.  The sorted list is cut into
+// chunks of equal length, one warp per chunk and column segment, so that a
+// frequent token's many rows are shared by many warps: a run that crosses a
+// chunk's border leaves fp32 partial sums, which a second kernel adds in order.
+// The blocks after those of the sums clear the rows that no token names, found
+// by a search in the sorted list.
 #include <stdint.h>
 
 #include "internal.hpp"
@@ -59,81 +60,41 @@ __global__ void __launch_bounds__(256) k_embed_fwd(TokenSrc ids, int64_t n, cons
 
 // ------------------------------------------------------------ sorted order
 
+constexpr int kRankMax = 4096;
 constexpr int kRankRows = 32;  // tokens per block
 constexpr int kRankThreads = 256;
-constexpr int kRankTile = 4096;  // ids in shared memory at a time
-
-// The rows of a table to clear: accesses of 16 bytes where its rows allow it.
-struct ZeroFill {
-  uint8_t *base;
-  int64_t row_bytes, ld_bytes, rows;  // rows 0: nothing to clear
-  int wide;                           // 16-byte accesses, else 2-byte ones
-};
-
-// Row groups of kZeroRows per block: a warp clears one row after the other.
-constexpr int kZeroRows = 64;
-__device__ __forceinline__ void zero_rows(const ZeroFill &z, int64_t block) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t r1 = min(z.rows, (block + 1) * kZeroRows);
-  for (int64_t r = block * kZeroRows + warp; r < r1; r += kRankThreads / 32) {
-    uint8_t *row = z.base + r * z.ld_bytes;
-    if (z.wide) {
-      uint4 *o = reinterpret_cast<uint4 *>(row);
-      const int64_t n = z.row_bytes / 16;
-      for (int64_t i = lane; i < n; i += 32) __stcs(o + i, make_uint4(0, 0, 0, 0));
-    } else {
-      uint16_t *o = reinterpret_cast<uint16_t *>(row);
-      const int64_t n = z.row_bytes / 2;
-      for (int64_t i = lane; i < n; i += 32) o[i] = 0;
-    }
-  }
-}
 
 // Place of token i among all: the number of (id, position) pairs before its
-// own.  Lane l of every warp holds token 32 own + l; the eight warps count over
-// interleaved groups of 32 tokens, whose ids they read from shared memory
-// (every lane the same word).  Every other block clears rows of the table
-// meanwhile: the counting is arithmetic, the clearing stores.
+// own.  Lane l of every warp holds token 32 blockIdx.x + l; the eight warps
+// count over interleaved groups of 32 tokens, whose ids they read from shared
+// memory (every lane the same word).
 __global__ void __launch_bounds__(kRankThreads) k_rank(TokenSrc ids, int n, uint32_t *__restrict__ keys,
-                                                       uint32_t *__restrict__ pos, int rank_blocks, ZeroFill zero) {
+                                                       uint32_t *__restrict__ pos) {
   pdl_wait();
-  // the two kinds of block alternate while both last
-  const int zero_blocks = (int)gridDim.x - rank_blocks, both = 2 * min(rank_blocks, zero_blocks);
-  const int b = (int)blockIdx.x;
-  const bool counts = b < both ? (b & 1) == 0 : rank_blocks > zero_blocks;
-  const int own = b < both ? b >> 1 : b - both / 2;
-  if (!counts) {
-    zero_rows(zero, own);
-    return;
-  }
-  __shared__ __align__(16) uint32_t s_ids[kRankTile];
+  __shared__ __align__(16) uint32_t s_ids[kRankMax];
   __shared__ int cnt[kRankThreads / 32][kRankRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = (n + 31) / 32;
+  for (int i = threadIdx.x; i < groups * 32; i += kRankThreads) s_ids[i] = i < n ? ids.key(i) : 0xFFFFFFFFu;
+  __syncthreads();
+  const int own = blockIdx.x;
   const int i = own * 32 + lane;
-  const uint32_t mine = i < n ? ids.key(i) : 0u;
+  const uint32_t mine = s_ids[i];
   int c = 0;
-  for (int t0 = 0; t0 < n; t0 += kRankTile) {
-    const int m = min(kRankTile, n - t0);
-    const int groups = (m + 31) / 32;
-    __syncthreads();
-    for (int k = threadIdx.x; k < groups * 32; k += kRankThreads) s_ids[k] = k < m ? ids.key(t0 + k) : 0xFFFFFFFFu;
-    __syncthreads();
-    for (int g = warp; g < groups; g += kRankThreads / 32) {
-      const int at = t0 / 32 + g;
-      if (at == own) {
+  for (int g = warp; g < groups; g += kRankThreads / 32) {
+    if (g == own) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const uint32_t k = s_ids[g * 32 + j];
-          c += (k < mine || (k == mine && j < lane)) ? 1 : 0;
-        }
-      } else {
-        const uint4 *q = reinterpret_cast<const uint4 *>(s_ids + g * 32);
-        const uint32_t lim = at < own ? mine + 1u : mine;  // an earlier token of the same id comes first
+      for (int j = 0; j < 32; ++j) {
+        const uint32_t k = s_ids[g * 32 + j];
+        c += (k < mine || (k == mine && j < lane)) ? 1 : 0;
+      }
+    } else {
+      const uint4 *q = reinterpret_cast<const uint4 *>(s_ids + g * 32);
+      const uint32_t lim = g < own ? mine + 1u : mine;  // an earlier token of the same id comes first
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4 k = q[j];
-          c += (k.x < lim) + (k.y < lim) + (k.z < lim) + (k.w < lim);
-        }
+      for (int j = 0; j < 8; ++j) {
+        const uint4 k = q[j];
+        c += (k.x < lim) + (k.y < lim) + (k.z < lim) + (k.w < lim);
       }
     }
   }
@@ -148,10 +109,124 @@ __global__ void __launch_bounds__(kRankThreads) k_rank(TokenSrc ids, int n, uint
   }
 }
 
-// the clearing alone, beside the radix sort's kernels (or with no tokens at all)
-__global__ void __launch_bounds__(kRankThreads) k_zero(ZeroFill zero) {
+// A stable LSD radix sort of up to 65,536 pairs by one cluster, in one launch.
+// Each of its eight blocks holds `tile` pairs in shared memory; a pass of up to
+// nine bits ranks them (a warp's equal digits by ballots, its counts before them in
+// its own histogram), the blocks read each other's digit totals, and every pair
+// goes straight to its place in the shared memory of the block that holds it.
+constexpr int kSortBlocks = 8;
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortRounds = 8;  // pairs per thread
+constexpr int kSortMost = kSortBlocks * kSortThreads * kSortRounds;
+constexpr size_t kSortTile = (size_t)kSortThreads * kSortRounds;
+// two buffers of pairs, and the warps' histograms
+constexpr int kSortBins = 512;  // digits of up to nine bits: two passes up to 2^18 ids
+constexpr size_t kSortSmem = 2 * kSortTile * 8 + (size_t)kSortWarps * kSortBins * 4;
+
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t block) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(block));
+  return r;
+}
+
+__global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThreads, 1)
+    k_sort(TokenSrc ids, int n, int tile, int passes, int digit_bits, uint32_t *__restrict__ keys, uint32_t *__restrict__ pos) {
   pdl_wait();
-  zero_rows(zero, blockIdx.x);
+  extern __shared__ __align__(16) uint8_t sort_smem[];
+  uint2 *buf = reinterpret_cast<uint2 *>(sort_smem);  // [2][tile]
+  uint32_t(*hist)[kSortBins] = reinterpret_cast<uint32_t(*)[kSortBins]>(sort_smem + 2 * kSortTile * 8);
+  __shared__ uint32_t totals[kSortBins];  // this block's pairs by digit
+  __shared__ uint32_t base[kSortBins];    // where they start in the whole order
+  __shared__ uint32_t warp_sum[kSortBins / 32];
+  const uint32_t bins = 1u << digit_bits, mask = bins - 1u;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t block = blockIdx.x;
+  const int first = (int)block * tile, mine = max(0, min(tile, n - first));
+  const int strip = tile / kSortWarps;  // pairs of a warp, in rounds of 32
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i = threadIdx.x; i < mine; i += kSortThreads) buf[i] = make_uint2(ids.key(first + i), (uint32_t)(first + i));
+  for (int p = 0; p < passes; ++p) {
+    uint2 *in = buf + (p & 1) * tile, *out = buf + ((p & 1) ^ 1) * tile;
+    for (int i = threadIdx.x; i < kSortWarps * kSortBins; i += kSortThreads) (&hist[0][0])[i] = 0;
+    __syncthreads();
+    uint2 pair[kSortRounds];
+    uint32_t rank[kSortRounds];
+#pragma unroll
+    for (int r = 0; r < kSortRounds; ++r) {
+      const int at = warp * strip + r * 32 + lane;
+      const bool here = r * 32 < strip && at < mine;
+      if (here) pair[r] = in[at];
+      const uint32_t digit = here ? (pair[r].x >> (digit_bits * p)) & mask : bins;
+      unsigned peers = 0xffffffffu;
+      for (int bit = 0; bit <= digit_bits; ++bit) {
+        const bool on = (digit >> bit) & 1;
+        const unsigned bal = __ballot_sync(0xffffffffu, on);
+        peers &= on ? bal : ~bal;
+      }
+      const uint32_t c = here ? hist[warp][digit] : 0u;
+      rank[r] = c + (uint32_t)__popc(peers & below);
+      __syncwarp();
+      if (here && (peers >> lane) == 1u) hist[warp][digit] = c + (uint32_t)__popc(peers);
+      __syncwarp();
+    }
+    __syncthreads();
+    if (threadIdx.x < kSortBins) {  // pairs of earlier warps, and the block's total
+      uint32_t t = 0;
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t c = hist[w][threadIdx.x];
+        hist[w][threadIdx.x] = t;
+        t += c;
+      }
+      totals[threadIdx.x] = t;
+    }
+    cluster_sync();
+    if (threadIdx.x < kSortBins) {
+      uint32_t all = 0, before = 0;
+#pragma unroll
+      for (uint32_t b = 0; b < kSortBlocks; ++b) {
+        uint32_t t;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(t) : "r"(cluster_addr(&totals[threadIdx.x], b)) : "memory");
+        all += t;
+        if (b < block) before += t;
+      }
+      const uint32_t inc = warp_inclusive_scan(all);
+      if (lane == 31) warp_sum[warp] = inc;
+      base[threadIdx.x] = before + inc - all;
+    }
+    __syncthreads();
+    if (threadIdx.x < kSortBins) {
+      uint32_t o = 0;
+      for (int w = 0; w < warp; ++w) o += warp_sum[w];
+      base[threadIdx.x] += o;
+    }
+    __syncthreads();
+    const bool last = p + 1 == passes;
+#pragma unroll
+    for (int r = 0; r < kSortRounds; ++r) {
+      const int at = warp * strip + r * 32 + lane;
+      if (r * 32 < strip && at < mine) {
+        const uint32_t digit = (pair[r].x >> (digit_bits * p)) & mask;
+        const uint32_t to = base[digit] + hist[warp][digit] + rank[r];
+        if (last) {
+          keys[to] = pair[r].x;
+          pos[to] = pair[r].y;
+        } else {
+          const uint32_t b = to / (uint32_t)tile;
+          asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(cluster_addr(&out[to - b * tile], b)),
+                       "r"(pair[r].x), "r"(pair[r].y)
+                       : "memory");
+        }
+      }
+    }
+    cluster_sync();  // the next pass's input is in place; after the last, no block's memory is read any more
+  }
 }
 
 // ------------------------------------------------------------ gradient
@@ -173,12 +248,14 @@ struct EmbedGrad {
   int chunk;        // sorted entries per chunk
   int64_t n_chunks;
   int n_seg;        // column segments
+  int64_t sum_blocks;
+  int zero_wide;    // rows of the table's gradient take 16-byte stores
 };
 
 constexpr int kGradWarps = 8;
 constexpr int kGradVecs = 2;   // accesses per lane
 constexpr int kGradBatch = 4;  // rows in flight per lane
-constexpr int kJoinBatch = 4;  // chunks whose partial sums are in flight
+constexpr int kZeroRows = 8;   // rows per warp of the clearing
 
 __device__ __forceinline__ int64_t lower_bound(const uint32_t *__restrict__ k, int64_t n, uint32_t v) {
   int64_t lo = 0, hi = n;
@@ -219,6 +296,27 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_embed_sum(const EmbedGrad g
   typedef Pack<T, B> P;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int acc_n = g.width / P::kN;
+  if ((int64_t)blockIdx.x >= g.sum_blocks) {  // ---- rows that no token names
+    const int64_t v0 = (((int64_t)blockIdx.x - g.sum_blocks) * kGradWarps + warp) * kZeroRows;
+    bool absent = false;
+    if (lane < kZeroRows && v0 + lane < (int64_t)g.vocab) {
+      const uint32_t v = (uint32_t)(v0 + lane);
+      const int64_t at = lower_bound(g.keys, g.n, v);
+      absent = at >= g.n || __ldg(g.keys + at) != v;
+    }
+    const unsigned rows = __ballot_sync(0xffffffffu, absent);
+    for (int r = 0; r < kZeroRows; ++r) {
+      if (!((rows >> r) & 1u)) continue;
+      T *o = reinterpret_cast<T *>(g.dtable) + (v0 + r) * g.table_ld;
+      if (g.zero_wide) {
+        const int n16 = g.width * (int)sizeof(T) / 16;
+        for (int i = lane; i < n16; i += 32) __stcs(reinterpret_cast<uint4 *>(o) + i, make_uint4(0, 0, 0, 0));
+      } else {
+        for (int i = lane; i < g.width; i += 32) o[i] = from_f32<T>(0.f);
+      }
+    }
+    return;
+  }
   const int64_t gw = (int64_t)blockIdx.x * kGradWarps + warp;
   const int64_t c = gw / g.n_seg;
   if (c >= g.n_chunks) return;
@@ -297,13 +395,15 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_embed_sum(const EmbedGrad g
 // A run that crosses chunk borders: the chunk it begins in adds the partial
 // sums of the chunks it covers, in order.  A warp does so for a run of up to
 // kJoinShort chunks; for a longer one the block's warps take an equal stretch
-// of it each, and their sums are added in the stretches' order.
-constexpr int kJoinShort = 8;
+// of it each, and their sums are added in the stretches' order.  (A block's
+// warps hold neighbouring chunks of one segment: few long runs begin in them.)
+constexpr int kJoinShort = 24;
 
 template <typename T, int B>
 __device__ __forceinline__ void add_parts(const EmbedGrad &g, int64_t q0, int64_t q1, int a0, int acc_n,
                                           float (&acc)[kGradVecs][Pack<T, B>::kN]) {
   constexpr int kN = Pack<T, B>::kN;
+  constexpr int kJoinBatch = kN >= 8 ? 4 : 8;
   for (; q0 < q1; q0 += kJoinBatch) {  // loads of several chunks in flight
     float v[kJoinBatch][kGradVecs][kN];
 #pragma unroll
@@ -351,20 +451,25 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_embed_join(const EmbedGrad 
   const int64_t w0 = (int64_t)blockIdx.x * kGradWarps;
   int64_t last_long = -1;
   {
-    const int64_t gw = w0 + warp, c = gw / g.n_seg;
-    if (c + 1 < g.n_chunks) {
+    const int64_t gw = w0 + warp, seg = gw / g.n_chunks, c = gw - seg * g.n_chunks;
+    if (seg < g.n_seg && c + 1 < g.n_chunks) {
       const int64_t j0 = c * g.chunk, j1 = j0 + g.chunk;
       const uint32_t cur = __ldg(g.keys + j1 - 1);
       const bool crosses = cur < g.vocab && __ldg(g.keys + j1) == cur;
       const bool earlier = j0 > 0 && __ldg(g.keys + j0) == cur && __ldg(g.keys + j0 - 1) == cur;
       if (crosses && !earlier) {
-        const int64_t end = j1 + lower_bound(g.keys + j1, g.n - j1, cur + 1u);
-        const int64_t last = (end - 1) / g.chunk;  // the chunk it ends in
+        int64_t last = c;  // the chunk it ends in: those after c that begin with it, 32 looked at per step
+        for (;;) {
+          const int64_t q = last + 1 + lane;
+          const unsigned same = __ballot_sync(0xffffffffu, q < g.n_chunks && __ldg(g.keys + q * g.chunk) == cur);
+          last += __popc(same);
+          if (same != 0xffffffffu) break;
+        }
         if (last - c > kJoinShort) {
           last_long = last;
           if (lane == 0) s_key[warp] = cur;
         } else {
-          const int a0 = (int)(gw - c * g.n_seg) * (32 * kGradVecs) + lane;
+          const int a0 = (int)seg * (32 * kGradVecs) + lane;
           clear();
           tail(c, a0);
           add_parts<T, B>(g, c + 1, last + 1, a0, acc_n, acc);
@@ -378,8 +483,8 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_embed_join(const EmbedGrad 
   for (int k = 0; k < kGradWarps; ++k) {
     const int64_t last = s_last[k];
     if (last < 0) continue;
-    const int64_t gw = w0 + k, c = gw / g.n_seg, n = last - c;
-    const int a0 = (int)(gw - c * g.n_seg) * (32 * kGradVecs) + lane;
+    const int64_t gw = w0 + k, seg = gw / g.n_chunks, c = gw - seg * g.n_chunks, n = last - c;
+    const int a0 = (int)seg * (32 * kGradVecs) + lane;
     clear();
     if (warp == 0) tail(c, a0);
     add_parts<T, B>(g, c + 1 + n * warp / kGradWarps, c + 1 + n * (warp + 1) / kGradWarps, a0, acc_n, acc);
@@ -410,15 +515,6 @@ int key_bits(uint32_t vocab) {
 
 constexpr int kSegElems = 32 * kGradVecs;  // accesses per segment
 
-// Whether the places are found by counting (n^2 comparisons, one kernel, beside
-// the clearing) or by a radix sort (three or four passes of four kernels).
-// Measured on GB300: the counting takes n^2 * 0.06 ns beside other work, the
-// sort about 55 us at 32768 tokens, in which memory idles.
-bool by_counting(int64_t n, int64_t clear_bytes) {
-  const double count_us = (double)n * (double)n * 6e-8, clear_us = (double)clear_bytes / 6.5e6;
-  return n <= 65536 && count_us <= (clear_us > 25.0 ? clear_us : 25.0);
-}
-
 struct GradWs {
   size_t keys, pos, k0, v0, k1, v1, temp, part, total;
   int chunk;
@@ -441,7 +537,7 @@ GradWs grad_ws(int64_t n, int32_t width) {
   o += align_up((size_t)n * 4, kAlign);
   w.pos = o;
   o += align_up((size_t)n * 4, kAlign);
-  const bool radix = n > 4096;  // it may be wanted
+  const bool radix = n > kSortMost;
   w.k0 = o;
   if (radix) o += align_up((size_t)n * 4, kAlign);
   w.v0 = o;
@@ -475,11 +571,13 @@ template <typename T, int B>
 cudaError_t launch_grad(EmbedGrad g, cudaStream_t s) {
   const int acc = g.width / Pack<T, B>::kN;
   g.n_seg = (int)ceil_div(acc, kSegElems);
-  const int64_t blocks = ceil_div(g.n_chunks * g.n_seg, kGradWarps);
+  g.sum_blocks = ceil_div(g.n_chunks * g.n_seg, kGradWarps);
+  const int64_t blocks = g.sum_blocks + (g.accumulate ? 0 : ceil_div((int64_t)g.vocab, (int64_t)kGradWarps * kZeroRows));
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if (blocks == 0) return cudaSuccess;
   cudaError_t e = launch_pdl(k_embed_sum<T, B>, (unsigned)blocks, kGradWarps * 32, 0, s, (const EmbedGrad)g);
   if (e != cudaSuccess || g.n_chunks < 2) return e;
-  return launch_pdl(k_embed_join<T, B>, (unsigned)blocks, kGradWarps * 32, 0, s, (const EmbedGrad)g);
+  return launch_pdl(k_embed_join<T, B>, (unsigned)g.sum_blocks, kGradWarps * 32, 0, s, (const EmbedGrad)g);
 }
 
 }  // namespace
@@ -567,41 +665,37 @@ snack_status snack_embed_grad(const void *ids, snack_index ids_t, int64_t n, con
   g.chunk = W.chunk;
   g.n_chunks = W.n_chunks;
   g.part_ld = W.part_ld;
-  ZeroFill z = {};
-  if (!accumulate) {
-    z.base = reinterpret_cast<uint8_t *>(dtable);
-    z.row_bytes = (int64_t)width * (int64_t)es;
-    z.ld_bytes = dtable_ld * (int64_t)es;
-    z.rows = vocab;
-    z.wide = access_bytes((uintptr_t)dtable | (uintptr_t)z.ld_bytes | (uintptr_t)z.row_bytes) == 16;
-  }
-  const int64_t zero_blocks = ceil_div(z.rows, (int64_t)kZeroRows);
-  const bool counting = n > 0 && by_counting(n, z.rows * z.row_bytes);
+  g.zero_wide = access_bytes((uintptr_t)dtable | (uintptr_t)(dtable_ld * es) | (uintptr_t)((size_t)width * es)) == 16;
   cudaError_t e = cudaSuccess;
-  if (!counting && zero_blocks > 0) e = launch_pdl(k_zero, (unsigned)zero_blocks, kRankThreads, 0, s, z);
-  if (e != cudaSuccess) return SNACK_ERR_CUDA;
-  if (n == 0) return SNACK_OK;
-  uint32_t *keys = reinterpret_cast<uint32_t *>(w + W.keys), *pos = reinterpret_cast<uint32_t *>(w + W.pos);
-  g.keys = keys;
-  g.pos = pos;
-  g.part = reinterpret_cast<float *>(w + W.part);
-  const TokenSrc src{ids, ids_t == SNACK_I64, (uint32_t)vocab};
-  if (counting) {
-    const int rank_blocks = (int)ceil_div(n, kRankRows);
-    e = launch_pdl(k_rank, (unsigned)(rank_blocks + zero_blocks), kRankThreads, 0, s, src, (int)n, keys, pos, rank_blocks,
-                   z);
-  } else {
+  if (n > 0) {
+    uint32_t *keys = reinterpret_cast<uint32_t *>(w + W.keys), *pos = reinterpret_cast<uint32_t *>(w + W.pos);
+    g.keys = keys;
+    g.pos = pos;
+    g.part = reinterpret_cast<float *>(w + W.part);
+    const TokenSrc src{ids, ids_t == SNACK_I64, (uint32_t)vocab};
+    const int bits = key_bits((uint32_t)vocab);
     try {
-      e = radix_sort_custom<uint32_t>(src, ArrayDst<uint32_t>{keys, pos}, n, key_bits((uint32_t)vocab),
-                                      reinterpret_cast<uint32_t *>(w + W.k0), reinterpret_cast<uint32_t *>(w + W.v0),
-                                      reinterpret_cast<uint32_t *>(w + W.k1), reinterpret_cast<uint32_t *>(w + W.v1),
-                                      w + W.temp, s);
+      if (n <= kRankMax) {
+        e = launch_pdl(k_rank, (unsigned)ceil_div(n, kRankRows), kRankThreads, 0, s, src, (int)n, keys, pos);
+      } else if (n <= kSortMost) {
+        const int passes = (bits + 8) / 9;
+        const int tile = (int)(ceil_div(ceil_div(n, kSortBlocks), kSortThreads) * kSortThreads);
+        e = raise_smem_limit(k_sort, kSortSmem);
+        if (e == cudaSuccess)
+          e = launch_pdl(k_sort, kSortBlocks, kSortThreads, kSortSmem, s, src, (int)n, tile, passes,
+                         (bits + passes - 1) / passes, keys, pos);
+      } else {
+        e = radix_sort_custom<uint32_t>(src, ArrayDst<uint32_t>{keys, pos}, n, bits,
+                                        reinterpret_cast<uint32_t *>(w + W.k0), reinterpret_cast<uint32_t *>(w + W.v0),
+                                        reinterpret_cast<uint32_t *>(w + W.k1), reinterpret_cast<uint32_t *>(w + W.v1),
+                                        w + W.temp, s);
+      }
     } catch (...) {  // the shared-memory table could not grow
       return SNACK_ERR_CUDA;
     }
+    if (e != cudaSuccess) return SNACK_ERR_CUDA;
   }
-  if (e != cudaSuccess) return SNACK_ERR_CUDA;
-  const int b = access_bytes((uintptr_t)dtable | (uintptr_t)dout | (uintptr_t)(dtable_ld * es) |
+  const int b = access_bytes((uintptr_t)dtable | (n > 0 ? (uintptr_t)dout : 0) | (uintptr_t)(dtable_ld * es) |
                              (uintptr_t)(dout_ld * es) | (uintptr_t)((size_t)width * es));
   if (t == SNACK_F32)
     e = b == 16 ? launch_grad<float, 16>(g, s) : b == 8 ? launch_grad<float, 8>(g, s) : launch_grad<float, 4>(g, s);

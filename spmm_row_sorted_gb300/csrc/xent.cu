@@ -772,41 +772,51 @@ __global__ void __launch_bounds__(1024) k_xent_total(const float *__restrict__ r
 }
 
 // [rows][width] into `parts` planes of bf16 [rows][out_ld]: the value, what
-// its rounding to bf16 leaves over, and what that leaves over.
+// its rounding to bf16 leaves over, and what that leaves over.  A warp per row,
+// four groups of eight elements per lane in flight.
 template <typename T>
 __global__ void __launch_bounds__(256) k_xent_pack(const T *__restrict__ in, int64_t ld, int64_t rows, int32_t width,
                                                    int parts, bf16 *__restrict__ out, int32_t out_ld, int64_t plane, int vec) {
   pdl_wait();
+  constexpr int kU = 4, kB = 16 / (int)sizeof(T);
+  const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (r >= rows) return;
   const int groups = out_ld / 8;
-  const int64_t total = rows * groups;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / groups;
-    const int c = (int)(i - r * groups) * 8;
-    float v[8];
-    const T *at = in + r * ld + c;
-    if (vec && c + 8 <= width) {
-      constexpr int kB = 16 / (int)sizeof(T);
+  for (int g0 = threadIdx.x & 31; g0 < groups; g0 += 32 * kU) {
+    float v[kU][8];
 #pragma unroll
-      for (int h = 0; h < 8 / kB; ++h) {
-        Pack<T, 16> q;
-        q.raw = __ldg(reinterpret_cast<const uint4 *>(at) + h);
+    for (int u = 0; u < kU; ++u) {
+      const int c = (g0 + 32 * u) * 8;
+      const T *at = in + r * ld + c;
+      if (vec && c + 8 <= width) {
 #pragma unroll
-        for (int j = 0; j < kB; ++j) v[h * kB + j] = q.get(j);
+        for (int h = 0; h < 8 / kB; ++h) {
+          Pack<T, 16> q;
+          q.raw = __ldg(reinterpret_cast<const uint4 *>(at) + h);
+#pragma unroll
+          for (int j = 0; j < kB; ++j) v[u][h * kB + j] = q.get(j);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[u][j] = c + j < width ? to_f32(at[j]) : 0.f;
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = c + j < width ? to_f32(at[j]) : 0.f;
     }
-    for (int p = 0; p < parts; ++p) {
-      Pack<bf16, 16> o;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float h = __bfloat162float(__float2bfloat16_rn(v[j]));
-        if (isinf(h) && !isinf(v[j])) h = __uint_as_float(__float_as_uint(v[j]) & 0xFFFF0000u);  // rounded past the largest
-        o.set(j, h);
-        v[j] = isfinite(v[j]) ? v[j] - h : 0.f;
+    for (int u = 0; u < kU; ++u) {
+      const int c = (g0 + 32 * u) * 8;
+      if (c >= out_ld) break;
+      for (int p = 0; p < parts; ++p) {
+        Pack<bf16, 16> o;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float x = v[u][j];
+          float h = __bfloat162float(__float2bfloat16_rn(x));
+          if (isinf(h) && !isinf(x)) h = __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);  // rounded past the largest
+          o.set(j, h);
+          v[u][j] = isfinite(x) ? x - h : 0.f;
+        }
+        reinterpret_cast<uint4 *>(out + p * plane + r * out_ld + c)[0] = o.raw;
       }
-      reinterpret_cast<uint4 *>(out + p * plane + r * out_ld + c)[0] = o.raw;
     }
   }
 }
@@ -1005,7 +1015,7 @@ XentWs xent_ws(const XentShape &s, bool grad) {
 bool rows_ready(const void *p, int64_t ld, int32_t n, bool grad) {
   if (!ptr_aligned(p, 16) || ld % 8 != 0) return false;
   const bool on_lines = ptr_aligned(p, 128) && ld % 64 == 0;
-  return on_lines || n < (grad ? 1024 : 4096);
+  return on_lines || n < (grad ? 1024 : 1536);
 }
 
 XentShape xent_shape(const void *x, int64_t x_ld, int32_t n, const void *wt, int64_t w_ld, int64_t vocab, int32_t width,
@@ -1057,9 +1067,7 @@ cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtens
 }
 
 cudaError_t pack(const XentShape &s, const void *in, int64_t ld, int64_t rows, void *out, cudaStream_t st) {
-  const int64_t total = rows * (s.ld / 8);
-  int64_t blocks = ceil_div(total, 256);
-  if (blocks > (int64_t)s.sms * 32) blocks = (int64_t)s.sms * 32;
+  const int64_t blocks = ceil_div(rows, 8);
   const int vec = ptr_aligned(in, 16) && (size_t)ld * dtype_size(s.t) % 16 == 0;
   if (s.t == SNACK_F32)
     return launch_pdl(k_xent_pack<float>, (unsigned)blocks, 256, 0, st, reinterpret_cast<const float *>(in), ld, rows,
