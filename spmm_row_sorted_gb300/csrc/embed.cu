@@ -269,31 +269,48 @@ __device__ __forceinline__ int64_t lower_bound(const uint32_t *__restrict__ k, i
   return lo;
 }
 
-// this lane's accesses of one row of the gradient: scale * acc (+ what is there)
+template <typename T>
+__device__ __forceinline__ T *table_row(const EmbedGrad &g, uint32_t row) {
+  return reinterpret_cast<T *>(g.dtable) + (int64_t)row * g.table_ld;
+}
+
+// this lane's accesses of a row as it is (accumulate)
+template <typename T, int B>
+__device__ __forceinline__ void get_row(const EmbedGrad &g, uint32_t row, int a0, int acc_n, Pack<T, B> (&old)[kGradVecs]) {
+  const typename Pack<T, B>::R *o = reinterpret_cast<const typename Pack<T, B>::R *>(table_row<T>(g, row));
+#pragma unroll
+  for (int u = 0; u < kGradVecs; ++u)
+    if (a0 + 32 * u < acc_n) old[u].raw = o[a0 + 32 * u];
+}
+
+// this lane's accesses of one row of the gradient: scale * acc (+ what was there)
 template <typename T, int B>
 __device__ __forceinline__ void put_row(const EmbedGrad &g, uint32_t row, int a0, int acc_n,
-                                        const float (&acc)[kGradVecs][Pack<T, B>::kN]) {
+                                        const float (&acc)[kGradVecs][Pack<T, B>::kN], bool add,
+                                        const Pack<T, B> (&old)[kGradVecs]) {
   typedef Pack<T, B> P;
-  typename P::R *o = reinterpret_cast<typename P::R *>(reinterpret_cast<T *>(g.dtable) + (int64_t)row * g.table_ld);
+  typename P::R *o = reinterpret_cast<typename P::R *>(table_row<T>(g, row));
 #pragma unroll
   for (int u = 0; u < kGradVecs; ++u) {
     const int a = a0 + 32 * u;
     if (a >= acc_n) continue;
     P v;
-    if (g.accumulate) v.raw = o[a];
 #pragma unroll
     for (int i = 0; i < P::kN; ++i) {
       const float t = g.scale * acc[u][i];
-      v.set(i, g.accumulate ? v.get(i) + t : t);
+      v.set(i, add ? old[u].get(i) + t : t);
     }
     o[a] = v.raw;
   }
 }
 
-template <typename T, int B>
+// kAdd: the sums are added to the rows that are there, which are read with the
+// batch in which their run begins.
+template <typename T, int B, bool kAdd>
 __global__ void __launch_bounds__(kGradWarps * 32) k_embed_sum(const EmbedGrad g) {
   pdl_wait();
   typedef Pack<T, B> P;
+  constexpr int kBatch = kAdd ? kGradBatch / 2 : kGradBatch;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int acc_n = g.width / P::kN;
   if ((int64_t)blockIdx.x >= g.sum_blocks) {  // ---- rows that no token names
@@ -335,6 +352,8 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_embed_sum(const EmbedGrad g
     for (int i = 0; i < P::kN; ++i) acc[u][i] = 0.f;
   uint32_t cur = first;
   bool head = from_before;  // the current run began in an earlier chunk
+  P old[kGradVecs];         // the current run's row (kAdd)
+  if (kAdd) get_row<T, B>(g, cur, a0, acc_n, old);
   auto keep_part = [&](int which) {
     float *p = g.part + (c * 2 + which) * g.part_ld;
 #pragma unroll
@@ -347,18 +366,21 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_embed_sum(const EmbedGrad g
     const uint32_t my_key = b + lane < j1 ? __ldg(g.keys + b + lane) : 0xFFFFFFFFu;
     const uint32_t my_pos = b + lane < j1 ? __ldg(g.pos + b + lane) : 0u;
     const int m = (int)min((int64_t)32, j1 - b);
-    for (int e0 = 0; e0 < m && cur < g.vocab; e0 += kGradBatch) {
-      P v[kGradBatch][kGradVecs];
+    for (int e0 = 0; e0 < m && cur < g.vocab; e0 += kBatch) {
+      P v[kBatch][kGradVecs], was[kAdd ? kBatch : 1][kGradVecs];
+      uint32_t prev = cur;
 #pragma unroll
-      for (int e = 0; e < kGradBatch; ++e) {
+      for (int e = 0; e < kBatch; ++e) {
         const uint32_t k = __shfl_sync(0xffffffffu, my_key, e0 + e), p = __shfl_sync(0xffffffffu, my_pos, e0 + e);
+        if (kAdd && k != prev && k < g.vocab) get_row<T, B>(g, k, a0, acc_n, was[kAdd ? e : 0]);
+        prev = k;
         const typename P::R *src = reinterpret_cast<const typename P::R *>(dout + (int64_t)p * g.dout_ld);
 #pragma unroll
         for (int u = 0; u < kGradVecs; ++u)
           if (k < g.vocab && a0 + 32 * u < acc_n) v[e][u].raw = __ldcs(src + a0 + 32 * u);
       }
 #pragma unroll
-      for (int e = 0; e < kGradBatch; ++e) {
+      for (int e = 0; e < kBatch; ++e) {
         const uint32_t k = __shfl_sync(0xffffffffu, my_key, e0 + e);
         if (k != cur) {
           if (cur >= g.vocab) break;
@@ -366,10 +388,13 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_embed_sum(const EmbedGrad g
           if (head)
             keep_part(0);
           else
-            put_row<T, B>(g, cur, a0, acc_n, acc);
+            put_row<T, B>(g, cur, a0, acc_n, acc, kAdd, old);
           head = false;
           cur = k;
           if (cur >= g.vocab) break;
+          if (kAdd)
+#pragma unroll
+            for (int u = 0; u < kGradVecs; ++u) old[u].raw = was[kAdd ? e : 0][u].raw;
 #pragma unroll
           for (int u = 0; u < kGradVecs; ++u)
 #pragma unroll
@@ -389,7 +414,7 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_embed_sum(const EmbedGrad g
   else if (after == cur)
     keep_part(1);
   else
-    put_row<T, B>(g, cur, a0, acc_n, acc);
+    put_row<T, B>(g, cur, a0, acc_n, acc, kAdd, old);
 }
 
 // A run that crosses chunk borders: the chunk it begins in adds the partial
@@ -435,6 +460,7 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_embed_join(const EmbedGrad 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int acc_n = g.width / kN;
   float acc[kGradVecs][kN];
+  Pack<T, B> old[kGradVecs];
   auto clear = [&] {
 #pragma unroll
     for (int u = 0; u < kGradVecs; ++u)
@@ -473,7 +499,8 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_embed_join(const EmbedGrad 
           clear();
           tail(c, a0);
           add_parts<T, B>(g, c + 1, last + 1, a0, acc_n, acc);
-          put_row<T, B>(g, cur, a0, acc_n, acc);
+          if (g.accumulate) get_row<T, B>(g, cur, a0, acc_n, old);
+          put_row<T, B>(g, cur, a0, acc_n, acc, g.accumulate != 0, old);
         }
       }
     }
@@ -499,7 +526,8 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_embed_join(const EmbedGrad 
         for (int u = 0; u < kGradVecs; ++u)
 #pragma unroll
           for (int i = 0; i < kN; ++i) acc[u][i] += s_sum[q][(u * kN + i) * 32 + lane];
-      put_row<T, B>(g, s_key[k], a0, acc_n, acc);
+      if (g.accumulate) get_row<T, B>(g, s_key[k], a0, acc_n, old);
+      put_row<T, B>(g, s_key[k], a0, acc_n, acc, g.accumulate != 0, old);
     }
     __syncthreads();
   }
@@ -575,7 +603,9 @@ cudaError_t launch_grad(EmbedGrad g, cudaStream_t s) {
   const int64_t blocks = g.sum_blocks + (g.accumulate ? 0 : ceil_div((int64_t)g.vocab, (int64_t)kGradWarps * kZeroRows));
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   if (blocks == 0) return cudaSuccess;
-  cudaError_t e = launch_pdl(k_embed_sum<T, B>, (unsigned)blocks, kGradWarps * 32, 0, s, (const EmbedGrad)g);
+  cudaError_t e = g.accumulate
+                      ? launch_pdl(k_embed_sum<T, B, true>, (unsigned)blocks, kGradWarps * 32, 0, s, (const EmbedGrad)g)
+                      : launch_pdl(k_embed_sum<T, B, false>, (unsigned)blocks, kGradWarps * 32, 0, s, (const EmbedGrad)g);
   if (e != cudaSuccess || g.n_chunks < 2) return e;
   return launch_pdl(k_embed_join<T, B>, (unsigned)g.sum_blocks, kGradWarps * 32, 0, s, (const EmbedGrad)g);
 }

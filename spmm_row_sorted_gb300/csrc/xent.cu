@@ -805,6 +805,13 @@ __global__ void __launch_bounds__(256) k_xent_pack(const T *__restrict__ in, int
     for (int u = 0; u < kU; ++u) {
       const int c = (g0 + 32 * u) * 8;
       if (c >= out_ld) break;
+      if (sizeof(T) == 2) {  // bf16 is its own only part
+        Pack<bf16, 16> o;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o.h[j] = (uint16_t)(__float_as_uint(v[u][j]) >> 16);
+        *reinterpret_cast<uint4 *>(out + r * out_ld + c) = o.raw;
+        continue;
+      }
       for (int p = 0; p < parts; ++p) {
         Pack<bf16, 16> o;
 #pragma unroll
@@ -1015,7 +1022,7 @@ XentWs xent_ws(const XentShape &s, bool grad) {
 bool rows_ready(const void *p, int64_t ld, int32_t n, bool grad) {
   if (!ptr_aligned(p, 16) || ld % 8 != 0) return false;
   const bool on_lines = ptr_aligned(p, 128) && ld % 64 == 0;
-  return on_lines || n < (grad ? 1024 : 1536);
+  return on_lines || n < (grad ? 1024 : 4096);
 }
 
 XentShape xent_shape(const void *x, int64_t x_ld, int32_t n, const void *wt, int64_t w_ld, int64_t vocab, int32_t width,
@@ -1036,15 +1043,14 @@ XentShape xent_shape(const void *x, int64_t x_ld, int32_t n, const void *wt, int
 // Units of K stages (64 each): see the note on rounding at the top.  Each unit
 // costs the tensor core about 450 cycles (the switch of accumulators, and the
 // epilogue's reads of tensor memory), of 512 a stage.  Sums that become the
-// loss or other fp32 results take short units, of equal length; what is rounded
+// loss or other fp32 results take short units, of equal length (shorter ones
+// for a short K, whose sums of few units are the further off); what is rounded
 // to bf16 (dz, dx and dw of bf16 operands) is far below half its ulp with long
 // ones.  Measured at 4096 x 131072 x 2048 bf16, against 64 bits: units of 4, 6,
 // 8 and 16 give a mean loss 5e-7, 8e-7, 1.1e-6 and 2.3e-6 off, and the forward
 // takes 1637, 1540, 1448 and 1380 us (1346 us without units).
-constexpr int kUnitExact = 5, kUnitBf16 = 64;
-
 int unit_of(int k_blocks, bool exact) {
-  const int most = exact ? kUnitExact : kUnitBf16;
+  const int most = !exact ? 64 : k_blocks < 32 ? 4 : 5;
   return (int)ceil_div(k_blocks, ceil_div(k_blocks, most));
 }
 
