@@ -93,6 +93,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
     if (mbar_try(bar, parity)) return true;
   return false;
 }
+// the same for a converged warp, with one answer for all its lanes
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
+  return __any_sync(0xffffffffu, mbar_wait(bar, parity));
+}
 // one lane of a converged warp
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -333,7 +337,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
     Tile r;
     r.split = t / (P.m_tiles * P.n_tiles);
     const int mn = t - r.split * (P.m_tiles * P.n_tiles);
-    if (kMode == kDw) {  // columns (D) run fastest: a row of tiles shares the piece's dz^T
+    if (kMode == kDx || kMode == kDw) {  // columns (D) run fastest: a row of tiles shares its part of dz
       r.m0 = mn / P.n_tiles * kM;
       r.n0 = mn % P.n_tiles * P.nt;
     } else {
@@ -361,7 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
         for (int c = 0; c < P.products && ok; ++c) {
           const int za = (P.a_part >> (4 * c)) & 15, zb = (P.b_part >> (4 * c)) & 15;
           for (int k = q.k0 * kKb; k < (q.k0 + q.nk) * kKb; k += kKb) {
-            if (!mbar_wait(&empty[s], phase ^ 1)) {
+            if (!warp_wait(&empty[s], phase ^ 1)) {
               ok = false;
               break;
             }
@@ -398,10 +402,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
       for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
         const Tile q = tile_at(t);
         const int steps = P.products * q.nk, lead = steps - q.nk;
-        bool ready = false;  // the next stage's bytes have been seen
+        bool seen = false;  // the next stage's bytes are there
         for (int i = 0; i < steps && ok; ++n_acc) {  // a unit of steps per accumulator
           const int buf = n_acc & 1;
-          if (!mbar_wait(&acc_free[buf], ((n_acc >> 1) & 1) ^ 1)) {
+          if (!warp_wait(&acc_free[buf], ((n_acc >> 1) & 1) ^ 1)) {
             ok = false;
             break;
           }
@@ -410,7 +414,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
           const int end = i < lead ? lead : min(steps, i + P.unit);
           uint32_t more = 0;  // the unit's first MMA overwrites
           for (; i < end; ++i) {
-            if (!ready && !mbar_wait(&full[s], phase)) {
+            if (!__any_sync(0xffffffffu, seen) && !warp_wait(&full[s], phase)) {
               ok = false;
               break;
             }
@@ -420,7 +424,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
               s = 0;
               phase ^= 1;
             }
-            ready = i + 1 < steps && mbar_try(&full[s], phase);  // answered while the MMAs below are issued
+            seen = i + 1 < steps && mbar_try(&full[s], phase);  // answered while the MMAs below are issued
             if (one) {
 #pragma unroll
               for (int k = 0; k < kKb / 16; ++k)
@@ -473,7 +477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
       const int units = (q.nk + P.unit - 1) / P.unit + (P.products > 1 ? 1 : 0);
       for (int u = 0; u < units; ++u, ++n_acc) {
         const int buf = n_acc & 1;
-        if (!mbar_wait(&acc_full[buf], (n_acc >> 1) & 1)) {
+        if (!warp_wait(&acc_full[buf], (n_acc >> 1) & 1)) {
           ok = false;
           break;
         }
@@ -1059,6 +1063,13 @@ cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtens
                         cudaStream_t s) {
   cudaError_t e = raise_smem_limit(k_xent<kMode>, kSmem);
   if (e != cudaSuccess) return e;
+  // the register split draws on what the launch gives: a kernel built with fewer would wait for ever
+  static const bool enough = [] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, k_xent<kMode>) == cudaSuccess &&
+           a.numRegs * kThreads >= 256 * kEpiRegs + 128 * kIssueRegs;
+  }();
+  if (!enough) return cudaErrorInvalidDeviceFunction;
   g.m_tiles = (int32_t)ceil_div(g.m, kM);
   g.n_tiles = (int32_t)ceil_div(g.n, g.nt);
   g.unit = unit_of((int)ceil_div(g.k_blocks, g.n_split), kMode == kStats || g.products > 1);
