@@ -109,11 +109,31 @@ __global__ void __launch_bounds__(kRankThreads) k_rank(TokenSrc ids, int n, uint
   }
 }
 
+// Rows of the table's gradient to clear, in 16-byte accesses where they allow it.
+struct ZeroRows {
+  uint8_t *base;
+  int64_t row_bytes, ld_bytes, rows;
+  int wide;
+};
+__device__ __forceinline__ void clear_row(const ZeroRows &z, int64_t r) {  // a warp
+  const int lane = threadIdx.x & 31;
+  uint8_t *row = z.base + r * z.ld_bytes;
+  if (z.wide) {
+    uint4 *o = reinterpret_cast<uint4 *>(row);
+    for (int64_t i = lane; i < z.row_bytes / 16; i += 32) __stcs(o + i, make_uint4(0, 0, 0, 0));
+  } else {
+    uint16_t *o = reinterpret_cast<uint16_t *>(row);
+    for (int64_t i = lane; i < z.row_bytes / 2; i += 32) o[i] = 0;
+  }
+}
+
 // A stable LSD radix sort of up to 65,536 pairs by one cluster, in one launch.
 // Each of its eight blocks holds `tile` pairs in shared memory; a pass of up to
 // nine bits ranks them (a warp's equal digits by ballots, its counts before them in
 // its own histogram), the blocks read each other's digit totals, and every pair
 // goes straight to its place in the shared memory of the block that holds it.
+// About 16 us at 32768 tokens; the other SMs clear the table's first rows, as
+// many as that takes.
 constexpr int kSortBlocks = 8;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -137,8 +157,16 @@ __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t block) 
 }
 
 __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThreads, 1)
-    k_sort(TokenSrc ids, int n, int tile, int passes, int digit_bits, uint32_t *__restrict__ keys, uint32_t *__restrict__ pos) {
+    k_sort(TokenSrc ids, int n, int tile_bits, int passes, int digit_bits, uint32_t *__restrict__ keys, uint32_t *__restrict__ pos,
+           const ZeroRows zero) {
   pdl_wait();
+  if (blockIdx.x >= kSortBlocks) {  // the clusters after the first clear rows meanwhile
+    const int warp = threadIdx.x >> 5;
+    for (int64_t r = (int64_t)(blockIdx.x - kSortBlocks) * kSortWarps + warp; r < zero.rows;
+         r += (int64_t)(gridDim.x - kSortBlocks) * kSortWarps)
+      clear_row(zero, r);
+    return;
+  }
   extern __shared__ __align__(16) uint8_t sort_smem[];
   uint2 *buf = reinterpret_cast<uint2 *>(sort_smem);  // [2][tile]
   uint32_t(*hist)[kSortBins] = reinterpret_cast<uint32_t(*)[kSortBins]>(sort_smem + 2 * kSortTile * 8);
@@ -148,8 +176,9 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
   const uint32_t bins = 1u << digit_bits, mask = bins - 1u;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t block = blockIdx.x;
+  const int tile = 1 << tile_bits;
   const int first = (int)block * tile, mine = max(0, min(tile, n - first));
-  const int strip = tile / kSortWarps;  // pairs of a warp, in rounds of 32
+  const int rounds = tile / kSortThreads;  // a warp's pairs, 32 at a time
   const uint32_t below = (1u << lane) - 1u;
   for (int i = threadIdx.x; i < mine; i += kSortThreads) buf[i] = make_uint2(ids.key(first + i), (uint32_t)(first + i));
   for (int p = 0; p < passes; ++p) {
@@ -160,12 +189,15 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
     uint32_t rank[kSortRounds];
 #pragma unroll
     for (int r = 0; r < kSortRounds; ++r) {
-      const int at = warp * strip + r * 32 + lane;
-      const bool here = r * 32 < strip && at < mine;
+      if (r >= rounds) break;
+      const int at = (warp * rounds + r) * 32 + lane;
+      const bool here = at < mine;
       if (here) pair[r] = in[at];
       const uint32_t digit = here ? (pair[r].x >> (digit_bits * p)) & mask : bins;
       unsigned peers = 0xffffffffu;
-      for (int bit = 0; bit <= digit_bits; ++bit) {
+#pragma unroll
+      for (int bit = 0; bit < 10; ++bit) {
+        if (bit > digit_bits) break;
         const bool on = (digit >> bit) & 1;
         const unsigned bal = __ballot_sync(0xffffffffu, on);
         peers &= on ? bal : ~bal;
@@ -210,16 +242,17 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
     const bool last = p + 1 == passes;
 #pragma unroll
     for (int r = 0; r < kSortRounds; ++r) {
-      const int at = warp * strip + r * 32 + lane;
-      if (r * 32 < strip && at < mine) {
+      if (r >= rounds) break;
+      const int at = (warp * rounds + r) * 32 + lane;
+      if (at < mine) {
         const uint32_t digit = (pair[r].x >> (digit_bits * p)) & mask;
         const uint32_t to = base[digit] + hist[warp][digit] + rank[r];
         if (last) {
           keys[to] = pair[r].x;
           pos[to] = pair[r].y;
         } else {
-          const uint32_t b = to / (uint32_t)tile;
-          asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(cluster_addr(&out[to - b * tile], b)),
+          const uint32_t b = to >> tile_bits;
+          asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(cluster_addr(&out[to & (uint32_t)(tile - 1)], b)),
                        "r"(pair[r].x), "r"(pair[r].y)
                        : "memory");
         }
@@ -249,7 +282,8 @@ struct EmbedGrad {
   int64_t n_chunks;
   int n_seg;        // column segments
   int64_t sum_blocks;
-  int zero_wide;    // rows of the table's gradient take 16-byte stores
+  ZeroRows zero;    // the rows that no token names, from `cleared` on
+  int64_t cleared;
 };
 
 constexpr int kGradWarps = 8;
@@ -314,7 +348,7 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_embed_sum(const EmbedGrad g
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int acc_n = g.width / P::kN;
   if ((int64_t)blockIdx.x >= g.sum_blocks) {  // ---- rows that no token names
-    const int64_t v0 = (((int64_t)blockIdx.x - g.sum_blocks) * kGradWarps + warp) * kZeroRows;
+    const int64_t v0 = g.cleared + (((int64_t)blockIdx.x - g.sum_blocks) * kGradWarps + warp) * kZeroRows;
     bool absent = false;
     if (lane < kZeroRows && v0 + lane < (int64_t)g.vocab) {
       const uint32_t v = (uint32_t)(v0 + lane);
@@ -322,16 +356,8 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_embed_sum(const EmbedGrad g
       absent = at >= g.n || __ldg(g.keys + at) != v;
     }
     const unsigned rows = __ballot_sync(0xffffffffu, absent);
-    for (int r = 0; r < kZeroRows; ++r) {
-      if (!((rows >> r) & 1u)) continue;
-      T *o = reinterpret_cast<T *>(g.dtable) + (v0 + r) * g.table_ld;
-      if (g.zero_wide) {
-        const int n16 = g.width * (int)sizeof(T) / 16;
-        for (int i = lane; i < n16; i += 32) __stcs(reinterpret_cast<uint4 *>(o) + i, make_uint4(0, 0, 0, 0));
-      } else {
-        for (int i = lane; i < g.width; i += 32) o[i] = from_f32<T>(0.f);
-      }
-    }
+    for (int r = 0; r < kZeroRows; ++r)
+      if ((rows >> r) & 1u) clear_row(g.zero, v0 + r);
     return;
   }
   const int64_t gw = (int64_t)blockIdx.x * kGradWarps + warp;
@@ -556,7 +582,7 @@ GradWs grad_ws(int64_t n, int32_t width) {
   GradWs w;
   const int64_t segs = ceil_div(width, 512);  // at 16-byte accesses; narrower ones have more
   int64_t chunk = 8;
-  while (chunk < 4096 && n / chunk * segs > 8192) chunk *= 2;
+  while (chunk < 4096 && n / chunk * segs > 4096) chunk *= 2;
   w.chunk = (int)chunk;
   w.n_chunks = n > 0 ? (n + chunk - 1) / chunk : 0;
   w.part_ld = (int64_t)align_up((size_t)width, 4);
@@ -600,7 +626,7 @@ cudaError_t launch_grad(EmbedGrad g, cudaStream_t s) {
   const int acc = g.width / Pack<T, B>::kN;
   g.n_seg = (int)ceil_div(acc, kSegElems);
   g.sum_blocks = ceil_div(g.n_chunks * g.n_seg, kGradWarps);
-  const int64_t blocks = g.sum_blocks + (g.accumulate ? 0 : ceil_div((int64_t)g.vocab, (int64_t)kGradWarps * kZeroRows));
+  const int64_t blocks = g.sum_blocks + (g.accumulate ? 0 : ceil_div((int64_t)g.vocab - g.cleared, (int64_t)kGradWarps * kZeroRows));
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   if (blocks == 0) return cudaSuccess;
   cudaError_t e = g.accumulate
@@ -695,7 +721,9 @@ snack_status snack_embed_grad(const void *ids, snack_index ids_t, int64_t n, con
   g.chunk = W.chunk;
   g.n_chunks = W.n_chunks;
   g.part_ld = W.part_ld;
-  g.zero_wide = access_bytes((uintptr_t)dtable | (uintptr_t)(dtable_ld * es) | (uintptr_t)((size_t)width * es)) == 16;
+  ZeroRows z = {reinterpret_cast<uint8_t *>(dtable), (int64_t)width * (int64_t)es, dtable_ld * (int64_t)es, vocab, 0};
+  z.wide = access_bytes((uintptr_t)dtable | (uintptr_t)z.ld_bytes | (uintptr_t)z.row_bytes) == 16;
+  g.zero = z;
   cudaError_t e = cudaSuccess;
   if (n > 0) {
     uint32_t *keys = reinterpret_cast<uint32_t *>(w + W.keys), *pos = reinterpret_cast<uint32_t *>(w + W.pos);
@@ -709,11 +737,19 @@ snack_status snack_embed_grad(const void *ids, snack_index ids_t, int64_t n, con
         e = launch_pdl(k_rank, (unsigned)ceil_div(n, kRankRows), kRankThreads, 0, s, src, (int)n, keys, pos);
       } else if (n <= kSortMost) {
         const int passes = (bits + 8) / 9;
-        const int tile = (int)(ceil_div(ceil_div(n, kSortBlocks), kSortThreads) * kSortThreads);
+        int tile_bits = 10;
+        while (((int64_t)kSortBlocks << tile_bits) < n) ++tile_bits;
+        // the rows that the rest of the GPU clears in the sort's time, at 5 TB/s (none: 235 us for 32768 tokens
+        // of 4096 over 131072 rows, and 121 us for 65536 of 1024; so many: 226 and 103 us)
+        z.rows = g.accumulate ? 0 : (int64_t)(5e6 * (5.0 + 3.4e-4 * (double)n)) / z.row_bytes;
+        if (z.rows > vocab) z.rows = vocab;
+        g.cleared = z.rows;
+        const int sms = current_sms(), clusters = z.rows > 0 && sms >= 2 * kSortBlocks ? sms / kSortBlocks : 1;
+        if (clusters == 1) g.cleared = 0;
         e = raise_smem_limit(k_sort, kSortSmem);
         if (e == cudaSuccess)
-          e = launch_pdl(k_sort, kSortBlocks, kSortThreads, kSortSmem, s, src, (int)n, tile, passes,
-                         (bits + passes - 1) / passes, keys, pos);
+          e = launch_pdl(k_sort, (unsigned)(clusters * kSortBlocks), kSortThreads, kSortSmem, s, src, (int)n, tile_bits, passes,
+                         (bits + passes - 1) / passes, keys, pos, z);
       } else {
         e = radix_sort_custom<uint32_t>(src, ArrayDst<uint32_t>{keys, pos}, n, bits,
                                         reinterpret_cast<uint32_t *>(w + W.k0), reinterpret_cast<uint32_t *>(w + W.v0),
