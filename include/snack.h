@@ -385,8 +385,8 @@ snack_status snack_embed_grad(const void *ids, snack_index ids_t, int64_t n, con
  *   loss[i] = lse[i] - z[i, targets[i]]
  * x [n, width] and w [vocab, width] in type t.  A target outside [0, vocab)
  * (such as -100) marks a position that is not trained on: its loss is 0, and
- * so is its row of the gradient; its row of x is still read and has to be
- * finite when dw is wanted.  loss receives n values (SNACK_NONE), their sum
+ * so is its row of dx, and dw holds nothing of it, whatever its row of x holds
+ * (infinities and NaN too).  loss receives n values (SNACK_NONE), their sum
  * over the trained positions (SNACK_SUM), or that divided by their count
  * (SNACK_MEAN; 0 when there are none).  state (n + 1 fp32 values) keeps each
  * row's lse, and 1 / count for the mean, for the gradient.

@@ -37,7 +37,8 @@
 // time, 24 in all), and a product is the sum of the six part products down to
 // 2^-16 of the leading one, smallest first; what is left out is below 2^-24.
 // The parts, and bf16 operands whose rows are not 16-byte aligned, are laid
-// out in the workspace, w's by pieces of the vocabulary.
+// out in the workspace, w's by pieces of the vocabulary; so is the gradient's x,
+// without the rows that are not trained on.
 //
 // Every wait on an mbarrier is bounded; when one runs out the CTA marks its
 // error word, waits (bounded) for what it has in flight, frees its tensor
@@ -775,16 +776,27 @@ __global__ void __launch_bounds__(1024) k_xent_total(const float *__restrict__ r
   }
 }
 
+// Rows that the gradient leaves out: no target in the vocabulary, or the weight 0.
+struct Drop {
+  TokenSrc targets;     // ids null: none are
+  const float *weight;  // per row, or null
+  __device__ __forceinline__ bool row(int64_t r) const {
+    return targets.ids && (targets.key(r) >= targets.vocab || (weight && weight[r] == 0.f));
+  }
+};
+
 // [rows][width] into `parts` planes of bf16 [rows][out_ld]: the value, what
 // its rounding to bf16 leaves over, and what that leaves over.  A warp per row,
-// four groups of eight elements per lane in flight.
+// four groups of eight elements per lane in flight.  Rows that are not trained
+// on (drop) become zeros: dz^T x then holds nothing of them, NaN neither.
 template <typename T>
 __global__ void __launch_bounds__(256) k_xent_pack(const T *__restrict__ in, int64_t ld, int64_t rows, int32_t width,
-                                                   int parts, bf16 *__restrict__ out, int32_t out_ld, int64_t plane, int vec) {
+                                                   int parts, bf16 *__restrict__ out, int32_t out_ld, int64_t plane, int vec, const Drop drop) {
   pdl_wait();
   constexpr int kU = 4, kB = 16 / (int)sizeof(T);
   const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (r >= rows) return;
+  const bool dropped = drop.row(r);
   const int groups = out_ld / 8;
   for (int g0 = threadIdx.x & 31; g0 < groups; g0 += 32 * kU) {
     float v[kU][8];
@@ -792,7 +804,10 @@ __global__ void __launch_bounds__(256) k_xent_pack(const T *__restrict__ in, int
     for (int u = 0; u < kU; ++u) {
       const int c = (g0 + 32 * u) * 8;
       const T *at = in + r * ld + c;
-      if (vec && c + 8 <= width) {
+      if (dropped) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[u][j] = 0.f;
+      } else if (vec && c + 8 <= width) {
 #pragma unroll
         for (int h = 0; h < 8 / kB; ++h) {
           Pack<T, 16> q;
@@ -1018,7 +1033,7 @@ XentWs xent_ws(const XentShape &s, bool grad) {
   return w;
 }
 
-// Whether a bf16 matrix can be read as it lies.  TMA asks for 16-byte aligned
+// Whether a bf16 matrix (w, and the forward's x) can be read as it lies.  TMA asks for 16-byte aligned
 // rows; off a 128-byte line every box row costs it one line more, and the
 // products run a fifth to a quarter slower (1999 x 50001 x 1000: gradient 499
 // against 402 us, forward 235 against 199 us), so large products lay it out
@@ -1037,7 +1052,7 @@ XentShape xent_shape(const void *x, int64_t x_ld, int32_t n, const void *wt, int
   s.vocab = vocab;
   s.t = t;
   s.parts = t == SNACK_F32 ? 3 : 1;
-  s.pack_x = t == SNACK_F32 || !rows_ready(x, x_ld, n, grad);
+  s.pack_x = grad || t == SNACK_F32 || !rows_ready(x, x_ld, n, grad);  // the gradient's leaves rows out
   s.pack_w = t == SNACK_F32 || !rows_ready(wt, w_ld, n, grad);
   s.ld = (int32_t)align_up((size_t)width, 64);
   s.sms = sms_of();
@@ -1083,19 +1098,19 @@ cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtens
   return e;
 }
 
-cudaError_t pack(const XentShape &s, const void *in, int64_t ld, int64_t rows, void *out, cudaStream_t st) {
+cudaError_t pack(const XentShape &s, const void *in, int64_t ld, int64_t rows, void *out, const Drop &drop, cudaStream_t st) {
   const int64_t blocks = ceil_div(rows, 8);
   const int vec = ptr_aligned(in, 16) && (size_t)ld * dtype_size(s.t) % 16 == 0;
   if (s.t == SNACK_F32)
     return launch_pdl(k_xent_pack<float>, (unsigned)blocks, 256, 0, st, reinterpret_cast<const float *>(in), ld, rows,
-                      s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld, vec);
+                      s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld, vec, drop);
   return launch_pdl(k_xent_pack<bf16>, (unsigned)blocks, 256, 0, st, reinterpret_cast<const bf16 *>(in), ld, rows,
-                    s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld, vec);
+                    s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld, vec, drop);
 }
 
 // x, or a piece of w from row v0 on, as the products read it
 cudaError_t operand(const XentShape &s, bool packed, const void *p, int64_t ld, int64_t v0, int64_t rows, void *buf,
-                    Operand *o, cudaStream_t st) {
+                    Operand *o, cudaStream_t st, const Drop &drop = Drop{}) {
   const size_t es = dtype_size(s.t);
   const uint8_t *at = reinterpret_cast<const uint8_t *>(p) + (size_t)v0 * (size_t)ld * es;
   o->rows = rows;
@@ -1111,7 +1126,7 @@ cudaError_t operand(const XentShape &s, bool packed, const void *p, int64_t ld, 
   o->ld = s.ld;
   o->planes = s.parts;
   o->plane = rows * s.ld;
-  return pack(s, at, ld, rows, buf, st);
+  return pack(s, at, ld, rows, buf, drop, st);
 }
 
 GemmArgs gemm_args(const XentShape &s, uint8_t *ws, const XentWs &W, int first) {
@@ -1241,7 +1256,9 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
   const bool wide = t == SNACK_F32;
   const uint32_t a_rows = n >= kMCta ? kMCta : (uint32_t)align_up((size_t)n, 8);
   Operand ox, ow;
-  XENT_CUDA(operand(S, S.pack_x, x, x_ld, 0, n, b + W.xp, &ox, s));
+  const TokenSrc tg{targets, targets_t == SNACK_I64, (uint32_t)vocab};
+  const float *weight = reduction == SNACK_NONE ? dloss : nullptr;
+  XENT_CUDA(operand(S, S.pack_x, x, x_ld, 0, n, b + W.xp, &ox, s, Drop{tg, weight}));
   CUtensorMap mx, mw, mxt, mwt, mdz, mdzt, mdz_out, macc, mdw;
   if (!load_map(&mx, ox, false, a_rows) || !load_map(&mxt, ox, true, 0)) return SNACK_ERR_CUDA;
   if (!make_map(&macc, b + W.acc, true, (uint64_t)width, (uint64_t)n, (uint64_t)W.acc_ld, (uint64_t)W.split,
@@ -1264,10 +1281,10 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
     g.n = (int32_t)rows;
     g.nt = nt;
     g.k_blocks = (int32_t)ceil_div(width, kKb);
-    g.targets = TokenSrc{targets, targets_t == SNACK_I64, (uint32_t)vocab};
+    g.targets = tg;
     g.v0 = (int32_t)v0;
     g.lse = state;
-    g.dloss = reduction == SNACK_NONE ? dloss : nullptr;
+    g.dloss = weight;
     g.out_parts = S.parts;
     XENT_CUDA(launch_gemm<kDlog>(mx, mw, mdz_out, g, S.sms, s));
     first = 0;

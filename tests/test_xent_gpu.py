@@ -194,6 +194,26 @@ def test_xent_not_finite_rows_stay_apart():
     assert torch.equal(dx, want)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_xent_rows_not_trained_on_may_hold_anything(dtype):
+    x, w, t = make(140, 600, 72, dtype, seed=21, ignored=0.2)
+    up = torch.rand(140, device="cuda") + 0.5
+    up[3], t[3] = 0.0, 17  # a weight of zero leaves a row out too
+    out = (t < 0) | (t >= 600)
+    out[3] = True
+    bad = x.clone()
+    bad[out] = torch.tensor([float("nan"), float("inf"), -float("inf")], device="cuda").repeat(24).to(x.dtype)
+    loss, state = snack.xent(x, w, t, reduction="none")
+    loss_bad, state_bad = snack.xent(bad, w, t, reduction="none")
+    keep = ~out
+    keep[3] = False
+    assert torch.equal(loss[keep], loss_bad[keep])
+    want = snack.xent_grad(x, w, t, state, up, reduction="none")
+    got = snack.xent_grad(bad, w, t, state_bad, up, reduction="none")
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    assert not got[0][out].any()
+
+
 def test_xent_in_pieces_of_the_vocabulary():
     """A workspace-bounded gradient: n * vocab large enough for several pieces of dz and of w's parts."""
     n, vocab, width = 8300, 40100, 64
