@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(kThreads) k_clip_norm(const __grid_constant__ 
   if (threadIdx.x == 0) sums[blockIdx.x] = b;
 }
 
-// The norm from all blocks' sums: one warp adds them in fp64 (which is slow here), the scaled sums only where they are needed.
+// The norm from all blocks' sums: one warp adds them in fp64 (which is slow
+// here), the scaled sums only where they are needed.
 __device__ __forceinline__ double warp_total(const float *p, int n_sums) {
   double m = 0;
   for (int i = threadIdx.x; i < n_sums; i += 32) m += (double)__ldg(p + 3 * i);

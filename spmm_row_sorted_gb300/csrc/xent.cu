@@ -19,19 +19,21 @@
 // Bound by the tensor cores; for a few tokens by reading w once.
 //
 // A pair of CTAs, one per SM, works through output tiles of 256 x up to 256,
-// 128 rows each: in each a warp loads its rows of A and its half of B by TMA
+// 128 rows each.  In each CTA a warp loads its rows of A and its half of B by TMA
 // into a ring of stages; one thread of the pair issues the tcgen05.mma, which
-// read both halves of B (a third fewer bytes from L2 than a tile per CTA, which
-// L2 held to 71 % of the tensor cores' cycles); in each eight warps run the epilogue of one tile from one half of the
-// tensor memory while the next one forms in the other.  Operands whose
-// rows run along K are K-major tiles (128-byte swizzle), the others (w for dx,
-// dz^T and x for dw) are read as they lie, as MN-major tiles: no transposes.
+// read both halves of B (a third fewer bytes from L2 than a tile per CTA: dx and
+// dw went from 1463 and 1509 to 1388 and 1362 us at 4096 x 131072 x 2048); and
+// eight warps run the epilogue of one accumulator from one half of the tensor
+// memory while the next one forms in the other.  Operands whose rows run along K
+// are K-major tiles (128-byte swizzle), the others (w for dx, dz^T and x for dw)
+// are read as they lie, as MN-major tiles: no transposes.
 //
 // The tensor core's fp32 accumulation rounds towards zero, which over a long K
-// is a bias: a sum of 4096 products came out 1e-5 of itself too small.  So an
-// accumulator takes 256 of K at a time (16 instructions) where that counts,
+// is a bias: a sum of 4096 products came out 5e-6 to 1.4e-5 of itself too small.
+// So an accumulator takes at most 512 of K (32 instructions) where that counts,
 // and the epilogue's warps add the partial sums in registers, rounding to
-// nearest, while the next one forms in the other half of the tensor memory.
+// nearest, while the next one forms in the other half of the tensor memory; the
+// logits' are multiplied by what the bias took on average (kLost).
 //
 // fp32 operands are cut into three bf16 parts each (8 significant bits at a
 // time, 24 in all), and a product is the sum of the six part products down to
@@ -42,8 +44,8 @@
 //
 // Every wait on an mbarrier is bounded; when one runs out the CTA marks its
 // error word, waits (bounded) for what it has in flight, frees its tensor
-// memory and returns, and the kernel that finishes a call makes the losses, dx and the first row
-// of dw NaN.
+// memory and returns, and the kernel that finishes a call makes the losses, dx
+// and the first row of dw NaN.
 #include <cuda.h>
 #include <math.h>
 
@@ -208,6 +210,12 @@ constexpr int kM = 256;           // rows of an output tile: 128 (the TMEM lanes
 constexpr int kMCta = kM / 2;
 constexpr int kNMax = 256;        // columns of the widest output tile
 constexpr int kKb = 64;           // K per stage
+// What an accumulation on the tensor core loses of the sum, on average, by
+// rounding towards zero: measured on GB300 for logits of random operands 1.4e-8
+// per instruction (16 of K), 1.7e-8 where the operands are aligned, 3.6e-8 where
+// every product is positive, 0.2e-8 where nine of ten are zero.  The logits'
+// partial sums are multiplied back by it.
+constexpr float kLost = 1.6e-8f;
 constexpr int kEpiWarps = 8;
 constexpr int kChunks = kNMax / 2 / 32;  // 32-column chunks of an epilogue warp's half tile
 constexpr int kThreads = (kEpiWarps + 4) * 32;  // and a warpgroup for the loads and the MMAs (two of its warps idle)
@@ -289,6 +297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   constexpr bool kAmn = kMode == kDw, kBmn = kMode == kDx || kMode == kDw;
+  constexpr bool kLogits = kMode == kStats || kMode == kDlog;
   const uint32_t rank = cta_rank();  // 0: the leader, which issues the pair's MMAs
   const int nb = P.nt / 2;           // rows of B in each CTA
   // With few rows a stage holds only those of A: the MMAs read 128 rows all the
@@ -476,8 +485,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
       // the tile's sums: one unit after the other, added in fp32
       float acc[kChunks][32];
       const int units = (q.nk + P.unit - 1) / P.unit + (P.products > 1 ? 1 : 0);
+      int left = q.nk;  // stages of the leading product not yet added
       for (int u = 0; u < units; ++u, ++n_acc) {
         const int buf = n_acc & 1;
+        const bool leading = P.products == 1 || u > 0;
+        const float back = kLogits && leading ? fmaf(kLost, 4.f * (float)min(P.unit, left), 1.f) : 1.f;
+        if (leading) left -= P.unit;
         if (!warp_wait(&acc_full[buf], (n_acc >> 1) & 1)) {
           ok = false;
           break;
@@ -498,7 +511,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
           tmem_wait();
           release();
 #pragma unroll
-          for (int h = 0; h < kChunks; ++h) tmem_ready(acc[h]);
+          for (int h = 0; h < kChunks; ++h) {
+            tmem_ready(acc[h]);
+            if (kLogits)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) acc[h][j] *= back;
+          }
         } else {
 #pragma unroll
           for (int h = 0; h < kChunks; h += 2) {
@@ -510,11 +528,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
             if (h + 2 >= chunks) release();
             tmem_ready(v[0]);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) acc[h][j] += v[0][j];
+            for (int j = 0; j < 32; ++j) acc[h][j] = kLogits ? fmaf(v[0][j], back, acc[h][j]) : acc[h][j] + v[0][j];
             if (h + 1 < chunks) {
               tmem_ready(v[1]);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) acc[h + 1][j] += v[1][j];
+              for (int j = 0; j < 32; ++j)
+                acc[h + 1][j] = kLogits ? fmaf(v[1][j], back, acc[h + 1][j]) : acc[h + 1][j] + v[1][j];
             }
           }
         }
@@ -824,24 +843,24 @@ __global__ void __launch_bounds__(256) k_xent_pack(const T *__restrict__ in, int
     for (int u = 0; u < kU; ++u) {
       const int c = (g0 + 32 * u) * 8;
       if (c >= out_ld) break;
-      if (sizeof(T) == 2) {  // bf16 is its own only part
+      if constexpr (sizeof(T) == 2) {  // bf16 is its own only part
         Pack<bf16, 16> o;
 #pragma unroll
         for (int j = 0; j < 8; ++j) o.h[j] = (uint16_t)(__float_as_uint(v[u][j]) >> 16);
         *reinterpret_cast<uint4 *>(out + r * out_ld + c) = o.raw;
-        continue;
-      }
-      for (int p = 0; p < parts; ++p) {
-        Pack<bf16, 16> o;
+      } else {
+        for (int p = 0; p < parts; ++p) {
+          Pack<bf16, 16> o;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float x = v[u][j];
-          float h = __bfloat162float(__float2bfloat16_rn(x));
-          if (isinf(h) && !isinf(x)) h = __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);  // rounded past the largest
-          o.set(j, h);
-          v[u][j] = isfinite(x) ? x - h : 0.f;
+          for (int j = 0; j < 8; ++j) {
+            const float x = v[u][j];
+            float h = __bfloat162float(__float2bfloat16_rn(x));
+            if (isinf(h) && !isinf(x)) h = __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);  // rounded past the largest
+            o.set(j, h);
+            v[u][j] = isfinite(x) ? x - h : 0.f;
+          }
+          *reinterpret_cast<uint4 *>(out + p * plane + r * out_ld + c) = o.raw;
         }
-        reinterpret_cast<uint4 *>(out + p * plane + r * out_ld + c)[0] = o.raw;
       }
     }
   }
@@ -1060,18 +1079,15 @@ XentShape xent_shape(const void *x, int64_t x_ld, int32_t n, const void *wt, int
 }
 
 // Units of K stages (64 each): see the note on rounding at the top.  Each unit
-// costs the tensor core about 450 cycles (the switch of accumulators, and the
-// epilogue's reads of tensor memory), of 512 a stage.  Sums that become the
-// loss or other fp32 results take short units, of equal length (shorter ones
-// for a short K, whose sums of few units are the further off); what is rounded
-// to bf16 (dz, dx and dw of bf16 operands) is far below half its ulp with long
-// ones.  Measured at 4096 x 131072 x 2048 bf16, against 64 bits: units of 4, 6,
-// 8 and 16 give a mean loss 5e-7, 8e-7, 1.1e-6 and 2.3e-6 off, and the forward
-// takes 1637, 1540, 1448 and 1380 us (1346 us without units).
-int unit_of(int k_blocks, bool exact) {
-  const int most = !exact ? 64 : k_blocks < 32 ? 4 : 5;
-  return (int)ceil_div(k_blocks, ceil_div(k_blocks, most));
-}
+// costs an exchange of accumulators and a read of 128 KB of tensor memory per
+// CTA (about 1900 cycles beside the MMAs, of 512 a stage).  Sums that become the
+// loss or other fp32 results take units of at most eight stages, of equal
+// length; what is rounded to bf16 (dz, dx and dw of bf16 operands) is far below
+// half its ulp with long ones.  Measured, forward and mean loss against 64 bits
+// (before the partial sums are corrected), for units of 4, 5, 6, 8, 16 and none:
+//   4096 x 131072 x 2048   1306 1253 1178 1112 1064 1058 us   5e-7 6e-7 8e-7 1.1e-6 2.3e-6 4.7e-6
+//   2048 x 65536 x 4096     669  623  582  556  543  539 us   6e-7 8e-7 9e-7 1.3e-6 2.8e-6 1.1e-5
+int unit_of(int k_blocks, bool exact) { return (int)ceil_div(k_blocks, ceil_div(k_blocks, exact ? 8 : 64)); }
 
 template <int kMode>
 cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o, GemmArgs &g, int sms,

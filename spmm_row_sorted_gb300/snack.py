@@ -608,7 +608,7 @@ def _xent_workspace(x, w, grad: int) -> torch.Tensor:
 
 def embed(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out: Optional[torch.Tensor] = None,
           stream=None) -> torch.Tensor:
-    """scale * table[ids]; zeros for an id outside the table.  ids of any shape; the result has that shape plus the width."""
+    """scale * table[ids], zeros for an id outside the table; ids of any shape, the result has that shape plus the width."""
     if _elsewhere(table, stream):
         with _On(table.device, stream):
             return embed(ids, table, scale, out)
@@ -685,7 +685,7 @@ def clip_grad_norm(grads, max_norm: float, out=None, stream=None) -> torch.Tenso
             raise ValueError("out must hold contiguous tensors of the gradients' types and sizes, on their device")
         to = list(map(T.data_ptr, outs))
     norm = torch.empty((), dtype=torch.float32, device=first.device)
-    types = [dtype_code(d) for d in dtypes] if len(grads) < 8 else list(map({d: dtype_code(d) for d in set(dtypes)}.get, dtypes))
+    types = list(map({d: dtype_code(d) for d in set(dtypes)}.get, dtypes))
     ws = _workspace(_clip_ws(len(grads)), first.device)
     snack_clip_grad_norm(addr, to, numel, types, float(max_norm), norm, ws)
     return norm
