@@ -16,7 +16,8 @@
 //   dx     adds dz w of the piece to fp32 sums (a TMA reduction: one addition
 //          per element and piece, in the pieces' order);
 //   dw     writes the piece's rows of dw.
-// Bound by the tensor cores; for a few tokens by reading w once.
+// Bound by the tensor cores; for a few tokens by reading w once (a few fp32
+// tokens: xent_small.cuh).
 //
 // A pair of CTAs, one per SM, works through output tiles of 256 x up to 256,
 // 128 rows each.  In each CTA a warp loads its rows of A and its half of B by TMA
@@ -37,7 +38,9 @@
 //
 // fp32 operands are cut into three bf16 parts each (8 significant bits at a
 // time, 24 in all), and a product is the sum of the six part products down to
-// 2^-16 of the leading one, smallest first; what is left out is below 2^-24.
+// 2^-16 of the leading one, the smaller ones summed apart; what is left out is
+// below 2^-24.  All six go over 512 of K before the next 512, so that the parts
+// of w that the SMs work on stay in L2.
 // The parts, and bf16 operands whose rows are not 16-byte aligned, are laid
 // out in the workspace, w's by pieces of the vocabulary; so is the gradient's x,
 // without the rows that are not trained on.
@@ -51,6 +54,7 @@
 
 #include "internal.hpp"
 #include "lm.hpp"
+#include "xent_small.cuh"
 
 namespace snack {
 namespace {
@@ -250,8 +254,8 @@ struct GemmArgs {
   int32_t k_blocks;         // of 64
   int32_t products;         // part products per element (1: bf16, 6: fp32)
   uint32_t a_part, b_part;  // 4 bits per product: its parts
-  int32_t unit;             // K stages of the leading part product summed on the tensor core before the sum moves
-                            // to registers (the smaller products before it are summed as one)
+  int32_t unit;             // K stages summed on the tensor core before the sums move to registers: of the smaller
+                            // part products together, then of the leading one
   int32_t stages;
   uint32_t *err;            // [256] error words, one per CTA
   int32_t first;            // the call's first launch writes every error word
@@ -372,34 +376,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
       for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
         const Tile q = tile_at(t);
         const int am = q.m0 + (int)rank * kMCta, bn = q.n0 + (int)rank * nb;
-        for (int c = 0; c < P.products && ok; ++c) {
-          const int za = (P.a_part >> (4 * c)) & 15, zb = (P.b_part >> (4 * c)) & 15;
-          for (int k = q.k0 * kKb; k < (q.k0 + q.nk) * kKb; k += kKb) {
-            if (!warp_wait(&empty[s], phase ^ 1)) {
-              ok = false;
-              break;
-            }
-            if (one) {
-              uint8_t *a = smem + (uint32_t)s * stage_bytes, *b = a + a_bytes;
-              const uint32_t bar = bar0 + 8u * s;
-              if (rank == 0) mbar_expect_tx(&full[s], 2 * stage_bytes);
-              if (kAmn) {
-                tma_load(a, &map_a, am, k, za, bar);
-                tma_load(a + 8192, &map_a, am + 64, k, za, bar);
-              } else {
-                tma_load(a, &map_a, k, am, za, bar);
+        for (int k0 = 0; k0 < q.nk && ok; k0 += P.unit) {
+          const int k1 = min(q.nk, k0 + P.unit);
+          for (int c = 0; c < P.products && ok; ++c) {
+            const int za = (P.a_part >> (4 * c)) & 15, zb = (P.b_part >> (4 * c)) & 15;
+            for (int k = (q.k0 + k0) * kKb; k < (q.k0 + k1) * kKb; k += kKb) {
+              if (!warp_wait(&empty[s], phase ^ 1)) {
+                ok = false;
+                break;
               }
-              if (kBmn) {
-                tma_load(b, &map_b, bn, k, zb, bar);
-                if (nb > 64) tma_load(b + 8192, &map_b, bn + 64, k, zb, bar);
-              } else {
-                tma_load(b, &map_b, k, bn, zb, bar);
+              if (one) {
+                uint8_t *a = smem + (uint32_t)s * stage_bytes, *b = a + a_bytes;
+                const uint32_t bar = bar0 + 8u * s;
+                if (rank == 0) mbar_expect_tx(&full[s], 2 * stage_bytes);
+                if (kAmn) {
+                  tma_load(a, &map_a, am, k, za, bar);
+                  tma_load(a + 8192, &map_a, am + 64, k, za, bar);
+                } else {
+                  tma_load(a, &map_a, k, am, za, bar);
+                }
+                if (kBmn) {
+                  tma_load(b, &map_b, bn, k, zb, bar);
+                  if (nb > 64) tma_load(b + 8192, &map_b, bn + 64, k, zb, bar);
+                } else {
+                  tma_load(b, &map_b, k, bn, zb, bar);
+                }
               }
-            }
-            __syncwarp();
-            if (++s == P.stages) {
-              s = 0;
-              phase ^= 1;
+              __syncwarp();
+              if (++s == P.stages) {
+                s = 0;
+                phase ^= 1;
+              }
             }
           }
         }
@@ -411,41 +418,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
       int n_acc = 0;
       for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
         const Tile q = tile_at(t);
-        const int steps = P.products * q.nk, lead = steps - q.nk;
+        const int steps = P.products * q.nk;
+        int i = 0;
         bool seen = false;  // the next stage's bytes are there
-        for (int i = 0; i < steps && ok; ++n_acc) {  // a unit of steps per accumulator
-          const int buf = n_acc & 1;
-          if (!warp_wait(&acc_free[buf], ((n_acc >> 1) & 1) ^ 1)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t d = tmem + (uint32_t)(buf * kNMax);
-          const int end = i < lead ? lead : min(steps, i + P.unit);
-          uint32_t more = 0;  // the unit's first MMA overwrites
-          for (; i < end; ++i) {
-            if (!__any_sync(0xffffffffu, seen) && !warp_wait(&full[s], phase)) {
+        for (int k0 = 0; k0 < q.nk && ok; k0 += P.unit) {
+          const int len = min(P.unit, q.nk - k0);
+          // the smaller part products (if any) in one accumulator, the leading one in the next
+          for (int unit = P.products > 1 ? 0 : 1; unit < 2 && ok; ++unit, ++n_acc) {
+            const int buf = n_acc & 1;
+            if (!warp_wait(&acc_free[buf], ((n_acc >> 1) & 1) ^ 1)) {
               ok = false;
               break;
             }
-            const uint32_t off = (uint32_t)s * (stage_bytes >> 4);
-            const int cur = s;
-            if (++s == P.stages) {
-              s = 0;
-              phase ^= 1;
-            }
-            seen = i + 1 < steps && mbar_try(&full[s], phase);  // answered while the MMAs below are issued
-            if (one) {
+            tc_fence_after();
+            const uint32_t d = tmem + (uint32_t)(buf * kNMax);
+            const int end = i + (unit ? len : (P.products - 1) * len);
+            uint32_t more = 0;  // the unit's first MMA overwrites
+            while (i < end) {
+              if (!__any_sync(0xffffffffu, seen) && !warp_wait(&full[s], phase)) {
+                ok = false;
+                break;
+              }
+              const uint32_t off = (uint32_t)s * (stage_bytes >> 4);
+              const int cur = s;
+              if (++s == P.stages) {
+                s = 0;
+                phase ^= 1;
+              }
+              seen = ++i < steps && mbar_try(&full[s], phase);  // answered while the MMAs below are issued
+              if (one) {
 #pragma unroll
-              for (int k = 0; k < kKb / 16; ++k)
-                umma(d, a_lo + off + k * kA16, b_lo + off + k * kB16, idesc, k == 0 ? more : 1u);
-              umma_commit(&empty[cur]);
+                for (int k = 0; k < kKb / 16; ++k)
+                  umma(d, a_lo + off + k * kA16, b_lo + off + k * kB16, idesc, k == 0 ? more : 1u);
+                umma_commit(&empty[cur]);
+              }
+              __syncwarp();
+              more = 1;
             }
+            if (ok && one) umma_commit(&acc_full[buf]);
             __syncwarp();
-            more = 1;
           }
-          if (ok && one) umma_commit(&acc_full[buf]);
-          __syncwarp();
         }
       }
       if (one) umma_commit(drained);
@@ -484,11 +496,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
       }
       // the tile's sums: one unit after the other, added in fp32
       float acc[kChunks][32];
-      const int units = (q.nk + P.unit - 1) / P.unit + (P.products > 1 ? 1 : 0);
+      const int units = (q.nk + P.unit - 1) / P.unit * (P.products > 1 ? 2 : 1);
       int left = q.nk;  // stages of the leading product not yet added
       for (int u = 0; u < units; ++u, ++n_acc) {
         const int buf = n_acc & 1;
-        const bool leading = P.products == 1 || u > 0;
+        const bool leading = P.products == 1 || (u & 1);
         const float back = kLogits && leading ? fmaf(kLost, 4.f * (float)min(P.unit, left), 1.f) : 1.f;
         if (leading) left -= P.unit;
         if (!warp_wait(&acc_full[buf], (n_acc >> 1) & 1)) {
@@ -712,6 +724,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
 }
 
 __device__ __forceinline__ bool any_error(const uint32_t *err) {
+  if (!err) return false;  // no product ran on the tensor cores
   uint32_t e = 0;
   for (int i = threadIdx.x; i < 256; i += blockDim.x) e |= err[i];
   return __syncthreads_or((int)e) != 0;
@@ -998,6 +1011,7 @@ struct XentShape {
   int64_t vocab;
   snack_dtype t;
   bool pack_x, pack_w;
+  bool few;    // the CUDA-core path of a few fp32 tokens
   int parts;
   int32_t ld;  // row length of packed planes
   int sms;
@@ -1011,6 +1025,8 @@ struct XentWs {
   int64_t dz_ld;
   int32_t acc_ld;
   int nt_d, split;    // dx, dw tile columns; K splits of dx
+  int few_nt;         // few tokens: the number that the kernels are built for
+  int64_t few_blocks, few_rows;  // blocks of the logits; vocabulary rows per split of dx
 };
 
 XentWs xent_ws(const XentShape &s, bool grad) {
@@ -1019,6 +1035,33 @@ XentWs xent_ws(const XentShape &s, bool grad) {
   const int64_t m_tiles = ceil_div(s.n, kM);
   w.err = o;
   o += align_up(256 * 4, kAlign);
+  if (s.few) {
+    w.few_nt = s.n <= 4 ? 4 : s.n <= 8 ? 8 : s.n <= 16 ? 16 : 32;
+    const int64_t tiles = ceil_div(s.vocab, (int64_t)kSmallWarps * small_rows(w.few_nt));
+    w.few_blocks = tiles < 2 * s.sms ? tiles : 2 * s.sms;
+    w.slots = w.few_blocks;
+    if (!grad) {
+      w.zt = o;
+      o += align_up((size_t)s.n * 4, kAlign);
+      w.row_loss = o;
+      o += align_up((size_t)s.n * 4, kAlign);
+      w.part = o;
+      o += align_up((size_t)w.slots * (size_t)s.n * 8, kAlign);
+    } else {
+      const int64_t groups = ceil_div(s.width, 128);
+      int64_t splits = ceil_div(4 * (int64_t)s.sms, groups);
+      if (splits > ceil_div(s.vocab, 64)) splits = ceil_div(s.vocab, 64);
+      w.few_rows = ceil_div(s.vocab, splits);
+      w.split = (int)ceil_div(s.vocab, w.few_rows);
+      w.acc_ld = (int32_t)align_up((size_t)s.width, 4);
+      w.dz = o;
+      o += align_up((size_t)s.vocab * (size_t)w.few_nt * 4, kAlign);
+      w.acc = o;
+      o += align_up((size_t)w.split * (size_t)s.n * (size_t)w.acc_ld * 4, kAlign);
+    }
+    w.total = o;
+    return w;
+  }
   const int64_t w_row = (int64_t)s.parts * s.ld * 2;
   w.nt = tile_cols(m_tiles, s.vocab, s.sms);
   w.xp = o;
@@ -1073,6 +1116,7 @@ XentShape xent_shape(const void *x, int64_t x_ld, int32_t n, const void *wt, int
   s.parts = t == SNACK_F32 ? 3 : 1;
   s.pack_x = grad || t == SNACK_F32 || !rows_ready(x, x_ld, n, grad);  // the gradient's leaves rows out
   s.pack_w = t == SNACK_F32 || !rows_ready(wt, w_ld, n, grad);
+  s.few = t == SNACK_F32 && n <= kSmallMostTokens;
   s.ld = (int32_t)align_up((size_t)width, 64);
   s.sms = sms_of();
   return s;
@@ -1156,6 +1200,59 @@ GemmArgs gemm_args(const XentShape &s, uint8_t *ws, const XentWs &W, int first) 
   return g;
 }
 
+cudaError_t finish_loss(const float2 *part, int slots, int32_t n, const float *zt, const TokenSrc &tg,
+                        snack_reduction reduction, float *row_loss, float *loss, float *state, const uint32_t *err,
+                        cudaStream_t s) {
+  cudaError_t e = launch_pdl(k_xent_join, (unsigned)ceil_div(n, 8), 256, 0, s, part, slots, n, zt, tg, row_loss, state, err);
+  if (e != cudaSuccess || reduction == SNACK_NONE) return e;
+  return launch_pdl(k_xent_total, 1, 1024, 0, s, (const float *)row_loss, n, tg, reduction == SNACK_MEAN, loss, state);
+}
+
+template <int kNt, bool kGrad>
+cudaError_t launch_few(const SmallArgs &a, int64_t blocks, cudaStream_t s) {
+  constexpr size_t smem = (size_t)(kNt * kSmallK + kSmallWarps * small_rows(kNt) * (kNt + 1)) * 4;
+  cudaError_t e = raise_smem_limit(k_xent_few<kNt, kGrad>, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_xent_few<kNt, kGrad>, (unsigned)blocks, kSmallWarps * 32, smem, s, a);
+}
+template <bool kGrad>
+cudaError_t run_few(const SmallArgs &a, const XentWs &W, cudaStream_t s) {
+  switch (W.few_nt) {
+    case 4:
+      return launch_few<4, kGrad>(a, W.few_blocks, s);
+    case 8:
+      return launch_few<8, kGrad>(a, W.few_blocks, s);
+    case 16:
+      return launch_few<16, kGrad>(a, W.few_blocks, s);
+    default:
+      return launch_few<32, kGrad>(a, W.few_blocks, s);
+  }
+}
+
+template <int kNt>
+cudaError_t launch_few_grad(const SmallGrad &a, dim3 grid, bool dx, bool dw, cudaStream_t s) {
+  if (dx && dw && kNt <= 16)  // both read dz and walk the rows of w and dw alike
+    return launch_pdl(k_xent_few_grad<kNt, true, (kNt <= 16)>, grid, kSmallWarps * 32, 0, s, a);
+  cudaError_t e = cudaSuccess;
+  if (dx) e = launch_pdl(k_xent_few_grad<kNt, true, false>, grid, kSmallWarps * 32, 0, s, a);
+  if (dw && e == cudaSuccess) e = launch_pdl(k_xent_few_grad<kNt, false, true>, grid, kSmallWarps * 32, 0, s, a);
+  return e;
+}
+
+SmallArgs small_args(const XentShape &S, const void *x, int64_t x_ld, const void *w, int64_t w_ld, const TokenSrc &tg) {
+  SmallArgs a = {};
+  a.x = reinterpret_cast<const float *>(x);
+  a.w = reinterpret_cast<const float *>(w);
+  a.x_ld = x_ld;
+  a.w_ld = w_ld;
+  a.n = S.n;
+  a.width = S.width;
+  a.vocab = S.vocab;
+  a.w_wide = ptr_aligned(w, 16) && w_ld % 4 == 0;
+  a.targets = tg;
+  return a;
+}
+
 snack_status xent_check(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld, int64_t vocab, int32_t width,
                         snack_dtype t) {
   if (!lm_dtype_ok(t) || n < 0 || vocab < 1 || width < 1 || x_ld < width || w_ld < width) return SNACK_ERR_INVALID_ARG;
@@ -1210,6 +1307,17 @@ snack_status snack_xent_fwd(const void *x, int64_t x_ld, int32_t n, const void *
   const XentWs W = xent_ws(S, false);
   if (ws_bytes < W.total) return SNACK_ERR_WORKSPACE;
   uint8_t *b = reinterpret_cast<uint8_t *>(ws);
+  float *zt = reinterpret_cast<float *>(b + W.zt);
+  float2 *part = reinterpret_cast<float2 *>(b + W.part);
+  float *row_loss = reduction == SNACK_NONE ? loss : reinterpret_cast<float *>(b + W.row_loss);
+  if (S.few) {
+    SmallArgs a = small_args(S, x, x_ld, w, w_ld, tg);
+    a.part = part;
+    a.zt = zt;
+    XENT_CUDA(run_few<false>(a, W, s));
+    XENT_CUDA(finish_loss(part, (int)W.slots, n, zt, tg, reduction, row_loss, loss, state, nullptr, s));
+    return SNACK_OK;
+  }
   const uint32_t a_rows = n >= kMCta ? kMCta : (uint32_t)align_up((size_t)n, 8);
   Operand ox, ow;
   XENT_CUDA(operand(S, S.pack_x, x, x_ld, 0, n, b + W.xp, &ox, s));
@@ -1219,8 +1327,8 @@ snack_status snack_xent_fwd(const void *x, int64_t x_ld, int32_t n, const void *
   g.m = n;
   g.nt = W.nt;
   g.k_blocks = (int32_t)ceil_div(width, kKb);
-  g.part = reinterpret_cast<float2 *>(b + W.part);
-  g.zt = reinterpret_cast<float *>(b + W.zt);
+  g.part = part;
+  g.zt = zt;
   g.targets = tg;
   for (int64_t v0 = 0; v0 < vocab; v0 += W.piece) {
     const int64_t rows = vocab - v0 < W.piece ? vocab - v0 : W.piece;
@@ -1231,11 +1339,7 @@ snack_status snack_xent_fwd(const void *x, int64_t x_ld, int32_t n, const void *
     XENT_CUDA(launch_gemm<kStats>(mx, mw, mx, g, S.sms, s));
     g.slot0 += 2 * g.n_tiles;
   }
-  float *row_loss = reduction == SNACK_NONE ? loss : reinterpret_cast<float *>(b + W.row_loss);
-  XENT_CUDA(launch_pdl(k_xent_join, (unsigned)ceil_div(n, 8), 256, 0, s, (const float2 *)g.part, g.slot0, n,
-                       (const float *)g.zt, tg, row_loss, state, (const uint32_t *)g.err));
-  if (reduction != SNACK_NONE)
-    XENT_CUDA(launch_pdl(k_xent_total, 1, 1024, 0, s, (const float *)row_loss, n, tg, reduction == SNACK_MEAN, loss, state));
+  XENT_CUDA(finish_loss(part, g.slot0, n, zt, tg, reduction, row_loss, loss, state, g.err, s));
   return SNACK_OK;
 } catch (...) {  // a host allocation failed
   return SNACK_ERR_CUDA;
@@ -1270,17 +1374,54 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
   if (!dx && !dw) return SNACK_OK;
   uint8_t *b = reinterpret_cast<uint8_t *>(ws);
   const bool wide = t == SNACK_F32;
-  const uint32_t a_rows = n >= kMCta ? kMCta : (uint32_t)align_up((size_t)n, 8);
-  Operand ox, ow;
   const TokenSrc tg{targets, targets_t == SNACK_I64, (uint32_t)vocab};
   const float *weight = reduction == SNACK_NONE ? dloss : nullptr;
+  const Factor factor = {reduction == SNACK_NONE ? nullptr : dloss, reduction == SNACK_MEAN ? state + n : nullptr};
+  if (S.few) {
+    SmallArgs a = small_args(S, x, x_ld, w, w_ld, tg);
+    a.lse = state;
+    a.weight = weight;
+    a.dz = reinterpret_cast<float *>(b + W.dz);
+    XENT_CUDA(run_few<true>(a, W, s));
+    SmallGrad g = {};
+    g.x = a.x;
+    g.w = a.w;
+    g.dz = a.dz;
+    g.x_ld = x_ld;
+    g.w_ld = w_ld;
+    g.dw_ld = dw_ld;
+    g.n = n;
+    g.width = width;
+    g.vocab = vocab;
+    g.rows_per_split = W.few_rows;
+    g.w_wide = a.w_wide;
+    g.dw_wide = ptr_aligned(dw, 16) && dw_ld % 4 == 0;
+    g.targets = tg;
+    g.weight = weight;
+    g.factor_a = factor.a;
+    g.factor_b = factor.b;
+    g.acc = reinterpret_cast<float *>(b + W.acc);
+    g.acc_ld = W.acc_ld;
+    g.dw = reinterpret_cast<float *>(dw);
+    const dim3 grid((unsigned)ceil_div(width, 128), (unsigned)W.split);
+    XENT_CUDA(W.few_nt == 4    ? launch_few_grad<4>(g, grid, dx, dw, s)
+              : W.few_nt == 8  ? launch_few_grad<8>(g, grid, dx, dw, s)
+              : W.few_nt == 16 ? launch_few_grad<16>(g, grid, dx, dw, s)
+                               : launch_few_grad<32>(g, grid, dx, dw, s));
+    if (dx)
+      XENT_CUDA(launch_pdl(k_xent_dx<float>, (unsigned)ceil_div((int64_t)n * (W.acc_ld / 4), 256), 256, 0, s,
+                           (const float *)g.acc, W.split, (int64_t)n * W.acc_ld, W.acc_ld, n, width,
+                           reinterpret_cast<float *>(dx), dx_ld, (float *)nullptr, factor, (const uint32_t *)nullptr));
+    return SNACK_OK;
+  }
+  const uint32_t a_rows = n >= kMCta ? kMCta : (uint32_t)align_up((size_t)n, 8);
+  Operand ox, ow;
   XENT_CUDA(operand(S, S.pack_x, x, x_ld, 0, n, b + W.xp, &ox, s, Drop{tg, weight}));
   CUtensorMap mx, mw, mxt, mwt, mdz, mdzt, mdz_out, macc, mdw;
   if (!load_map(&mx, ox, false, a_rows) || !load_map(&mxt, ox, true, 0)) return SNACK_ERR_CUDA;
   if (!make_map(&macc, b + W.acc, true, (uint64_t)width, (uint64_t)n, (uint64_t)W.acc_ld, (uint64_t)W.split,
                 (uint64_t)n * (uint64_t)W.acc_ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B))
     return SNACK_ERR_CUDA;
-  const Factor factor = {reduction == SNACK_NONE ? nullptr : dloss, reduction == SNACK_MEAN ? state + n : nullptr};
   int first = 1;
   for (int64_t v0 = 0; v0 < vocab; v0 += W.piece) {
     const int64_t rows = vocab - v0 < W.piece ? vocab - v0 : W.piece;

@@ -301,3 +301,26 @@ def test_xent_refusals():
     with pytest.raises(snack.SnackError) as e:
         snack.snack_xent_fwd(x, w, t, 7, loss, state, ws)
     assert e.value.status == 1
+
+
+@pytest.mark.parametrize("reduction", ["none", "mean"])
+@pytest.mark.parametrize("n,vocab,width,gap,lead", [
+    (1, 700, 513, 0, 0), (4, 64, 700, 0, 0), (5, 2100, 1100, 0, 0), (8, 129, 2050, 2, 2), (9, 1000, 128, 4, 0),
+    (16, 333, 515, 0, 1), (17, 4097, 260, 0, 0), (32, 1000, 1030, 0, 0), (32, 65, 512, 0, 0),
+])
+def test_xent_few_fp32_tokens(n, vocab, width, gap, lead, reduction):
+    x, w, t = make(n, vocab, width, "f32", seed=n * vocab, gap=gap, lead=lead, ignored=0.2 if n > 2 else 0.0)
+    inside = ((t >= 0) & (t < vocab)).cpu().numpy()
+    up = np.random.default_rng(n).normal(size=n).astype(np.float32)
+    g = up.astype(np.float64) if reduction == "none" else np.full(n, 0.7 / max(1, inside.sum()))
+    dloss = torch.from_numpy(up).cuda() if reduction == "none" else torch.tensor(0.7, device="cuda")
+    r = reference(x, w, t, g)
+    check_loss(snack.xent(x, w, t, reduction="none")[0], r)
+    loss, state = snack.xent(x, w, t, reduction=reduction)
+    dx, dw = snack.xent_grad(x, w, t, state, dloss, reduction=reduction)
+    check_grads(dx, dw, r, "f32")
+    only_x, _ = snack.xent_grad(x, w, t, state, dloss, reduction=reduction, want_dw=False)
+    _, only_w = snack.xent_grad(x, w, t, state, dloss, reduction=reduction, want_dx=False)
+    check_grads(only_x, only_w, r, "f32")
+    again = snack.xent_grad(x, w, t, state, dloss, reduction=reduction)
+    assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
