@@ -1036,9 +1036,9 @@ XentWs xent_ws(const XentShape &s, bool grad) {
   w.err = o;
   o += align_up(256 * 4, kAlign);
   if (s.few) {
-    w.few_nt = s.n <= 4 ? 4 : s.n <= 8 ? 8 : s.n <= 16 ? 16 : 32;
+    w.few_nt = s.n <= 4 ? 4 : s.n <= 8 ? 8 : 16;
     const int64_t tiles = ceil_div(s.vocab, (int64_t)kSmallWarps * small_rows(w.few_nt));
-    w.few_blocks = tiles < 2 * s.sms ? tiles : 2 * s.sms;
+    w.few_blocks = tiles < s.sms ? tiles : s.sms;
     w.slots = w.few_blocks;
     if (!grad) {
       w.zt = o;
@@ -1048,7 +1048,7 @@ XentWs xent_ws(const XentShape &s, bool grad) {
       w.part = o;
       o += align_up((size_t)w.slots * (size_t)s.n * 8, kAlign);
     } else {
-      const int64_t groups = ceil_div(s.width, 128);
+      const int64_t groups = ceil_div(s.width, 32 * few_cols(w.few_nt));
       int64_t splits = ceil_div(4 * (int64_t)s.sms, groups);
       if (splits > ceil_div(s.vocab, 64)) splits = ceil_div(s.vocab, 64);
       w.few_rows = ceil_div(s.vocab, splits);
@@ -1210,33 +1210,24 @@ cudaError_t finish_loss(const float2 *part, int slots, int32_t n, const float *z
 
 template <int kNt, bool kGrad>
 cudaError_t launch_few(const SmallArgs &a, int64_t blocks, cudaStream_t s) {
-  constexpr size_t smem = (size_t)(kNt * kSmallK + kSmallWarps * small_rows(kNt) * (kNt + 1)) * 4;
+  const size_t smem = (size_t)(kNt * a.chunk + kSmallWarps * small_rows(kNt) * (kNt + 1)) * 4;
   cudaError_t e = raise_smem_limit(k_xent_few<kNt, kGrad>, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_xent_few<kNt, kGrad>, (unsigned)blocks, kSmallWarps * 32, smem, s, a);
 }
 template <bool kGrad>
 cudaError_t run_few(const SmallArgs &a, const XentWs &W, cudaStream_t s) {
-  switch (W.few_nt) {
-    case 4:
-      return launch_few<4, kGrad>(a, W.few_blocks, s);
-    case 8:
-      return launch_few<8, kGrad>(a, W.few_blocks, s);
-    case 16:
-      return launch_few<16, kGrad>(a, W.few_blocks, s);
-    default:
-      return launch_few<32, kGrad>(a, W.few_blocks, s);
-  }
+  return W.few_nt == 4   ? launch_few<4, kGrad>(a, W.few_blocks, s)
+         : W.few_nt == 8 ? launch_few<8, kGrad>(a, W.few_blocks, s)
+                         : launch_few<16, kGrad>(a, W.few_blocks, s);
 }
 
 template <int kNt>
 cudaError_t launch_few_grad(const SmallGrad &a, dim3 grid, bool dx, bool dw, cudaStream_t s) {
-  if (dx && dw && kNt <= 16)  // both read dz and walk the rows of w and dw alike
-    return launch_pdl(k_xent_few_grad<kNt, true, (kNt <= 16)>, grid, kSmallWarps * 32, 0, s, a);
-  cudaError_t e = cudaSuccess;
-  if (dx) e = launch_pdl(k_xent_few_grad<kNt, true, false>, grid, kSmallWarps * 32, 0, s, a);
-  if (dw && e == cudaSuccess) e = launch_pdl(k_xent_few_grad<kNt, false, true>, grid, kSmallWarps * 32, 0, s, a);
-  return e;
+  auto kernel = dx && dw ? k_xent_few_grad<kNt, true, true>
+                : dx     ? k_xent_few_grad<kNt, true, false>
+                         : k_xent_few_grad<kNt, false, true>;
+  return launch_pdl(kernel, grid, kFewWarps * 32, 0, s, a);
 }
 
 SmallArgs small_args(const XentShape &S, const void *x, int64_t x_ld, const void *w, int64_t w_ld, const TokenSrc &tg) {
@@ -1248,7 +1239,9 @@ SmallArgs small_args(const XentShape &S, const void *x, int64_t x_ld, const void
   a.n = S.n;
   a.width = S.width;
   a.vocab = S.vocab;
+  a.x_wide = ptr_aligned(x, 16) && x_ld % 4 == 0;
   a.w_wide = ptr_aligned(w, 16) && w_ld % 4 == 0;
+  a.chunk = small_k(S.n <= 4 ? 4 : S.n <= 8 ? 8 : 16, S.width);
   a.targets = tg;
   return a;
 }
@@ -1403,11 +1396,10 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
     g.acc = reinterpret_cast<float *>(b + W.acc);
     g.acc_ld = W.acc_ld;
     g.dw = reinterpret_cast<float *>(dw);
-    const dim3 grid((unsigned)ceil_div(width, 128), (unsigned)W.split);
-    XENT_CUDA(W.few_nt == 4    ? launch_few_grad<4>(g, grid, dx, dw, s)
-              : W.few_nt == 8  ? launch_few_grad<8>(g, grid, dx, dw, s)
-              : W.few_nt == 16 ? launch_few_grad<16>(g, grid, dx, dw, s)
-                               : launch_few_grad<32>(g, grid, dx, dw, s));
+    const dim3 grid((unsigned)ceil_div(width, 32 * few_cols(W.few_nt)), (unsigned)W.split);
+    XENT_CUDA(W.few_nt == 4   ? launch_few_grad<4>(g, grid, dx, dw, s)
+              : W.few_nt == 8 ? launch_few_grad<8>(g, grid, dx, dw, s)
+                              : launch_few_grad<16>(g, grid, dx, dw, s));
     if (dx)
       XENT_CUDA(launch_pdl(k_xent_dx<float>, (unsigned)ceil_div((int64_t)n * (W.acc_ld / 4), 256), 256, 0, s,
                            (const float *)g.acc, W.split, (int64_t)n * W.acc_ld, W.acc_ld, n, width,

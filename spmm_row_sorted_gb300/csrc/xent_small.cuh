@@ -2,7 +2,7 @@
 // cores, reading w as it lies.  The tensor cores would need w cut into bf16
 // parts first, 10 bytes moved per element to save arithmetic that a few tokens
 // do not have; here every pass reads the 4 bytes once (bound by memory up to
-// about 16 tokens, by fp32 arithmetic from there on).  Included by xent.cu.
+// about 8 tokens, by fp32 arithmetic from there on).  Included by xent.cu.
 #pragma once
 
 #include "lm.hpp"
@@ -10,13 +10,19 @@
 namespace snack {
 namespace {
 
-constexpr int kSmallMostTokens = 32;
-constexpr int kSmallWarps = 8;
-constexpr int kSmallK = 512;  // of the width in shared memory at a time
+constexpr int kSmallMostTokens = 16;
+constexpr int kSmallWarps = 16;
+constexpr int kSmallXBytes = 192 * 1024;  // of x in shared memory
 
 // tokens a kernel is built for, and the rows of w a warp works on at once: their
 // sums stay in registers
-__host__ __device__ constexpr int small_rows(int nt) { return nt <= 8 ? 8 : 4; }
+__host__ __device__ constexpr int small_rows(int nt) { return nt <= 4 ? 8 : 4; }
+// of the width in shared memory at a time: all of it up to 12288, 6144 or 3072
+// for 4, 8 or 16 tokens
+inline int small_k(int nt, int32_t width) {
+  const int most = kSmallXBytes / 4 / nt / 128 * 128, all = (width + 127) / 128 * 128;
+  return all < most ? all : most;
+}
 
 // Four consecutive elements; zeros from `left` on.  `wide`: 16-byte aligned rows.
 __device__ __forceinline__ float4 load4(const float *p, int left, bool wide) {
@@ -34,7 +40,8 @@ struct SmallArgs {
   int64_t x_ld, w_ld;
   int32_t n, width;
   int64_t vocab;
-  int w_wide;
+  int32_t chunk;  // of the width in shared memory at a time
+  int x_wide, w_wide;
   TokenSrc targets;
   // loss
   float2 *part;  // [blocks][n] (maximum, sum of exp(z - maximum))
@@ -49,12 +56,12 @@ struct SmallArgs {
 // from shared memory, one read for all the rows), and the lanes' sums are added
 // at the end.  kGrad: dz instead of the loss's statistics.
 template <int kNt, bool kGrad>
-__global__ void __launch_bounds__(kSmallWarps * 32) k_xent_few(const SmallArgs a) {
+__global__ void __launch_bounds__(kSmallWarps * 32, 1) k_xent_few(const SmallArgs a) {
   pdl_wait();
   constexpr int kR = small_rows(kNt), kTile = kSmallWarps * kR;
   extern __shared__ __align__(16) float few_smem[];
-  float *xs = few_smem;                   // [kNt][kSmallK]
-  float *zs = few_smem + kNt * kSmallK;   // [kTile][kNt + 1]
+  float *xs = few_smem;                   // [kNt][chunk]
+  float *zs = few_smem + kNt * a.chunk;   // [kTile][kNt + 1]
   __shared__ float run_max[kNt], run_sum[kNt];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x < kNt) {
@@ -69,19 +76,18 @@ __global__ void __launch_bounds__(kSmallWarps * 32) k_xent_few(const SmallArgs a
     for (int r = 0; r < kR; ++r)
 #pragma unroll
       for (int t = 0; t < kNt; ++t) acc[r][t] = 0.f;
-    for (int k0 = 0; k0 < a.width; k0 += kSmallK) {
-      if (k0 > 0 || tile == (int64_t)blockIdx.x || a.width > kSmallK) {  // one chunk stays for all tiles
+    for (int k0 = 0; k0 < a.width; k0 += a.chunk) {
+      if (tile == (int64_t)blockIdx.x || a.width > a.chunk) {  // a single chunk stays for all tiles
         __syncthreads();
-        for (int i = threadIdx.x * 4; i < kNt * kSmallK; i += kSmallWarps * 32 * 4) {
-          const int t = i / kSmallK, k = i % kSmallK;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (t < a.n) v = load4(a.x + t * a.x_ld + k0 + k, a.width - k0 - k, false);
-          *reinterpret_cast<float4 *>(xs + i) = v;
-        }
+#pragma unroll
+        for (int t = 0; t < kNt; ++t)
+          for (int k = threadIdx.x * 4; k < a.chunk; k += kSmallWarps * 32 * 4)
+            *reinterpret_cast<float4 *>(xs + t * a.chunk + k) =
+                t < a.n ? load4(a.x + t * a.x_ld + k0 + k, a.width - k0 - k, a.x_wide) : make_float4(0.f, 0.f, 0.f, 0.f);
         __syncthreads();
       }
 #pragma unroll 2
-      for (int k = lane * 4; k < kSmallK; k += 128) {
+      for (int k = lane * 4; k < a.chunk; k += 128) {
         const int left = a.width - k0 - k;
         if (left <= 0) break;
         float4 w[kR];
@@ -90,7 +96,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32) k_xent_few(const SmallArgs a
           w[r] = v0 + r < a.vocab ? load4(a.w + (v0 + r) * a.w_ld + k0 + k, left, a.w_wide) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int t = 0; t < kNt; ++t) {
-          const float4 x = *reinterpret_cast<const float4 *>(xs + t * kSmallK + k);
+          const float4 x = *reinterpret_cast<const float4 *>(xs + t * a.chunk + k);
 #pragma unroll
           for (int r = 0; r < kR; ++r)
             acc[r][t] = fmaf(w[r].x, x.x, fmaf(w[r].y, x.y, fmaf(w[r].z, x.z, fmaf(w[r].w, x.w, acc[r][t]))));
@@ -165,78 +171,108 @@ struct SmallGrad {
   float *dw;
 };
 
-// 128 columns per block; its warps take every 8th row of a range of the
-// vocabulary.  A lane holds four columns of all tokens: their sums of dx, and x
-// for dw.  The warps' sums of dx meet in shared memory.
+// A lane holds kC columns of all tokens: their sums of dx, and x for dw.  A
+// block's warps share 32 kC columns and a range of the vocabulary, whose dz lies
+// in shared memory 128 rows at a time (every lane reads the same words); their
+// sums of dx meet in shared memory at the end.
+constexpr int kFewWarps = 8;
+constexpr int kFewRows = 128;
+__host__ __device__ constexpr int few_cols(int nt) { return nt <= 8 ? 4 : 2; }
+
+template <int kC>
+struct Cols {
+  float v[kC];
+  __device__ __forceinline__ void load(const float *p, int left, bool wide) {
+    if (left >= kC && wide) {
+      if constexpr (kC == 4) {
+        const float4 q = __ldg(reinterpret_cast<const float4 *>(p));
+        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+      } else {
+        const float2 q = __ldg(reinterpret_cast<const float2 *>(p));
+        v[0] = q.x, v[1] = q.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kC; ++i) v[i] = i < left ? __ldg(p + i) : 0.f;
+    }
+  }
+  __device__ __forceinline__ void store(float *p, int left, bool wide) const {
+    if (left >= kC && wide) {
+      if constexpr (kC == 4)
+        __stcs(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
+      else
+        __stcs(reinterpret_cast<float2 *>(p), make_float2(v[0], v[1]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kC; ++i)
+        if (i < left) p[i] = v[i];
+    }
+  }
+};
+
 template <int kNt, bool kDxOut, bool kDwOut>
-__global__ void __launch_bounds__(kSmallWarps * 32) k_xent_few_grad(const SmallGrad a) {
+__global__ void __launch_bounds__(kFewWarps * 32) k_xent_few_grad(const SmallGrad a) {
   pdl_wait();
-  __shared__ float4 sum[kDxOut ? kSmallWarps : 1][32];
+  constexpr int kC = few_cols(kNt), kU = 4;  // rows in flight per warp
+  __shared__ __align__(16) float dzs[kFewRows * kNt];
+  __shared__ float sum[kDxOut ? kFewWarps : 1][32 * kC];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 128 + lane * 4, left = a.width - c;
-  float4 acc[kDxOut ? kNt : 1], x[kDwOut ? kNt : 1];
+  const int c = (blockIdx.x * 32 + lane) * kC, left = a.width - c;
+  float acc[kDxOut ? kNt : 1][kC];
+  Cols<kC> x[kDwOut ? kNt : 1];
   if (kDxOut)
 #pragma unroll
-    for (int t = 0; t < kNt; ++t) acc[kDxOut ? t : 0] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int t = 0; t < kNt; ++t)
+#pragma unroll
+      for (int i = 0; i < kC; ++i) acc[kDxOut ? t : 0][i] = 0.f;
   if (kDwOut) {
     const float f = (a.factor_a ? *a.factor_a : 1.f) * (a.factor_b ? *a.factor_b : 1.f);
 #pragma unroll
     for (int t = 0; t < kNt; ++t) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      Cols<kC> &v = x[kDwOut ? t : 0];
       // rows that are left out add nothing, whatever they hold
-      if (t < a.n && a.targets.key(t) < a.targets.vocab && !(a.weight && a.weight[t] == 0.f))
-        v = load4(a.x + t * a.x_ld + c, left, false);
-      x[kDwOut ? t : 0] = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+      const bool in = t < a.n && a.targets.key(t) < a.targets.vocab && !(a.weight && a.weight[t] == 0.f);
+      v.load(a.x + (in ? t : 0) * a.x_ld + c, in ? left : 0, false);
+#pragma unroll
+      for (int i = 0; i < kC; ++i) v.v[i] *= f;
     }
   }
   const int64_t r0 = (int64_t)blockIdx.y * a.rows_per_split;
   const int64_t r1 = r0 + a.rows_per_split < a.vocab ? r0 + a.rows_per_split : a.vocab;
-  constexpr int kU = kNt <= 8 ? 4 : 2;  // rows in flight
-  for (int64_t v0 = r0 + warp; v0 < r1; v0 += kU * kSmallWarps) {
-    float4 w[kU];
-    float4 d[kU][kNt / 4];
+  for (int64_t b = r0; b < r1; b += kFewRows) {
+    const int rows = (int)(r1 - b < kFewRows ? r1 - b : kFewRows);
+    __syncthreads();
+    for (int i = threadIdx.x * 4; i < rows * kNt; i += kFewWarps * 32 * 4)
+      *reinterpret_cast<float4 *>(dzs + i) = __ldg(reinterpret_cast<const float4 *>(a.dz + b * kNt + i));
+    __syncthreads();
+    for (int q = warp; q < rows; q += kU * kFewWarps) {
+      Cols<kC> w[kU];
+      if (kDxOut)
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int64_t v = v0 + u * kSmallWarps;
-      if (kDxOut) w[u] = v < r1 ? load4(a.w + v * a.w_ld + c, left, a.w_wide) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int u = 0; u < kU; ++u)
+          if (q + u * kFewWarps < rows) w[u].load(a.w + (b + q + u * kFewWarps) * a.w_ld + c, left, a.w_wide);
 #pragma unroll
-      for (int q = 0; q < kNt / 4; ++q)
-        d[u][q] = v < r1 ? __ldg(reinterpret_cast<const float4 *>(a.dz + v * kNt) + q) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+      for (int u = 0; u < kU; ++u) {
+        const int r = q + u * kFewWarps;
+        if (r >= rows) break;
+        Cols<kC> o;
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int64_t v = v0 + u * kSmallWarps;
-      if (v >= r1) break;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < kC; ++i) o.v[i] = 0.f;
 #pragma unroll
-      for (int t = 0; t < kNt; ++t) {
-        const float4 q = d[u][t / 4];
-        const float z = (t & 3) == 0 ? q.x : (t & 3) == 1 ? q.y : (t & 3) == 2 ? q.z : q.w;
-        if (kDxOut) {
-          float4 &s = acc[kDxOut ? t : 0];
-          s.x = fmaf(z, w[u].x, s.x);
-          s.y = fmaf(z, w[u].y, s.y);
-          s.z = fmaf(z, w[u].z, s.z);
-          s.w = fmaf(z, w[u].w, s.w);
+        for (int t4 = 0; t4 < kNt / 4; ++t4) {
+          const float4 z4 = *reinterpret_cast<const float4 *>(dzs + r * kNt + 4 * t4);
+          const float z[4] = {z4.x, z4.y, z4.z, z4.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int t = 4 * t4 + e;
+#pragma unroll
+            for (int i = 0; i < kC; ++i) {
+              if (kDxOut) acc[kDxOut ? t : 0][i] = fmaf(z[e], w[u].v[i], acc[kDxOut ? t : 0][i]);
+              if (kDwOut) o.v[i] = fmaf(z[e], x[kDwOut ? t : 0].v[i], o.v[i]);
+            }
+          }
         }
-        if (kDwOut) {
-          const float4 b = x[kDwOut ? t : 0];
-          o.x = fmaf(z, b.x, o.x);
-          o.y = fmaf(z, b.y, o.y);
-          o.z = fmaf(z, b.z, o.z);
-          o.w = fmaf(z, b.w, o.w);
-        }
-      }
-      if (kDwOut) {
-        float *to = a.dw + v * a.dw_ld + c;
-        if (left >= 4 && a.dw_wide) {
-          __stcs(reinterpret_cast<float4 *>(to), o);
-        } else {
-          if (left > 0) to[0] = o.x;
-          if (left > 1) to[1] = o.y;
-          if (left > 2) to[2] = o.z;
-          if (left > 3) to[3] = o.w;
-        }
+        if (kDwOut && left > 0) o.store(a.dw + (b + r) * a.dw_ld + c, left, a.dw_wide);
       }
     }
   }
@@ -244,22 +280,17 @@ __global__ void __launch_bounds__(kSmallWarps * 32) k_xent_few_grad(const SmallG
 #pragma unroll
     for (int t = 0; t < kNt; ++t) {
       if (t >= a.n) break;
-      sum[warp][lane] = acc[t];
       __syncthreads();
-      if (warp == 0 && left > 0) {
-        float4 s = sum[0][lane];
 #pragma unroll
-        for (int q = 1; q < kSmallWarps; ++q) {
-          const float4 b = sum[q][lane];
-          s.x += b.x;
-          s.y += b.y;
-          s.z += b.z;
-          s.w += b.w;
-        }
-        // acc_ld is a multiple of four: columns past the width are its own
-        *reinterpret_cast<float4 *>(a.acc + ((size_t)blockIdx.y * (size_t)a.n + t) * (size_t)a.acc_ld + c) = s;
-      }
+      for (int i = 0; i < kC; ++i) sum[warp][lane * kC + i] = acc[t][i];
       __syncthreads();
+      for (int i = threadIdx.x; i < 32 * kC; i += kFewWarps * 32) {
+        const int col = blockIdx.x * 32 * kC + i;
+        float s = 0.f;
+#pragma unroll
+        for (int q = 0; q < kFewWarps; ++q) s += sum[q][i];
+        if (col < a.acc_ld) a.acc[((size_t)blockIdx.y * (size_t)a.n + t) * (size_t)a.acc_ld + col] = s;
+      }
     }
   }
 }
