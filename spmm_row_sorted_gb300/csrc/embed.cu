@@ -282,14 +282,15 @@ struct EmbedGrad {
   int64_t n_chunks;
   int n_seg;        // column segments
   int64_t sum_blocks;
-  ZeroRows zero;    // the rows that no token names, from `cleared` on
+  ZeroRows zero;    // the rows that no token names, from `cleared` on,
   int64_t cleared;
+  int zero_rows;    // so many per warp
 };
 
 constexpr int kGradWarps = 8;
 constexpr int kGradVecs = 2;   // accesses per lane
 constexpr int kGradBatch = 4;  // rows in flight per lane
-constexpr int kZeroRows = 8;   // rows per warp of the clearing
+constexpr int kZeroMost = 8;   // rows per warp of the clearing, at most
 
 __device__ __forceinline__ int64_t lower_bound(const uint32_t *__restrict__ k, int64_t n, uint32_t v) {
   int64_t lo = 0, hi = n;
@@ -347,20 +348,22 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_embed_sum(const EmbedGrad g
   constexpr int kBatch = kAdd ? kGradBatch / 2 : kGradBatch;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int acc_n = g.width / P::kN;
-  if ((int64_t)blockIdx.x >= g.sum_blocks) {  // ---- rows that no token names
-    const int64_t v0 = g.cleared + (((int64_t)blockIdx.x - g.sum_blocks) * kGradWarps + warp) * kZeroRows;
+  const bool sums = (int64_t)blockIdx.x < g.sum_blocks;
+  const int64_t own = sums ? (int64_t)blockIdx.x : (int64_t)blockIdx.x - g.sum_blocks;
+  if (!sums) {  // ---- rows that no token names
+    const int64_t v0 = g.cleared + (own * kGradWarps + warp) * g.zero_rows;
     bool absent = false;
-    if (lane < kZeroRows && v0 + lane < (int64_t)g.vocab) {
+    if (lane < g.zero_rows && v0 + lane < (int64_t)g.vocab) {
       const uint32_t v = (uint32_t)(v0 + lane);
       const int64_t at = lower_bound(g.keys, g.n, v);
       absent = at >= g.n || __ldg(g.keys + at) != v;
     }
     const unsigned rows = __ballot_sync(0xffffffffu, absent);
-    for (int r = 0; r < kZeroRows; ++r)
+    for (int r = 0; r < g.zero_rows; ++r)
       if ((rows >> r) & 1u) clear_row(g.zero, v0 + r);
     return;
   }
-  const int64_t gw = (int64_t)blockIdx.x * kGradWarps + warp;
+  const int64_t gw = own * kGradWarps + warp;
   const int64_t c = gw / g.n_seg;
   if (c >= g.n_chunks) return;
   const int seg = (int)(gw - c * g.n_seg);
@@ -626,7 +629,9 @@ cudaError_t launch_grad(EmbedGrad g, cudaStream_t s) {
   const int acc = g.width / Pack<T, B>::kN;
   g.n_seg = (int)ceil_div(acc, kSegElems);
   g.sum_blocks = ceil_div(g.n_chunks * g.n_seg, kGradWarps);
-  const int64_t blocks = g.sum_blocks + (g.accumulate ? 0 : ceil_div((int64_t)g.vocab - g.cleared, (int64_t)kGradWarps * kZeroRows));
+  const int64_t rows = g.accumulate ? 0 : (int64_t)g.vocab - g.cleared;
+  g.zero_rows = (int)(rows / 4096 < 1 ? 1 : rows / 4096 > kZeroMost ? kZeroMost : rows / 4096);
+  const int64_t blocks = g.sum_blocks + ceil_div(rows, (int64_t)kGradWarps * g.zero_rows);
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   if (blocks == 0) return cudaSuccess;
   cudaError_t e = g.accumulate
