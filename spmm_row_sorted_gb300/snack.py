@@ -136,7 +136,7 @@ def load(path: Optional[str] = None):
 
 
 def _check(fn: str, status: int) -> None:
-    if status != SNACK_OK:
+    if status:
         raise SnackError(fn, status, load().snack_status_string(status).decode())
 
 
@@ -147,7 +147,7 @@ def _addr(t: Optional[torch.Tensor]):
 def _raw_stream(stream):
     """The cudaStream_t of `stream`, or of torch's current one, as an integer."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -335,28 +335,29 @@ def snack_embed_grad(ids, dout, scale: float, accumulate: bool, dtable, ws, stre
 
 def snack_clip_workspace_size(numel, types) -> int:
     b = ctypes.c_size_t(0)
+    m, t = _array("q", numel), _array("i", types)
     _check("snack_clip_workspace_size",
-           load().snack_clip_workspace_size(len(numel), _array("q", numel), _array("i", types), ctypes.byref(b)))
+           load().snack_clip_workspace_size(len(numel), _at(m), _at(t), ctypes.byref(b)))
     return b.value
 
 
-def _array(code: str, values):
-    """A C array of `values` ("Q" addresses, "q" int64, "i" int) and its address, kept alive with it."""
-    a = array.array(code, values)
-    p = ctypes.c_void_p(a.buffer_info()[0] if values else None)
-    p.owner = a
-    return p
+def _array(code: str, values) -> array.array:
+    """`values` as a C array: "Q" addresses, "q" int64, "i" int."""
+    return array.array(code, values)
+
+
+def _at(a: array.array):
+    return a.buffer_info()[0] if a else None
 
 
 def snack_clip_grad_norm(grads, outs, numel, types, max_norm: float, norm, ws, stream=None) -> None:
     """grads and outs: lists of device addresses (outs None: the norm alone); numel, types: lists of their sizes."""
     if not len(grads) == len(numel) == len(types) or (outs is not None and len(outs) != len(grads)):
         raise ValueError("one address, size and type per tensor")
+    g, o, m, t = (_array(c, v) for c, v in (("Q", grads), ("Q", outs or ()), ("q", numel), ("i", types)))
     _check("snack_clip_grad_norm",
-           (_lib or load()).snack_clip_grad_norm(len(grads), _array("Q", grads),
-                                                 None if outs is None else _array("Q", outs), _array("q", numel),
-                                                 _array("i", types), max_norm, _addr(norm), _addr(ws), _nbytes(ws),
-                                                 _raw_stream(stream)))
+           (_lib or load()).snack_clip_grad_norm(len(grads), _at(g), None if outs is None else _at(o), _at(m), _at(t),
+                                                 max_norm, _addr(norm), _addr(ws), _nbytes(ws), _raw_stream(stream)))
 
 
 def snack_xent_workspace_size(x, w, grad: bool) -> int:
@@ -550,7 +551,7 @@ def _elsewhere(t: torch.Tensor, stream) -> bool:
     """Whether a call on t has to enter a stream or a device first; refuses what is not on a GPU."""
     if not t.is_cuda:
         raise ValueError("expected CUDA tensors")
-    return stream is not None or t.get_device() != torch.cuda.current_device()
+    return stream is not None or t.get_device() != torch._C._cuda_getDevice()
 
 
 def _same_device(first: torch.Tensor, *others) -> None:
