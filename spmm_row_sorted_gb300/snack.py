@@ -547,28 +547,37 @@ class _On:
         self.outer.__exit__(*exc)
 
 
-def _elsewhere(t: torch.Tensor, stream) -> bool:
-    """Whether a call on t has to enter a stream or a device first; refuses what is not on a GPU."""
-    if not t.is_cuda:
+def _here(t: torch.Tensor, stream, *others) -> bool:
+    """Whether a call on t can run as things stand (torch's current device and stream); all tensors on one GPU."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("expected CUDA tensors")
-    return stream is not None or t.get_device() != torch._C._cuda_getDevice()
-
-
-def _same_device(first: torch.Tensor, *others) -> None:
-    dev = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != dev:
+    for o in others:
+        if o is not None and o.get_device() != dev:
             raise ValueError("all tensors must be on one CUDA device")
+    return stream is None and dev == torch._C._cuda_getDevice()
 
 
-def _rows(t: torch.Tensor) -> torch.Tensor:
-    """t as a matrix whose rows are contiguous (their distance may exceed their length)."""
+def _matrix(t: torch.Tensor):
+    """t (copied where its rows are not contiguous), its address, rows, width and row step."""
     if t.dim() != 2:
         raise ValueError("expected a matrix")
+    rows, width = t.shape
     step, one = t.stride()
-    if (one == 1 or t.shape[1] == 1) and step >= t.shape[1]:
-        return t
-    return t.contiguous()
+    if (one != 1 and width != 1) or step < width:
+        t, step = t.contiguous(), width
+    return t, t.data_ptr(), rows, width, step
+
+
+def _code(table, dtype) -> int:
+    try:
+        return table[dtype]
+    except KeyError:
+        raise ValueError(f"unsupported dtype {dtype}") from None
+
+
+_DTYPES = {torch.float32: SNACK_F32, torch.bfloat16: SNACK_BF16}
+_INDICES = {torch.int32: SNACK_I32, torch.int64: SNACK_I64}
 
 
 def _out_rows(out: torch.Tensor, rows: int, width: int, dtype) -> torch.Tensor:
@@ -600,25 +609,22 @@ def _xent_ws(device: int, x_bits: int, x_ld: int, n: int, w_bits: int, w_ld: int
     return b.value
 
 
-def _xent_workspace(x, w, grad: int) -> torch.Tensor:
-    # of the addresses, their place within 256 bytes
-    nbytes = _xent_ws(x.get_device(), x.data_ptr() % 256, x.stride(0), x.shape[0], w.data_ptr() % 256, w.stride(0),
-                      w.shape[0], w.shape[1], dtype_code(w.dtype), grad)
-    return _workspace(nbytes, x.device)
-
-
 def embed(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out: Optional[torch.Tensor] = None,
           stream=None) -> torch.Tensor:
     """scale * table[ids], zeros for an id outside the table; ids of any shape, the result has that shape plus the width."""
-    if _elsewhere(table, stream):
+    if not _here(table, stream, ids, out):
         with _On(table.device, stream):
             return embed(ids, table, scale, out)
-    _same_device(table, ids, out)
-    tab, flat = _rows(table), ids.contiguous()
-    n, width = flat.numel(), tab.shape[1]
-    y = tab.new_empty((n, width)) if out is None else _out_rows(out, n, width, tab.dtype)
-    snack_embed_fwd(flat, tab, float(scale), y)
-    return y.view(*ids.shape, width) if out is None and ids.dim() != 1 else y
+    tab, addr, vocab, width, ld = _matrix(table)
+    flat, kind = ids.contiguous(), tab.dtype
+    n = flat.numel()
+    y = torch.empty((n, width), dtype=kind, device=tab.device) if out is None else _out_rows(out, n, width, kind)
+    st = (_lib or load()).snack_embed_fwd(flat.data_ptr(), _code(_INDICES, flat.dtype), n, addr, ld, vocab, width,
+                                          _code(_DTYPES, kind), float(scale), y.data_ptr(), width if out is None else y.stride(0),
+                                          _raw_stream(None))
+    if st:
+        _check("snack_embed_fwd", st)
+    return y if out is not None or ids.dim() == 1 else y.view(*ids.shape, width)
 
 
 def embed_grad(ids: torch.Tensor, dout: torch.Tensor, vocab: int, scale: float = 1.0,
@@ -626,17 +632,23 @@ def embed_grad(ids: torch.Tensor, dout: torch.Tensor, vocab: int, scale: float =
     """The gradient of embed's table, [vocab, width] in dout's type.  With accumulate the sums are added to `out`."""
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    if _elsewhere(dout, stream):
+    if not _here(dout, stream, ids, out):
         with _On(dout.device, stream):
             return embed_grad(ids, dout, vocab, scale, out, accumulate)
-    _same_device(dout, ids, out)
-    width = dout.shape[-1]
-    d, flat = _rows(dout if dout.dim() == 2 else dout.reshape(-1, width)), ids.contiguous()
+    d, addr, rows, width, ld = _matrix(dout if dout.dim() == 2 else dout.reshape(-1, dout.shape[-1]))
+    flat, kind = ids.contiguous(), d.dtype
     n = flat.numel()
-    if d.shape[0] != n:
+    if rows != n:
         raise ValueError("dout needs one row per id")
-    g = d.new_empty((vocab, width)) if out is None else _out_rows(out, vocab, width, d.dtype)
-    snack_embed_grad(flat, d, float(scale), accumulate, g, _workspace(_embed_grad_ws(n, vocab, width), d.device))
+    g = torch.empty((vocab, width), dtype=kind, device=d.device) if out is None else _out_rows(out, vocab, width, kind)
+    nbytes = _embed_grad_ws(n, vocab, width)
+    ws = _workspace(nbytes, d.device)
+    st = (_lib or load()).snack_embed_grad(flat.data_ptr(), _code(_INDICES, flat.dtype), n, addr, ld, vocab, width,
+                                           _code(_DTYPES, kind), float(scale), 1 if accumulate else 0, g.data_ptr(),
+                                           width if out is None else g.stride(0), ws.data_ptr(), max(nbytes, 256),
+                                           _raw_stream(None))
+    if st:
+        _check("snack_embed_grad", st)
     return g
 
 
@@ -669,7 +681,7 @@ def clip_grad_norm(grads, max_norm: float, out=None, stream=None) -> torch.Tenso
     if not grads:
         raise ValueError("no gradients")
     first = grads[0]
-    if _elsewhere(first, stream):
+    if not _here(first, stream):
         with _On(first.device, stream):
             return clip_grad_norm(grads, max_norm, out)
     # one call over all tensors per property: a model has hundreds of gradients
@@ -686,20 +698,31 @@ def clip_grad_norm(grads, max_norm: float, out=None, stream=None) -> torch.Tenso
             raise ValueError("out must hold contiguous tensors of the gradients' types and sizes, on their device")
         to = list(map(T.data_ptr, outs))
     norm = torch.empty((), dtype=torch.float32, device=first.device)
-    types = list(map({d: dtype_code(d) for d in set(dtypes)}.get, dtypes))
+    types = [_code(_DTYPES, d) for d in dtypes]
     ws = _workspace(_clip_ws(len(grads)), first.device)
     snack_clip_grad_norm(addr, to, numel, types, float(max_norm), norm, ws)
     return norm
 
 
-def _xent_args(x, w, targets, reduction):
+def _xent_args(x, w, targets, reduction, grad):
+    """What both calls take of x, w and targets, the reduction, and a workspace; and x, w, targets to keep alive."""
+    x, xa, n, width, x_ld = _matrix(x)
+    w, wa, vocab, w_width, w_ld = _matrix(w)
+    kind = w.dtype
+    if width != w_width or x.dtype != kind:
+        raise ValueError("x [n, width] and w [vocab, width] must have one type and width")
+    if targets.numel() != n:
+        raise ValueError("targets needs one entry per row of x")
     if reduction not in REDUCTIONS:
         raise ValueError(f"reduction must be one of {sorted(REDUCTIONS)}")
-    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1] or x.dtype != w.dtype:
-        raise ValueError("x [n, width] and w [vocab, width] must have one type and width")
-    if targets.numel() != x.shape[0]:
-        raise ValueError("targets needs one entry per row of x")
-    return _rows(x), _rows(w), targets.contiguous(), REDUCTIONS[reduction]
+    targets = targets.contiguous()
+    code = _code(_DTYPES, kind)
+    # of the addresses, their place within 256 bytes
+    nbytes = max(256, _xent_ws(x.get_device(), xa % 256, x_ld, n, wa % 256, w_ld, vocab, width, code, grad))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    args = (xa, x_ld, n, wa, w_ld, vocab, width, code, targets.data_ptr(), _code(_INDICES, targets.dtype),
+            REDUCTIONS[reduction])
+    return args, ws, nbytes, (x, w, targets)
 
 
 def xent(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, reduction: str = "mean", stream=None):
@@ -708,16 +731,18 @@ def xent(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, reduction: str
     A target outside the vocabulary (such as -100) is not trained on.  state
     (float32, n + 1) is what xent_grad needs beside the same arguments.
     """
-    if _elsewhere(x, stream):
+    if not _here(x, stream, w, targets):
         with _On(x.device, stream):
             return xent(x, w, targets, reduction)
-    _same_device(x, w, targets)
-    x, w, targets, red = _xent_args(x, w, targets, reduction)
-    n = x.shape[0]
-    loss = torch.empty((n,) if reduction == "none" else (), dtype=torch.float32, device=x.device)
-    state = torch.empty(n + 1, dtype=torch.float32, device=x.device)
+    args, ws, nbytes, kept = _xent_args(x, w, targets, reduction, 0)
+    n, dev = args[2], x.device
+    loss = torch.empty((n,) if reduction == "none" else (), dtype=torch.float32, device=dev)
+    state = torch.empty(n + 1, dtype=torch.float32, device=dev)
     if n or reduction != "none":
-        snack_xent_fwd(x, w, targets, red, loss, state, _xent_workspace(x, w, 0))
+        st = (_lib or load()).snack_xent_fwd(*args, loss.data_ptr(), state.data_ptr(), ws.data_ptr(), nbytes,
+                                             _raw_stream(None))
+        if st:
+            _check("snack_xent_fwd", st)
     return loss, state
 
 
@@ -725,22 +750,25 @@ def xent_grad(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, state: to
               dloss: Optional[torch.Tensor] = None, reduction: str = "mean", want_dx: bool = True,
               want_dw: bool = True, stream=None):
     """(dx, dw) of xent for an upstream gradient dloss (1 when None; one value per row for "none")."""
-    if _elsewhere(x, stream):
+    if not _here(x, stream, w, targets, state, dloss):
         with _On(x.device, stream):
             return xent_grad(x, w, targets, state, dloss, reduction, want_dx, want_dw)
-    _same_device(x, w, targets, state, dloss)
-    x, w, targets, red = _xent_args(x, w, targets, reduction)
-    if state.dtype != torch.float32 or state.numel() != x.shape[0] + 1 or not state.is_contiguous():
+    args, ws, nbytes, kept = _xent_args(x, w, targets, reduction, 1)
+    n, width, vocab, kind, dev = args[2], args[6], args[5], x.dtype, x.device
+    if state.dtype != torch.float32 or state.numel() != n + 1 or not state.is_contiguous():
         raise ValueError("state must be what xent returned for these arguments")
     if dloss is not None:
-        if dloss.numel() != (x.shape[0] if reduction == "none" else 1):
+        if dloss.numel() != (n if reduction == "none" else 1):
             raise ValueError("dloss has the loss's shape")
         dloss = dloss.contiguous().float()
     elif reduction == "none":
         raise ValueError('reduction "none" needs dloss')
-    dx = x.new_empty(x.shape) if want_dx else None
-    dw = w.new_empty(w.shape) if want_dw else None
-    snack_xent_bwd(x, w, targets, red, state, dloss, dx, dw, _xent_workspace(x, w, 1))
+    dx = torch.empty((n, width), dtype=kind, device=dev) if want_dx else None
+    dw = torch.empty((vocab, width), dtype=kind, device=dev) if want_dw else None
+    st = (_lib or load()).snack_xent_bwd(*args, state.data_ptr(), _addr(dloss), _addr(dx), width, _addr(dw), width,
+                                         ws.data_ptr(), nbytes, _raw_stream(None))
+    if st:
+        _check("snack_xent_bwd", st)
     return dx, dw
 
 
