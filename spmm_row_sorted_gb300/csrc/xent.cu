@@ -52,6 +52,8 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "internal.hpp"
 #include "lm.hpp"
 #include "xent_small.cuh"
@@ -680,17 +682,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
             }
           } else {  // rows that TMA cannot address: a warp writes one after the other
             __syncwarp();
-            for (int r = 0; r < 32; ++r) {
-              const int orow = m0 + quarter * 32 + r;
-              if (orow >= P.m) break;
-              for (int j = lane; j < step && x0 + j < P.n; j += 32) {
-                if (wide)
-                  reinterpret_cast<float *>(P.out)[(int64_t)orow * P.out_ld + x0 + j] =
-                      *reinterpret_cast<const float *>(stage + stage_off(r, j >> 2) + (j & 3) * 4);
-                else
-                  reinterpret_cast<uint16_t *>(P.out)[(int64_t)orow * P.out_ld + x0 + j] =
+            const int rows = x0 < P.n ? min(32, P.m - (m0 + quarter * 32)) : 0;
+            const int64_t first = (int64_t)(m0 + quarter * 32) * P.out_ld + x0;
+            if (wide) {
+#pragma unroll 4
+              for (int r = 0; r < rows; ++r)
+                if (x0 + lane < P.n)
+                  reinterpret_cast<float *>(P.out)[first + r * P.out_ld + lane] =
+                      *reinterpret_cast<const float *>(stage + stage_off(r, lane >> 2) + (lane & 3) * 4);
+            } else {
+              for (int r = 0; r < rows; ++r)
+                for (int j = lane; j < step && x0 + j < P.n; j += 32)
+                  reinterpret_cast<uint16_t *>(P.out)[first + r * P.out_ld + j] =
                       *reinterpret_cast<const uint16_t *>(stage + stage_off(r, j >> 3) + (j & 7) * 2);
-              }
             }
             __syncwarp();
           }
@@ -879,6 +883,31 @@ __global__ void __launch_bounds__(256) k_xent_pack(const T *__restrict__ in, int
   }
 }
 
+// Rows of bf16 from 16-byte aligned ones to any others, two elements per store:
+// where a row starts in the middle of a word, two neighbouring words of the
+// source make one of it.  (Stores of single elements out of the product's
+// epilogue took 440 us for 86926 rows of 1709, this and the aligned stores 190.)
+__global__ void __launch_bounds__(256) k_xent_rows(const bf16 *__restrict__ in, int64_t in_ld, int64_t rows, int32_t width,
+                                                   bf16 *__restrict__ out, int64_t out_ld) {
+  pdl_wait();
+  const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  const int lane = threadIdx.x & 31;
+  const uint32_t *from = reinterpret_cast<const uint32_t *>(in + r * in_ld);
+  bf16 *row = out + r * out_ld;
+  const int shift = (int)(((uintptr_t)row >> 1) & 1);
+  uint32_t *to = reinterpret_cast<uint32_t *>(row + shift);
+  const int words = (width - shift) / 2;
+  const bf16 *single = in + r * in_ld;
+#pragma unroll 4
+  for (int k = lane; k < words; k += 32) {
+    const uint32_t a = __ldg(from + k);
+    to[k] = shift ? __funnelshift_r(a, __ldg(from + k + 1), 16) : a;
+  }
+  if (lane == 0 && shift) row[0] = single[0];
+  if (lane == 1 && shift + 2 * words < width) row[width - 1] = single[width - 1];
+}
+
 // dx = the splits' sums, added in order and rounded once.  The last kernel of a
 // gradient: after an error it makes dx and the first row of dw NaN.
 template <typename T>
@@ -989,15 +1018,18 @@ int64_t piece_rows(int64_t vocab, int64_t row_bytes) {
 }
 
 // How many ways the K of a product is split: the choice whose last wave of
-// tiles wastes least, each tile counted as its K blocks and the fixed cost of
-// eight more.
-int pick_split(int64_t tiles, int64_t k_steps, int sms) {
+// tiles wastes least, each tile counted as its K stages (weight of them per K
+// block, 0.27 us each) and the fixed cost of eight more, and the reading of the
+// splits' sums at the end.
+int pick_split(int64_t tiles, int64_t k_blocks, int64_t weight, int64_t sum_bytes, int sms) {
   int best = 1;
-  int64_t best_cost = INT64_MAX;
-  for (int s = 1; s <= 8; ++s) {
-    const int64_t per = ceil_div(k_steps, s);
-    if (s > 1 && (per < 8 || (s - 1) * per >= k_steps)) break;
-    const int64_t cost = ceil_div(tiles * s, sms / 2) * (per + 8);
+  double best_cost = 1e30;
+  for (int s = 1; s <= 64; ++s) {
+    const int64_t per = ceil_div(k_blocks, s);
+    if (s > 1 && per * weight < 8) break;
+    if ((s - 1) * per >= k_blocks) continue;  // a split without work
+    const double cost = (double)(ceil_div(tiles * s, sms / 2) * (per * weight + 8)) +
+                        (double)s * (double)sum_bytes / 6.5e6 / 0.27;
     if (cost < best_cost) {
       best_cost = cost;
       best = s;
@@ -1011,6 +1043,7 @@ struct XentShape {
   int64_t vocab;
   snack_dtype t;
   bool pack_x, pack_w;
+  bool pack_dw;  // bf16 rows of dw that TMA cannot store: by way of the workspace
   bool few;    // the CUDA-core path of a few fp32 tokens
   int parts;
   int32_t ld;  // row length of packed planes
@@ -1018,7 +1051,7 @@ struct XentShape {
 };
 
 struct XentWs {
-  size_t err, zt, row_loss, part, xp, wp, dz, acc, total;
+  size_t err, zt, row_loss, part, xp, wp, dz, acc, dwp, total;
   int nt;             // forward tile
   int64_t piece;      // vocabulary rows at a time (forward: of packed w; gradient: of dz)
   int64_t slots;
@@ -1078,17 +1111,22 @@ XentWs xent_ws(const XentShape &s, bool grad) {
     o += align_up((size_t)w.slots * (size_t)s.n * 8, kAlign);
   } else {
     const int64_t dz_row = (int64_t)s.parts * s.n * 2;
-    w.piece = piece_rows(s.vocab, s.pack_w && w_row > dz_row ? w_row : dz_row);
+    const int64_t dw_row = s.pack_dw ? (int64_t)s.ld * 2 : 0;
+    w.piece = piece_rows(s.vocab, std::max(std::max(s.pack_w ? w_row : 0, dz_row), dw_row));
     if (w.piece > s.vocab) w.piece = s.vocab;
     w.dz_ld = ceil_div(w.piece, 64) * 64;
     w.nt_d = s.width > 128 ? 256 : 128;  // a CTA's half of B is 64 columns at least
     w.acc_ld = (int32_t)align_up((size_t)s.width, 4);
-    w.split = pick_split(m_tiles * ceil_div(s.width, w.nt_d), ceil_div(w.piece, kKb), s.sms);
+    // the pieces' products are alike: all of them as one piece of so many times the K stages
+    w.split = pick_split(m_tiles * ceil_div(s.width, w.nt_d), ceil_div(w.piece, kKb),
+                         (s.parts == 3 ? 6 : 1) * ceil_div(s.vocab, w.piece), (int64_t)s.n * w.acc_ld * 4, s.sms);
     w.dz = o;
     o += align_up((size_t)s.parts * (size_t)s.n * (size_t)w.dz_ld * 2, kAlign);
     w.acc = o;
     o += align_up((size_t)w.split * (size_t)s.n * (size_t)w.acc_ld * 4, kAlign);
   }
+  w.dwp = o;
+  if (grad && s.pack_dw) o += align_up((size_t)w.piece * (size_t)s.ld * 2, kAlign);
   w.wp = o;
   if (s.pack_w) o += align_up((size_t)s.parts * (size_t)w.piece * (size_t)s.ld * 2, kAlign);
   w.total = o;
@@ -1117,6 +1155,7 @@ XentShape xent_shape(const void *x, int64_t x_ld, int32_t n, const void *wt, int
   s.pack_x = grad || t == SNACK_F32 || !rows_ready(x, x_ld, n, grad);  // the gradient's leaves rows out
   s.pack_w = t == SNACK_F32 || !rows_ready(wt, w_ld, n, grad);
   s.few = t == SNACK_F32 && n <= kSmallMostTokens;
+  s.pack_dw = t == SNACK_BF16 && width % 8 != 0;
   s.ld = (int32_t)align_up((size_t)width, 64);
   s.sms = sms_of();
   return s;
@@ -1454,15 +1493,21 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
       h.nt = W.nt_d;
       h.k_blocks = (int32_t)ceil_div(n, kKb);
       uint8_t *to = reinterpret_cast<uint8_t *>(dw) + (size_t)v0 * (size_t)dw_ld * es;
-      h.out = to;
+      const bool direct = ptr_aligned(to, 16) && (size_t)dw_ld * es % 16 == 0, by_ws = !direct && S.pack_dw;
+      uint8_t *out = by_ws ? b + W.dwp : to;
+      const int64_t out_ld = by_ws ? S.ld : dw_ld;
+      h.out = out;
       h.factor = factor;
-      h.out_ld = dw_ld;
+      h.out_ld = out_ld;
       h.out_wide = wide;
-      h.out_tma = ptr_aligned(to, 16) && (size_t)dw_ld * es % 16 == 0;
-      if (h.out_tma && !make_map(&mdw, to, wide, (uint64_t)width, (uint64_t)rows, (uint64_t)dw_ld, 1,
-                                 (uint64_t)rows * (uint64_t)dw_ld, wide ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+      h.out_tma = direct || by_ws;
+      if (h.out_tma && !make_map(&mdw, out, wide, (uint64_t)width, (uint64_t)rows, (uint64_t)out_ld, 1,
+                                 (uint64_t)rows * (uint64_t)out_ld, wide ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
         return SNACK_ERR_CUDA;
       XENT_CUDA(launch_gemm<kDw>(mdzt, mxt, h.out_tma ? mdw : mxt, h, S.sms, s));
+      if (by_ws)
+        XENT_CUDA(launch_pdl(k_xent_rows, (unsigned)ceil_div(rows, 8), 256, 0, s, reinterpret_cast<const bf16 *>(out),
+                             out_ld, rows, width, reinterpret_cast<bf16 *>(to), dw_ld));
     }
   }
   const int64_t total = dx ? (int64_t)n * (W.acc_ld / 4) : 0;

@@ -324,3 +324,24 @@ def test_xent_few_fp32_tokens(n, vocab, width, gap, lead, reduction):
     check_grads(only_x, only_w, r, "f32")
     again = snack.xent_grad(x, w, t, state, dloss, reduction=reduction)
     assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
+
+
+@pytest.mark.parametrize("n,vocab,width,dtype", [(20, 3000, 129, "bf16"), (40, 700, 130, "bf16"), (300, 513, 77, "bf16"),
+                                                 (33, 2000, 61, "f32"), (60, 5000, 30, "f32")])
+def test_xent_grad_rows_off_every_boundary(n, vocab, width, dtype):
+    """dw rows that start in the middle of a word, into a caller's matrix with gaps that stay as they are; products
+    split many ways along the vocabulary."""
+    x, w, t = make(n, vocab, width, dtype, seed=n)
+    loss, state = snack.xent(x, w, t)
+    scale = 1.0 / float(((t >= 0) & (t < vocab)).sum())
+    r = reference(x, w, t, np.full(n, scale))
+    check_grads(*snack.xent_grad(x, w, t, state), r, dtype)
+    for gap, lead in ((0, 1), (3, 0), (1, 2)):
+        buf = torch.full((vocab * (width + gap) + lead,), 7.0, device="cuda", dtype=DTYPES[dtype])
+        dw = buf[lead:].view(vocab, width + gap)[:, :width]
+        ws = torch.empty(snack.snack_xent_workspace_size(x, w, True), dtype=torch.uint8, device="cuda")
+        snack.snack_xent_bwd(x, w, t, 2, state, None, None, dw, ws)
+        check_grads(None, dw, r, dtype)
+        if gap:
+            assert torch.all(buf[lead:].view(vocab, width + gap)[:, width:] == 7.0)
+        assert torch.all(buf[:lead] == 7.0)
