@@ -1009,12 +1009,18 @@ int tile_cols(int64_t m_tiles, int64_t n, int sms) {
   return best;
 }
 
-// Equal pieces of the vocabulary, multiples of 256 rows, of at most `bytes` each.
-int64_t piece_rows(int64_t vocab, int64_t row_bytes) {
-  int64_t most = (int64_t)(kPieceBytes / (size_t)row_bytes) / 256 * 256;
+// Pieces of the vocabulary of about equal size and at most kPieceBytes: a
+// multiple of the rows that give every pair of SMs one 256-column tile (67 fp32
+// tokens, 119598 x 2176: 78 tiles a piece on 76 pairs took two waves, 76 take
+// one), or of 256 where those are too many.
+int64_t piece_rows(int64_t vocab, int64_t row_bytes, int64_t m_tiles, int sms) {
+  const int64_t pairs = sms / 2, wave = 256 * (m_tiles < pairs ? pairs / m_tiles : 1);
+  int64_t most = (int64_t)(kPieceBytes / (size_t)row_bytes);
+  const int64_t unit = most >= wave ? wave : 256;
+  most = most / unit * unit;
   if (most < 1024) most = 1024;
-  const int64_t pieces = ceil_div(vocab, most);
-  return ceil_div(ceil_div(vocab, pieces), 256) * 256;
+  const int64_t equal = ceil_div(ceil_div(vocab, ceil_div(vocab, most)), unit) * unit;
+  return equal < most ? equal : most;
 }
 
 // How many ways the K of a product is split: the choice whose last wave of
@@ -1096,12 +1102,12 @@ XentWs xent_ws(const XentShape &s, bool grad) {
     return w;
   }
   const int64_t w_row = (int64_t)s.parts * s.ld * 2;
-  w.nt = tile_cols(m_tiles, s.vocab, s.sms);
   w.xp = o;
   if (s.pack_x) o += align_up((size_t)s.parts * (size_t)s.n * (size_t)s.ld * 2, kAlign);
   if (!grad) {
-    w.piece = s.pack_w ? piece_rows(s.vocab, w_row) : s.vocab;
+    w.piece = s.pack_w ? piece_rows(s.vocab, w_row, m_tiles, s.sms) : s.vocab;
     if (w.piece > s.vocab) w.piece = s.vocab;
+    w.nt = tile_cols(m_tiles, w.piece, s.sms);
     w.slots = 2 * (ceil_div(s.vocab, w.piece) * ceil_div(w.piece, w.nt));
     w.zt = o;
     o += align_up((size_t)s.n * 4, kAlign);
@@ -1112,7 +1118,7 @@ XentWs xent_ws(const XentShape &s, bool grad) {
   } else {
     const int64_t dz_row = (int64_t)s.parts * s.n * 2;
     const int64_t dw_row = s.pack_dw ? (int64_t)s.ld * 2 : 0;
-    w.piece = piece_rows(s.vocab, std::max(std::max(s.pack_w ? w_row : 0, dz_row), dw_row));
+    w.piece = piece_rows(s.vocab, std::max(std::max(s.pack_w ? w_row : 0, dz_row), dw_row), m_tiles, s.sms);
     if (w.piece > s.vocab) w.piece = s.vocab;
     w.dz_ld = ceil_div(w.piece, 64) * 64;
     w.nt_d = s.width > 128 ? 256 : 128;  // a CTA's half of B is 64 columns at least
@@ -1493,7 +1499,9 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
       h.nt = W.nt_d;
       h.k_blocks = (int32_t)ceil_div(n, kKb);
       uint8_t *to = reinterpret_cast<uint8_t *>(dw) + (size_t)v0 * (size_t)dw_ld * es;
-      const bool direct = ptr_aligned(to, 16) && (size_t)dw_ld * es % 16 == 0, by_ws = !direct && S.pack_dw;
+      // a TMA store writes whole 16 bytes at a row's end: of rows of other lengths it would write past them
+      const bool direct = ptr_aligned(to, 16) && (size_t)dw_ld * es % 16 == 0 && (size_t)width * es % 16 == 0;
+      const bool by_ws = !direct && S.pack_dw;
       uint8_t *out = by_ws ? b + W.dwp : to;
       const int64_t out_ld = by_ws ? S.ld : dw_ld;
       h.out = out;

@@ -226,3 +226,17 @@ def test_embed_refusals():
     with pytest.raises(snack.SnackError) as e:
         snack.snack_embed_grad(torch.zeros(4000, dtype=torch.int64, device="cuda"), d, 1.0, False, table, ws)
     assert e.value.status == 4
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_embed_grad_leaves_the_gaps_of_its_output(dtype):
+    n, vocab, width = 700, 300, 52
+    ids = make_ids(n, vocab, "padded", 4, torch.int64)
+    dout = strided(n, width, 0, 0, dtype, seed=9)
+    want = snack.embed_grad(ids, dout, vocab, 0.5)
+    for lead, gap in ((0, 4), (1, 3), (8, 12)):
+        buf = torch.full((vocab * (width + gap) + lead,), 7.0, device="cuda", dtype=DTYPES[dtype])
+        out = buf[lead:].view(vocab, width + gap)[:, :width]
+        snack.embed_grad(ids, dout, vocab, 0.5, out=out)
+        assert torch.equal(out.contiguous(), want)
+        assert torch.all(buf[lead:].view(vocab, width + gap)[:, width:] == 7.0) and torch.all(buf[:lead] == 7.0)
