@@ -21,6 +21,7 @@ import threading
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import build as _build
 
@@ -660,6 +661,7 @@ class _EmbedFn(torch.autograd.Function):
         return embed(ids, table, scale)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         (ids,) = ctx.saved_tensors
         return embed_grad(ids, dy, ctx.vocab, ctx.scale), None, None
@@ -675,7 +677,8 @@ def clip_grad_norm(grads, max_norm: float, out=None, stream=None) -> torch.Tenso
 
     grads: a sequence of contiguous CUDA tensors, float32 and bfloat16 as they
     come.  The clipped gradients go to `out` (tensors of the same types and
-    sizes), or in place when it is None.
+    sizes), or in place when it is None.  No output may overlap another tensor
+    of the call (a gradient that several parameters share is given once).
     """
     grads = list(grads)
     if not grads:
@@ -698,7 +701,9 @@ def clip_grad_norm(grads, max_norm: float, out=None, stream=None) -> torch.Tenso
             raise ValueError("out must hold contiguous tensors of the gradients' types and sizes, on their device")
         to = list(map(T.data_ptr, outs))
     norm = torch.empty((), dtype=torch.float32, device=first.device)
-    types = [_code(_DTYPES, d) for d in dtypes]
+    types = list(map(_DTYPES.get, dtypes))
+    if None in types:
+        raise ValueError("gradients must be float32 or bfloat16")
     ws = _workspace(_clip_ws(len(grads)), first.device)
     snack_clip_grad_norm(addr, to, numel, types, float(max_norm), norm, ws)
     return norm
@@ -781,6 +786,7 @@ class _XentFn(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dloss):
         x, w, targets, state = ctx.saved_tensors
         dx, dw = xent_grad(x, w, targets, state, dloss, ctx.reduction, ctx.needs_input_grad[0], ctx.needs_input_grad[1])

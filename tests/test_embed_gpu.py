@@ -240,3 +240,12 @@ def test_embed_grad_leaves_the_gaps_of_its_output(dtype):
         snack.embed_grad(ids, dout, vocab, 0.5, out=out)
         assert torch.equal(out.contiguous(), want)
         assert torch.all(buf[lead:].view(vocab, width + gap)[:, width:] == 7.0) and torch.all(buf[:lead] == 7.0)
+
+
+def test_embedding_refuses_a_second_derivative():
+    table = torch.randn(10, 8, device="cuda", requires_grad=True)
+    y = snack.embedding(torch.arange(4, device="cuda"), table)
+    up = torch.ones(4, 8, device="cuda", requires_grad=True)
+    (g,) = torch.autograd.grad(y, table, up, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()

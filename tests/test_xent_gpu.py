@@ -345,3 +345,27 @@ def test_xent_grad_rows_off_every_boundary(n, vocab, width, dtype):
         if gap:
             assert torch.all(buf[lead:].view(vocab, width + gap)[:, width:] == 7.0)
         assert torch.all(buf[:lead] == 7.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("reduction", ["sum", "mean"])
+@pytest.mark.parametrize("n", [1, 16, 17, 32, 33])
+def test_xent_totals_of_a_few_rows(n, reduction, dtype):
+    x, w, t = make(n, 900, 72, dtype, seed=100 + n, ignored=0.4)
+    loss, state = snack.xent(x, w, t, reduction)
+    r = reference(x, w, t, np.ones(n))
+    count = max(1, int(r["inside"].sum()))
+    over = count if reduction == "mean" else 1
+    # the rows' bounds, and the total's rounding to fp32 (it is added in 64 bits)
+    bound = (2 * A * r["T"] + 2.0 ** -16 + 2.0 ** -22 * np.abs(r["lse"]))[r["inside"]].sum() / over
+    want = r["loss"].sum() / over
+    assert abs(float(loss) - want) <= bound + 2.0 ** -23 * abs(want)
+    assert float(state[n]) == (float(np.float32(1) / np.float32(count)) if reduction == "mean" else 1.0)
+
+
+def test_linear_cross_entropy_refuses_a_second_derivative():
+    x, w, t = make(4, 9, 8, "f32", seed=15)
+    x = x.contiguous().requires_grad_()
+    (g,) = torch.autograd.grad(snack.linear_cross_entropy(x, w.contiguous(), t), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
