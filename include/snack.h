@@ -397,9 +397,12 @@ typedef enum snack_reduction { SNACK_NONE = 0, SNACK_SUM = 1, SNACK_MEAN = 2 } s
  * Workspace of snack_xent_fwd (grad == 0) or snack_xent_bwd (grad != 0); of x
  * and w only the alignment is looked at, and has to be that of the call's
  * (rows of bf16 matrices that are not 16-byte aligned are laid out again in
- * the workspace, as are the bf16 parts of fp32 matrices).  It grows with n *
- * vocab / 32 for the forward and holds at most about 256 MB of dz at a time
- * for the gradient (1024 rows of the vocabulary at least).
+ * the workspace, as are the bf16 parts of fp32 matrices).  The forward keeps
+ * about n * vocab / 16 bytes of partial sums (more where its tiles are narrow),
+ * the gradient some fp32 sums of dx; both work on pieces of the vocabulary, of
+ * which they hold 256 MB of dz, or of weights laid out again, at a time (1024
+ * rows at least).  It depends on the number of multiprocessors of the current
+ * device.
  * vocab < 2^30, n < 2^24, width < 2^20.
  */
 snack_status snack_xent_workspace_size(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld,
@@ -431,8 +434,9 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
  * grads, outs, numel and types are host arrays of n_tensors entries (read
  * during the call): device pointers, element counts (0 allowed) and element
  * types; out[k] has its gradient's type and count, and is the gradient itself
- * (in place) or overlaps no gradient.  outs may be NULL: only the norm is
- * computed.  norm (device, fp32) may be NULL.  In place nothing is written
+ * (in place) or overlaps none; it overlaps no other output either (so a
+ * gradient given twice is refused in place).  outs may be NULL: only the norm
+ * is computed.  norm (device, fp32) may be NULL.  In place nothing is written
  * when the factor is 1.  The squares are summed at three scales, so the norm
  * is right (to fp32) also where squares over- or underflow fp32.  An infinite
  * norm gives the factor 0 (an infinite element becomes NaN), a NaN norm makes

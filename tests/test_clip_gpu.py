@@ -139,3 +139,27 @@ def test_clip_refusals():
         assert e.value.status == 1
     with pytest.raises(snack.SnackError):  # shifted on itself
         snack.clip_grad_norm([g[:50]], 1.0, out=[g[10:60]])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_clip_norm_of_elements_that_are_alike(dtype):
+    # every rounding of a running sum of equal terms errs to the same side.  A thread's longest chain: 32 squares
+    # of a batch, 4 batches of a piece, 5 pieces of a block (2^26 elements are 4096 at most), 13 additions of threads;
+    # the root halves that, and rounds twice (4)
+    g = torch.full((2 ** 26,), 0.1, device="cuda", dtype=dtype)
+    want = float(g[0]) * 2.0 ** 13
+    assert abs(float(snack.clip_grad_norm([g], 1e9)) - want) <= (32 + 4 + 5 + 13 + 4) * 2.0 ** -25 * want
+
+
+def test_clip_refuses_a_gradient_given_twice():
+    buf = torch.ones(200, device="cuda")
+    g, h = buf[:100], buf[100:]
+    apart = [torch.empty_like(g) for _ in range(2)]
+    snack.clip_grad_norm([g, g], 1e9, out=apart)  # twice as a gradient alone is well defined
+    assert torch.equal(apart[0], g) and torch.equal(apart[1], g)
+    for grads, out in (([g, g], None), ([g, buf[50:150]], None), ([g, h], [h, g]), ([g, h], [apart[0], apart[0]]),
+                       ([g, h], [apart[0], g])):
+        with pytest.raises(snack.SnackError) as e:
+            snack.clip_grad_norm(grads, 1.0, out=out)
+        assert e.value.status == 1
+    assert bool((buf == 1).all())

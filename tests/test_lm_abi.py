@@ -134,3 +134,11 @@ def test_python_functions_refuse_cpu_tensors():
                  lambda: snack.xent(torch.zeros(3, 8), table, ids), lambda: snack.clip_grad_norm([table], 1.0)):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("grads,outs", [
+    ((A, A), (A, A)), ((A, A + 200), (A, A + 200)), ((A, B), (B, A)), ((A, B), (A + 4096, A + 4096)), ((A, B), (A + 4096, A)),
+    ((B, A), (B, B + 396)),
+])
+def test_clip_refuses_outputs_on_other_tensors(lib, grads, outs):
+    assert clip(lib, grads=grads, outs=outs) == 1
