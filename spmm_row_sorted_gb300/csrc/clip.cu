@@ -32,7 +32,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int64_t kPiece = 64 * 1024;  // bytes of one tensor per piece of the norm
-// and of the scaling: 64 KB where all of it is in place, and may have nothing to
+// and of the scaling (norm and scaling of 1e9 bf16 elements: 860 us, three passes
+// at 7.0 TB/s): 64 KB where all of it is in place, and may have nothing to
 // do (2 GB of fp32 with the factor 1: 286 us of norm, and 55 us of blocks that
 // return at once at 16 KB each)
 constexpr int64_t kScalePiece = 16 * 1024, kScalePieceInPlace = 64 * 1024;
@@ -305,7 +306,8 @@ __global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__
 
 // A few small tensors: one cluster of kCluster blocks does it all in one
 // launch.  Its threads keep their elements in registers between the norm and
-// the scaling; the blocks' sums meet in the first block's shared memory.
+// the scaling; the blocks' sums meet in every block's shared memory.  Bound by its
+// latencies: 7.4 us for 51,026 elements in four tensors, launch included.
 constexpr int kCluster = 8;
 constexpr int kClusterThreads = 1024;
 constexpr int kKeep = 8;  // elements per thread
@@ -315,7 +317,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kClusterThrea
     k_clip_small(const __grid_constant__ ClipTable<kSmallTable> t, int scale, float max_norm, float *norm) {
   pdl_wait();
   __shared__ Sum3 part[kClusterThreads / 32];
-  __shared__ Sum3 all[kCluster];  // of the first block
+  __shared__ Sum3 all[kCluster];  // every block's sum
   __shared__ float result;
   uint32_t rank;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));

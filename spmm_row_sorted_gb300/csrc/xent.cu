@@ -295,6 +295,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// One product.  4096 tokens against 131072 x 2048 bf16: 1.11 to 1.2 ms each of
+// the four, 1.7 to 1.9 PFLOP/s as the power allows (90 % of the tensor cores'
+// cycles; 80 to 88 % where partial sums are read).
 template <int kMode>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(const __grid_constant__ CUtensorMap map_a,
                                                       const __grid_constant__ CUtensorMap map_b,

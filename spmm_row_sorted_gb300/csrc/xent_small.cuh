@@ -2,7 +2,9 @@
 // cores, reading w as it lies.  The tensor cores would need w cut into bf16
 // parts first, 10 bytes moved per element to save arithmetic that a few tokens
 // do not have; here every pass reads the 4 bytes once (bound by memory up to
-// about 8 tokens, by fp32 arithmetic from there on).  Included by xent.cu.
+// about 8 tokens, by fp32 arithmetic from there on).  Loss and gradients of 3
+// tokens against 129472 x 2784: 1192 us, by way of the tensor cores 3813 (w read
+// three times and dw written, 5.8 GB: 4.8 TB/s).  Included by xent.cu.
 #pragma once
 
 #include "lm.hpp"
@@ -17,8 +19,8 @@ constexpr int kSmallXBytes = 192 * 1024;  // of x in shared memory
 // tokens a kernel is built for, and the rows of w a warp works on at once: their
 // sums stay in registers
 __host__ __device__ constexpr int small_rows(int nt) { return nt <= 4 ? 8 : 4; }
-// of the width in shared memory at a time: all of it up to 12288, 6144 or 3072
-// for 4, 8 or 16 tokens
+// of the width in shared memory at a time: all of it where kSmallXBytes hold the
+// tokens (12288 columns of 4)
 inline int small_k(int nt, int32_t width) {
   const int most = kSmallXBytes / 4 / nt / 128 * 128, all = (width + 127) / 128 * 128;
   return all < most ? all : most;
