@@ -17,7 +17,7 @@
 //          per element and piece, in the pieces' order);
 //   dw     writes the piece's rows of dw.
 // Bound by the tensor cores; for a few tokens by reading w once (a few fp32
-// tokens: xent_small.cuh).
+// tokens: xent_small.cuh and xent_cut.cuh).
 //
 // A pair of CTAs, one per SM, works through output tiles of 256 x up to 256,
 // 128 rows each.  In each CTA a warp loads its rows of A and its half of B by TMA
@@ -56,6 +56,7 @@
 
 #include "internal.hpp"
 #include "lm.hpp"
+#include "xent_cut.cuh"
 #include "xent_small.cuh"
 
 namespace snack {
@@ -1075,7 +1076,9 @@ struct XentShape {
   snack_dtype t;
   bool pack_x, pack_w;
   bool pack_dw;  // bf16 rows of dw that TMA cannot store: by way of the workspace
-  bool few;    // the CUDA-core path of a few fp32 tokens
+  bool few_logits;  // the CUDA cores' logits of a few fp32 tokens,
+  bool few;         // and all of a loss, or of the gradients, there
+  bool cut;    // the loss of some more: w cut into parts in registers
   int parts;
   int32_t ld;  // row length of packed planes
   int sms;
@@ -1093,6 +1096,12 @@ struct XentWs {
   int64_t few_blocks, few_rows;  // blocks of the logits; vocabulary rows per split of dx
 };
 
+// blocks of k_xent_cut: one per SM
+int64_t cut_blocks(const XentShape &s) {
+  const int64_t tiles = ceil_div(s.vocab, (int64_t)cut_rows(s.n, cut_split(s.n, s.vocab, s.width, s.sms)));
+  return tiles < s.sms ? tiles : s.sms;
+}
+
 XentWs xent_ws(const XentShape &s, bool grad) {
   XentWs w = {};
   size_t o = 0;
@@ -1100,8 +1109,8 @@ XentWs xent_ws(const XentShape &s, bool grad) {
   w.err = o;
   o += align_up(256 * 4, kAlign);
   if (s.few) {
-    w.few_nt = s.n <= 4 ? 4 : s.n <= 8 ? 8 : 16;
-    const int64_t tiles = ceil_div(s.vocab, (int64_t)kSmallWarps * small_rows(w.few_nt));
+    w.few_nt = s.few_logits ? kFewMostLogits : s.n <= 8 ? 8 : 16;
+    const int64_t tiles = ceil_div(s.vocab, (int64_t)kSmallWarps * kSmallRows);
     w.few_blocks = tiles < s.sms ? tiles : s.sms;
     w.slots = w.few_blocks;
     if (!grad) {
@@ -1123,6 +1132,17 @@ XentWs xent_ws(const XentShape &s, bool grad) {
       w.acc = o;
       o += align_up((size_t)w.split * (size_t)s.n * (size_t)w.acc_ld * 4, kAlign);
     }
+    w.total = o;
+    return w;
+  }
+  if (s.cut) {
+    w.slots = cut_blocks(s);
+    w.zt = o;
+    o += align_up((size_t)s.n * 4, kAlign);
+    w.row_loss = o;
+    o += align_up((size_t)s.n * 4, kAlign);
+    w.part = o;
+    o += align_up((size_t)w.slots * (size_t)s.n * 8, kAlign);
     w.total = o;
     return w;
   }
@@ -1185,7 +1205,9 @@ XentShape xent_shape(const void *x, int64_t x_ld, int32_t n, const void *wt, int
   s.parts = t == SNACK_F32 ? 3 : 1;
   s.pack_x = grad || t == SNACK_F32 || !rows_ready(x, x_ld, n, grad);  // the gradient's leaves rows out
   s.pack_w = t == SNACK_F32 || !rows_ready(wt, w_ld, n, grad);
-  s.few = t == SNACK_F32 && n <= kSmallMostTokens;
+  s.few_logits = t == SNACK_F32 && few_fits(n, vocab, sms_of());
+  s.few = t == SNACK_F32 && (grad ? n <= kSmallMostTokens : s.few_logits);
+  s.cut = t == SNACK_F32 && !grad && !s.few && cut_fits(n, width);
   s.pack_dw = t == SNACK_BF16 && width % 8 != 0;
   s.ld = (int32_t)align_up((size_t)width, 64);
   s.sms = sms_of();
@@ -1282,18 +1304,37 @@ cudaError_t finish_loss(const float2 *part, int slots, int32_t n, const float *z
   return launch_pdl(k_xent_total, 1, 1024, 0, s, (const float *)row_loss, n, tg, reduction == SNACK_MEAN, loss, state);
 }
 
-template <int kNt, bool kGrad>
-cudaError_t launch_few(const SmallArgs &a, int64_t blocks, cudaStream_t s) {
-  const size_t smem = (size_t)(kNt * a.chunk + kSmallWarps * small_rows(kNt) * (kNt + 1)) * 4;
-  cudaError_t e = raise_smem_limit(k_xent_few<kNt, kGrad>, smem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k_xent_few<kNt, kGrad>, (unsigned)blocks, kSmallWarps * 32, smem, s, a);
-}
 template <bool kGrad>
-cudaError_t run_few(const SmallArgs &a, const XentWs &W, cudaStream_t s) {
-  return W.few_nt == 4   ? launch_few<4, kGrad>(a, W.few_blocks, s)
-         : W.few_nt == 8 ? launch_few<8, kGrad>(a, W.few_blocks, s)
-                         : launch_few<16, kGrad>(a, W.few_blocks, s);
+cudaError_t launch_few(const SmallArgs &a, int64_t blocks, cudaStream_t s) {
+  const size_t smem = (size_t)(kFewMostLogits * a.chunk + kSmallWarps * kSmallRows * (kFewMostLogits + 1)) * 4;
+  cudaError_t e = raise_smem_limit(k_xent_few<kGrad>, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_xent_few<kGrad>, (unsigned)blocks, kSmallWarps * 32, smem, s, a);
+}
+
+template <int kTiles, int kAcross, bool kGrad>
+cudaError_t launch_cut(const CutArgs &a, int64_t blocks, cudaStream_t s) {
+  const size_t smem = cut_smem_bytes(a, kTiles, kAcross);
+  cudaError_t e = raise_smem_limit(k_xent_cut<kTiles, kAcross, kGrad>, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_xent_cut<kTiles, kAcross, kGrad>, (unsigned)blocks, kCutWarps * 32, smem, s, a);
+}
+
+CutArgs cut_args(const XentShape &S, const void *x, int64_t x_ld, const void *w, int64_t w_ld, const TokenSrc &tg) {
+  CutArgs a = {};
+  a.x = reinterpret_cast<const float *>(x);
+  a.w = reinterpret_cast<const float *>(w);
+  a.x_ld = x_ld;
+  a.w_ld = w_ld;
+  a.n = S.n;
+  a.width = S.width;
+  a.vocab = S.vocab;
+  a.chunk = cut_chunk(S.n, S.width);
+  a.split = cut_split(S.n, S.vocab, S.width, S.sms);
+  a.x_wide = ptr_aligned(x, 16) && x_ld % 4 == 0;
+  a.w_wide = ptr_aligned(w, 16) && w_ld % 4 == 0;
+  a.targets = tg;
+  return a;
 }
 
 template <int kNt>
@@ -1315,7 +1356,7 @@ SmallArgs small_args(const XentShape &S, const void *x, int64_t x_ld, const void
   a.vocab = S.vocab;
   a.x_wide = ptr_aligned(x, 16) && x_ld % 4 == 0;
   a.w_wide = ptr_aligned(w, 16) && w_ld % 4 == 0;
-  a.chunk = small_k(S.n <= 4 ? 4 : S.n <= 8 ? 8 : 16, S.width);
+  a.chunk = small_k(S.width);
   a.targets = tg;
   return a;
 }
@@ -1381,7 +1422,18 @@ snack_status snack_xent_fwd(const void *x, int64_t x_ld, int32_t n, const void *
     SmallArgs a = small_args(S, x, x_ld, w, w_ld, tg);
     a.part = part;
     a.zt = zt;
-    XENT_CUDA(run_few<false>(a, W, s));
+    XENT_CUDA(launch_few<false>(a, W.few_blocks, s));
+    XENT_CUDA(finish_loss(part, (int)W.slots, n, zt, tg, reduction, row_loss, loss, state, nullptr, s));
+    return SNACK_OK;
+  }
+  if (S.cut) {
+    CutArgs a = cut_args(S, x, x_ld, w, w_ld, tg);
+    a.part = part;
+    a.zt = zt;
+    XENT_CUDA(n <= 8    ? (launch_cut<1, 1, false>(a, W.slots, s))
+              : n <= 16 ? (launch_cut<2, 1, false>(a, W.slots, s))
+              : n <= 32 ? (launch_cut<4, 1, false>(a, W.slots, s))
+                        : (launch_cut<4, 2, false>(a, W.slots, s)));
     XENT_CUDA(finish_loss(part, (int)W.slots, n, zt, tg, reduction, row_loss, loss, state, nullptr, s));
     return SNACK_OK;
   }
@@ -1449,7 +1501,15 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
     a.lse = state;
     a.weight = weight;
     a.dz = reinterpret_cast<float *>(b + W.dz);
-    XENT_CUDA(run_few<true>(a, W, s));
+    if (S.few_logits) {
+      XENT_CUDA(launch_few<true>(a, W.few_blocks, s));
+    } else {
+      CutArgs c = cut_args(S, x, x_ld, w, w_ld, tg);
+      c.lse = a.lse;
+      c.weight = weight;
+      c.dz = a.dz;
+      XENT_CUDA(n <= 8 ? (launch_cut<1, 1, true>(c, cut_blocks(S), s)) : (launch_cut<2, 1, true>(c, cut_blocks(S), s)));
+    }
     SmallGrad g = {};
     g.x = a.x;
     g.w = a.w;

@@ -1,10 +1,11 @@
-// Cross entropy of a few fp32 tokens: the logits and both gradients on the CUDA
-// cores, reading w as it lies.  The tensor cores would need w cut into bf16
-// parts first, 10 bytes moved per element to save arithmetic that a few tokens
-// do not have; here every pass reads the 4 bytes once (bound by memory up to
-// about 8 tokens, by fp32 arithmetic from there on).  Loss and gradients of 3
-// tokens against 129472 x 2784: 1192 us, by way of the tensor cores 3813 (w read
-// three times and dw written, 5.8 GB: 4.8 TB/s).  Included by xent.cu.
+// Cross entropy of a few fp32 tokens on the CUDA cores, reading w as it lies: the
+// logits of up to 4 tokens (of more: xent_cut.cuh), and both gradients of up to
+// 16.  The tensor cores of the large products would need w cut into bf16 parts
+// first, 10 bytes moved per element to save arithmetic that a few tokens do not
+// have; here every pass reads the 4 bytes once (bound by memory up to about 8
+// tokens, by fp32 arithmetic from there on).  Loss and gradients of 3 tokens
+// against 129472 x 2784: 1192 us, by way of the tensor cores 3813 (w read three
+// times and dw written, 5.8 GB: 4.8 TB/s).  Included by xent.cu.
 #pragma once
 
 #include "lm.hpp"
@@ -12,17 +13,21 @@
 namespace snack {
 namespace {
 
-constexpr int kSmallMostTokens = 16;
+constexpr int kSmallMostTokens = 16;  // of the gradients
+constexpr int kFewMostLogits = 4;     // of k_xent_few
 constexpr int kSmallWarps = 16;
 constexpr int kSmallXBytes = 192 * 1024;  // of x in shared memory
+constexpr int kSmallRows = 8;             // rows of w a warp works on at once: their sums stay in registers
 
-// tokens a kernel is built for, and the rows of w a warp works on at once: their
-// sums stay in registers
-__host__ __device__ constexpr int small_rows(int nt) { return nt <= 4 ? 8 : 4; }
-// of the width in shared memory at a time: all of it where kSmallXBytes hold the
-// tokens (12288 columns of 4)
-inline int small_k(int nt, int32_t width) {
-  const int most = kSmallXBytes / 4 / nt / 128 * 128, all = (width + 127) / 128 * 128;
+// Whether the CUDA cores form the logits: with fewer rows than one tile per SM, warps that share
+// rows are faster (xent_cut.cuh; 4 tokens, 2000 x 4096: 20 us, here 36; 119598 x 2176: 217 and 189).
+inline bool few_fits(int n, int64_t vocab, int sms) {
+  return n <= kFewMostLogits && vocab >= (int64_t)kSmallWarps * kSmallRows * sms;
+}
+
+// of the width in shared memory at a time
+inline int small_k(int32_t width) {
+  const int most = kSmallXBytes / 4 / kFewMostLogits / 128 * 128, all = (width + 127) / 128 * 128;
   return all < most ? all : most;
 }
 
@@ -50,17 +55,17 @@ struct SmallArgs {
   float *zt;     // [n]
   // gradient
   const float *lse, *weight;  // weight: of each row, or null
-  float *dz;                  // [vocab][tokens built for]
+  float *dz;                  // [vocab][kFewMostLogits]
 };
 
-// A block's warps take neighbouring groups of small_rows(kNt) rows of w; a
+// A block's warps take neighbouring groups of kSmallRows rows of w; a
 // lane adds the products of every 32nd four columns for all rows and tokens (x
 // from shared memory, one read for all the rows), and the lanes' sums are added
 // at the end.  kGrad: dz instead of the loss's statistics.
-template <int kNt, bool kGrad>
+template <bool kGrad>
 __global__ void __launch_bounds__(kSmallWarps * 32, 1) k_xent_few(const SmallArgs a) {
   pdl_wait();
-  constexpr int kR = small_rows(kNt), kTile = kSmallWarps * kR;
+  constexpr int kNt = kFewMostLogits, kR = kSmallRows, kTile = kSmallWarps * kR;
   extern __shared__ __align__(16) float few_smem[];
   float *xs = few_smem;                   // [kNt][chunk]
   float *zs = few_smem + kNt * a.chunk;   // [kTile][kNt + 1]

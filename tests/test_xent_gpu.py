@@ -14,6 +14,10 @@ magnitudes, and a bf16 output half an ulp.  E below is the sum over the
 magnitudes g (p + [v = t]) |w| (or |x|).
 """
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -369,3 +373,78 @@ def test_linear_cross_entropy_refuses_a_second_derivative():
     (g,) = torch.autograd.grad(snack.linear_cross_entropy(x, w.contiguous(), t), x, create_graph=True)
     with pytest.raises(RuntimeError):
         g.sum().backward()
+
+
+@pytest.mark.parametrize("n,vocab,width,gap,lead", [
+    (5, 1, 1, 0, 0), (6, 300, 31, 0, 0), (7, 257, 4101, 0, 0), (8, 4500, 64, 4, 4), (12, 255, 33, 0, 3), (13, 2049, 2052, 0, 0),
+    (24, 513, 961, 0, 0), (31, 40000, 36, 0, 0), (33, 129, 449, 0, 1), (48, 3000, 100, 4, 0), (64, 1000, 1300, 0, 0),
+    (64, 200, 2049, 0, 0), (65, 300, 64, 0, 0),
+])
+def test_xent_some_fp32_tokens(n, vocab, width, gap, lead):
+    x, w, t = make(n, vocab, width, "f32", seed=n + vocab, gap=gap, lead=lead, ignored=0.2)
+    up = torch.from_numpy(np.random.default_rng(n).normal(size=n).astype(np.float32)).cuda()
+    r = reference(x, w, t, up.cpu().numpy().astype(np.float64))
+    loss, state = snack.xent(x, w, t, reduction="none")
+    check_loss(loss, r)
+    assert torch.equal(loss, snack.xent(x, w, t, reduction="none")[0])
+    check_grads(*snack.xent_grad(x, w, t, state, up, reduction="none"), r, "f32")
+
+
+@pytest.mark.parametrize("n", [8, 30, 50, 70])
+def test_xent_fp32_not_finite_rows_stay_apart(n):
+    x, w, t = make(n, 700, 96, "f32", seed=n, ignored=0.0)
+    clean, _ = snack.xent(x, w, t, reduction="none")
+    bad = x.clone()
+    bad[1, 3] = float("nan")
+    bad[n - 2, 0] = float("inf")
+    loss, _ = snack.xent(bad, w, t, reduction="none")
+    assert torch.isnan(loss[1]) and not torch.isfinite(loss[n - 2])
+    keep = torch.ones(n, dtype=torch.bool, device="cuda")
+    keep[1] = keep[n - 2] = False
+    assert torch.equal(loss[keep], clean[keep])
+    t[1] = t[n - 2] = -100
+    loss, state = snack.xent(bad, w, t, reduction="none")
+    assert float(loss[1]) == 0.0 and float(loss[n - 2]) == 0.0
+    ones = torch.ones(n, device="cuda")
+    dx, dw = snack.xent_grad(bad, w, t, state, ones, reduction="none")
+    assert bool(torch.isfinite(dx).all()) and bool(torch.isfinite(dw).all()) and not dx[1].any() and not dx[n - 2].any()
+    # a weight that is no number spoils every row's loss, and is not lost on the way
+    w[5, 7] = float("nan")
+    assert bool(torch.isnan(snack.xent(x, w, t, reduction="none")[0][t >= 0]).all())
+
+
+@pytest.mark.parametrize("n", [4, 8, 16, 32, 64, 100])
+def test_xent_fp32_losses_are_fp32(n):
+    # the tensor core rounds sums towards zero: 750 instructions in a row (2000 of K, six part products) would lose
+    # 750 / 2 * 1.4e-8 = 5e-6 of a logit, 1.6e-4 of a loss near 32.  Held to half of that: 2^-20 of lse and what
+    # fp32 sums of this many terms round (2^-18 of a thirtieth of the magnitudes' sum, near the sum's own size)
+    x, w, t = make(n, 2000, 2000, "f32", seed=n, ignored=0.0, spread=8.0)
+    r = reference(x, w, t, np.ones(n))
+    loss, _ = snack.xent(x, w, t, reduction="none")
+    assert np.all(np.abs(f64(loss) - r["loss"]) <= 2.0 ** -18 * r["T"] / 30 + 2.0 ** -20 * np.abs(r["lse"]))
+
+
+@pytest.mark.parametrize("n", [1, 3, 4])
+@pytest.mark.parametrize("vocab", [1, 17, 19455, 19456, 19700])
+def test_xent_a_few_fp32_tokens_of_any_vocabulary(n, vocab):
+    x, w, t = make(n, vocab, 45, "f32", seed=n + vocab, ignored=0.0)
+    r = reference(x, w, t, np.full(n, 0.5))
+    loss, state = snack.xent(x, w, t, reduction="none")
+    check_loss(loss, r)
+    check_grads(*snack.xent_grad(x, w, t, state, torch.full((n,), 0.5, device="cuda"), reduction="none"), r, "f32")
+
+
+def test_xent_first_calls_of_a_process():
+    """Kernels whose shared memory lies near the limit that a launch may use without asking for more."""
+    code = """
+import torch
+from spmm_row_sorted_gb300 import snack
+for n, vocab, width in ((32, 257, 64), (30, 500, 250), (16, 300, 400), (8, 300, 900), (64, 100, 100), (2, 20000, 2900)):
+    x, w = torch.randn(n, width, device="cuda"), torch.randn(vocab, width, device="cuda") / width
+    t = torch.zeros(n, dtype=torch.int64, device="cuda")
+    loss, state = snack.xent(x, w, t)
+    want = torch.nn.functional.cross_entropy(x.double() @ w.double().t(), t)
+    assert abs(float(loss) - float(want)) < 1e-4
+    snack.xent_grad(x, w, t, state)
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
