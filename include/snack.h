@@ -388,7 +388,8 @@ snack_status snack_embed_grad(const void *ids, snack_index ids_t, int64_t n, con
  * so is its row of dx, and dw holds nothing of it, whatever its row of x holds
  * (infinities and NaN too).  loss receives n values (SNACK_NONE), their sum
  * over the trained positions (SNACK_SUM), or that divided by their count
- * (SNACK_MEAN; 0 when there are none).  state (n + 1 fp32 values) keeps each
+ * (SNACK_MEAN; 0 when there are none).  An infinite fp32 operand may give NaN
+ * where the logit is infinite (products are sums over parts of it).  state (n + 1 fp32 values) keeps each
  * row's lse, and 1 / count for the mean, for the gradient.
  */
 typedef enum snack_reduction { SNACK_NONE = 0, SNACK_SUM = 1, SNACK_MEAN = 2 } snack_reduction;
