@@ -1218,8 +1218,12 @@ XentShape xent_shape(const void *x, int64_t x_ld, int32_t n, const void *wt, int
 // costs an exchange of accumulators and a read of 128 KB of tensor memory per
 // CTA (about 1900 cycles beside the MMAs, of 512 a stage).  Sums that become the
 // loss or other fp32 results take units of at most eight stages, of equal
-// length; what is rounded to bf16 (dz, dx and dw of bf16 operands) is far below
-// half its ulp with long ones.  Measured, forward and mean loss against 64 bits
+// length, and so do the gradient's logits: dz = p - 1 of a confident token is far
+// smaller than p, so they have to be the very sums that lse came from (one
+// accumulator over 4096 of K made dz wrong by 2e-4 at logits of 40, at 1 - p of
+// 2e-3; the same units for both cost 1 to 3 % of a large gradient).  What is rounded to
+// bf16 without such a difference (dx and dw of bf16 operands) is far below half
+// its ulp with long ones.  Measured, forward and mean loss against 64 bits
 // (before the partial sums are corrected), for units of 4, 5, 6, 8, 16 and none:
 //   4096 x 131072 x 2048   1306 1253 1178 1112 1064 1058 us   5e-7 6e-7 8e-7 1.1e-6 2.3e-6 4.7e-6
 //   2048 x 65536 x 4096     669  623  582  556  543  539 us   6e-7 8e-7 9e-7 1.3e-6 2.8e-6 1.1e-5
@@ -1239,7 +1243,7 @@ cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtens
   if (!enough) return cudaErrorInvalidDeviceFunction;
   g.m_tiles = (int32_t)ceil_div(g.m, kM);
   g.n_tiles = (int32_t)ceil_div(g.n, g.nt);
-  g.unit = unit_of((int)ceil_div(g.k_blocks, g.n_split), kMode == kStats || g.products > 1);
+  g.unit = unit_of((int)ceil_div(g.k_blocks, g.n_split), kMode == kStats || kMode == kDlog || g.products > 1);
   g.a_rows = kMode == kDw || g.m >= kMCta ? kMCta : (int32_t)align_up((size_t)g.m, 8);
   g.stages = kRing / ((g.a_rows + g.nt / 2) * kKb * 2);
   if (g.stages > kMaxStages) g.stages = kMaxStages;

@@ -448,3 +448,49 @@ for n, vocab, width in ((32, 257, 64), (30, 500, 250), (16, 300, 400), (8, 300, 
     snack.xent_grad(x, w, t, state)
 """
     subprocess.run([sys.executable, "-c", code], check=True, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+
+def confident(n, width, dtype, seed):
+    """Rows of x along their own target's row of w, all operands positive: logits of 40 for the target and near 30 for the
+    63 others, so 1 - p is some 1e-3."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    w = torch.rand(64, width, device="cuda", generator=g).to(DTYPES[dtype])
+    t = torch.arange(n, device="cuda") % 64
+    x = (w[t].float() * (120.0 / width) * (1.0 + torch.rand(n, 1, device="cuda", generator=g) / 16)).to(DTYPES[dtype])
+    return x, w, t
+
+
+@pytest.mark.parametrize("n,width,dtype", [
+    (64, 4096, "bf16"), (40, 2500, "bf16"), (150, 4160, "bf16"), (300, 1000, "bf16"),
+    (4, 4096, "f32"), (16, 4096, "f32"), (64, 4096, "f32"), (100, 4096, "f32"),
+])
+def test_xent_grad_of_confident_tokens(n, width, dtype):
+    # At the target dz = p - 1 cancels to 1e-3, so the gradient's logits have to agree with the loss's far better than
+    # each agrees with 64 bits.  Allowed of dz there: the rounding of lse (2^-19 below 64), of its logarithm, of the sum and of
+    # the exponential (2^-21 each): 2^-18.
+    # Elsewhere p moves by the differences of logits, 2^-14 relative; dz is rounded to bf16 (2^-9) or to fp32 parts;
+    # products lose up to 2^-16 of their magnitudes on the way (2^-20 for fp32).
+    x, w, t = confident(n, width, dtype, seed=n + width)
+    up = torch.full((n,), 1.0, device="cuda")
+    r = reference(x, w, t, np.ones(n))
+    loss, state = snack.xent(x, w, t, reduction="none")
+    dx, dw = snack.xent_grad(x, w, t, state, up, reduction="none")
+    X, W, T = f64(x), f64(w), t.cpu().numpy()
+    z = X @ W.T
+    z -= z.max(1, keepdims=True)
+    p = np.exp(z)
+    p /= p.sum(1, keepdims=True)
+    hot = np.zeros_like(p)
+    hot[np.arange(n), T] = 1.0
+    dz = p - hot
+    dz[np.arange(n), T] = -(p * (1 - hot)).sum(1)  # 1 - p without cancellation
+    assert 1e-4 < -dz[np.arange(n), T].max() and -dz[np.arange(n), T].min() < 5e-2
+    err = (2.0 ** -14 + (2.0 ** -9 if dtype == "bf16" else 2.0 ** -22)) * np.abs(dz) + 2.0 ** -18 * hot
+    product = 2.0 ** -16 if dtype == "bf16" else 2.0 ** -20
+    for got, ref, bound in ((dx, dz @ W, err @ np.abs(W) + product * (np.abs(dz) @ np.abs(W))),
+                            (dw, dz.T @ X, err.T @ np.abs(X) + product * (np.abs(dz).T @ np.abs(X)))):
+        if dtype == "bf16":
+            bound = bound + bf16_half_ulp(np.abs(ref) + bound)
+        off = np.abs(f64(got) - ref) / bound
+        assert off.max() <= 1.0, off.max()
+    assert np.all(np.abs(f64(loss) - r["loss"]) <= 2 * A * r["T"])
