@@ -31,10 +31,10 @@
 //
 // The tensor core's fp32 accumulation rounds towards zero, which over a long K
 // is a bias: a sum of 4096 products came out 5e-6 to 1.4e-5 of itself too small.
-// So an accumulator takes at most 512 of K (32 instructions) where that counts,
-// and the epilogue's warps add the partial sums in registers, rounding to
-// nearest, while the next one forms in the other half of the tensor memory; the
-// logits' are multiplied by what the bias took on average (kLost).
+// So an accumulator takes at most 512 of K (32 instructions; 256 of fp32
+// operands' logits) where that counts, and the epilogue's warps add the partial
+// sums in registers, rounding to nearest, while the next one forms in the other
+// half of the tensor memory.  What is left is at most 1e-6 of a logit (unit_of).
 //
 // fp32 operands are cut into three bf16 parts each (8 significant bits at a
 // time, 24 in all), and a product is the sum of the six part products down to
@@ -217,12 +217,6 @@ constexpr int kM = 256;           // rows of an output tile: 128 (the TMEM lanes
 constexpr int kMCta = kM / 2;
 constexpr int kNMax = 256;        // columns of the widest output tile
 constexpr int kKb = 64;           // K per stage
-// What an accumulation on the tensor core loses of the sum, on average, by
-// rounding towards zero: measured on GB300 for logits of random operands 1.4e-8
-// per instruction (16 of K), 1.7e-8 where the operands are aligned, 3.6e-8 where
-// every product is positive, 0.2e-8 where nine of ten are zero.  The logits'
-// partial sums are multiplied back by it.
-constexpr float kLost = 1.6e-8f;
 constexpr int kEpiWarps = 8;
 constexpr int kChunks = kNMax / 2 / 32;  // 32-column chunks of an epilogue warp's half tile
 constexpr int kThreads = (kEpiWarps + 4) * 32;  // and a warpgroup for the loads and the MMAs (two of its warps idle)
@@ -307,7 +301,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   constexpr bool kAmn = kMode == kDw, kBmn = kMode == kDx || kMode == kDw;
-  constexpr bool kLogits = kMode == kStats || kMode == kDlog;
   const uint32_t rank = cta_rank();  // 0: the leader, which issues the pair's MMAs
   const int nb = P.nt / 2;           // rows of B in each CTA
   // With few rows a stage holds only those of A: the MMAs read 128 rows all the
@@ -503,12 +496,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
       // the tile's sums: one unit after the other, added in fp32
       float acc[kChunks][32];
       const int units = (q.nk + P.unit - 1) / P.unit * (P.products > 1 ? 2 : 1);
-      int left = q.nk;  // stages of the leading product not yet added
       for (int u = 0; u < units; ++u, ++n_acc) {
         const int buf = n_acc & 1;
-        const bool leading = P.products == 1 || (u & 1);
-        const float back = kLogits && leading ? fmaf(kLost, 4.f * (float)min(P.unit, left), 1.f) : 1.f;
-        if (leading) left -= P.unit;
         if (!warp_wait(&acc_full[buf], (n_acc >> 1) & 1)) {
           ok = false;
           break;
@@ -529,12 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
           tmem_wait();
           release();
 #pragma unroll
-          for (int h = 0; h < kChunks; ++h) {
-            tmem_ready(acc[h]);
-            if (kLogits)
-#pragma unroll
-              for (int j = 0; j < 32; ++j) acc[h][j] *= back;
-          }
+          for (int h = 0; h < kChunks; ++h) tmem_ready(acc[h]);
         } else {
 #pragma unroll
           for (int h = 0; h < kChunks; h += 2) {
@@ -546,12 +530,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
             if (h + 2 >= chunks) release();
             tmem_ready(v[0]);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) acc[h][j] = kLogits ? fmaf(v[0][j], back, acc[h][j]) : acc[h][j] + v[0][j];
+            for (int j = 0; j < 32; ++j) acc[h][j] += v[0][j];
             if (h + 1 < chunks) {
               tmem_ready(v[1]);
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                acc[h + 1][j] = kLogits ? fmaf(v[1][j], back, acc[h + 1][j]) : acc[h + 1][j] + v[1][j];
+              for (int j = 0; j < 32; ++j) acc[h + 1][j] += v[1][j];
             }
           }
         }
@@ -1216,18 +1199,22 @@ XentShape xent_shape(const void *x, int64_t x_ld, int32_t n, const void *wt, int
 
 // Units of K stages (64 each): see the note on rounding at the top.  Each unit
 // costs an exchange of accumulators and a read of 128 KB of tensor memory per
-// CTA (about 1900 cycles beside the MMAs, of 512 a stage).  Sums that become the
-// loss or other fp32 results take units of at most eight stages, of equal
-// length, and so do the gradient's logits: dz = p - 1 of a confident token is far
-// smaller than p, so they have to be the very sums that lse came from (one
+// CTA (about 1900 cycles beside the MMAs, of 512 a stage and product).  Sums that
+// become the loss or other fp32 results take units of at most eight stages, of
+// equal length, and so do the gradient's logits: dz = p - 1 of a confident token is
+// far smaller than p, so they have to be the very sums that lse came from (one
 // accumulator over 4096 of K made dz wrong by 2e-4 at logits of 40, at 1 - p of
-// 2e-3; the same units for both cost 1 to 3 % of a large gradient).  What is rounded to
-// bf16 without such a difference (dx and dw of bf16 operands) is far below half
-// its ulp with long ones.  Measured, forward and mean loss against 64 bits
-// (before the partial sums are corrected), for units of 4, 5, 6, 8, 16 and none:
-//   4096 x 131072 x 2048   1306 1253 1178 1112 1064 1058 us   5e-7 6e-7 8e-7 1.1e-6 2.3e-6 4.7e-6
-//   2048 x 65536 x 4096     669  623  582  556  543  539 us   6e-7 8e-7 9e-7 1.3e-6 2.8e-6 1.1e-5
-int unit_of(int k_blocks, bool exact) { return (int)ceil_div(k_blocks, ceil_div(k_blocks, exact ? 8 : 64)); }
+// 2e-3; the same units for both cost 1 to 3 % of a large gradient).  What is rounded
+// to bf16 without such a difference (dx and dw of bf16 operands) is far below half
+// its ulp with long ones.  Logits of fp32 operands take four: six part products
+// hide the reads (1024 x 16384 x 768: 131 us with 8 and with 4, 137 with 2).
+// Measured, relative error of logits of 40 (width 4096) on average, and the loss of
+// 2048 x 65536 x 4096 bf16 and of 67 x 119598 x 2176 fp32, us:
+//   unit   random    positive  nine of ten zero    bf16   fp32
+//      8  -5.9e-7    -8.1e-7    -1.6e-7             568    961
+//      4  -2.9e-7    -3.5e-7    -0.7e-7             678    984
+//      2  -1.5e-7    -1.7e-7    -0.3e-7            1099   1033
+int unit_of(int k_blocks, int most) { return (int)ceil_div(k_blocks, ceil_div(k_blocks, most)); }
 
 template <int kMode>
 cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o, GemmArgs &g, int sms,
@@ -1243,7 +1230,8 @@ cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtens
   if (!enough) return cudaErrorInvalidDeviceFunction;
   g.m_tiles = (int32_t)ceil_div(g.m, kM);
   g.n_tiles = (int32_t)ceil_div(g.n, g.nt);
-  g.unit = unit_of((int)ceil_div(g.k_blocks, g.n_split), kMode == kStats || kMode == kDlog || g.products > 1);
+  const bool logits = kMode == kStats || kMode == kDlog;
+  g.unit = unit_of((int)ceil_div(g.k_blocks, g.n_split), g.products > 1 ? (logits ? 4 : 8) : logits ? 8 : 64);
   g.a_rows = kMode == kDw || g.m >= kMCta ? kMCta : (int32_t)align_up((size_t)g.m, 8);
   g.stages = kRing / ((g.a_rows + g.nt / 2) * kKb * 2);
   if (g.stages > kMaxStages) g.stages = kMaxStages;

@@ -494,3 +494,51 @@ def test_xent_grad_of_confident_tokens(n, width, dtype):
         off = np.abs(f64(got) - ref) / bound
         assert off.max() <= 1.0, off.max()
     assert np.all(np.abs(f64(loss) - r["loss"]) <= 2 * A * r["T"])
+
+
+def operands_of_a_kind(kind, n, width, dtype):
+    """Logits of about 40 for one of 63 rows of w, row 0 of which is zero: the loss of target 0 is lse."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+
+    def some(rows):
+        a = torch.randn(rows, width, device="cuda", generator=g)
+        if kind == "positive":
+            return a.abs()
+        return a * (torch.rand(rows, width, device="cuda", generator=g) < 0.1) if kind == "nine of ten zero" else a
+
+    w = some(64)
+    w[0] = 0.0
+    w = (w * (40.0 / width * (10.0 ** 0.5 if kind == "nine of ten zero" else 1.0))).to(DTYPES[dtype])
+    owner = torch.arange(n, device="cuda") % 63 + 1
+    x = (w[owner].float() * (width / 40.0) + some(n)).to(DTYPES[dtype])
+    return x, w, torch.zeros(n, dtype=torch.int64, device="cuda")
+
+
+@pytest.mark.parametrize("kind", ["random", "positive", "nine of ten zero"])
+@pytest.mark.parametrize("n,dtype", [(256, "bf16"), (16, "f32"), (64, "f32"), (256, "f32")])
+def test_xent_mean_error_of_the_logits(n, dtype, kind):
+    # The accumulator rounds towards zero: an instruction (16 of K) costs a sum of positive products 3.6e-8 of itself at
+    # most, and 32 of them run in a row (16 of fp32 operands), so a logit is up to 1.15e-6 (5.8e-7) too small; rounding
+    # to nearest, elsewhere, leaves less than 1e-7 on average.  Never too large: nothing is put back by guess.
+    x, w, t = operands_of_a_kind(kind, n, 4096, dtype)
+    loss, _ = snack.xent(x, w, t, reduction="none")
+    z = x.double() @ w.double().T
+    mean = float(((loss.double() - torch.logsumexp(z, 1)) / z.amax(1)).mean())
+    assert -(1.15e-6 if dtype == "bf16" else 5.8e-7) <= mean <= 1e-7, mean
+
+
+@pytest.mark.parametrize("n,dtype", [(1, "bf16"), (200, "bf16"), (4, "f32"), (16, "f32"), (64, "f32"), (200, "f32")])
+def test_xent_logits_of_few_bits_are_exact(n, dtype):
+    # whole numbers below 2^9 as logits, and all their partial sums: only lse, its logarithm and the sum of
+    # exponentials round, 2^-24 of lse each at most, and 2^-20 of the loss's other terms
+    g = torch.Generator(device="cuda").manual_seed(n)
+    w = torch.randint(-2, 3, (300, 2048), device="cuda", generator=g) * (torch.rand(300, 2048, device="cuda", generator=g) < 0.1)
+    w[0] = 0
+    owner = torch.arange(n, device="cuda") % 299 + 1
+    x = w[owner]
+    z = x.double() @ w.double().T
+    t = torch.zeros(n, dtype=torch.int64, device="cuda")
+    loss, state = snack.xent(x.to(DTYPES[dtype]), w.to(DTYPES[dtype]), t, reduction="none")
+    lse = torch.logsumexp(z, 1)
+    assert 200.0 < float(lse.amin()) and float(lse.amax()) < 512.0
+    assert bool(((loss.double() - lse).abs() <= 2.0 ** -23 * lse + 2.0 ** -20).all())
