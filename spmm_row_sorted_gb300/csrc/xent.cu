@@ -762,10 +762,10 @@ __global__ void __launch_bounds__(32 * kRows) k_xent_join(const float2 *__restri
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   if (lane == 0 && own < m) {
-    float lse = nm + logf(sum);
-    if (bad) lse = NAN;
-    state[own] = lse;
-    const float l = targets.key(own) < targets.vocab ? lse - zt[own] : 0.f;
+    const float rest = bad ? NAN : logf(sum);
+    state[own] = nm + rest;
+    // not lse - z: a confident token's loss is far below the spacing of lse
+    const float l = targets.key(own) < targets.vocab ? (nm - zt[own]) + rest : 0.f;
     if (kTotal)
       row_loss[warp] = l;
     else

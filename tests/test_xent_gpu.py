@@ -542,3 +542,33 @@ def test_xent_logits_of_few_bits_are_exact(n, dtype):
     lse = torch.logsumexp(z, 1)
     assert 200.0 < float(lse.amin()) and float(lse.amax()) < 512.0
     assert bool(((loss.double() - lse).abs() <= 2.0 ** -23 * lse + 2.0 ** -20).all())
+
+
+@pytest.mark.parametrize("reduction", ["none", "mean"])
+@pytest.mark.parametrize("n,vocab,dtype", [(1, 64, "bf16"), (20, 64, "bf16"), (64, 300, "bf16"), (200, 1000, "bf16"), (3, 64, "f32"),
+                                           (4, 20000, "f32"), (16, 64, "f32"), (64, 64, "f32"), (100, 300, "f32")])
+def test_xent_loss_of_confident_tokens(n, vocab, dtype, reduction):
+    """A loss far below the logits it is the difference of: not rounded to the spacing of lse."""
+    # Operands of few bits, so that every product and sum is exact: logits of 384 + d for the target and 384 and less for
+    # the others.  What is left: differences of logits, each within two fp32 spacings at 384 (2^-14) relative of a
+    # loss; 2^-20 for the exponentials, the sum near 1 and its logarithm.  lse alone has spacing 2^-15.
+    rng = np.random.default_rng(n + vocab)
+    d = rng.integers(14, 26, n) / 2.0
+    x, w = np.zeros((n, 16)), np.zeros((vocab, 16))
+    x[:, 0], w[:, 0] = 24.0, 16.0
+    x[:, 1] = 1.0
+    w[1:, 1] = -rng.integers(0, 9, vocab - 1) / 2.0
+    x[:, 2], w[0, 2] = d, 1.0
+    x, w = (torch.from_numpy(a).to(DTYPES[dtype]).cuda() for a in (x, w))
+    t = torch.zeros(n, dtype=torch.int64, device="cuda")
+    X, W = f64(x), f64(w)
+    z = X @ W.T
+    rest = np.exp(z[:, 1:] - z[:, :1]).sum(1)
+    want = np.log1p(rest)
+    bound = 2.0 ** -14 * want + 2.0 ** -20
+    loss, state = snack.xent(x, w, t, reduction=reduction)
+    if reduction == "mean":
+        assert abs(float(loss) - want.mean()) <= bound.mean()
+    else:
+        assert np.all(np.abs(f64(loss) - want) <= bound)
+    assert np.all(np.abs(f64(state)[:n] - (z[:, 0] + want)) <= 2.0 ** -20 * z[:, 0])
