@@ -536,7 +536,8 @@ class _On:
 
     def __init__(self, device: torch.device, stream):
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
+            # the default stream's handle is 0, of which ExternalStream makes a stream of its own
+            stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
         if stream is not None and stream.device != device:
             raise ValueError("the stream belongs to another device than the tensors")
         self.outer = torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)

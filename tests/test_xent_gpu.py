@@ -572,3 +572,20 @@ def test_xent_loss_of_confident_tokens(n, vocab, dtype, reduction):
     else:
         assert np.all(np.abs(f64(loss) - want) <= bound)
     assert np.all(np.abs(f64(state)[:n] - (z[:, 0] + want)) <= 2.0 ** -20 * z[:, 0])
+
+
+def test_calls_on_the_default_stream_by_its_handle():
+    """The default stream's handle is 0: the call runs there, not on a stream of its own."""
+    x, w, t = make(40, 300, 64, "bf16", seed=3)
+    for handle in (0, torch.cuda.default_stream().cuda_stream, torch.cuda.default_stream()):
+        with snack._On(x.device, handle):
+            assert torch.cuda.current_stream().cuda_stream == 0
+    side = torch.cuda.Stream()
+    for handle in (side, side.cuda_stream):
+        with snack._On(x.device, handle):
+            assert torch.cuda.current_stream().cuda_stream == side.cuda_stream
+    loss, _ = snack.xent(x, w, t)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):  # from another stream
+        assert torch.equal(snack.xent(x, w, t, stream=0)[0].cpu(), loss.cpu())
+    torch.cuda.synchronize()
