@@ -420,7 +420,8 @@ snack_status snack_xent_fwd(const void *x, int64_t x_ld, int32_t n, const void *
  *   dz[i, v] = g_i * (exp(z[i, v] - lse[i]) - [v == targets[i]])
  *   dx = dz w   [n, width],     dw = dz^T x   [vocab, width]      in type t
  * with g_i = dloss[i] (SNACK_NONE), or *dloss (1 when dloss is NULL) times 1
- * (SNACK_SUM) or 1 / count (SNACK_MEAN).  dx or dw may be NULL.  dz is rounded
+ * (SNACK_SUM) or 1 / count (SNACK_MEAN).  dx or dw may be NULL.  A row that is
+ * not trained on stays out also where *dloss is not finite.  dz is rounded
  * to bf16 for bf16 operands and kept to fp32 precision for fp32 ones.
  */
 snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld, int64_t vocab,

@@ -260,7 +260,7 @@ struct GemmArgs {
   float2 *part;             // [slots][m] (maximum, sum of exp(z - maximum)) per half tile
   int32_t slot0;
   float *zt;                // [m] the target's logit
-  // stats, dlog
+  // stats, dlog, dw
   TokenSrc targets;
   int32_t v0;               // first vocabulary row of the piece
   // dlog
@@ -271,6 +271,7 @@ struct GemmArgs {
   int32_t add;              // add to the sums (else write them)
   // dw
   Factor factor;
+  int32_t tokens;           // of `targets`
   void *out;                // first row of the piece; used where TMA cannot store
   int64_t out_ld;
   int32_t out_wide;         // fp32 (else bf16)
@@ -283,6 +284,13 @@ constexpr uint32_t kPartA = 0x001012u, kPartB = 0x010210u;
 // Byte offset of 16-byte chunk c of row r in a warp's staging tile (32 rows
 // of 128 bytes, 128-byte swizzle: what the store's tensor map undoes).
 __device__ __forceinline__ uint32_t stage_off(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+// Whether a row is trained on at all (a converged warp; mostly its first look answers).
+__device__ __forceinline__ bool any_trained(const TokenSrc &targets, int32_t n) {
+  for (int32_t i = threadIdx.x & 31; __any_sync(0xffffffffu, i < n); i += 32)
+    if (__any_sync(0xffffffffu, i < n && targets.key(i) < targets.vocab)) return true;
+  return false;
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
@@ -625,7 +633,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
       } else {
         const bool wide = kMode == kDx || P.out_wide;
         if (kMode == kDw) {
-          const float f = P.factor.get();
+          float f = P.factor.get();
+          if (!isfinite(f) && !any_trained(P.targets, P.tokens)) f = 0.f;  // sums of nothing stay 0
 #pragma unroll
           for (int h = 0; h < kChunks; ++h)
 #pragma unroll
@@ -917,16 +926,18 @@ __global__ void __launch_bounds__(256) k_xent_rows(const bf16 *__restrict__ in, 
   if (lane == 1 && shift + 2 * words < width) row[width - 1] = single[width - 1];
 }
 
-// dx = the splits' sums, added in order and rounded once.  The last kernel of a
-// gradient: after an error it makes dx and the first row of dw NaN.
+// dx = the splits' sums, added in order and rounded once; rows that are left out
+// stay 0 also where the factor is not finite.  The last kernel of a gradient:
+// after an error it makes dx and the first row of dw NaN.
 template <typename T>
 __global__ void __launch_bounds__(256) k_xent_dx(const float *__restrict__ acc, int splits, int64_t plane, int32_t acc_ld,
                                                  int32_t m, int32_t width, T *__restrict__ dx, int64_t ld,
-                                                 T *__restrict__ dw, Factor factor,
+                                                 T *__restrict__ dw, Factor factor, const Drop drop,
                                                  const uint32_t *__restrict__ err) {
   pdl_wait();
   const bool bad = any_error(err);
   const float f = bad ? NAN : factor.get();
+  const bool look = !bad && !isfinite(f);
   if (bad && dw && blockIdx.x == 0)
     for (int i = threadIdx.x; i < width; i += 256) dw[i] = from_f32<T>(NAN);
   const int groups = acc_ld / 4;
@@ -943,7 +954,8 @@ __global__ void __launch_bounds__(256) k_xent_dx(const float *__restrict__ acc, 
       s.w += b.w;
     }
     T *o = dx + r * ld + c;
-    const float e[4] = {s.x * f, s.y * f, s.z * f, s.w * f};
+    const float fr = look && drop.row(r) ? 0.f : f;
+    const float e[4] = {s.x * fr, s.y * fr, s.z * fr, s.w * fr};
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (c + j < width) o[j] = from_f32<T>(e[j]);
@@ -1529,7 +1541,7 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
     if (dx)
       XENT_CUDA(launch_pdl(k_xent_dx<float>, (unsigned)ceil_div((int64_t)n * (W.acc_ld / 4), 256), 256, 0, s,
                            (const float *)g.acc, W.split, (int64_t)n * W.acc_ld, W.acc_ld, n, width,
-                           reinterpret_cast<float *>(dx), dx_ld, (float *)nullptr, factor, (const uint32_t *)nullptr));
+                           reinterpret_cast<float *>(dx), dx_ld, (float *)nullptr, factor, Drop{tg, weight}, (const uint32_t *)nullptr));
     return SNACK_OK;
   }
   const uint32_t a_rows = n >= kMCta ? kMCta : (uint32_t)align_up((size_t)n, 8);
@@ -1587,6 +1599,8 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
       const int64_t out_ld = by_ws ? S.ld : dw_ld;
       h.out = out;
       h.factor = factor;
+      h.targets = tg;
+      h.tokens = n;
       h.out_ld = out_ld;
       h.out_wide = wide;
       h.out_tma = direct || by_ws;
@@ -1608,11 +1622,11 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
   if (wide)
     XENT_CUDA(launch_pdl(k_xent_dx<float>, (unsigned)blocks, 256, 0, s, acc, W.split, (int64_t)n * W.acc_ld, W.acc_ld,
                          dx ? n : 0, width, reinterpret_cast<float *>(dx), dx_ld, reinterpret_cast<float *>(dw), factor,
-                         err));
+                         Drop{tg, weight}, err));
   else
     XENT_CUDA(launch_pdl(k_xent_dx<bf16>, (unsigned)blocks, 256, 0, s, acc, W.split, (int64_t)n * W.acc_ld, W.acc_ld,
                          dx ? n : 0, width, reinterpret_cast<bf16 *>(dx), dx_ld, reinterpret_cast<bf16 *>(dw), factor,
-                         err));
+                         Drop{tg, weight}, err));
   return SNACK_OK;
 } catch (...) {  // a host allocation failed
   return SNACK_ERR_CUDA;

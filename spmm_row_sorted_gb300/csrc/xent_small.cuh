@@ -239,11 +239,11 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_xent_few_grad(const SmallGra
 #pragma unroll
     for (int t = 0; t < kNt; ++t) {
       Cols<kC> &v = x[kDwOut ? t : 0];
-      // rows that are left out add nothing, whatever they hold
+      // rows that are left out add nothing, whatever they and the factor hold
       const bool in = t < a.n && a.targets.key(t) < a.targets.vocab && !(a.weight && a.weight[t] == 0.f);
       v.load(a.x + (in ? t : 0) * a.x_ld + c, in ? left : 0, false);
 #pragma unroll
-      for (int i = 0; i < kC; ++i) v.v[i] *= f;
+      for (int i = 0; i < kC; ++i) v.v[i] = in ? v.v[i] * f : 0.f;
     }
   }
   const int64_t r0 = (int64_t)blockIdx.y * a.rows_per_split;

@@ -589,3 +589,22 @@ def test_calls_on_the_default_stream_by_its_handle():
     with torch.cuda.stream(side):  # from another stream
         assert torch.equal(snack.xent(x, w, t, stream=0)[0].cpu(), loss.cpu())
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("reduction", ["sum", "mean"])
+@pytest.mark.parametrize("n,dtype", [(3, "f32"), (12, "f32"), (40, "f32"), (90, "f32"), (5, "bf16"), (140, "bf16")])
+def test_xent_rows_not_trained_on_stay_out_whatever_the_upstream_gradient(n, dtype, reduction, value):
+    x, w, t = make(n, 300, 72, dtype, seed=n, ignored=0.0)
+    t[n // 2] = -100
+    up = torch.tensor(value, device="cuda")
+    loss, state = snack.xent(x, w, t, reduction=reduction)
+    dx, dw = snack.xent_grad(x, w, t, state, up, reduction=reduction)
+    keep = (t >= 0) & (t < 300)
+    assert not torch.isfinite(dx[keep]).any()
+    assert not dx[~keep].any()  # a NaN counts as not zero
+    assert not torch.isfinite(dw).all()
+    t[:] = -100  # nothing to train on
+    loss, state = snack.xent(x, w, t, reduction=reduction)
+    dx, dw = snack.xent_grad(x, w, t, state, up, reduction=reduction)
+    assert float(loss) == 0.0 and not dx.any() and not dw.any()
