@@ -22,6 +22,7 @@ from typing import Optional
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 from . import build as _build
 
@@ -528,7 +529,8 @@ def sparse_linear(x: torch.Tensor, layer: SparseLinear) -> torch.Tensor:
 #
 # Plain functions on CUDA tensors (float32 or bfloat16; ids and targets int32 or
 # int64).  Outputs and workspaces come from torch's allocator, on the stream
-# that the kernels run on: torch's current one, or `stream`.
+# that the kernels run on: torch's current one, or `stream`.  Tensors that a call
+# writes in place count as modified (autograd refuses to use what it saved of them).
 
 
 class _On:
@@ -626,6 +628,8 @@ def embed(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out: Optio
                                           _raw_stream(None))
     if st:
         _check("snack_embed_fwd", st)
+    if out is not None:
+        increment_version(out)
     return y if out is not None or ids.dim() == 1 else y.view(*ids.shape, width)
 
 
@@ -651,6 +655,8 @@ def embed_grad(ids: torch.Tensor, dout: torch.Tensor, vocab: int, scale: float =
                                            _raw_stream(None))
     if st:
         _check("snack_embed_grad", st)
+    if out is not None:
+        increment_version(out)
     return g
 
 
@@ -694,7 +700,7 @@ def clip_grad_norm(grads, max_norm: float, out=None, stream=None) -> torch.Tenso
     addr = list(map(T.data_ptr, grads))
     if not all(map(T.is_contiguous, grads)) or set(map(T.get_device, grads)) != {first.get_device()}:
         raise ValueError("gradients must be contiguous tensors on one CUDA device")
-    to = addr
+    to, outs = addr, grads
     if out is not None:
         outs = list(out)
         if list(map(T.numel, outs)) != numel or [o.dtype for o in outs] != dtypes \
@@ -707,6 +713,7 @@ def clip_grad_norm(grads, max_norm: float, out=None, stream=None) -> torch.Tenso
         raise ValueError("gradients must be float32 or bfloat16")
     ws = _workspace(_clip_ws(len(grads)), first.device)
     snack_clip_grad_norm(addr, to, numel, types, float(max_norm), norm, ws)
+    increment_version(outs)
     return norm
 
 

@@ -163,3 +163,23 @@ def test_clip_refuses_a_gradient_given_twice():
             snack.clip_grad_norm(grads, 1.0, out=out)
         assert e.value.status == 1
     assert bool((buf == 1).all())
+
+
+def test_tensors_written_in_place_are_seen_by_autograd():
+    g = torch.rand(100, device="cuda")
+    h = torch.rand(50, device="cuda").bfloat16()
+    weight = torch.ones(100, device="cuda", requires_grad=True)
+    y = (weight * g).sum()  # keeps g for its gradient
+    before = g._version, h._version
+    snack.clip_grad_norm([g, h], 1.0)
+    assert g._version > before[0] and h._version > before[1]
+    with pytest.raises(RuntimeError):
+        y.backward()
+    out = [torch.empty_like(g), torch.empty_like(h)]
+    marks = g._version, h._version, out[0]._version, out[1]._version
+    snack.clip_grad_norm([g, h], 1.0, out=out)  # the gradients are read only
+    assert (g._version, h._version) == marks[:2] and out[0]._version > marks[2] and out[1]._version > marks[3]
+    with torch.inference_mode():
+        held = torch.rand(10, device="cuda")
+        snack.clip_grad_norm([held], 1.0)
+    snack.clip_grad_norm([held, g], 1.0)  # no version to keep: as before

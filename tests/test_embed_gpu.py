@@ -249,3 +249,21 @@ def test_embedding_refuses_a_second_derivative():
     (g,) = torch.autograd.grad(y, table, up, create_graph=True)
     with pytest.raises(RuntimeError):
         g.sum().backward()
+
+
+def test_outputs_given_are_seen_by_autograd():
+    table = strided(30, 16, 0, 0, "f32", seed=1)
+    ids = make_ids(8, 30, "uniform", 1, torch.int64)
+    buf = torch.zeros(8, 16, device="cuda")
+    before = buf._version
+    snack.embed(ids, table, out=buf)
+    assert buf._version > before
+    grad = torch.zeros(30, 16, device="cuda")
+    for accumulate in (False, True):
+        before = grad._version
+        snack.embed_grad(ids, buf, 30, out=grad, accumulate=accumulate)
+        assert grad._version > before
+    with torch.inference_mode():
+        held = torch.zeros(8, 16, device="cuda")
+        snack.embed(ids, table, out=held)
+    snack.embed(ids, table, out=held)
