@@ -351,7 +351,9 @@ int snack_version(void);
  * buffer is an argument, they run on the CUDA device current at the call (the
  * stream's), and they keep nothing between calls.  A matrix is row-major with
  * its rows `ld` >= width elements apart, aligned to its element; 16-byte
- * aligned rows run fastest.  Workspaces are 256-byte aligned.  Sums are fp32,
+ * aligned rows run fastest.  Workspaces are 256-byte aligned.  What a call writes,
+ * its workspace too, overlaps none of its other arguments (SNACK_ERR_INVALID_ARG;
+ * clipping in place is the exception).  Sums are fp32,
  * each output is rounded once to its type, and results repeat bit for bit.
  */
 

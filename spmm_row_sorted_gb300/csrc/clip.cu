@@ -484,6 +484,21 @@ snack_status run_clip(const ClipCall &c, cudaStream_t s) {
   return SNACK_OK;
 }
 
+// Whether the norm or the workspace overlaps a tensor of the call, or each other.
+bool clip_scratch_overlaps(int32_t n, const void *const *grads, void *const *outs, const int64_t *numel,
+                           const snack_dtype *types, const float *norm, const void *ws, size_t ws_bytes) {
+  const size_t norm_bytes = norm ? sizeof(float) : 0;
+  if (spans_overlap(norm, norm_bytes, ws, ws_bytes)) return true;
+  for (int32_t k = 0; k < n; ++k) {
+    const size_t bytes = (size_t)numel[k] * dtype_size(types[k]);
+    if (spans_overlap(grads[k], bytes, ws, ws_bytes) || spans_overlap(grads[k], bytes, norm, norm_bytes)) return true;
+    if (outs && outs[k] != grads[k] &&
+        (spans_overlap(outs[k], bytes, ws, ws_bytes) || spans_overlap(outs[k], bytes, norm, norm_bytes)))
+      return true;
+  }
+  return false;
+}
+
 // Whether an output overlaps another tensor of the call: a gradient given twice
 // in place would be scaled twice, or once, as its blocks happen to run.
 bool clip_overlaps(int32_t n, const void *const *grads, void *const *outs, const int64_t *numel, const snack_dtype *types) {
@@ -554,6 +569,7 @@ snack_status snack_clip_grad_norm(int32_t n_tensors, const void *const *grads, v
   if (norm && !ptr_aligned(norm, 4)) return SNACK_ERR_INVALID_ARG;
   if (!ws || !ptr_aligned(ws, kAlign)) return SNACK_ERR_INVALID_ARG;
   if (ws_bytes < clip_ws(n_tensors)) return SNACK_ERR_WORKSPACE;
+  if (clip_scratch_overlaps(n_tensors, grads, outs, numel, types, norm, ws, clip_ws(n_tensors))) return SNACK_ERR_INVALID_ARG;
   ClipCall c = {n_tensors, grads, outs, numel, types, max_norm, norm,
                 reinterpret_cast<Sum3 *>(reinterpret_cast<uint8_t *>(ws) + kAlign), reinterpret_cast<float *>(ws),
                 current_sms()};

@@ -714,6 +714,9 @@ snack_status snack_embed_grad(const void *ids, snack_index ids_t, int64_t n, con
         spans_overlap(dtable, nd, ids, (size_t)n * index_size(ids_t)) || spans_overlap(dtable, nd, ws, ws_bytes))
       return SNACK_ERR_INVALID_ARG;
     if (ws_bytes < W.total) return SNACK_ERR_WORKSPACE;
+    if (spans_overlap(ws, W.total, dout, span_bytes(n, width, dout_ld, es)) ||
+        spans_overlap(ws, W.total, ids, (size_t)n * index_size(ids_t)))
+      return SNACK_ERR_INVALID_ARG;
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t *w = reinterpret_cast<uint8_t *>(ws);

@@ -1377,6 +1377,22 @@ snack_status xent_check(const void *x, int64_t x_ld, int32_t n, const void *w, i
   return SNACK_OK;
 }
 
+struct Span {
+  const void *p;
+  size_t bytes;
+};
+// Whether one of the buffers that a call writes overlaps any other of its buffers (absent ones have no bytes).
+template <int kWritten, int kRead>
+bool any_overlap(const Span (&written)[kWritten], const Span (&read)[kRead]) {
+  for (int i = 0; i < kWritten; ++i) {
+    for (int j = i + 1; j < kWritten; ++j)
+      if (spans_overlap(written[i].p, written[i].bytes, written[j].p, written[j].bytes)) return true;
+    for (const Span &r : read)
+      if (spans_overlap(written[i].p, written[i].bytes, r.p, r.bytes)) return true;
+  }
+  return false;
+}
+
 }  // namespace
 }  // namespace snack
 
@@ -1418,6 +1434,11 @@ snack_status snack_xent_fwd(const void *x, int64_t x_ld, int32_t n, const void *
   const XentShape S = xent_shape(x, x_ld, n, w, w_ld, vocab, width, t, false);
   const XentWs W = xent_ws(S, false);
   if (ws_bytes < W.total) return SNACK_ERR_WORKSPACE;
+  const size_t es = dtype_size(t);
+  const Span written[] = {{loss, (reduction == SNACK_NONE ? (size_t)n : 1) * 4}, {state, ((size_t)n + 1) * 4}, {ws, W.total}};
+  const Span read[] = {{x, span_bytes(n, width, x_ld, es)}, {w, span_bytes(vocab, width, w_ld, es)},
+                       {targets, (size_t)n * index_size(targets_t)}};
+  if (any_overlap(written, read)) return SNACK_ERR_INVALID_ARG;
   uint8_t *b = reinterpret_cast<uint8_t *>(ws);
   float *zt = reinterpret_cast<float *>(b + W.zt);
   float2 *part = reinterpret_cast<float2 *>(b + W.part);
@@ -1486,13 +1507,14 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
   if (!x || !w || !targets || !state || !ws || !ptr_aligned(targets, index_size(targets_t)) || !ptr_aligned(state, 4) ||
       !ptr_aligned(ws, kAlign) || (dloss && !ptr_aligned(dloss, 4)) || (reduction == SNACK_NONE && !dloss))
     return SNACK_ERR_INVALID_ARG;
-  const size_t nx = span_bytes(n, width, x_ld, es), nw = span_bytes(vocab, width, w_ld, es);
-  const size_t ndx = dx ? span_bytes(n, width, dx_ld, es) : 0, ndw = dw ? span_bytes(vocab, width, dw_ld, es) : 0;
-  if (spans_overlap(dx, ndx, x, nx) || spans_overlap(dx, ndx, w, nw) || spans_overlap(dw, ndw, x, nx) ||
-      spans_overlap(dw, ndw, w, nw) || spans_overlap(dx, ndx, dw, ndw))
-    return SNACK_ERR_INVALID_ARG;
   const XentShape S = xent_shape(x, x_ld, n, w, w_ld, vocab, width, t, true);
   const XentWs W = xent_ws(S, true);
+  const Span written[] = {{dx, dx ? span_bytes(n, width, dx_ld, es) : 0}, {dw, dw ? span_bytes(vocab, width, dw_ld, es) : 0},
+                          {ws, std::min(ws_bytes, W.total)}};
+  const Span read[] = {{x, span_bytes(n, width, x_ld, es)}, {w, span_bytes(vocab, width, w_ld, es)},
+                       {targets, (size_t)n * index_size(targets_t)}, {state, ((size_t)n + 1) * 4},
+                       {dloss, dloss ? (reduction == SNACK_NONE ? (size_t)n : 1) * 4 : 0}};
+  if (any_overlap(written, read)) return SNACK_ERR_INVALID_ARG;
   if (ws_bytes < W.total) return SNACK_ERR_WORKSPACE;
   if (!dx && !dw) return SNACK_OK;
   uint8_t *b = reinterpret_cast<uint8_t *>(ws);
