@@ -1073,7 +1073,7 @@ struct XentShape {
   bool pack_dw;  // bf16 rows of dw that TMA cannot store: by way of the workspace
   bool few_logits;  // the CUDA cores' logits of a few fp32 tokens,
   bool few;         // and all of a loss, or of the gradients, there
-  bool cut;    // the loss of some more: w cut into parts in registers
+  bool cut;    // the logits of some more: w cut into parts in registers
   int parts;
   int32_t ld;  // row length of packed planes
   int sms;
@@ -1091,9 +1091,9 @@ struct XentWs {
   int64_t few_blocks, few_rows;  // blocks of the logits; vocabulary rows per split of dx
 };
 
-// blocks of k_xent_cut: one per SM
-int64_t cut_blocks(const XentShape &s) {
-  const int64_t tiles = ceil_div(s.vocab, (int64_t)cut_rows(s.n, cut_split(s.n, s.vocab, s.width, s.sms)));
+// blocks of k_xent_cut for `rows` of the vocabulary: one per SM
+int64_t cut_blocks(const XentShape &s, int64_t rows) {
+  const int64_t tiles = ceil_div(rows, (int64_t)cut_rows(s.n, cut_split(s.n, s.vocab, s.width, s.sms)));
   return tiles < s.sms ? tiles : s.sms;
 }
 
@@ -1130,8 +1130,8 @@ XentWs xent_ws(const XentShape &s, bool grad) {
     w.total = o;
     return w;
   }
-  if (s.cut) {
-    w.slots = cut_blocks(s);
+  if (s.cut && !grad) {
+    w.slots = cut_blocks(s, s.vocab);
     w.zt = o;
     o += align_up((size_t)s.n * 4, kAlign);
     w.row_loss = o;
@@ -1202,7 +1202,7 @@ XentShape xent_shape(const void *x, int64_t x_ld, int32_t n, const void *wt, int
   s.pack_w = t == SNACK_F32 || !rows_ready(wt, w_ld, n, grad);
   s.few_logits = t == SNACK_F32 && few_fits(n, vocab, sms_of());
   s.few = t == SNACK_F32 && (grad ? n <= kSmallMostTokens : s.few_logits);
-  s.cut = t == SNACK_F32 && !grad && !s.few && cut_fits(n, width);
+  s.cut = t == SNACK_F32 && !s.few && cut_fits(n, width);
   s.pack_dw = t == SNACK_BF16 && width % 8 != 0;
   s.ld = (int32_t)align_up((size_t)width, 64);
   s.sms = sms_of();
@@ -1322,6 +1322,15 @@ cudaError_t launch_cut(const CutArgs &a, int64_t blocks, cudaStream_t s) {
   cudaError_t e = raise_smem_limit(k_xent_cut<kTiles, kAcross, kGrad>, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_xent_cut<kTiles, kAcross, kGrad>, (unsigned)blocks, kCutWarps * 32, smem, s, a);
+}
+
+// the kernel for the call's tokens
+template <bool kGrad>
+cudaError_t launch_cut_for(const CutArgs &a, int64_t blocks, cudaStream_t s) {
+  return a.n <= 8    ? launch_cut<1, 1, kGrad>(a, blocks, s)
+         : a.n <= 16 ? launch_cut<2, 1, kGrad>(a, blocks, s)
+         : a.n <= 32 ? launch_cut<4, 1, kGrad>(a, blocks, s)
+                     : launch_cut<4, 2, kGrad>(a, blocks, s);
 }
 
 CutArgs cut_args(const XentShape &S, const void *x, int64_t x_ld, const void *w, int64_t w_ld, const TokenSrc &tg) {
@@ -1455,10 +1464,7 @@ snack_status snack_xent_fwd(const void *x, int64_t x_ld, int32_t n, const void *
     CutArgs a = cut_args(S, x, x_ld, w, w_ld, tg);
     a.part = part;
     a.zt = zt;
-    XENT_CUDA(n <= 8    ? (launch_cut<1, 1, false>(a, W.slots, s))
-              : n <= 16 ? (launch_cut<2, 1, false>(a, W.slots, s))
-              : n <= 32 ? (launch_cut<4, 1, false>(a, W.slots, s))
-                        : (launch_cut<4, 2, false>(a, W.slots, s)));
+    XENT_CUDA(launch_cut_for<false>(a, W.slots, s));
     XENT_CUDA(finish_loss(part, (int)W.slots, n, zt, tg, reduction, row_loss, loss, state, nullptr, s));
     return SNACK_OK;
   }
@@ -1534,7 +1540,7 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
       c.lse = a.lse;
       c.weight = weight;
       c.dz = a.dz;
-      XENT_CUDA(n <= 8 ? (launch_cut<1, 1, true>(c, cut_blocks(S), s)) : (launch_cut<2, 1, true>(c, cut_blocks(S), s)));
+      XENT_CUDA(launch_cut_for<true>(c, cut_blocks(S, vocab), s));
     }
     SmallGrad g = {};
     g.x = a.x;
@@ -1577,28 +1583,41 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
   int first = 1;
   for (int64_t v0 = 0; v0 < vocab; v0 += W.piece) {
     const int64_t rows = vocab - v0 < W.piece ? vocab - v0 : W.piece;
-    XENT_CUDA(operand(S, S.pack_w, w, w_ld, v0, rows, b + W.wp, &ow, s));
+    if (dx || !S.cut) XENT_CUDA(operand(S, S.pack_w, w, w_ld, v0, rows, b + W.wp, &ow, s));
     const Operand dz = {b + W.dz, n, W.dz_ld, (int64_t)n * W.dz_ld, (int32_t)rows, S.parts};
-    const int nt = tile_cols(ceil_div(n, kM), rows, S.sms);
-    if (!load_map(&mw, ow, false, (uint32_t)nt / 2) || !load_map(&mwt, ow, true, 0) || !load_map(&mdz, dz, false, a_rows) ||
-        !load_map(&mdzt, dz, true, 0) ||
-        !make_map(&mdz_out, dz.p, false, (uint64_t)rows, (uint64_t)n, (uint64_t)W.dz_ld, (uint64_t)S.parts,
-                  (uint64_t)dz.plane, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+    if (!load_map(&mdz, dz, false, a_rows) || !load_map(&mdzt, dz, true, 0) || (dx && !load_map(&mwt, ow, true, 0)))
       return SNACK_ERR_CUDA;
-    GemmArgs g = gemm_args(S, b, W, first);
-    g.m = n;
-    g.n = (int32_t)rows;
-    g.nt = nt;
-    g.k_blocks = (int32_t)ceil_div(width, kKb);
-    g.targets = tg;
-    g.v0 = (int32_t)v0;
-    g.lse = state;
-    g.dloss = weight;
-    g.out_parts = S.parts;
-    XENT_CUDA(launch_gemm<kDlog>(mx, mw, mdz_out, g, S.sms, s));
-    first = 0;
+    if (S.cut) {  // as the loss's were
+      CutArgs c = cut_args(S, x, x_ld, reinterpret_cast<const float *>(w) + v0 * w_ld, w_ld, tg);
+      c.vocab = rows;
+      c.v0 = (int32_t)v0;
+      c.lse = state;
+      c.weight = weight;
+      c.dz_parts = reinterpret_cast<bf16 *>(b + W.dz);
+      c.dz_ld = W.dz_ld;
+      c.plane = dz.plane;
+      XENT_CUDA(launch_cut_for<true>(c, cut_blocks(S, rows), s));
+    } else {
+      const int nt = tile_cols(ceil_div(n, kM), rows, S.sms);
+      if (!load_map(&mw, ow, false, (uint32_t)nt / 2) ||
+          !make_map(&mdz_out, dz.p, false, (uint64_t)rows, (uint64_t)n, (uint64_t)W.dz_ld, (uint64_t)S.parts,
+                    (uint64_t)dz.plane, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+        return SNACK_ERR_CUDA;
+      GemmArgs g = gemm_args(S, b, W, first);
+      g.m = n;
+      g.n = (int32_t)rows;
+      g.nt = nt;
+      g.k_blocks = (int32_t)ceil_div(width, kKb);
+      g.targets = tg;
+      g.v0 = (int32_t)v0;
+      g.lse = state;
+      g.dloss = weight;
+      g.out_parts = S.parts;
+      XENT_CUDA(launch_gemm<kDlog>(mx, mw, mdz_out, g, S.sms, s));
+      first = 0;
+    }
     if (dx) {
-      GemmArgs h = gemm_args(S, b, W, 0);
+      GemmArgs h = gemm_args(S, b, W, first);
       h.m = n;
       h.n = width;
       h.nt = W.nt_d;
@@ -1606,9 +1625,10 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
       h.k_blocks = (int32_t)ceil_div(rows, kKb);
       h.add = v0 > 0;
       XENT_CUDA(launch_gemm<kDx>(mdz, mwt, macc, h, S.sms, s));
+      first = 0;
     }
     if (dw) {
-      GemmArgs h = gemm_args(S, b, W, 0);
+      GemmArgs h = gemm_args(S, b, W, first);
       h.m = (int32_t)rows;
       h.n = width;
       h.nt = W.nt_d;
@@ -1630,6 +1650,7 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
                                  (uint64_t)rows * (uint64_t)out_ld, wide ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
         return SNACK_ERR_CUDA;
       XENT_CUDA(launch_gemm<kDw>(mdzt, mxt, h.out_tma ? mdw : mxt, h, S.sms, s));
+      first = 0;
       if (by_ws)
         XENT_CUDA(launch_pdl(k_xent_rows, (unsigned)ceil_div(rows, 8), 256, 0, s, reinterpret_cast<const bf16 *>(out),
                              out_ld, rows, width, reinterpret_cast<bf16 *>(to), dw_ld));

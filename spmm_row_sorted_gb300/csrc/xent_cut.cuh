@@ -40,7 +40,10 @@ struct CutArgs {
   float *zt;     // [n]
   // gradient
   const float *lse, *weight;  // weight: of each row, or null
-  float *dz;                  // [vocab][tokens built for]
+  int32_t v0;                 // first vocabulary row of w here, which may be a piece of it
+  float *dz;                  // [vocab][tokens built for],
+  bf16 *dz_parts;             //  or its three bf16 parts [3][n][dz_ld], `plane` elements apart
+  int64_t dz_ld, plane;
 };
 
 // fp32 losses that run here.  Above 32 tokens two warps read (and cut) each row of
@@ -110,7 +113,9 @@ __device__ __forceinline__ void drop_top(float &v) { v -= __uint_as_float(__floa
 // x; w's are cut off without rounding, three of 8 bits.  The tensor core rounds
 // sums towards zero, so it only adds up 32 of K, the ten small part products
 // before the two leading ones; those sums are added in fp32.  kGrad: dz instead of
-// the loss's statistics.
+// the loss's statistics, from the very same logits: a confident token's dz = p - 1
+// shows what two ways of summing them differ by (17 to 64 tokens against logits of
+// the large products: 1e-5 where 1 - p was 2e-3).
 template <int kTiles, int kAcross, bool kGrad>
 __global__ void __launch_bounds__(kCutWarps * 32, 1) k_xent_cut(const CutArgs a) {
   pdl_wait();
@@ -279,8 +284,19 @@ __global__ void __launch_bounds__(kCutWarps * 32, 1) k_xent_cut(const CutArgs a)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int64_t r = r0 + 8 * h;
+            if (r >= a.vocab) continue;
             const float p = expf(acc[j][2 * h + e] - lse);
-            if (r < a.vocab) a.dz[r * kTokens + t] = u != 0.f ? u * ((int64_t)id == r ? p - 1.f : p) : 0.f;
+            float d = u != 0.f ? u * ((int64_t)id == a.v0 + r ? p - 1.f : p) : 0.f;
+            if (!a.dz_parts) {
+              a.dz[r * kTokens + t] = d;
+            } else if (t < a.n) {
+#pragma unroll
+              for (int k = 0; k < 3; ++k) {
+                const bf16 part = __float2bfloat16_rn(d);
+                a.dz_parts[k * a.plane + t * a.dz_ld + r] = part;
+                d -= __bfloat162float(part);
+              }
+            }
           }
           continue;
         }

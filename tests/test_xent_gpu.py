@@ -463,6 +463,7 @@ def confident(n, width, dtype, seed):
 @pytest.mark.parametrize("n,width,dtype", [
     (64, 4096, "bf16"), (40, 2500, "bf16"), (150, 4160, "bf16"), (300, 1000, "bf16"),
     (4, 4096, "f32"), (16, 4096, "f32"), (64, 4096, "f32"), (100, 4096, "f32"),
+    (17, 4096, "f32"), (32, 4096, "f32"), (64, 512, "f32"),
 ])
 def test_xent_grad_of_confident_tokens(n, width, dtype):
     # At the target dz = p - 1 cancels to 1e-3, so the gradient's logits have to agree with the loss's far better than
