@@ -267,3 +267,38 @@ def test_outputs_given_are_seen_by_autograd():
         held = torch.zeros(8, 16, device="cuda")
         snack.embed(ids, table, out=held)
     snack.embed(ids, table, out=held)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n,vocab,width,dtype,kind", [
+    (4095, 3000, 24, "f32", "skewed"), (4096, 3000, 24, "f32", "padded"),  # places counted up to 4096 tokens,
+    (4097, 3000, 24, "f32", "padded"), (9000, 511, 24, "bf16", "skewed"),  # from there sorted by one cluster of blocks:
+    (20000, 512, 16, "f32", "uniform"),                                    #  keys of nine bits, of ten (two passes),
+    (30000, 2 ** 18 - 1, 8, "bf16", "skewed"),                             #  of 18 (two passes of nine),
+    (30000, 2 ** 18, 8, "bf16", "padded"), (65535, 2 ** 21, 2, "f32", "uniform"),  # of 19 and 22 (three),
+    (5000, 2 ** 27 + 1, 1, "bf16", "skewed"), (65536, 2 ** 28, 1, "bf16", "padded"),  # of 28 and 29 (four);
+    (65536, 700, 16, "f32", "one"), (65536, 700, 16, "f32", "padded"),
+    (65537, 700, 16, "f32", "padded"), (65537, 2 ** 18, 8, "bf16", "skewed"),  # and over the whole device above 65536:
+    (200001, 70000, 4, "f32", "uniform"), (70000, 2 ** 27 + 1, 1, "bf16", "uniform"),  # three and four bytes of a key
+    (300000, 9, 40, "f32", "skewed"),                                          # long runs over many chunks
+])
+def test_embed_grad_sorts_of_every_size(n, vocab, width, dtype, kind, accumulate):
+    ids = make_ids(n, vocab, kind, n + vocab, torch.int64 if n % 2 else torch.int32)
+    dout = strided(n, width, 0, 0, dtype, seed=n)
+    start = torch.full((vocab, width), 0.75, device="cuda", dtype=DTYPES[dtype])
+    out = start.clone()
+    snack.embed_grad(ids, dout, vocab, 0.5, out=out, accumulate=accumulate)
+    inside = (ids >= 0) & (ids < vocab)
+    rows, at, m = torch.unique(ids[inside].long(), return_inverse=True, return_counts=True)
+    d = dout[inside].double()
+    ref = torch.zeros(len(rows), width, device="cuda", dtype=torch.float64).index_add_(0, at, d) * 0.5
+    mag = torch.zeros(len(rows), width, device="cuda", dtype=torch.float64).index_add_(0, at, d.abs()) * 0.5
+    bound = (m[:, None] + 2) * U * mag
+    if accumulate:
+        ref, bound = ref + 0.75, bound + U * (mag + 0.75)
+    got = out[rows]
+    if dtype == "bf16":
+        bound = bound + torch.from_numpy(bf16_half_ulp((ref.abs() + bound).cpu().numpy())).cuda()
+    assert bool(((got.double() - ref).abs() <= bound).all())
+    out[rows] = start[0, 0] if accumulate else 0  # every other row: as it was, or zero
+    assert torch.equal(out, start if accumulate else torch.zeros_like(start))
