@@ -609,3 +609,130 @@ def test_xent_rows_not_trained_on_stay_out_whatever_the_upstream_gradient(n, dty
     loss, state = snack.xent(x, w, t, reduction=reduction)
     dx, dw = snack.xent_grad(x, w, t, state, up, reduction=reduction)
     assert float(loss) == 0.0 and not dx.any() and not dw.any()
+
+
+def piece_targets(n, vocab, seed):
+    """Targets over the whole vocabulary, many of them on either side of multiples of 256: where pieces of it may end."""
+    rng = np.random.default_rng(seed)
+    t = rng.integers(0, vocab, n)
+    edges = np.arange(1, (vocab + 255) // 256) * 256
+    near = rng.choice(edges, n // 2) - rng.integers(0, 2, n // 2)
+    t[:n // 2] = near
+    for pair in (19456, 77824):  # whole waves of tiles of a GPU of 152 multiprocessors
+        e = np.arange(pair, vocab, pair)
+        k = min(len(e), n // 8)
+        t[n // 2:n // 2 + k], t[n // 2 + k:n // 2 + 2 * k] = e[:k], e[:k] - 1
+    t[-1], t[-2], t[-3] = vocab - 1, 0, -100
+    return torch.from_numpy(t).cuda()
+
+
+@pytest.mark.parametrize("n,vocab,width,dtype,spread", [
+    (70, 120000, 512, "f32", 3.0),     # w's three parts, 369 MB: two pieces of the loss and of the gradient
+    (70, 120000, 512, "f32", 0.03),    # nearly equal logits: what the products round shows
+    (60, 120000, 512, "f32", 3.0),     # the same with w cut as it is read
+    (3000, 40000, 64, "f32", 3.0),     # dz's three parts, 720 MB: several pieces of the gradient alone
+    (80, 300001, 513, "bf16", 3.0),    # rows that are laid out again, 346 MB: several pieces of both
+    (4200, 70000, 136, "bf16", 3.0),   # dz of 588 MB; rows off 128-byte lines
+])
+def test_xent_in_several_pieces_of_every_kind(n, vocab, width, dtype, spread):
+    x, w, _ = make(n, vocab, width, dtype, seed=n + width, spread=spread)
+    t = piece_targets(n, vocab, n)
+    inside = (t >= 0) & (t < vocab)
+    count = int(inside.sum())
+    X, W = x.double(), w.double()
+    at = torch.where(inside, t, 0)[:, None]
+    loss, state = snack.xent(x, w, t, reduction="none")
+    mean, kept = snack.xent(x, w, t)
+    dx, dw = snack.xent_grad(x, w, t, kept)
+    T = float(w.abs().double().sum(1).max()) * float(x.abs().max())  # above every row's sum of magnitudes
+    T = min(T, float((X[:64].abs() @ W.abs().T).max()) * 1.5)
+    want, lse = torch.empty(n, device="cuda", dtype=torch.float64), torch.empty(n, device="cuda", dtype=torch.float64)
+    ref_x, mag_x = torch.zeros_like(X), torch.zeros_like(X)
+    ref_w, mag_w = torch.zeros_like(W), torch.zeros_like(W)
+    for a in range(0, n, 512):  # rows at a time: the logits in 64 bits are large
+        s = slice(a, min(n, a + 512))
+        z = X[s] @ W.T
+        lse[s] = torch.logsumexp(z, 1)
+        want[s] = torch.where(inside[s], lse[s] - z.gather(1, at[s])[:, 0], 0.0)
+        p = torch.exp(z - lse[s][:, None])
+        del z
+        weight = (inside[s].double() / count)[:, None]
+        p *= weight
+        mag = p.clone().scatter_add_(1, at[s], weight)
+        p.scatter_add_(1, at[s], -weight)
+        ref_x[s], mag_x[s] = p @ W, mag @ W.abs()
+        ref_w += p.T @ X[s]
+        mag_w += mag.T @ X[s].abs()
+        del p, mag
+    bound = 2 * A * T + 2.0 ** -16 + 2.0 ** -22 * lse.abs()
+    assert bool(((loss.double() - want).abs() <= bound).all())
+    assert abs(float(mean) - float(want.sum()) / count) <= float(bound.max()) + 2.0 ** -23 * abs(float(mean))
+    e = 2 * A * T + 2.0 ** -16 + A + (2.0 ** -8 if dtype == "bf16" else 2.0 ** -22)
+    for got, ref, mag in ((dx, ref_x, mag_x), (dw, ref_w, mag_w)):
+        tol = e * mag
+        if dtype == "bf16":
+            tol = tol + torch.from_numpy(bf16_half_ulp((ref.abs() + tol).cpu().numpy())).cuda()
+        assert bool(((got.double() - ref).abs() <= tol + 1e-300).all())
+    assert not dx[~inside].any()
+
+
+@pytest.mark.parametrize("n,vocab,width", [(64, 300, 513), (64, 300, 1000), (130, 700, 4160), (20, 1000, 2048), (260, 513, 1100)])
+def test_xent_bf16_widths_of_several_units(n, vocab, width):
+    """More of K than the tensor core sums at a time."""
+    x, w, t = make(n, vocab, width, "bf16", seed=n + width)
+    up = torch.from_numpy(np.random.default_rng(n).normal(size=n).astype(np.float32)).cuda()
+    r = reference(x, w, t, up.cpu().numpy().astype(np.float64))
+    loss, state = snack.xent(x, w, t, reduction="none")
+    check_loss(loss, r)
+    check_grads(*snack.xent_grad(x, w, t, state, up, reduction="none"), r, "bf16")
+
+
+def few_terms(n, vocab, width, seed):
+    """Nearly equal logits (sums of tiny values), so that dz is known to fp32 and a gradient shows what its products round:
+    two rows that are trained on (dw's sums have two terms), and a vocabulary of `vocab` (dx's)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(n, width, device="cuda", generator=g)
+    w = torch.randn(vocab, width, device="cuda", generator=g) * 2.0 ** -10
+    t = torch.full((n,), -100, dtype=torch.int64, device="cuda")
+    t[1], t[n - 1] = 0, vocab - 1
+    return x, w, t
+
+
+def parts_of(a, parts):
+    """a as a sum of `parts` bf16 values, each the rounding of what the ones before leave over."""
+    out = np.zeros_like(a)
+    for _ in range(parts):
+        out += torch.from_numpy((a - out).astype(np.float32)).to(torch.bfloat16).double().numpy()
+    return out
+
+
+@pytest.mark.parametrize("n,vocab,width", [
+    (2, 3, 64), (4, 20000, 40), (4, 3, 300), (8, 2, 64), (16, 3, 129),   # the CUDA cores
+    (17, 3, 64), (33, 2, 100), (64, 3, 520), (65, 3, 64), (100, 2, 777), (300, 3, 256), (100, 200, 64),  # the tensor cores
+])
+def test_xent_fp32_gradients_are_fp32(n, vocab, width):
+    # p = exp(z - lse): lse and its logarithm round to 2^-24 of lse < 16 each, the exponent's argument to as much, 2^x to 2^-22:
+    # 2^-19.5 of p at lse = 10, 2^-21 near log 3.  At the target the difference rounds once more, 2^-24.
+    # A product of parts leaves out 2^-23 of itself, its sum of a few terms rounds to 2^-22 of the magnitudes, the
+    # factor and the output to 2^-23.
+    x, w, t = few_terms(n, vocab, width, seed=n + vocab)
+    X, W, T = f64(x), f64(w), t.cpu().numpy()
+    inside = T >= 0
+    z = X @ W.T
+    lse = np.log(np.exp(z).sum(1))
+    p = np.where(inside[:, None], np.exp(z - lse[:, None]), 0.0)
+    hot = np.zeros_like(p)
+    hot[np.arange(n)[inside], T[inside]] = 1.0
+    dz = (p - hot) / inside.sum()
+    err = (2.0 ** -23 * (4 + 1.5 * np.abs(lse))[:, None] * p + 2.0 ** -24 * hot) / inside.sum()
+    product = 2.0 ** -23 + 2.0 ** -22 + 2.0 ** -23
+    loss, state = snack.xent(x, w, t)
+    dx, dw = snack.xent_grad(x, w, t, state)
+    for got, a, b, e in ((dx, dz, W, err), (dw, dz.T, X, err.T)):
+        ref, mag = a @ b, np.abs(a) @ np.abs(b)
+        bound = e @ np.abs(b) + product * mag + 2.0 ** -149
+        off = np.abs(f64(got) - ref) / bound
+        assert off.max() <= 1.0, off.max()
+        # the same with two parts of either operand would be outside: of dz where its terms are few and its values several
+        assert (np.abs(a @ parts_of(b, 2) - ref) > bound).any()
+        assert n < 8 or (np.abs(parts_of(a, 2) @ b - ref) > bound).any()
