@@ -10,7 +10,7 @@
 // forward's logits, the same again for the gradient, dx and dw), all by one
 // kernel with four epilogues:
 //   stats  keeps of a logits tile only each row's maximum and sum of
-//          exponentials, per half tile, and the target's logit;
+//          exponentials, per half tile, without the target's;
 //   dlog   turns a logits tile into dz, stored as bf16 for one piece of the
 //          vocabulary;
 //   dx     adds dz w of the piece to fp32 sums (a TMA reduction: one addition
@@ -35,6 +35,10 @@
 // operands' logits) where that counts, and the epilogue's warps add the partial
 // sums in registers, rounding to nearest, while the next one forms in the other
 // half of the tensor memory.  What is left is at most 1e-6 of a logit (unit_of).
+// The target's logit, of which loss and dz = p - 1 are small differences, does not
+// come from there: a warp per row forms it in fp32 (target_logit), the same bits for
+// the loss and the gradient.  (With it from the tensor core the losses of 2048 x 65536 x
+// 4096 were 1.2e-6 of themselves off, so they are 1.8e-7.)
 //
 // fp32 operands are cut into three bf16 parts each (8 significant bits at a
 // time, 24 in all), and a product is the sum of the six part products down to
@@ -259,12 +263,11 @@ struct GemmArgs {
   // stats
   float2 *part;             // [slots][m] (maximum, sum of exp(z - maximum)) per half tile
   int32_t slot0;
-  float *zt;                // [m] the target's logit
   // stats, dlog, dw
   TokenSrc targets;
   int32_t v0;               // first vocabulary row of the piece
   // dlog
-  const float *lse;         // [m]
+  const float *lse, *zt;    // [m] each, zt: the target's logit
   const float *dloss;       // upstream gradient of each row, or null (1: a common factor is applied to the sums)
   int32_t out_parts;        // bf16 parts of dz
   // dx
@@ -488,7 +491,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
       const int col0 = q.n0 + half * width0;
       // the target's column of this tile's half, or below zero
       int tcol = -1;
-      float lse = 0.f, g = 0.f;
+      float lse = 0.f, g = 0.f, hot = 0.f;  // hot: dz at the target
       if (kMode == kStats || kMode == kDlog) {
         if (row_ok) {
           const uint32_t id = P.targets.key(row);
@@ -497,6 +500,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
             if (kMode == kDlog) {
               lse = P.lse[row];
               g = P.dloss ? P.dloss[row] : 1.f;
+              if (tcol >= 0 && tcol < c_end) hot = g * expm1f(P.zt[row] - lse);
             }
           }
         }
@@ -561,12 +565,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
             for (int j = 0; j < 32; ++j)
               if (j >= valid) v[j] = -INFINITY;
           }
-          if (tcol >= c && tcol < c + 32 && tcol < P.n - col0) {
-            float z = 0.f;
+          if (tcol >= c && tcol < c + 32) {  // joined later
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (tcol == c + j) z = v[j];
-            P.zt[row] = z;
+              if (tcol == c + j) v[j] = -INFINITY;
           }
           float m4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
@@ -592,7 +594,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
           if (tcol >= c && tcol < c + 32) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (tcol == c + j) v[j] -= g;
+              if (tcol == c + j) v[j] = hot;
           }
           if (g == 0.f) {  // not trained on, whatever its logits
 #pragma unroll
@@ -730,14 +732,47 @@ __device__ __forceinline__ bool any_error(const uint32_t *err) {
   return __syncthreads_or((int)e) != 0;
 }
 
+// The logit of a row's target, by a warp: 32 sums in fp32, added at the end.
+struct TargetLogit {
+  const void *x, *w;  // x null: there is none to form
+  int64_t x_ld, w_ld;
+  int32_t width;
+  int bf, vec;  // bf16 operands; rows of both 16-byte aligned
+  template <typename T>
+  __device__ __forceinline__ float dot(int64_t row, uint32_t id) const {
+    constexpr int kN = 16 / (int)sizeof(T);
+    const int lane = threadIdx.x & 31;
+    const T *a = reinterpret_cast<const T *>(x) + row * x_ld, *b = reinterpret_cast<const T *>(w) + (int64_t)id * w_ld;
+    const int groups = vec ? width / kN : 0;
+    float s = 0.f;
+#pragma unroll 4
+    for (int g = lane; g < groups; g += 32) {
+      Pack<T, 16> p, q;
+      p.raw = __ldg(reinterpret_cast<const uint4 *>(a) + g);
+      q.raw = __ldg(reinterpret_cast<const uint4 *>(b) + g);
+      float t = 0.f;
+#pragma unroll
+      for (int e = 0; e < kN; ++e) t = fmaf(p.get(e), q.get(e), t);
+      s += t;
+    }
+#pragma unroll 4
+    for (int k = groups * kN + lane; k < width; k += 32) s = fmaf(to_f32(a[k]), to_f32(b[k]), s);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    return s;
+  }
+  __device__ __forceinline__ float get(int64_t row, uint32_t id) const { return bf ? dot<bf16>(row, id) : dot<float>(row, id); }
+};
+
 // Per row: the maximum and sum over all slots, the loss, the kept state; 32
-// threads per row, each over every 32nd slot.  Blocks of eight rows; up to
+// threads per row, each over every 32nd slot.  Where the slots leave the target
+// out (tl), its logit is formed here and joins them; else zt has it.  Blocks of eight rows; up to
 // kJoinMost rows one block has them all and adds their losses too (kTotal; mean
 // of 16 rows, 32768 x 1024 bf16: 19.3 us, with a launch for the total 21.9).
 constexpr int kJoinMost = 32;
 template <int kRows, bool kTotal>
 __global__ void __launch_bounds__(32 * kRows) k_xent_join(const float2 *__restrict__ part, int slots, int m,
-                                                          const float *__restrict__ zt, TokenSrc targets,
+                                                          const float *__restrict__ zt, const TargetLogit tl, TokenSrc targets,
                                                           float *__restrict__ loss, float *__restrict__ state,
                                                           const uint32_t *__restrict__ err, int mean) {
   pdl_wait();
@@ -746,6 +781,11 @@ __global__ void __launch_bounds__(32 * kRows) k_xent_join(const float2 *__restri
   __shared__ float row_loss[kRows];
   const int r = threadIdx.x % kRows, q = threadIdx.x / kRows;
   const int row = blockIdx.x * kRows + r;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int own = blockIdx.x * kRows + warp;  // a warp for each row
+  const uint32_t id = own < m ? targets.key(own) : targets.vocab;
+  const bool trained = id < targets.vocab;
+  const float z = !trained ? 0.f : tl.x ? tl.get(own, id) : zt[own];
   float mx = -INFINITY, sum = 0.f;
   if (row < m) {
     for (int s = q; s < slots; s += 32) {
@@ -761,8 +801,6 @@ __global__ void __launch_bounds__(32 * kRows) k_xent_join(const float2 *__restri
   }
   red[q][r] = make_float2(mx, sum);
   __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int own = blockIdx.x * kRows + warp;  // a warp for each row
   const float2 p = red[lane][warp];
   float nm = p.x;
 #pragma unroll
@@ -771,10 +809,19 @@ __global__ void __launch_bounds__(32 * kRows) k_xent_join(const float2 *__restri
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   if (lane == 0 && own < m) {
-    const float rest = bad ? NAN : logf(sum);
+    float rest;
+    if (trained && tl.x) {
+      const float top = fmaxf(nm, z);
+      if (nm != -INFINITY) sum *= expf(nm - top);
+      rest = z == top ? log1pf(sum) : logf(sum + expf(z - top));
+      nm = top;
+    } else {
+      rest = logf(sum);
+    }
+    if (bad) rest = NAN;
     state[own] = nm + rest;
     // not lse - z: a confident token's loss is far below the spacing of lse
-    const float l = targets.key(own) < targets.vocab ? (nm - zt[own]) + rest : 0.f;
+    const float l = trained ? (nm - z) + rest : 0.f;
     if (kTotal)
       row_loss[warp] = l;
     else
@@ -784,8 +831,7 @@ __global__ void __launch_bounds__(32 * kRows) k_xent_join(const float2 *__restri
   if (!kTotal) return;
   __syncthreads();
   if (warp) return;
-  const bool trained = lane < m && targets.key(lane) < targets.vocab;
-  const int count = max(1, __popc(__ballot_sync(0xffffffffu, trained)));
+  const int count = max(1, __popc(__ballot_sync(0xffffffffu, lane < m && targets.key(lane) < targets.vocab)));
   double total = lane < m ? (double)row_loss[lane] : 0.0;
 #pragma unroll
   for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
@@ -842,15 +888,21 @@ struct Drop {
 // [rows][width] into `parts` planes of bf16 [rows][out_ld]: the value, what
 // its rounding to bf16 leaves over, and what that leaves over.  A warp per row,
 // four groups of eight elements per lane in flight.  Rows that are not trained
-// on (drop) become zeros: dz^T x then holds nothing of them, NaN neither.
+// on (drop) become zeros: dz^T x then holds nothing of them, NaN neither.  The
+// others' target logits go to zt where it is asked for.
 template <typename T>
 __global__ void __launch_bounds__(256) k_xent_pack(const T *__restrict__ in, int64_t ld, int64_t rows, int32_t width,
-                                                   int parts, bf16 *__restrict__ out, int32_t out_ld, int64_t plane, int vec, const Drop drop) {
+                                                   int parts, bf16 *__restrict__ out, int32_t out_ld, int64_t plane, int vec, const Drop drop,
+                                                   const TargetLogit tl, float *__restrict__ zt) {
   pdl_wait();
   constexpr int kU = 4, kB = 16 / (int)sizeof(T);
   const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (r >= rows) return;
   const bool dropped = drop.row(r);
+  if (zt && !dropped) {
+    const float z = tl.get(r, drop.targets.key(r));
+    if ((threadIdx.x & 31) == 0) zt[r] = z;
+  }
   const int groups = out_ld / 8;
   for (int g0 = threadIdx.x & 31; g0 < groups; g0 += 32 * kU) {
     float v[kU][8];
@@ -1149,8 +1201,6 @@ XentWs xent_ws(const XentShape &s, bool grad) {
     if (w.piece > s.vocab) w.piece = s.vocab;
     w.nt = tile_cols(m_tiles, w.piece, s.sms);
     w.slots = 2 * (ceil_div(s.vocab, w.piece) * ceil_div(w.piece, w.nt));
-    w.zt = o;
-    o += align_up((size_t)s.n * 4, kAlign);
     w.row_loss = o;
     o += align_up((size_t)s.n * 4, kAlign);
     w.part = o;
@@ -1166,6 +1216,8 @@ XentWs xent_ws(const XentShape &s, bool grad) {
     // the pieces' products are alike: all of them as one piece of so many times the K stages
     w.split = pick_split(m_tiles * ceil_div(s.width, w.nt_d), ceil_div(w.piece, kKb),
                          (s.parts == 3 ? 6 : 1) * ceil_div(s.vocab, w.piece), (int64_t)s.n * w.acc_ld * 4, s.sms);
+    w.zt = o;
+    o += align_up((size_t)s.n * 4, kAlign);
     w.dz = o;
     o += align_up((size_t)s.parts * (size_t)s.n * (size_t)w.dz_ld * 2, kAlign);
     w.acc = o;
@@ -1254,19 +1306,26 @@ cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtens
   return e;
 }
 
-cudaError_t pack(const XentShape &s, const void *in, int64_t ld, int64_t rows, void *out, const Drop &drop, cudaStream_t st) {
+// the targets of a gradient's rows, for x's layout
+struct RowInfo {
+  Drop drop;
+  TargetLogit tl;
+  float *zt;
+};
+
+cudaError_t pack(const XentShape &s, const void *in, int64_t ld, int64_t rows, void *out, const RowInfo &ri, cudaStream_t st) {
   const int64_t blocks = ceil_div(rows, 8);
   const int vec = ptr_aligned(in, 16) && (size_t)ld * dtype_size(s.t) % 16 == 0;
   if (s.t == SNACK_F32)
     return launch_pdl(k_xent_pack<float>, (unsigned)blocks, 256, 0, st, reinterpret_cast<const float *>(in), ld, rows,
-                      s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld, vec, drop);
+                      s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld, vec, ri.drop, ri.tl, ri.zt);
   return launch_pdl(k_xent_pack<bf16>, (unsigned)blocks, 256, 0, st, reinterpret_cast<const bf16 *>(in), ld, rows,
-                    s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld, vec, drop);
+                    s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld, vec, ri.drop, ri.tl, ri.zt);
 }
 
 // x, or a piece of w from row v0 on, as the products read it
 cudaError_t operand(const XentShape &s, bool packed, const void *p, int64_t ld, int64_t v0, int64_t rows, void *buf,
-                    Operand *o, cudaStream_t st, const Drop &drop = Drop{}) {
+                    Operand *o, cudaStream_t st, const RowInfo &ri = RowInfo{}) {
   const size_t es = dtype_size(s.t);
   const uint8_t *at = reinterpret_cast<const uint8_t *>(p) + (size_t)v0 * (size_t)ld * es;
   o->rows = rows;
@@ -1282,7 +1341,7 @@ cudaError_t operand(const XentShape &s, bool packed, const void *p, int64_t ld, 
   o->ld = s.ld;
   o->planes = s.parts;
   o->plane = rows * s.ld;
-  return pack(s, at, ld, rows, buf, drop, st);
+  return pack(s, at, ld, rows, buf, ri, st);
 }
 
 GemmArgs gemm_args(const XentShape &s, uint8_t *ws, const XentWs &W, int first) {
@@ -1296,13 +1355,19 @@ GemmArgs gemm_args(const XentShape &s, uint8_t *ws, const XentWs &W, int first) 
   return g;
 }
 
-cudaError_t finish_loss(const float2 *part, int slots, int32_t n, const float *zt, const TokenSrc &tg,
+TargetLogit target_logit(const XentShape &s, const void *x, int64_t x_ld, const void *w, int64_t w_ld) {
+  const size_t es = dtype_size(s.t);
+  return {x, w, x_ld, w_ld, s.width, s.t == SNACK_BF16,
+          access_bytes((uintptr_t)x | (uintptr_t)w | (uintptr_t)(x_ld * es) | (uintptr_t)(w_ld * es)) == 16};
+}
+
+cudaError_t finish_loss(const float2 *part, int slots, int32_t n, const float *zt, const TargetLogit &tl, const TokenSrc &tg,
                         snack_reduction reduction, float *row_loss, float *loss, float *state, const uint32_t *err,
                         cudaStream_t s) {
   if (n <= kJoinMost && reduction != SNACK_NONE)
-    return launch_pdl(k_xent_join<kJoinMost, true>, 1, 32 * kJoinMost, 0, s, part, slots, n, zt, tg, loss, state, err,
+    return launch_pdl(k_xent_join<kJoinMost, true>, 1, 32 * kJoinMost, 0, s, part, slots, n, zt, tl, tg, loss, state, err,
                       reduction == SNACK_MEAN ? 1 : 0);
-  cudaError_t e = launch_pdl(k_xent_join<8, false>, (unsigned)ceil_div(n, 8), 256, 0, s, part, slots, n, zt, tg, row_loss,
+  cudaError_t e = launch_pdl(k_xent_join<8, false>, (unsigned)ceil_div(n, 8), 256, 0, s, part, slots, n, zt, tl, tg, row_loss,
                              state, err, 0);
   if (e != cudaSuccess || reduction == SNACK_NONE) return e;
   return launch_pdl(k_xent_total, 1, 1024, 0, s, (const float *)row_loss, n, tg, reduction == SNACK_MEAN, loss, state);
@@ -1457,7 +1522,7 @@ snack_status snack_xent_fwd(const void *x, int64_t x_ld, int32_t n, const void *
     a.part = part;
     a.zt = zt;
     XENT_CUDA(launch_few<false>(a, W.few_blocks, s));
-    XENT_CUDA(finish_loss(part, (int)W.slots, n, zt, tg, reduction, row_loss, loss, state, nullptr, s));
+    XENT_CUDA(finish_loss(part, (int)W.slots, n, zt, TargetLogit{}, tg, reduction, row_loss, loss, state, nullptr, s));
     return SNACK_OK;
   }
   if (S.cut) {
@@ -1465,7 +1530,7 @@ snack_status snack_xent_fwd(const void *x, int64_t x_ld, int32_t n, const void *
     a.part = part;
     a.zt = zt;
     XENT_CUDA(launch_cut_for<false>(a, W.slots, s));
-    XENT_CUDA(finish_loss(part, (int)W.slots, n, zt, tg, reduction, row_loss, loss, state, nullptr, s));
+    XENT_CUDA(finish_loss(part, (int)W.slots, n, zt, TargetLogit{}, tg, reduction, row_loss, loss, state, nullptr, s));
     return SNACK_OK;
   }
   const uint32_t a_rows = n >= kMCta ? kMCta : (uint32_t)align_up((size_t)n, 8);
@@ -1478,7 +1543,6 @@ snack_status snack_xent_fwd(const void *x, int64_t x_ld, int32_t n, const void *
   g.nt = W.nt;
   g.k_blocks = (int32_t)ceil_div(width, kKb);
   g.part = part;
-  g.zt = zt;
   g.targets = tg;
   for (int64_t v0 = 0; v0 < vocab; v0 += W.piece) {
     const int64_t rows = vocab - v0 < W.piece ? vocab - v0 : W.piece;
@@ -1489,7 +1553,8 @@ snack_status snack_xent_fwd(const void *x, int64_t x_ld, int32_t n, const void *
     XENT_CUDA(launch_gemm<kStats>(mx, mw, mx, g, S.sms, s));
     g.slot0 += 2 * g.n_tiles;
   }
-  XENT_CUDA(finish_loss(part, g.slot0, n, zt, tg, reduction, row_loss, loss, state, g.err, s));
+  XENT_CUDA(finish_loss(part, g.slot0, n, nullptr, target_logit(S, x, x_ld, w, w_ld), tg, reduction, row_loss, loss, state,
+                        g.err, s));
   return SNACK_OK;
 } catch (...) {  // a host allocation failed
   return SNACK_ERR_CUDA;
@@ -1574,7 +1639,9 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
   }
   const uint32_t a_rows = n >= kMCta ? kMCta : (uint32_t)align_up((size_t)n, 8);
   Operand ox, ow;
-  XENT_CUDA(operand(S, S.pack_x, x, x_ld, 0, n, b + W.xp, &ox, s, Drop{tg, weight}));
+  float *zt = reinterpret_cast<float *>(b + W.zt);
+  XENT_CUDA(operand(S, S.pack_x, x, x_ld, 0, n, b + W.xp, &ox, s,
+                    RowInfo{Drop{tg, weight}, target_logit(S, x, x_ld, w, w_ld), S.cut ? nullptr : zt}));
   CUtensorMap mx, mw, mxt, mwt, mdz, mdzt, mdz_out, macc, mdw;
   if (!load_map(&mx, ox, false, a_rows) || !load_map(&mxt, ox, true, 0)) return SNACK_ERR_CUDA;
   if (!make_map(&macc, b + W.acc, true, (uint64_t)width, (uint64_t)n, (uint64_t)W.acc_ld, (uint64_t)W.split,
@@ -1611,6 +1678,7 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
       g.targets = tg;
       g.v0 = (int32_t)v0;
       g.lse = state;
+      g.zt = zt;
       g.dloss = weight;
       g.out_parts = S.parts;
       XENT_CUDA(launch_gemm<kDlog>(mx, mw, mdz_out, g, S.sms, s));

@@ -736,3 +736,21 @@ def test_xent_fp32_gradients_are_fp32(n, vocab, width):
         # the same with two parts of either operand would be outside: of dz where its terms are few and its values several
         assert (np.abs(a @ parts_of(b, 2) - ref) > bound).any()
         assert n < 8 or (np.abs(parts_of(a, 2) @ b - ref) > bound).any()
+
+
+@pytest.mark.parametrize("n,width,dtype", [(100, 4096, "bf16"), (100, 4096, "f32"), (40, 2048, "bf16"), (300, 1001, "f32")])
+def test_xent_loss_does_not_take_the_accumulators_bias_of_the_target(n, width, dtype):
+    # a target's logit near 8 above others of about 1: on the tensor core it would come out 6e-7 of itself too small, 5e-6
+    # of the loss.  In fp32 it rounds to either side; what remains is the others' bias, at most 1.15e-6 of their average in
+    # lse, which is below 1.5
+    g = torch.Generator(device="cuda").manual_seed(width)
+    w = (torch.randn(20000, width, device="cuda", generator=g) / width ** 0.5).to(DTYPES[dtype])
+    t = torch.randint(0, 20000, (n,), device="cuda", generator=g)
+    x = (torch.randn(n, width, device="cuda", generator=g) + 8.0 * w[t].float()).to(DTYPES[dtype])
+    z = x.double() @ w.double().T
+    lse = torch.logsumexp(z, 1)
+    rest = torch.exp(z - lse[:, None])
+    assert float((rest * z).sum(1).sub((rest * z).gather(1, t[:, None])[:, 0]).mean()) < 1.5
+    want = lse - z.gather(1, t[:, None])[:, 0]
+    loss, _ = snack.xent(x, w, t, reduction="none")
+    assert abs(float((loss.double() - want).mean())) <= 1.15e-6 * 1.5
