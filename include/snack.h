@@ -390,9 +390,13 @@ snack_status snack_embed_grad(const void *ids, snack_index ids_t, int64_t n, con
  * so is its row of dx, and dw holds nothing of it, whatever its row of x holds
  * (infinities and NaN too).  loss receives n values (SNACK_NONE), their sum
  * over the trained positions (SNACK_SUM), or that divided by their count
- * (SNACK_MEAN; 0 when there are none).  An infinite fp32 operand may give NaN
- * where the logit is infinite (products are sums over parts of it).  state (n + 1 fp32 values) keeps each
- * row's lse, and 1 / count for the mean, for the gradient.
+ * (SNACK_MEAN; 0 when there are none).  Logits of bf16 operands follow fp32
+ * arithmetic where they are not finite.  Those of fp32 operands do so in losses of
+ * up to 4 tokens against at least 128 vocabulary rows per multiprocessor;
+ * elsewhere a product is a sum over parts of its operands, and a logit that has an
+ * infinite term, or leaves fp32's range, may be NaN, and with it its row's loss.  state
+ * (n + 1 fp32 values) keeps each row's lse, and 1 / count for the mean, for the
+ * gradient.
  */
 typedef enum snack_reduction { SNACK_NONE = 0, SNACK_SUM = 1, SNACK_MEAN = 2 } snack_reduction;
 
@@ -424,7 +428,9 @@ snack_status snack_xent_fwd(const void *x, int64_t x_ld, int32_t n, const void *
  * with g_i = dloss[i] (SNACK_NONE), or *dloss (1 when dloss is NULL) times 1
  * (SNACK_SUM) or 1 / count (SNACK_MEAN).  dx or dw may be NULL.  A row that is
  * not trained on stays out also where *dloss is not finite.  dz is rounded
- * to bf16 for bf16 operands and kept to fp32 precision for fp32 ones.
+ * to bf16 for bf16 operands (a relative 2^-9 of each entry, which adds about a fifth
+ * to the error that the rounding of dx and dw to bf16 makes) and kept to fp32
+ * precision for fp32 ones.
  */
 snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld, int64_t vocab,
                             int32_t width, snack_dtype t, const void *targets, snack_index targets_t,

@@ -35,7 +35,8 @@ constexpr int64_t kPiece = 64 * 1024;  // bytes of one tensor per piece of the n
 // and of the scaling (norm and scaling of 1e9 bf16 elements: 860 us, three passes
 // at 7.0 TB/s): 64 KB where all of it is in place, and may have nothing to
 // do (2 GB of fp32 with the factor 1: 286 us of norm, and 55 us of blocks that
-// return at once at 16 KB each)
+// return at once at 16 KB each; where it has to be scaled, 2 GB of bf16 in place, 64 KB
+// take 871 us and 16 KB 860)
 constexpr int64_t kScalePiece = 16 * 1024, kScalePieceInPlace = 64 * 1024;
 constexpr int kBlocksPerSm = 6;
 constexpr float kDown = 8.271806125530277e-25f;   // 2^-80

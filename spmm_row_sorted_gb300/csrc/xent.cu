@@ -12,7 +12,10 @@
 //   stats  keeps of a logits tile only each row's maximum and sum of
 //          exponentials, per half tile, without the target's;
 //   dlog   turns a logits tile into dz, stored as bf16 for one piece of the
-//          vocabulary;
+//          vocabulary (one part for bf16 operands, 2^-9 of an entry: dx and dw of
+//          4096 x 131072 x 2048 then lie 0.0020 from 64 bits, where their own
+//          rounding gives 0.0017; a second part would double both products that
+//          read dz);
 //   dx     adds dz w of the piece to fp32 sums (a TMA reduction: one addition
 //          per element and piece, in the pieces' order);
 //   dw     writes the piece's rows of dw.
@@ -31,8 +34,8 @@
 //
 // The tensor core's fp32 accumulation rounds towards zero, which over a long K
 // is a bias: a sum of 4096 products came out 5e-6 to 1.4e-5 of itself too small.
-// So an accumulator takes at most 512 of K (32 instructions; 256 of fp32
-// operands' logits) where that counts, and the epilogue's warps add the partial
+// So an accumulator takes at most 512 of K (32 instructions; 256 for the losses of
+// fp32 operands) where that counts, and the epilogue's warps add the partial
 // sums in registers, rounding to nearest, while the next one forms in the other
 // half of the tensor memory.  What is left is at most 1e-6 of a logit (unit_of).
 // The target's logit, of which loss and dz = p - 1 are small differences, does not
@@ -732,31 +735,39 @@ __device__ __forceinline__ bool any_error(const uint32_t *err) {
   return __syncthreads_or((int)e) != 0;
 }
 
-// The logit of a row's target, by a warp: 32 sums in fp32, added at the end.
+// The logit of a row's target, by a warp: 32 sums in fp32, added at the end, in an
+// order that does not depend on how the rows lie.
 struct TargetLogit {
   const void *x, *w;  // x null: there is none to form
   int64_t x_ld, w_ld;
   int32_t width;
-  int bf, vec;  // bf16 operands; rows of both 16-byte aligned
+  int bf, x_wide, w_wide;  // bf16 operands; rows 16-byte aligned
+  template <typename T>
+  static __device__ __forceinline__ Pack<T, 16> some(const T *row, int g, int32_t width, int wide) {
+    constexpr int kN = 16 / (int)sizeof(T);
+    Pack<T, 16> p;
+    if (wide && (g + 1) * kN <= width) {
+      p.raw = __ldg(reinterpret_cast<const uint4 *>(row) + g);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kN; ++e) p.set(e, g * kN + e < width ? to_f32(row[g * kN + e]) : 0.f);
+    }
+    return p;
+  }
   template <typename T>
   __device__ __forceinline__ float dot(int64_t row, uint32_t id) const {
     constexpr int kN = 16 / (int)sizeof(T);
-    const int lane = threadIdx.x & 31;
     const T *a = reinterpret_cast<const T *>(x) + row * x_ld, *b = reinterpret_cast<const T *>(w) + (int64_t)id * w_ld;
-    const int groups = vec ? width / kN : 0;
+    const int groups = (width + kN - 1) / kN;
     float s = 0.f;
 #pragma unroll 4
-    for (int g = lane; g < groups; g += 32) {
-      Pack<T, 16> p, q;
-      p.raw = __ldg(reinterpret_cast<const uint4 *>(a) + g);
-      q.raw = __ldg(reinterpret_cast<const uint4 *>(b) + g);
+    for (int g = threadIdx.x & 31; g < groups; g += 32) {
+      const Pack<T, 16> p = some(a, g, width, x_wide), q = some(b, g, width, w_wide);
       float t = 0.f;
 #pragma unroll
       for (int e = 0; e < kN; ++e) t = fmaf(p.get(e), q.get(e), t);
       s += t;
     }
-#pragma unroll 4
-    for (int k = groups * kN + lane; k < width; k += 32) s = fmaf(to_f32(a[k]), to_f32(b[k]), s);
 #pragma unroll
     for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
     return s;
@@ -768,7 +779,7 @@ struct TargetLogit {
 // threads per row, each over every 32nd slot.  Where the slots leave the target
 // out (tl), its logit is formed here and joins them; else zt has it.  Blocks of eight rows; up to
 // kJoinMost rows one block has them all and adds their losses too (kTotal; mean
-// of 16 rows, 32768 x 1024 bf16: 19.3 us, with a launch for the total 21.9).
+// of 16 rows, 32768 x 1024 bf16: a launch for the total took 2.6 us more of 22).
 constexpr int kJoinMost = 32;
 template <int kRows, bool kTotal>
 __global__ void __launch_bounds__(32 * kRows) k_xent_join(const float2 *__restrict__ part, int slots, int m,
@@ -1265,13 +1276,11 @@ XentShape xent_shape(const void *x, int64_t x_ld, int32_t n, const void *wt, int
 // costs an exchange of accumulators and a read of 128 KB of tensor memory per
 // CTA (about 1900 cycles beside the MMAs, of 512 a stage and product).  Sums that
 // become the loss or other fp32 results take units of at most eight stages, of
-// equal length, and so do the gradient's logits: dz = p - 1 of a confident token is
-// far smaller than p, so they have to be the very sums that lse came from (one
-// accumulator over 4096 of K made dz wrong by 2e-4 at logits of 40, at 1 - p of
-// 2e-3; the same units for both cost 1 to 3 % of a large gradient).  What is rounded
-// to bf16 without such a difference (dx and dw of bf16 operands) is far below half
-// its ulp with long ones.  Logits of fp32 operands take four: six part products
-// hide the reads (1024 x 16384 x 768: 131 us with 8 and with 4, 137 with 2).
+// equal length; the losses of fp32 operands take four (six part products hide most
+// of the reads: 1024 x 16384 x 768, 5 us of 92).  What is rounded to bf16 (dz, dx
+// and dw of bf16 operands) is far below half its ulp with long ones; dz at the
+// target, p - 1, is not, and does not come from them: one accumulator over 4096 of K
+// would make it wrong by 2e-4 at logits of 40, where 1 - p was 2e-3.
 // Measured, relative error of logits of 40 (width 4096) on average, and the loss of
 // 2048 x 65536 x 4096 bf16 and of 67 x 119598 x 2176 fp32, us:
 //   unit   random    positive  nine of ten zero    bf16   fp32
@@ -1294,8 +1303,7 @@ cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtens
   if (!enough) return cudaErrorInvalidDeviceFunction;
   g.m_tiles = (int32_t)ceil_div(g.m, kM);
   g.n_tiles = (int32_t)ceil_div(g.n, g.nt);
-  const bool logits = kMode == kStats || kMode == kDlog;
-  g.unit = unit_of((int)ceil_div(g.k_blocks, g.n_split), g.products > 1 ? (logits ? 4 : 8) : logits ? 8 : 64);
+  g.unit = unit_of((int)ceil_div(g.k_blocks, g.n_split), g.products > 1 ? (kMode == kStats ? 4 : 8) : kMode == kStats ? 8 : 64);
   g.a_rows = kMode == kDw || g.m >= kMCta ? kMCta : (int32_t)align_up((size_t)g.m, 8);
   g.stages = kRing / ((g.a_rows + g.nt / 2) * kKb * 2);
   if (g.stages > kMaxStages) g.stages = kMaxStages;
@@ -1357,8 +1365,8 @@ GemmArgs gemm_args(const XentShape &s, uint8_t *ws, const XentWs &W, int first) 
 
 TargetLogit target_logit(const XentShape &s, const void *x, int64_t x_ld, const void *w, int64_t w_ld) {
   const size_t es = dtype_size(s.t);
-  return {x, w, x_ld, w_ld, s.width, s.t == SNACK_BF16,
-          access_bytes((uintptr_t)x | (uintptr_t)w | (uintptr_t)(x_ld * es) | (uintptr_t)(w_ld * es)) == 16};
+  const auto wide = [es](const void *p, int64_t ld) { return ptr_aligned(p, 16) && (size_t)ld * es % 16 == 0; };
+  return {x, w, x_ld, w_ld, s.width, s.t == SNACK_BF16, wide(x, x_ld), wide(w, w_ld)};
 }
 
 cudaError_t finish_loss(const float2 *part, int slots, int32_t n, const float *zt, const TargetLogit &tl, const TokenSrc &tg,
@@ -1553,8 +1561,9 @@ snack_status snack_xent_fwd(const void *x, int64_t x_ld, int32_t n, const void *
     XENT_CUDA(launch_gemm<kStats>(mx, mw, mx, g, S.sms, s));
     g.slot0 += 2 * g.n_tiles;
   }
-  XENT_CUDA(finish_loss(part, g.slot0, n, nullptr, target_logit(S, x, x_ld, w, w_ld), tg, reduction, row_loss, loss, state,
-                        g.err, s));
+  const bool copied = S.pack_x && t == SNACK_BF16;  // x laid out again, on better boundaries
+  XENT_CUDA(finish_loss(part, g.slot0, n, nullptr, target_logit(S, copied ? ox.p : x, copied ? ox.ld : x_ld, w, w_ld), tg,
+                        reduction, row_loss, loss, state, g.err, s));
   return SNACK_OK;
 } catch (...) {  // a host allocation failed
   return SNACK_ERR_CUDA;

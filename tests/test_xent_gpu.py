@@ -754,3 +754,20 @@ def test_xent_loss_does_not_take_the_accumulators_bias_of_the_target(n, width, d
     want = lse - z.gather(1, t[:, None])[:, 0]
     loss, _ = snack.xent(x, w, t, reduction="none")
     assert abs(float((loss.double() - want).mean())) <= 1.15e-6 * 1.5
+
+
+@pytest.mark.parametrize("n,vocab,dtype", [(3, 20000, "f32"), (3, 500, "bf16"), (70, 500, "bf16"), (300, 700, "bf16")])
+def test_xent_logits_of_minus_infinity(n, vocab, dtype):
+    """Vocabulary rows that an infinite weight takes out: as fp32 arithmetic has it, where the products are not over parts.
+    (The smallest vocabulary of the fp32 case's kernel is 128 rows for each of a GPU's multiprocessors.)"""
+    x, w, t = make(n, vocab, 64, dtype, seed=n + vocab, ignored=0.0)
+    x, w = x.abs().contiguous(), w.clone()
+    gone = torch.arange(vocab, device="cuda") % 3 == 1
+    w[gone, 5] = -float("inf")
+    t[t % 3 == 1] = 2
+    r = reference(x, w[~gone].contiguous(), t - (t + 1) // 3, np.ones(n))
+    loss, state = snack.xent(x, w, t, reduction="none")
+    check_loss(loss, r)
+    t[0] = 1  # a target that is out
+    loss, state = snack.xent(x, w, t, reduction="none")
+    assert float(loss[0]) == float("inf") and torch.isfinite(loss[1:]).all() and torch.isfinite(state).all()
