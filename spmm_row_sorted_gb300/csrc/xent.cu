@@ -12,10 +12,10 @@
 //   stats  keeps of a logits tile only each row's maximum and sum of
 //          exponentials, per half tile, without the target's;
 //   dlog   turns a logits tile into dz, stored as bf16 for one piece of the
-//          vocabulary (one part for bf16 operands, 2^-9 of an entry: dx and dw of
-//          4096 x 131072 x 2048 then lie 0.0020 from 64 bits, where their own
-//          rounding gives 0.0017; a second part would double both products that
-//          read dz);
+//          vocabulary (one part for bf16 operands, 2^-9 of an entry: dw of 4096 x
+//          131072 x 2048 then lies 0.0020 from 64 bits, where its own rounding gives
+//          0.0017; a second part would double both products that read dz; dx takes
+//          what the target's entry lost at the end);
 //   dx     adds dz w of the piece to fp32 sums (a TMA reduction: one addition
 //          per element and piece, in the pieces' order);
 //   dw     writes the piece's rows of dw.
@@ -270,7 +270,7 @@ struct GemmArgs {
   TokenSrc targets;
   int32_t v0;               // first vocabulary row of the piece
   // dlog
-  const float *lse, *zt;    // [m] each, zt: the target's logit
+  const float *lse, *hot;   // [m] each, hot: dz at the target
   const float *dloss;       // upstream gradient of each row, or null (1: a common factor is applied to the sums)
   int32_t out_parts;        // bf16 parts of dz
   // dx
@@ -494,7 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
       const int col0 = q.n0 + half * width0;
       // the target's column of this tile's half, or below zero
       int tcol = -1;
-      float lse = 0.f, g = 0.f, hot = 0.f;  // hot: dz at the target
+      float lse = 0.f, g = 0.f, hot = 0.f;
       if (kMode == kStats || kMode == kDlog) {
         if (row_ok) {
           const uint32_t id = P.targets.key(row);
@@ -503,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
             if (kMode == kDlog) {
               lse = P.lse[row];
               g = P.dloss ? P.dloss[row] : 1.f;
-              if (tcol >= 0 && tcol < c_end) hot = g * expm1f(P.zt[row] - lse);
+              hot = P.hot[row];
             }
           }
         }
@@ -899,20 +899,21 @@ struct Drop {
 // [rows][width] into `parts` planes of bf16 [rows][out_ld]: the value, what
 // its rounding to bf16 leaves over, and what that leaves over.  A warp per row,
 // four groups of eight elements per lane in flight.  Rows that are not trained
-// on (drop) become zeros: dz^T x then holds nothing of them, NaN neither.  The
-// others' target logits go to zt where it is asked for.
+// on (drop) become zeros: dz^T x then holds nothing of them, NaN neither.  Where
+// it is asked for, hot receives dz at every row's target, from its logit in fp32.
 template <typename T>
 __global__ void __launch_bounds__(256) k_xent_pack(const T *__restrict__ in, int64_t ld, int64_t rows, int32_t width,
                                                    int parts, bf16 *__restrict__ out, int32_t out_ld, int64_t plane, int vec, const Drop drop,
-                                                   const TargetLogit tl, float *__restrict__ zt) {
+                                                   const TargetLogit tl, const float *__restrict__ lse,
+                                                   float *__restrict__ hot) {
   pdl_wait();
   constexpr int kU = 4, kB = 16 / (int)sizeof(T);
   const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (r >= rows) return;
   const bool dropped = drop.row(r);
-  if (zt && !dropped) {
-    const float z = tl.get(r, drop.targets.key(r));
-    if ((threadIdx.x & 31) == 0) zt[r] = z;
+  if (hot) {
+    const float z = dropped ? 0.f : tl.get(r, drop.targets.key(r));
+    if ((threadIdx.x & 31) == 0) hot[r] = dropped ? 0.f : (drop.weight ? drop.weight[r] : 1.f) * expm1f(z - lse[r]);
   }
   const int groups = out_ld / 8;
   for (int g0 = threadIdx.x & 31; g0 < groups; g0 += 32 * kU) {
@@ -990,13 +991,17 @@ __global__ void __launch_bounds__(256) k_xent_rows(const bf16 *__restrict__ in, 
 }
 
 // dx = the splits' sums, added in order and rounded once; rows that are left out
-// stay 0 also where the factor is not finite.  The last kernel of a gradient:
-// after an error it makes dx and the first row of dw NaN.
+// stay 0 also where the factor is not finite.  With hot (dz rounded to bf16), what
+// the rounding left over of the target's entry, mostly the largest of its row, times
+// the target's row of w: dx of 4096 x 131072 x 2048 lies 0.0017 from 64 bits, its own
+// rounding to bf16, so 0.0020.  The last kernel of a gradient: after an error it
+// makes dx and the first row of dw NaN.
 template <typename T>
 __global__ void __launch_bounds__(256) k_xent_dx(const float *__restrict__ acc, int splits, int64_t plane, int32_t acc_ld,
                                                  int32_t m, int32_t width, T *__restrict__ dx, int64_t ld,
                                                  T *__restrict__ dw, Factor factor, const Drop drop,
-                                                 const uint32_t *__restrict__ err) {
+                                                 const float *__restrict__ hot, const T *__restrict__ w, int64_t w_ld,
+                                                 int w_vec, const uint32_t *__restrict__ err) {
   pdl_wait();
   const bool bad = any_error(err);
   const float f = bad ? NAN : factor.get();
@@ -1015,6 +1020,24 @@ __global__ void __launch_bounds__(256) k_xent_dx(const float *__restrict__ acc, 
       s.y += b.y;
       s.z += b.z;
       s.w += b.w;
+    }
+    if (hot) {
+      const float h = hot[r], over = h - __bfloat162float(__float2bfloat16_rn(h));
+      const uint32_t id = drop.targets.key(r);
+      if (over != 0.f && id < drop.targets.vocab) {
+        const T *at = w + (int64_t)id * w_ld + c;
+        Pack<T, 4 * sizeof(T)> q;
+        if (w_vec && c + 4 <= width) {
+          q.raw = __ldg(reinterpret_cast<const typename Pack<T, 4 * sizeof(T)>::R *>(at));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) q.set(j, c + j < width ? to_f32(at[j]) : 0.f);
+        }
+        s.x = fmaf(over, q.get(0), s.x);
+        s.y = fmaf(over, q.get(1), s.y);
+        s.z = fmaf(over, q.get(2), s.z);
+        s.w = fmaf(over, q.get(3), s.w);
+      }
     }
     T *o = dx + r * ld + c;
     const float fr = look && drop.row(r) ? 0.f : f;
@@ -1143,7 +1166,7 @@ struct XentShape {
 };
 
 struct XentWs {
-  size_t err, zt, row_loss, part, xp, wp, dz, acc, dwp, total;
+  size_t err, zt, hot, row_loss, part, xp, wp, dz, acc, dwp, total;
   int nt;             // forward tile
   int64_t piece;      // vocabulary rows at a time (forward: of packed w; gradient: of dz)
   int64_t slots;
@@ -1227,7 +1250,7 @@ XentWs xent_ws(const XentShape &s, bool grad) {
     // the pieces' products are alike: all of them as one piece of so many times the K stages
     w.split = pick_split(m_tiles * ceil_div(s.width, w.nt_d), ceil_div(w.piece, kKb),
                          (s.parts == 3 ? 6 : 1) * ceil_div(s.vocab, w.piece), (int64_t)s.n * w.acc_ld * 4, s.sms);
-    w.zt = o;
+    w.hot = o;
     o += align_up((size_t)s.n * 4, kAlign);
     w.dz = o;
     o += align_up((size_t)s.parts * (size_t)s.n * (size_t)w.dz_ld * 2, kAlign);
@@ -1318,7 +1341,8 @@ cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtens
 struct RowInfo {
   Drop drop;
   TargetLogit tl;
-  float *zt;
+  const float *lse;
+  float *hot;
 };
 
 cudaError_t pack(const XentShape &s, const void *in, int64_t ld, int64_t rows, void *out, const RowInfo &ri, cudaStream_t st) {
@@ -1326,9 +1350,11 @@ cudaError_t pack(const XentShape &s, const void *in, int64_t ld, int64_t rows, v
   const int vec = ptr_aligned(in, 16) && (size_t)ld * dtype_size(s.t) % 16 == 0;
   if (s.t == SNACK_F32)
     return launch_pdl(k_xent_pack<float>, (unsigned)blocks, 256, 0, st, reinterpret_cast<const float *>(in), ld, rows,
-                      s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld, vec, ri.drop, ri.tl, ri.zt);
+                      s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld, vec, ri.drop, ri.tl, ri.lse,
+                    ri.hot);
   return launch_pdl(k_xent_pack<bf16>, (unsigned)blocks, 256, 0, st, reinterpret_cast<const bf16 *>(in), ld, rows,
-                    s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld, vec, ri.drop, ri.tl, ri.zt);
+                    s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld, vec, ri.drop, ri.tl, ri.lse,
+                    ri.hot);
 }
 
 // x, or a piece of w from row v0 on, as the products read it
@@ -1643,14 +1669,15 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
     if (dx)
       XENT_CUDA(launch_pdl(k_xent_dx<float>, (unsigned)ceil_div((int64_t)n * (W.acc_ld / 4), 256), 256, 0, s,
                            (const float *)g.acc, W.split, (int64_t)n * W.acc_ld, W.acc_ld, n, width,
-                           reinterpret_cast<float *>(dx), dx_ld, (float *)nullptr, factor, Drop{tg, weight}, (const uint32_t *)nullptr));
+                           reinterpret_cast<float *>(dx), dx_ld, (float *)nullptr, factor, Drop{tg, weight},
+                           (const float *)nullptr, (const float *)nullptr, (int64_t)0, 0, (const uint32_t *)nullptr));
     return SNACK_OK;
   }
   const uint32_t a_rows = n >= kMCta ? kMCta : (uint32_t)align_up((size_t)n, 8);
   Operand ox, ow;
-  float *zt = reinterpret_cast<float *>(b + W.zt);
+  float *hot = reinterpret_cast<float *>(b + W.hot);
   XENT_CUDA(operand(S, S.pack_x, x, x_ld, 0, n, b + W.xp, &ox, s,
-                    RowInfo{Drop{tg, weight}, target_logit(S, x, x_ld, w, w_ld), S.cut ? nullptr : zt}));
+                    RowInfo{Drop{tg, weight}, target_logit(S, x, x_ld, w, w_ld), state, S.cut ? nullptr : hot}));
   CUtensorMap mx, mw, mxt, mwt, mdz, mdzt, mdz_out, macc, mdw;
   if (!load_map(&mx, ox, false, a_rows) || !load_map(&mxt, ox, true, 0)) return SNACK_ERR_CUDA;
   if (!make_map(&macc, b + W.acc, true, (uint64_t)width, (uint64_t)n, (uint64_t)W.acc_ld, (uint64_t)W.split,
@@ -1687,7 +1714,7 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
       g.targets = tg;
       g.v0 = (int32_t)v0;
       g.lse = state;
-      g.zt = zt;
+      g.hot = hot;
       g.dloss = weight;
       g.out_parts = S.parts;
       XENT_CUDA(launch_gemm<kDlog>(mx, mw, mdz_out, g, S.sms, s));
@@ -1742,11 +1769,12 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
   if (wide)
     XENT_CUDA(launch_pdl(k_xent_dx<float>, (unsigned)blocks, 256, 0, s, acc, W.split, (int64_t)n * W.acc_ld, W.acc_ld,
                          dx ? n : 0, width, reinterpret_cast<float *>(dx), dx_ld, reinterpret_cast<float *>(dw), factor,
-                         Drop{tg, weight}, err));
+                         Drop{tg, weight}, (const float *)nullptr, (const float *)nullptr, (int64_t)0, 0, err));
   else
     XENT_CUDA(launch_pdl(k_xent_dx<bf16>, (unsigned)blocks, 256, 0, s, acc, W.split, (int64_t)n * W.acc_ld, W.acc_ld,
                          dx ? n : 0, width, reinterpret_cast<bf16 *>(dx), dx_ld, reinterpret_cast<bf16 *>(dw), factor,
-                         Drop{tg, weight}, err));
+                         Drop{tg, weight}, (const float *)hot, reinterpret_cast<const bf16 *>(w), w_ld,
+                         ptr_aligned(w, 8) && w_ld % 4 == 0 ? 1 : 0, err));
   return SNACK_OK;
 } catch (...) {  // a host allocation failed
   return SNACK_ERR_CUDA;

@@ -771,3 +771,35 @@ def test_xent_logits_of_minus_infinity(n, vocab, dtype):
     t[0] = 1  # a target that is out
     loss, state = snack.xent(x, w, t, reduction="none")
     assert float(loss[0]) == float("inf") and torch.isfinite(loss[1:]).all() and torch.isfinite(state).all()
+
+
+@pytest.mark.parametrize("n,vocab,width,gap,lead", [(100, 300, 128, 0, 0), (5, 64, 1000, 0, 0), (70, 500, 77, 0, 0), (300, 1500, 96, 4, 4),
+                                                    (64, 200, 100, 3, 1)])
+@pytest.mark.parametrize("reduction", ["none", "mean"])
+def test_xent_dx_of_bf16_has_the_targets_entry_unrounded(n, vocab, width, gap, lead, reduction):
+    # logits with probabilities near a half at the target, whose dz is most of the row's: its rounding to bf16 would be
+    # up to 2^-9 of dx.  Left: every other entry's (2^-9 p), fp32 sums (2^-20 of T for a logit, 2^-16 of a product's
+    # magnitudes) and dx's own rounding
+    x, w, t = make(n, vocab, width, "bf16", seed=n + vocab, gap=gap, lead=lead, ignored=0.1, spread=1.0)
+    inside = (t >= 0) & (t < vocab)
+    at = torch.where(inside, t, 0)
+    aim = w.float()[at]
+    x.copy_((x.float() * 0.1 + aim * (float(np.log(vocab)) / aim.square().sum(1, keepdim=True))))
+    up = torch.rand(n, device="cuda") + 0.5
+    weight = f64(up) if reduction == "none" else np.full(n, 1.0 / max(1, int(inside.sum())))
+    r = reference(x, w, t, weight)
+    loss, state = snack.xent(x, w, t, reduction=reduction)
+    dx, dw = snack.xent_grad(x, w, t, state, up if reduction == "none" else None, reduction=reduction)
+    X, W, T = f64(x), f64(w), at.cpu().numpy()
+    z = X @ W.T
+    p = np.exp(z - r["lse"][:, None])
+    hot = np.zeros_like(p)
+    hot[np.arange(n), T] = r["inside"]
+    assert 0.2 < np.median(p[hot > 0]) < 0.8
+    g = np.where(r["inside"], weight, 0.0)[:, None]
+    noise = (2.0 ** -20 * r["T"] + 2.0 ** -16)[:, None]
+    bound = (g * (p * (noise + 2.0 ** -9 * (1 - hot)) + 2.0 ** -16 * (p + hot))) @ np.abs(W)
+    bound = bound + bf16_half_ulp(np.abs(r["dx"]) + bound)
+    off = np.abs(f64(dx) - r["dx"]) / (bound + 1e-300)
+    assert off.max() <= 1.0, off.max()
+    check_grads(None, dw, r, "bf16")
