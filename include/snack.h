@@ -428,8 +428,8 @@ snack_status snack_xent_fwd(const void *x, int64_t x_ld, int32_t n, const void *
  * with g_i = dloss[i] (SNACK_NONE), or *dloss (1 when dloss is NULL) times 1
  * (SNACK_SUM) or 1 / count (SNACK_MEAN).  dx or dw may be NULL.  A row that is
  * not trained on stays out also where *dloss is not finite.  dz is rounded
- * to bf16 for bf16 operands (a relative 2^-9 of each entry, which adds a fifth to
- * a half to the error that rounding dw to bf16 makes; dx has the target's entry
+ * to bf16 for bf16 operands (a relative 2^-9 of each entry, which adds a tenth to
+ * a third to the error that rounding dw to bf16 makes; dx has the target's entry
  * unrounded) and kept to fp32 precision for fp32 ones.
  */
 snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld, int64_t vocab,

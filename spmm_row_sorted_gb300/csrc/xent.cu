@@ -13,8 +13,8 @@
 //          exponentials, per half tile, without the target's;
 //   dlog   turns a logits tile into dz, stored as bf16 for one piece of the
 //          vocabulary (one part for bf16 operands, 2^-9 of an entry: dw of 4096 x
-//          131072 x 2048 then lies 0.0020 from 64 bits, where its own rounding gives
-//          0.0017; a second part would double both products that read dz; dx takes
+//          131072 x 2048 then lies 0.0019 from 64 bits, where its own rounding gives
+//          0.0016; a second part would double both products that read dz; dx takes
 //          what the target's entry lost at the end);
 //   dx     adds dz w of the piece to fp32 sums (a TMA reduction: one addition
 //          per element and piece, in the pieces' order);
@@ -993,8 +993,8 @@ __global__ void __launch_bounds__(256) k_xent_rows(const bf16 *__restrict__ in, 
 // dx = the splits' sums, added in order and rounded once; rows that are left out
 // stay 0 also where the factor is not finite.  With hot (dz rounded to bf16), what
 // the rounding left over of the target's entry, mostly the largest of its row, times
-// the target's row of w: dx of 4096 x 131072 x 2048 lies 0.0017 from 64 bits, its own
-// rounding to bf16, so 0.0020.  The last kernel of a gradient: after an error it
+// the target's row of w: dx of 4096 x 131072 x 2048 lies 0.0017 from 64 bits, as far as
+// its own rounding to bf16 puts it, without that 0.0020.  The last kernel of a gradient: after an error it
 // makes dx and the first row of dw NaN.
 template <typename T>
 __global__ void __launch_bounds__(256) k_xent_dx(const float *__restrict__ acc, int splits, int64_t plane, int32_t acc_ld,
