@@ -459,6 +459,48 @@ snack_status snack_clip_grad_norm(int32_t n_tensors, const void *const *grads, v
                                   void *ws, size_t ws_bytes, snack_stream_t stream);
 
 /*
+ * Low-rank adapters of many requests beside a shared projection (a sparse
+ * layer's, or any other): row i belongs to a request with the adapter
+ * k = which[i], and
+ *   h[i] = A_k x[i]                          (rank values, fp32)
+ *   y[i] = base[i] + scales[k] * B_k h[i]    added in fp32, rounded once to t
+ * a [n_adapters, rank, in_f] and b [n_adapters, out_f, rank] are contiguous, in
+ * type t as x [n, in_f], base and y [n, out_f] are; scales holds n_adapters fp32
+ * values, or is NULL (1).  A row whose which[i] is outside [0, n_adapters) has no
+ * adapter: y[i] is base[i], and nothing is computed of it.  Rows may come in any
+ * order.  base may be y itself (in place, with the same row step) or NULL (0: the
+ * adapters' part alone); otherwise y overlaps no other argument.  h (n * rank fp32
+ * values, rows without an adapter untouched) is kept for the gradient, or NULL.
+ * n < 2^24, rank <= 256, n_adapters <= 32768, in_f, out_f < 2^20.  The workspace
+ * takes n * (rank + 1) * 4 bytes and some per adapter.
+ * fp32 products are sums over parts of their operands: one with an infinite or NaN
+ * operand is NaN, and so is its row.
+ */
+snack_status snack_adapt_workspace_size(int64_t n, int32_t n_adapters, int32_t rank, size_t *bytes);
+snack_status snack_adapt_fwd(const void *x, int64_t x_ld, int64_t n, const void *a, const void *b, int32_t n_adapters,
+                             int32_t rank, int32_t in_f, int32_t out_f, snack_dtype t, const void *which,
+                             snack_index which_t, const float *scales, const void *base, int64_t base_ld, void *y,
+                             int64_t y_ld, float *h, void *ws, size_t ws_bytes, snack_stream_t stream);
+
+/*
+ * The adapters' gradients for dy = dL/dy [n, out_f], with k = which[i]:
+ *   dh[i] = scales[k] * B_k^T dy[i]
+ *   dx[i] = A_k^T dh[i]                      (+ what is there, with accumulate != 0)
+ *   da[k] = sum_i dh[i] x[i]^T,   db[k] = scales[k] * sum_i dy[i] h[i]^T
+ * summed in fp32 over the adapter's rows and rounded once to t.  dx is the
+ * adapters' part alone: accumulate adds it to the projection's own input
+ * gradient.  Rows without an adapter have dx = 0 (or stay, with accumulate) and
+ * are in no sum; an adapter without rows has gradients of 0.  dx, da or db may be
+ * NULL; h (of snack_adapt_fwd) may be NULL where db is.  The workspace is
+ * snack_adapt_workspace_size's.
+ */
+snack_status snack_adapt_bwd(const void *x, int64_t x_ld, int64_t n, const void *a, const void *b, int32_t n_adapters,
+                             int32_t rank, int32_t in_f, int32_t out_f, snack_dtype t, const void *which,
+                             snack_index which_t, const float *scales, const float *h, const void *dy, int64_t dy_ld,
+                             int accumulate, void *dx, int64_t dx_ld, void *da, void *db, void *ws, size_t ws_bytes,
+                             snack_stream_t stream);
+
+/*
  * Kernel trace of the calling host thread (a profiling aid).  While a trace
  * is open, every kernel the library launches from this thread is bracketed by
  * two CUDA events recorded on its stream, in a ring of `capacity` records:

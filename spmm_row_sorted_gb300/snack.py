@@ -40,7 +40,8 @@ EXPORTED = ("snack_query_sizes", "snack_create", "snack_spmm_fwd", "snack_spmm_f
             "snack_restructure_rows", "snack_wait_plan", "snack_destroy", "snack_status_string", "snack_version",
             "snack_trace_start", "snack_trace_read", "snack_trace_stop", "snack_embed_fwd",
             "snack_embed_grad_workspace_size", "snack_embed_grad", "snack_clip_workspace_size",
-            "snack_clip_grad_norm", "snack_xent_workspace_size", "snack_xent_fwd", "snack_xent_bwd")
+            "snack_clip_grad_norm", "snack_xent_workspace_size", "snack_xent_fwd", "snack_xent_bwd",
+            "snack_adapt_workspace_size", "snack_adapt_fwd", "snack_adapt_bwd")
 
 
 class SnackLibraryMissing(RuntimeError):
@@ -133,6 +134,14 @@ def load(path: Optional[str] = None):
         lib.snack_xent_bwd.argtypes = [vp, i64, i32, vp, i64, i64, i32, st, vp, st, st, vp, vp, vp, i64, vp, i64, vp, sz,
                                        vp]
         lib.snack_xent_bwd.restype = st
+        lib.snack_adapt_workspace_size.argtypes = [i64, i32, i32, ctypes.POINTER(sz)]
+        lib.snack_adapt_workspace_size.restype = st
+        lib.snack_adapt_fwd.argtypes = [vp, i64, i64, vp, vp, i32, i32, i32, i32, st, vp, st, vp, vp, i64, vp, i64, vp, vp,
+                                        sz, vp]
+        lib.snack_adapt_fwd.restype = st
+        lib.snack_adapt_bwd.argtypes = [vp, i64, i64, vp, vp, i32, i32, i32, i32, st, vp, st, vp, vp, vp, i64, ctypes.c_int,
+                                        vp, i64, vp, vp, vp, sz, vp]
+        lib.snack_adapt_bwd.restype = st
         _lib = lib
         return lib
 
@@ -385,6 +394,31 @@ def snack_xent_bwd(x, w, targets, reduction: int, state, dloss, dx, dw, ws, stre
                                  0 if dw is None else dw.stride(0), _addr(ws), _nbytes(ws), _raw_stream(stream)))
 
 
+def snack_adapt_workspace_size(n: int, n_adapters: int, rank: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check("snack_adapt_workspace_size",
+           (_lib or load()).snack_adapt_workspace_size(n, n_adapters, rank, ctypes.byref(b)))
+    return b.value
+
+
+def snack_adapt_fwd(x, a, b, which, scales, base, y, h, ws, stream=None) -> None:
+    _check("snack_adapt_fwd",
+           (_lib or load()).snack_adapt_fwd(_addr(x), x.stride(0), x.shape[0], _addr(a), _addr(b), a.shape[0], a.shape[1],
+                                            x.shape[1], y.shape[1], dtype_code(x.dtype), _addr(which),
+                                            index_code(which.dtype), _addr(scales), _addr(base),
+                                            0 if base is None else base.stride(0), _addr(y), y.stride(0), _addr(h),
+                                            _addr(ws), _nbytes(ws), _raw_stream(stream)))
+
+
+def snack_adapt_bwd(x, a, b, which, scales, h, dy, accumulate: bool, dx, da, db, ws, stream=None) -> None:
+    _check("snack_adapt_bwd",
+           (_lib or load()).snack_adapt_bwd(_addr(x), x.stride(0), x.shape[0], _addr(a), _addr(b), a.shape[0], a.shape[1],
+                                            x.shape[1], dy.shape[1], dtype_code(x.dtype), _addr(which),
+                                            index_code(which.dtype), _addr(scales), _addr(h), _addr(dy), dy.stride(0),
+                                            1 if accumulate else 0, _addr(dx), 0 if dx is None else dx.stride(0),
+                                            _addr(da), _addr(db), _addr(ws), _nbytes(ws), _raw_stream(stream)))
+
+
 # ------------------------------------------------------------- layer owner
 
 
@@ -442,6 +476,13 @@ class SparseLinear:
         snack_spmm_fwd_gelu(self.handle, self.row, self.col, self.val, x, x.shape[0], self.bias, pre, y, self.ws,
                             stream)
         return y, pre
+
+    def forward_adapted(self, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, which: torch.Tensor,
+                        scales: Optional[torch.Tensor] = None, keep: bool = False, stream=None):
+        """x W^T + b with each row's low-rank adapter beside it (see adapt); with keep, (y, h) for adapt_grad."""
+        x = x.contiguous()
+        y = self.forward(x, stream=stream)
+        return adapt(x, y, a, b, which, scales, out=y, keep=keep, stream=stream)
 
     def grad_input_gelu(self, dy: torch.Tensor, x_pre: torch.Tensor, stream=None) -> torch.Tensor:
         """(dy W) * GELU'(x_pre): the gradient at the pre-activation of this layer's input."""
@@ -804,3 +845,123 @@ class _XentFn(torch.autograd.Function):
 def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, reduction: str = "mean"):
     """Autograd-aware xent: the loss alone; gradients flow to x and w."""
     return _XentFn.apply(x, w, targets, reduction)
+
+
+_adapt_ws = functools.lru_cache(maxsize=256)(snack_adapt_workspace_size)
+
+
+def _adapt_args(x, a, b, which, scales):
+    """What both calls take of x and the adapters, and a workspace; and what to keep alive."""
+    x, xa, n, width, x_ld = _matrix(x)
+    if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2] or a.shape[2] != width:
+        raise ValueError("a must be [adapters, rank, width of x] and b [adapters, width of the output, rank]")
+    kind = x.dtype
+    if a.dtype != kind or b.dtype != kind:
+        raise ValueError("x, a and b must have one type")
+    if which.numel() != n:
+        raise ValueError("which needs one entry per row of x")
+    adapters, rank, _ = a.shape
+    if scales is not None:
+        if scales.dtype != torch.float32 or scales.numel() != adapters:
+            raise ValueError("scales must hold one float32 value per adapter")
+        scales = scales.contiguous()
+    a, b, which = a.contiguous(), b.contiguous(), which.contiguous()
+    nbytes = max(256, _adapt_ws(n, adapters, rank))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    args = (xa, x_ld, n, a.data_ptr(), b.data_ptr(), adapters, rank, width, b.shape[1], _code(_DTYPES, kind),
+            which.data_ptr(), _code(_INDICES, which.dtype), _addr(scales))
+    return args, ws, nbytes, (x, a, b, which, scales)
+
+
+def adapt(x: torch.Tensor, base: Optional[torch.Tensor], a: torch.Tensor, b: torch.Tensor, which: torch.Tensor,
+          scales: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, keep: bool = False, stream=None):
+    """base + scales[k] * (x A_k^T) B_k^T, where k = which[i] is the adapter of row i's request.
+
+    x [n, in], base [n, out] (None: 0), a [adapters, rank, in] and b [adapters,
+    out, rank] in one type; a row whose entry of which is outside the adapters keeps
+    its base.  The result goes to `out`, which may be base.  With keep, returns (y,
+    h): h (float32, [n, rank]) is what adapt_grad needs.
+    """
+    if not _here(x, stream, base, a, b, which, scales, out):
+        with _On(x.device, stream):
+            return adapt(x, base, a, b, which, scales, out, keep)
+    args, ws, nbytes, kept = _adapt_args(x, a, b, which, scales)
+    n, rank, out_f, kind = args[2], args[6], args[8], kept[0].dtype
+    base_addr, base_ld = None, 0
+    if base is not None:
+        if base.dtype != kind or tuple(base.shape) != (n, out_f):
+            raise ValueError(f"base must be a {kind} matrix [{n}, {out_f}]")
+        if out is not base:
+            base, base_addr, _, _, base_ld = _matrix(base)
+    y = torch.empty((n, out_f), dtype=kind, device=x.device) if out is None else _out_rows(out, n, out_f, kind)
+    y_ld = out_f if out is None or n < 2 else y.stride(0)
+    if base is not None and out is base:
+        base_addr, base_ld = y.data_ptr(), y_ld
+    h = torch.empty((n, rank), dtype=torch.float32, device=x.device) if keep else None
+    st = (_lib or load()).snack_adapt_fwd(*args, base_addr, base_ld, y.data_ptr(), y_ld, _addr(h), ws.data_ptr(), nbytes,
+                                          _raw_stream(None))
+    if st:
+        _check("snack_adapt_fwd", st)
+    if out is not None:
+        increment_version(out)
+    return (y, h) if keep else y
+
+
+def adapt_grad(x: torch.Tensor, dy: torch.Tensor, a: torch.Tensor, b: torch.Tensor, which: torch.Tensor,
+               h: Optional[torch.Tensor], scales: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+               want_dx: bool = True, want_da: bool = True, want_db: bool = True, stream=None):
+    """(dx, da, db) of adapt for the upstream gradient dy; base's gradient is dy itself.
+
+    dx is the adapters' part alone; given as an argument, it is added to what is
+    there (the projection's own input gradient).  h is what adapt kept (needed for db).
+    """
+    if not _here(x, stream, dy, a, b, which, h, scales, dx):
+        with _On(x.device, stream):
+            return adapt_grad(x, dy, a, b, which, h, scales, dx, want_dx, want_da, want_db)
+    args, ws, nbytes, kept = _adapt_args(x, a, b, which, scales)
+    n, adapters, rank, width, out_f, kind = args[2], args[5], args[6], args[7], args[8], kept[0].dtype
+    if dy.dtype != kind or tuple(dy.shape) != (n, out_f):
+        raise ValueError(f"dy must be a {kind} matrix [{n}, {out_f}]")
+    dy, dy_addr, _, _, dy_ld = _matrix(dy)
+    if h is None:
+        if want_db:
+            raise ValueError("the gradient of b needs h")
+    elif h.dtype != torch.float32 or tuple(h.shape) != (n, rank) or not h.is_contiguous():
+        raise ValueError("h must be what adapt kept for these arguments")
+    add = dx is not None
+    if add:
+        _out_rows(dx, n, width, kind)
+    elif want_dx:
+        dx = torch.empty((n, width), dtype=kind, device=x.device)
+    da = torch.empty((adapters, rank, width), dtype=kind, device=x.device) if want_da else None
+    db = torch.empty((adapters, out_f, rank), dtype=kind, device=x.device) if want_db else None
+    dx_ld = 0 if dx is None else width if n < 2 else dx.stride(0)
+    st = (_lib or load()).snack_adapt_bwd(*args, _addr(h), dy_addr, dy_ld, 1 if add else 0, _addr(dx), dx_ld, _addr(da),
+                                          _addr(db), ws.data_ptr(), nbytes, _raw_stream(None))
+    if st:
+        _check("snack_adapt_bwd", st)
+    if add:
+        increment_version(dx)
+    return dx, da, db
+
+
+class _AdaptFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, base, a, b, which, scales):
+        y, h = adapt(x, base, a, b, which, scales, keep=True)
+        ctx.save_for_backward(x, a, b, which, h, scales)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, a, b, which, h, scales = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, da, db = adapt_grad(x, dy, a, b, which, h, scales, None, need[0], need[2], need[3])
+        return dx, dy if need[1] else None, da, db, None, None
+
+
+def adapted(x: torch.Tensor, base: torch.Tensor, a: torch.Tensor, b: torch.Tensor, which: torch.Tensor,
+            scales: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Autograd-aware adapt; gradients flow to x, base, a and b (not to scales)."""
+    return _AdaptFn.apply(x, base, a, b, which, scales)
