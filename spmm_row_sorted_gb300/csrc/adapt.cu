@@ -179,42 +179,63 @@ struct Op;
 template <>
 struct Op<bf16> {
   static constexpr int kSteps = 2, kParts = 1, kLane = 8, kGroup = 32;  // elements per lane, K per group
+  static constexpr int kOwnParts = 2;                                   // of h and dh
 };
 template <>
 struct Op<float> {
   static constexpr int kSteps = 1, kParts = 3, kLane = 4, kGroup = 16;
+  static constexpr int kOwnParts = 3;
 };
 
-// V consecutive elements as they are; zeros from `left` on.  kConst: of memory that
-// the kernel does not write.
-template <typename T, int V, bool kConst = true>
+// V consecutive elements as they are; zeros from `left` on
+template <typename T, int V>
 __device__ __forceinline__ Pack<T, V * (int)sizeof(T)> load_vec(const T *p, int left, bool wide) {
   Pack<T, V * (int)sizeof(T)> r;
-  auto get = [](auto *at) { return kConst ? __ldg(at) : *at; };
   if (wide && left >= V) {
-    r.raw = get(reinterpret_cast<const typename Raw<V * (int)sizeof(T)>::type *>(p));
+    r.raw = __ldg(reinterpret_cast<const typename Raw<V * (int)sizeof(T)>::type *>(p));
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if constexpr (sizeof(T) == 4)
-        r.w[i] = i < left ? __float_as_uint(get(p + i)) : 0u;
+        r.w[i] = i < left ? __float_as_uint(__ldg(p + i)) : 0u;
       else
-        r.h[i] = i < left ? get(reinterpret_cast<const uint16_t *>(p) + i) : (uint16_t)0;
+        r.h[i] = i < left ? __ldg(reinterpret_cast<const uint16_t *>(p) + i) : (uint16_t)0;
     }
   }
   return r;
 }
-// the same of more than 16 bytes
-template <typename T, int V>
-struct Many {
-  static constexpr int kPer = V * (int)sizeof(T) > 16 ? 16 / (int)sizeof(T) : V;
-  Pack<T, kPer * (int)sizeof(T)> p[V / kPer];
-  __device__ __forceinline__ void load(const T *at, int left, bool wide) {
+
+// The same into shared memory, on its way while the lane works on: a lane reads
+// only what it wrote there itself, so its own wait is all that it needs.  kWide: the
+// address is aligned to V elements; bf16 that are not are read at once.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void *to, const void *from, int bytes) {
+  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(at), "l"(from), "r"(bytes), "n"(kBytes) : "memory");
+}
+template <typename T, int V, bool kWide>
+__device__ __forceinline__ void fetch_vec(void *to, const T *p, int left) {
+  constexpr int kBytes = V * (int)sizeof(T);
+  if constexpr (kWide) {
+    copy_async<kBytes>(to, p, max(0, min(left, V)) * (int)sizeof(T));
+  } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < V / kPer; ++i) p[i] = load_vec<T, kPer>(at + i * kPer, left - i * kPer, wide);
+    for (int i = 0; i < V; ++i) copy_async<4>(reinterpret_cast<float *>(to) + i, p + (i < left ? i : 0), i < left ? 4 : 0);
+  } else {
+    Pack<T, kBytes> r;
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.h[i] = i < left ? reinterpret_cast<const uint16_t *>(p)[i] : (uint16_t)0;
+    *reinterpret_cast<typename Raw<kBytes>::type *>(to) = r.raw;
   }
-  __device__ __forceinline__ float get(int i) const { return p[i / kPer].get(i % kPer); }
-};
+}
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void fetch_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
 
 // The upper halves of two words, as a pair of bf16.
 __device__ __forceinline__ uint32_t upper_halves(float lo, float hi) {
@@ -227,16 +248,15 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
   return r;
 }
 
-// A pair of values as kParts words of two bf16: three cut off, 8 significant bits
+// A pair of values as words of two bf16: three parts cut off, 8 significant bits
 // each, or two rounded.
 template <int kParts>
 __device__ __forceinline__ void cut_pair(float a, float b, uint32_t (&w)[kParts]) {
-  if constexpr (kParts == 1) {
-    w[0] = upper_halves(a, b);  // values that are bf16
-  } else if constexpr (kParts == 2) {
+  if constexpr (kParts == 2) {
     w[0] = pack_pair(a, b);
     w[1] = pack_pair(a - bf16_lo(w[0]), b - bf16_hi(w[0]));
   } else {
+    static_assert(kParts == 3, "two or three parts");
 #pragma unroll
     for (int p = 0; p < 3; ++p) {
       if (p) {
@@ -276,25 +296,29 @@ __device__ __forceinline__ void mma_step(float (&acc)[4], const uint32_t (&lo)[2
 }
 
 // a lane's words of a row along K: [step][half of the step's pairs][part]
-template <typename T>
+template <typename T, int V>
 struct Along {
-  uint32_t w[Op<T>::kSteps][2][Op<T>::kParts];
-  __device__ __forceinline__ void set(const Pack<T, 16> &v) {
-    if constexpr (sizeof(T) == 2) {
+  static constexpr int kSteps = V / 4;
+  uint32_t w[kSteps][2][Op<T>::kParts];
+  __device__ __forceinline__ void set(const Pack<T, V * (int)sizeof(T)> &v) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+    for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) w[s][h][0] = v.w[2 * s + h];
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) cut_pair<3>(v.get(2 * h), v.get(2 * h + 1), w[0][h]);
-    }
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (sizeof(T) == 2)
+          w[s][h][0] = v.w[2 * s + h];
+        else
+          cut_pair<3>(v.get(4 * s + 2 * h), v.get(4 * s + 2 * h + 1), w[s][h]);
+      }
   }
 };
-// pairs of element j of two rows that follow one another along K
-template <typename T, typename V>
-__device__ __forceinline__ void across(const V &a, const V &b, int j, uint32_t (&w)[Op<T>::kParts]) {
-  cut_pair<Op<T>::kParts>(a.get(j), b.get(j), w);
+// the pair of elements j of two rows that follow one another along K
+template <typename T, int B>
+__device__ __forceinline__ void across(const Pack<T, B> &a, const Pack<T, B> &b, int j, uint32_t (&w)[Op<T>::kParts]) {
+  if constexpr (sizeof(T) == 2)
+    w[0] = __byte_perm(a.w[j >> 1], b.w[j >> 1], j & 1 ? 0x7632 : 0x5410);
+  else
+    cut_pair<3>(a.get(j), b.get(j), w);
 }
 
 // ------------------------------------------------------------ h and dh
@@ -309,16 +333,22 @@ struct DownArgs {
   int32_t adapters;
   const float *scales;  // null: 1
   float *h;             // [n][rank]
-  int x_wide, m_wide;
 };
 
 constexpr int kDownWarps = 8;
+// groups of K a warp has on their way or in hand, so that an SM has 130 to 190 KB
+__host__ __device__ constexpr int down_stages(int nt) { return nt >= 8 ? 3 : 4; }
+__host__ __device__ constexpr int down_smem(int nt) {
+  const int ring = kDownWarps * down_stages(nt) * (kTile / 8 + nt) * 512, sums = 4 * kTile * 8 * nt * 4;
+  return ring > sums ? ring : sums;
+}
 
-// The sums of kDownWarps warps over their parts of K, and of the cluster's blocks.
-template <typename T, int MT, int NT, bool kAlong>
+// The sums of kDownWarps warps over their groups of K, and of the cluster's blocks.
+template <typename T, int MT, int NT, bool kAlong, bool kWide>
 __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, float *smem) {
   typedef Op<T> O;
-  constexpr int kRows = 16 * MT, kCols = 8 * NT;
+  constexpr int kRows = 16 * MT, kCols = 8 * NT, kStages = down_stages(NT), kSlots = kTile / 8 + NT;
+  typedef Pack<T, NT * (int)sizeof(T)> Cross;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, q = lane & 3;
   const int r0 = blockIdx.y * kCols;
@@ -330,65 +360,88 @@ __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, f
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
-  const T *row[MT][2];
+  const T *row[2 * MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {  // the rows past the tile's end are the last one's again, and not kept
-      const int at = min(16 * m + 8 * h + g, tile.count - 1);
-      row[m][h] = reinterpret_cast<const T *>(a.x) + (int64_t)__ldg(a.order + tile.first + at) * a.x_ld + O::kLane * q;
-    }
+  for (int i = 0; i < 2 * MT; ++i)  // the rows past the tile's end are the last one's again, and not kept
+    row[i] = reinterpret_cast<const T *>(a.x) + (int64_t)__ldg(a.order + tile.first + min(8 * i + g, tile.count - 1)) * a.x_ld +
+             O::kLane * q;
   const T *mat = reinterpret_cast<const T *>(a.m) + (int64_t)tile.adapter * a.rank * a.k;
-  for (int k0 = (int)(rank * kDownWarps + warp) * O::kGroup; k0 < a.k; k0 += (int)blocks * kDownWarps * O::kGroup) {
-    const int left = a.k - k0 - O::kLane * q;
-    Pack<T, 16> xv[MT][2];
+  // this lane's ring: kStages x (its 16 bytes of every 8th row; of the matrix NT of them, or the same bytes in smaller pieces)
+  uint4 *ring = reinterpret_cast<uint4 *>(smem) + (warp * kStages * kSlots) * 32 + lane;
+  const int step = (int)blocks * kDownWarps * O::kGroup;
+  int next = (int)(rank * kDownWarps + warp) * O::kGroup;
+  auto fetch = [&](int stage) {
+    if (next < a.k) {
+      uint4 *to = ring + stage * kSlots * 32;
+      const int left = a.k - next - O::kLane * q;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+      for (int i = 0; i < 2 * MT; ++i) fetch_vec<T, O::kLane, kWide>(to + i * 32, row[i] + next, left);
+      to += kTile / 8 * 32;
+      if constexpr (kAlong) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) xv[m][h] = load_vec<T, O::kLane>(row[m][h] + k0, left, a.x_wide);
-    if constexpr (kAlong) {
-      Pack<T, 16> mv[NT];
+        for (int j = 0; j < NT; ++j) {
+          const int r = r0 + 8 * j + g;
+          fetch_vec<T, O::kLane, kWide>(to + j * 32, mat + (int64_t)min(r, a.rank - 1) * a.k + next + O::kLane * q, r < a.rank ? left : 0);
+        }
+      } else {  // rows next + kLane q + i: ranks NT g .. NT g + NT - 1
+        typename Cross::R *piece = reinterpret_cast<typename Cross::R *>(to - lane) + lane;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int r = r0 + 8 * j + g;
-        mv[j] = load_vec<T, O::kLane>(mat + (int64_t)min(r, a.rank - 1) * a.k + k0 + O::kLane * q, r < a.rank ? left : 0, a.m_wide);
+        for (int i = 0; i < O::kLane; ++i)
+          fetch_vec<T, NT, kWide>(piece + i * 32, mat + (int64_t)min(next + O::kLane * q + i, a.k - 1) * a.rank + r0 + NT * g,
+                                  i < left ? a.rank - r0 - NT * g : 0);
       }
-      Along<T> xa[MT][2];
+    }
+    fetch_commit();
+    next += step;
+  };
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+  for (int s = 0; s < kStages - 1; ++s) fetch(s);
+  int stage = 0;
+  for (int k0 = next - (kStages - 1) * step; k0 < a.k; k0 += step) {
+    fetch(stage == 0 ? kStages - 1 : stage - 1);
+    fetch_wait<kStages - 1>();
+    const uint4 *from = ring + stage * kSlots * 32;
+    Along<T, O::kLane> xa[2 * MT];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) xa[m][h].set(xv[m][h]);
+    for (int i = 0; i < 2 * MT; ++i) {
+      Pack<T, 16> v;
+      v.raw = from[i * 32];
+      xa[i].set(v);
+    }
+    from += kTile / 8 * 32;
+    if constexpr (kAlong) {
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        Along<T> b;
-        b.set(mv[j]);
+        Pack<T, 16> v;
+        v.raw = from[j * 32];
+        Along<T, O::kLane> b;
+        b.set(v);
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int s = 0; s < O::kSteps; ++s)
 #pragma unroll
-          for (int s = 0; s < O::kSteps; ++s) mma_step(acc[m][j], xa[m][0].w[s], xa[m][1].w[s], b.w[s]);
+          for (int m = 0; m < MT; ++m) mma_step(acc[m][j], xa[2 * m].w[s], xa[2 * m + 1].w[s], b.w[s]);
       }
     } else {
-      Many<T, NT> mv[O::kLane];  // rows k0 + kLane q + i: ranks NT g .. NT g + NT - 1
+      const typename Cross::R *piece = reinterpret_cast<const typename Cross::R *>(from - lane) + lane;
 #pragma unroll
-      for (int i = 0; i < O::kLane; ++i)
-        mv[i].load(mat + (int64_t)min(k0 + O::kLane * q + i, a.k - 1) * a.rank + r0 + NT * g, i < left ? a.rank - r0 - NT * g : 0, a.m_wide);
-      Along<T> xa[MT][2];
+      for (int s = 0; s < O::kSteps; ++s) {
+        Cross v[4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+        for (int i = 0; i < 4; ++i) v[i].raw = piece[(4 * s + i) * 32];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) xa[m][h].set(xv[m][h]);
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int s = 0; s < O::kSteps; ++s) {
+        for (int j = 0; j < NT; ++j) {
           uint32_t b[2][O::kParts];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) across<T>(mv[4 * s + 2 * h], mv[4 * s + 2 * h + 1], j, b[h]);
+          for (int h = 0; h < 2; ++h) across<T>(v[2 * h], v[2 * h + 1], j, b[h]);
 #pragma unroll
-          for (int m = 0; m < MT; ++m) mma_step(acc[m][j], xa[m][0].w[s], xa[m][1].w[s], b);
+          for (int m = 0; m < MT; ++m) mma_step(acc[m][j], xa[2 * m].w[s], xa[2 * m + 1].w[s], b);
         }
+      }
     }
+    if (++stage == kStages) stage = 0;
   }
+  fetch_wait<0>();
+  __syncthreads();  // the ring becomes the sums
   // the warps' sums: the upper half's to the lower half, then those of the four
   float *own = smem + (warp & 3) * (kRows * kCols);
   auto each = [&](auto f) {
@@ -425,16 +478,16 @@ __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, f
   if (blocks > 1) cluster_sync();  // no block's memory is read any more
 }
 
-template <typename T, int NT, bool kAlong>
-__global__ void __launch_bounds__(kDownWarps * 32) k_adapt_down(const DownArgs a) {
+template <typename T, int NT, bool kAlong, bool kWide>
+__global__ void __launch_bounds__(kDownWarps * 32, 1) k_adapt_down(const DownArgs a) {
   pdl_wait();
-  extern __shared__ __align__(16) float down_smem[];
+  extern __shared__ __align__(16) float down_ring[];
   const Tile tile = a.tiles[blockIdx.x / cluster_blocks()];
   if (tile.adapter < 0 || tile.adapter >= a.adapters) return;  // the whole cluster's
   if (tile.count <= 16)
-    down_tile<T, 1, NT, kAlong>(a, tile, down_smem);
+    down_tile<T, 1, NT, kAlong, kWide>(a, tile, down_ring);
   else
-    down_tile<T, 4, NT, kAlong>(a, tile, down_smem);
+    down_tile<T, 4, NT, kAlong, kWide>(a, tile, down_ring);
 }
 
 // ------------------------------------------------------------ y and dx
@@ -452,22 +505,43 @@ struct UpArgs {
   void *out;
   int64_t out_ld;
   int groups;            // of 32 columns, per warp
-  int m_wide, base_wide, out_wide;
+  int h_wide;
 };
 
-constexpr int kUpWarps = 4;
+constexpr int kUpWarps = 8;
 constexpr int kUpCols = 32;  // columns of a warp at a time
 
-// of a row of h's parts in shared memory, in elements: rows start 32 bytes apart modulo 128
-__host__ __device__ __forceinline__ int up_ld(int rank) { return (rank + 63) / 64 * 64 + 16; }
+// Of a row of h in shared memory, in elements: rows start 32 bytes apart modulo 128 as
+// bf16 (its two parts), 64 as fp32 (which is cut into parts as it is read); the
+// highest ranks have no room for that.
+__host__ __device__ constexpr int up_ld(int rank) { return rank > 240 ? kMostRank + 4 : (rank + 63) / 64 * 64 + 16; }
+constexpr size_t up_h_bytes(int rank) { return (size_t)kTile * up_ld(rank) * 4; }
+// shared memory of a lane: its 16-byte pieces of the base, and its pieces of the matrix (8 bytes of bf16, 16 of fp32)
+template <typename T>
+__host__ __device__ constexpr int up_base_bytes() { return kTile / 8 * 8 * (int)sizeof(T); }
+template <typename T, int kSteps>
+__host__ __device__ constexpr int up_stage_bytes() { return up_base_bytes<T>() + kSteps * 4 * 4 * (int)sizeof(T); }
+template <typename T>
+__host__ __device__ constexpr int up_stages() { return sizeof(T) == 2 ? 3 : 2; }
 
-template <typename T, bool kAlong>
-__global__ void __launch_bounds__(kUpWarps * 32) k_adapt_up(const UpArgs a) {
+static_assert(kUpWarps * up_stages<bf16>() * up_stage_bytes<bf16, 4>() * 32 + up_h_bytes(64) <= 232448 &&
+                  kUpWarps * up_stages<bf16>() * up_stage_bytes<bf16, 2>() * 32 + up_h_bytes(kMostRank) <= 232448 &&
+                  kUpWarps * up_stages<float>() * up_stage_bytes<float, 1>() * 32 + up_h_bytes(kMostRank) <= 232448,
+              "shared memory of one block");
+
+// A warp takes 32 columns of the tile after 32 others; what it reads of the base and
+// the matrix is on its way one or two turns before, kSteps of 16 of the rank per turn.
+// The sums begin with the base, so the result is rounded as it leaves; h has its
+// scale before it is cut into parts.
+template <typename T, bool kAlong, int kSteps, bool kWide>
+__global__ void __launch_bounds__(kUpWarps * 32, 1) k_adapt_up(const UpArgs a) {
   pdl_wait();
-  constexpr int kHp = sizeof(T) == 2 ? 2 : 3, kBp = Op<T>::kParts, MT = kTile / 16, NT = 4;
+  constexpr int kHp = Op<T>::kOwnParts, kBp = Op<T>::kParts, MT = kTile / 16, NT = 4, kStages = up_stages<T>();
   typedef Pack<T, 16> P;
+  typedef Pack<T, 4 * (int)sizeof(T)> P4;
   constexpr int kPer = P::kN, kVecs = 8 / kPer;  // accesses for a lane's 8 columns
-  extern __shared__ __align__(16) uint32_t up_smem[];
+  constexpr int kStage = up_stage_bytes<T, kSteps>() * 32;
+  extern __shared__ __align__(16) uint8_t up_ring[];
   const Tile tile = a.tiles[blockIdx.x];
   if (tile.adapter < 0) return;
   const bool none = tile.adapter >= a.adapters;
@@ -475,111 +549,184 @@ __global__ void __launch_bounds__(kUpWarps * 32) k_adapt_up(const UpArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, q = lane & 3;
   const int ld = up_ld(a.rank) / 2, plane = kTile * ld;  // in words
-  const int steps = (a.rank + 15) / 16;
+  const int steps = none ? 1 : (a.rank + 15) / 16, turns = (steps + kSteps - 1) / kSteps;
   const int m_tiles = (tile.count + 15) / 16;
-  if (!none) {
-    const int pairs = steps * 8;
-    for (int i = threadIdx.x; i < m_tiles * 16 * pairs; i += kUpWarps * 32) {
-      const int t = i / pairs, r = (i - t * pairs) * 2;
-      const float *at = a.h + (int64_t)(t < tile.count ? a.order[tile.first + t] : 0) * a.rank + r;
-      const float lo = t < tile.count && r < a.rank ? __ldg(at) : 0.f, hi = t < tile.count && r + 1 < a.rank ? __ldg(at + 1) : 0.f;
-      uint32_t w[kHp];
-      cut_pair<kHp>(lo, hi, w);
+  uint8_t *ring = up_ring + warp * kStages * kStage;
+  uint32_t *hs = reinterpret_cast<uint32_t *>(up_ring + kUpWarps * kStages * kStage);
+  const T *mat = reinterpret_cast<const T *>(a.m) + (none ? 0 : (int64_t)tile.adapter * a.rank * a.cols);
+  int32_t token[2 * MT];
 #pragma unroll
-      for (int p = 0; p < kHp; ++p) up_smem[p * plane + t * ld + (r >> 1)] = w[p];
+  for (int i = 0; i < 2 * MT; ++i) token[i] = 8 * i + g < tile.count ? __ldg(a.order + tile.first + 8 * i + g) : -1;
+  const int col0 = (blockIdx.y * a.groups * kUpWarps + warp) * kUpCols;
+  const int items = (a.cols <= col0 ? 0 : min(a.groups, (a.cols - col0 + kUpWarps * kUpCols - 1) / (kUpWarps * kUpCols))) * turns;
+  int next_col = col0, next_turn = 0, next_stage = 0, next_item = 0;
+  auto fetch = [&] {
+    if (next_item < items) {
+      uint8_t *to = ring + next_stage * kStage;
+      const int left = a.cols - next_col - 8 * q;
+      if (next_turn == 0 && a.base) {
+        uint4 *at = reinterpret_cast<uint4 *>(to) + lane;
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) {
+          if (i >= 2 * m_tiles) break;
+          const T *from = reinterpret_cast<const T *>(a.base) + max(token[i], 0) * a.base_ld + next_col + 8 * q;
+#pragma unroll
+          for (int v = 0; v < kVecs; ++v) fetch_vec<T, kPer, kWide>(at + (i * kVecs + v) * 32, from + v * kPer, left - v * kPer);
+        }
+      }
+      if (!none) {
+        typename P4::R *at = reinterpret_cast<typename P4::R *>(to + up_base_bytes<T>() * 32) + lane;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (kAlong) {  // lane g has column 8 (g / 2) + 2 j + g % 2: a lane's sums are 8 neighbours
+              const int col = next_col + 8 * (g >> 1) + 2 * j + (g & 1), r = 16 * (next_turn * kSteps + s) + 4 * q;
+              fetch_vec<T, 4, kWide>(at + (4 * s + j) * 32, mat + (int64_t)min(col, a.cols - 1) * a.rank + (r < a.rank ? r : 0),
+                                     col < a.cols ? a.rank - r : 0);
+            } else {  // columns 4 g .. 4 g + 3
+              const int r = 16 * (next_turn * kSteps + s) + 4 * q + j;
+              fetch_vec<T, 4, kWide>(at + (4 * s + j) * 32, mat + (int64_t)min(r, a.rank - 1) * a.cols + (next_col + 4 * g < a.cols ? next_col + 4 * g : 0),
+                                     r < a.rank ? a.cols - next_col - 4 * g : 0);
+            }
+          }
+      }
+      if (++next_turn == turns) {
+        next_turn = 0;
+        next_col += kUpWarps * kUpCols;
+      }
+    }
+    fetch_commit();
+    ++next_item;
+    if (++next_stage == kStages) next_stage = 0;
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) fetch();
+  if (!none) {
+    const float scale = a.scales ? a.scales[tile.adapter] : 1.f;
+    const int quads = steps * 4;
+    for (int i = threadIdx.x; i < m_tiles * 16 * quads; i += kUpWarps * 32) {
+      const int t = i / quads, r = (i - t * quads) * 4;
+      const bool in = t < tile.count;
+      const auto v = load_vec<float, 4>(a.h + (int64_t)(in ? __ldg(a.order + tile.first + t) : 0) * a.rank + r, in ? a.rank - r : 0, a.h_wide);
+      if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4 *>(hs + t * up_ld(a.rank) + r) =
+            make_float4(scale * v.get(0), scale * v.get(1), scale * v.get(2), scale * v.get(3));
+      } else {
+        uint32_t w[2][kHp];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) cut_pair<kHp>(scale * v.get(2 * h), scale * v.get(2 * h + 1), w[h]);
+#pragma unroll
+        for (int p = 0; p < kHp; ++p) *reinterpret_cast<uint2 *>(hs + p * plane + t * ld + (r >> 1)) = make_uint2(w[0][p], w[1][p]);
+      }
     }
   }
   __syncthreads();
-  const float scale = none ? 0.f : a.scales ? a.scales[tile.adapter] : 1.f;
-  const T *mat = reinterpret_cast<const T *>(a.m) + (none ? 0 : (int64_t)tile.adapter * a.rank * a.cols);
-  for (int u = 0; u < a.groups; ++u) {
-    const int n0 = ((blockIdx.y * a.groups + u) * kUpWarps + warp) * kUpCols;
-    if (n0 >= a.cols) break;
-    float acc[MT][NT][4];
+  float acc[MT][NT][4];
+  // a lane's 8 columns: which sum has column e of row half h
+  auto sum_at = [&](int m, int h, int e) -> float & { return kAlong ? acc[m][e >> 1][2 * h + (e & 1)] : acc[m][e & 3][2 * h + (e >> 2)]; };
+  int c = col0 + 8 * q, turn = 0, stage = 0;
+  for (int item = 0; item < items; ++item) {
+    fetch();
+    fetch_wait<kStages - 1>();
+    const uint8_t *from = ring + stage * kStage;
+    if (turn == 0) {
+      const uint4 *at = reinterpret_cast<const uint4 *>(from) + lane;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
-    for (int s = 0; s < (none ? 0 : steps); ++s) {
-      uint32_t b[NT][2][kBp];
-      if constexpr (kAlong) {  // lane g has column 8 (g / 2) + 2 j + g % 2: a lane's sums are 8 neighbours
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const int c = n0 + 8 * (g >> 1) + 2 * j + (g & 1), r = 16 * s + 4 * q;
-          const auto v = load_vec<T, 4>(mat + (int64_t)min(c, a.cols - 1) * a.rank + r, c < a.cols ? a.rank - r : 0, a.m_wide);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) cut_pair<kBp>(v.get(2 * h), v.get(2 * h + 1), b[j][h]);
-        }
-      } else {  // column 4 g + j
-        Pack<T, 4 * (int)sizeof(T)> v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 16 * s + 4 * q + i;
-          v[i] = load_vec<T, 4>(mat + (int64_t)min(r, a.rank - 1) * a.cols + n0 + 4 * g, r < a.rank ? a.cols - n0 - 4 * g : 0, a.m_wide);
-        }
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) across<T>(v[2 * h], v[2 * h + 1], j, b[j][h]);
-      }
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        if (m >= m_tiles) break;
-        uint32_t w[2][2][kHp];  // rows g and g + 8
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int p = 0; p < kHp; ++p) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(up_smem + p * plane + (16 * m + 8 * h + g) * ld + 8 * s + 2 * q);
-            w[h][0][p] = v.x;
-            w[h][1][p] = v.y;
-          }
-#pragma unroll
-        for (int j = 0; j < NT; ++j) mma_step(acc[m][j], w[0], w[1], b[j]);
-      }
-    }
-    const int c = n0 + 8 * q, left = a.cols - c;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      if (m >= m_tiles) break;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int t = 16 * m + 8 * h + g;
-        if (t >= tile.count || left <= 0) continue;
-        const int64_t token = a.order[tile.first + t];
-        const T *base = reinterpret_cast<const T *>(a.base) + token * a.base_ld + c;
-        T *out = reinterpret_cast<T *>(a.out) + token * a.out_ld + c;
+      for (int i = 0; i < 2 * MT; ++i) {
+        if (i >= 2 * m_tiles) break;
 #pragma unroll
         for (int v = 0; v < kVecs; ++v) {
-          P o;
-          if (a.base)
-            o = load_vec<T, kPer, false>(base + v * kPer, left - v * kPer, a.base_wide);
-          else
-            o.raw = make_uint4(0, 0, 0, 0);
-          if (!none)
+          P old;
+          old.raw = a.base ? at[(i * kVecs + v) * 32] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-              const int e = v * kPer + i;  // of the lane's 8 columns
-              const float d = kAlong ? acc[m][e >> 1][2 * h + (e & 1)] : acc[m][e & 3][2 * h + (e >> 2)];
-              o.set(i, fmaf(scale, d, o.get(i)));
-            }
-          if (a.out_wide && left >= (v + 1) * kPer) {
-            *reinterpret_cast<uint4 *>(out + v * kPer) = o.raw;
-          } else {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-              if (v * kPer + i < left) {
-                if constexpr (sizeof(T) == 4)
-                  out[v * kPer + i] = o.get(i);
-                else
-                  reinterpret_cast<uint16_t *>(out)[v * kPer + i] = o.h[i];
-              }
-          }
+          for (int e = 0; e < kPer; ++e) sum_at(i >> 1, i & 1, v * kPer + e) = old.get(e);
         }
       }
     }
+    if (!none) {
+      const typename P4::R *at = reinterpret_cast<const typename P4::R *>(from + up_base_bytes<T>() * 32) + lane;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int k = turn * kSteps + s;
+        if (k >= steps) break;
+        P4 mv[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mv[j].raw = at[(4 * s + j) * 32];
+        uint32_t b[NT][2][kBp];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          if constexpr (kAlong) {
+            Along<T, 4> w;
+            w.set(mv[j]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int p = 0; p < kBp; ++p) b[j][h][p] = w.w[0][h][p];
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) across<T>(mv[2 * h], mv[2 * h + 1], j, b[j][h]);
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if (m >= m_tiles) break;
+          uint32_t w[2][2][kHp];  // rows g and g + 8
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int t = 16 * m + 8 * h + g;
+            if constexpr (sizeof(T) == 4) {
+              const float4 v = *reinterpret_cast<const float4 *>(hs + t * up_ld(a.rank) + 16 * k + 4 * q);
+              cut_pair<kHp>(v.x, v.y, w[h][0]);
+              cut_pair<kHp>(v.z, v.w, w[h][1]);
+            } else {
+#pragma unroll
+              for (int p = 0; p < kHp; ++p) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(hs + p * plane + t * ld + 8 * k + 2 * q);
+                w[h][0][p] = v.x;
+                w[h][1][p] = v.y;
+              }
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) mma_step(acc[m][j], w[0], w[1], b[j]);
+        }
+      }
+    }
+    if (++stage == kStages) stage = 0;
+    if (++turn < turns) continue;
+    turn = 0;
+    const int left = a.cols - c;
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) {
+      if (i >= 2 * m_tiles) break;
+      if (token[i] < 0 || left <= 0) continue;
+      T *out = reinterpret_cast<T *>(a.out) + token[i] * a.out_ld + c;
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) {
+        P o;
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o.w[e] = pack_pair(sum_at(i >> 1, i & 1, 2 * e), sum_at(i >> 1, i & 1, 2 * e + 1));
+        } else {
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) o.set(e, sum_at(i >> 1, i & 1, v * kPer + e));
+        }
+        if constexpr (kWide) {  // all of it or nothing: whole accesses make up a row
+          if (left >= (v + 1) * kPer) *reinterpret_cast<uint4 *>(out + v * kPer) = o.raw;
+        } else {
+#pragma unroll
+          for (int e = 0; e < kPer; ++e)
+            if (v * kPer + e < left) {
+              if constexpr (sizeof(T) == 4)
+                out[v * kPer + e] = o.get(e);
+              else
+                reinterpret_cast<uint16_t *>(out)[v * kPer + e] = o.h[e];
+            }
+        }
+      }
+    }
+    c += kUpWarps * kUpCols;
   }
 }
 
@@ -594,29 +741,41 @@ struct OuterArgs {
   const float *scales;  // null: 1
   void *out;            // [rank][cols] of each adapter, or [cols][rank]
   int turned;           // the latter
-  int v_wide, x_wide;
+  int v_wide;
 };
 
-constexpr int kOuterWarps = 8, kOuterSlices = 4;  // slices of columns x shares of the rows
-
-// An adapter's sums over its rows for up to 16 MT of the rank and four slices of 8
-// kLane columns: a warp has one slice and every other 16 rows of the block's, the
-// cluster's blocks have stretches of the rows.
+constexpr int kOuterWarps = 8;
+constexpr int kOuterRows = 32;    // rows of v in shared memory at a time: two steps of 16
+constexpr int kOuterStages = 4;   // of x, on its way
+__host__ __device__ constexpr int outer_cols(int lane) { return kOuterWarps * 8 * lane; }  // of a block
 template <typename T, int MT>
-__global__ void __launch_bounds__(kOuterWarps * 32) k_adapt_outer(const OuterArgs a) {
+constexpr int outer_v_words() { return Op<T>::kOwnParts * 2 * MT * 128; }  // a fragment: 4 words of 32 lanes
+template <typename T, int MT>
+constexpr size_t outer_smem() {
+  const size_t ring = (size_t)kOuterWarps * kOuterStages * 8 * 512 + 2 * (size_t)outer_v_words<T, MT>() * 4;
+  const size_t sums = (size_t)16 * MT * (outer_cols(Op<T>::kLane) + 1) * 4;
+  return ring > sums ? ring : sums;
+}
+
+// An adapter's sums over its rows, 32 at a time, for 16 MT of the rank: a warp has 8
+// kLane columns, the cluster's blocks have every so many of the rows.  The block's
+// warps share the rows' v, cut into parts and laid out as mma.sync reads it.
+template <typename T, int MT, bool kWide>
+__global__ void __launch_bounds__(kOuterWarps * 32, 1) k_adapt_outer(const OuterArgs a) {
   pdl_wait();
   typedef Op<T> O;
-  constexpr int NT = O::kLane, kCols = 8 * NT, kRank = 16 * MT, kPer = 2 * MT;  // ranks of a lane
-  constexpr int kVp = sizeof(T) == 2 ? 2 : 3;
-  extern __shared__ __align__(16) float outer_smem[];  // [kOuterSlices][kRank][kCols]
+  constexpr int NT = O::kLane, kCols = 8 * NT, kRank = 16 * MT, kVp = O::kOwnParts, kThreads = kOuterWarps * 32;
+  constexpr int kVWords = outer_v_words<T, MT>(), kPitch = outer_cols(NT) + 1;
+  extern __shared__ __align__(16) uint32_t outer_ring[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, q = lane & 3;
   const uint32_t block = cluster_rank(), blocks = cluster_blocks();
-  const int slice = warp % kOuterSlices, share = warp / kOuterSlices;
-  constexpr int kShares = kOuterWarps / kOuterSlices;
   const int adapter = blockIdx.y, r0 = blockIdx.z * kRank;
-  const int c0 = ((int)(blockIdx.x / blocks) * kOuterSlices + slice) * kCols;
+  const int b0 = (int)(blockIdx.x / blocks) * kOuterWarps * kCols;
   const int first = a.start[adapter], end = a.start[adapter + 1];
+  const int lane_c = b0 + warp * kCols + NT * g, left = a.cols - lane_c;
+  uint4 *ring = reinterpret_cast<uint4 *>(outer_ring) + warp * kOuterStages * 8 * 32 + lane;
+  uint32_t *vs = outer_ring + kOuterWarps * kOuterStages * 8 * 128;  // [2][step][part][m tile][lane][4]
   float acc[MT][NT][4];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -624,75 +783,135 @@ __global__ void __launch_bounds__(kOuterWarps * 32) k_adapt_outer(const OuterArg
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
-  const int lane_c = c0 + NT * g, left = a.cols - lane_c, lane_r = r0 + kPer * g, r_left = a.rank - lane_r;
-  if (c0 < a.cols)
-    for (int p0 = first + (int)(block * kShares + share) * 16; p0 < end; p0 += (int)blocks * kShares * 16) {
-      Pack<T, 16> xv[4];
-      Many<float, kPer> vv[4];
+  const int step = (int)blocks * kOuterRows;
+  const int p_first = first + (int)block * kOuterRows;
+  // lane l: the row at place l of the 32 from p0 on (-1 past the end)
+  auto tokens_at = [&](int p0) { return p0 + lane < end ? __ldg(a.order + p0 + lane) : -1; };
+  // x: rows 16 s + 4 q + i; zeros past the end
+  auto fetch = [&](int tokens, bool any, int stage) {
+    if (any) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // rows 4 q + i of the 16; zeros past the end
-        const int p = p0 + 4 * q + i;
-        const int64_t token = a.order[min(p, end - 1)];
-        xv[i] = load_vec<T, NT>(reinterpret_cast<const T *>(a.x) + token * a.x_ld + lane_c, p < end ? left : 0, a.x_wide);
-        vv[i].load(a.v + token * a.rank + lane_r, p < end ? r_left : 0, a.v_wide);
-      }
-      uint32_t w[MT][2][2][kVp];  // m tile, rows g and g + 8 of it: ranks 2 m and 2 m + 1 of the lane's
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) cut_pair<kVp>(vv[2 * k].get(2 * m + h), vv[2 * k + 1].get(2 * m + h), w[m][h][k]);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        uint32_t b[2][O::kParts];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) across<T>(xv[2 * k], xv[2 * k + 1], j, b[k]);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) mma_step(acc[m][j], w[m][0], w[m][1], b);
+      for (int i = 0; i < 8; ++i) {
+        const int token = __shfl_sync(0xffffffffu, tokens, 16 * (i >> 2) + 4 * q + (i & 3));
+        fetch_vec<T, NT, kWide>(ring + (stage * 8 + i) * 32, reinterpret_cast<const T *>(a.x) + max(token, 0) * a.x_ld + (left > 0 ? lane_c : 0),
+                                token >= 0 ? left : 0);
       }
     }
-  float *own = outer_smem + slice * kRank * kCols;
-  auto each = [&](auto f) {
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          f(own[(kPer * g + 2 * m + (e >> 1)) * kCols + NT * (2 * q + (e & 1)) + j], acc[m][j][e]);
+    fetch_commit();
   };
+  // v: a thread has four ranks of two neighbouring rows, several times for the larger ranks
+  constexpr int kQuads = kRank / 4, kJobs = kOuterRows / 2 * kQuads, kOwn = (kJobs + kThreads - 1) / kThreads;
+  Pack<float, 16> held[kOwn][2];
+  auto read_v = [&](int tokens) {
 #pragma unroll
-  for (int s = 0; s < kShares; ++s) {
-    if (share == s) {
-      if (s == 0)
-        each([](float &t, float &v) { t = v; });
-      else
-        each([](float &t, float &v) { t += v; });
+    for (int o = 0; o < kOwn; ++o) {
+      const int job = threadIdx.x + o * kThreads, r = r0 + job % kQuads * 4;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int token = __shfl_sync(0xffffffffu, tokens, (job / kQuads * 2 + k) & 31);
+        const bool in = (kJobs % kThreads == 0 || job < kJobs) && token >= 0;
+        held[o][k] = load_vec<float, 4>(a.v + (in ? (int64_t)token * a.rank + r : 0), in ? a.rank - r : 0, a.v_wide);
+      }
     }
-    __syncthreads();
+  };
+  auto put_v = [&](uint32_t *to) {
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o) {
+      const int job = threadIdx.x + o * kThreads;
+      if (kJobs % kThreads != 0 && job >= kJobs) break;
+      // row 16 s + 4 q' + 2 k of the pair; rank 16 m + 8 h + g'
+      const int row = job / kQuads * 2, s = row >> 4, qq = (row >> 2) & 3, k = (row >> 1) & 1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = job % kQuads * 4 + e, m = r >> 4, h = (r >> 3) & 1, gg = r & 7;
+        uint32_t w[kVp];
+        cut_pair<kVp>(held[o][0].get(e), held[o][1].get(e), w);
+#pragma unroll
+        for (int p = 0; p < kVp; ++p) to[(((s * kVp + p) * MT + m) * 32 + gg * 4 + qq) * 4 + 2 * k + h] = w[p];
+      }
+    }
+  };
+  if (p_first < end) {
+    int ahead[kOuterStages];  // the rows of the steps to come: of the next one, ..., of the one to fetch
+    {
+      const int now = tokens_at(p_first);
+#pragma unroll
+      for (int s = 0; s < kOuterStages; ++s) ahead[s] = tokens_at(p_first + (s + 1) * step);
+      fetch(now, true, 0);
+      read_v(now);
+#pragma unroll
+      for (int s = 1; s < kOuterStages - 1; ++s) fetch(ahead[s - 1], p_first + s * step < end, s);
+    }
+    int stage = 0, turn = 0;
+    for (int p0 = p_first; p0 < end; p0 += step, turn ^= 1) {
+      put_v(vs + turn * kVWords);
+      fetch(ahead[kOuterStages - 2], p0 + (kOuterStages - 1) * step < end, stage == 0 ? kOuterStages - 1 : stage - 1);
+      if (p0 + step < end) read_v(ahead[0]);
+#pragma unroll
+      for (int s = 0; s + 1 < kOuterStages; ++s) ahead[s] = ahead[s + 1];
+      ahead[kOuterStages - 1] = tokens_at(p0 + (kOuterStages + 1) * step);
+      __syncthreads();  // one per turn: a buffer is written again after the other one's
+      fetch_wait<kOuterStages - 1>();
+      const uint4 *frag = reinterpret_cast<const uint4 *>(vs + turn * kVWords) + lane;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        Pack<T, 16> xv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xv[i].raw = ring[(stage * 8 + 4 * s + i) * 32];
+        uint32_t w[MT][2][2][kVp];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int p = 0; p < kVp; ++p) {
+            const uint4 f = frag[((s * kVp + p) * MT + m) * 32];
+            w[m][0][0][p] = f.x;
+            w[m][1][0][p] = f.y;
+            w[m][0][1][p] = f.z;
+            w[m][1][1][p] = f.w;
+          }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          uint32_t b[2][O::kParts];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) across<T>(xv[2 * k], xv[2 * k + 1], j, b[k]);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) mma_step(acc[m][j], w[m][0], w[m][1], b);
+        }
+      }
+      if (++stage == kOuterStages) stage = 0;
+    }
+    fetch_wait<0>();
   }
-  if (blocks > 1) cluster_sync();
+  __syncthreads();  // the rings become the sums
+  float *sums = reinterpret_cast<float *>(outer_ring);
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        sums[(16 * m + 8 * (e >> 1) + g) * kPitch + warp * kCols + NT * (2 * q + (e & 1)) + j] = acc[m][j][e];
+  if (blocks > 1)
+    cluster_sync();
+  else
+    __syncthreads();
   const float scale = a.scales ? a.scales[adapter] : 1.f;
   T *out = reinterpret_cast<T *>(a.out) + (int64_t)adapter * a.rank * a.cols;
-  const int b0 = (int)(blockIdx.x / blocks) * kOuterSlices * kCols;
-  for (int i = (int)block * kOuterWarps * 32 + threadIdx.x; i < kOuterSlices * kCols * kRank; i += (int)blocks * kOuterWarps * 32) {
+  for (int i = (int)block * kThreads + threadIdx.x; i < outer_cols(NT) * kRank; i += (int)blocks * kThreads) {
     int r, c;  // of the block's
     if (a.turned) {
       r = i % kRank;
       c = i / kRank;
     } else {
-      c = i % (kOuterSlices * kCols);
-      r = i / (kOuterSlices * kCols);
+      c = i % outer_cols(NT);
+      r = i / outer_cols(NT);
     }
     if (r0 + r >= a.rank || b0 + c >= a.cols) continue;
-    const float *at = outer_smem + (c / kCols * kRank + r) * kCols + c % kCols;
-    float s;
+    const float *at = sums + r * kPitch + c;
+    float s = *at;
     if (blocks > 1) {
       s = ld_cluster(at, 0);
       for (uint32_t b = 1; b < blocks; ++b) s += ld_cluster(at, b);
-    } else {
-      s = *at;
     }
     // an adapter without rows has no gradient, whatever its scale
     const float v = first == end ? 0.f : s * scale;
@@ -741,63 +960,88 @@ int64_t likely_tiles(int64_t n, int32_t adapters) {
   return ceil_div(n, kTile) + std::min<int64_t>(n, adapters) / 2;
 }
 
-// blocks of a cluster so that about two blocks per SM share the work, and each has some of it
+// blocks of a cluster: as many as the SMs have room for at a block each, and each with some of the shares
 unsigned cluster_for(int64_t blocks, int64_t shares, int sms) {
   unsigned c = 1;
-  while (c < kMostCluster && blocks * c < 2 * (int64_t)sms && shares >= 2 * (int64_t)c) c *= 2;
+  while (c < kMostCluster && blocks * 2 * c <= (int64_t)sms && shares >= 2 * (int64_t)c) c *= 2;
   return c;
 }
 
-template <typename T, int NT, bool kAlong>
+template <typename T, int NT, bool kAlong, bool kWide>
 cudaError_t launch_down(const DownArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
-  const size_t smem = (size_t)4 * kTile * 8 * NT * 4;
-  cudaError_t e = raise_smem_limit(k_adapt_down<T, NT, kAlong>, smem);
+  const size_t smem = down_smem(NT);
+  const auto kernel = k_adapt_down<T, NT, kAlong, kWide>;
+  cudaError_t e = raise_smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
   const unsigned slices = (unsigned)ceil_div(a.rank, 8 * NT);
   const unsigned c = cluster_for(likely_tiles(n, a.adapters) * slices, ceil_div(a.k, Op<T>::kGroup * kDownWarps), sms);
-  return launch_cluster(c, k_adapt_down<T, NT, kAlong>, dim3((unsigned)tile_cap * c, slices), kDownWarps * 32, smem, s, a);
+  return launch_cluster(c, kernel, dim3((unsigned)tile_cap * c, slices), kDownWarps * 32, smem, s, a);
+}
+template <typename T, int NT, bool kAlong>
+cudaError_t down_by(const DownArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
+  const size_t es = sizeof(T);
+  const bool wide = row_wide(a.x, a.x_ld, es) && (kAlong ? row_wide(a.m, a.k, es) : ptr_aligned(a.m, NT * es) && a.rank % NT == 0);
+  return wide ? launch_down<T, NT, kAlong, true>(a, n, tile_cap, sms, s) : launch_down<T, NT, kAlong, false>(a, n, tile_cap, sms, s);
 }
 template <typename T, bool kAlong>
 cudaError_t down(const DownArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
   constexpr int kMost = sizeof(T) == 2 ? 8 : 4;
-  if (a.rank <= 8) return launch_down<T, 1, kAlong>(a, n, tile_cap, sms, s);
-  if (a.rank <= 16) return launch_down<T, 2, kAlong>(a, n, tile_cap, sms, s);
-  if (a.rank <= 32 || kMost == 4) return launch_down<T, 4, kAlong>(a, n, tile_cap, sms, s);
-  return launch_down<T, kMost, kAlong>(a, n, tile_cap, sms, s);
+  if (a.rank <= 16) return down_by<T, 2, kAlong>(a, n, tile_cap, sms, s);
+  if (a.rank <= 32 || kMost == 4) return down_by<T, 4, kAlong>(a, n, tile_cap, sms, s);
+  return down_by<T, kMost, kAlong>(a, n, tile_cap, sms, s);
 }
 
-template <typename T, bool kAlong>
-cudaError_t up(UpArgs a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
-  constexpr int kParts = sizeof(T) == 2 ? 2 : 3;
-  const size_t smem = (size_t)kParts * kTile * up_ld(a.rank) * 2;
-  cudaError_t e = raise_smem_limit(k_adapt_up<T, kAlong>, smem);
+template <typename T, bool kAlong, int kSteps, bool kWide>
+cudaError_t launch_up(UpArgs a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
+  const size_t smem = (size_t)kUpWarps * up_stages<T>() * up_stage_bytes<T, kSteps>() * 32 + up_h_bytes(a.rank);
+  const auto kernel = k_adapt_up<T, kAlong, kSteps, kWide>;
+  cudaError_t e = raise_smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
   const int64_t all = ceil_div(a.cols, kUpWarps * kUpCols);
-  // a block that has more columns reads its rows of h for all of them, as long as there are eight blocks per SM
-  int64_t groups = std::max<int64_t>(1, likely_tiles(n, a.adapters) * all / (8 * (int64_t)sms));
-  groups = std::min<int64_t>(groups, 8);
+  // a block that has more columns reads its rows of h for all of them, as long as there are four blocks per SM
+  int64_t groups = std::max<int64_t>(1, likely_tiles(n, a.adapters) * all / (4 * (int64_t)sms));
+  groups = std::min<int64_t>(groups, 16);
   if (ceil_div(all, groups) > 65535) groups = ceil_div(all, 65535);
   a.groups = (int)groups;
-  return launch_pdl(k_adapt_up<T, kAlong>, dim3((unsigned)tile_cap, (unsigned)ceil_div(all, groups)), kUpWarps * 32, smem, s,
-                    (const UpArgs)a);
+  return launch_pdl(kernel, dim3((unsigned)tile_cap, (unsigned)ceil_div(all, groups)), kUpWarps * 32, smem, s, (const UpArgs)a);
+}
+template <typename T, bool kAlong, int kSteps>
+cudaError_t up_by(const UpArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
+  const size_t es = sizeof(T);
+  // whole accesses of 16 bytes of the rows, of four elements of the matrix
+  const bool wide = row_wide(a.base, a.base_ld, es) && row_wide(a.out, a.out_ld, es) && (size_t)a.cols * es % 16 == 0 &&
+                    ptr_aligned(a.m, 4 * es) && (kAlong ? a.rank : a.cols) % 4 == 0;
+  return wide ? launch_up<T, kAlong, kSteps, true>(a, n, tile_cap, sms, s) : launch_up<T, kAlong, kSteps, false>(a, n, tile_cap, sms, s);
+}
+template <typename T, bool kAlong>
+cudaError_t up(const UpArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
+  if (a.rank <= 16 || sizeof(T) == 4) return up_by<T, kAlong, 1>(a, n, tile_cap, sms, s);
+  if constexpr (sizeof(T) == 2) {
+    if (a.rank > 32 && a.rank <= 64) return up_by<T, kAlong, 4>(a, n, tile_cap, sms, s);
+    return up_by<T, kAlong, 2>(a, n, tile_cap, sms, s);
+  }
+  return cudaErrorInvalidValue;
 }
 
-template <typename T, int MT>
+template <typename T, int MT, bool kWide>
 cudaError_t launch_outer(const OuterArgs &a, int64_t n, int32_t adapters, int sms, cudaStream_t s) {
-  constexpr int kCols = 8 * Op<T>::kLane;
-  const size_t smem = (size_t)kOuterSlices * 16 * MT * kCols * 4;
-  cudaError_t e = raise_smem_limit(k_adapt_outer<T, MT>, smem);
+  const size_t smem = outer_smem<T, MT>();
+  const auto kernel = k_adapt_outer<T, MT, kWide>;
+  cudaError_t e = raise_smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
-  const int64_t slices = ceil_div(a.cols, kOuterSlices * kCols), ranks = ceil_div(a.rank, 16 * MT);
-  const unsigned c = cluster_for(slices * ranks * adapters, ceil_div(n, (int64_t)adapters * 32), sms);
-  return launch_cluster(c, k_adapt_outer<T, MT>, dim3((unsigned)(slices * c), (unsigned)adapters, (unsigned)ranks), kOuterWarps * 32,
-                        smem, s, a);
+  const int64_t slices = ceil_div(a.cols, outer_cols(Op<T>::kLane)), ranks = ceil_div(a.rank, 16 * MT);
+  const unsigned c = cluster_for(slices * ranks * adapters, ceil_div(n, (int64_t)adapters * kOuterRows), sms);
+  return launch_cluster(c, kernel, dim3((unsigned)(slices * c), (unsigned)adapters, (unsigned)ranks), kOuterWarps * 32, smem, s, a);
+}
+template <typename T, int MT>
+cudaError_t outer_by(const OuterArgs &a, int64_t n, int32_t adapters, int sms, cudaStream_t s) {
+  return row_wide(a.x, a.x_ld, sizeof(T)) ? launch_outer<T, MT, true>(a, n, adapters, sms, s) : launch_outer<T, MT, false>(a, n, adapters, sms, s);
 }
 template <typename T>
 cudaError_t outer(const OuterArgs &a, int64_t n, int32_t adapters, int sms, cudaStream_t s) {
-  if (a.rank <= 16) return launch_outer<T, 1>(a, n, adapters, sms, s);
-  if (a.rank <= 32) return launch_outer<T, 2>(a, n, adapters, sms, s);
-  return launch_outer<T, 4>(a, n, adapters, sms, s);
+  if (a.rank <= 16) return outer_by<T, 1>(a, n, adapters, sms, s);
+  if (a.rank <= 32) return outer_by<T, 2>(a, n, adapters, sms, s);
+  return outer_by<T, 4>(a, n, adapters, sms, s);
 }
 
 snack_status adapt_check(int64_t n, int32_t adapters, int32_t rank, int32_t in_f, int32_t out_f, snack_dtype t) {
@@ -886,8 +1130,6 @@ snack_status snack_adapt_fwd(const void *x, int64_t x_ld, int64_t n, const void 
   d.tiles = reinterpret_cast<const Tile *>(w + W.tiles);
   d.adapters = n_adapters;
   d.h = h ? h : reinterpret_cast<float *>(w + W.h);
-  d.x_wide = row_wide(x, x_ld, es);
-  d.m_wide = row_wide(a, in_f, es);
   UpArgs u = {};
   u.h = d.h;
   u.m = b;
@@ -901,9 +1143,7 @@ snack_status snack_adapt_fwd(const void *x, int64_t x_ld, int64_t n, const void 
   u.base_ld = base_ld;
   u.out = y;
   u.out_ld = y_ld;
-  u.m_wide = ptr_aligned(b, 4 * es) && rank % 4 == 0;
-  u.base_wide = row_wide(base, base_ld, es);
-  u.out_wide = row_wide(y, y_ld, es);
+  u.h_wide = rank % 4 == 0 && ptr_aligned(d.h, 16);
   ADAPT_CUDA(t == SNACK_F32 ? run_fwd<float>(d, u, n, W, sms, s) : run_fwd<bf16>(d, u, n, W, sms, s));
   return SNACK_OK;
 } catch (...) {  // a host allocation failed
@@ -955,7 +1195,6 @@ snack_status snack_adapt_bwd(const void *x, int64_t x_ld, int64_t n, const void 
   ADAPT_CUDA(launch_group(TokenSrc{which, which_t == SNACK_I64, (uint32_t)n_adapters}, (int)n, w, W, s));
   const int32_t *order = reinterpret_cast<const int32_t *>(w + W.order), *start = reinterpret_cast<const int32_t *>(w + W.start);
   float *dh = reinterpret_cast<float *>(w + W.h);
-  const int ranks = rank <= 8 ? 1 : rank <= 16 ? 2 : rank <= 32 || wide32 ? 4 : 8;  // a lane's of a row of b
   if (dx || da) {
     DownArgs d = {};
     d.x = dy;
@@ -968,8 +1207,6 @@ snack_status snack_adapt_bwd(const void *x, int64_t x_ld, int64_t n, const void 
     d.adapters = n_adapters;
     d.scales = scales;
     d.h = dh;
-    d.x_wide = row_wide(dy, dy_ld, es);
-    d.m_wide = ptr_aligned(b, ranks * es) && rank % ranks == 0;
     ADAPT_CUDA(wide32 ? down<float, false>(d, n, W.tile_cap, sms, s) : down<bf16, false>(d, n, W.tile_cap, sms, s));
   }
   if (dx) {
@@ -985,8 +1222,7 @@ snack_status snack_adapt_bwd(const void *x, int64_t x_ld, int64_t n, const void 
     u.base_ld = dx_ld;
     u.out = dx;
     u.out_ld = dx_ld;
-    u.m_wide = ptr_aligned(a, 4 * es) && in_f % 4 == 0;
-    u.base_wide = u.out_wide = row_wide(dx, dx_ld, es);
+    u.h_wide = rank % 4 == 0;
     ADAPT_CUDA(wide32 ? up<float, false>(u, n, W.tile_cap, sms, s) : up<bf16, false>(u, n, W.tile_cap, sms, s));
   }
   OuterArgs o = {};
@@ -1000,7 +1236,6 @@ snack_status snack_adapt_bwd(const void *x, int64_t x_ld, int64_t n, const void 
     o.x_ld = x_ld;
     o.cols = in_f;
     o.out = da;
-    o.x_wide = row_wide(x, x_ld, es);
     ADAPT_CUDA(wide32 ? outer<float>(o, n, n_adapters, sms, s) : outer<bf16>(o, n, n_adapters, sms, s));
   }
   if (db) {
@@ -1012,7 +1247,6 @@ snack_status snack_adapt_bwd(const void *x, int64_t x_ld, int64_t n, const void 
     o.out = db;
     o.turned = 1;
     o.scales = scales;
-    o.x_wide = row_wide(dy, dy_ld, es);
     ADAPT_CUDA(wide32 ? outer<float>(o, n, n_adapters, sms, s) : outer<bf16>(o, n, n_adapters, sms, s));
   }
   return SNACK_OK;
