@@ -216,6 +216,14 @@ __device__ __forceinline__ void copy_async(void *to, const void *from, int bytes
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(at), "l"(from), "r"(bytes), "n"(kBytes) : "memory");
 }
+template <int kBytes>
+__device__ __forceinline__ void copy_whole(void *to, const void *from) {
+  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(kBytes) : "memory");
+}
 template <typename T, int V, bool kWide>
 __device__ __forceinline__ void fetch_vec(void *to, const T *p, int left) {
   constexpr int kBytes = V * (int)sizeof(T);
@@ -275,43 +283,57 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// acc += a b over 16 of K: rows g (lo) and g + 8 (hi) of a, in parts; the small
-// products first, and those of fp32 operands summed apart from what is there.
-template <int kA, int kB>
-__device__ __forceinline__ void mma_step(float (&acc)[4], const uint32_t (&lo)[2][kA], const uint32_t (&hi)[2][kA],
-                                         const uint32_t (&b)[2][kB]) {
+// acc[i] += a[i] b[i] over 16 of K for kN independent sums: rows g (lo) and g + 8 (hi)
+// of a, in parts; the small products first, and those of fp32 operands summed apart
+// from what is there.  One part after the other for all sums: none waits for its own.
+template <int kN, int kA, int kB, typename FA, typename FB, typename FAcc>
+__device__ __forceinline__ void mma_all(FAcc acc, FA a, FB b) {
+  typedef const uint32_t(&Rows)[2][2][kA];  // [row half][pair of K][part]
+  typedef const uint32_t(&Cols)[2][kB];     // [pair of K][part]
   if constexpr (kA == 3 && kB == 3) {
-    float d[4] = {0.f, 0.f, 0.f, 0.f};
+    float d[kN][4];
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[n][e] = 0.f;
 #pragma unroll
     for (int sum = 2; sum >= 0; --sum)
 #pragma unroll
-      for (int i = sum; i >= 0; --i) mma(d, lo[0][i], hi[0][i], lo[1][i], hi[1][i], b[0][sum - i], b[1][sum - i]);
+      for (int i = sum; i >= 0; --i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] += d[e];
+        for (int n = 0; n < kN; ++n) {
+          Rows w = a(n);
+          Cols v = b(n);
+          mma(d[n], w[0][0][i], w[1][0][i], w[0][1][i], w[1][1][i], v[0][sum - i], v[1][sum - i]);
+        }
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc(n)[e] += d[n][e];
   } else {
     static_assert(kB == 1, "one part");
 #pragma unroll
-    for (int i = kA - 1; i >= 0; --i) mma(acc, lo[0][i], hi[0][i], lo[1][i], hi[1][i], b[0][0], b[1][0]);
+    for (int i = kA - 1; i >= 0; --i)
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        Rows w = a(n);
+        Cols v = b(n);
+        mma(acc(n), w[0][0][i], w[1][0][i], w[0][1][i], w[1][1][i], v[0][0], v[1][0]);
+      }
   }
 }
 
-// a lane's words of a row along K: [step][half of the step's pairs][part]
-template <typename T, int V>
-struct Along {
-  static constexpr int kSteps = V / 4;
-  uint32_t w[kSteps][2][Op<T>::kParts];
-  __device__ __forceinline__ void set(const Pack<T, V * (int)sizeof(T)> &v) {
+// a lane's words of four consecutive elements of a row along K: [pair][part]
+template <typename T, int B>
+__device__ __forceinline__ void along(const Pack<T, B> &v, int s, uint32_t (&w)[2][Op<T>::kParts]) {
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if constexpr (sizeof(T) == 2)
-          w[s][h][0] = v.w[2 * s + h];
-        else
-          cut_pair<3>(v.get(4 * s + 2 * h), v.get(4 * s + 2 * h + 1), w[s][h]);
-      }
+  for (int h = 0; h < 2; ++h) {
+    if constexpr (sizeof(T) == 2)
+      w[h][0] = v.w[2 * s + h];
+    else
+      cut_pair<3>(v.get(4 * s + 2 * h), v.get(4 * s + 2 * h + 1), w[h]);
   }
-};
+}
 // the pair of elements j of two rows that follow one another along K
 template <typename T, int B>
 __device__ __forceinline__ void across(const Pack<T, B> &a, const Pack<T, B> &b, int j, uint32_t (&w)[Op<T>::kParts]) {
@@ -368,8 +390,9 @@ __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, f
   const T *mat = reinterpret_cast<const T *>(a.m) + (int64_t)tile.adapter * a.rank * a.k;
   // this lane's ring: kStages x (its 16 bytes of every 8th row; of the matrix NT of them, or the same bytes in smaller pieces)
   uint4 *ring = reinterpret_cast<uint4 *>(smem) + (warp * kStages * kSlots) * 32 + lane;
-  const int step = (int)blocks * kDownWarps * O::kGroup;
-  int next = (int)(rank * kDownWarps + warp) * O::kGroup;
+  // two neighbouring groups, a line of the rows, then the two so many further on
+  const int step = (int)blocks * kDownWarps * 2 * O::kGroup;
+  int next = (int)(rank * kDownWarps + warp) * 2 * O::kGroup, odd = 0;
   auto fetch = [&](int stage) {
     if (next < a.k) {
       uint4 *to = ring + stage * kSlots * 32;
@@ -392,51 +415,52 @@ __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, f
       }
     }
     fetch_commit();
-    next += step;
+    next += odd ? step - O::kGroup : O::kGroup;
+    odd ^= 1;
   };
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) fetch(s);
-  int stage = 0;
-  for (int k0 = next - (kStages - 1) * step; k0 < a.k; k0 += step) {
+  int stage = 0, odd_now = 0;
+  for (int k0 = (int)(rank * kDownWarps + warp) * 2 * O::kGroup; k0 < a.k; k0 += odd_now ? step - O::kGroup : O::kGroup, odd_now ^= 1) {
     fetch(stage == 0 ? kStages - 1 : stage - 1);
     fetch_wait<kStages - 1>();
     const uint4 *from = ring + stage * kSlots * 32;
-    Along<T, O::kLane> xa[2 * MT];
+    uint32_t xa[O::kSteps][MT][2][2][O::kParts];
 #pragma unroll
     for (int i = 0; i < 2 * MT; ++i) {
       Pack<T, 16> v;
       v.raw = from[i * 32];
-      xa[i].set(v);
+#pragma unroll
+      for (int s = 0; s < O::kSteps; ++s) along<T>(v, s, xa[s][i >> 1][i & 1]);
     }
     from += kTile / 8 * 32;
+    const typename Cross::R *piece = reinterpret_cast<const typename Cross::R *>(from - lane) + lane;
+    uint32_t bw[O::kSteps][NT][2][O::kParts];
     if constexpr (kAlong) {
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         Pack<T, 16> v;
         v.raw = from[j * 32];
-        Along<T, O::kLane> b;
-        b.set(v);
 #pragma unroll
-        for (int s = 0; s < O::kSteps; ++s)
-#pragma unroll
-          for (int m = 0; m < MT; ++m) mma_step(acc[m][j], xa[2 * m].w[s], xa[2 * m + 1].w[s], b.w[s]);
+        for (int s = 0; s < O::kSteps; ++s) along<T>(v, s, bw[s][j]);
       }
-    } else {
-      const typename Cross::R *piece = reinterpret_cast<const typename Cross::R *>(from - lane) + lane;
+    }
 #pragma unroll
-      for (int s = 0; s < O::kSteps; ++s) {
+    for (int s = 0; s < O::kSteps; ++s) {
+      if constexpr (!kAlong) {
         Cross v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i].raw = piece[(4 * s + i) * 32];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          uint32_t b[2][O::kParts];
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) across<T>(v[2 * h], v[2 * h + 1], j, b[h]);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) mma_step(acc[m][j], xa[2 * m].w[s], xa[2 * m + 1].w[s], b);
-        }
+          for (int h = 0; h < 2; ++h) across<T>(v[2 * h], v[2 * h + 1], j, bw[s][j][h]);
       }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        mma_all<MT, O::kParts, O::kParts>([&](int m) -> float(&)[4] { return acc[m][j]; },
+                                          [&](int m) -> const uint32_t(&)[2][2][O::kParts] { return xa[s][m]; },
+                                          [&](int) -> const uint32_t(&)[2][O::kParts] { return bw[s][j]; });
     }
     if (++stage == kStages) stage = 0;
   }
@@ -511,11 +535,15 @@ struct UpArgs {
 constexpr int kUpWarps = 8;
 constexpr int kUpCols = 32;  // columns of a warp at a time
 
-// Of a row of h in shared memory, in elements: rows start 32 bytes apart modulo 128 as
+// Of a row of h in shared memory, in elements: rows start 16 bytes apart modulo 128 as
 // bf16 (its two parts), 64 as fp32 (which is cut into parts as it is read); the
-// highest ranks have no room for that.
-__host__ __device__ constexpr int up_ld(int rank) { return rank > 240 ? kMostRank + 4 : (rank + 63) / 64 * 64 + 16; }
-constexpr size_t up_h_bytes(int rank) { return (size_t)kTile * up_ld(rank) * 4; }
+// highest ranks of fp32 have no room for that.
+template <typename T>
+__host__ __device__ constexpr int up_ld(int rank) {
+  return sizeof(T) == 2 ? (rank + 63) / 64 * 64 + 8 : rank > 240 ? kMostRank + 8 : (rank + 63) / 64 * 64 + 16;
+}
+template <typename T>
+constexpr size_t up_h_bytes(int rank) { return (size_t)kTile * up_ld<T>(rank) * 4; }
 // shared memory of a lane: its 16-byte pieces of the base, and its pieces of the matrix (8 bytes of bf16, 16 of fp32)
 template <typename T>
 __host__ __device__ constexpr int up_base_bytes() { return kTile / 8 * 8 * (int)sizeof(T); }
@@ -524,40 +552,42 @@ __host__ __device__ constexpr int up_stage_bytes() { return up_base_bytes<T>() +
 template <typename T>
 __host__ __device__ constexpr int up_stages() { return sizeof(T) == 2 ? 3 : 2; }
 
-static_assert(kUpWarps * up_stages<bf16>() * up_stage_bytes<bf16, 4>() * 32 + up_h_bytes(64) <= 232448 &&
-                  kUpWarps * up_stages<bf16>() * up_stage_bytes<bf16, 2>() * 32 + up_h_bytes(kMostRank) <= 232448 &&
-                  kUpWarps * up_stages<float>() * up_stage_bytes<float, 1>() * 32 + up_h_bytes(kMostRank) <= 232448,
+static_assert(kUpWarps * up_stages<bf16>() * up_stage_bytes<bf16, 4>() * 32 + up_h_bytes<bf16>(64) <= 232448 &&
+                  kUpWarps * up_stages<bf16>() * up_stage_bytes<bf16, 2>() * 32 + up_h_bytes<bf16>(kMostRank) <= 232448 &&
+                  kUpWarps * up_stages<float>() * up_stage_bytes<float, 1>() * 32 + up_h_bytes<float>(kMostRank) <= 232448,
               "shared memory of one block");
 
 // A warp takes 32 columns of the tile after 32 others; what it reads of the base and
 // the matrix is on its way one or two turns before, kSteps of 16 of the rank per turn.
 // The sums begin with the base, so the result is rounded as it leaves; h has its
 // scale before it is cut into parts.
-template <typename T, bool kAlong, int kSteps, bool kWide>
-__global__ void __launch_bounds__(kUpWarps * 32, 1) k_adapt_up(const UpArgs a) {
-  pdl_wait();
+//
+// kWhole: 64 rows, whole groups of columns and steps of the rank: nothing to check.
+template <typename T, bool kAlong, int kSteps, bool kWide, bool kWhole>
+__device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, uint8_t *up_ring) {
   constexpr int kHp = Op<T>::kOwnParts, kBp = Op<T>::kParts, MT = kTile / 16, NT = 4, kStages = up_stages<T>();
   typedef Pack<T, 16> P;
   typedef Pack<T, 4 * (int)sizeof(T)> P4;
   constexpr int kPer = P::kN, kVecs = 8 / kPer;  // accesses for a lane's 8 columns
   constexpr int kStage = up_stage_bytes<T, kSteps>() * 32;
-  extern __shared__ __align__(16) uint8_t up_ring[];
-  const Tile tile = a.tiles[blockIdx.x];
-  if (tile.adapter < 0) return;
-  const bool none = tile.adapter >= a.adapters;
-  if (none && a.base == a.out) return;
+  const bool none = !kWhole && tile.adapter >= a.adapters;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, q = lane & 3;
-  const int ld = up_ld(a.rank) / 2, plane = kTile * ld;  // in words
-  const int steps = none ? 1 : (a.rank + 15) / 16, turns = (steps + kSteps - 1) / kSteps;
-  const int m_tiles = (tile.count + 15) / 16;
+  const int ld = up_ld<T>(a.rank) / 2, plane = kTile * ld;  // in words
+  const int steps = none ? 1 : (a.rank + 15) / 16, turns = kWhole && kSteps == 4 ? 1 : (steps + kSteps - 1) / kSteps;
+  const int m_tiles = kWhole ? MT : (tile.count + 15) / 16;
   uint8_t *ring = up_ring + warp * kStages * kStage;
   uint32_t *hs = reinterpret_cast<uint32_t *>(up_ring + kUpWarps * kStages * kStage);
   const T *mat = reinterpret_cast<const T *>(a.m) + (none ? 0 : (int64_t)tile.adapter * a.rank * a.cols);
-  int32_t token[2 * MT];
-#pragma unroll
-  for (int i = 0; i < 2 * MT; ++i) token[i] = 8 * i + g < tile.count ? __ldg(a.order + tile.first + 8 * i + g) : -1;
   const int col0 = (blockIdx.y * a.groups * kUpWarps + warp) * kUpCols;
+  // this lane's rows, from its 8 columns on
+  int32_t token[2 * MT];
+  const T *base[2 * MT];
+#pragma unroll
+  for (int i = 0; i < 2 * MT; ++i) {
+    token[i] = kWhole || 8 * i + g < tile.count ? __ldg(a.order + tile.first + 8 * i + g) : -1;
+    base[i] = reinterpret_cast<const T *>(a.base) + (int64_t)max(token[i], 0) * a.base_ld + col0 + 8 * q;
+  }
   const int items = (a.cols <= col0 ? 0 : min(a.groups, (a.cols - col0 + kUpWarps * kUpCols - 1) / (kUpWarps * kUpCols))) * turns;
   int next_col = col0, next_turn = 0, next_stage = 0, next_item = 0;
   auto fetch = [&] {
@@ -569,25 +599,37 @@ __global__ void __launch_bounds__(kUpWarps * 32, 1) k_adapt_up(const UpArgs a) {
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i) {
           if (i >= 2 * m_tiles) break;
-          const T *from = reinterpret_cast<const T *>(a.base) + max(token[i], 0) * a.base_ld + next_col + 8 * q;
+          const T *from = base[i] + (next_col - col0);
 #pragma unroll
-          for (int v = 0; v < kVecs; ++v) fetch_vec<T, kPer, kWide>(at + (i * kVecs + v) * 32, from + v * kPer, left - v * kPer);
+          for (int v = 0; v < kVecs; ++v) {
+            if constexpr (kWhole)
+              copy_whole<16>(at + (i * kVecs + v) * 32, from + v * kPer);
+            else
+              fetch_vec<T, kPer, kWide>(at + (i * kVecs + v) * 32, from + v * kPer, left - v * kPer);
+          }
         }
       }
       if (!none) {
         typename P4::R *at = reinterpret_cast<typename P4::R *>(to + up_base_bytes<T>() * 32) + lane;
+        const int r0 = 16 * next_turn * kSteps + 4 * q;
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int s = 0; s < kSteps; ++s) {
             if constexpr (kAlong) {  // lane g has column 8 (g / 2) + 2 j + g % 2: a lane's sums are 8 neighbours
-              const int col = next_col + 8 * (g >> 1) + 2 * j + (g & 1), r = 16 * (next_turn * kSteps + s) + 4 * q;
-              fetch_vec<T, 4, kWide>(at + (4 * s + j) * 32, mat + (int64_t)min(col, a.cols - 1) * a.rank + (r < a.rank ? r : 0),
-                                     col < a.cols ? a.rank - r : 0);
+              const int col = next_col + 8 * (g >> 1) + 2 * j + (g & 1), r = r0 + 16 * s;
+              if constexpr (kWhole)
+                copy_whole<4 * (int)sizeof(T)>(at + (4 * s + j) * 32, mat + (int64_t)col * a.rank + r);
+              else
+                fetch_vec<T, 4, kWide>(at + (4 * s + j) * 32, mat + (int64_t)min(col, a.cols - 1) * a.rank + (r < a.rank ? r : 0),
+                                       col < a.cols ? a.rank - r : 0);
             } else {  // columns 4 g .. 4 g + 3
-              const int r = 16 * (next_turn * kSteps + s) + 4 * q + j;
-              fetch_vec<T, 4, kWide>(at + (4 * s + j) * 32, mat + (int64_t)min(r, a.rank - 1) * a.cols + (next_col + 4 * g < a.cols ? next_col + 4 * g : 0),
-                                     r < a.rank ? a.cols - next_col - 4 * g : 0);
+              const int r = r0 + 16 * s + j, col = next_col + 4 * g;
+              if constexpr (kWhole)
+                copy_whole<4 * (int)sizeof(T)>(at + (4 * s + j) * 32, mat + (int64_t)r * a.cols + col);
+              else
+                fetch_vec<T, 4, kWide>(at + (4 * s + j) * 32, mat + (int64_t)min(r, a.rank - 1) * a.cols + (col < a.cols ? col : 0),
+                                       r < a.rank ? a.cols - col : 0);
             }
           }
       }
@@ -610,18 +652,22 @@ __global__ void __launch_bounds__(kUpWarps * 32, 1) k_adapt_up(const UpArgs a) {
       const bool in = t < tile.count;
       const auto v = load_vec<float, 4>(a.h + (int64_t)(in ? __ldg(a.order + tile.first + t) : 0) * a.rank + r, in ? a.rank - r : 0, a.h_wide);
       if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4 *>(hs + t * up_ld(a.rank) + r) =
+        *reinterpret_cast<float4 *>(hs + t * up_ld<T>(a.rank) + r) =
             make_float4(scale * v.get(0), scale * v.get(1), scale * v.get(2), scale * v.get(3));
-      } else {
+      } else {  // the pairs of a step of 16: the lanes' first ones, then their second ones, as ldmatrix hands them out
         uint32_t w[2][kHp];
 #pragma unroll
         for (int h = 0; h < 2; ++h) cut_pair<kHp>(scale * v.get(2 * h), scale * v.get(2 * h + 1), w[h]);
 #pragma unroll
-        for (int p = 0; p < kHp; ++p) *reinterpret_cast<uint2 *>(hs + p * plane + t * ld + (r >> 1)) = make_uint2(w[0][p], w[1][p]);
+        for (int p = 0; p < kHp; ++p)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) hs[p * plane + t * ld + (r >> 4) * 8 + 4 * h + ((r >> 2) & 3)] = w[h][p];
       }
     }
   }
   __syncthreads();
+  // ldmatrix: lanes 0 to 15 name rows 0 to 15 of their first pairs, lanes 16 to 31 of the second
+  const uint32_t h_at = static_cast<uint32_t>(__cvta_generic_to_shared(hs)) + (uint32_t)((lane & 15) * ld * 4 + (lane >> 4) * 16);
   float acc[MT][NT][4];
   // a lane's 8 columns: which sum has column e of row half h
   auto sum_at = [&](int m, int h, int e) -> float & { return kAlong ? acc[m][e >> 1][2 * h + (e & 1)] : acc[m][e & 3][2 * h + (e >> 2)]; };
@@ -649,7 +695,7 @@ __global__ void __launch_bounds__(kUpWarps * 32, 1) k_adapt_up(const UpArgs a) {
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         const int k = turn * kSteps + s;
-        if (k >= steps) break;
+        if (!kWhole && k >= steps) break;
         P4 mv[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) mv[j].raw = at[(4 * s + j) * 32];
@@ -657,12 +703,7 @@ __global__ void __launch_bounds__(kUpWarps * 32, 1) k_adapt_up(const UpArgs a) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           if constexpr (kAlong) {
-            Along<T, 4> w;
-            w.set(mv[j]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int p = 0; p < kBp; ++p) b[j][h][p] = w.w[0][h][p];
+            along<T>(mv[j], 0, b[j]);
           } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) across<T>(mv[2 * h], mv[2 * h + 1], j, b[j][h]);
@@ -672,24 +713,24 @@ __global__ void __launch_bounds__(kUpWarps * 32, 1) k_adapt_up(const UpArgs a) {
         for (int m = 0; m < MT; ++m) {
           if (m >= m_tiles) break;
           uint32_t w[2][2][kHp];  // rows g and g + 8
+          if constexpr (sizeof(T) == 4) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int t = 16 * m + 8 * h + g;
-            if constexpr (sizeof(T) == 4) {
-              const float4 v = *reinterpret_cast<const float4 *>(hs + t * up_ld(a.rank) + 16 * k + 4 * q);
+            for (int h = 0; h < 2; ++h) {
+              const float4 v = *reinterpret_cast<const float4 *>(hs + (16 * m + 8 * h + g) * up_ld<T>(a.rank) + 16 * k + 4 * q);
               cut_pair<kHp>(v.x, v.y, w[h][0]);
               cut_pair<kHp>(v.z, v.w, w[h][1]);
-            } else {
-#pragma unroll
-              for (int p = 0; p < kHp; ++p) {
-                const uint2 v = *reinterpret_cast<const uint2 *>(hs + p * plane + t * ld + 8 * k + 2 * q);
-                w[h][0][p] = v.x;
-                w[h][1][p] = v.y;
-              }
             }
-          }
+          } else {
 #pragma unroll
-          for (int j = 0; j < NT; ++j) mma_step(acc[m][j], w[0], w[1], b[j]);
+            for (int p = 0; p < kHp; ++p)
+              asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(w[0][0][p]), "=r"(w[1][0][p]), "=r"(w[0][1][p]), "=r"(w[1][1][p])
+                           : "r"(h_at + (uint32_t)(p * plane + 16 * m * ld + 8 * k) * 4)
+                           : "memory");
+          }
+          mma_all<NT, kHp, kBp>([&](int j) -> float(&)[4] { return acc[m][j]; },
+                                [&](int) -> const uint32_t(&)[2][2][kHp] { return w; },
+                                [&](int j) -> const uint32_t(&)[2][kBp] { return b[j]; });
         }
       }
     }
@@ -700,7 +741,7 @@ __global__ void __launch_bounds__(kUpWarps * 32, 1) k_adapt_up(const UpArgs a) {
 #pragma unroll
     for (int i = 0; i < 2 * MT; ++i) {
       if (i >= 2 * m_tiles) break;
-      if (token[i] < 0 || left <= 0) continue;
+      if (!kWhole && (token[i] < 0 || left <= 0)) continue;
       T *out = reinterpret_cast<T *>(a.out) + token[i] * a.out_ld + c;
 #pragma unroll
       for (int v = 0; v < kVecs; ++v) {
@@ -713,7 +754,7 @@ __global__ void __launch_bounds__(kUpWarps * 32, 1) k_adapt_up(const UpArgs a) {
           for (int e = 0; e < kPer; ++e) o.set(e, sum_at(i >> 1, i & 1, v * kPer + e));
         }
         if constexpr (kWide) {  // all of it or nothing: whole accesses make up a row
-          if (left >= (v + 1) * kPer) *reinterpret_cast<uint4 *>(out + v * kPer) = o.raw;
+          if (kWhole || left >= (v + 1) * kPer) *reinterpret_cast<uint4 *>(out + v * kPer) = o.raw;
         } else {
 #pragma unroll
           for (int e = 0; e < kPer; ++e)
@@ -728,6 +769,23 @@ __global__ void __launch_bounds__(kUpWarps * 32, 1) k_adapt_up(const UpArgs a) {
     }
     c += kUpWarps * kUpCols;
   }
+}
+
+template <typename T, bool kAlong, int kSteps, bool kWide>
+__global__ void __launch_bounds__(kUpWarps * 32, 1) k_adapt_up(const UpArgs a) {
+  pdl_wait();
+  extern __shared__ __align__(16) uint8_t up_ring[];
+  const Tile tile = a.tiles[blockIdx.x];
+  if (tile.adapter < 0) return;
+  const bool none = tile.adapter >= a.adapters;
+  if (none && a.base == a.out) return;
+  if constexpr (kWide) {
+    if (!none && tile.count == kTile && a.cols % kUpCols == 0 && a.rank % (16 * kSteps) == 0) {
+      up_tile<T, kAlong, kSteps, true, true>(a, tile, up_ring);
+      return;
+    }
+  }
+  up_tile<T, kAlong, kSteps, kWide, false>(a, tile, up_ring);
 }
 
 // ------------------------------------------------------------ dA and dB
@@ -819,7 +877,8 @@ __global__ void __launch_bounds__(kOuterWarps * 32, 1) k_adapt_outer(const Outer
     for (int o = 0; o < kOwn; ++o) {
       const int job = threadIdx.x + o * kThreads;
       if (kJobs % kThreads != 0 && job >= kJobs) break;
-      // row 16 s + 4 q' + 2 k of the pair; rank 16 m + 8 h + g'
+      // row 16 s + 4 q' + 2 k of the pair; rank 16 m + 8 h + g'; the lanes' places turned so that a warp's words
+      // fall on all banks
       const int row = job / kQuads * 2, s = row >> 4, qq = (row >> 2) & 3, k = (row >> 1) & 1;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -827,7 +886,7 @@ __global__ void __launch_bounds__(kOuterWarps * 32, 1) k_adapt_outer(const Outer
         uint32_t w[kVp];
         cut_pair<kVp>(held[o][0].get(e), held[o][1].get(e), w);
 #pragma unroll
-        for (int p = 0; p < kVp; ++p) to[(((s * kVp + p) * MT + m) * 32 + gg * 4 + qq) * 4 + 2 * k + h] = w[p];
+        for (int p = 0; p < kVp; ++p) to[(((s * kVp + p) * MT + m) * 32 + ((gg * 4 + qq) ^ (m | (gg & 4)))) * 4 + 2 * k + h] = w[p];
       }
     }
   };
@@ -852,7 +911,6 @@ __global__ void __launch_bounds__(kOuterWarps * 32, 1) k_adapt_outer(const Outer
       ahead[kOuterStages - 1] = tokens_at(p0 + (kOuterStages + 1) * step);
       __syncthreads();  // one per turn: a buffer is written again after the other one's
       fetch_wait<kOuterStages - 1>();
-      const uint4 *frag = reinterpret_cast<const uint4 *>(vs + turn * kVWords) + lane;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         Pack<T, 16> xv[4];
@@ -863,7 +921,7 @@ __global__ void __launch_bounds__(kOuterWarps * 32, 1) k_adapt_outer(const Outer
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int p = 0; p < kVp; ++p) {
-            const uint4 f = frag[((s * kVp + p) * MT + m) * 32];
+            const uint4 f = reinterpret_cast<const uint4 *>(vs + turn * kVWords)[((s * kVp + p) * MT + m) * 32 + (lane ^ (m | (g & 4)))];
             w[m][0][0][p] = f.x;
             w[m][1][0][p] = f.y;
             w[m][0][1][p] = f.z;
@@ -874,8 +932,9 @@ __global__ void __launch_bounds__(kOuterWarps * 32, 1) k_adapt_outer(const Outer
           uint32_t b[2][O::kParts];
 #pragma unroll
           for (int k = 0; k < 2; ++k) across<T>(xv[2 * k], xv[2 * k + 1], j, b[k]);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) mma_step(acc[m][j], w[m][0], w[m][1], b);
+          mma_all<MT, kVp, O::kParts>([&](int m) -> float(&)[4] { return acc[m][j]; },
+                                      [&](int m) -> const uint32_t(&)[2][2][kVp] { return w[m]; },
+                                      [&](int) -> const uint32_t(&)[2][O::kParts] { return b; });
         }
       }
       if (++stage == kOuterStages) stage = 0;
@@ -993,7 +1052,7 @@ cudaError_t down(const DownArgs &a, int64_t n, int tile_cap, int sms, cudaStream
 
 template <typename T, bool kAlong, int kSteps, bool kWide>
 cudaError_t launch_up(UpArgs a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
-  const size_t smem = (size_t)kUpWarps * up_stages<T>() * up_stage_bytes<T, kSteps>() * 32 + up_h_bytes(a.rank);
+  const size_t smem = (size_t)kUpWarps * up_stages<T>() * up_stage_bytes<T, kSteps>() * 32 + up_h_bytes<T>(a.rank);
   const auto kernel = k_adapt_up<T, kAlong, kSteps, kWide>;
   cudaError_t e = raise_smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
