@@ -438,6 +438,48 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
                             void *dw, int64_t dw_ld, void *ws, size_t ws_bytes, snack_stream_t stream);
 
 /*
+ * Log probabilities of given tokens under the same projection, the entropies of its
+ * distributions, and their likeliest tokens, without the logits:
+ *   logp[i]    = z[i, targets[i]] - lse[i]
+ *   entropy[i] = -sum_v p[i, v] log p[i, v],    p = exp(z - lse)
+ *   top_ids[i, 0 .. top) the ids with the largest logits in their order, of equal ones
+ *   the lower id first, and top_logp their log probabilities
+ * x, w, t and targets are as for snack_xent_fwd.  A target outside [0, vocab) marks a
+ * row that is not scored: its results are 0, and its ids -1, whatever its row of x
+ * holds.  targets may be NULL: then every row is scored, and logp has to be NULL.
+ * logp, entropy (n values each), and top_ids and top_logp (n * top) where top is 0,
+ * may be NULL.  0 <= top <= 24 (SNACK_ERR_UNSUPPORTED above) and top <= vocab.  Logits
+ * are formed as the loss's are; where neighbours in the order of the likeliest tokens
+ * are too close for that, their products are summed again in about twice fp32's
+ * precision (so the order is that of the exact logits unless more than eight beyond the
+ * last one asked for are that close to it).  A row with a NaN or an infinite largest
+ * logit has NaN results; its ids are some of the vocabulary.  state (2 n values: each
+ * row's lse and entropy) is kept for the gradient.  With top the workspace holds up to
+ * 256 MB of logits at a time (1024 columns at least); the other sizes are as for
+ * snack_xent_workspace_size.
+ */
+snack_status snack_score_workspace_size(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld,
+                                        int64_t vocab, int32_t width, snack_dtype t, int32_t top, int grad, size_t *bytes);
+snack_status snack_score_fwd(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld, int64_t vocab,
+                             int32_t width, snack_dtype t, const void *targets, snack_index targets_t, float *logp,
+                             float *entropy, int32_t top, int64_t *top_ids, float *top_logp, float *state, void *ws,
+                             size_t ws_bytes, snack_stream_t stream);
+
+/*
+ * Their gradients for upstream gradients dlogp and dentropy (n values each, or NULL: 0),
+ * from the state that snack_score_fwd left:
+ *   dz[i, v] = dlogp[i] [v == targets[i]] - p (dlogp[i] + dentropy[i] (log p + entropy[i]))
+ *   dx = dz w   [n, width],     dw = dz^T x   [vocab, width]      in type t
+ * dx or dw may be NULL; targets may be NULL where dlogp is.  A row that is not scored,
+ * or whose two gradients are 0, adds nothing, whatever it holds.  dz is rounded as
+ * snack_xent_bwd's is.  The workspace is snack_score_workspace_size's with grad != 0.
+ */
+snack_status snack_score_bwd(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld, int64_t vocab,
+                             int32_t width, snack_dtype t, const void *targets, snack_index targets_t, const float *state,
+                             const float *dlogp, const float *dentropy, void *dx, int64_t dx_ld, void *dw, int64_t dw_ld,
+                             void *ws, size_t ws_bytes, snack_stream_t stream);
+
+/*
  * Global norm of a model's gradients, and clipping:
  *   norm   = sqrt(sum over all tensors and elements of g^2)
  *   out[k] = g[k] * min(1, max_norm / (norm + 1e-6))

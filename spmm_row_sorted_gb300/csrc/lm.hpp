@@ -56,6 +56,19 @@ struct TokenSrc {
   __device__ __forceinline__ uint32_t val(int64_t i) const { return (uint32_t)i; }
 };
 
+// The entropies of the rows' distributions in a gradient: a weight per row (null: none)
+// and the entropy itself.
+struct Entropy {
+  const float *weight, *value;
+};
+// exp(d) below this is 0, and d times it as well, also where d is infinite
+constexpr float kFarBelow = -200.f;
+// what exp(d) is multiplied by in dz, where d is a log probability: g of the loss, and
+// of the entropy H, dH/dz = -p (d + H), with the weight's sign turned
+__device__ __forceinline__ float entropy_slope(float g, float weight, float d, float entropy) {
+  return fmaf(weight, fmaxf(d, kFarBelow) + entropy, g);
+}
+
 // B bytes of consecutive elements of T: one load or store of that width.
 template <int B>
 struct Raw;

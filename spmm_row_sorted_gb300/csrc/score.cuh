@@ -1,0 +1,570 @@
+// Log probabilities of given tokens under a projection to a vocabulary, the entropies
+// of its distributions and their likeliest tokens; and the gradients of the first two.
+//
+//   z[i, v] = sum_d x[i, d] w[v, d],   M = max_v z,   S = sum_v e^(z - M)
+//   logp[i] = (z[i, t_i] - M) - log S
+//   H[i]    = log S - (sum_v e^(z - M) (z - M)) / S
+//   dz[i, v] = g_i [v = t_i] - p (g_i + h_i (log p + H_i))
+//
+// The logits are the loss's (xent.cu; of a few fp32 tokens xent_small.cuh and
+// xent_cut.cuh), with statistics of half a tile (of 32 logits there): the maximum, how
+// often it occurs, and of the others the sums of e^(z - M) and of e^(z - M) (z - M), so
+// that a confident row's log S and H, which are far below 1, keep their digits.  The
+// target is left out of them and joins at the end with its logit in fp32.
+//
+// Likeliest tokens.  The `keep` largest logits lie in the `keep` groups of 32 logits
+// with the largest maxima (of equal ones the first): each of those has a logit that
+// comes before any of another group.  So the product writes the maxima, and the logits
+// themselves for a piece of the vocabulary; a block per row then reads V / 32 maxima and
+// `keep` lines of logits, whatever the data.  Eight more than asked for are kept: where
+// neighbours in the order are within 2^-12 of the largest magnitude, some hundred times
+// what the logits are off by, they are ranked by their products summed again in twice
+// fp32's precision.  Equal logits rank by their ids.  Included by xent.cu.
+#pragma once
+
+namespace snack {
+namespace {
+
+constexpr int kMostTop = 24;
+constexpr int kKeepMore = 8;
+constexpr int kFinishWarps = 4;
+constexpr int kNoId = 0x7FFFFFFF;
+
+// ------------------------------------------------------------ statistics
+
+// (maximum, how often, rest, slope) of two sets of logits
+__device__ __forceinline__ float4 join_stats(float4 a, float4 b) {
+  if (b.x > a.x) {
+    const float4 t = a;
+    a = b;
+    b = t;
+  }
+  if (b.x == a.x) {
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
+  } else if (b.x == -INFINITY) {
+    a.z += b.z;  // 0, or a NaN to keep
+  } else {
+    const float d = b.x - a.x, f = expf(d), all = b.y + b.z;
+    a.z = fmaf(f, all, a.z);
+    a.w = fmaf(f, fmaf(all, fmaxf(d, kFarBelow), b.w), a.w);
+  }
+  return a;
+}
+
+// Statistics and maxima of the logits of a few tokens, [vocab][tokens]: a thread for
+// each group of 32 and token.
+__global__ void __launch_bounds__(256) k_score_stats(const float *__restrict__ z, int32_t tokens, int32_t n, int64_t vocab,
+                                                     int32_t groups, TokenSrc targets, float4 *__restrict__ stats,
+                                                     float *__restrict__ high, float *__restrict__ zt) {
+  pdl_wait();
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int t = (int)(i % tokens);
+  const int64_t group = i / tokens;
+  if (group >= groups || t >= n) return;
+  const uint32_t id = targets.ids ? targets.key(t) : (uint32_t)vocab;
+  const int64_t v0 = group * 32;
+  const int own = (int64_t)id >= v0 && (int64_t)id < v0 + 32 && id < (uint32_t)vocab ? (int)(id - v0) : -1;
+  float v[32], top = -INFINITY, mx = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = v0 + j < vocab ? __ldg(z + (v0 + j) * tokens + t) : -INFINITY;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    top = fmaxf(top, v[j]);
+    if (j == own) {  // joined later
+      zt[t] = v[j];
+      v[j] = -INFINITY;
+    }
+    mx = fmaxf(mx, v[j]);
+  }
+  const float base = mx == -INFINITY ? 0.f : mx;
+  float often = 0.f, rest = 0.f, slope = 0.f;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const float d = v[j] - base, e = expf(d);
+    if (d == 0.f && mx != -INFINITY)
+      often += 1.f;
+    else
+      rest += e;
+    slope = fmaf(e, fmaxf(d, kFarBelow), slope);
+  }
+  stats[(size_t)t * groups + group] = make_float4(mx, often, rest, slope);
+  if (high) high[(size_t)t * groups + group] = top;
+}
+
+// ------------------------------------------------------------ likeliest tokens
+
+struct FinishArgs {
+  int32_t n;
+  TokenSrc targets;  // ids null: none given
+  // likeliest tokens: the piece's maxima and logits
+  int32_t top, keep, groups, rows, v0;
+  const float *high, *z;
+  int64_t high_ld, z_row, z_col;  // steps of a logit's row and column
+  float2 *list;                   // [n][32] what is kept from piece to piece: logit, id
+  int first, last;
+  TargetLogit at;                 // x and w
+  // statistics
+  const float4 *stats;
+  int64_t stats_ld;
+  int32_t slots;
+  const float *zt;                // the targets' logits (else formed here)
+  // results
+  float *logp, *entropy, *top_logp, *lse, *kept_entropy;
+  int64_t *top_ids;
+  const uint32_t *err;
+};
+
+// a before b: larger, of equal ones with the lower id
+__device__ __forceinline__ bool precedes(float a, int ia, float b, int ib) { return a > b || (a == b && ia < ib); }
+
+// A warp's list, sorted: lane l has the l-th.
+struct Best {
+  float v;
+  int id;
+  __device__ __forceinline__ void clear() {
+    v = -INFINITY;
+    id = kNoId;
+  }
+  __device__ __forceinline__ void insert(float nv, int nid, int lane) {
+    const int at = __popc(__ballot_sync(0xffffffffu, precedes(v, id, nv, nid)));
+    const float uv = __shfl_up_sync(0xffffffffu, v, 1);
+    const int uid = __shfl_up_sync(0xffffffffu, id, 1);
+    if (lane == at) {
+      v = nv;
+      id = nid;
+    } else if (lane > at) {
+      v = uv;
+      id = uid;
+    }
+  }
+  // what each lane has to offer (id kNoId: nothing)
+  __device__ __forceinline__ void offer(float ov, int oid, int keep, int lane) {
+    for (;;) {
+      const float lv = __shfl_sync(0xffffffffu, v, keep - 1);
+      const int lid = __shfl_sync(0xffffffffu, id, keep - 1);
+      const unsigned m = __ballot_sync(0xffffffffu, oid != kNoId && precedes(ov, oid, lv, lid));
+      if (!m) return;
+      const int from = __ffs(m) - 1;
+      insert(__shfl_sync(0xffffffffu, ov, from), __shfl_sync(0xffffffffu, oid, from), lane);
+      if (lane == from) oid = kNoId;
+    }
+  }
+};
+__device__ __forceinline__ float no_nan(float v) { return isnan(v) ? -INFINITY : v; }
+
+// The block's lists into warp 0's.
+__device__ __forceinline__ void join_lists(Best &b, float2 (&lists)[kFinishWarps][32], int keep, int warp, int lane) {
+  lists[warp][lane] = make_float2(b.v, __int_as_float(b.id));
+  __syncthreads();
+  if (warp == 0)
+    for (int w = 1; w < kFinishWarps; ++w) b.offer(lists[w][lane].x, __float_as_int(lists[w][lane].y), keep, lane);
+  __syncthreads();
+}
+
+// hi + lo += a * b, to about twice fp32's precision
+__device__ __forceinline__ void add_product(float &hi, float &lo, float a, float b) {
+  const float p = __fmul_rn(a, b), e = __fmaf_rn(a, b, -p);
+  const float s = __fadd_rn(hi, p), t = __fsub_rn(s, hi);
+  lo = __fadd_rn(lo, __fadd_rn(e, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(p, t))));
+  hi = s;
+}
+// the logit of a row and a token, by a warp
+template <typename T>
+__device__ __forceinline__ double long_logit(const TargetLogit &at, int64_t row, int64_t id, int lane) {
+  constexpr int kN = 16 / (int)sizeof(T);
+  const T *a = reinterpret_cast<const T *>(at.x) + row * at.x_ld, *b = reinterpret_cast<const T *>(at.w) + id * at.w_ld;
+  const int groups = (at.width + kN - 1) / kN;
+  float hi = 0.f, lo = 0.f;
+#pragma unroll 2
+  for (int g = lane; g < groups; g += 32) {
+    const Pack<T, 16> p = TargetLogit::some(a, g, at.width, at.x_wide), q = TargetLogit::some(b, g, at.width, at.w_wide);
+#pragma unroll
+    for (int e = 0; e < kN; ++e) add_product(hi, lo, p.get(e), q.get(e));
+  }
+  double s = (double)hi + (double)lo;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  return s;
+}
+
+// A block per row.
+__global__ void __launch_bounds__(kFinishWarps * 32) k_score_finish(const FinishArgs a) {
+  pdl_wait();
+  __shared__ float2 lists[kFinishWarps][32];
+  __shared__ float4 sums[kFinishWarps];
+  __shared__ double exact[32];
+  __shared__ unsigned again;
+  const int64_t row = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool bad = a.last && any_error(a.err);
+  const uint32_t target = a.targets.ids ? a.targets.key(row) : a.targets.vocab;
+  const bool given = target < a.targets.vocab;
+  if (a.targets.ids && !given) {  // not scored
+    if (!a.last) return;
+    for (int i = threadIdx.x; i < a.top; i += kFinishWarps * 32) {
+      a.top_ids[row * a.top + i] = -1;
+      a.top_logp[row * a.top + i] = 0.f;
+    }
+    if (threadIdx.x == 0) {
+      if (a.logp) a.logp[row] = 0.f;
+      if (a.entropy) a.entropy[row] = 0.f;
+      a.lse[row] = 0.f;
+      a.kept_entropy[row] = 0.f;
+    }
+    return;
+  }
+  Best b;
+  if (a.top) {
+    // the groups with the largest maxima
+    b.clear();
+    const float *high = a.high + row * a.high_ld;
+    for (int g = warp * 32; g < a.groups; g += kFinishWarps * 32) {
+      const bool in = g + lane < a.groups;
+      b.offer(in ? no_nan(__ldg(high + g + lane)) : 0.f, in ? g + lane : kNoId, a.keep, lane);
+    }
+    join_lists(b, lists, a.keep, warp, lane);
+    if (warp == 0) lists[0][lane] = make_float2(b.v, __int_as_float(b.id));
+    __syncthreads();
+    // and the largest of their logits: none below the last group's maximum
+    constexpr int kMost = (kMostTop + kKeepMore + kFinishWarps - 1) / kFinishWarps;
+    const float least = lists[0][a.keep - 1].x;
+    float v[kMost];
+    int col[kMost];
+#pragma unroll
+    for (int u = 0; u < kMost; ++u) {
+      const int i = warp + u * kFinishWarps;
+      const int g = i < a.keep ? __float_as_int(lists[0][i].y) : kNoId;
+      col[u] = g != kNoId && g * 32 + lane < a.rows ? g * 32 + lane : -1;
+      v[u] = col[u] >= 0 ? no_nan(__ldg(a.z + row * a.z_row + col[u] * a.z_col)) : 0.f;
+    }
+    __syncthreads();
+    b.clear();
+    if (warp == 0 && !a.first) {
+      const float2 e = a.list[row * 32 + lane];
+      b.v = e.x;
+      b.id = __float_as_int(e.y);
+    }
+#pragma unroll
+    for (int u = 0; u < kMost; ++u) b.offer(v[u], col[u] >= 0 && v[u] >= least ? a.v0 + col[u] : kNoId, a.keep, lane);
+    join_lists(b, lists, a.keep, warp, lane);
+    if (!a.last) {
+      if (warp == 0) a.list[row * 32 + lane] = make_float2(b.v, __int_as_float(b.id));
+      return;
+    }
+  }
+  // the row's statistics
+  float4 s = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+  for (int i = threadIdx.x; i < a.slots; i += kFinishWarps * 32) s = join_stats(s, a.stats[row * a.stats_ld + i]);
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {  // lane by lane upwards: the same result in all
+    float4 o;
+    o.x = __shfl_xor_sync(0xffffffffu, s.x, d);
+    o.y = __shfl_xor_sync(0xffffffffu, s.y, d);
+    o.z = __shfl_xor_sync(0xffffffffu, s.z, d);
+    o.w = __shfl_xor_sync(0xffffffffu, s.w, d);
+    s = lane & d ? join_stats(o, s) : join_stats(s, o);
+  }
+  if (lane == 0) sums[warp] = s;
+  if (a.top && warp == 0) {  // which of the list are too close to tell
+    const float above = __shfl_up_sync(0xffffffffu, b.v, 1);
+    float size = lane < a.keep && isfinite(b.v) ? fabsf(b.v) : 0.f;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, d));
+    const bool close = lane > 0 && lane < a.keep && b.id != kNoId && above - b.v <= size * 0x1p-12f;  // not of two infinities
+    const unsigned joined = __ballot_sync(0xffffffffu, close);  // bit l: l goes with l - 1
+    // a run of them that begins before place `top`
+    const int begin = 31 - __clz(~joined & (0xffffffffu >> (31 - lane)));
+    const bool run = close || (lane < 31 && (joined >> (lane + 1)) & 1);
+    const unsigned m = __ballot_sync(0xffffffffu, run && begin < a.top);
+    if (lane == 0) again = m;
+    lists[0][lane] = make_float2(b.v, __int_as_float(b.id));
+  }
+  __syncthreads();
+  if (a.top) {
+    int k = 0;
+    for (unsigned m = again; m; m &= m - 1, ++k) {
+      if (k % kFinishWarps != warp) continue;
+      const int i = __ffs(m) - 1, id = __float_as_int(lists[0][i].y);
+      const double l = a.at.bf ? long_logit<bf16>(a.at, row, id, lane) : long_logit<float>(a.at, row, id, lane);
+      if (lane == 0) exact[i] = l;
+    }
+    __syncthreads();
+  }
+  if (warp) return;
+  s = sums[0];
+#pragma unroll
+  for (int w = 1; w < kFinishWarps; ++w) s = join_stats(s, sums[w]);
+  float z = 0.f;
+  if (given) z = a.zt ? a.zt[row] : a.at.get(row, target);
+  // the largest logit with the target's, and of the sums relative to it what is over 1
+  float high = s.x, over, slope;
+  if (given && z >= s.x) {
+    const float d = s.x - z, f = s.x == -INFINITY ? 0.f : expf(d), all = s.y + s.z;
+    high = z;
+    over = s.x == -INFINITY ? s.z : f * all;
+    slope = s.x == -INFINITY ? 0.f : f * fmaf(all, fmaxf(d, kFarBelow), s.w);
+  } else {
+    const float d = z - s.x, f = given ? expf(d) : 0.f;
+    over = (s.y - 1.f) + s.z + f;
+    slope = given ? fmaf(f, fmaxf(d, kFarBelow), s.w) : s.w;
+  }
+  if (bad || !(high < INFINITY) || isnan(z)) over = NAN;
+  const float log_sum = log1pf(over), logp = (z - high) - log_sum, entropy = log_sum - slope / (1.f + over);
+  if (lane == 0) {
+    if (a.logp) a.logp[row] = given ? logp : 0.f;
+    if (a.entropy) a.entropy[row] = entropy;
+    a.lse[row] = high + log_sum;
+    a.kept_entropy[row] = entropy;
+  }
+  if (!a.top) return;
+  double l = b.v;
+  if ((again >> lane) & 1 && isfinite(exact[lane])) l = exact[lane];
+  int place = 0;
+  for (int j = 0; j < a.keep; ++j) {
+    const double lj = __shfl_sync(0xffffffffu, l, j);
+    const int ij = __shfl_sync(0xffffffffu, b.id, j);
+    place += lj > l || (lj == l && ij < b.id) ? 1 : 0;
+  }
+  if (lane < a.keep && place < a.top) {
+    const float own = given && b.id == (int)target ? logp : ((float)l - high) - log_sum;
+    a.top_ids[row * a.top + place] = b.id;
+    a.top_logp[row * a.top + place] = own;
+  }
+}
+
+// The gradients' weights as the loss's: of the log probability's negative, and of the
+// entropy; and targets where none are given.
+__global__ void __launch_bounds__(256) k_score_weights(int32_t n, const float *__restrict__ dlogp, const float *__restrict__ dentropy,
+                                                       float *__restrict__ weight, float *__restrict__ went, int32_t *__restrict__ ids) {
+  pdl_wait();
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  weight[i] = dlogp ? -dlogp[i] : 0.f;
+  went[i] = dentropy ? -dentropy[i] : 0.f;
+  if (ids) ids[i] = 0;
+}
+
+// ------------------------------------------------------------ host side
+
+struct ScoreWs {
+  size_t err, zt, xp, wp, z, stats, high, list, total;
+  int32_t tokens;             // few tokens: those that the logits' kernel is built for
+  int64_t piece, slots;
+  int64_t z_ld, high_ld;
+  int nt;
+};
+
+ScoreWs score_ws(const XentShape &s, int32_t top) {
+  ScoreWs w = {};
+  size_t o = 0;
+  auto take = [&o](size_t bytes) {
+    const size_t at = o;
+    o += align_up(bytes, kAlign);
+    return at;
+  };
+  const int64_t m_tiles = ceil_div(s.n, kM);
+  w.err = take(256 * 4);
+  w.zt = take((size_t)s.n * 4);
+  if (s.few || s.cut) {
+    w.tokens = s.few ? kFewMostLogits : cut_tokens(s.n);
+    w.piece = s.vocab;
+    w.high_ld = w.slots = ceil_div(s.vocab, 32);
+    w.z = take((size_t)s.vocab * (size_t)w.tokens * 4);
+  } else {
+    const int64_t w_row = (int64_t)s.parts * s.ld * 2, row = std::max(s.pack_w ? w_row : 0, top ? (int64_t)s.n * 4 : 0);
+    if (s.pack_x) w.xp = take((size_t)s.parts * (size_t)s.n * (size_t)s.ld * 2);
+    w.piece = row ? piece_rows(s.vocab, row, m_tiles, s.sms) : s.vocab;
+    if (w.piece > s.vocab) w.piece = s.vocab;
+    if (s.pack_w) w.wp = take((size_t)s.parts * (size_t)w.piece * (size_t)s.ld * 2);
+    w.nt = tile_cols(m_tiles, w.piece, s.sms);
+    w.slots = 2 * (ceil_div(s.vocab, w.piece) * ceil_div(w.piece, w.nt));
+    w.z_ld = ceil_div(w.piece, 64) * 64;
+    w.high_ld = ceil_div(w.piece, w.nt) * w.nt / 32;
+    if (top) w.z = take((size_t)s.n * (size_t)w.z_ld * 4);
+    if (top && w.piece < s.vocab) w.list = take((size_t)s.n * 32 * 8);
+  }
+  w.stats = take((size_t)s.n * (size_t)w.slots * 16);
+  if (top) w.high = take((size_t)s.n * (size_t)w.high_ld * 4);
+  w.total = o;
+  return w;
+}
+
+cudaError_t score_logits_few(const XentShape &S, const ScoreWs &W, const void *x, int64_t x_ld, const void *w, int64_t w_ld,
+                             const TokenSrc &tg, float *z, cudaStream_t s) {
+  if (S.few) {
+    SmallArgs a = small_args(S, x, x_ld, w, w_ld, tg);
+    a.dz = z;
+    const int64_t tiles = ceil_div(S.vocab, (int64_t)kSmallWarps * kSmallRows);
+    return launch_few<true>(a, tiles < S.sms ? tiles : S.sms, s);
+  }
+  CutArgs c = cut_args(S, x, x_ld, w, w_ld, tg);
+  c.dz = z;
+  return launch_cut_for<true>(c, cut_blocks(S, S.vocab), s);
+}
+
+}  // namespace
+}  // namespace snack
+
+extern "C" {
+
+snack_status snack_score_workspace_size(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld,
+                                        int64_t vocab, int32_t width, snack_dtype t, int32_t top, int grad, size_t *bytes) {
+  if (!bytes) return SNACK_ERR_INVALID_ARG;
+  const snack_status st = xent_check(x, x_ld, n, w, w_ld, vocab, width, t);
+  if (st != SNACK_OK) return st;
+  if (top < 0 || top > vocab) return SNACK_ERR_INVALID_ARG;
+  if (top > kMostTop) return SNACK_ERR_UNSUPPORTED;
+  const XentShape S = xent_shape(x, x_ld, n, w, w_ld, vocab, width, t, grad != 0);
+  *bytes = n == 0 ? 0 : grad ? xent_ws(S, true).total + 3 * align_up((size_t)n * 4, kAlign) : score_ws(S, top).total;
+  return SNACK_OK;
+}
+
+snack_status snack_score_fwd(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld, int64_t vocab,
+                             int32_t width, snack_dtype t, const void *targets, snack_index targets_t, float *logp,
+                             float *entropy, int32_t top, int64_t *top_ids, float *top_logp, float *state, void *ws,
+                             size_t ws_bytes, snack_stream_t stream) try {
+  const snack_status ck = xent_check(x, x_ld, n, w, w_ld, vocab, width, t);
+  if (ck != SNACK_OK) return ck;
+  if (!lm_index_ok(targets_t) || top < 0 || top > vocab) return SNACK_ERR_INVALID_ARG;
+  if (top > kMostTop) return SNACK_ERR_UNSUPPORTED;
+  if (n == 0) return SNACK_OK;
+  if (!x || !w || !state || !ws || (top > 0 && (!top_ids || !top_logp)) || (logp && !targets) ||
+      !ptr_aligned(targets, index_size(targets_t)) || !ptr_aligned(logp, 4) || !ptr_aligned(entropy, 4) || !ptr_aligned(state, 4) ||
+      !ptr_aligned(top_ids, 8) || !ptr_aligned(top_logp, 4) || !ptr_aligned(ws, kAlign))
+    return SNACK_ERR_INVALID_ARG;
+  const XentShape S = xent_shape(x, x_ld, n, w, w_ld, vocab, width, t, false);
+  const ScoreWs W = score_ws(S, top);
+  if (ws_bytes < W.total) return SNACK_ERR_WORKSPACE;
+  const size_t es = dtype_size(t);
+  const Span written[] = {{logp, logp ? (size_t)n * 4 : 0},
+                          {entropy, entropy ? (size_t)n * 4 : 0},
+                          {top_ids, (size_t)n * (size_t)top * 8},
+                          {top_logp, (size_t)n * (size_t)top * 4},
+                          {state, (size_t)n * 8},
+                          {ws, W.total}};
+  const Span read[] = {{x, span_bytes(n, width, x_ld, es)}, {w, span_bytes(vocab, width, w_ld, es)},
+                       {targets, targets ? (size_t)n * index_size(targets_t) : 0}};
+  if (any_overlap(written, read)) return SNACK_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t *b = reinterpret_cast<uint8_t *>(ws);
+  const TokenSrc tg{targets, targets_t == SNACK_I64, (uint32_t)vocab};
+  FinishArgs f = {};
+  f.n = n;
+  f.targets = tg;
+  f.top = top;
+  f.keep = (int32_t)std::min<int64_t>(top + kKeepMore, vocab);
+  f.high = top ? reinterpret_cast<const float *>(b + W.high) : nullptr;
+  f.high_ld = W.high_ld;
+  f.z = reinterpret_cast<const float *>(b + W.z);
+  f.list = reinterpret_cast<float2 *>(b + W.list);
+  f.first = f.last = 1;
+  f.at = target_logit(S, x, x_ld, w, w_ld);
+  f.stats = reinterpret_cast<const float4 *>(b + W.stats);
+  f.stats_ld = W.slots;
+  f.logp = logp;
+  f.entropy = entropy;
+  f.top_logp = top_logp;
+  f.top_ids = top_ids;
+  f.lse = state;
+  f.kept_entropy = state + n;
+  auto finish = [&] { return launch_pdl(k_score_finish, (unsigned)n, kFinishWarps * 32, 0, s, (const FinishArgs)f); };
+  if (W.tokens) {
+    float *z = reinterpret_cast<float *>(b + W.z), *zt = reinterpret_cast<float *>(b + W.zt);
+    XENT_CUDA(score_logits_few(S, W, x, x_ld, w, w_ld, tg, z, s));
+    const int64_t threads = W.slots * W.tokens;
+    XENT_CUDA(launch_pdl(k_score_stats, (unsigned)ceil_div(threads, 256), 256, 0, s, (const float *)z, W.tokens, n, vocab,
+                         (int32_t)W.slots, tg, reinterpret_cast<float4 *>(b + W.stats), top ? reinterpret_cast<float *>(b + W.high) : nullptr,
+                         zt));
+    f.groups = f.slots = (int32_t)W.slots;
+    f.rows = (int32_t)vocab;
+    f.z_row = 1;
+    f.z_col = W.tokens;
+    f.zt = zt;  // of the same sums as the others, and the gradient's
+    XENT_CUDA(finish());
+    return SNACK_OK;
+  }
+  const uint32_t a_rows = n >= kMCta ? kMCta : (uint32_t)align_up((size_t)n, 8);
+  Operand ox, ow;
+  XENT_CUDA(operand(S, S.pack_x, x, x_ld, 0, n, b + W.xp, &ox, s));
+  CUtensorMap mx, mw, mz;
+  if (!load_map(&mx, ox, false, a_rows)) return SNACK_ERR_CUDA;
+  GemmArgs g = gemm_args(S, b, XentWs{}, 1);
+  g.err = reinterpret_cast<uint32_t *>(b + W.err);
+  g.m = n;
+  g.nt = W.nt;
+  g.k_blocks = (int32_t)ceil_div(width, kKb);
+  g.targets = tg;
+  g.stats = reinterpret_cast<float4 *>(b + W.stats);
+  g.stats_ld = W.slots;
+  g.high = top ? reinterpret_cast<float *>(b + W.high) : nullptr;
+  g.high_ld = W.high_ld;
+  f.err = g.err;
+  f.z_row = W.z_ld;
+  f.z_col = 1;
+  for (int64_t v0 = 0; v0 < vocab; v0 += W.piece) {
+    const int64_t rows = vocab - v0 < W.piece ? vocab - v0 : W.piece;
+    XENT_CUDA(operand(S, S.pack_w, w, w_ld, v0, rows, b + W.wp, &ow, s));
+    if (!load_map(&mw, ow, false, (uint32_t)W.nt / 2)) return SNACK_ERR_CUDA;
+    if (top && !make_map(&mz, f.z, true, (uint64_t)rows, (uint64_t)n, (uint64_t)W.z_ld, 1, (uint64_t)n * (uint64_t)W.z_ld, 32, 32,
+                         CU_TENSOR_MAP_SWIZZLE_128B))
+      return SNACK_ERR_CUDA;
+    g.n = (int32_t)rows;
+    g.v0 = (int32_t)v0;
+    XENT_CUDA(launch_gemm<kScore>(mx, mw, top ? mz : mx, g, S.sms, s));
+    g.slot0 += 2 * g.n_tiles;
+    f.last = v0 + rows == vocab;
+    f.slots = g.slot0;
+    f.groups = (int32_t)ceil_div(rows, 32);
+    f.rows = (int32_t)rows;
+    f.v0 = (int32_t)v0;
+    if (top || f.last) XENT_CUDA(finish());
+    f.first = 0;
+  }
+  return SNACK_OK;
+} catch (...) {  // a host allocation failed
+  return SNACK_ERR_CUDA;
+}
+
+snack_status snack_score_bwd(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld, int64_t vocab,
+                             int32_t width, snack_dtype t, const void *targets, snack_index targets_t, const float *state,
+                             const float *dlogp, const float *dentropy, void *dx, int64_t dx_ld, void *dw, int64_t dw_ld,
+                             void *ws, size_t ws_bytes, snack_stream_t stream) try {
+  const snack_status ck = xent_check(x, x_ld, n, w, w_ld, vocab, width, t);
+  if (ck != SNACK_OK) return ck;
+  const size_t es = dtype_size(t);
+  if (!lm_index_ok(targets_t) || (dlogp && !targets)) return SNACK_ERR_INVALID_ARG;
+  if ((dx && (dx_ld < width || !ptr_aligned(dx, es))) || (dw && (dw_ld < width || !ptr_aligned(dw, es))))
+    return SNACK_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (n == 0) {
+    if (dw) XENT_CUDA(cudaMemset2DAsync(dw, (size_t)dw_ld * es, 0, (size_t)width * es, (size_t)vocab, s));
+    return SNACK_OK;
+  }
+  if (!x || !w || !state || !ws || !ptr_aligned(targets, index_size(targets_t)) || !ptr_aligned(state, 4) || !ptr_aligned(ws, kAlign) ||
+      !ptr_aligned(dlogp, 4) || !ptr_aligned(dentropy, 4))
+    return SNACK_ERR_INVALID_ARG;
+  const XentShape S = xent_shape(x, x_ld, n, w, w_ld, vocab, width, t, true);
+  const XentWs W = xent_ws(S, true);
+  const size_t each = align_up((size_t)n * 4, kAlign), total = W.total + 3 * each;
+  const Span written[] = {{dx, dx ? span_bytes(n, width, dx_ld, es) : 0}, {dw, dw ? span_bytes(vocab, width, dw_ld, es) : 0},
+                          {ws, std::min(ws_bytes, total)}};
+  const Span read[] = {{x, span_bytes(n, width, x_ld, es)}, {w, span_bytes(vocab, width, w_ld, es)},
+                       {targets, targets ? (size_t)n * index_size(targets_t) : 0}, {state, (size_t)n * 8},
+                       {dlogp, dlogp ? (size_t)n * 4 : 0}, {dentropy, dentropy ? (size_t)n * 4 : 0}};
+  if (any_overlap(written, read)) return SNACK_ERR_INVALID_ARG;
+  if (ws_bytes < total) return SNACK_ERR_WORKSPACE;
+  if (!dx && !dw) return SNACK_OK;
+  uint8_t *extra = reinterpret_cast<uint8_t *>(ws) + W.total;
+  float *weight = reinterpret_cast<float *>(extra), *went = reinterpret_cast<float *>(extra + each);
+  int32_t *ids = targets ? nullptr : reinterpret_cast<int32_t *>(extra + 2 * each);
+  XENT_CUDA(launch_pdl(k_score_weights, (unsigned)ceil_div(n, 256), 256, 0, s, n, dlogp, dentropy, weight, went, ids));
+  const TokenSrc tg = targets ? TokenSrc{targets, targets_t == SNACK_I64, (uint32_t)vocab} : TokenSrc{ids, 0, (uint32_t)vocab};
+  return xent_gradient(S, W, x, x_ld, w, w_ld, tg, weight, Entropy{went, state + n}, Factor{nullptr, nullptr}, state, dx, dx_ld, dw,
+                       dw_ld, reinterpret_cast<uint8_t *>(ws), s);
+} catch (...) {  // a host allocation failed
+  return SNACK_ERR_CUDA;
+}
+
+}  // extern "C"

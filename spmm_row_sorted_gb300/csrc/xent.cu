@@ -240,7 +240,7 @@ constexpr int kSmem = 1024 + kRing + kEpiWarps * kStaging + kBarBytes;
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 static_assert(kStageA <= kEpiWarps * kStaging, "a short A tile's reads end within the CTA's shared memory");
 
-enum { kStats = 0, kDlog = 1, kDx = 2, kDw = 3 };
+enum { kStats = 0, kDlog = 1, kDx = 2, kDw = 3, kScore = 4 };  // kScore: score.cuh
 
 // The factor common to all rows of dz (sum and mean): a product of up to two
 // device values.  It is applied to the finished sums, so dz itself lies in
@@ -271,6 +271,7 @@ struct GemmArgs {
   int32_t v0;               // first vocabulary row of the piece
   // dlog
   const float *lse, *hot;   // [m] each, hot: dz at the target
+  Entropy ent;
   const float *dloss;       // upstream gradient of each row, or null (1: a common factor is applied to the sums)
   int32_t out_parts;        // bf16 parts of dz
   // dx
@@ -282,6 +283,10 @@ struct GemmArgs {
   int64_t out_ld;
   int32_t out_wide;         // fp32 (else bf16)
   int32_t out_tma;
+  // score
+  float4 *stats;            // [m][slots] (maximum, how often, sum of exp(z - maximum) of the others, sum of it times z - maximum)
+  float *high;              // [m][high_ld] maximum of 32 neighbouring logits each, or null: then no logits are kept
+  int64_t stats_ld, high_ld;
 };
 
 // the six part products, smallest first: parts (2,0) (1,1) (0,2) (1,0) (0,1) (0,0)
@@ -308,9 +313,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // the four, 1.7 to 1.9 PFLOP/s as the power allows (90 % of the tensor cores'
 // cycles; 80 to 88 % where partial sums are read).
 template <int kMode>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(const __grid_constant__ CUtensorMap map_a,
-                                                      const __grid_constant__ CUtensorMap map_b,
-                                                      const __grid_constant__ CUtensorMap map_o, const GemmArgs P) {
+__device__ __forceinline__ void product(const CUtensorMap &map_a, const CUtensorMap &map_b, const CUtensorMap &map_o,
+                                        const GemmArgs &P) {
   pdl_wait();
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -495,8 +499,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
       // the target's column of this tile's half, or below zero
       int tcol = -1;
       float lse = 0.f, g = 0.f, hot = 0.f;
-      if (kMode == kStats || kMode == kDlog) {
-        if (row_ok) {
+      float went = 0.f, ent = 0.f;
+      if (kMode == kStats || kMode == kDlog || kMode == kScore) {
+        if (row_ok && (kMode != kScore || P.targets.ids)) {
           const uint32_t id = P.targets.key(row);
           if (id < P.targets.vocab) {
             tcol = (int)id - P.v0 - col0;  // beyond c_end: another half's
@@ -504,6 +509,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
               lse = P.lse[row];
               g = P.dloss ? P.dloss[row] : 1.f;
               hot = P.hot[row];
+              if (P.ent.weight) {
+                went = P.ent.weight[row];
+                ent = P.ent.value[row];
+              }
             }
           }
         }
@@ -586,20 +595,93 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
         }
         if (row_ok)
           P.part[(size_t)(P.slot0 + 2 * (q.n0 / P.nt) + half) * (size_t)P.m + row] = make_float2(mx, sum);
+      } else if (kMode == kScore) {
+        const int slot = 2 * (q.n0 / P.nt) + half;
+        float high[kChunks], mx = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < kChunks; ++h) {
+          const int c = 32 * h;
+          high[h] = -INFINITY;
+          if (c >= c_end) continue;
+          float(&v)[32] = acc[h];
+          if (P.high) {  // the logits as they are
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch)
+              *reinterpret_cast<float4 *>(stage + stage_off(lane, ch)) =
+                  make_float4(v[4 * ch], v[4 * ch + 1], v[4 * ch + 2], v[4 * ch + 3]);
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0 && col0 + c < P.n && m0 + quarter * 32 < P.m) {
+              tma_store(&map_o, stage, col0 + c, m0 + quarter * 32, 0);
+              bulk_commit();
+            }
+          }
+          const int valid = P.n - col0 - c;
+          if (valid < 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j >= valid) v[j] = -INFINITY;
+          }
+          auto largest = [&] {
+            float m4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+            for (int j = 4; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], v[j]);
+            return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          };
+          float top = largest();
+          high[h] = top;
+          if (tcol >= c && tcol < c + 32) {  // joined later
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (tcol == c + j) v[j] = -INFINITY;
+            top = largest();
+          }
+          mx = fmaxf(mx, top);
+        }
+        // the maximum apart from the rest: of a confident row's sums the rest is what counts
+        const float base = mx == -INFINITY ? 0.f : mx;
+        float often = 0.f, rest[2] = {0.f, 0.f}, slope[2] = {0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < kChunks; ++h) {
+          if (32 * h >= c_end) break;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float d = acc[h][j] - base, e = ex2(d * kLog2e);
+            if (d == 0.f && mx != -INFINITY)
+              often += 1.f;
+            else
+              rest[j & 1] += e;
+            slope[j & 1] = fmaf(e, fmaxf(d, kFarBelow), slope[j & 1]);
+          }
+        }
+        if (row_ok) {
+          P.stats[(size_t)row * (size_t)P.stats_ld + P.slot0 + slot] = make_float4(mx, often, rest[0] + rest[1], slope[0] + slope[1]);
+          if (P.high)
+#pragma unroll
+            for (int h = 0; h < kChunks; ++h)
+              if (32 * h < c_end) P.high[(size_t)row * (size_t)P.high_ld + (col0 / 32 + h)] = high[h];
+        }
       } else if (kMode == kDlog) {
 #pragma unroll
         for (int h = 0; h < kChunks; ++h) {
           const int c = 32 * h;
           if (c >= c_end) break;
           float(&v)[32] = acc[h];
+          if (P.ent.weight) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = g * ex2((v[j] - lse) * kLog2e);
+            for (int j = 0; j < 32; ++j) v[j] = ex2((v[j] - lse) * kLog2e) * entropy_slope(g, went, v[j] - lse, ent);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = g * ex2((v[j] - lse) * kLog2e);
+          }
           if (tcol >= c && tcol < c + 32) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (tcol == c + j) v[j] = hot;
           }
-          if (g == 0.f) {  // not trained on, whatever its logits
+          if (g == 0.f && went == 0.f) {  // not trained on, whatever its logits
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = 0.f;
           }
@@ -726,6 +808,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(
   pair_sync();  // nothing of either CTA is still at work in the other's memory
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+template <int kMode>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_xent(const __grid_constant__ CUtensorMap map_a,
+                                                      const __grid_constant__ CUtensorMap map_b,
+                                                      const __grid_constant__ CUtensorMap map_o, const GemmArgs P) {
+  product<kMode>(map_a, map_b, map_o, P);
+}
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ CUtensorMap map_a,
+                                                      const __grid_constant__ CUtensorMap map_b,
+                                                      const __grid_constant__ CUtensorMap map_o, const GemmArgs P) {
+  product<kScore>(map_a, map_b, map_o, P);
 }
 
 __device__ __forceinline__ bool any_error(const uint32_t *err) {
@@ -891,8 +985,9 @@ __global__ void __launch_bounds__(1024) k_xent_total(const float *__restrict__ r
 struct Drop {
   TokenSrc targets;     // ids null: none are
   const float *weight;  // per row, or null
+  const float *went;    // of the rows' entropies, or null
   __device__ __forceinline__ bool row(int64_t r) const {
-    return targets.ids && (targets.key(r) >= targets.vocab || (weight && weight[r] == 0.f));
+    return targets.ids && (targets.key(r) >= targets.vocab || (weight && weight[r] == 0.f && (!went || went[r] == 0.f)));
   }
 };
 
@@ -905,7 +1000,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) k_xent_pack(const T *__restrict__ in, int64_t ld, int64_t rows, int32_t width,
                                                    int parts, bf16 *__restrict__ out, int32_t out_ld, int64_t plane, int vec, const Drop drop,
                                                    const TargetLogit tl, const float *__restrict__ lse,
-                                                   float *__restrict__ hot) {
+                                                   const Entropy ent, float *__restrict__ hot) {
   pdl_wait();
   constexpr int kU = 4, kB = 16 / (int)sizeof(T);
   const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -913,7 +1008,12 @@ __global__ void __launch_bounds__(256) k_xent_pack(const T *__restrict__ in, int
   const bool dropped = drop.row(r);
   if (hot) {
     const float z = dropped ? 0.f : tl.get(r, drop.targets.key(r));
-    if ((threadIdx.x & 31) == 0) hot[r] = dropped ? 0.f : (drop.weight ? drop.weight[r] : 1.f) * expm1f(z - lse[r]);
+    if ((threadIdx.x & 31) == 0) {
+      const float d = dropped ? 0.f : z - lse[r];
+      float v = dropped ? 0.f : (drop.weight ? drop.weight[r] : 1.f) * expm1f(d);
+      if (ent.weight && !dropped) v = fmaf(expf(d), entropy_slope(0.f, ent.weight[r], d, ent.value[r]), v);
+      hot[r] = v;
+    }
   }
   const int groups = out_ld / 8;
   for (int g0 = threadIdx.x & 31; g0 < groups; g0 += 32 * kU) {
@@ -1315,24 +1415,31 @@ int unit_of(int k_blocks, int most) { return (int)ceil_div(k_blocks, ceil_div(k_
 template <int kMode>
 cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o, GemmArgs &g, int sms,
                         cudaStream_t s) {
-  cudaError_t e = raise_smem_limit(k_xent<kMode>, kSmem);
+  static constexpr auto kernel = [] {
+    if constexpr (kMode == kScore)
+      return k_score;
+    else
+      return k_xent<kMode>;
+  }();
+  constexpr bool kLogits = kMode == kStats || kMode == kScore;
+  cudaError_t e = raise_smem_limit(kernel, kSmem);
   if (e != cudaSuccess) return e;
   // the register split draws on what the launch gives: a kernel built with fewer would wait for ever
   static const bool enough = [] {
     cudaFuncAttributes a;
-    return cudaFuncGetAttributes(&a, k_xent<kMode>) == cudaSuccess &&
+    return cudaFuncGetAttributes(&a, kernel) == cudaSuccess &&
            a.numRegs * kThreads >= 256 * kEpiRegs + 128 * kIssueRegs;
   }();
   if (!enough) return cudaErrorInvalidDeviceFunction;
   g.m_tiles = (int32_t)ceil_div(g.m, kM);
   g.n_tiles = (int32_t)ceil_div(g.n, g.nt);
-  g.unit = unit_of((int)ceil_div(g.k_blocks, g.n_split), g.products > 1 ? (kMode == kStats ? 4 : 8) : kMode == kStats ? 8 : 64);
+  g.unit = unit_of((int)ceil_div(g.k_blocks, g.n_split), g.products > 1 ? (kLogits ? 4 : 8) : kLogits ? 8 : 64);
   g.a_rows = kMode == kDw || g.m >= kMCta ? kMCta : (int32_t)align_up((size_t)g.m, 8);
   g.stages = kRing / ((g.a_rows + g.nt / 2) * kKb * 2);
   if (g.stages > kMaxStages) g.stages = kMaxStages;
   const int64_t tiles = (int64_t)g.m_tiles * g.n_tiles * g.n_split;
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
-  e = launch_pdl(k_xent<kMode>, 2 * (unsigned)(tiles < sms / 2 ? tiles : sms / 2), kThreads, kSmem, s, a, b, o, (const GemmArgs)g);
+  e = launch_pdl(kernel, 2 * (unsigned)(tiles < sms / 2 ? tiles : sms / 2), kThreads, kSmem, s, a, b, o, (const GemmArgs)g);
   g.first = 0;
   return e;
 }
@@ -1342,6 +1449,7 @@ struct RowInfo {
   Drop drop;
   TargetLogit tl;
   const float *lse;
+  Entropy ent;
   float *hot;
 };
 
@@ -1351,10 +1459,10 @@ cudaError_t pack(const XentShape &s, const void *in, int64_t ld, int64_t rows, v
   if (s.t == SNACK_F32)
     return launch_pdl(k_xent_pack<float>, (unsigned)blocks, 256, 0, st, reinterpret_cast<const float *>(in), ld, rows,
                       s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld, vec, ri.drop, ri.tl, ri.lse,
-                    ri.hot);
+                    ri.ent, ri.hot);
   return launch_pdl(k_xent_pack<bf16>, (unsigned)blocks, 256, 0, st, reinterpret_cast<const bf16 *>(in), ld, rows,
                     s.width, s.parts, reinterpret_cast<bf16 *>(out), s.ld, (int64_t)rows * s.ld, vec, ri.drop, ri.tl, ri.lse,
-                    ri.hot);
+                    ri.ent, ri.hot);
 }
 
 // x, or a piece of w from row v0 on, as the products read it
@@ -1501,15 +1609,180 @@ bool any_overlap(const Span (&written)[kWritten], const Span (&read)[kRead]) {
   return false;
 }
 
-}  // namespace
-}  // namespace snack
-
-using namespace snack;
-
 #define XENT_CUDA(x)                               \
   do {                                             \
     if ((x) != cudaSuccess) return SNACK_ERR_CUDA; \
   } while (0)
+
+// The gradients of a loss whose dz[i, v] is weight[i] (1 where weight is null) times
+// (p - [v = target]), and with ent weights of the rows' entropies besides, all times
+// factor.  state: the rows' log sums of exponentials.
+snack_status xent_gradient(const XentShape &S, const XentWs &W, const void *x, int64_t x_ld, const void *w, int64_t w_ld,
+                           const TokenSrc &tg, const float *weight, const Entropy &ent, const Factor &factor,
+                           const float *state, void *dx, int64_t dx_ld, void *dw, int64_t dw_ld, uint8_t *b, cudaStream_t s) {
+  const int32_t n = S.n, width = S.width;
+  const int64_t vocab = S.vocab;
+  const size_t es = dtype_size(S.t);
+  const bool wide = S.t == SNACK_F32;
+  if (S.few) {
+    SmallArgs a = small_args(S, x, x_ld, w, w_ld, tg);
+    a.lse = state;
+    a.weight = weight;
+    a.ent = ent;
+    a.dz = reinterpret_cast<float *>(b + W.dz);
+    if (S.few_logits) {
+      XENT_CUDA(launch_few<true>(a, W.few_blocks, s));
+    } else {
+      CutArgs c = cut_args(S, x, x_ld, w, w_ld, tg);
+      c.lse = a.lse;
+      c.weight = weight;
+      c.ent = ent;
+      c.dz = a.dz;
+      XENT_CUDA(launch_cut_for<true>(c, cut_blocks(S, vocab), s));
+    }
+    SmallGrad g = {};
+    g.x = a.x;
+    g.w = a.w;
+    g.dz = a.dz;
+    g.x_ld = x_ld;
+    g.w_ld = w_ld;
+    g.dw_ld = dw_ld;
+    g.n = n;
+    g.width = width;
+    g.vocab = vocab;
+    g.rows_per_split = W.few_rows;
+    g.w_wide = a.w_wide;
+    g.dw_wide = ptr_aligned(dw, 16) && dw_ld % 4 == 0;
+    g.targets = tg;
+    g.weight = weight;
+    g.went = ent.weight;
+    g.factor_a = factor.a;
+    g.factor_b = factor.b;
+    g.acc = reinterpret_cast<float *>(b + W.acc);
+    g.acc_ld = W.acc_ld;
+    g.dw = reinterpret_cast<float *>(dw);
+    const dim3 grid((unsigned)ceil_div(width, 32 * few_cols(W.few_nt)), (unsigned)W.split);
+    XENT_CUDA(W.few_nt == 4   ? launch_few_grad<4>(g, grid, dx, dw, s)
+              : W.few_nt == 8 ? launch_few_grad<8>(g, grid, dx, dw, s)
+                              : launch_few_grad<16>(g, grid, dx, dw, s));
+    if (dx)
+      XENT_CUDA(launch_pdl(k_xent_dx<float>, (unsigned)ceil_div((int64_t)n * (W.acc_ld / 4), 256), 256, 0, s,
+                           (const float *)g.acc, W.split, (int64_t)n * W.acc_ld, W.acc_ld, n, width,
+                           reinterpret_cast<float *>(dx), dx_ld, (float *)nullptr, factor, Drop{tg, weight, ent.weight},
+                           (const float *)nullptr, (const float *)nullptr, (int64_t)0, 0, (const uint32_t *)nullptr));
+    return SNACK_OK;
+  }
+  const uint32_t a_rows = n >= kMCta ? kMCta : (uint32_t)align_up((size_t)n, 8);
+  Operand ox, ow;
+  float *hot = reinterpret_cast<float *>(b + W.hot);
+  XENT_CUDA(operand(S, S.pack_x, x, x_ld, 0, n, b + W.xp, &ox, s,
+                    RowInfo{Drop{tg, weight, ent.weight}, target_logit(S, x, x_ld, w, w_ld), state, ent, S.cut ? nullptr : hot}));
+  CUtensorMap mx, mw, mxt, mwt, mdz, mdzt, mdz_out, macc, mdw;
+  if (!load_map(&mx, ox, false, a_rows) || !load_map(&mxt, ox, true, 0)) return SNACK_ERR_CUDA;
+  if (!make_map(&macc, b + W.acc, true, (uint64_t)width, (uint64_t)n, (uint64_t)W.acc_ld, (uint64_t)W.split,
+                (uint64_t)n * (uint64_t)W.acc_ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+    return SNACK_ERR_CUDA;
+  int first = 1;
+  for (int64_t v0 = 0; v0 < vocab; v0 += W.piece) {
+    const int64_t rows = vocab - v0 < W.piece ? vocab - v0 : W.piece;
+    if (dx || !S.cut) XENT_CUDA(operand(S, S.pack_w, w, w_ld, v0, rows, b + W.wp, &ow, s));
+    const Operand dz = {b + W.dz, n, W.dz_ld, (int64_t)n * W.dz_ld, (int32_t)rows, S.parts};
+    if (!load_map(&mdz, dz, false, a_rows) || !load_map(&mdzt, dz, true, 0) || (dx && !load_map(&mwt, ow, true, 0)))
+      return SNACK_ERR_CUDA;
+    if (S.cut) {  // as the loss's were
+      CutArgs c = cut_args(S, x, x_ld, reinterpret_cast<const float *>(w) + v0 * w_ld, w_ld, tg);
+      c.vocab = rows;
+      c.v0 = (int32_t)v0;
+      c.lse = state;
+      c.weight = weight;
+      c.ent = ent;
+      c.dz_parts = reinterpret_cast<bf16 *>(b + W.dz);
+      c.dz_ld = W.dz_ld;
+      c.plane = dz.plane;
+      XENT_CUDA(launch_cut_for<true>(c, cut_blocks(S, rows), s));
+    } else {
+      const int nt = tile_cols(ceil_div(n, kM), rows, S.sms);
+      if (!load_map(&mw, ow, false, (uint32_t)nt / 2) ||
+          !make_map(&mdz_out, dz.p, false, (uint64_t)rows, (uint64_t)n, (uint64_t)W.dz_ld, (uint64_t)S.parts,
+                    (uint64_t)dz.plane, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+        return SNACK_ERR_CUDA;
+      GemmArgs g = gemm_args(S, b, W, first);
+      g.m = n;
+      g.n = (int32_t)rows;
+      g.nt = nt;
+      g.k_blocks = (int32_t)ceil_div(width, kKb);
+      g.targets = tg;
+      g.v0 = (int32_t)v0;
+      g.lse = state;
+      g.hot = hot;
+      g.dloss = weight;
+      g.ent = ent;
+      g.out_parts = S.parts;
+      XENT_CUDA(launch_gemm<kDlog>(mx, mw, mdz_out, g, S.sms, s));
+      first = 0;
+    }
+    if (dx) {
+      GemmArgs h = gemm_args(S, b, W, first);
+      h.m = n;
+      h.n = width;
+      h.nt = W.nt_d;
+      h.n_split = W.split;
+      h.k_blocks = (int32_t)ceil_div(rows, kKb);
+      h.add = v0 > 0;
+      XENT_CUDA(launch_gemm<kDx>(mdz, mwt, macc, h, S.sms, s));
+      first = 0;
+    }
+    if (dw) {
+      GemmArgs h = gemm_args(S, b, W, first);
+      h.m = (int32_t)rows;
+      h.n = width;
+      h.nt = W.nt_d;
+      h.k_blocks = (int32_t)ceil_div(n, kKb);
+      uint8_t *to = reinterpret_cast<uint8_t *>(dw) + (size_t)v0 * (size_t)dw_ld * es;
+      // a TMA store writes whole 16 bytes at a row's end: of rows of other lengths it would write past them
+      const bool direct = ptr_aligned(to, 16) && (size_t)dw_ld * es % 16 == 0 && (size_t)width * es % 16 == 0;
+      const bool by_ws = !direct && S.pack_dw;
+      uint8_t *out = by_ws ? b + W.dwp : to;
+      const int64_t out_ld = by_ws ? S.ld : dw_ld;
+      h.out = out;
+      h.factor = factor;
+      h.targets = tg;
+      h.tokens = n;
+      h.out_ld = out_ld;
+      h.out_wide = wide;
+      h.out_tma = direct || by_ws;
+      if (h.out_tma && !make_map(&mdw, out, wide, (uint64_t)width, (uint64_t)rows, (uint64_t)out_ld, 1,
+                                 (uint64_t)rows * (uint64_t)out_ld, wide ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+        return SNACK_ERR_CUDA;
+      XENT_CUDA(launch_gemm<kDw>(mdzt, mxt, h.out_tma ? mdw : mxt, h, S.sms, s));
+      first = 0;
+      if (by_ws)
+        XENT_CUDA(launch_pdl(k_xent_rows, (unsigned)ceil_div(rows, 8), 256, 0, s, reinterpret_cast<const bf16 *>(out),
+                             out_ld, rows, width, reinterpret_cast<bf16 *>(to), dw_ld));
+    }
+  }
+  const int64_t total = dx ? (int64_t)n * (W.acc_ld / 4) : 0;
+  int64_t blocks = ceil_div(total, 256);
+  if (blocks > (int64_t)S.sms * 16) blocks = (int64_t)S.sms * 16;
+  if (blocks < 1) blocks = 1;
+  const float *acc = reinterpret_cast<const float *>(b + W.acc);
+  const uint32_t *err = reinterpret_cast<const uint32_t *>(b + W.err);
+  if (wide)
+    XENT_CUDA(launch_pdl(k_xent_dx<float>, (unsigned)blocks, 256, 0, s, acc, W.split, (int64_t)n * W.acc_ld, W.acc_ld,
+                         dx ? n : 0, width, reinterpret_cast<float *>(dx), dx_ld, reinterpret_cast<float *>(dw), factor,
+                         Drop{tg, weight, ent.weight}, (const float *)nullptr, (const float *)nullptr, (int64_t)0, 0, err));
+  else
+    XENT_CUDA(launch_pdl(k_xent_dx<bf16>, (unsigned)blocks, 256, 0, s, acc, W.split, (int64_t)n * W.acc_ld, W.acc_ld,
+                         dx ? n : 0, width, reinterpret_cast<bf16 *>(dx), dx_ld, reinterpret_cast<bf16 *>(dw), factor,
+                         Drop{tg, weight, ent.weight}, (const float *)hot, reinterpret_cast<const bf16 *>(w), w_ld,
+                         ptr_aligned(w, 8) && w_ld % 4 == 0 ? 1 : 0, err));
+  return SNACK_OK;
+}
+
+}  // namespace
+}  // namespace snack
+
+using namespace snack;
 
 extern "C" {
 
@@ -1623,161 +1896,15 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
   if (any_overlap(written, read)) return SNACK_ERR_INVALID_ARG;
   if (ws_bytes < W.total) return SNACK_ERR_WORKSPACE;
   if (!dx && !dw) return SNACK_OK;
-  uint8_t *b = reinterpret_cast<uint8_t *>(ws);
-  const bool wide = t == SNACK_F32;
   const TokenSrc tg{targets, targets_t == SNACK_I64, (uint32_t)vocab};
   const float *weight = reduction == SNACK_NONE ? dloss : nullptr;
   const Factor factor = {reduction == SNACK_NONE ? nullptr : dloss, reduction == SNACK_MEAN ? state + n : nullptr};
-  if (S.few) {
-    SmallArgs a = small_args(S, x, x_ld, w, w_ld, tg);
-    a.lse = state;
-    a.weight = weight;
-    a.dz = reinterpret_cast<float *>(b + W.dz);
-    if (S.few_logits) {
-      XENT_CUDA(launch_few<true>(a, W.few_blocks, s));
-    } else {
-      CutArgs c = cut_args(S, x, x_ld, w, w_ld, tg);
-      c.lse = a.lse;
-      c.weight = weight;
-      c.dz = a.dz;
-      XENT_CUDA(launch_cut_for<true>(c, cut_blocks(S, vocab), s));
-    }
-    SmallGrad g = {};
-    g.x = a.x;
-    g.w = a.w;
-    g.dz = a.dz;
-    g.x_ld = x_ld;
-    g.w_ld = w_ld;
-    g.dw_ld = dw_ld;
-    g.n = n;
-    g.width = width;
-    g.vocab = vocab;
-    g.rows_per_split = W.few_rows;
-    g.w_wide = a.w_wide;
-    g.dw_wide = ptr_aligned(dw, 16) && dw_ld % 4 == 0;
-    g.targets = tg;
-    g.weight = weight;
-    g.factor_a = factor.a;
-    g.factor_b = factor.b;
-    g.acc = reinterpret_cast<float *>(b + W.acc);
-    g.acc_ld = W.acc_ld;
-    g.dw = reinterpret_cast<float *>(dw);
-    const dim3 grid((unsigned)ceil_div(width, 32 * few_cols(W.few_nt)), (unsigned)W.split);
-    XENT_CUDA(W.few_nt == 4   ? launch_few_grad<4>(g, grid, dx, dw, s)
-              : W.few_nt == 8 ? launch_few_grad<8>(g, grid, dx, dw, s)
-                              : launch_few_grad<16>(g, grid, dx, dw, s));
-    if (dx)
-      XENT_CUDA(launch_pdl(k_xent_dx<float>, (unsigned)ceil_div((int64_t)n * (W.acc_ld / 4), 256), 256, 0, s,
-                           (const float *)g.acc, W.split, (int64_t)n * W.acc_ld, W.acc_ld, n, width,
-                           reinterpret_cast<float *>(dx), dx_ld, (float *)nullptr, factor, Drop{tg, weight},
-                           (const float *)nullptr, (const float *)nullptr, (int64_t)0, 0, (const uint32_t *)nullptr));
-    return SNACK_OK;
-  }
-  const uint32_t a_rows = n >= kMCta ? kMCta : (uint32_t)align_up((size_t)n, 8);
-  Operand ox, ow;
-  float *hot = reinterpret_cast<float *>(b + W.hot);
-  XENT_CUDA(operand(S, S.pack_x, x, x_ld, 0, n, b + W.xp, &ox, s,
-                    RowInfo{Drop{tg, weight}, target_logit(S, x, x_ld, w, w_ld), state, S.cut ? nullptr : hot}));
-  CUtensorMap mx, mw, mxt, mwt, mdz, mdzt, mdz_out, macc, mdw;
-  if (!load_map(&mx, ox, false, a_rows) || !load_map(&mxt, ox, true, 0)) return SNACK_ERR_CUDA;
-  if (!make_map(&macc, b + W.acc, true, (uint64_t)width, (uint64_t)n, (uint64_t)W.acc_ld, (uint64_t)W.split,
-                (uint64_t)n * (uint64_t)W.acc_ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B))
-    return SNACK_ERR_CUDA;
-  int first = 1;
-  for (int64_t v0 = 0; v0 < vocab; v0 += W.piece) {
-    const int64_t rows = vocab - v0 < W.piece ? vocab - v0 : W.piece;
-    if (dx || !S.cut) XENT_CUDA(operand(S, S.pack_w, w, w_ld, v0, rows, b + W.wp, &ow, s));
-    const Operand dz = {b + W.dz, n, W.dz_ld, (int64_t)n * W.dz_ld, (int32_t)rows, S.parts};
-    if (!load_map(&mdz, dz, false, a_rows) || !load_map(&mdzt, dz, true, 0) || (dx && !load_map(&mwt, ow, true, 0)))
-      return SNACK_ERR_CUDA;
-    if (S.cut) {  // as the loss's were
-      CutArgs c = cut_args(S, x, x_ld, reinterpret_cast<const float *>(w) + v0 * w_ld, w_ld, tg);
-      c.vocab = rows;
-      c.v0 = (int32_t)v0;
-      c.lse = state;
-      c.weight = weight;
-      c.dz_parts = reinterpret_cast<bf16 *>(b + W.dz);
-      c.dz_ld = W.dz_ld;
-      c.plane = dz.plane;
-      XENT_CUDA(launch_cut_for<true>(c, cut_blocks(S, rows), s));
-    } else {
-      const int nt = tile_cols(ceil_div(n, kM), rows, S.sms);
-      if (!load_map(&mw, ow, false, (uint32_t)nt / 2) ||
-          !make_map(&mdz_out, dz.p, false, (uint64_t)rows, (uint64_t)n, (uint64_t)W.dz_ld, (uint64_t)S.parts,
-                    (uint64_t)dz.plane, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
-        return SNACK_ERR_CUDA;
-      GemmArgs g = gemm_args(S, b, W, first);
-      g.m = n;
-      g.n = (int32_t)rows;
-      g.nt = nt;
-      g.k_blocks = (int32_t)ceil_div(width, kKb);
-      g.targets = tg;
-      g.v0 = (int32_t)v0;
-      g.lse = state;
-      g.hot = hot;
-      g.dloss = weight;
-      g.out_parts = S.parts;
-      XENT_CUDA(launch_gemm<kDlog>(mx, mw, mdz_out, g, S.sms, s));
-      first = 0;
-    }
-    if (dx) {
-      GemmArgs h = gemm_args(S, b, W, first);
-      h.m = n;
-      h.n = width;
-      h.nt = W.nt_d;
-      h.n_split = W.split;
-      h.k_blocks = (int32_t)ceil_div(rows, kKb);
-      h.add = v0 > 0;
-      XENT_CUDA(launch_gemm<kDx>(mdz, mwt, macc, h, S.sms, s));
-      first = 0;
-    }
-    if (dw) {
-      GemmArgs h = gemm_args(S, b, W, first);
-      h.m = (int32_t)rows;
-      h.n = width;
-      h.nt = W.nt_d;
-      h.k_blocks = (int32_t)ceil_div(n, kKb);
-      uint8_t *to = reinterpret_cast<uint8_t *>(dw) + (size_t)v0 * (size_t)dw_ld * es;
-      // a TMA store writes whole 16 bytes at a row's end: of rows of other lengths it would write past them
-      const bool direct = ptr_aligned(to, 16) && (size_t)dw_ld * es % 16 == 0 && (size_t)width * es % 16 == 0;
-      const bool by_ws = !direct && S.pack_dw;
-      uint8_t *out = by_ws ? b + W.dwp : to;
-      const int64_t out_ld = by_ws ? S.ld : dw_ld;
-      h.out = out;
-      h.factor = factor;
-      h.targets = tg;
-      h.tokens = n;
-      h.out_ld = out_ld;
-      h.out_wide = wide;
-      h.out_tma = direct || by_ws;
-      if (h.out_tma && !make_map(&mdw, out, wide, (uint64_t)width, (uint64_t)rows, (uint64_t)out_ld, 1,
-                                 (uint64_t)rows * (uint64_t)out_ld, wide ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
-        return SNACK_ERR_CUDA;
-      XENT_CUDA(launch_gemm<kDw>(mdzt, mxt, h.out_tma ? mdw : mxt, h, S.sms, s));
-      first = 0;
-      if (by_ws)
-        XENT_CUDA(launch_pdl(k_xent_rows, (unsigned)ceil_div(rows, 8), 256, 0, s, reinterpret_cast<const bf16 *>(out),
-                             out_ld, rows, width, reinterpret_cast<bf16 *>(to), dw_ld));
-    }
-  }
-  const int64_t total = dx ? (int64_t)n * (W.acc_ld / 4) : 0;
-  int64_t blocks = ceil_div(total, 256);
-  if (blocks > (int64_t)S.sms * 16) blocks = (int64_t)S.sms * 16;
-  if (blocks < 1) blocks = 1;
-  const float *acc = reinterpret_cast<const float *>(b + W.acc);
-  const uint32_t *err = reinterpret_cast<const uint32_t *>(b + W.err);
-  if (wide)
-    XENT_CUDA(launch_pdl(k_xent_dx<float>, (unsigned)blocks, 256, 0, s, acc, W.split, (int64_t)n * W.acc_ld, W.acc_ld,
-                         dx ? n : 0, width, reinterpret_cast<float *>(dx), dx_ld, reinterpret_cast<float *>(dw), factor,
-                         Drop{tg, weight}, (const float *)nullptr, (const float *)nullptr, (int64_t)0, 0, err));
-  else
-    XENT_CUDA(launch_pdl(k_xent_dx<bf16>, (unsigned)blocks, 256, 0, s, acc, W.split, (int64_t)n * W.acc_ld, W.acc_ld,
-                         dx ? n : 0, width, reinterpret_cast<bf16 *>(dx), dx_ld, reinterpret_cast<bf16 *>(dw), factor,
-                         Drop{tg, weight}, (const float *)hot, reinterpret_cast<const bf16 *>(w), w_ld,
-                         ptr_aligned(w, 8) && w_ld % 4 == 0 ? 1 : 0, err));
-  return SNACK_OK;
+  return xent_gradient(S, W, x, x_ld, w, w_ld, tg, weight, Entropy{}, factor, state, dx, dx_ld, dw, dw_ld,
+                       reinterpret_cast<uint8_t *>(ws), s);
 } catch (...) {  // a host allocation failed
   return SNACK_ERR_CUDA;
 }
 
 }  // extern "C"
+
+#include "score.cuh"

@@ -43,7 +43,8 @@ struct CutArgs {
   float2 *part;  // [blocks][n] (maximum, sum of exp(z - maximum))
   float *zt;     // [n]
   // gradient
-  const float *lse, *weight;  // weight: of each row, or null
+  const float *lse, *weight;  // weight: of each row, or null; lse null: the logits themselves
+  Entropy ent;
   int32_t v0;                 // first vocabulary row of w here, which may be a piece of it
   float *dz;                  // [vocab][tokens built for],
   bf16 *dz_parts;             //  or its three bf16 parts [3][n][dz_ld], `plane` elements apart
@@ -281,16 +282,24 @@ __global__ void __launch_bounds__(kCutWarps * 32, 1) k_xent_cut(const CutArgs a)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int t = tok0 + 8 * j + 2 * q + e;
+        if (kGrad && !a.lse) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (r0 + 8 * h < a.vocab) a.dz[(r0 + 8 * h) * kTokens + t] = acc[j][2 * h + e];
+          continue;
+        }
         const uint32_t id = t < a.n ? a.targets.key(t) : a.targets.vocab;
         if (kGrad) {
           const float u = id < a.targets.vocab ? (a.weight ? a.weight[t] : 1.f) : 0.f;
-          const float lse = u != 0.f ? a.lse[t] : 0.f;
+          const float went = id < a.targets.vocab && a.ent.weight ? a.ent.weight[t] : 0.f;
+          const float lse = u != 0.f || went != 0.f ? a.lse[t] : 0.f;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int64_t r = r0 + 8 * h;
             if (r >= a.vocab) continue;
-            const float p = expf(acc[j][2 * h + e] - lse);
+            const float l = acc[j][2 * h + e] - lse, p = expf(l);
             float d = u != 0.f ? u * ((int64_t)id == a.v0 + r ? p - 1.f : p) : 0.f;
+            if (went != 0.f) d = fmaf(p, entropy_slope(0.f, went, l, a.ent.value[t]), d);
             if (!a.dz_parts) {
               a.dz[r * kTokens + t] = d;
             } else if (t < a.n) {

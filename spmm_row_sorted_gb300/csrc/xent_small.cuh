@@ -54,7 +54,8 @@ struct SmallArgs {
   float2 *part;  // [blocks][n] (maximum, sum of exp(z - maximum))
   float *zt;     // [n]
   // gradient
-  const float *lse, *weight;  // weight: of each row, or null
+  const float *lse, *weight;  // weight: of each row, or null; lse null: the logits themselves
+  Entropy ent;
   float *dz;                  // [vocab][kFewMostLogits]
 };
 
@@ -126,12 +127,16 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) k_xent_few(const SmallArg
       for (int i = threadIdx.x; i < rows * kNt; i += kSmallWarps * 32) {
         const int r = i / kNt, t = i % kNt;
         float d = 0.f;
-        if (t < a.n) {
+        if (!a.lse) {
+          d = zs[r * (kNt + 1) + t];
+        } else if (t < a.n) {
           const uint32_t id = a.targets.key(t);
-          const float g = id < a.targets.vocab ? (a.weight ? a.weight[t] : 1.f) : 0.f;
-          if (g != 0.f) {
-            const float p = expf(zs[r * (kNt + 1) + t] - a.lse[t]);
+          const bool in = id < a.targets.vocab;
+          const float g = in ? (a.weight ? a.weight[t] : 1.f) : 0.f, went = in && a.ent.weight ? a.ent.weight[t] : 0.f;
+          if (g != 0.f || went != 0.f) {
+            const float l = zs[r * (kNt + 1) + t] - a.lse[t], p = expf(l);
             d = g * ((int64_t)id == tile * kTile + r ? p - 1.f : p);
+            if (went != 0.f) d = fmaf(p, entropy_slope(0.f, went, l, a.ent.value[t]), d);
           }
         }
         a.dz[tile * kTile * kNt + i] = d;
@@ -171,7 +176,7 @@ struct SmallGrad {
   int64_t vocab, rows_per_split;
   int w_wide, dw_wide;
   TokenSrc targets;
-  const float *weight;
+  const float *weight, *went;  // of the loss and of the entropy of each row, or null
   const float *factor_a, *factor_b;  // common factor of dw: their product (null: 1)
   float *acc;                        // [splits][n][acc_ld] sums of dx
   int32_t acc_ld;
@@ -240,7 +245,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) k_xent_few_grad(const SmallGra
     for (int t = 0; t < kNt; ++t) {
       Cols<kC> &v = x[kDwOut ? t : 0];
       // rows that are left out add nothing, whatever they and the factor hold
-      const bool in = t < a.n && a.targets.key(t) < a.targets.vocab && !(a.weight && a.weight[t] == 0.f);
+      const bool in = t < a.n && a.targets.key(t) < a.targets.vocab && !(a.weight && a.weight[t] == 0.f && (!a.went || a.went[t] == 0.f));
       v.load(a.x + (in ? t : 0) * a.x_ld + c, in ? left : 0, false);
 #pragma unroll
       for (int i = 0; i < kC; ++i) v.v[i] = in ? v.v[i] * f : 0.f;

@@ -41,7 +41,8 @@ EXPORTED = ("snack_query_sizes", "snack_create", "snack_spmm_fwd", "snack_spmm_f
             "snack_trace_start", "snack_trace_read", "snack_trace_stop", "snack_embed_fwd",
             "snack_embed_grad_workspace_size", "snack_embed_grad", "snack_clip_workspace_size",
             "snack_clip_grad_norm", "snack_xent_workspace_size", "snack_xent_fwd", "snack_xent_bwd",
-            "snack_adapt_workspace_size", "snack_adapt_fwd", "snack_adapt_bwd")
+            "snack_adapt_workspace_size", "snack_adapt_fwd", "snack_adapt_bwd", "snack_score_workspace_size",
+            "snack_score_fwd", "snack_score_bwd")
 
 
 class SnackLibraryMissing(RuntimeError):
@@ -142,6 +143,12 @@ def load(path: Optional[str] = None):
         lib.snack_adapt_bwd.argtypes = [vp, i64, i64, vp, vp, i32, i32, i32, i32, st, vp, st, vp, vp, vp, i64, ctypes.c_int,
                                         vp, i64, vp, vp, vp, sz, vp]
         lib.snack_adapt_bwd.restype = st
+        lib.snack_score_workspace_size.argtypes = [vp, i64, i32, vp, i64, i64, i32, st, i32, ctypes.c_int, ctypes.POINTER(sz)]
+        lib.snack_score_workspace_size.restype = st
+        lib.snack_score_fwd.argtypes = [vp, i64, i32, vp, i64, i64, i32, st, vp, st, vp, vp, i32, vp, vp, vp, vp, sz, vp]
+        lib.snack_score_fwd.restype = st
+        lib.snack_score_bwd.argtypes = [vp, i64, i32, vp, i64, i64, i32, st, vp, st, vp, vp, vp, vp, i64, vp, i64, vp, sz, vp]
+        lib.snack_score_bwd.restype = st
         _lib = lib
         return lib
 
@@ -417,6 +424,34 @@ def snack_adapt_bwd(x, a, b, which, scales, h, dy, accumulate: bool, dx, da, db,
                                             index_code(which.dtype), _addr(scales), _addr(h), _addr(dy), dy.stride(0),
                                             1 if accumulate else 0, _addr(dx), 0 if dx is None else dx.stride(0),
                                             _addr(da), _addr(db), _addr(ws), _nbytes(ws), _raw_stream(stream)))
+
+
+def snack_score_workspace_size(x, w, top: int, grad: bool) -> int:
+    b = ctypes.c_size_t(0)
+    _check("snack_score_workspace_size",
+           (_lib or load()).snack_score_workspace_size(_addr(x), x.stride(0), x.shape[0], _addr(w), w.stride(0), w.shape[0],
+                                                       w.shape[1], dtype_code(w.dtype), top, 1 if grad else 0,
+                                                       ctypes.byref(b)))
+    return b.value
+
+
+def snack_score_fwd(x, w, targets, logp, entropy, top: int, top_ids, top_logp, state, ws, stream=None) -> None:
+    _check("snack_score_fwd",
+           (_lib or load()).snack_score_fwd(_addr(x), x.stride(0), x.shape[0], _addr(w), w.stride(0), w.shape[0], w.shape[1],
+                                            dtype_code(w.dtype), _addr(targets),
+                                            SNACK_I64 if targets is None else index_code(targets.dtype), _addr(logp),
+                                            _addr(entropy), top, _addr(top_ids), _addr(top_logp), _addr(state), _addr(ws),
+                                            _nbytes(ws), _raw_stream(stream)))
+
+
+def snack_score_bwd(x, w, targets, state, dlogp, dentropy, dx, dw, ws, stream=None) -> None:
+    _check("snack_score_bwd",
+           (_lib or load()).snack_score_bwd(_addr(x), x.stride(0), x.shape[0], _addr(w), w.stride(0), w.shape[0], w.shape[1],
+                                            dtype_code(w.dtype), _addr(targets),
+                                            SNACK_I64 if targets is None else index_code(targets.dtype), _addr(state),
+                                            _addr(dlogp), _addr(dentropy), _addr(dx), 0 if dx is None else dx.stride(0),
+                                            _addr(dw), 0 if dw is None else dw.stride(0), _addr(ws), _nbytes(ws),
+                                            _raw_stream(stream)))
 
 
 # ------------------------------------------------------------- layer owner
@@ -845,6 +880,107 @@ class _XentFn(torch.autograd.Function):
 def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, reduction: str = "mean"):
     """Autograd-aware xent: the loss alone; gradients flow to x and w."""
     return _XentFn.apply(x, w, targets, reduction)
+
+
+@functools.lru_cache(maxsize=256)
+def _score_ws(device: int, x_bits: int, x_ld: int, n: int, w_bits: int, w_ld: int, vocab: int, width: int, t: int, top: int,
+              grad: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check("snack_score_workspace_size",
+           load().snack_score_workspace_size(x_bits, x_ld, n, w_bits, w_ld, vocab, width, t, top, grad, ctypes.byref(b)))
+    return b.value
+
+
+def _score_args(x, w, targets, top, grad):
+    """What both calls take of x, w and targets, and a workspace; and what to keep alive."""
+    x, xa, n, width, x_ld = _matrix(x)
+    w, wa, vocab, w_width, w_ld = _matrix(w)
+    kind = w.dtype
+    if width != w_width or x.dtype != kind:
+        raise ValueError("x [n, width] and w [vocab, width] must have one type and width")
+    ids, ids_t = None, SNACK_I64
+    if targets is not None:
+        if targets.numel() != n:
+            raise ValueError("targets needs one entry per row of x")
+        targets = targets.contiguous()
+        ids, ids_t = targets.data_ptr(), _code(_INDICES, targets.dtype)
+    code = _code(_DTYPES, kind)
+    nbytes = max(256, _score_ws(x.get_device(), xa % 256, x_ld, n, wa % 256, w_ld, vocab, width, code, top, grad))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    return (xa, x_ld, n, wa, w_ld, vocab, width, code, ids, ids_t), ws, nbytes, (x, w, targets)
+
+
+def score(x: torch.Tensor, w: torch.Tensor, targets: Optional[torch.Tensor] = None, top: int = 0, stream=None):
+    """Log probabilities of targets under softmax(x w^T), entropies, likeliest tokens: (logp, entropy, ids, top_logp, state).
+
+    logp is None without targets; ids (int64, [n, top], likeliest first, of equal
+    logits the lower id) and top_logp are None where top is 0.  A row whose target is
+    outside the vocabulary (such as -100) is not scored: its results are 0, its ids
+    -1.  state (float32, [2, n]) is what score_grad needs beside the same arguments.
+    """
+    if not _here(x, stream, w, targets):
+        with _On(x.device, stream):
+            return score(x, w, targets, top)
+    top = int(top)
+    args, ws, nbytes, kept = _score_args(x, w, targets, top, 0)
+    n, dev = args[2], x.device
+    logp = torch.empty(n, dtype=torch.float32, device=dev) if targets is not None else None
+    entropy = torch.empty(n, dtype=torch.float32, device=dev)
+    ids = torch.empty((n, top), dtype=torch.int64, device=dev) if top else None
+    top_logp = torch.empty((n, top), dtype=torch.float32, device=dev) if top else None
+    state = torch.empty((2, n), dtype=torch.float32, device=dev)
+    st = (_lib or load()).snack_score_fwd(*args, _addr(logp), entropy.data_ptr(), top, _addr(ids), _addr(top_logp),
+                                          state.data_ptr(), ws.data_ptr(), nbytes, _raw_stream(None))
+    if st:
+        _check("snack_score_fwd", st)
+    return logp, entropy, ids, top_logp, state
+
+
+def score_grad(x: torch.Tensor, w: torch.Tensor, targets: Optional[torch.Tensor], state: torch.Tensor,
+               dlogp: Optional[torch.Tensor] = None, dentropy: Optional[torch.Tensor] = None, want_dx: bool = True,
+               want_dw: bool = True, stream=None):
+    """(dx, dw) of score for upstream gradients of its log probabilities and entropies (None: 0)."""
+    if not _here(x, stream, w, targets, state, dlogp, dentropy):
+        with _On(x.device, stream):
+            return score_grad(x, w, targets, state, dlogp, dentropy, want_dx, want_dw)
+    args, ws, nbytes, kept = _score_args(x, w, targets, 0, 1)
+    n, vocab, width, kind, dev = args[2], args[5], args[6], x.dtype, x.device
+    if state.dtype != torch.float32 or tuple(state.shape) != (2, n) or not state.is_contiguous():
+        raise ValueError("state must be what score returned for these arguments")
+    if targets is None and dlogp is not None:
+        raise ValueError("dlogp needs targets")
+    up = []
+    for d in (dlogp, dentropy):
+        if d is not None and d.numel() != n:
+            raise ValueError("dlogp and dentropy need one entry per row of x")
+        up.append(None if d is None else d.contiguous().float())
+    dx = torch.empty((n, width), dtype=kind, device=dev) if want_dx else None
+    dw = torch.empty((vocab, width), dtype=kind, device=dev) if want_dw else None
+    st = (_lib or load()).snack_score_bwd(*args, state.data_ptr(), _addr(up[0]), _addr(up[1]), _addr(dx), width, _addr(dw),
+                                          width, ws.data_ptr(), nbytes, _raw_stream(None))
+    if st:
+        _check("snack_score_bwd", st)
+    return dx, dw
+
+
+class _ScoreFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, targets):
+        logp, entropy, _, _, state = score(x, w, targets)
+        ctx.save_for_backward(x, w, targets, state)
+        return logp, entropy
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dlogp, dentropy):
+        x, w, targets, state = ctx.saved_tensors
+        dx, dw = score_grad(x, w, targets, state, dlogp, dentropy, ctx.needs_input_grad[0], ctx.needs_input_grad[1])
+        return dx, dw, None
+
+
+def token_logprobs(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor):
+    """Autograd-aware score: (log probabilities of targets, entropies); gradients flow to x and w."""
+    return _ScoreFn.apply(x, w, targets)
 
 
 _adapt_ws = functools.lru_cache(maxsize=256)(snack_adapt_workspace_size)
