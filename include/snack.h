@@ -455,7 +455,7 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
  * last one asked for are that close to it).  A row with a NaN or an infinite largest
  * logit has NaN results; its ids are some of the vocabulary.  state (2 n values: each
  * row's lse and entropy) is kept for the gradient.  With top the workspace holds up to
- * 256 MB of logits at a time (1024 columns at least); the other sizes are as for
+ * a gigabyte of logits at a time (1024 columns at least); the other sizes are as for
  * snack_xent_workspace_size.
  */
 snack_status snack_score_workspace_size(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld,

@@ -102,7 +102,7 @@ struct FinishArgs {
   int32_t top, keep, groups, rows, v0;
   const float *high, *z;
   int64_t high_ld, z_row, z_col;  // steps of a logit's row and column
-  float2 *list;                   // [n][32] what is kept from piece to piece: logit, id
+  unsigned long long *list;       // [n][32] what is kept from piece to piece
   int first, last;
   TargetLogit at;                 // x and w
   // statistics
@@ -116,51 +116,49 @@ struct FinishArgs {
   const uint32_t *err;
 };
 
-// a before b: larger, of equal ones with the lower id
-__device__ __forceinline__ bool precedes(float a, int ia, float b, int ib) { return a > b || (a == b && ia < ib); }
+// A logit and its id as one number, in the order of the likeliest: larger logits, of
+// equal ones lower ids (0: none).  NaN counts as the lowest logit, -0 as 0.
+typedef unsigned long long Key;
+__device__ __forceinline__ Key key_of(float v, int id) {
+  const uint32_t u = __float_as_uint((isnan(v) ? -INFINITY : v) + 0.f);
+  return ((Key)(u & 0x80000000u ? ~u : u | 0x80000000u) << 32) | (uint32_t)~id;
+}
+__device__ __forceinline__ float key_value(Key k) {
+  const uint32_t u = (uint32_t)(k >> 32);
+  return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+__device__ __forceinline__ int key_id(Key k) { return (int)~(uint32_t)k; }
 
-// A warp's list, sorted: lane l has the l-th.
-struct Best {
-  float v;
-  int id;
-  __device__ __forceinline__ void clear() {
-    v = -INFINITY;
-    id = kNoId;
+// Lists of 32 keys, lane l has the l-th largest; all of a converged warp.
+__device__ __forceinline__ Key swap_step(Key k, int d, bool larger) {
+  const Key o = __shfl_xor_sync(0xffffffffu, k, d);
+  return larger == (k > o) ? k : o;
+}
+__device__ __forceinline__ Key sorted(Key k, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+    for (int d = size / 2; d; d /= 2) k = swap_step(k, d, ((lane & d) == 0) == ((lane & size) == 0 || size == 32));
+  return k;
+}
+// the 32 largest of two sorted lists
+__device__ __forceinline__ Key joined(Key a, Key b, int lane) {
+  const Key o = __shfl_sync(0xffffffffu, b, 31 - lane);
+  Key k = a > o ? a : o;
+#pragma unroll
+  for (int d = 16; d; d /= 2) k = swap_step(k, d, (lane & d) == 0);
+  return k;
+}
+// the list with what each lane has to offer, if that is among its first `keep`
+__device__ __forceinline__ Key offered(Key list, Key k, int keep, int lane) {
+  unsigned m = __ballot_sync(0xffffffffu, k > __shfl_sync(0xffffffffu, list, keep - 1));
+  if (__popc(m) > 4) return joined(list, sorted(k, lane), lane);
+  for (; m; m &= m - 1) {
+    const Key n = __shfl_sync(0xffffffffu, k, __ffs(m) - 1), up = __shfl_up_sync(0xffffffffu, list, 1);
+    const int at = __popc(__ballot_sync(0xffffffffu, list > n));
+    list = lane < at ? list : lane == at ? n : up;
   }
-  __device__ __forceinline__ void insert(float nv, int nid, int lane) {
-    const int at = __popc(__ballot_sync(0xffffffffu, precedes(v, id, nv, nid)));
-    const float uv = __shfl_up_sync(0xffffffffu, v, 1);
-    const int uid = __shfl_up_sync(0xffffffffu, id, 1);
-    if (lane == at) {
-      v = nv;
-      id = nid;
-    } else if (lane > at) {
-      v = uv;
-      id = uid;
-    }
-  }
-  // what each lane has to offer (id kNoId: nothing)
-  __device__ __forceinline__ void offer(float ov, int oid, int keep, int lane) {
-    for (;;) {
-      const float lv = __shfl_sync(0xffffffffu, v, keep - 1);
-      const int lid = __shfl_sync(0xffffffffu, id, keep - 1);
-      const unsigned m = __ballot_sync(0xffffffffu, oid != kNoId && precedes(ov, oid, lv, lid));
-      if (!m) return;
-      const int from = __ffs(m) - 1;
-      insert(__shfl_sync(0xffffffffu, ov, from), __shfl_sync(0xffffffffu, oid, from), lane);
-      if (lane == from) oid = kNoId;
-    }
-  }
-};
-__device__ __forceinline__ float no_nan(float v) { return isnan(v) ? -INFINITY : v; }
-
-// The block's lists into warp 0's.
-__device__ __forceinline__ void join_lists(Best &b, float2 (&lists)[kFinishWarps][32], int keep, int warp, int lane) {
-  lists[warp][lane] = make_float2(b.v, __int_as_float(b.id));
-  __syncthreads();
-  if (warp == 0)
-    for (int w = 1; w < kFinishWarps; ++w) b.offer(lists[w][lane].x, __float_as_int(lists[w][lane].y), keep, lane);
-  __syncthreads();
+  return list;
 }
 
 // hi + lo += a * b, to about twice fp32's precision
@@ -192,10 +190,12 @@ __device__ __forceinline__ double long_logit(const TargetLogit &at, int64_t row,
 // A block per row.
 __global__ void __launch_bounds__(kFinishWarps * 32) k_score_finish(const FinishArgs a) {
   pdl_wait();
-  __shared__ float2 lists[kFinishWarps][32];
+  __shared__ Key lists[kFinishWarps][32];
+  __shared__ Key found[(kMostTop + kKeepMore) * 32];
   __shared__ float4 sums[kFinishWarps];
   __shared__ double exact[32];
   __shared__ unsigned again;
+  __shared__ int n_found;
   const int64_t row = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool bad = a.last && any_error(a.err);
@@ -215,44 +215,57 @@ __global__ void __launch_bounds__(kFinishWarps * 32) k_score_finish(const Finish
     }
     return;
   }
-  Best b;
+  Key list = 0;
   if (a.top) {
     // the groups with the largest maxima
-    b.clear();
+    constexpr int kAhead = 8;  // loads in flight
     const float *high = a.high + row * a.high_ld;
-    for (int g = warp * 32; g < a.groups; g += kFinishWarps * 32) {
-      const bool in = g + lane < a.groups;
-      b.offer(in ? no_nan(__ldg(high + g + lane)) : 0.f, in ? g + lane : kNoId, a.keep, lane);
+    for (int g0 = warp * 32; g0 < a.groups; g0 += kFinishWarps * 32 * kAhead) {
+      float v[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int g = g0 + u * kFinishWarps * 32 + lane;
+        v[u] = g < a.groups ? __ldg(high + g) : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int g = g0 + u * kFinishWarps * 32 + lane;
+        if (g - lane >= a.groups) break;
+        list = offered(list, g < a.groups ? key_of(v[u], g) : 0, a.keep, lane);
+      }
     }
-    join_lists(b, lists, a.keep, warp, lane);
-    if (warp == 0) lists[0][lane] = make_float2(b.v, __int_as_float(b.id));
+    lists[warp][lane] = list;
+    if (threadIdx.x == 0) n_found = 0;
     __syncthreads();
-    // and the largest of their logits: none below the last group's maximum
+    if (warp == 0) {
+#pragma unroll
+      for (int w = 1; w < kFinishWarps; ++w) list = joined(list, lists[w][lane], lane);
+      lists[0][lane] = list;
+    }
+    __syncthreads();
+    // and of their logits those that are not below the last group's maximum
     constexpr int kMost = (kMostTop + kKeepMore + kFinishWarps - 1) / kFinishWarps;
-    const float least = lists[0][a.keep - 1].x;
-    float v[kMost];
-    int col[kMost];
+    const Key last_group = lists[0][a.keep - 1];
+    const Key least = last_group ? key_of(key_value(last_group), kNoId) : 0;
+    Key k[kMost];
 #pragma unroll
     for (int u = 0; u < kMost; ++u) {
       const int i = warp + u * kFinishWarps;
-      const int g = i < a.keep ? __float_as_int(lists[0][i].y) : kNoId;
-      col[u] = g != kNoId && g * 32 + lane < a.rows ? g * 32 + lane : -1;
-      v[u] = col[u] >= 0 ? no_nan(__ldg(a.z + row * a.z_row + col[u] * a.z_col)) : 0.f;
-    }
-    __syncthreads();
-    b.clear();
-    if (warp == 0 && !a.first) {
-      const float2 e = a.list[row * 32 + lane];
-      b.v = e.x;
-      b.id = __float_as_int(e.y);
+      const Key of = i < a.keep ? lists[0][i] : 0;
+      const int col = of ? key_id(of) * 32 + lane : a.rows;
+      k[u] = col < a.rows ? key_of(__ldg(a.z + row * a.z_row + col * a.z_col), a.v0 + col) : 0;
     }
 #pragma unroll
-    for (int u = 0; u < kMost; ++u) b.offer(v[u], col[u] >= 0 && v[u] >= least ? a.v0 + col[u] : kNoId, a.keep, lane);
-    join_lists(b, lists, a.keep, warp, lane);
-    if (!a.last) {
-      if (warp == 0) a.list[row * 32 + lane] = make_float2(b.v, __int_as_float(b.id));
-      return;
+    for (int u = 0; u < kMost; ++u)
+      if (k[u] && k[u] >= least) found[atomicAdd(&n_found, 1)] = k[u];  // their order does not matter
+    __syncthreads();
+    if (warp == 0) {
+      list = 0;
+      if (!a.first) list = a.list[row * 32 + lane];
+      for (int i = 0; i < n_found; i += 32) list = offered(list, i + lane < n_found ? found[i + lane] : 0, a.keep, lane);
+      if (!a.last) a.list[row * 32 + lane] = list;
     }
+    if (!a.last) return;
   }
   // the row's statistics
   float4 s = make_float4(-INFINITY, 0.f, 0.f, 0.f);
@@ -268,25 +281,25 @@ __global__ void __launch_bounds__(kFinishWarps * 32) k_score_finish(const Finish
   }
   if (lane == 0) sums[warp] = s;
   if (a.top && warp == 0) {  // which of the list are too close to tell
-    const float above = __shfl_up_sync(0xffffffffu, b.v, 1);
-    float size = lane < a.keep && isfinite(b.v) ? fabsf(b.v) : 0.f;
+    const float mine = list ? key_value(list) : -INFINITY, above = __shfl_up_sync(0xffffffffu, mine, 1);
+    float size = lane < a.keep && isfinite(mine) ? fabsf(mine) : 0.f;
 #pragma unroll
     for (int d = 16; d; d >>= 1) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, d));
-    const bool close = lane > 0 && lane < a.keep && b.id != kNoId && above - b.v <= size * 0x1p-12f;  // not of two infinities
-    const unsigned joined = __ballot_sync(0xffffffffu, close);  // bit l: l goes with l - 1
+    const bool close = lane > 0 && lane < a.keep && list && above - mine <= size * 0x1p-12f;  // not of two infinities
+    const unsigned with = __ballot_sync(0xffffffffu, close);  // bit l: l goes with l - 1
     // a run of them that begins before place `top`
-    const int begin = 31 - __clz(~joined & (0xffffffffu >> (31 - lane)));
-    const bool run = close || (lane < 31 && (joined >> (lane + 1)) & 1);
+    const int begin = 31 - __clz(~with & (0xffffffffu >> (31 - lane)));
+    const bool run = close || (lane < 31 && (with >> (lane + 1)) & 1);
     const unsigned m = __ballot_sync(0xffffffffu, run && begin < a.top);
     if (lane == 0) again = m;
-    lists[0][lane] = make_float2(b.v, __int_as_float(b.id));
+    lists[0][lane] = list;
   }
   __syncthreads();
   if (a.top) {
     int k = 0;
     for (unsigned m = again; m; m &= m - 1, ++k) {
       if (k % kFinishWarps != warp) continue;
-      const int i = __ffs(m) - 1, id = __float_as_int(lists[0][i].y);
+      const int i = __ffs(m) - 1, id = key_id(lists[0][i]);
       const double l = a.at.bf ? long_logit<bf16>(a.at, row, id, lane) : long_logit<float>(a.at, row, id, lane);
       if (lane == 0) exact[i] = l;
     }
@@ -319,34 +332,72 @@ __global__ void __launch_bounds__(kFinishWarps * 32) k_score_finish(const Finish
     a.kept_entropy[row] = entropy;
   }
   if (!a.top) return;
-  double l = b.v;
+  const int id = key_id(list);
+  double l = key_value(list);
   if ((again >> lane) & 1 && isfinite(exact[lane])) l = exact[lane];
   int place = 0;
   for (int j = 0; j < a.keep; ++j) {
     const double lj = __shfl_sync(0xffffffffu, l, j);
-    const int ij = __shfl_sync(0xffffffffu, b.id, j);
-    place += lj > l || (lj == l && ij < b.id) ? 1 : 0;
+    const int ij = __shfl_sync(0xffffffffu, id, j);
+    place += lj > l || (lj == l && ij < id) ? 1 : 0;
   }
   if (lane < a.keep && place < a.top) {
-    const float own = given && b.id == (int)target ? logp : ((float)l - high) - log_sum;
-    a.top_ids[row * a.top + place] = b.id;
+    const float own = given && id == (int)target ? logp : ((float)l - high) - log_sum;
+    a.top_ids[row * a.top + place] = id;
     a.top_logp[row * a.top + place] = own;
   }
 }
 
 // The gradients' weights as the loss's: of the log probability's negative, and of the
-// entropy; and targets where none are given.
+// entropy; targets where none are given; and which rows of x have which target.
 __global__ void __launch_bounds__(256) k_score_weights(int32_t n, const float *__restrict__ dlogp, const float *__restrict__ dentropy,
-                                                       float *__restrict__ weight, float *__restrict__ went, int32_t *__restrict__ ids) {
+                                                       float *__restrict__ weight, float *__restrict__ went, int32_t *__restrict__ ids,
+                                                       TokenSrc targets, const Hits hits) {
   pdl_wait();
   const int i = blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
-  weight[i] = dlogp ? -dlogp[i] : 0.f;
-  went[i] = dentropy ? -dentropy[i] : 0.f;
-  if (ids) ids[i] = 0;
+  const float g = dlogp ? -dlogp[i] : 0.f, h = dentropy ? -dentropy[i] : 0.f;
+  weight[i] = g;
+  went[i] = h;
+  if (ids) {
+    ids[i] = 0;
+  } else if (hits.first && g != 0.f) {
+    const uint32_t id = targets.key(i);
+    if (id < targets.vocab) {
+      atomicMin(hits.first + id, i);
+      atomicMax(hits.last + id, i);
+    }
+  }
 }
 
 // ------------------------------------------------------------ host side
+
+// What the gradient takes besides the loss's: weights and targets, and for bf16 the
+// targets' rows of dw.
+struct ScoreGradWs {
+  size_t weight, went, ids, first, last, rows, total;
+  int64_t rows_ld;
+};
+ScoreGradWs score_grad_ws(const XentShape &s, const XentWs &x) {
+  ScoreGradWs w = {};
+  size_t o = x.total;
+  auto take = [&o](size_t bytes) {
+    const size_t at = o;
+    o += align_up(bytes, kAlign);
+    return at;
+  };
+  w.weight = take((size_t)s.n * 4);
+  w.went = take((size_t)s.n * 4);
+  w.ids = take((size_t)s.n * 4);
+  if (s.t == SNACK_BF16) {
+    w.first = take((size_t)s.vocab * 4);
+    w.last = take((size_t)s.vocab * 4);
+    w.rows_ld = (int64_t)align_up((size_t)s.width, 4);
+    w.rows = take((size_t)s.n * (size_t)w.rows_ld * 4);
+  }
+  w.total = o;
+  return w;
+}
 
 struct ScoreWs {
   size_t err, zt, xp, wp, z, stats, high, list, total;
@@ -373,7 +424,8 @@ ScoreWs score_ws(const XentShape &s, int32_t top) {
     w.high_ld = w.slots = ceil_div(s.vocab, 32);
     w.z = take((size_t)s.vocab * (size_t)w.tokens * 4);
   } else {
-    const int64_t w_row = (int64_t)s.parts * s.ld * 2, row = std::max(s.pack_w ? w_row : 0, top ? (int64_t)s.n * 4 : 0);
+    // logits a gigabyte at a time, w's copies a quarter of that
+    const int64_t w_row = (int64_t)s.parts * s.ld * 2, row = std::max(s.pack_w ? w_row : 0, top ? (int64_t)s.n : 0);
     if (s.pack_x) w.xp = take((size_t)s.parts * (size_t)s.n * (size_t)s.ld * 2);
     w.piece = row ? piece_rows(s.vocab, row, m_tiles, s.sms) : s.vocab;
     if (w.piece > s.vocab) w.piece = s.vocab;
@@ -417,7 +469,7 @@ snack_status snack_score_workspace_size(const void *x, int64_t x_ld, int32_t n, 
   if (top < 0 || top > vocab) return SNACK_ERR_INVALID_ARG;
   if (top > kMostTop) return SNACK_ERR_UNSUPPORTED;
   const XentShape S = xent_shape(x, x_ld, n, w, w_ld, vocab, width, t, grad != 0);
-  *bytes = n == 0 ? 0 : grad ? xent_ws(S, true).total + 3 * align_up((size_t)n * 4, kAlign) : score_ws(S, top).total;
+  *bytes = n == 0 ? 0 : grad ? score_grad_ws(S, xent_ws(S, true)).total : score_ws(S, top).total;
   return SNACK_OK;
 }
 
@@ -458,7 +510,7 @@ snack_status snack_score_fwd(const void *x, int64_t x_ld, int32_t n, const void 
   f.high = top ? reinterpret_cast<const float *>(b + W.high) : nullptr;
   f.high_ld = W.high_ld;
   f.z = reinterpret_cast<const float *>(b + W.z);
-  f.list = reinterpret_cast<float2 *>(b + W.list);
+  f.list = reinterpret_cast<unsigned long long *>(b + W.list);
   f.first = f.last = 1;
   f.at = target_logit(S, x, x_ld, w, w_ld);
   f.stats = reinterpret_cast<const float4 *>(b + W.stats);
@@ -547,22 +599,28 @@ snack_status snack_score_bwd(const void *x, int64_t x_ld, int32_t n, const void 
     return SNACK_ERR_INVALID_ARG;
   const XentShape S = xent_shape(x, x_ld, n, w, w_ld, vocab, width, t, true);
   const XentWs W = xent_ws(S, true);
-  const size_t each = align_up((size_t)n * 4, kAlign), total = W.total + 3 * each;
+  const ScoreGradWs E = score_grad_ws(S, W);
   const Span written[] = {{dx, dx ? span_bytes(n, width, dx_ld, es) : 0}, {dw, dw ? span_bytes(vocab, width, dw_ld, es) : 0},
-                          {ws, std::min(ws_bytes, total)}};
+                          {ws, std::min(ws_bytes, E.total)}};
   const Span read[] = {{x, span_bytes(n, width, x_ld, es)}, {w, span_bytes(vocab, width, w_ld, es)},
                        {targets, targets ? (size_t)n * index_size(targets_t) : 0}, {state, (size_t)n * 8},
                        {dlogp, dlogp ? (size_t)n * 4 : 0}, {dentropy, dentropy ? (size_t)n * 4 : 0}};
   if (any_overlap(written, read)) return SNACK_ERR_INVALID_ARG;
-  if (ws_bytes < total) return SNACK_ERR_WORKSPACE;
+  if (ws_bytes < E.total) return SNACK_ERR_WORKSPACE;
   if (!dx && !dw) return SNACK_OK;
-  uint8_t *extra = reinterpret_cast<uint8_t *>(ws) + W.total;
-  float *weight = reinterpret_cast<float *>(extra), *went = reinterpret_cast<float *>(extra + each);
-  int32_t *ids = targets ? nullptr : reinterpret_cast<int32_t *>(extra + 2 * each);
-  XENT_CUDA(launch_pdl(k_score_weights, (unsigned)ceil_div(n, 256), 256, 0, s, n, dlogp, dentropy, weight, went, ids));
+  uint8_t *b = reinterpret_cast<uint8_t *>(ws);
+  float *weight = reinterpret_cast<float *>(b + E.weight), *went = reinterpret_cast<float *>(b + E.went);
+  int32_t *ids = targets ? nullptr : reinterpret_cast<int32_t *>(b + E.ids);
+  Hits hits = {};
+  if (t == SNACK_BF16 && dw && dlogp) {
+    hits = {reinterpret_cast<int32_t *>(b + E.first), reinterpret_cast<int32_t *>(b + E.last), reinterpret_cast<float *>(b + E.rows), E.rows_ld};
+    XENT_CUDA(cudaMemsetAsync(hits.first, 0x7F, (size_t)vocab * 4, s));  // above every row
+    XENT_CUDA(cudaMemsetAsync(hits.last, 0, (size_t)vocab * 4, s));
+  }
   const TokenSrc tg = targets ? TokenSrc{targets, targets_t == SNACK_I64, (uint32_t)vocab} : TokenSrc{ids, 0, (uint32_t)vocab};
-  return xent_gradient(S, W, x, x_ld, w, w_ld, tg, weight, Entropy{went, state + n}, Factor{nullptr, nullptr}, state, dx, dx_ld, dw,
-                       dw_ld, reinterpret_cast<uint8_t *>(ws), s);
+  XENT_CUDA(launch_pdl(k_score_weights, (unsigned)ceil_div(n, 256), 256, 0, s, n, dlogp, dentropy, weight, went, ids, tg, hits));
+  return xent_gradient(S, W, x, x_ld, w, w_ld, tg, weight, Entropy{went, state + n}, hits, Factor{nullptr, nullptr}, state, dx, dx_ld, dw,
+                       dw_ld, b, s);
 } catch (...) {  // a host allocation failed
   return SNACK_ERR_CUDA;
 }

@@ -250,6 +250,13 @@ struct Factor {
   __device__ __forceinline__ float get() const { return (a ? *a : 1.f) * (b ? *b : 1.f); }
 };
 
+// The vocabulary rows that are targets, for the rows of dw that are finished apart (score.cuh).
+struct Hits {
+  int32_t *first, *last;  // [vocab] the first and the last row of x with the target (first: beyond all rows, if none); null: none
+  float *rows;            // [n][ld] such a row's sums, at its first row of x
+  int64_t ld;
+};
+
 struct GemmArgs {
   int32_t m, n;             // rows and columns of the product
   int32_t nt;               // columns of a tile: a multiple of 32 (128 or 256 where B is MN-major)
@@ -283,6 +290,7 @@ struct GemmArgs {
   int64_t out_ld;
   int32_t out_wide;         // fp32 (else bf16)
   int32_t out_tma;
+  Hits hits;
   // score
   float4 *stats;            // [m][slots] (maximum, how often, sum of exp(z - maximum) of the others, sum of it times z - maximum)
   float *high;              // [m][high_ld] maximum of 32 neighbouring logits each, or null: then no logits are kept
@@ -726,6 +734,18 @@ __device__ __forceinline__ void product(const CUtensorMap &map_a, const CUtensor
           for (int h = 0; h < kChunks; ++h)
 #pragma unroll
             for (int j = 0; j < 32; ++j) acc[h][j] *= f;
+          if (P.hits.first) {
+            const int first = row_ok ? P.hits.first[P.v0 + row] : P.tokens;
+            if (first < P.tokens) {
+              float *to = P.hits.rows + (int64_t)first * P.hits.ld + col0;
+#pragma unroll
+              for (int h = 0; h < kChunks; ++h)
+#pragma unroll
+                for (int j = 0; j < 32; j += 4)
+                  if (32 * h < c_end && col0 + 32 * h + j < P.n)
+                    *reinterpret_cast<float4 *>(to + 32 * h + j) = make_float4(acc[h][j], acc[h][j + 1], acc[h][j + 2], acc[h][j + 3]);
+            }
+          }
         }
         const int step = wide ? 32 : 64;  // columns of 128 bytes
 #pragma unroll
@@ -1088,6 +1108,70 @@ __global__ void __launch_bounds__(256) k_xent_rows(const bf16 *__restrict__ in, 
   }
   if (lane == 0 && shift) row[0] = single[0];
   if (lane == 1 && shift + 2 * words < width) row[width - 1] = single[width - 1];
+}
+
+// The rows of dw that are targets: their sums, with what rounding dz to bf16 lost of its
+// entries there, mostly by far the largest: for each row of x with the target, in their
+// order, that much of it.  A block per row of x, at work for the first of each target.
+__global__ void __launch_bounds__(128) k_xent_hits(const Hits hits, TokenSrc targets, int32_t n, const float *__restrict__ hot,
+                                                   const bf16 *__restrict__ x, int64_t x_ld, int32_t width, bf16 *__restrict__ dw,
+                                                   int64_t dw_ld, int wide) {
+  pdl_wait();
+  __shared__ int rows[128];
+  __shared__ int counts[4];
+  const int i = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t id = targets.key(i);
+  if (id >= targets.vocab || hits.first[id] != i) return;
+  const int last = hits.last[id];
+  const int c = blockIdx.y * 1024 + threadIdx.x * 8;
+  float acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; j += 4) {
+    const float4 v = c + j < width ? *reinterpret_cast<const float4 *>(hits.rows + (int64_t)i * hits.ld + c + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+    acc[j] = v.x;
+    acc[j + 1] = v.y;
+    acc[j + 2] = v.z;
+    acc[j + 3] = v.w;
+  }
+  for (int r0 = i; r0 <= last; r0 += 128) {
+    const int r = r0 + threadIdx.x;
+    const bool here = r <= last && targets.key(r) == id;
+    const unsigned m = __ballot_sync(0xffffffffu, here);
+    if (lane == 0) counts[warp] = __popc(m);
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (w < warp) before += counts[w];
+      all += counts[w];
+    }
+    if (here) rows[before + __popc(m & ((1u << lane) - 1u))] = r;
+    __syncthreads();
+    if (c < width) {
+#pragma unroll 4
+      for (int k = 0; k < all; ++k) {
+        const float h = hot[rows[k]], over = h - __bfloat162float(__float2bfloat16_rn(h));
+        Pack<bf16, 16> v;
+        v.raw = __ldg(reinterpret_cast<const uint4 *>(x + rows[k] * x_ld + c));
+        if (over != 0.f)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] = fmaf(over, v.get(j), acc[j]);
+      }
+    }
+    __syncthreads();
+  }
+  if (c >= width) return;
+  bf16 *to = dw + (int64_t)id * dw_ld + c;
+  if (wide && c + 8 <= width) {
+    Pack<bf16, 16> o;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o.set(j, acc[j]);
+    *reinterpret_cast<uint4 *>(to) = o.raw;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < width) to[j] = __float2bfloat16_rn(acc[j]);
+  }
 }
 
 // dx = the splits' sums, added in order and rounded once; rows that are left out
@@ -1616,9 +1700,9 @@ bool any_overlap(const Span (&written)[kWritten], const Span (&read)[kRead]) {
 
 // The gradients of a loss whose dz[i, v] is weight[i] (1 where weight is null) times
 // (p - [v = target]), and with ent weights of the rows' entropies besides, all times
-// factor.  state: the rows' log sums of exponentials.
+// factor.  state: the rows' log sums of exponentials.  hits: rows of dw to keep.
 snack_status xent_gradient(const XentShape &S, const XentWs &W, const void *x, int64_t x_ld, const void *w, int64_t w_ld,
-                           const TokenSrc &tg, const float *weight, const Entropy &ent, const Factor &factor,
+                           const TokenSrc &tg, const float *weight, const Entropy &ent, const Hits &hits, const Factor &factor,
                            const float *state, void *dx, int64_t dx_ld, void *dw, int64_t dw_ld, uint8_t *b, cudaStream_t s) {
   const int32_t n = S.n, width = S.width;
   const int64_t vocab = S.vocab;
@@ -1745,6 +1829,8 @@ snack_status xent_gradient(const XentShape &S, const XentWs &W, const void *x, i
       uint8_t *out = by_ws ? b + W.dwp : to;
       const int64_t out_ld = by_ws ? S.ld : dw_ld;
       h.out = out;
+      h.v0 = (int32_t)v0;
+      h.hits = hits;
       h.factor = factor;
       h.targets = tg;
       h.tokens = n;
@@ -1761,6 +1847,10 @@ snack_status xent_gradient(const XentShape &S, const XentWs &W, const void *x, i
                              out_ld, rows, width, reinterpret_cast<bf16 *>(to), dw_ld));
     }
   }
+  if (dw && hits.first)
+    XENT_CUDA(launch_pdl(k_xent_hits, dim3((unsigned)n, (unsigned)ceil_div(width, 1024)), 128, 0, s, hits, tg, n, (const float *)hot,
+                         reinterpret_cast<const bf16 *>(ox.p), ox.ld, width, reinterpret_cast<bf16 *>(dw), dw_ld,
+                         ptr_aligned(dw, 16) && dw_ld % 8 == 0 ? 1 : 0));
   const int64_t total = dx ? (int64_t)n * (W.acc_ld / 4) : 0;
   int64_t blocks = ceil_div(total, 256);
   if (blocks > (int64_t)S.sms * 16) blocks = (int64_t)S.sms * 16;
@@ -1899,7 +1989,7 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
   const TokenSrc tg{targets, targets_t == SNACK_I64, (uint32_t)vocab};
   const float *weight = reduction == SNACK_NONE ? dloss : nullptr;
   const Factor factor = {reduction == SNACK_NONE ? nullptr : dloss, reduction == SNACK_MEAN ? state + n : nullptr};
-  return xent_gradient(S, W, x, x_ld, w, w_ld, tg, weight, Entropy{}, factor, state, dx, dx_ld, dw, dw_ld,
+  return xent_gradient(S, W, x, x_ld, w, w_ld, tg, weight, Entropy{}, Hits{}, factor, state, dx, dx_ld, dw, dw_ld,
                        reinterpret_cast<uint8_t *>(ws), s);
 } catch (...) {  // a host allocation failed
   return SNACK_ERR_CUDA;

@@ -88,7 +88,7 @@ def test_score_workspace_follows_the_shapes(lib):
     assert size(lib, top=1)[1] >= base + 100 * 1000 * 4      # the logits
     assert size(lib, top=24)[1] == size(lib, top=1)[1]
     assert size(lib, x_ld=65)[1] > base                      # rows off 16 bytes are laid out again
-    assert size(lib, n=8192, vocab=1 << 17, top=8)[1] < (700 << 20)  # a piece of the logits at a time
+    assert size(lib, n=8192, vocab=1 << 17, top=8)[1] < (1500 << 20)  # a piece of the logits at a time
     assert size(lib, grad=1)[1] > size(lib, n=1, grad=1)[1]
     for bad, status in ((dict(top=-1), 1), (dict(top=1001), 1), (dict(top=25), 7), (dict(t=4), 1), (dict(n=-1), 1), (dict(vocab=1 << 30), 7)):
         assert size(lib, **bad)[0] == status
