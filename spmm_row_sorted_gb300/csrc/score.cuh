@@ -29,6 +29,7 @@ constexpr int kMostTop = 24;
 constexpr int kKeepMore = 8;
 constexpr int kFinishWarps = 4;
 constexpr int kNoId = 0x7FFFFFFF;
+constexpr int kFound = (kMostTop + kKeepMore) * 32;  // all logits of the groups that are looked at
 
 // ------------------------------------------------------------ statistics
 
@@ -191,10 +192,11 @@ __device__ __forceinline__ double long_logit(const TargetLogit &at, int64_t row,
 __global__ void __launch_bounds__(kFinishWarps * 32) k_score_finish(const FinishArgs a) {
   pdl_wait();
   __shared__ Key lists[kFinishWarps][32];
-  __shared__ Key found[(kMostTop + kKeepMore) * 32];
+  __shared__ Key found[kFound];
   __shared__ float4 sums[kFinishWarps];
   __shared__ double exact[32];
   __shared__ unsigned again;
+  __shared__ float target_z;
   __shared__ int n_found;
   const int64_t row = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -217,32 +219,50 @@ __global__ void __launch_bounds__(kFinishWarps * 32) k_score_finish(const Finish
   }
   Key list = 0;
   if (a.top) {
-    // the groups with the largest maxima
-    constexpr int kAhead = 8;  // loads in flight
+    // The groups with the largest maxima: none of them comes after the keep-th of the
+    // threads' own largest ones, and few others come before it.
     const float *high = a.high + row * a.high_ld;
-    for (int g0 = warp * 32; g0 < a.groups; g0 += kFinishWarps * 32 * kAhead) {
-      float v[kAhead];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int g = g0 + u * kFinishWarps * 32 + lane;
-        v[u] = g < a.groups ? __ldg(high + g) : 0.f;
-      }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int g = g0 + u * kFinishWarps * 32 + lane;
-        if (g - lane >= a.groups) break;
-        list = offered(list, g < a.groups ? key_of(v[u], g) : 0, a.keep, lane);
-      }
+    Key best = 0;
+#pragma unroll 4
+    for (int g = threadIdx.x; g < a.groups; g += kFinishWarps * 32) {
+      const Key k = key_of(__ldg(high + g), g);
+      if (k > best) best = k;
     }
-    lists[warp][lane] = list;
+    lists[warp][lane] = sorted(best, lane);
     if (threadIdx.x == 0) n_found = 0;
     __syncthreads();
     if (warp == 0) {
-#pragma unroll
+      list = lists[0][lane];
+#pragma unroll 1
       for (int w = 1; w < kFinishWarps; ++w) list = joined(list, lists[w][lane], lane);
+      const Key from = __shfl_sync(0xffffffffu, list, a.keep - 1);
+      if (lane == 0) lists[0][0] = from;
+    }
+    __syncthreads();
+    const Key from = lists[0][0];
+#pragma unroll 4
+    for (int g = threadIdx.x; g < a.groups; g += kFinishWarps * 32) {
+      const Key k = key_of(__ldg(high + g), g);
+      if (k >= from) {
+        const int at = atomicAdd(&n_found, 1);  // their order does not matter
+        if (at < kFound) found[at] = k;
+      }
+    }
+    __syncthreads();
+    if (warp == 0) {
+      list = 0;
+      const int n = n_found;
+      if (n <= kFound) {
+#pragma unroll 1
+        for (int i = 0; i < n; i += 32) list = offered(list, i + lane < n ? found[i + lane] : 0, a.keep, lane);
+      } else {  // a few threads have most of the large ones
+#pragma unroll 1
+        for (int g = lane; g - lane < a.groups; g += 32) list = offered(list, g < a.groups ? key_of(__ldg(high + g), g) : 0, a.keep, lane);
+      }
       lists[0][lane] = list;
     }
     __syncthreads();
+    if (threadIdx.x == 0) n_found = 0;
     // and of their logits those that are not below the last group's maximum
     constexpr int kMost = (kMostTop + kKeepMore + kFinishWarps - 1) / kFinishWarps;
     const Key last_group = lists[0][a.keep - 1];
@@ -255,14 +275,17 @@ __global__ void __launch_bounds__(kFinishWarps * 32) k_score_finish(const Finish
       const int col = of ? key_id(of) * 32 + lane : a.rows;
       k[u] = col < a.rows ? key_of(__ldg(a.z + row * a.z_row + col * a.z_col), a.v0 + col) : 0;
     }
+    __syncthreads();
 #pragma unroll
     for (int u = 0; u < kMost; ++u)
-      if (k[u] && k[u] >= least) found[atomicAdd(&n_found, 1)] = k[u];  // their order does not matter
+      if (k[u] && k[u] >= least) found[atomicAdd(&n_found, 1)] = k[u];
     __syncthreads();
     if (warp == 0) {
       list = 0;
       if (!a.first) list = a.list[row * 32 + lane];
-      for (int i = 0; i < n_found; i += 32) list = offered(list, i + lane < n_found ? found[i + lane] : 0, a.keep, lane);
+      const int n = n_found;
+#pragma unroll 1
+      for (int i = 0; i < n; i += 32) list = offered(list, i + lane < n ? found[i + lane] : 0, a.keep, lane);
       if (!a.last) a.list[row * 32 + lane] = list;
     }
     if (!a.last) return;
@@ -280,6 +303,10 @@ __global__ void __launch_bounds__(kFinishWarps * 32) k_score_finish(const Finish
     s = lane & d ? join_stats(o, s) : join_stats(s, o);
   }
   if (lane == 0) sums[warp] = s;
+  if (given && warp == kFinishWarps - 1) {  // beside warp 0's work
+    const float z = a.zt ? a.zt[row] : a.at.get(row, target);
+    if (lane == 0) target_z = z;
+  }
   if (a.top && warp == 0) {  // which of the list are too close to tell
     const float mine = list ? key_value(list) : -INFINITY, above = __shfl_up_sync(0xffffffffu, mine, 1);
     float size = lane < a.keep && isfinite(mine) ? fabsf(mine) : 0.f;
@@ -309,8 +336,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32) k_score_finish(const Finish
   s = sums[0];
 #pragma unroll
   for (int w = 1; w < kFinishWarps; ++w) s = join_stats(s, sums[w]);
-  float z = 0.f;
-  if (given) z = a.zt ? a.zt[row] : a.at.get(row, target);
+  const float z = given ? target_z : 0.f;
   // the largest logit with the target's, and of the sums relative to it what is over 1
   float high = s.x, over, slope;
   if (given && z >= s.x) {

@@ -1112,44 +1112,53 @@ __global__ void __launch_bounds__(256) k_xent_rows(const bf16 *__restrict__ in, 
 
 // The rows of dw that are targets: their sums, with what rounding dz to bf16 lost of its
 // entries there, mostly by far the largest: for each row of x with the target, in their
-// order, that much of it.  A block per row of x, at work for the first of each target.
+// order, that much of it.  A block per row of x and 256 columns, at work for the first
+// of each target; its warps share the rows of a target (frequent tokens have hundreds).
+constexpr int kHitRows = 512;  // rows of x looked at at a time
 __global__ void __launch_bounds__(128) k_xent_hits(const Hits hits, TokenSrc targets, int32_t n, const float *__restrict__ hot,
                                                    const bf16 *__restrict__ x, int64_t x_ld, int32_t width, bf16 *__restrict__ dw,
                                                    int64_t dw_ld, int wide) {
   pdl_wait();
-  __shared__ int rows[128];
+  __shared__ int rows[kHitRows];
   __shared__ int counts[4];
+  __shared__ float part[3][32][9];
   const int i = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t id = targets.key(i);
   if (id >= targets.vocab || hits.first[id] != i) return;
   const int last = hits.last[id];
-  const int c = blockIdx.y * 1024 + threadIdx.x * 8;
+  const int c = blockIdx.y * 256 + lane * 8;
   float acc[8];
 #pragma unroll
-  for (int j = 0; j < 8; j += 4) {
-    const float4 v = c + j < width ? *reinterpret_cast<const float4 *>(hits.rows + (int64_t)i * hits.ld + c + j) : make_float4(0.f, 0.f, 0.f, 0.f);
-    acc[j] = v.x;
-    acc[j + 1] = v.y;
-    acc[j + 2] = v.z;
-    acc[j + 3] = v.w;
-  }
-  for (int r0 = i; r0 <= last; r0 += 128) {
-    const int r = r0 + threadIdx.x;
-    const bool here = r <= last && targets.key(r) == id;
-    const unsigned m = __ballot_sync(0xffffffffu, here);
-    if (lane == 0) counts[warp] = __popc(m);
+  for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+  for (int r0 = i; r0 <= last; r0 += kHitRows) {
+    constexpr int kOwn = kHitRows / 128;
+    const int first = r0 + threadIdx.x * kOwn;
+    unsigned here = 0;
+#pragma unroll
+    for (int u = 0; u < kOwn; ++u)
+      if (first + u <= last && targets.key(first + u) == id) here |= 1u << u;
+    int before = __popc(here);
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int o = __shfl_up_sync(0xffffffffu, before, d);
+      if (lane >= d) before += o;
+    }
+    if (lane == 31) counts[warp] = before;
+    before -= __popc(here);
     __syncthreads();
-    int before = 0, all = 0;
+    int all = 0;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       if (w < warp) before += counts[w];
       all += counts[w];
     }
-    if (here) rows[before + __popc(m & ((1u << lane) - 1u))] = r;
+#pragma unroll
+    for (int u = 0; u < kOwn; ++u)
+      if ((here >> u) & 1) rows[before++] = first + u;
     __syncthreads();
     if (c < width) {
 #pragma unroll 4
-      for (int k = 0; k < all; ++k) {
+      for (int k = warp; k < all; k += 4) {
         const float h = hot[rows[k]], over = h - __bfloat162float(__float2bfloat16_rn(h));
         Pack<bf16, 16> v;
         v.raw = __ldg(reinterpret_cast<const uint4 *>(x + rows[k] * x_ld + c));
@@ -1160,7 +1169,24 @@ __global__ void __launch_bounds__(128) k_xent_hits(const Hits hits, TokenSrc tar
     }
     __syncthreads();
   }
-  if (c >= width) return;
+  if (warp)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[warp - 1][lane][j] = acc[j];
+  __syncthreads();
+  if (warp || c >= width) return;
+#pragma unroll
+  for (int w = 0; w < 3; ++w)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] += part[w][lane][j];
+#pragma unroll
+  for (int j = 0; j < 8; j += 4)
+    if (c + j < width) {
+      const float4 v = *reinterpret_cast<const float4 *>(hits.rows + (int64_t)i * hits.ld + c + j);
+      acc[j] += v.x;
+      acc[j + 1] += v.y;
+      acc[j + 2] += v.z;
+      acc[j + 3] += v.w;
+    }
   bf16 *to = dw + (int64_t)id * dw_ld + c;
   if (wide && c + 8 <= width) {
     Pack<bf16, 16> o;
@@ -1848,7 +1874,7 @@ snack_status xent_gradient(const XentShape &S, const XentWs &W, const void *x, i
     }
   }
   if (dw && hits.first)
-    XENT_CUDA(launch_pdl(k_xent_hits, dim3((unsigned)n, (unsigned)ceil_div(width, 1024)), 128, 0, s, hits, tg, n, (const float *)hot,
+    XENT_CUDA(launch_pdl(k_xent_hits, dim3((unsigned)n, (unsigned)ceil_div(width, 256)), 128, 0, s, hits, tg, n, (const float *)hot,
                          reinterpret_cast<const bf16 *>(ox.p), ox.ld, width, reinterpret_cast<bf16 *>(dw), dw_ld,
                          ptr_aligned(dw, 16) && dw_ld % 8 == 0 ? 1 : 0));
   const int64_t total = dx ? (int64_t)n * (W.acc_ld / 4) : 0;
