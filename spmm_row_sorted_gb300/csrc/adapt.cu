@@ -78,8 +78,8 @@ constexpr int kGroupThreads = 1024;
 constexpr int kGroupKeep = 8;                    // keys a lane keeps between the two passes
 constexpr int kGroupBytes = 208 * 1024;          // of counts in shared memory
 
-int group_warps(int groups) {
-  const int w = kGroupBytes / 4 / groups;
+int group_warps(int groups, int n) {
+  const int w = std::min(kGroupBytes / 4 / groups, (n + 31) / 32);
   return w < 1 ? 1 : w > kGroupThreads / 32 ? kGroupThreads / 32 : w;
 }
 
@@ -277,8 +277,7 @@ __device__ __forceinline__ void cut_pair(float a, float b, uint32_t (&w)[kParts]
 }
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -801,6 +800,11 @@ struct OuterArgs {
   int turned;           // the latter
   int v_wide;
 };
+// dA and dB, one beside the other: the first `slices` of the grid's columns are dA's
+struct OuterPair {
+  OuterArgs a[2];
+  int32_t slices;
+};
 
 constexpr int kOuterWarps = 8;
 constexpr int kOuterRows = 32;    // rows of v in shared memory at a time: two steps of 16
@@ -819,17 +823,19 @@ constexpr size_t outer_smem() {
 // kLane columns, the cluster's blocks have every so many of the rows.  The block's
 // warps share the rows' v, cut into parts and laid out as mma.sync reads it.
 template <typename T, int MT, bool kWide>
-__global__ void __launch_bounds__(kOuterWarps * 32, 1) k_adapt_outer(const OuterArgs a) {
+__global__ void __launch_bounds__(kOuterWarps * 32, 1) k_adapt_outer(const OuterPair pair) {
   pdl_wait();
+  const uint32_t block = cluster_rank(), blocks = cluster_blocks();
+  const int slice = (int)(blockIdx.x / blocks), second = slice >= pair.slices ? 1 : 0;
+  const OuterArgs &a = pair.a[second];
   typedef Op<T> O;
   constexpr int NT = O::kLane, kCols = 8 * NT, kRank = 16 * MT, kVp = O::kOwnParts, kThreads = kOuterWarps * 32;
   constexpr int kVWords = outer_v_words<T, MT>(), kPitch = outer_cols(NT) + 1;
   extern __shared__ __align__(16) uint32_t outer_ring[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, q = lane & 3;
-  const uint32_t block = cluster_rank(), blocks = cluster_blocks();
   const int adapter = blockIdx.y, r0 = blockIdx.z * kRank;
-  const int b0 = (int)(blockIdx.x / blocks) * kOuterWarps * kCols;
+  const int b0 = (slice - second * pair.slices) * kOuterWarps * kCols;
   const int first = a.start[adapter], end = a.start[adapter + 1];
   const int lane_c = b0 + warp * kCols + NT * g, left = a.cols - lane_c;
   uint4 *ring = reinterpret_cast<uint4 *>(outer_ring) + warp * kOuterStages * 8 * 32 + lane;
@@ -1006,7 +1012,7 @@ AdaptWs adapt_ws(int64_t n, int32_t adapters, int32_t rank) {
 bool row_wide(const void *p, int64_t ld, size_t es) { return ptr_aligned(p, 16) && (size_t)ld * es % 16 == 0; }
 
 cudaError_t launch_group(const TokenSrc &which, int n, uint8_t *b, const AdaptWs &W, cudaStream_t s) {
-  const int groups = (int)which.vocab + 1, warps = group_warps(groups);
+  const int groups = (int)which.vocab + 1, warps = group_warps(groups, n);
   const size_t smem = (size_t)warps * groups * 4;
   cudaError_t e = raise_smem_limit(k_adapt_group, smem);
   if (e != cudaSuccess) return e;
@@ -1083,24 +1089,30 @@ cudaError_t up(const UpArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s
 }
 
 template <typename T, int MT, bool kWide>
-cudaError_t launch_outer(const OuterArgs &a, int64_t n, int32_t adapters, int sms, cudaStream_t s) {
+cudaError_t launch_outer(OuterPair p, int64_t n, int32_t adapters, int sms, cudaStream_t s) {
   const size_t smem = outer_smem<T, MT>();
   const auto kernel = k_adapt_outer<T, MT, kWide>;
   cudaError_t e = raise_smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
-  const int64_t slices = ceil_div(a.cols, outer_cols(Op<T>::kLane)), ranks = ceil_div(a.rank, 16 * MT);
+  constexpr int kCols = outer_cols(Op<T>::kLane);
+  p.slices = p.a[0].out ? (int32_t)ceil_div(p.a[0].cols, kCols) : 0;
+  const int64_t slices = p.slices + (p.a[1].out ? ceil_div(p.a[1].cols, kCols) : 0);
+  const int32_t rank = p.a[p.slices ? 0 : 1].rank;
+  const int64_t ranks = ceil_div(rank, 16 * MT);
   const unsigned c = cluster_for(slices * ranks * adapters, ceil_div(n, (int64_t)adapters * kOuterRows), sms);
-  return launch_cluster(c, kernel, dim3((unsigned)(slices * c), (unsigned)adapters, (unsigned)ranks), kOuterWarps * 32, smem, s, a);
+  return launch_cluster(c, kernel, dim3((unsigned)(slices * c), (unsigned)adapters, (unsigned)ranks), kOuterWarps * 32, smem, s,
+                        (const OuterPair)p);
 }
 template <typename T, int MT>
-cudaError_t outer_by(const OuterArgs &a, int64_t n, int32_t adapters, int sms, cudaStream_t s) {
-  return row_wide(a.x, a.x_ld, sizeof(T)) ? launch_outer<T, MT, true>(a, n, adapters, sms, s) : launch_outer<T, MT, false>(a, n, adapters, sms, s);
+cudaError_t outer_by(const OuterPair &p, int64_t n, int32_t adapters, int sms, cudaStream_t s) {
+  const auto wide = [](const OuterArgs &a) { return !a.out || row_wide(a.x, a.x_ld, sizeof(T)); };
+  return wide(p.a[0]) && wide(p.a[1]) ? launch_outer<T, MT, true>(p, n, adapters, sms, s) : launch_outer<T, MT, false>(p, n, adapters, sms, s);
 }
 template <typename T>
-cudaError_t outer(const OuterArgs &a, int64_t n, int32_t adapters, int sms, cudaStream_t s) {
-  if (a.rank <= 16) return outer_by<T, 1>(a, n, adapters, sms, s);
-  if (a.rank <= 32) return outer_by<T, 2>(a, n, adapters, sms, s);
-  return outer_by<T, 4>(a, n, adapters, sms, s);
+cudaError_t outer(const OuterPair &p, int32_t rank, int64_t n, int32_t adapters, int sms, cudaStream_t s) {
+  if (rank <= 16) return outer_by<T, 1>(p, n, adapters, sms, s);
+  if (rank <= 32) return outer_by<T, 2>(p, n, adapters, sms, s);
+  return outer_by<T, 4>(p, n, adapters, sms, s);
 }
 
 snack_status adapt_check(int64_t n, int32_t adapters, int32_t rank, int32_t in_f, int32_t out_f, snack_dtype t) {
@@ -1284,29 +1296,28 @@ snack_status snack_adapt_bwd(const void *x, int64_t x_ld, int64_t n, const void 
     u.h_wide = rank % 4 == 0;
     ADAPT_CUDA(wide32 ? up<float, false>(u, n, W.tile_cap, sms, s) : up<bf16, false>(u, n, W.tile_cap, sms, s));
   }
-  OuterArgs o = {};
-  o.rank = rank;
-  o.order = order;
-  o.start = start;
-  if (da) {
-    o.v = dh;
-    o.v_wide = rank % 4 == 0;
-    o.x = x;
-    o.x_ld = x_ld;
-    o.cols = in_f;
-    o.out = da;
-    ADAPT_CUDA(wide32 ? outer<float>(o, n, n_adapters, sms, s) : outer<bf16>(o, n, n_adapters, sms, s));
-  }
-  if (db) {
-    o.v = h;
-    o.v_wide = rank % 4 == 0 && ptr_aligned(h, 16);
-    o.x = dy;
-    o.x_ld = dy_ld;
-    o.cols = out_f;
-    o.out = db;
-    o.turned = 1;
-    o.scales = scales;
-    ADAPT_CUDA(wide32 ? outer<float>(o, n, n_adapters, sms, s) : outer<bf16>(o, n, n_adapters, sms, s));
+  if (da || db) {
+    OuterPair p = {};
+    for (OuterArgs &o : p.a) {
+      o.rank = rank;
+      o.order = order;
+      o.start = start;
+    }
+    p.a[0].v = dh;
+    p.a[0].v_wide = rank % 4 == 0;
+    p.a[0].x = x;
+    p.a[0].x_ld = x_ld;
+    p.a[0].cols = in_f;
+    p.a[0].out = da;
+    p.a[1].v = h;
+    p.a[1].v_wide = rank % 4 == 0 && ptr_aligned(h, 16);
+    p.a[1].x = dy;
+    p.a[1].x_ld = dy_ld;
+    p.a[1].cols = out_f;
+    p.a[1].out = db;
+    p.a[1].turned = 1;
+    p.a[1].scales = scales;
+    ADAPT_CUDA(wide32 ? outer<float>(p, rank, n, n_adapters, sms, s) : outer<bf16>(p, rank, n, n_adapters, sms, s));
   }
   return SNACK_OK;
 } catch (...) {  // a host allocation failed
