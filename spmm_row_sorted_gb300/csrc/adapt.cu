@@ -205,8 +205,8 @@ __device__ __forceinline__ Pack<T, V * (int)sizeof(T)> load_vec(const T *p, int 
   return r;
 }
 
-// The same into shared memory, on its way while the lane works on: a lane reads
-// only what it wrote there itself, so its own wait is all that it needs.  kWide: the
+// The same into shared memory, on its way while the lane works on.  A lane reads what
+// it wrote there itself, or what the same lane of its pair's other warp did.  kWide: the
 // address is aligned to V elements; bf16 that are not are read at once.
 template <int kBytes>
 __device__ __forceinline__ void copy_async(void *to, const void *from, int bytes) {
@@ -244,6 +244,9 @@ template <int kLeft>
 __device__ __forceinline__ void fetch_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
+
+// two warps that share what they read
+__device__ __forceinline__ void pair_sync(int pair) { asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory"); }
 
 // The upper halves of two words, as a pair of bf16.
 __device__ __forceinline__ uint32_t upper_halves(float lo, float hi) {
@@ -356,23 +359,26 @@ struct DownArgs {
   float *h;             // [n][rank]
 };
 
-constexpr int kDownWarps = 8;
-// groups of K a warp has on their way or in hand, so that an SM has 130 to 190 KB
-__host__ __device__ constexpr int down_stages(int nt) { return nt >= 8 ? 3 : 4; }
-__host__ __device__ constexpr int down_smem(int nt) {
-  const int ring = kDownWarps * down_stages(nt) * (kTile / 8 + nt) * 512, sums = 4 * kTile * 8 * nt * 4;
+constexpr int kDownParts = 8;  // shares of K in a block: a warp each, or a pair that shares the rows' part and has half the
+                               // ranks each (one warp with all 64: 128 sums, eight warps on an SM; dh of 8192 x 16384 130 us)
+// groups of K a pair has on their way or in hand, so that an SM has 130 to 190 KB
+__host__ __device__ constexpr int down_stages(int cols) { return cols >= 64 ? 3 : 4; }
+__host__ __device__ constexpr int down_smem(int cols) {
+  const int ring = kDownParts * down_stages(cols) * (kTile / 8 + cols / 8) * 512, sums = 4 * kTile * cols * 4;
   return ring > sums ? ring : sums;
 }
 
-// The sums of kDownWarps warps over their groups of K, and of the cluster's blocks.
-template <typename T, int MT, int NT, bool kAlong, bool kWide>
+// The sums of the block's shares of K, and of the cluster's blocks; NT: a warp's ranks / 8.
+template <typename T, int MT, int NT, int kHalves, bool kAlong, bool kWide>
 __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, float *smem) {
   typedef Op<T> O;
-  constexpr int kRows = 16 * MT, kCols = 8 * NT, kStages = down_stages(NT), kSlots = kTile / 8 + NT;
+  constexpr int kRows = 16 * MT, kCols = 8 * NT * kHalves, kStages = down_stages(kCols), kSlots = kTile / 8 + NT * kHalves;
+  constexpr int kThreads = kDownParts * kHalves * 32;
   typedef Pack<T, NT * (int)sizeof(T)> Cross;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int part = warp / kHalves, half = warp % kHalves;
   const int g = lane >> 2, q = lane & 3;
-  const int r0 = blockIdx.y * kCols;
+  const int r0 = blockIdx.y * kCols + half * 8 * NT;
   const uint32_t rank = cluster_rank(), blocks = cluster_blocks();
   float acc[MT][NT][4];
 #pragma unroll
@@ -381,24 +387,28 @@ __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, f
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
-  const T *row[2 * MT];
+  // the rows that this warp reads of the tile (8 i + g for its share of i); past the end the last one again, and not kept
+  constexpr int kRead = 2 * MT / kHalves;
+  const T *row[kRead];
 #pragma unroll
-  for (int i = 0; i < 2 * MT; ++i)  // the rows past the tile's end are the last one's again, and not kept
-    row[i] = reinterpret_cast<const T *>(a.x) + (int64_t)__ldg(a.order + tile.first + min(8 * i + g, tile.count - 1)) * a.x_ld +
-             O::kLane * q;
+  for (int i = 0; i < kRead; ++i)
+    row[i] = reinterpret_cast<const T *>(a.x) +
+             (int64_t)__ldg(a.order + tile.first + min(8 * (half * kRead + i) + g, tile.count - 1)) * a.x_ld + O::kLane * q;
   const T *mat = reinterpret_cast<const T *>(a.m) + (int64_t)tile.adapter * a.rank * a.k;
-  // this lane's ring: kStages x (its 16 bytes of every 8th row; of the matrix NT of them, or the same bytes in smaller pieces)
-  uint4 *ring = reinterpret_cast<uint4 *>(smem) + (warp * kStages * kSlots) * 32 + lane;
+  // the part's ring: kStages x (of the rows 16 bytes of every 8th per lane; then each warp's of the matrix NT of them, or
+  // the same bytes in smaller pieces)
+  uint4 *ring = reinterpret_cast<uint4 *>(smem) + part * kStages * kSlots * 32;
   // two neighbouring groups, a line of the rows, then the two so many further on
-  const int step = (int)blocks * kDownWarps * 2 * O::kGroup;
-  int next = (int)(rank * kDownWarps + warp) * 2 * O::kGroup, odd = 0;
+  const int step = (int)blocks * kDownParts * 2 * O::kGroup;
+  const int k_first = (int)(rank * kDownParts + part) * 2 * O::kGroup;
+  int next = k_first, odd = 0;
   auto fetch = [&](int stage) {
     if (next < a.k) {
-      uint4 *to = ring + stage * kSlots * 32;
+      uint4 *to = ring + stage * kSlots * 32 + lane;
       const int left = a.k - next - O::kLane * q;
 #pragma unroll
-      for (int i = 0; i < 2 * MT; ++i) fetch_vec<T, O::kLane, kWide>(to + i * 32, row[i] + next, left);
-      to += kTile / 8 * 32;
+      for (int i = 0; i < kRead; ++i) fetch_vec<T, O::kLane, kWide>(to + (half * kRead + i) * 32, row[i] + next, left);
+      to += (kTile / 8 + half * NT) * 32;
       if constexpr (kAlong) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -407,10 +417,11 @@ __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, f
         }
       } else {  // rows next + kLane q + i: ranks NT g .. NT g + NT - 1
         typename Cross::R *piece = reinterpret_cast<typename Cross::R *>(to - lane) + lane;
+        const int ranks = a.rank - r0 - NT * g;
 #pragma unroll
         for (int i = 0; i < O::kLane; ++i)
-          fetch_vec<T, NT, kWide>(piece + i * 32, mat + (int64_t)min(next + O::kLane * q + i, a.k - 1) * a.rank + r0 + NT * g,
-                                  i < left ? a.rank - r0 - NT * g : 0);
+          fetch_vec<T, NT, kWide>(piece + i * 32, mat + (int64_t)min(next + O::kLane * q + i, a.k - 1) * a.rank + (ranks > 0 ? r0 + NT * g : 0),
+                                  i < left ? ranks : 0);
       }
     }
     fetch_commit();
@@ -420,10 +431,11 @@ __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, f
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) fetch(s);
   int stage = 0, odd_now = 0;
-  for (int k0 = (int)(rank * kDownWarps + warp) * 2 * O::kGroup; k0 < a.k; k0 += odd_now ? step - O::kGroup : O::kGroup, odd_now ^= 1) {
+  for (int k0 = k_first; k0 < a.k; k0 += odd_now ? step - O::kGroup : O::kGroup, odd_now ^= 1) {
+    fetch_wait<kStages - 2>();
+    if (kHalves > 1) pair_sync(part);  // the other warp's part is there, and it has done with the stage that is filled next
     fetch(stage == 0 ? kStages - 1 : stage - 1);
-    fetch_wait<kStages - 1>();
-    const uint4 *from = ring + stage * kSlots * 32;
+    const uint4 *from = ring + stage * kSlots * 32 + lane;
     uint32_t xa[O::kSteps][MT][2][2][O::kParts];
 #pragma unroll
     for (int i = 0; i < 2 * MT; ++i) {
@@ -432,7 +444,7 @@ __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, f
 #pragma unroll
       for (int s = 0; s < O::kSteps; ++s) along<T>(v, s, xa[s][i >> 1][i & 1]);
     }
-    from += kTile / 8 * 32;
+    from += (kTile / 8 + half * NT) * 32;
     const typename Cross::R *piece = reinterpret_cast<const typename Cross::R *>(from - lane) + lane;
     uint32_t bw[O::kSteps][NT][2][O::kParts];
     if constexpr (kAlong) {
@@ -465,8 +477,8 @@ __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, f
   }
   fetch_wait<0>();
   __syncthreads();  // the ring becomes the sums
-  // the warps' sums: the upper half's to the lower half, then those of the four
-  float *own = smem + (warp & 3) * (kRows * kCols);
+  // the parts' sums: the upper half's to the lower half, then those of the four
+  float *own = smem + (part & 3) * (kRows * kCols) + half * 8 * NT;
   auto each = [&](auto f) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -478,19 +490,19 @@ __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, f
           f(own[(16 * m + 8 * (e >> 1) + g) * kCols + c], acc[m][j][e]);
         }
   };
-  if (warp >= 4) each([](float &s, float &v) { s = v; });
+  if (part >= 4) each([](float &s, float &v) { s = v; });
   __syncthreads();
-  if (warp < 4) each([](float &s, float &v) { s += v; });
+  if (part < 4) each([](float &s, float &v) { s += v; });
   __syncthreads();
-  for (int i = threadIdx.x; i < kRows * kCols; i += kDownWarps * 32)
+  for (int i = threadIdx.x; i < kRows * kCols; i += kThreads)
     smem[i] = (smem[i] + smem[kRows * kCols + i]) + (smem[2 * kRows * kCols + i] + smem[3 * kRows * kCols + i]);
   if (blocks > 1)
     cluster_sync();
   else
     __syncthreads();
   const float scale = a.scales ? a.scales[tile.adapter] : 1.f;
-  for (int i = (int)rank * kDownWarps * 32 + threadIdx.x; i < tile.count * kCols; i += (int)blocks * kDownWarps * 32) {
-    const int t = i / kCols, r = r0 + i % kCols;
+  for (int i = (int)rank * kThreads + threadIdx.x; i < tile.count * kCols; i += (int)blocks * kThreads) {
+    const int t = i / kCols, r = blockIdx.y * kCols + i % kCols;
     float s = smem[i];
     if (blocks > 1) {
       s = ld_cluster(smem + i, 0);
@@ -501,16 +513,16 @@ __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, f
   if (blocks > 1) cluster_sync();  // no block's memory is read any more
 }
 
-template <typename T, int NT, bool kAlong, bool kWide>
-__global__ void __launch_bounds__(kDownWarps * 32, 1) k_adapt_down(const DownArgs a) {
+template <typename T, int NT, int kHalves, bool kAlong, bool kWide>
+__global__ void __launch_bounds__(kDownParts * kHalves * 32, 1) k_adapt_down(const DownArgs a) {
   pdl_wait();
   extern __shared__ __align__(16) float down_ring[];
   const Tile tile = a.tiles[blockIdx.x / cluster_blocks()];
   if (tile.adapter < 0 || tile.adapter >= a.adapters) return;  // the whole cluster's
   if (tile.count <= 16)
-    down_tile<T, 1, NT, kAlong, kWide>(a, tile, down_ring);
+    down_tile<T, 1, NT, kHalves, kAlong, kWide>(a, tile, down_ring);
   else
-    down_tile<T, 4, NT, kAlong, kWide>(a, tile, down_ring);
+    down_tile<T, 4, NT, kHalves, kAlong, kWide>(a, tile, down_ring);
 }
 
 // ------------------------------------------------------------ y and dx
@@ -531,8 +543,8 @@ struct UpArgs {
   int h_wide;
 };
 
-constexpr int kUpWarps = 8;
-constexpr int kUpCols = 32;  // columns of a warp at a time
+constexpr int kUpWarps = 8;     // pairs of them: half of the tile's rows each
+constexpr int kUpCols = 32;  // columns of a pair at a time
 
 // Of a row of h in shared memory, in elements: rows start 16 bytes apart modulo 128 as
 // bf16 (its two parts), 64 as fp32 (which is cut into parts as it is read); the
@@ -543,7 +555,7 @@ __host__ __device__ constexpr int up_ld(int rank) {
 }
 template <typename T>
 constexpr size_t up_h_bytes(int rank) { return (size_t)kTile * up_ld<T>(rank) * 4; }
-// shared memory of a lane: its 16-byte pieces of the base, and its pieces of the matrix (8 bytes of bf16, 16 of fp32)
+// shared memory of a pair's lane: its 16-byte pieces of the base, and its pieces of the matrix (8 bytes of bf16, 16 of fp32)
 template <typename T>
 __host__ __device__ constexpr int up_base_bytes() { return kTile / 8 * 8 * (int)sizeof(T); }
 template <typename T, int kSteps>
@@ -556,35 +568,36 @@ static_assert(kUpWarps * up_stages<bf16>() * up_stage_bytes<bf16, 4>() * 32 + up
                   kUpWarps * up_stages<float>() * up_stage_bytes<float, 1>() * 32 + up_h_bytes<float>(kMostRank) <= 232448,
               "shared memory of one block");
 
-// A warp takes 32 columns of the tile after 32 others; what it reads of the base and
-// the matrix is on its way one or two turns before, kSteps of 16 of the rank per turn.
+// A pair of warps takes 32 columns of the tile after 32 others; what it reads of the base
+// and the matrix is on its way one or two turns before, kSteps of 16 of the rank per turn.
 // The sums begin with the base, so the result is rounded as it leaves; h has its
 // scale before it is cut into parts.
 //
 // kWhole: 64 rows, whole groups of columns and steps of the rank: nothing to check.
 template <typename T, bool kAlong, int kSteps, bool kWide, bool kWhole>
 __device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, uint8_t *up_ring) {
-  constexpr int kHp = Op<T>::kOwnParts, kBp = Op<T>::kParts, MT = kTile / 16, NT = 4, kStages = up_stages<T>();
+  constexpr int kHp = Op<T>::kOwnParts, kBp = Op<T>::kParts, MT = kTile / 32, NT = 4, kStages = up_stages<T>();
   typedef Pack<T, 16> P;
   typedef Pack<T, 4 * (int)sizeof(T)> P4;
   constexpr int kPer = P::kN, kVecs = 8 / kPer;  // accesses for a lane's 8 columns
   constexpr int kStage = up_stage_bytes<T, kSteps>() * 32;
   const bool none = !kWhole && tile.adapter >= a.adapters;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pair = warp >> 1, half = warp & 1;
   const int g = lane >> 2, q = lane & 3;
   const int ld = up_ld<T>(a.rank) / 2, plane = kTile * ld;  // in words
   const int steps = none ? 1 : (a.rank + 15) / 16, turns = kWhole && kSteps == 4 ? 1 : (steps + kSteps - 1) / kSteps;
-  const int m_tiles = kWhole ? MT : (tile.count + 15) / 16;
-  uint8_t *ring = up_ring + warp * kStages * kStage;
+  const int first_row = 32 * half, m_tiles = kWhole ? MT : max(0, min(MT, (tile.count - first_row + 15) / 16));
+  uint8_t *ring = up_ring + pair * kStages * kStage;
   uint32_t *hs = reinterpret_cast<uint32_t *>(up_ring + kUpWarps * kStages * kStage);
   const T *mat = reinterpret_cast<const T *>(a.m) + (none ? 0 : (int64_t)tile.adapter * a.rank * a.cols);
-  const int col0 = (blockIdx.y * a.groups * kUpWarps + warp) * kUpCols;
+  const int col0 = (blockIdx.y * a.groups * kUpWarps + pair) * kUpCols;
   // this lane's rows, from its 8 columns on
   int32_t token[2 * MT];
   const T *base[2 * MT];
 #pragma unroll
   for (int i = 0; i < 2 * MT; ++i) {
-    token[i] = kWhole || 8 * i + g < tile.count ? __ldg(a.order + tile.first + 8 * i + g) : -1;
+    const int t = first_row + 8 * i + g;
+    token[i] = kWhole || t < tile.count ? __ldg(a.order + tile.first + t) : -1;
     base[i] = reinterpret_cast<const T *>(a.base) + (int64_t)max(token[i], 0) * a.base_ld + col0 + 8 * q;
   }
   const int items = (a.cols <= col0 ? 0 : min(a.groups, (a.cols - col0 + kUpWarps * kUpCols - 1) / (kUpWarps * kUpCols))) * turns;
@@ -594,7 +607,7 @@ __device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, uint8
       uint8_t *to = ring + next_stage * kStage;
       const int left = a.cols - next_col - 8 * q;
       if (next_turn == 0 && a.base) {
-        uint4 *at = reinterpret_cast<uint4 *>(to) + lane;
+        uint4 *at = reinterpret_cast<uint4 *>(to) + half * (2 * MT * kVecs) * 32 + lane;
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i) {
           if (i >= 2 * m_tiles) break;
@@ -612,9 +625,10 @@ __device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, uint8
         typename P4::R *at = reinterpret_cast<typename P4::R *>(to + up_base_bytes<T>() * 32) + lane;
         const int r0 = 16 * next_turn * kSteps + 4 * q;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int jj = 0; jj < 2; ++jj)  // the other two are the pair's other warp's
 #pragma unroll
           for (int s = 0; s < kSteps; ++s) {
+            const int j = 2 * half + jj;
             if constexpr (kAlong) {  // lane g has column 8 (g / 2) + 2 j + g % 2: a lane's sums are 8 neighbours
               const int col = next_col + 8 * (g >> 1) + 2 * j + (g & 1), r = r0 + 16 * s;
               if constexpr (kWhole)
@@ -645,8 +659,8 @@ __device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, uint8
   for (int s = 0; s < kStages - 1; ++s) fetch();
   if (!none) {
     const float scale = a.scales ? a.scales[tile.adapter] : 1.f;
-    const int quads = steps * 4;
-    for (int i = threadIdx.x; i < m_tiles * 16 * quads; i += kUpWarps * 32) {
+    const int quads = steps * 4, rows = (tile.count + 15) / 16 * 16;
+    for (int i = threadIdx.x; i < rows * quads; i += kUpWarps * 64) {
       const int t = i / quads, r = (i - t * quads) * 4;
       const bool in = t < tile.count;
       const auto v = load_vec<float, 4>(a.h + (int64_t)(in ? __ldg(a.order + tile.first + t) : 0) * a.rank + r, in ? a.rank - r : 0, a.h_wide);
@@ -666,17 +680,18 @@ __device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, uint8
   }
   __syncthreads();
   // ldmatrix: lanes 0 to 15 name rows 0 to 15 of their first pairs, lanes 16 to 31 of the second
-  const uint32_t h_at = static_cast<uint32_t>(__cvta_generic_to_shared(hs)) + (uint32_t)((lane & 15) * ld * 4 + (lane >> 4) * 16);
+  const uint32_t h_at = static_cast<uint32_t>(__cvta_generic_to_shared(hs)) + (uint32_t)((first_row + (lane & 15)) * ld * 4 + (lane >> 4) * 16);
   float acc[MT][NT][4];
   // a lane's 8 columns: which sum has column e of row half h
   auto sum_at = [&](int m, int h, int e) -> float & { return kAlong ? acc[m][e >> 1][2 * h + (e & 1)] : acc[m][e & 3][2 * h + (e >> 2)]; };
   int c = col0 + 8 * q, turn = 0, stage = 0;
   for (int item = 0; item < items; ++item) {
+    fetch_wait<kStages - 2>();
+    pair_sync(pair);  // the other warp's part is there, and it has done with the stage that is filled next
     fetch();
-    fetch_wait<kStages - 1>();
     const uint8_t *from = ring + stage * kStage;
     if (turn == 0) {
-      const uint4 *at = reinterpret_cast<const uint4 *>(from) + lane;
+      const uint4 *at = reinterpret_cast<const uint4 *>(from) + half * (2 * MT * kVecs) * 32 + lane;
 #pragma unroll
       for (int i = 0; i < 2 * MT; ++i) {
         if (i >= 2 * m_tiles) break;
@@ -715,7 +730,7 @@ __device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, uint8
           if constexpr (sizeof(T) == 4) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float4 v = *reinterpret_cast<const float4 *>(hs + (16 * m + 8 * h + g) * up_ld<T>(a.rank) + 16 * k + 4 * q);
+              const float4 v = *reinterpret_cast<const float4 *>(hs + (first_row + 16 * m + 8 * h + g) * up_ld<T>(a.rank) + 16 * k + 4 * q);
               cut_pair<kHp>(v.x, v.y, w[h][0]);
               cut_pair<kHp>(v.z, v.w, w[h][1]);
             }
@@ -724,8 +739,7 @@ __device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, uint8
             for (int p = 0; p < kHp; ++p)
               asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                            : "=r"(w[0][0][p]), "=r"(w[1][0][p]), "=r"(w[0][1][p]), "=r"(w[1][1][p])
-                           : "r"(h_at + (uint32_t)(p * plane + 16 * m * ld + 8 * k) * 4)
-                           : "memory");
+                           : "r"(h_at + (uint32_t)(p * plane + 16 * m * ld + 8 * k) * 4));
           }
           mma_all<NT, kHp, kBp>([&](int j) -> float(&)[4] { return acc[m][j]; },
                                 [&](int) -> const uint32_t(&)[2][2][kHp] { return w; },
@@ -771,7 +785,7 @@ __device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, uint8
 }
 
 template <typename T, bool kAlong, int kSteps, bool kWide>
-__global__ void __launch_bounds__(kUpWarps * 32, 1) k_adapt_up(const UpArgs a) {
+__global__ void __launch_bounds__(kUpWarps * 64, 1) k_adapt_up(const UpArgs a) {
   pdl_wait();
   extern __shared__ __align__(16) uint8_t up_ring[];
   const Tile tile = a.tiles[blockIdx.x];
@@ -1032,28 +1046,30 @@ unsigned cluster_for(int64_t blocks, int64_t shares, int sms) {
   return c;
 }
 
-template <typename T, int NT, bool kAlong, bool kWide>
+template <typename T, int NT, int kHalves, bool kAlong, bool kWide>
 cudaError_t launch_down(const DownArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
-  const size_t smem = down_smem(NT);
-  const auto kernel = k_adapt_down<T, NT, kAlong, kWide>;
+  constexpr int kCols = 8 * NT * kHalves;
+  const size_t smem = down_smem(kCols);
+  const auto kernel = k_adapt_down<T, NT, kHalves, kAlong, kWide>;
   cudaError_t e = raise_smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
-  const unsigned slices = (unsigned)ceil_div(a.rank, 8 * NT);
-  const unsigned c = cluster_for(likely_tiles(n, a.adapters) * slices, ceil_div(a.k, Op<T>::kGroup * kDownWarps), sms);
-  return launch_cluster(c, kernel, dim3((unsigned)tile_cap * c, slices), kDownWarps * 32, smem, s, a);
+  const unsigned slices = (unsigned)ceil_div(a.rank, kCols);
+  const unsigned c = cluster_for(likely_tiles(n, a.adapters) * slices, ceil_div(a.k, Op<T>::kGroup * kDownParts), sms);
+  return launch_cluster(c, kernel, dim3((unsigned)tile_cap * c, slices), kDownParts * kHalves * 32, smem, s, a);
 }
-template <typename T, int NT, bool kAlong>
+template <typename T, int NT, int kHalves, bool kAlong>
 cudaError_t down_by(const DownArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
   const size_t es = sizeof(T);
   const bool wide = row_wide(a.x, a.x_ld, es) && (kAlong ? row_wide(a.m, a.k, es) : ptr_aligned(a.m, NT * es) && a.rank % NT == 0);
-  return wide ? launch_down<T, NT, kAlong, true>(a, n, tile_cap, sms, s) : launch_down<T, NT, kAlong, false>(a, n, tile_cap, sms, s);
+  return wide ? launch_down<T, NT, kHalves, kAlong, true>(a, n, tile_cap, sms, s)
+              : launch_down<T, NT, kHalves, kAlong, false>(a, n, tile_cap, sms, s);
 }
 template <typename T, bool kAlong>
 cudaError_t down(const DownArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
-  constexpr int kMost = sizeof(T) == 2 ? 8 : 4;
-  if (a.rank <= 16) return down_by<T, 2, kAlong>(a, n, tile_cap, sms, s);
-  if (a.rank <= 32 || kMost == 4) return down_by<T, 4, kAlong>(a, n, tile_cap, sms, s);
-  return down_by<T, kMost, kAlong>(a, n, tile_cap, sms, s);
+  if (a.rank <= 16) return down_by<T, 2, 1, kAlong>(a, n, tile_cap, sms, s);
+  if (a.rank <= 32 || sizeof(T) == 4) return down_by<T, 2, 2, kAlong>(a, n, tile_cap, sms, s);
+  if constexpr (sizeof(T) == 2) return down_by<T, 4, 2, kAlong>(a, n, tile_cap, sms, s);
+  return cudaErrorInvalidValue;
 }
 
 template <typename T, bool kAlong, int kSteps, bool kWide>
@@ -1068,7 +1084,7 @@ cudaError_t launch_up(UpArgs a, int64_t n, int tile_cap, int sms, cudaStream_t s
   groups = std::min<int64_t>(groups, 16);
   if (ceil_div(all, groups) > 65535) groups = ceil_div(all, 65535);
   a.groups = (int)groups;
-  return launch_pdl(kernel, dim3((unsigned)tile_cap, (unsigned)ceil_div(all, groups)), kUpWarps * 32, smem, s, (const UpArgs)a);
+  return launch_pdl(kernel, dim3((unsigned)tile_cap, (unsigned)ceil_div(all, groups)), kUpWarps * 64, smem, s, (const UpArgs)a);
 }
 template <typename T, bool kAlong, int kSteps>
 cudaError_t up_by(const UpArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
