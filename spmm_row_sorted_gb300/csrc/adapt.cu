@@ -833,6 +833,34 @@ constexpr size_t outer_smem() {
   return ring > sums ? ring : sums;
 }
 
+// The cluster's sums [kRank][kCols] to the output, this block's share of them.
+template <typename T, int kRank, int kCols, int kThreads>
+__device__ __forceinline__ void outer_write(const OuterArgs &a, const float *sums, int pitch, uint32_t block, uint32_t blocks, int adapter,
+                                            int r0, int b0, bool empty) {
+  const float scale = a.scales ? a.scales[adapter] : 1.f;
+  T *out = reinterpret_cast<T *>(a.out) + (int64_t)adapter * a.rank * a.cols;
+  for (int i = (int)block * kThreads + threadIdx.x; i < kCols * kRank; i += (int)blocks * kThreads) {
+    int r, c;  // of the block's
+    if (a.turned) {
+      r = i % kRank;
+      c = i / kRank;
+    } else {
+      c = i % kCols;
+      r = i / kCols;
+    }
+    if (r0 + r >= a.rank || b0 + c >= a.cols) continue;
+    const float *at = sums + r * pitch + c;
+    float s = *at;
+    if (blocks > 1) {
+      s = ld_cluster(at, 0);
+      for (uint32_t b = 1; b < blocks; ++b) s += ld_cluster(at, b);
+    }
+    // an adapter without rows has no gradient, whatever its scale
+    const float v = empty ? 0.f : s * scale;
+    out[a.turned ? (int64_t)(b0 + c) * a.rank + r0 + r : (int64_t)(r0 + r) * a.cols + b0 + c] = from_f32<T>(v);
+  }
+}
+
 // An adapter's sums over its rows, 32 at a time, for 16 MT of the rank: a warp has 8
 // kLane columns, the cluster's blocks have every so many of the rows.  The block's
 // warps share the rows' v, cut into parts and laid out as mma.sync reads it.
@@ -974,28 +1002,7 @@ __global__ void __launch_bounds__(kOuterWarps * 32, 1) k_adapt_outer(const Outer
     cluster_sync();
   else
     __syncthreads();
-  const float scale = a.scales ? a.scales[adapter] : 1.f;
-  T *out = reinterpret_cast<T *>(a.out) + (int64_t)adapter * a.rank * a.cols;
-  for (int i = (int)block * kThreads + threadIdx.x; i < outer_cols(NT) * kRank; i += (int)blocks * kThreads) {
-    int r, c;  // of the block's
-    if (a.turned) {
-      r = i % kRank;
-      c = i / kRank;
-    } else {
-      c = i % outer_cols(NT);
-      r = i / outer_cols(NT);
-    }
-    if (r0 + r >= a.rank || b0 + c >= a.cols) continue;
-    const float *at = sums + r * kPitch + c;
-    float s = *at;
-    if (blocks > 1) {
-      s = ld_cluster(at, 0);
-      for (uint32_t b = 1; b < blocks; ++b) s += ld_cluster(at, b);
-    }
-    // an adapter without rows has no gradient, whatever its scale
-    const float v = first == end ? 0.f : s * scale;
-    out[a.turned ? (int64_t)(b0 + c) * a.rank + r0 + r : (int64_t)(r0 + r) * a.cols + b0 + c] = from_f32<T>(v);
-  }
+  outer_write<T, kRank, outer_cols(NT), kThreads>(a, sums, kPitch, block, blocks, adapter, r0, b0, first == end);
   if (blocks > 1) cluster_sync();
 }
 
@@ -1104,6 +1111,12 @@ cudaError_t up(const UpArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s
   return cudaErrorInvalidValue;
 }
 
+}  // namespace
+}  // namespace snack
+#include "adapt_tc.cuh"
+namespace snack {
+namespace {
+
 template <typename T, int MT, bool kWide>
 cudaError_t launch_outer(OuterPair p, int64_t n, int32_t adapters, int sms, cudaStream_t s) {
   const size_t smem = outer_smem<T, MT>();
@@ -1119,16 +1132,20 @@ cudaError_t launch_outer(OuterPair p, int64_t n, int32_t adapters, int sms, cuda
   return launch_cluster(c, kernel, dim3((unsigned)(slices * c), (unsigned)adapters, (unsigned)ranks), kOuterWarps * 32, smem, s,
                         (const OuterPair)p);
 }
-template <typename T, int MT>
-cudaError_t outer_by(const OuterPair &p, int64_t n, int32_t adapters, int sms, cudaStream_t s) {
-  const auto wide = [](const OuterArgs &a) { return !a.out || row_wide(a.x, a.x_ld, sizeof(T)); };
-  return wide(p.a[0]) && wide(p.a[1]) ? launch_outer<T, MT, true>(p, n, adapters, sms, s) : launch_outer<T, MT, false>(p, n, adapters, sms, s);
-}
 template <typename T>
 cudaError_t outer(const OuterPair &p, int32_t rank, int64_t n, int32_t adapters, int sms, cudaStream_t s) {
-  if (rank <= 16) return outer_by<T, 1>(p, n, adapters, sms, s);
-  if (rank <= 32) return outer_by<T, 2>(p, n, adapters, sms, s);
-  return outer_by<T, 4>(p, n, adapters, sms, s);
+  const auto aligned = [](const OuterArgs &a) { return !a.out || row_wide(a.x, a.x_ld, sizeof(T)); };
+  const bool wide = aligned(p.a[0]) && aligned(p.a[1]);
+  if constexpr (sizeof(T) == 2) {
+    if (wide) return rank <= 32 ? launch_outer_tc<32>(p, n, adapters, sms, s) : launch_outer_tc<64>(p, n, adapters, sms, s);
+  } else if (wide) {
+    return rank <= 16   ? launch_outer<T, 1, true>(p, n, adapters, sms, s)
+           : rank <= 32 ? launch_outer<T, 2, true>(p, n, adapters, sms, s)
+                        : launch_outer<T, 4, true>(p, n, adapters, sms, s);
+  }
+  return rank <= 16   ? launch_outer<T, 1, false>(p, n, adapters, sms, s)
+         : rank <= 32 ? launch_outer<T, 2, false>(p, n, adapters, sms, s)
+                      : launch_outer<T, 4, false>(p, n, adapters, sms, s);
 }
 
 snack_status adapt_check(int64_t n, int32_t adapters, int32_t rank, int32_t in_f, int32_t out_f, snack_dtype t) {
