@@ -87,7 +87,7 @@ int group_warps(int groups, int n) {
 // adapters and warps, say where its rows go.  8192 rows: see adapt_fwd's figures.
 __global__ void __launch_bounds__(kGroupThreads, 1)
     k_adapt_group(TokenSrc which, int n, int warps, int32_t *__restrict__ order, int32_t *__restrict__ start,
-                  Tile *__restrict__ tiles, int tile_cap) {
+                  Tile *__restrict__ tiles, int tile_cap, int tile_rows) {
   pdl_wait();
   extern __shared__ __align__(16) int32_t hist[];  // [warps][groups]
   __shared__ int2 warp_sum[32];
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
         hist[w * groups + g] = count;
         count += c;
       }
-    const int own = (count + kTile - 1) / kTile;
+    const int own = (count + tile_rows - 1) / tile_rows;
     int2 inc = make_int2(count, own);
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -161,11 +161,14 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
       start[g] = from;
       for (int w = 0; w < warps; ++w) hist[w * groups + g] += from;
       for (int t = 0; t < own; ++t)
-        tiles[tile + t] = Tile{g, from + t * kTile, min(kTile, count - t * kTile), 0};
+        tiles[tile + t] = Tile{g, from + t * tile_rows, min(tile_rows, count - t * tile_rows), 0};
     }
     __syncthreads();
   }
-  if (threadIdx.x == 0) start[groups] = n;
+  if (threadIdx.x == 0) {
+    start[groups] = n;
+    start[groups + 1] = carry.y;  // tiles
+  }
   for (int t = carry.y + threadIdx.x; t < tile_cap; t += kGroupThreads) tiles[t] = Tile{-1, 0, 0, 0};
   pass(true);
 }
@@ -540,6 +543,7 @@ struct UpArgs {
   void *out;
   int64_t out_ld;
   int groups;            // of 32 columns, per warp
+  const int32_t *n_tiles;
   int h_wide;
 };
 
@@ -1019,7 +1023,7 @@ AdaptWs adapt_ws(int64_t n, int32_t adapters, int32_t rank) {
   w.order = o;
   o += align_up((size_t)n * 4, kAlign);
   w.start = o;
-  o += align_up(((size_t)adapters + 2) * 4, kAlign);
+  o += align_up(((size_t)adapters + 3) * 4, kAlign);
   // every adapter's last tile, and the rows' without one, may be short
   w.tile_cap = (int)(ceil_div(n, kTile) + std::min<int64_t>(n, (int64_t)adapters + 1));
   w.tiles = o;
@@ -1030,20 +1034,24 @@ AdaptWs adapt_ws(int64_t n, int32_t adapters, int32_t rank) {
   return w;
 }
 
+const int32_t *tile_count(const uint8_t *ws, const AdaptWs &W, int32_t adapters) {
+  return reinterpret_cast<const int32_t *>(ws + W.start) + adapters + 2;
+}
+
 bool row_wide(const void *p, int64_t ld, size_t es) { return ptr_aligned(p, 16) && (size_t)ld * es % 16 == 0; }
 
-cudaError_t launch_group(const TokenSrc &which, int n, uint8_t *b, const AdaptWs &W, cudaStream_t s) {
+cudaError_t launch_group(const TokenSrc &which, int n, int tile_rows, uint8_t *b, const AdaptWs &W, cudaStream_t s) {
   const int groups = (int)which.vocab + 1, warps = group_warps(groups, n);
   const size_t smem = (size_t)warps * groups * 4;
   cudaError_t e = raise_smem_limit(k_adapt_group, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_adapt_group, 1, kGroupThreads, smem, s, which, n, warps, reinterpret_cast<int32_t *>(b + W.order),
-                    reinterpret_cast<int32_t *>(b + W.start), reinterpret_cast<Tile *>(b + W.tiles), W.tile_cap);
+                    reinterpret_cast<int32_t *>(b + W.start), reinterpret_cast<Tile *>(b + W.tiles), W.tile_cap, tile_rows);
 }
 
 // tiles that a call is likely to have: half of the short ones
-int64_t likely_tiles(int64_t n, int32_t adapters) {
-  return ceil_div(n, kTile) + std::min<int64_t>(n, adapters) / 2;
+int64_t likely_tiles(int64_t n, int32_t adapters, int tile_rows) {
+  return ceil_div(n, tile_rows) + std::min<int64_t>(n, adapters) / 2;
 }
 
 // blocks of a cluster: as many as the SMs have room for at a block each, and each with some of the shares
@@ -1053,6 +1061,12 @@ unsigned cluster_for(int64_t blocks, int64_t shares, int sms) {
   return c;
 }
 
+}  // namespace
+}  // namespace snack
+#include "adapt_tc.cuh"
+namespace snack {
+namespace {
+
 template <typename T, int NT, int kHalves, bool kAlong, bool kWide>
 cudaError_t launch_down(const DownArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
   constexpr int kCols = 8 * NT * kHalves;
@@ -1061,7 +1075,7 @@ cudaError_t launch_down(const DownArgs &a, int64_t n, int tile_cap, int sms, cud
   cudaError_t e = raise_smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
   const unsigned slices = (unsigned)ceil_div(a.rank, kCols);
-  const unsigned c = cluster_for(likely_tiles(n, a.adapters) * slices, ceil_div(a.k, Op<T>::kGroup * kDownParts), sms);
+  const unsigned c = cluster_for(likely_tiles(n, a.adapters, kTile) * slices, ceil_div(a.k, Op<T>::kGroup * kDownParts), sms);
   return launch_cluster(c, kernel, dim3((unsigned)tile_cap * c, slices), kDownParts * kHalves * 32, smem, s, a);
 }
 template <typename T, int NT, int kHalves, bool kAlong>
@@ -1072,7 +1086,9 @@ cudaError_t down_by(const DownArgs &a, int64_t n, int tile_cap, int sms, cudaStr
               : launch_down<T, NT, kHalves, kAlong, false>(a, n, tile_cap, sms, s);
 }
 template <typename T, bool kAlong>
-cudaError_t down(const DownArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
+cudaError_t down(const DownArgs &a, int64_t n, int tile_rows, int tile_cap, int sms, cudaStream_t s) {
+  if constexpr (sizeof(T) == 2)
+    if (tile_rows == kTcTile) return launch_down_tc<kAlong>(a, likely_tiles(n, a.adapters, kTcTile), tile_cap, sms, s);
   if (a.rank <= 16) return down_by<T, 2, 1, kAlong>(a, n, tile_cap, sms, s);
   if (a.rank <= 32 || sizeof(T) == 4) return down_by<T, 2, 2, kAlong>(a, n, tile_cap, sms, s);
   if constexpr (sizeof(T) == 2) return down_by<T, 4, 2, kAlong>(a, n, tile_cap, sms, s);
@@ -1087,7 +1103,7 @@ cudaError_t launch_up(UpArgs a, int64_t n, int tile_cap, int sms, cudaStream_t s
   if (e != cudaSuccess) return e;
   const int64_t all = ceil_div(a.cols, kUpWarps * kUpCols);
   // a block that has more columns reads its rows of h for all of them, as long as there are four blocks per SM
-  int64_t groups = std::max<int64_t>(1, likely_tiles(n, a.adapters) * all / (4 * (int64_t)sms));
+  int64_t groups = std::max<int64_t>(1, likely_tiles(n, a.adapters, kTile) * all / (4 * (int64_t)sms));
   groups = std::min<int64_t>(groups, 16);
   if (ceil_div(all, groups) > 65535) groups = ceil_div(all, 65535);
   a.groups = (int)groups;
@@ -1102,7 +1118,9 @@ cudaError_t up_by(const UpArgs &a, int64_t n, int tile_cap, int sms, cudaStream_
   return wide ? launch_up<T, kAlong, kSteps, true>(a, n, tile_cap, sms, s) : launch_up<T, kAlong, kSteps, false>(a, n, tile_cap, sms, s);
 }
 template <typename T, bool kAlong>
-cudaError_t up(const UpArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
+cudaError_t up(const UpArgs &a, int64_t n, int tile_rows, int tile_cap, int sms, cudaStream_t s) {
+  if constexpr (sizeof(T) == 2)
+    if (tile_rows == kTcTile) return launch_up_tc<kAlong>(a, tile_cap, sms, s);
   if (a.rank <= 16 || sizeof(T) == 4) return up_by<T, kAlong, 1>(a, n, tile_cap, sms, s);
   if constexpr (sizeof(T) == 2) {
     if (a.rank > 32 && a.rank <= 64) return up_by<T, kAlong, 4>(a, n, tile_cap, sms, s);
@@ -1110,12 +1128,6 @@ cudaError_t up(const UpArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s
   }
   return cudaErrorInvalidValue;
 }
-
-}  // namespace
-}  // namespace snack
-#include "adapt_tc.cuh"
-namespace snack {
-namespace {
 
 template <typename T, int MT, bool kWide>
 cudaError_t launch_outer(OuterPair p, int64_t n, int32_t adapters, int sms, cudaStream_t s) {
@@ -1161,10 +1173,20 @@ struct Span {
 };
 bool overlaps(const Span &a, const Span &b) { return spans_overlap(a.p, a.bytes, b.p, b.bytes); }
 
+// Rows of a tile: of bf16 whose rows (dx's and y's whole ones) lie on 16 bytes, and the matrices' on 8, those of TMEM.
+bool on8(const void *m, int32_t ld) { return ptr_aligned(m, 8) && ld % 4 == 0; }
+int down_tile_rows(const DownArgs &d, int32_t m_ld, snack_dtype t) {
+  return t == SNACK_BF16 && row_wide(d.x, d.x_ld, 2) && on8(d.m, m_ld) ? kTcTile : kTile;
+}
+int up_tile_rows(const UpArgs &u, int32_t m_ld, snack_dtype t) {
+  return t == SNACK_BF16 && row_wide(u.base, u.base_ld, 2) && row_wide(u.out, u.out_ld, 2) && u.cols % 8 == 0 && on8(u.m, m_ld) ? kTcTile
+                                                                                                                               : kTile;
+}
+
 template <typename T>
-cudaError_t run_fwd(const DownArgs &d, const UpArgs &u, int64_t n, const AdaptWs &W, int sms, cudaStream_t s) {
-  cudaError_t e = down<T, true>(d, n, W.tile_cap, sms, s);
-  return e != cudaSuccess ? e : up<T, true>(u, n, W.tile_cap, sms, s);
+cudaError_t run_fwd(const DownArgs &d, const UpArgs &u, int64_t n, int tile_rows, const AdaptWs &W, int sms, cudaStream_t s) {
+  cudaError_t e = down<T, true>(d, n, tile_rows, W.tile_cap, sms, s);
+  return e != cudaSuccess ? e : up<T, true>(u, n, tile_rows, W.tile_cap, sms, s);
 }
 
 int sms_here() {
@@ -1223,7 +1245,6 @@ snack_status snack_adapt_fwd(const void *x, int64_t x_ld, int64_t n, const void 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t *w = reinterpret_cast<uint8_t *>(ws);
   const int sms = sms_here();
-  ADAPT_CUDA(launch_group(TokenSrc{which, which_t == SNACK_I64, (uint32_t)n_adapters}, (int)n, w, W, s));
   DownArgs d = {};
   d.x = x;
   d.x_ld = x_ld;
@@ -1241,6 +1262,7 @@ snack_status snack_adapt_fwd(const void *x, int64_t x_ld, int64_t n, const void 
   u.rank = rank;
   u.order = d.order;
   u.tiles = d.tiles;
+  u.n_tiles = tile_count(w, W, n_adapters);
   u.adapters = n_adapters;
   u.scales = scales;
   u.base = base;
@@ -1248,7 +1270,9 @@ snack_status snack_adapt_fwd(const void *x, int64_t x_ld, int64_t n, const void 
   u.out = y;
   u.out_ld = y_ld;
   u.h_wide = rank % 4 == 0 && ptr_aligned(d.h, 16);
-  ADAPT_CUDA(t == SNACK_F32 ? run_fwd<float>(d, u, n, W, sms, s) : run_fwd<bf16>(d, u, n, W, sms, s));
+  const int rows = std::min(down_tile_rows(d, in_f, t), up_tile_rows(u, rank, t));
+  ADAPT_CUDA(launch_group(TokenSrc{which, which_t == SNACK_I64, (uint32_t)n_adapters}, (int)n, rows, w, W, s));
+  ADAPT_CUDA(t == SNACK_F32 ? run_fwd<float>(d, u, n, rows, W, sms, s) : run_fwd<bf16>(d, u, n, rows, W, sms, s));
   return SNACK_OK;
 } catch (...) {  // a host allocation failed
   return SNACK_ERR_CUDA;
@@ -1296,39 +1320,38 @@ snack_status snack_adapt_bwd(const void *x, int64_t x_ld, int64_t n, const void 
   uint8_t *w = reinterpret_cast<uint8_t *>(ws);
   const int sms = sms_here();
   const bool wide32 = t == SNACK_F32;
-  ADAPT_CUDA(launch_group(TokenSrc{which, which_t == SNACK_I64, (uint32_t)n_adapters}, (int)n, w, W, s));
   const int32_t *order = reinterpret_cast<const int32_t *>(w + W.order), *start = reinterpret_cast<const int32_t *>(w + W.start);
   float *dh = reinterpret_cast<float *>(w + W.h);
-  if (dx || da) {
-    DownArgs d = {};
-    d.x = dy;
-    d.x_ld = dy_ld;
-    d.m = b;
-    d.k = out_f;
-    d.rank = rank;
-    d.order = order;
-    d.tiles = reinterpret_cast<const Tile *>(w + W.tiles);
-    d.adapters = n_adapters;
-    d.scales = scales;
-    d.h = dh;
-    ADAPT_CUDA(wide32 ? down<float, false>(d, n, W.tile_cap, sms, s) : down<bf16, false>(d, n, W.tile_cap, sms, s));
-  }
-  if (dx) {
-    UpArgs u = {};
-    u.h = dh;
-    u.m = a;
-    u.cols = in_f;
-    u.rank = rank;
-    u.order = order;
-    u.tiles = reinterpret_cast<const Tile *>(w + W.tiles);
-    u.adapters = n_adapters;
-    u.base = accumulate ? dx : nullptr;
-    u.base_ld = dx_ld;
-    u.out = dx;
-    u.out_ld = dx_ld;
-    u.h_wide = rank % 4 == 0;
-    ADAPT_CUDA(wide32 ? up<float, false>(u, n, W.tile_cap, sms, s) : up<bf16, false>(u, n, W.tile_cap, sms, s));
-  }
+  DownArgs d = {};
+  d.x = dy;
+  d.x_ld = dy_ld;
+  d.m = b;
+  d.k = out_f;
+  d.rank = rank;
+  d.order = order;
+  d.tiles = reinterpret_cast<const Tile *>(w + W.tiles);
+  d.adapters = n_adapters;
+  d.scales = scales;
+  d.h = dh;
+  UpArgs u = {};
+  u.h = dh;
+  u.m = a;
+  u.cols = in_f;
+  u.rank = rank;
+  u.order = order;
+  u.tiles = d.tiles;
+  u.n_tiles = tile_count(w, W, n_adapters);
+  u.adapters = n_adapters;
+  u.base = accumulate ? dx : nullptr;
+  u.base_ld = dx_ld;
+  u.out = dx;
+  u.out_ld = dx_ld;
+  u.h_wide = rank % 4 == 0;
+  const int rows = dx ? std::min(down_tile_rows(d, rank, t), up_tile_rows(u, in_f, t)) : down_tile_rows(d, rank, t);
+  ADAPT_CUDA(launch_group(TokenSrc{which, which_t == SNACK_I64, (uint32_t)n_adapters}, (int)n, rows, w, W, s));
+  if (dx || da)
+    ADAPT_CUDA(wide32 ? down<float, false>(d, n, rows, W.tile_cap, sms, s) : down<bf16, false>(d, n, rows, W.tile_cap, sms, s));
+  if (dx) ADAPT_CUDA(wide32 ? up<float, false>(u, n, rows, W.tile_cap, sms, s) : up<bf16, false>(u, n, rows, W.tile_cap, sms, s));
   if (da || db) {
     OuterPair p = {};
     for (OuterArgs &o : p.a) {

@@ -27,6 +27,9 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
   }
   return false;
 }
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(bar)) : "memory");
+}
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -56,7 +59,7 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(bar)) : "memory");
 }
 // fp32 sums (bit 4) of bf16 operands (bits 7 and 10), MN-major A and B (bits 15 and 16), N / 8 at bit 17, M / 16 at bit 24
-constexpr uint32_t tc_inst(int m, int n, bool a_mn, bool b_mn) {
+__host__ __device__ constexpr uint32_t tc_inst(int m, int n, bool a_mn, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(m >> 4) << 24);
 }
@@ -76,18 +79,7 @@ __device__ __forceinline__ void tmem_wait(float (&a)[16], float (&b)[16]) {
   for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(a[i]), "+f"(b[i]));
 }
 
-// ------------------------------------------------------------ dA and dB
-
-constexpr int kTcCols = 256;     // columns of a block: two tiles of 128, the lanes of TMEM
-constexpr int kTcRows = 32;      // rows (of K) per stage
-constexpr int kTcStages = 3;
 constexpr int kTcThreads = 256;
-constexpr int kTcBox = kTcRows * 128;  // bytes of 64 columns of a stage
-__host__ __device__ constexpr int tc_outer_stage(int ranks) { return (kTcCols + 2 * ranks) / 64 * kTcBox; }
-constexpr size_t tc_outer_smem(int ranks) {
-  const size_t ring = (size_t)kTcStages * tc_outer_stage(ranks), sums = std::max((size_t)ranks * (kTcCols + 4), (size_t)kTcCols * (ranks + 4)) * 4;
-  return (ring > sums ? ring : sums) + 1024;
-}
 
 __device__ __forceinline__ float4 ld_cluster4(const float *p, uint32_t block) {
   uint32_t at;
@@ -95,6 +87,476 @@ __device__ __forceinline__ float4 ld_cluster4(const float *p, uint32_t block) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(su32(p)), "r"(block));
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
   return v;
+}
+
+// ------------------------------------------------------------ h and dh
+
+constexpr int kTcTile = 128;  // rows of a tile: the lanes of TMEM
+constexpr int kTcK = 64;      // of K per stage: 128 bytes of a row
+constexpr int kTcRowBox = kTcTile * 128;  // bytes of 64 elements of the rows
+
+// of the rank: padded to steps of 16, and 64 of it per 128 bytes
+__host__ __device__ constexpr int tc_steps(int rank) { return (rank + 15) / 16; }
+__host__ __device__ constexpr int tc_blocks(int rank) { return (rank + 63) / 64; }
+__host__ __device__ constexpr uint32_t tc_tmem_cols(int cols) { return cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256; }
+
+constexpr int kTcDownStages = 4;
+__host__ __device__ constexpr int tc_down_stage(int rank) { return kTcRowBox + tc_blocks(rank) * kTcK * 128; }
+__host__ __device__ constexpr size_t tc_down_smem(int rank) {
+  const size_t ring = (size_t)kTcDownStages * tc_down_stage(rank), sums = (size_t)kTcTile * (16 * tc_steps(rank) + 4) * 4;
+  return (ring > sums ? ring : sums) + 1024;
+}
+
+// A pieces of 16 bytes as 16 or, where the rows lie on 8, twice 8 of them; `bytes` of them are there.
+__device__ __forceinline__ void copy_piece(void *to, const void *from, int bytes, bool wide) {
+  if (wide) {
+    copy_async<16>(to, from, bytes);
+  } else {
+    copy_async<8>(to, from, min(bytes, 8));
+    copy_async<8>(reinterpret_cast<uint8_t *>(to) + 8, reinterpret_cast<const uint8_t *>(from) + (bytes > 8 ? 8 : 0), max(bytes - 8, 0));
+  }
+}
+
+// 64 of K (rows and columns of the swizzled tiles) of an adapter's matrix for the product: with K along its rows
+// ([cols][k], n of them from row `n0` on) or across them ([k][cols], columns from `n0` on).  kBox rows of K or of the
+// matrix are 128-byte rows of the tile, 64 elements each; what is past the end is zeros.
+//
+// Rows of 128 bytes `rows`, whose first elements are `at` + row * ld, `left_rows` and `left` elements of them there.
+template <int kThreads>
+__device__ __forceinline__ void fetch_box(uint8_t *to, const bf16 *from, int64_t ld, int rows, int left_rows, int chunks, int left, bool wide) {
+  for (int i = threadIdx.x; i < rows * chunks; i += kThreads) {
+    const int r = i / chunks, c = i - r * chunks;
+    const int bytes = r < left_rows ? max(0, min(left - 8 * c, 8)) * 2 : 0;
+    copy_piece(to + r * 128 + ((c ^ (r & 7)) << 4), bytes ? from + r * ld + 8 * c : from, bytes, wide);
+  }
+}
+
+// A tile of 128 rows against an adapter's matrix, all of its ranks (N); the cluster's blocks have every so many 64 of K.
+template <bool kAlong>
+__global__ void __launch_bounds__(kTcThreads, 2) k_adapt_down_tc(const DownArgs a, int m_wide) {
+  pdl_wait();
+  const uint32_t block = cluster_rank(), blocks = cluster_blocks();
+  const Tile tile = a.tiles[blockIdx.x / blocks];
+  if (tile.adapter < 0 || tile.adapter >= a.adapters) return;  // the whole cluster's
+  extern __shared__ uint8_t tc_raw[];
+  __shared__ uint64_t done[kTcDownStages];
+  __shared__ uint32_t tmem_at;
+  uint8_t *ring = tc_raw + ((1024 - (su32(tc_raw) & 1023)) & 1023);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = a.rank, n_pad = 16 * tc_steps(rank), stage_bytes = tc_down_stage(rank);
+  const uint32_t tmem_cols = tc_tmem_cols(n_pad);
+  if (warp == 0) tmem_alloc(&tmem_at, tmem_cols);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kTcDownStages; ++s) mbar_init(&done[s], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_at;
+  bool ok = true;
+  const int k_blocks = (a.k + kTcK - 1) / kTcK, steps = (int)block < k_blocks ? (k_blocks - (int)block + (int)blocks - 1) / (int)blocks : 0;
+  // the rows: eight lanes have 128 bytes of one, a warp four at a time
+  constexpr int kPasses = kTcTile / (kTcThreads / 8);
+  const bf16 *row[kPasses];
+#pragma unroll
+  for (int u = 0; u < kPasses; ++u) {
+    const int t = threadIdx.x / 8 + u * (kTcThreads / 8);
+    row[u] = reinterpret_cast<const bf16 *>(a.x) + (int64_t)__ldg(a.order + tile.first + min(t, tile.count - 1)) * a.x_ld + 8 * (lane & 7);
+  }
+  const bf16 *mat = reinterpret_cast<const bf16 *>(a.m) + (int64_t)tile.adapter * rank * a.k;
+  auto fetch = [&](int i) {
+    if (i < steps) {
+      const int k0 = (i * (int)blocks + (int)block) * kTcK;
+      uint8_t *to = ring + (i % kTcDownStages) * stage_bytes;
+      const int left = a.k - k0, bytes = max(0, min(left - 8 * (lane & 7), 8)) * 2;
+#pragma unroll
+      for (int u = 0; u < kPasses; ++u) {
+        const int t = threadIdx.x / 8 + u * (kTcThreads / 8);
+        if (t < tile.count) copy_async<16>(to + t * 128 + (((lane & 7) ^ (t & 7)) << 4), bytes ? row[u] + k0 : row[u], bytes);
+      }
+      to += kTcRowBox;
+      if constexpr (kAlong) {
+        fetch_box<kTcThreads>(to, mat + k0, a.k, n_pad, rank, 8, left, m_wide);
+      } else {
+        for (int b = 0; b < tc_blocks(rank); ++b)
+          fetch_box<kTcThreads>(to + b * kTcK * 128, mat + (int64_t)k0 * rank + 64 * b, rank, kTcK, left, min(8, (n_pad - 64 * b) / 8), rank - 64 * b,
+                                m_wide);
+      }
+    }
+    fetch_commit();
+  };
+  // the rows past the tile's end stay as they are: a row's sums are its own
+  if (steps) {
+    const uint32_t inst = tc_inst(kTcTile, n_pad, false, !kAlong);
+    for (int s = 0; s < kTcDownStages - 1; ++s) fetch(s);
+    for (int i = 0; i < steps; ++i) {
+      fetch_wait<kTcDownStages - 2>();
+      fence_async_shared();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        tc_fence_after();
+        const uint32_t at = su32(ring) + (i % kTcDownStages) * stage_bytes, b = at + kTcRowBox;
+#pragma unroll
+        for (int s = 0; s < kTcK / 16; ++s)
+          tc_mma(tmem, tc_desc(at + s * 32, 16), kAlong ? tc_desc(b + s * 32, 16) : tc_desc(b + s * 2048, kTcK * 128), inst, i > 0 || s > 0);
+        tc_commit(&done[i % kTcDownStages]);
+      }
+      if (i > 0) ok = mbar_wait(&done[(i - 1) % kTcDownStages], ((i - 1) / kTcDownStages) & 1) && ok;
+      fetch(i + kTcDownStages - 1);
+    }
+    fetch_wait<0>();
+    ok = mbar_wait(&done[(steps - 1) % kTcDownStages], ((steps - 1) / kTcDownStages) & 1) && ok;
+    tc_fence_after();
+  }
+  __syncthreads();  // the ring becomes the sums
+  float *sums = reinterpret_cast<float *>(ring);
+  const int pitch = n_pad + 4;
+  for (int c = 16 * (warp >> 2); c < n_pad; c += 32) {
+    float v[16];
+    if (steps) {
+      tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + c, v);
+      tmem_wait(v, v);
+    }
+    float *to = sums + (32 * (warp & 3) + lane) * pitch + c;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = !ok ? NAN : steps ? v[e] : 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4 *>(to + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+  }
+  tc_fence_before();
+  if (blocks > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, tmem_cols);
+  }
+  const float scale = a.scales ? a.scales[tile.adapter] : 1.f;
+  const int quads = n_pad / 4;
+  for (int i = (int)block * kTcThreads + threadIdx.x; i < tile.count * quads; i += (int)blocks * kTcThreads) {
+    const int t = i / quads, r = (i - t * quads) * 4;
+    if (r >= rank) continue;
+    const float *at = sums + t * pitch + r;
+    float4 s = *reinterpret_cast<const float4 *>(at);
+    if (blocks > 1) {
+      s = ld_cluster4(at, 0);
+      for (uint32_t b = 1; b < blocks; ++b) {
+        const float4 o = ld_cluster4(at, b);
+        s.x += o.x;
+        s.y += o.y;
+        s.z += o.z;
+        s.w += o.w;
+      }
+    }
+    float *to = a.h + (int64_t)a.order[tile.first + t] * rank + r;
+    const float w[4] = {s.x * scale, s.y * scale, s.z * scale, s.w * scale};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (r + e < rank) to[e] = w[e];
+  }
+  if (blocks > 1) cluster_sync();  // no block's memory is read any more
+}
+
+template <bool kAlong>
+cudaError_t launch_down_tc(const DownArgs &a, int64_t tiles, int tile_cap, int sms, cudaStream_t s) {
+  const size_t smem = tc_down_smem(a.rank);
+  const auto kernel = k_adapt_down_tc<kAlong>;
+  cudaError_t e = raise_smem_limit(kernel, smem);
+  if (e != cudaSuccess) return e;
+  const int m_wide = ptr_aligned(a.m, 16) && (kAlong ? a.k : a.rank) % 8 == 0;
+  const unsigned c = cluster_for(tiles, ceil_div(a.k, 2 * kTcK), 2 * sms);
+  return launch_cluster(c, kernel, dim3((unsigned)tile_cap * c), kTcThreads, smem, s, a, m_wide);
+}
+
+// ------------------------------------------------------------ y and dx
+
+constexpr int kTcUpCols = 128;  // columns of a unit
+constexpr int kTcUpEpi = 256;   // threads that write results; a warp more fetches the matrix, another one issues the products
+constexpr int kTcUpThreads = kTcUpEpi + 64;
+constexpr int kTcUpMostStages = 3;
+constexpr int64_t kTcUpRun = 8; // units of a block that follow one another, about
+__host__ __device__ constexpr int tc_up_stage(int rank) { return tc_blocks(rank) * kTcUpCols * 128; }
+__host__ __device__ constexpr int tc_up_stages(int rank) { return tc_blocks(rank) <= 2 ? 3 : tc_blocks(rank) == 3 ? 2 : 1; }
+__host__ __device__ constexpr size_t tc_up_smem(int rank) {
+  return (size_t)2 * tc_blocks(rank) * kTcRowBox + (size_t)tc_up_stages(rank) * tc_up_stage(rank) + 1024;
+}
+static_assert(tc_up_smem(kMostRank) <= 232448 - 1024 && tc_up_smem(192) <= 232448 - 1024 && tc_up_smem(128) <= 232448 - 1024 &&
+                  tc_down_smem(kMostRank) <= 232448 - 1024,
+              "shared memory of one block");
+
+// the warps that lay out h and the one that issues products
+__device__ __forceinline__ void tc_rows_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kTcUpEpi + 32) : "memory"); }
+
+// 32 columns of 16 lanes of TMEM as a product's fragments: v[4 j + 2 h + e] is row 8 h + lane / 4, column 8 j + 2 (lane % 4) + e
+__device__ __forceinline__ void tmem_ld_rows(uint32_t at, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(at)
+      : "memory");
+}
+// the pairs (j, lane % 4) of a fragment turned into (lane % 4, j): a lane has eight neighbours of each row then
+__device__ __forceinline__ void turn_pairs(float (&v)[16], int lane) {
+#pragma unroll
+  for (int d = 1; d <= 2; d *= 2) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j & d) continue;  // lanes without the bit keep chunk j and take their partner's j for their chunk j + d
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float mine = up ? v[4 * j + k] : v[4 * (j + d) + k];
+        const float other = __shfl_xor_sync(0xffffffffu, mine, d);
+        if (up)
+          v[4 * j + k] = other;
+        else
+          v[4 * (j + d) + k] = other;
+      }
+    }
+  }
+}
+
+// Units of a tile of 128 rows and 128 columns: h in its two parts (A, K-major) against the matrix's columns (B).  A block
+// has runs of units; all blocks' runs one beside the other, so that what is read and written at a time are some tiles'
+// rows.  One warp fetches the matrix, one issues the products into two sets of sums in turn, eight add the base, which
+// they have read ahead, and write the result: 32 rows and 64 columns each, 64 bytes of a row from four lanes together.
+// For that the matrix's rows lie in the order of a fragment's columns (kAlong), or pairs change lanes.
+// (Base and result through shared memory, 64 columns at a time: 143 us for y of 8192 x 16384 of rank 64, 41 % of shared
+// memory's cycles; eight warps doing everything in turn 190, of a step's 3700 cycles 1200 waiting for the products.)
+template <bool kAlong>
+__global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a, int m_wide) {
+  pdl_wait();
+  extern __shared__ uint8_t tc_raw[];
+  __shared__ uint64_t full[kTcUpMostStages], empty[kTcUpMostStages], done[2], taken[2];
+  __shared__ uint32_t tmem_at;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int across = (a.cols + kTcUpCols - 1) / kTcUpCols;
+  const int64_t units = (int64_t)__ldg(a.n_tiles) * across;
+  const int64_t per = (units + gridDim.x - 1) / gridDim.x, rounds = max((int64_t)1, per / kTcUpRun), run = (per + rounds - 1) / rounds;
+  int64_t u0 = blockIdx.x * run, u_end = min(units, u0 + run);
+  if (u0 >= units) return;
+  const int rank = a.rank, steps = tc_steps(rank), k_blocks = tc_blocks(rank), stages = tc_up_stages(rank), stage_bytes = tc_up_stage(rank);
+  uint8_t *hs = tc_raw + ((1024 - (su32(tc_raw) & 1023)) & 1023), *ring = hs + 2 * k_blocks * kTcRowBox;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kTcUpMostStages; ++s) {
+      mbar_init(&full[s], 32);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&done[s], 1);
+      mbar_init(&taken[s], kTcUpEpi / 32);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kTcUpThreads / 32 - 1) tmem_alloc(&tmem_at, 2 * kTcUpCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_at;
+  bool ok = true;
+  int s = 0, turn = 0;       // the stage in hand and how often the ring has been round, modulo 2
+  uint32_t g = 0;            // units with products so far
+  while (u0 < units) {
+    const int at = (int)(u0 / across), first = (int)(u0 - (int64_t)at * across);
+    const int items = (int)min((int64_t)(across - first), u_end - u0), col0 = first * kTcUpCols;
+    u0 += items;
+    if (u0 == u_end) {
+      u0 += (gridDim.x - 1) * run;
+      u_end = min(units, u0 + run);
+    }
+    const Tile tile = a.tiles[at];
+    const bool none = tile.adapter >= a.adapters;  // the base as it is
+    if (none && a.base == a.out) continue;
+    if (warp < kTcUpEpi / 32) {
+      const int first_row = 32 * (warp & 3), q = lane & 3, col = col0 + 64 * (warp >> 2) + 8 * q;
+      int32_t token[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = first_row + 8 * i + (lane >> 2);
+        token[i] = t < tile.count ? __ldg(a.order + tile.first + t) : -1;
+      }
+      uint4 base[2][4];
+      auto read = [&](int c, uint4 (&to)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          to[i] = a.base && token[i] >= 0 && c < a.cols
+                      ? *reinterpret_cast<const uint4 *>(reinterpret_cast<const bf16 *>(a.base) + token[i] * a.base_ld + c)
+                      : make_uint4(0, 0, 0, 0);
+      };
+      read(col, base[0]);
+      read(col + 32, base[1]);
+      if (!none) {  // h, when no product reads the tile's before any more: two threads have a row, eight ranks at a time; zeros
+                    // past the tile's rows and the rank
+        const float scale = a.scales ? a.scales[tile.adapter] : 1.f;
+        const int t = threadIdx.x >> 1;
+        const float *from = a.h + (int64_t)__ldg(a.order + tile.first + (t < tile.count ? t : 0)) * rank;
+        for (int e0 = threadIdx.x & 1; e0 < 2 * steps; e0 += 4) {
+          Pack<float, 16> v[2][2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              const int r = 8 * (e0 + 2 * u) + 4 * p;
+              v[u][p] = load_vec<float, 4>(from + (r < rank ? r : 0), t < tile.count ? rank - r : 0, a.h_wide);
+            }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int e8 = e0 + 2 * u;
+            if (e8 >= 2 * steps) break;
+            uint32_t w[4][2];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) cut_pair<2>(scale * v[u][p >> 1].get(2 * (p & 1)), scale * v[u][p >> 1].get(2 * (p & 1) + 1), w[p]);
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+              *reinterpret_cast<uint4 *>(hs + (p * k_blocks + (e8 >> 3)) * kTcRowBox + t * 128 + (((e8 & 7) ^ (t & 7)) << 4)) =
+                  make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+          }
+        }
+        fence_async_shared();
+        tc_rows_sync();
+      }
+      for (int i = 0; i < items; ++i) {
+        if (!none) {
+          ok = ok && mbar_wait(&done[g & 1], (g >> 1) & 1);
+          tc_fence_after();
+        }
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+          const int c = col + i * kTcUpCols + 32 * sub;
+          float v[2][16];
+          if (!none) {
+            const uint32_t from = tmem + ((uint32_t)first_row << 16) + (g & 1) * kTcUpCols + 64 * (warp >> 2) + 32 * sub;
+            tmem_ld_rows(from, v[0]);
+            tmem_ld_rows(from + (16u << 16), v[1]);
+            tmem_wait(v[0], v[1]);
+            if (sub == 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&taken[g & 1]);
+            }
+            if constexpr (!kAlong) {
+              turn_pairs(v[0], lane);
+              turn_pairs(v[1], lane);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float *x = &v[r >> 1][2 * (r & 1)];
+              uint32_t(&o)[4] = reinterpret_cast<uint32_t(&)[4]>(base[sub][r]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[j] = ok ? pack_pair(bf16_lo(o[j]) + x[4 * j], bf16_hi(o[j]) + x[4 * j + 1]) : 0x7FFF7FFFu;
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (token[r] >= 0 && c < a.cols) *reinterpret_cast<uint4 *>(reinterpret_cast<bf16 *>(a.out) + token[r] * a.out_ld + c) = base[sub][r];
+          if (i + 1 < items) read(c + kTcUpCols, base[sub]);
+        }
+        if (!none) ++g;
+      }
+    } else if (none) {
+      continue;
+    } else if (warp == kTcUpEpi / 32) {
+      const bf16 *mat = reinterpret_cast<const bf16 *>(a.m) + (int64_t)tile.adapter * rank * a.cols;
+      for (int i = 0; i < items; ++i, ++g) {
+        if (g >= (uint32_t)stages) ok = ok && mbar_wait(&empty[s], turn ^ 1);
+        uint8_t *to = ring + s * stage_bytes;
+        const int col = col0 + i * kTcUpCols, left = a.cols - col;
+        if constexpr (kAlong) {  // eight lanes have 128 bytes of a row, four rows at a time
+          const int c = lane & 7, r0 = lane >> 3;
+          for (int b = 0; b < k_blocks; ++b, to += kTcUpCols * 128) {
+            if (64 * b + 8 * c >= 16 * steps) break;
+            const int bytes = max(0, min(rank - 64 * b - 8 * c, 8)) * 2;
+#pragma unroll 8
+            for (int u = 0; u < kTcUpCols / 4; ++u) {
+              const int r = r0 + 4 * u, n = (r & ~31) + 8 * ((r >> 1) & 3) + 2 * ((r >> 3) & 3) + (r & 1), there = n < left ? bytes : 0;
+              copy_piece(to + r * 128 + ((c ^ (r & 7)) << 4), there ? mat + (int64_t)(col + n) * rank + 64 * b + 8 * c : mat, there, m_wide);
+            }
+          }
+        } else {  // 16 lanes have the 256 bytes of a row
+          const int c = lane & 15, r0 = lane >> 4, bytes = max(0, min(left - 8 * c, 8)) * 2;
+          to += (c >> 3) * k_blocks * 64 * 128;
+#pragma unroll 8
+          for (int k = r0; k < 16 * steps; k += 2) {
+            const int there = k < rank ? bytes : 0;
+            copy_piece(to + k * 128 + (((c & 7) ^ (k & 7)) << 4), there ? mat + (int64_t)k * a.cols + col + 8 * c : mat, there, m_wide);
+          }
+        }
+        fetch_commit();
+        if (stages == 1) {
+          fetch_wait<0>();
+          fence_async_shared();
+          mbar_arrive(&full[s]);
+        } else if (g > 0) {  // the one before is there
+          fetch_wait<1>();
+          fence_async_shared();
+          mbar_arrive(&full[s == 0 ? stages - 1 : s - 1]);
+        }
+        if (++s == stages) {
+          s = 0;
+          turn ^= 1;
+        }
+      }
+    } else {
+      tc_rows_sync();
+      constexpr uint32_t kInst = tc_inst(kTcTile, kTcUpCols, false, !kAlong);
+      for (int i = 0; i < items; ++i, ++g) {
+        ok = ok && mbar_wait(&full[s], turn) && (g < 2 || mbar_wait(&taken[g & 1], ((g >> 1) & 1) ^ 1));
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t h_at = su32(hs), b = su32(ring) + s * stage_bytes, d = tmem + (g & 1) * kTcUpCols;
+          for (int p = 1; p >= 0; --p)
+            for (int k = 0; k < steps; ++k)
+              tc_mma(d, tc_desc(h_at + (p * k_blocks + (k >> 2)) * kTcRowBox + (k & 3) * 32, 16),
+                     kAlong ? tc_desc(b + (k >> 2) * kTcUpCols * 128 + (k & 3) * 32, 16) : tc_desc(b + k * 2048, k_blocks * 64 * 128), kInst,
+                     p == 0 || k > 0);
+          tc_commit(&empty[s]);
+          tc_commit(&done[g & 1]);
+        }
+        __syncwarp();
+        if (++s == stages) {
+          s = 0;
+          turn ^= 1;
+        }
+      }
+    }
+  }
+  if (warp == kTcUpEpi / 32 && g > 0 && stages > 1) {
+    fetch_wait<0>();
+    fence_async_shared();
+    mbar_arrive(&full[s == 0 ? stages - 1 : s - 1]);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kTcUpThreads / 32 - 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 2 * kTcUpCols);
+  }
+}
+
+template <bool kAlong>
+cudaError_t launch_up_tc(const UpArgs &a, int tile_cap, int sms, cudaStream_t s) {
+  const size_t smem = tc_up_smem(a.rank);
+  const auto kernel = k_adapt_up_tc<kAlong>;
+  cudaError_t e = raise_smem_limit(kernel, smem);
+  if (e != cudaSuccess) return e;
+  const int m_wide = ptr_aligned(a.m, 16) && (kAlong ? a.rank : a.cols) % 8 == 0;
+  const int64_t most = tile_cap * ceil_div(a.cols, kTcUpCols), room = (int64_t)sms * (smem <= 113 * 1024 ? 2 : 1);
+  return launch_pdl(kernel, (unsigned)std::min(most, room), kTcUpThreads, smem, s, a, m_wide);
+}
+
+// ------------------------------------------------------------ dA and dB
+
+constexpr int kTcCols = 256;     // columns of a block: two tiles of 128, the lanes of TMEM
+constexpr int kTcRows = 32;      // rows (of K) per stage
+constexpr int kTcStages = 3;
+constexpr int kTcBox = kTcRows * 128;  // bytes of 64 columns of a stage
+__host__ __device__ constexpr int tc_outer_stage(int ranks) { return (kTcCols + 2 * ranks) / 64 * kTcBox; }
+constexpr size_t tc_outer_smem(int ranks) {
+  const size_t ring = (size_t)kTcStages * tc_outer_stage(ranks), sums = std::max((size_t)ranks * (kTcCols + 4), (size_t)kTcCols * (ranks + 4)) * 4;
+  return (ring > sums ? ring : sums) + 1024;
 }
 
 // The cluster's sums, kMajor rows of kMinor + 4, to rows `at_major` on and columns `at_minor` on of [major][minor]: this
