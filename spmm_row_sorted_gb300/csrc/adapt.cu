@@ -242,6 +242,14 @@ __device__ __forceinline__ void fetch_vec(void *to, const T *p, int left) {
     *reinterpret_cast<typename Raw<kBytes>::type *>(to) = r.raw;
   }
 }
+// of kernels for rows that are not all aligned: these may be
+template <typename T, int V, bool kWide>
+__device__ __forceinline__ void fetch_some(void *to, const T *p, int left, int wide) {
+  if (kWide || wide)
+    fetch_vec<T, V, true>(to, p, left);
+  else
+    fetch_vec<T, V, false>(to, p, left);
+}
 __device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
 __device__ __forceinline__ void fetch_wait() {
@@ -360,6 +368,7 @@ struct DownArgs {
   int32_t adapters;
   const float *scales;  // null: 1
   float *h;             // [n][rank]
+  int x_wide, m_wide;   // the rows, the matrices are aligned to whole accesses
 };
 
 constexpr int kDownParts = 8;  // shares of K in a block: a warp each, or a pair that shares the rows' part and has half the
@@ -373,7 +382,7 @@ __host__ __device__ constexpr int down_smem(int cols) {
 
 // The sums of the block's shares of K, and of the cluster's blocks; NT: a warp's ranks / 8.
 template <typename T, int MT, int NT, int kHalves, bool kAlong, bool kWide>
-__device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, float *smem) {
+__device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, int slice, float *smem) {
   typedef Op<T> O;
   constexpr int kRows = 16 * MT, kCols = 8 * NT * kHalves, kStages = down_stages(kCols), kSlots = kTile / 8 + NT * kHalves;
   constexpr int kThreads = kDownParts * kHalves * 32;
@@ -381,7 +390,7 @@ __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, f
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int part = warp / kHalves, half = warp % kHalves;
   const int g = lane >> 2, q = lane & 3;
-  const int r0 = blockIdx.y * kCols + half * 8 * NT;
+  const int r0 = slice * kCols + half * 8 * NT;
   const uint32_t rank = cluster_rank(), blocks = cluster_blocks();
   float acc[MT][NT][4];
 #pragma unroll
@@ -396,7 +405,7 @@ __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, f
 #pragma unroll
   for (int i = 0; i < kRead; ++i)
     row[i] = reinterpret_cast<const T *>(a.x) +
-             (int64_t)__ldg(a.order + tile.first + min(8 * (half * kRead + i) + g, tile.count - 1)) * a.x_ld + O::kLane * q;
+             (int64_t)a.order[tile.first + min(8 * (half * kRead + i) + g, tile.count - 1)] * a.x_ld + O::kLane * q;
   const T *mat = reinterpret_cast<const T *>(a.m) + (int64_t)tile.adapter * a.rank * a.k;
   // the part's ring: kStages x (of the rows 16 bytes of every 8th per lane; then each warp's of the matrix NT of them, or
   // the same bytes in smaller pieces)
@@ -410,21 +419,21 @@ __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, f
       uint4 *to = ring + stage * kSlots * 32 + lane;
       const int left = a.k - next - O::kLane * q;
 #pragma unroll
-      for (int i = 0; i < kRead; ++i) fetch_vec<T, O::kLane, kWide>(to + (half * kRead + i) * 32, row[i] + next, left);
+      for (int i = 0; i < kRead; ++i) fetch_some<T, O::kLane, kWide>(to + (half * kRead + i) * 32, row[i] + next, left, a.x_wide);
       to += (kTile / 8 + half * NT) * 32;
       if constexpr (kAlong) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const int r = r0 + 8 * j + g;
-          fetch_vec<T, O::kLane, kWide>(to + j * 32, mat + (int64_t)min(r, a.rank - 1) * a.k + next + O::kLane * q, r < a.rank ? left : 0);
+          fetch_some<T, O::kLane, kWide>(to + j * 32, mat + (int64_t)min(r, a.rank - 1) * a.k + next + O::kLane * q, r < a.rank ? left : 0, a.m_wide);
         }
       } else {  // rows next + kLane q + i: ranks NT g .. NT g + NT - 1
         typename Cross::R *piece = reinterpret_cast<typename Cross::R *>(to - lane) + lane;
         const int ranks = a.rank - r0 - NT * g;
 #pragma unroll
         for (int i = 0; i < O::kLane; ++i)
-          fetch_vec<T, NT, kWide>(piece + i * 32, mat + (int64_t)min(next + O::kLane * q + i, a.k - 1) * a.rank + (ranks > 0 ? r0 + NT * g : 0),
-                                  i < left ? ranks : 0);
+          fetch_some<T, NT, kWide>(piece + i * 32, mat + (int64_t)min(next + O::kLane * q + i, a.k - 1) * a.rank + (ranks > 0 ? r0 + NT * g : 0),
+                                   i < left ? ranks : 0, a.m_wide);
       }
     }
     fetch_commit();
@@ -505,7 +514,7 @@ __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, f
     __syncthreads();
   const float scale = a.scales ? a.scales[tile.adapter] : 1.f;
   for (int i = (int)rank * kThreads + threadIdx.x; i < tile.count * kCols; i += (int)blocks * kThreads) {
-    const int t = i / kCols, r = blockIdx.y * kCols + i % kCols;
+    const int t = i / kCols, r = slice * kCols + i % kCols;
     float s = smem[i];
     if (blocks > 1) {
       s = ld_cluster(smem + i, 0);
@@ -523,9 +532,9 @@ __global__ void __launch_bounds__(kDownParts * kHalves * 32, 1) k_adapt_down(con
   const Tile tile = a.tiles[blockIdx.x / cluster_blocks()];
   if (tile.adapter < 0 || tile.adapter >= a.adapters) return;  // the whole cluster's
   if (tile.count <= 16)
-    down_tile<T, 1, NT, kHalves, kAlong, kWide>(a, tile, down_ring);
+    down_tile<T, 1, NT, kHalves, kAlong, kWide>(a, tile, blockIdx.y, down_ring);
   else
-    down_tile<T, 4, NT, kHalves, kAlong, kWide>(a, tile, down_ring);
+    down_tile<T, 4, NT, kHalves, kAlong, kWide>(a, tile, blockIdx.y, down_ring);
 }
 
 // ------------------------------------------------------------ y and dx
@@ -544,7 +553,7 @@ struct UpArgs {
   int64_t out_ld;
   int groups;            // of 32 columns, per warp
   const int32_t *n_tiles;
-  int h_wide;
+  int h_wide, m_wide;    // h, the matrices are aligned to four elements
 };
 
 constexpr int kUpWarps = 8;     // pairs of them: half of the tile's rows each
@@ -572,6 +581,25 @@ static_assert(kUpWarps * up_stages<bf16>() * up_stage_bytes<bf16, 4>() * 32 + up
                   kUpWarps * up_stages<float>() * up_stage_bytes<float, 1>() * 32 + up_h_bytes<float>(kMostRank) <= 232448,
               "shared memory of one block");
 
+// four values of h, which another block of the cluster may have written
+__device__ __forceinline__ Pack<float, 16> load_h(const float *p, int left, bool wide) {
+  Pack<float, 16> r;
+  if (wide && left >= 4) {
+    r.raw = __ldcg(reinterpret_cast<const uint4 *>(p));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = i < left ? __float_as_uint(__ldcg(p + i)) : 0u;
+  }
+  return r;
+}
+
+// where the pieces of a stage have column `col` of a warp's row 8 i + r
+template <typename T>
+__device__ __forceinline__ int place_of(int i, int r, int col) {
+  constexpr int kPer = 16 / (int)sizeof(T);
+  return ((i * (8 / kPer) + (col & 7) / kPer) * 32 + 4 * r + (col >> 3)) * 16 + (col & 7) % kPer * (int)sizeof(T);
+}
+
 // A pair of warps takes 32 columns of the tile after 32 others; what it reads of the base
 // and the matrix is on its way one or two turns before, kSteps of 16 of the rank per turn.
 // The sums begin with the base, so the result is rounded as it leaves; h has its
@@ -579,7 +607,7 @@ static_assert(kUpWarps * up_stages<bf16>() * up_stage_bytes<bf16, 4>() * 32 + up
 //
 // kWhole: 64 rows, whole groups of columns and steps of the rank: nothing to check.
 template <typename T, bool kAlong, int kSteps, bool kWide, bool kWhole>
-__device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, uint8_t *up_ring) {
+__device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, int slice, uint8_t *up_ring) {
   constexpr int kHp = Op<T>::kOwnParts, kBp = Op<T>::kParts, MT = kTile / 32, NT = 4, kStages = up_stages<T>();
   typedef Pack<T, 16> P;
   typedef Pack<T, 4 * (int)sizeof(T)> P4;
@@ -594,14 +622,14 @@ __device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, uint8
   uint8_t *ring = up_ring + pair * kStages * kStage;
   uint32_t *hs = reinterpret_cast<uint32_t *>(up_ring + kUpWarps * kStages * kStage);
   const T *mat = reinterpret_cast<const T *>(a.m) + (none ? 0 : (int64_t)tile.adapter * a.rank * a.cols);
-  const int col0 = (blockIdx.y * a.groups * kUpWarps + pair) * kUpCols;
+  const int col0 = (slice * a.groups * kUpWarps + pair) * kUpCols;
   // this lane's rows, from its 8 columns on
   int32_t token[2 * MT];
   const T *base[2 * MT];
 #pragma unroll
   for (int i = 0; i < 2 * MT; ++i) {
     const int t = first_row + 8 * i + g;
-    token[i] = kWhole || t < tile.count ? __ldg(a.order + tile.first + t) : -1;
+    token[i] = kWhole || t < tile.count ? a.order[tile.first + t] : -1;
     base[i] = reinterpret_cast<const T *>(a.base) + (int64_t)max(token[i], 0) * a.base_ld + col0 + 8 * q;
   }
   const int items = (a.cols <= col0 ? 0 : min(a.groups, (a.cols - col0 + kUpWarps * kUpCols - 1) / (kUpWarps * kUpCols))) * turns;
@@ -611,17 +639,40 @@ __device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, uint8
       uint8_t *to = ring + next_stage * kStage;
       const int left = a.cols - next_col - 8 * q;
       if (next_turn == 0 && a.base) {
-        uint4 *at = reinterpret_cast<uint4 *>(to) + half * (2 * MT * kVecs) * 32 + lane;
+        uint8_t *part = to + half * (2 * MT * kVecs) * 512;
+        if constexpr (kWide) {
+          uint4 *at = reinterpret_cast<uint4 *>(part) + lane;
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) {
-          if (i >= 2 * m_tiles) break;
-          const T *from = base[i] + (next_col - col0);
+          for (int i = 0; i < 2 * MT; ++i) {
+            if (i >= 2 * m_tiles) break;
+            const T *from = base[i] + (next_col - col0);
 #pragma unroll
-          for (int v = 0; v < kVecs; ++v) {
-            if constexpr (kWhole)
-              copy_whole<16>(at + (i * kVecs + v) * 32, from + v * kPer);
-            else
-              fetch_vec<T, kPer, kWide>(at + (i * kVecs + v) * 32, from + v * kPer, left - v * kPer);
+            for (int v = 0; v < kVecs; ++v) {
+              if constexpr (kWhole)
+                copy_whole<16>(at + (i * kVecs + v) * 32, from + v * kPer);
+              else
+                fetch_vec<T, kPer, true>(at + (i * kVecs + v) * 32, from + v * kPer, left - v * kPer);
+            }
+          }
+        } else {  // a row's 32 columns by the warp, one each
+          const int c = next_col + lane;
+#pragma unroll
+          for (int i = 0; i < 2 * MT; ++i) {
+            if (i >= 2 * m_tiles) break;
+            T kept[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+              const int row = __shfl_sync(0xffffffffu, token[i], 4 * r);
+              const bool in = row >= 0 && c < a.cols;
+              const T *from = reinterpret_cast<const T *>(a.base) + (in ? row * a.base_ld + c : 0);
+              if constexpr (sizeof(T) == 4)
+                copy_async<4>(part + place_of<T>(i, r, lane), from, in ? 4 : 0);
+              else
+                kept[r] = in ? *from : from_f32<T>(0.f);
+            }
+            if constexpr (sizeof(T) == 2)
+#pragma unroll
+              for (int r = 0; r < 8; ++r) *reinterpret_cast<T *>(part + place_of<T>(i, r, lane)) = kept[r];
           }
         }
       }
@@ -638,15 +689,15 @@ __device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, uint8
               if constexpr (kWhole)
                 copy_whole<4 * (int)sizeof(T)>(at + (4 * s + j) * 32, mat + (int64_t)col * a.rank + r);
               else
-                fetch_vec<T, 4, kWide>(at + (4 * s + j) * 32, mat + (int64_t)min(col, a.cols - 1) * a.rank + (r < a.rank ? r : 0),
-                                       col < a.cols ? a.rank - r : 0);
+                fetch_some<T, 4, kWide>(at + (4 * s + j) * 32, mat + (int64_t)min(col, a.cols - 1) * a.rank + (r < a.rank ? r : 0),
+                                        col < a.cols ? a.rank - r : 0, a.m_wide);
             } else {  // columns 4 g .. 4 g + 3
               const int r = r0 + 16 * s + j, col = next_col + 4 * g;
               if constexpr (kWhole)
                 copy_whole<4 * (int)sizeof(T)>(at + (4 * s + j) * 32, mat + (int64_t)r * a.cols + col);
               else
-                fetch_vec<T, 4, kWide>(at + (4 * s + j) * 32, mat + (int64_t)min(r, a.rank - 1) * a.cols + (col < a.cols ? col : 0),
-                                       r < a.rank ? a.cols - col : 0);
+                fetch_some<T, 4, kWide>(at + (4 * s + j) * 32, mat + (int64_t)min(r, a.rank - 1) * a.cols + (col < a.cols ? col : 0),
+                                        r < a.rank ? a.cols - col : 0, a.m_wide);
             }
           }
       }
@@ -667,7 +718,7 @@ __device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, uint8
     for (int i = threadIdx.x; i < rows * quads; i += kUpWarps * 64) {
       const int t = i / quads, r = (i - t * quads) * 4;
       const bool in = t < tile.count;
-      const auto v = load_vec<float, 4>(a.h + (int64_t)(in ? __ldg(a.order + tile.first + t) : 0) * a.rank + r, in ? a.rank - r : 0, a.h_wide);
+      const Pack<float, 16> v = load_h(a.h + (int64_t)(in ? a.order[tile.first + t] : 0) * a.rank + r, in ? a.rank - r : 0, a.h_wide);
       if constexpr (sizeof(T) == 4) {
         *reinterpret_cast<float4 *>(hs + t * up_ld<T>(a.rank) + r) =
             make_float4(scale * v.get(0), scale * v.get(1), scale * v.get(2), scale * v.get(3));
@@ -755,10 +806,11 @@ __device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, uint8
     if (++turn < turns) continue;
     turn = 0;
     const int left = a.cols - c;
+    uint8_t *part = const_cast<uint8_t *>(from) + half * (2 * MT * kVecs) * 512;  // !kWide: the stage's, read already
 #pragma unroll
     for (int i = 0; i < 2 * MT; ++i) {
       if (i >= 2 * m_tiles) break;
-      if (!kWhole && (token[i] < 0 || left <= 0)) continue;
+      if (kWide && !kWhole && (token[i] < 0 || left <= 0)) continue;
       T *out = reinterpret_cast<T *>(a.out) + token[i] * a.out_ld + c;
 #pragma unroll
       for (int v = 0; v < kVecs; ++v) {
@@ -770,8 +822,10 @@ __device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, uint8
 #pragma unroll
           for (int e = 0; e < kPer; ++e) o.set(e, sum_at(i >> 1, i & 1, v * kPer + e));
         }
-        if constexpr (kWide) {  // all of it or nothing: whole accesses make up a row
-          if (kWhole || left >= (v + 1) * kPer) *reinterpret_cast<uint4 *>(out + v * kPer) = o.raw;
+        if constexpr (!kWide) {
+          reinterpret_cast<uint4 *>(part)[(i * kVecs + v) * 32 + lane] = o.raw;
+        } else if (kWhole || left >= (v + 1) * kPer) {
+          *reinterpret_cast<uint4 *>(out + v * kPer) = o.raw;
         } else {
 #pragma unroll
           for (int e = 0; e < kPer; ++e)
@@ -783,6 +837,21 @@ __device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, uint8
             }
         }
       }
+    }
+    if constexpr (!kWide) {  // a row's 32 columns by the warp, one each
+      __syncwarp();
+      const int own = c - 8 * q + lane;
+#pragma unroll
+      for (int i = 0; i < 2 * MT; ++i) {
+        if (i >= 2 * m_tiles) break;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const int row = __shfl_sync(0xffffffffu, token[i], 4 * r);
+          if (row >= 0 && own < a.cols)
+            reinterpret_cast<T *>(a.out)[row * a.out_ld + own] = *reinterpret_cast<const T *>(part + place_of<T>(i, r, lane));
+        }
+      }
+      __syncwarp();
     }
     c += kUpWarps * kUpCols;
   }
@@ -798,11 +867,62 @@ __global__ void __launch_bounds__(kUpWarps * 64, 1) k_adapt_up(const UpArgs a) {
   if (none && a.base == a.out) return;
   if constexpr (kWide) {
     if (!none && tile.count == kTile && a.cols % kUpCols == 0 && a.rank % (16 * kSteps) == 0) {
-      up_tile<T, kAlong, kSteps, true, true>(a, tile, up_ring);
+      up_tile<T, kAlong, kSteps, true, true>(a, tile, blockIdx.y, up_ring);
       return;
     }
   }
-  up_tile<T, kAlong, kSteps, kWide, false>(a, tile, up_ring);
+  up_tile<T, kAlong, kSteps, kWide, false>(a, tile, blockIdx.y, up_ring);
+}
+
+// ------------------------------------------------------------ few rows
+
+// Of few rows both products in one launch, without the rows' order in memory: a cluster per row, which goes on if its row
+// is the first of up to 64 with its adapter; its blocks share K, then the columns.  bf16 of 4096 to 4096, from cold caches:
+// one row of rank 16 11 us, 64 of 64 requests 15 (the three launches 22 and 32); 256 rows of two requests, rank 64, 33 (26):
+// more rows of a higher rank are for the others.
+constexpr int kFewRows = 256;
+constexpr int kFewThreads = 512;
+static_assert(kFewThreads == kUpWarps * 64 && kFewThreads == kDownParts * 64, "both products' threads");
+
+template <typename T, int NT, int kSteps, bool kWide>
+__global__ void __launch_bounds__(kFewThreads, 1) k_adapt_few(const DownArgs down, const UpArgs up, TokenSrc which, int n) {
+  pdl_wait();
+  extern __shared__ __align__(16) uint8_t few_ring[];
+  __shared__ int32_t rows[kTile];
+  __shared__ int32_t found[kFewRows / 32];
+  const int i = (int)(blockIdx.x / cluster_blocks()), j = threadIdx.x, lane = j & 31, warp = j >> 5;
+  const uint32_t own = which.key(i);
+  const bool same = j < n && which.key(j) == own;
+  if (__syncthreads_count(same && j < i) % kTile != 0) return;  // the whole cluster's
+  const bool mine = same && j >= i;
+  const unsigned peers = __ballot_sync(0xffffffffu, mine);
+  if (lane == 0 && warp < kFewRows / 32) found[warp] = __popc(peers);
+  __syncthreads();
+  int at = __popc(peers & ((1u << lane) - 1u)), count = 0;
+#pragma unroll
+  for (int w = 0; w < kFewRows / 32; ++w) {
+    if (w < warp) at += found[w];
+    count += found[w];
+  }
+  if (mine && at < kTile) rows[at] = j;
+  __syncthreads();
+  const Tile tile = {(int32_t)own, 0, min(count, kTile), 0};
+  if (tile.adapter < down.adapters) {
+    DownArgs a = down;
+    a.order = rows;
+    for (int slice = 0; slice * 16 * NT < a.rank; ++slice) {
+      if (tile.count <= 16)
+        down_tile<T, 1, NT, 2, true, kWide>(a, tile, slice, reinterpret_cast<float *>(few_ring));
+      else
+        down_tile<T, 4, NT, 2, true, kWide>(a, tile, slice, reinterpret_cast<float *>(few_ring));
+      __syncthreads();
+    }
+  } else if (up.base == up.out) {
+    return;
+  }
+  UpArgs a = up;  // h is there: down_tile ends with the cluster's barrier
+  a.order = rows;
+  up_tile<T, true, kSteps, kWide, false>(a, tile, (int)cluster_rank(), few_ring);
 }
 
 // ------------------------------------------------------------ dA and dB
@@ -1078,12 +1198,18 @@ cudaError_t launch_down(const DownArgs &a, int64_t n, int tile_cap, int sms, cud
   const unsigned c = cluster_for(likely_tiles(n, a.adapters, kTile) * slices, ceil_div(a.k, Op<T>::kGroup * kDownParts), sms);
   return launch_cluster(c, kernel, dim3((unsigned)tile_cap * c, slices), kDownParts * kHalves * 32, smem, s, a);
 }
-template <typename T, int NT, int kHalves, bool kAlong>
-cudaError_t down_by(const DownArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
+// whole accesses of 16 bytes of the rows and of a matrix that runs along K, of `across` elements of one that does not
+template <typename T, bool kAlong>
+bool down_wide(DownArgs *a, int across) {
   const size_t es = sizeof(T);
-  const bool wide = row_wide(a.x, a.x_ld, es) && (kAlong ? row_wide(a.m, a.k, es) : ptr_aligned(a.m, NT * es) && a.rank % NT == 0);
-  return wide ? launch_down<T, NT, kHalves, kAlong, true>(a, n, tile_cap, sms, s)
-              : launch_down<T, NT, kHalves, kAlong, false>(a, n, tile_cap, sms, s);
+  a->x_wide = row_wide(a->x, a->x_ld, es);
+  a->m_wide = kAlong ? row_wide(a->m, a->k, es) : ptr_aligned(a->m, across * es) && a->rank % across == 0;
+  return a->x_wide && a->m_wide;
+}
+template <typename T, int NT, int kHalves, bool kAlong>
+cudaError_t down_by(DownArgs a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
+  return down_wide<T, kAlong>(&a, NT) ? launch_down<T, NT, kHalves, kAlong, true>(a, n, tile_cap, sms, s)
+                                      : launch_down<T, NT, kHalves, kAlong, false>(a, n, tile_cap, sms, s);
 }
 template <typename T, bool kAlong>
 cudaError_t down(const DownArgs &a, int64_t n, int tile_rows, int tile_cap, int sms, cudaStream_t s) {
@@ -1109,13 +1235,16 @@ cudaError_t launch_up(UpArgs a, int64_t n, int tile_cap, int sms, cudaStream_t s
   a.groups = (int)groups;
   return launch_pdl(kernel, dim3((unsigned)tile_cap, (unsigned)ceil_div(all, groups)), kUpWarps * 64, smem, s, (const UpArgs)a);
 }
-template <typename T, bool kAlong, int kSteps>
-cudaError_t up_by(const UpArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
+// whole accesses of 16 bytes of the rows, of four elements of the matrix
+template <typename T, bool kAlong>
+bool up_wide(UpArgs *a) {
   const size_t es = sizeof(T);
-  // whole accesses of 16 bytes of the rows, of four elements of the matrix
-  const bool wide = row_wide(a.base, a.base_ld, es) && row_wide(a.out, a.out_ld, es) && (size_t)a.cols * es % 16 == 0 &&
-                    ptr_aligned(a.m, 4 * es) && (kAlong ? a.rank : a.cols) % 4 == 0;
-  return wide ? launch_up<T, kAlong, kSteps, true>(a, n, tile_cap, sms, s) : launch_up<T, kAlong, kSteps, false>(a, n, tile_cap, sms, s);
+  a->m_wide = ptr_aligned(a->m, 4 * es) && (kAlong ? a->rank : a->cols) % 4 == 0;
+  return row_wide(a->base, a->base_ld, es) && row_wide(a->out, a->out_ld, es) && a->m_wide;
+}
+template <typename T, bool kAlong, int kSteps>
+cudaError_t up_by(UpArgs a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
+  return up_wide<T, kAlong>(&a) ? launch_up<T, kAlong, kSteps, true>(a, n, tile_cap, sms, s) : launch_up<T, kAlong, kSteps, false>(a, n, tile_cap, sms, s);
 }
 template <typename T, bool kAlong>
 cudaError_t up(const UpArgs &a, int64_t n, int tile_rows, int tile_cap, int sms, cudaStream_t s) {
@@ -1127,6 +1256,25 @@ cudaError_t up(const UpArgs &a, int64_t n, int tile_rows, int tile_cap, int sms,
     return up_by<T, kAlong, 2>(a, n, tile_cap, sms, s);
   }
   return cudaErrorInvalidValue;
+}
+
+template <typename T, int NT, int kSteps, bool kWide>
+cudaError_t launch_few(const DownArgs &d, UpArgs u, const TokenSrc &which, int n, int sms, cudaStream_t s) {
+  const size_t smem = std::max((size_t)down_smem(16 * NT),
+                               (size_t)kUpWarps * up_stages<T>() * up_stage_bytes<T, kSteps>() * 32 + up_h_bytes<T>(u.rank));
+  const auto kernel = k_adapt_few<T, NT, kSteps, kWide>;
+  cudaError_t e = raise_smem_limit(kernel, smem);
+  if (e != cudaSuccess) return e;
+  const unsigned c = cluster_for(std::min<int64_t>(n, (int64_t)d.adapters + 1), ceil_div(d.k, Op<T>::kGroup * kDownParts), sms);
+  u.groups = (int)ceil_div(u.cols, (int64_t)c * kUpWarps * kUpCols);
+  return launch_cluster(c, kernel, dim3((unsigned)n * c), kFewThreads, smem, s, d, (const UpArgs)u, which, n);
+}
+template <typename T>
+cudaError_t few(DownArgs d, UpArgs u, const TokenSrc &which, int n, int sms, cudaStream_t s) {
+  const bool wide_in = down_wide<T, true>(&d, 8), wide = up_wide<T, true>(&u) && wide_in;
+  constexpr int kSteps = sizeof(T) == 2 ? 2 : 1;
+  if (d.rank <= 16) return wide ? launch_few<T, 1, 1, true>(d, u, which, n, sms, s) : launch_few<T, 1, 1, false>(d, u, which, n, sms, s);
+  return wide ? launch_few<T, 2, kSteps, true>(d, u, which, n, sms, s) : launch_few<T, 2, kSteps, false>(d, u, which, n, sms, s);
 }
 
 template <typename T, int MT, bool kWide>
@@ -1173,14 +1321,13 @@ struct Span {
 };
 bool overlaps(const Span &a, const Span &b) { return spans_overlap(a.p, a.bytes, b.p, b.bytes); }
 
-// Rows of a tile: of bf16 whose rows (dx's and y's whole ones) lie on 16 bytes, and the matrices' on 8, those of TMEM.
+// Rows of a tile: of bf16 whose rows lie on 16 bytes, and the matrices' on 8, those of TMEM.
 bool on8(const void *m, int32_t ld) { return ptr_aligned(m, 8) && ld % 4 == 0; }
 int down_tile_rows(const DownArgs &d, int32_t m_ld, snack_dtype t) {
   return t == SNACK_BF16 && row_wide(d.x, d.x_ld, 2) && on8(d.m, m_ld) ? kTcTile : kTile;
 }
 int up_tile_rows(const UpArgs &u, int32_t m_ld, snack_dtype t) {
-  return t == SNACK_BF16 && row_wide(u.base, u.base_ld, 2) && row_wide(u.out, u.out_ld, 2) && u.cols % 8 == 0 && on8(u.m, m_ld) ? kTcTile
-                                                                                                                               : kTile;
+  return t == SNACK_BF16 && row_wide(u.base, u.base_ld, 2) && row_wide(u.out, u.out_ld, 2) && on8(u.m, m_ld) ? kTcTile : kTile;
 }
 
 template <typename T>
@@ -1270,8 +1417,13 @@ snack_status snack_adapt_fwd(const void *x, int64_t x_ld, int64_t n, const void 
   u.out = y;
   u.out_ld = y_ld;
   u.h_wide = rank % 4 == 0 && ptr_aligned(d.h, 16);
+  const TokenSrc ids{which, which_t == SNACK_I64, (uint32_t)n_adapters};
+  if (n <= (rank <= 32 ? kFewRows : kFewRows / 4)) {
+    ADAPT_CUDA(t == SNACK_F32 ? few<float>(d, u, ids, (int)n, sms, s) : few<bf16>(d, u, ids, (int)n, sms, s));
+    return SNACK_OK;
+  }
   const int rows = std::min(down_tile_rows(d, in_f, t), up_tile_rows(u, rank, t));
-  ADAPT_CUDA(launch_group(TokenSrc{which, which_t == SNACK_I64, (uint32_t)n_adapters}, (int)n, rows, w, W, s));
+  ADAPT_CUDA(launch_group(ids, (int)n, rows, w, W, s));
   ADAPT_CUDA(t == SNACK_F32 ? run_fwd<float>(d, u, n, rows, W, sms, s) : run_fwd<bf16>(d, u, n, rows, W, sms, s));
   return SNACK_OK;
 } catch (...) {  // a host allocation failed

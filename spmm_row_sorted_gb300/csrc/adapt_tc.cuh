@@ -381,10 +381,19 @@ __global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a,
       uint4 base[2][4];
       auto read = [&](int c, uint4 (&to)[4]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          to[i] = a.base && token[i] >= 0 && c < a.cols
-                      ? *reinterpret_cast<const uint4 *>(reinterpret_cast<const bf16 *>(a.base) + token[i] * a.base_ld + c)
-                      : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 4; ++i) {
+          to[i] = make_uint4(0, 0, 0, 0);
+          if (!a.base || token[i] < 0 || c >= a.cols) continue;
+          const uint16_t *from = reinterpret_cast<const uint16_t *>(a.base) + token[i] * a.base_ld + c;
+          if (c + 8 <= a.cols) {
+            to[i] = *reinterpret_cast<const uint4 *>(from);
+          } else {
+            uint16_t v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = c + e < a.cols ? from[e] : (uint16_t)0;
+            to[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+          }
+        }
       };
       read(col, base[0]);
       read(col + 32, base[1]);
@@ -451,7 +460,17 @@ __global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a,
           }
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            if (token[r] >= 0 && c < a.cols) *reinterpret_cast<uint4 *>(reinterpret_cast<bf16 *>(a.out) + token[r] * a.out_ld + c) = base[sub][r];
+            if (token[r] >= 0 && c < a.cols) {
+              uint16_t *to = reinterpret_cast<uint16_t *>(a.out) + token[r] * a.out_ld + c;
+              if (c + 8 <= a.cols) {
+                *reinterpret_cast<uint4 *>(to) = base[sub][r];
+              } else {
+                const uint32_t w[4] = {base[sub][r].x, base[sub][r].y, base[sub][r].z, base[sub][r].w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  if (c + e < a.cols) to[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+              }
+            }
           if (i + 1 < items) read(c + kTcUpCols, base[sub]);
         }
         if (!none) ++g;

@@ -323,3 +323,47 @@ def test_sparse_layer_with_adapters():
     # autograd adds two rounded parts where the call adds once: an addition's rounding apart
     assert bool(((x.grad - got[0]).abs() <= 2.0 ** -22 * (x.grad.abs() + 2 * layer.grad_input(c.dy).abs())).all())
     layer.close()
+
+
+# rows by the hundred: tiles of 128, several columns' units and tiles per block, tails of columns, every step of the rank
+MANY = [
+    # n, adapters, rank, width, out, dtype, kind, gap
+    (700, 3, 4, 72, 1160, "bf16", "mixed", 0),
+    (513, 2, 12, 136, 1032, "bf16", "runs", 0),
+    (1030, 4, 16, 200, 2048, "bf16", "mixed", 8),
+    (700, 3, 48, 264, 1043, "bf16", "runs", 5),      # the last columns of a row short of an access
+    (641, 2, 64, 128, 3080, "bf16", "mixed", 0),
+    (700, 3, 100, 1000, 520, "bf16", "runs", 0),     # the matrix's rows on 8 bytes
+    (513, 2, 128, 192, 264, "bf16", "mixed", 0),
+    (400, 2, 192, 96, 392, "bf16", "runs", 0),
+    (400, 2, 256, 264, 392, "bf16", "mixed", 0),
+    (700, 3, 7, 200, 264, "bf16", "runs", 0),        # the matrix's rows on 2
+    (600, 2, 20, 161, 333, "bf16", "mixed", 3),
+    (600, 2, 20, 161, 333, "f32", "mixed", 3),
+    (600, 2, 40, 160, 334, "f32", "runs", 2),
+]
+
+
+@pytest.mark.parametrize("n,adapters,rank,width,out,dtype,kind,gap", MANY)
+def test_adapt_of_many_rows_matches_definition(n, adapters, rank, width, out, dtype, kind, gap):
+    c = Case(n, adapters, rank, width, out, dtype, kind, gap, seed=n)
+    val, mag = c.want()
+    rel = bounds(c)
+    y, h = snack.adapt(c.x, c.base, *c.args(), c.scales, keep=True)
+    check(y, val[0], mag[0], rel[0], "y")
+    outside = (c.which < 0) | (c.which >= adapters)
+    assert torch.equal(y[outside], c.base[outside])
+    held = strided(n, out, gap, 0, c.x.dtype, n + 2)  # the base's values, to be overwritten
+    wide = held._base if held._base is not None else held
+    gaps = torch.isnan(wide).sum()
+    assert torch.equal(snack.adapt(c.x, held, *c.args(), c.scales, out=held), y) and torch.isnan(wide).sum() == gaps
+    assert torch.equal(snack.adapt(c.x, None, *c.args(), c.scales), snack.adapt(c.x, torch.zeros_like(c.base), *c.args(), c.scales))
+    dx, da, db = snack.adapt_grad(c.x, c.dy, *c.args(), h, c.scales)
+    for got, i, what in ((dx, 1, "dx"), (da, 2, "da"), (db, 3, "db")):
+        check(got, val[i], mag[i], rel[i], what)
+    assert bool((dx[outside] == 0).all())
+    into = strided(n, width, gap, 0, c.x.dtype, n + 9)
+    start = into.clone()
+    snack.adapt_grad(c.x, c.dy, *c.args(), h, c.scales, dx=into)
+    check(into, val[1] + start.double(), mag[1] + start.double().abs(), rel[1], "dx added")
+    assert torch.equal(into[outside], start[outside])
