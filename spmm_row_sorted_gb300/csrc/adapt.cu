@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
   for (int i = threadIdx.x; i < warps * groups; i += kGroupThreads) hist[i] = 0;
   __syncthreads();
   uint32_t kept[kGroupKeep];
+  unsigned peers[kGroupKeep];
   auto pass = [&](bool place) {
     if (warp >= warps) return;
     int32_t *mine = hist + (int64_t)warp * groups;
@@ -109,16 +110,18 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
           const int64_t i = first + (int64_t)(r0 + u) * 32 + lane;
           kept[u] = r0 + u < rounds && i < n ? which.key(i) : 0xFFFFFFFFu;
         }
+#pragma unroll
+        for (int u = 0; u < kGroupKeep; ++u)
+          if (r0 + u < rounds) peers[u] = __match_any_sync(0xffffffffu, kept[u]);
       }
 #pragma unroll
       for (int u = 0; u < kGroupKeep; ++u) {
         if (r0 + u >= rounds) break;
-        const unsigned peers = __match_any_sync(0xffffffffu, kept[u]);
         const bool here = kept[u] != 0xFFFFFFFFu;
         const int at = here ? mine[kept[u]] : 0;
         __syncwarp();
-        if (here && (peers & below) == 0) mine[kept[u]] = at + __popc(peers);
-        if (here && place) order[at + __popc(peers & below)] = (int32_t)(first + (int64_t)(r0 + u) * 32 + lane);
+        if (here && (peers[u] & below) == 0) mine[kept[u]] = at + __popc(peers[u]);
+        if (here && place) order[at + __popc(peers[u] & below)] = (int32_t)(first + (int64_t)(r0 + u) * 32 + lane);
         __syncwarp();
       }
     }
@@ -130,10 +133,15 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
     const int g = g0 + threadIdx.x;
     int count = 0;
     if (g < groups)
-      for (int w = 0; w < warps; ++w) {
-        const int c = hist[w * groups + g];
-        hist[w * groups + g] = count;
-        count += c;
+      for (int w0 = 0; w0 < warps; w0 += 8) {  // eight reads in flight
+        int c[8];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) c[w] = w0 + w < warps ? hist[(w0 + w) * groups + g] : 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          if (w0 + w < warps) hist[(w0 + w) * groups + g] = count;
+          count += c[w];
+        }
       }
     const int own = (count + tile_rows - 1) / tile_rows;
     int2 inc = make_int2(count, own);
@@ -147,19 +155,32 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
     }
     if (lane == 31) warp_sum[warp] = inc;
     __syncthreads();
-    int2 before = carry;
-    for (int w = 0; w < kGroupThreads / 32; ++w) {
-      if (w < warp) {
-        before.x += warp_sum[w].x;
-        before.y += warp_sum[w].y;
+    int2 sums = warp_sum[lane], before = carry;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int a = __shfl_up_sync(0xffffffffu, sums.x, d), b = __shfl_up_sync(0xffffffffu, sums.y, d);
+      if (lane >= d) {
+        sums.x += a;
+        sums.y += b;
       }
-      carry.x += warp_sum[w].x;
-      carry.y += warp_sum[w].y;
     }
+    if (warp) {
+      before.x += __shfl_sync(0xffffffffu, sums.x, warp - 1);
+      before.y += __shfl_sync(0xffffffffu, sums.y, warp - 1);
+    }
+    carry.x += __shfl_sync(0xffffffffu, sums.x, 31);
+    carry.y += __shfl_sync(0xffffffffu, sums.y, 31);
     const int from = before.x + inc.x - count, tile = before.y + inc.y - own;
     if (g < groups) {
       start[g] = from;
-      for (int w = 0; w < warps; ++w) hist[w * groups + g] += from;
+      for (int w0 = 0; w0 < warps; w0 += 8) {
+        int c[8];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) c[w] = w0 + w < warps ? hist[(w0 + w) * groups + g] : 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w)
+          if (w0 + w < warps) hist[(w0 + w) * groups + g] = c[w] + from;
+      }
       for (int t = 0; t < own; ++t)
         tiles[tile + t] = Tile{g, from + t * tile_rows, min(tile_rows, count - t * tile_rows), 0};
     }

@@ -27,7 +27,11 @@ namespace {
 
 constexpr int kMostTop = 24;
 constexpr int kKeepMore = 8;
-constexpr int kFinishWarps = 4;
+// of a block: four warps, or where the rows are few four for the likeliest tokens, four for the statistics beside them and
+// one for the target's logit (8 rows of 32768, 20 tokens: the call 39 and 35 us; 2048 rows of 65536, 8: 62 and 74 us)
+constexpr int kTopWarps = 4, kTopThreads = kTopWarps * 32;
+constexpr int kFinishThreads = (2 * kTopWarps + 1) * 32;
+constexpr int kFoundFew = 256;  // keys that are ranked by counting
 constexpr int kNoId = 0x7FFFFFFF;
 constexpr int kFound = (kMostTop + kKeepMore) * 32;  // all logits of the groups that are looked at
 
@@ -120,10 +124,11 @@ struct FinishArgs {
 // A logit and its id as one number, in the order of the likeliest: larger logits, of
 // equal ones lower ids (0: none).  NaN counts as the lowest logit, -0 as 0.
 typedef unsigned long long Key;
-__device__ __forceinline__ Key key_of(float v, int id) {
+__device__ __forceinline__ uint32_t place_of_value(float v) {
   const uint32_t u = __float_as_uint((isnan(v) ? -INFINITY : v) + 0.f);
-  return ((Key)(u & 0x80000000u ? ~u : u | 0x80000000u) << 32) | (uint32_t)~id;
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+__device__ __forceinline__ Key key_of(float v, int id) { return (Key)place_of_value(v) << 32 | (uint32_t)~id; }
 __device__ __forceinline__ float key_value(Key k) {
   const uint32_t u = (uint32_t)(k >> 32);
   return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
@@ -151,7 +156,7 @@ __device__ __forceinline__ Key joined(Key a, Key b, int lane) {
   return k;
 }
 // the list with what each lane has to offer, if that is among its first `keep`
-__device__ __forceinline__ Key offered(Key list, Key k, int keep, int lane) {
+__device__ __noinline__ Key offered(Key list, Key k, int keep, int lane) {
   unsigned m = __ballot_sync(0xffffffffu, k > __shfl_sync(0xffffffffu, list, keep - 1));
   if (__popc(m) > 4) return joined(list, sorted(k, lane), lane);
   for (; m; m &= m - 1) {
@@ -162,6 +167,19 @@ __device__ __forceinline__ Key offered(Key list, Key k, int keep, int lane) {
   return list;
 }
 
+// the warps that look for the likeliest
+__device__ __forceinline__ void top_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kTopThreads) : "memory"); }
+// the `keep` largest of n distinct keys, in their order; all of them
+__device__ __noinline__ void choose(const Key *keys, int n, Key *chosen, int keep) {
+  for (int i = threadIdx.x; i < n; i += kTopThreads) {
+    const Key own = keys[i];
+    int place = 0;
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) place += keys[j] > own ? 1 : 0;
+    if (place < keep) chosen[place] = own;
+  }
+}
+
 // hi + lo += a * b, to about twice fp32's precision
 __device__ __forceinline__ void add_product(float &hi, float &lo, float a, float b) {
   const float p = __fmul_rn(a, b), e = __fmaf_rn(a, b, -p);
@@ -169,43 +187,60 @@ __device__ __forceinline__ void add_product(float &hi, float &lo, float a, float
   lo = __fadd_rn(lo, __fadd_rn(e, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(p, t))));
   hi = s;
 }
-// the logit of a row and a token, by a warp
+// a number in the order of hi + lo, an integer (double's own comparisons and sums are slow here)
+__device__ __forceinline__ long long order_of(float hi, float lo) {
+  const long long bits = __double_as_longlong((double)(hi + 0.f) + (double)lo);  // -0 as 0
+  return bits < 0 ? bits ^ 0x7FFFFFFFFFFFFFFFLL : bits;
+}
+// hi + lo = a + b, exactly
+__device__ __forceinline__ void add_two(float &hi, float &lo, float b_hi, float b_lo) {
+  const float s = __fadd_rn(hi, b_hi), t = __fsub_rn(s, hi);
+  const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(b_hi, t));
+  lo = __fadd_rn(__fadd_rn(lo, b_lo), e);
+  hi = s;
+}
+// the logit of a row and a token, by a warp: hi + lo
 template <typename T>
-__device__ __forceinline__ double long_logit(const TargetLogit &at, int64_t row, int64_t id, int lane) {
+__device__ __noinline__ float2 long_logit(const TargetLogit &at, int64_t row, int64_t id, int lane) {
   constexpr int kN = 16 / (int)sizeof(T);
   const T *a = reinterpret_cast<const T *>(at.x) + row * at.x_ld, *b = reinterpret_cast<const T *>(at.w) + id * at.w_ld;
   const int groups = (at.width + kN - 1) / kN;
   float hi = 0.f, lo = 0.f;
-#pragma unroll 2
+#pragma unroll 4
   for (int g = lane; g < groups; g += 32) {
     const Pack<T, 16> p = TargetLogit::some(a, g, at.width, at.x_wide), q = TargetLogit::some(b, g, at.width, at.w_wide);
 #pragma unroll
     for (int e = 0; e < kN; ++e) add_product(hi, lo, p.get(e), q.get(e));
   }
-  double s = (double)hi + (double)lo;
 #pragma unroll
-  for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-  return s;
+  for (int d = 16; d; d >>= 1) {
+    const float o_hi = __shfl_xor_sync(0xffffffffu, hi, d), o_lo = __shfl_xor_sync(0xffffffffu, lo, d);
+    add_two(hi, lo, o_hi, o_lo);
+  }
+  return make_float2(hi, lo);
 }
 
 // A block per row.
-__global__ void __launch_bounds__(kFinishWarps * 32) k_score_finish(const FinishArgs a) {
+__global__ void __launch_bounds__(kFinishThreads) k_score_finish(const FinishArgs a) {
   pdl_wait();
-  __shared__ Key lists[kFinishWarps][32];
-  __shared__ Key found[kFound];
-  __shared__ float4 sums[kFinishWarps];
-  __shared__ double exact[32];
+  __shared__ Key chosen[32];
+  __shared__ __align__(16) uint32_t bests[kTopThreads];
+  __shared__ uint32_t least_best;
+  __shared__ __align__(16) Key found[kFound + 32];
+  __shared__ float4 sums[kTopWarps];
+  __shared__ float2 exact[32];
   __shared__ unsigned again;
   __shared__ float target_z;
   __shared__ int n_found;
   const int64_t row = blockIdx.x;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const bool wide = warps > kTopWarps;
   const bool bad = a.last && any_error(a.err);
   const uint32_t target = a.targets.ids ? a.targets.key(row) : a.targets.vocab;
   const bool given = target < a.targets.vocab;
   if (a.targets.ids && !given) {  // not scored
     if (!a.last) return;
-    for (int i = threadIdx.x; i < a.top; i += kFinishWarps * 32) {
+    for (int i = threadIdx.x; i < a.top; i += 32 * warps) {
       a.top_ids[row * a.top + i] = -1;
       a.top_logp[row * a.top + i] = 0.f;
     }
@@ -218,40 +253,42 @@ __global__ void __launch_bounds__(kFinishWarps * 32) k_score_finish(const Finish
     return;
   }
   Key list = 0;
-  if (a.top) {
-    // The groups with the largest maxima: none of them comes after the keep-th of the
-    // threads' own largest ones, and few others come before it.
+  if (warp < kTopWarps && a.top) {
+    // The groups with the largest maxima: none of them is below what `keep` of the threads'
+    // own largest ones reach, and few others reach it.
     const float *high = a.high + row * a.high_ld;
-    Key best = 0;
-#pragma unroll 4
-    for (int g = threadIdx.x; g < a.groups; g += kFinishWarps * 32) {
-      const Key k = key_of(__ldg(high + g), g);
-      if (k > best) best = k;
+    uint32_t best = 0;
+#pragma unroll 8
+    for (int g = threadIdx.x; g < a.groups; g += kTopThreads) best = max(best, place_of_value(__ldg(high + g)));
+    bests[threadIdx.x] = best;
+    if (threadIdx.x < 32) chosen[threadIdx.x] = 0;
+    if (threadIdx.x == 0) {
+      n_found = 0;
+      least_best = 0;
     }
-    lists[warp][lane] = sorted(best, lane);
-    if (threadIdx.x == 0) n_found = 0;
-    __syncthreads();
-    if (warp == 0) {
-      list = lists[0][lane];
-#pragma unroll 1
-      for (int w = 1; w < kFinishWarps; ++w) list = joined(list, lists[w][lane], lane);
-      const Key from = __shfl_sync(0xffffffffu, list, a.keep - 1);
-      if (lane == 0) lists[0][0] = from;
+    top_sync();
+    int reached = 0;
+#pragma unroll
+    for (int i = 0; i < kTopThreads; i += 4) {
+      const uint4 four = *reinterpret_cast<const uint4 *>(bests + i);
+      reached += (four.x >= best ? 1 : 0) + (four.y >= best ? 1 : 0) + (four.z >= best ? 1 : 0) + (four.w >= best ? 1 : 0);
     }
-    __syncthreads();
-    const Key from = lists[0][0];
+    if (reached >= a.keep) atomicMax(&least_best, best);
+    top_sync();
+    const uint32_t from = least_best;
 #pragma unroll 4
-    for (int g = threadIdx.x; g < a.groups; g += kFinishWarps * 32) {
-      const Key k = key_of(__ldg(high + g), g);
-      if (k >= from) {
+    for (int g = threadIdx.x; g < a.groups; g += kTopThreads) {
+      const float v = __ldg(high + g);
+      if (place_of_value(v) >= from) {
         const int at = atomicAdd(&n_found, 1);  // their order does not matter
-        if (at < kFound) found[at] = k;
+        if (at < kFound) found[at] = key_of(v, g);
       }
     }
-    __syncthreads();
-    if (warp == 0) {
-      list = 0;
-      const int n = n_found;
+    top_sync();
+    int n = n_found;
+    if (n <= kFoundFew) {
+      choose(found, n, chosen, a.keep);
+    } else if (warp == 0) {
       if (n <= kFound) {
 #pragma unroll 1
         for (int i = 0; i < n; i += 32) list = offered(list, i + lane < n ? found[i + lane] : 0, a.keep, lane);
@@ -259,83 +296,94 @@ __global__ void __launch_bounds__(kFinishWarps * 32) k_score_finish(const Finish
 #pragma unroll 1
         for (int g = lane; g - lane < a.groups; g += 32) list = offered(list, g < a.groups ? key_of(__ldg(high + g), g) : 0, a.keep, lane);
       }
-      lists[0][lane] = list;
+      chosen[lane] = list;
     }
-    __syncthreads();
+    top_sync();
     if (threadIdx.x == 0) n_found = 0;
     // and of their logits those that are not below the last group's maximum
-    constexpr int kMost = (kMostTop + kKeepMore + kFinishWarps - 1) / kFinishWarps;
-    const Key last_group = lists[0][a.keep - 1];
+    constexpr int kMost = (kMostTop + kKeepMore + kTopWarps - 1) / kTopWarps;
+    const Key last_group = chosen[a.keep - 1];
     const Key least = last_group ? key_of(key_value(last_group), kNoId) : 0;
     Key k[kMost];
 #pragma unroll
     for (int u = 0; u < kMost; ++u) {
-      const int i = warp + u * kFinishWarps;
-      const Key of = i < a.keep ? lists[0][i] : 0;
+      const int i = warp + u * kTopWarps;
+      const Key of = i < a.keep ? chosen[i] : 0;
       const int col = of ? key_id(of) * 32 + lane : a.rows;
       k[u] = col < a.rows ? key_of(__ldg(a.z + row * a.z_row + col * a.z_col), a.v0 + col) : 0;
     }
-    __syncthreads();
+    top_sync();
 #pragma unroll
     for (int u = 0; u < kMost; ++u)
       if (k[u] && k[u] >= least) found[atomicAdd(&n_found, 1)] = k[u];
-    __syncthreads();
-    if (warp == 0) {
+    if (!a.first && warp == 0) {
+      const Key old = a.list[row * 32 + lane];
+      if (old) found[atomicAdd(&n_found, 1)] = old;
+    }
+    if (warp == kTopWarps - 1) chosen[lane] = 0;  // read by all already
+    top_sync();
+    n = n_found;
+    if (n <= kFoundFew) {
+      choose(found, n, chosen, a.keep);
+    } else if (warp == 0) {
       list = 0;
-      if (!a.first) list = a.list[row * 32 + lane];
-      const int n = n_found;
 #pragma unroll 1
       for (int i = 0; i < n; i += 32) list = offered(list, i + lane < n ? found[i + lane] : 0, a.keep, lane);
-      if (!a.last) a.list[row * 32 + lane] = list;
+      chosen[lane] = lane < a.keep ? list : 0;
     }
-    if (!a.last) return;
-  }
-  // the row's statistics
-  float4 s = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-  for (int i = threadIdx.x; i < a.slots; i += kFinishWarps * 32) s = join_stats(s, a.stats[row * a.stats_ld + i]);
+    top_sync();
+    if (warp == 0) {
+      list = chosen[lane];
+      if (!a.last) a.list[row * 32 + lane] = list;
+      // which of them are too close to tell
+      const float mine = list ? key_value(list) : -INFINITY, above = __shfl_up_sync(0xffffffffu, mine, 1);
+      float size = lane < a.keep && isfinite(mine) ? fabsf(mine) : 0.f;
 #pragma unroll
-  for (int d = 1; d < 32; d *= 2) {  // lane by lane upwards: the same result in all
-    float4 o;
-    o.x = __shfl_xor_sync(0xffffffffu, s.x, d);
-    o.y = __shfl_xor_sync(0xffffffffu, s.y, d);
-    o.z = __shfl_xor_sync(0xffffffffu, s.z, d);
-    o.w = __shfl_xor_sync(0xffffffffu, s.w, d);
-    s = lane & d ? join_stats(o, s) : join_stats(s, o);
+      for (int d = 16; d; d >>= 1) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, d));
+      const bool close = lane > 0 && lane < a.keep && list && above - mine <= size * 0x1p-12f;  // not of two infinities
+      const unsigned with = __ballot_sync(0xffffffffu, close);  // bit l: l goes with l - 1
+      // a run of them that begins before place `top`
+      const int begin = 31 - __clz(~with & (0xffffffffu >> (31 - lane)));
+      const bool run = close || (lane < 31 && (with >> (lane + 1)) & 1);
+      const unsigned m = __ballot_sync(0xffffffffu, run && begin < a.top);
+      if (lane == 0) again = m;
+    }
   }
-  if (lane == 0) sums[warp] = s;
-  if (given && warp == kFinishWarps - 1) {  // beside warp 0's work
+  if (!a.last) return;
+  if (const int mine = warp - (wide ? kTopWarps : 0); mine >= 0 && mine < kTopWarps) {  // the row's statistics
+    float4 s = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 32 * mine + lane; i < a.slots; i += kTopThreads) s = join_stats(s, a.stats[row * a.stats_ld + i]);
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {  // lane by lane upwards: the same result in all
+      float4 o;
+      o.x = __shfl_xor_sync(0xffffffffu, s.x, d);
+      o.y = __shfl_xor_sync(0xffffffffu, s.y, d);
+      o.z = __shfl_xor_sync(0xffffffffu, s.z, d);
+      o.w = __shfl_xor_sync(0xffffffffu, s.w, d);
+      s = lane & d ? join_stats(o, s) : join_stats(s, o);
+    }
+    if (lane == 0) sums[mine] = s;
+  }
+  if (given && warp == warps - 1) {
     const float z = a.zt ? a.zt[row] : a.at.get(row, target);
     if (lane == 0) target_z = z;
-  }
-  if (a.top && warp == 0) {  // which of the list are too close to tell
-    const float mine = list ? key_value(list) : -INFINITY, above = __shfl_up_sync(0xffffffffu, mine, 1);
-    float size = lane < a.keep && isfinite(mine) ? fabsf(mine) : 0.f;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, d));
-    const bool close = lane > 0 && lane < a.keep && list && above - mine <= size * 0x1p-12f;  // not of two infinities
-    const unsigned with = __ballot_sync(0xffffffffu, close);  // bit l: l goes with l - 1
-    // a run of them that begins before place `top`
-    const int begin = 31 - __clz(~with & (0xffffffffu >> (31 - lane)));
-    const bool run = close || (lane < 31 && (with >> (lane + 1)) & 1);
-    const unsigned m = __ballot_sync(0xffffffffu, run && begin < a.top);
-    if (lane == 0) again = m;
-    lists[0][lane] = list;
   }
   __syncthreads();
   if (a.top) {
     int k = 0;
     for (unsigned m = again; m; m &= m - 1, ++k) {
-      if (k % kFinishWarps != warp) continue;
-      const int i = __ffs(m) - 1, id = key_id(lists[0][i]);
-      const double l = a.at.bf ? long_logit<bf16>(a.at, row, id, lane) : long_logit<float>(a.at, row, id, lane);
+      if (k % warps != warp) continue;
+      const int i = __ffs(m) - 1, id = key_id(chosen[i]);
+      const float2 l = a.at.bf ? long_logit<bf16>(a.at, row, id, lane) : long_logit<float>(a.at, row, id, lane);
       if (lane == 0) exact[i] = l;
     }
     __syncthreads();
   }
   if (warp) return;
-  s = sums[0];
+  float4 s = sums[0];
 #pragma unroll
-  for (int w = 1; w < kFinishWarps; ++w) s = join_stats(s, sums[w]);
+  for (int w = 1; w < kTopWarps; ++w) s = join_stats(s, sums[w]);
   const float z = given ? target_z : 0.f;
   // the largest logit with the target's, and of the sums relative to it what is over 1
   float high = s.x, over, slope;
@@ -359,16 +407,17 @@ __global__ void __launch_bounds__(kFinishWarps * 32) k_score_finish(const Finish
   }
   if (!a.top) return;
   const int id = key_id(list);
-  double l = key_value(list);
-  if ((again >> lane) & 1 && isfinite(exact[lane])) l = exact[lane];
+  float2 l = make_float2(key_value(list), 0.f);
+  if ((again >> lane) & 1 && isfinite(exact[lane].x)) l = exact[lane];
+  const long long mine = order_of(l.x, l.y);
   int place = 0;
   for (int j = 0; j < a.keep; ++j) {
-    const double lj = __shfl_sync(0xffffffffu, l, j);
+    const long long other = __shfl_sync(0xffffffffu, mine, j);
     const int ij = __shfl_sync(0xffffffffu, id, j);
-    place += lj > l || (lj == l && ij < id) ? 1 : 0;
+    place += other > mine || (other == mine && ij < id) ? 1 : 0;
   }
   if (lane < a.keep && place < a.top) {
-    const float own = given && id == (int)target ? logp : ((float)l - high) - log_sum;
+    const float own = given && id == (int)target ? logp : (l.x - high) - log_sum;
     a.top_ids[row * a.top + place] = id;
     a.top_logp[row * a.top + place] = own;
   }
@@ -547,7 +596,13 @@ snack_status snack_score_fwd(const void *x, int64_t x_ld, int32_t n, const void 
   f.top_ids = top_ids;
   f.lse = state;
   f.kept_entropy = state + n;
-  auto finish = [&] { return launch_pdl(k_score_finish, (unsigned)n, kFinishWarps * 32, 0, s, (const FinishArgs)f); };
+  auto finish = [&] { return launch_pdl(k_score_finish, (unsigned)n, n <= S.sms ? kFinishThreads : kTopThreads, 0, s, (const FinishArgs)f); };
+  if (W.tokens) {
+    f.groups = f.slots = (int32_t)W.slots;
+    f.rows = (int32_t)vocab;
+    f.z_row = 1;
+    f.z_col = W.tokens;
+  }
   if (W.tokens) {
     float *z = reinterpret_cast<float *>(b + W.z), *zt = reinterpret_cast<float *>(b + W.zt);
     XENT_CUDA(score_logits_few(S, W, x, x_ld, w, w_ld, tg, z, s));
@@ -555,10 +610,6 @@ snack_status snack_score_fwd(const void *x, int64_t x_ld, int32_t n, const void 
     XENT_CUDA(launch_pdl(k_score_stats, (unsigned)ceil_div(threads, 256), 256, 0, s, (const float *)z, W.tokens, n, vocab,
                          (int32_t)W.slots, tg, reinterpret_cast<float4 *>(b + W.stats), top ? reinterpret_cast<float *>(b + W.high) : nullptr,
                          zt));
-    f.groups = f.slots = (int32_t)W.slots;
-    f.rows = (int32_t)vocab;
-    f.z_row = 1;
-    f.z_col = W.tokens;
     f.zt = zt;  // of the same sums as the others, and the gradient's
     XENT_CUDA(finish());
     return SNACK_OK;
