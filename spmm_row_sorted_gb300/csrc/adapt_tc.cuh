@@ -117,20 +117,6 @@ __device__ __forceinline__ void copy_piece(void *to, const void *from, int bytes
   }
 }
 
-// 64 of K (rows and columns of the swizzled tiles) of an adapter's matrix for the product: with K along its rows
-// ([cols][k], n of them from row `n0` on) or across them ([k][cols], columns from `n0` on).  kBox rows of K or of the
-// matrix are 128-byte rows of the tile, 64 elements each; what is past the end is zeros.
-//
-// Rows of 128 bytes `rows`, whose first elements are `at` + row * ld, `left_rows` and `left` elements of them there.
-template <int kThreads>
-__device__ __forceinline__ void fetch_box(uint8_t *to, const bf16 *from, int64_t ld, int rows, int left_rows, int chunks, int left, bool wide) {
-  for (int i = threadIdx.x; i < rows * chunks; i += kThreads) {
-    const int r = i / chunks, c = i - r * chunks;
-    const int bytes = r < left_rows ? max(0, min(left - 8 * c, 8)) * 2 : 0;
-    copy_piece(to + r * 128 + ((c ^ (r & 7)) << 4), bytes ? from + r * ld + 8 * c : from, bytes, wide);
-  }
-}
-
 // A tile of 128 rows against an adapter's matrix, all of its ranks (N); the cluster's blocks have every so many 64 of K.
 template <bool kAlong>
 __global__ void __launch_bounds__(kTcThreads, 2) k_adapt_down_tc(const DownArgs a, int m_wide) {
@@ -176,12 +162,23 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_adapt_down_tc(const DownArgs 
         if (t < tile.count) copy_async<16>(to + t * 128 + (((lane & 7) ^ (t & 7)) << 4), bytes ? row[u] + k0 : row[u], bytes);
       }
       to += kTcRowBox;
+      // the matrix: eight threads have 128 bytes of every 32nd row; zeros past the end
+      const int c = lane & 7, r0 = threadIdx.x >> 3;
+      to += r0 * 128 + ((c ^ (r0 & 7)) << 4);
       if constexpr (kAlong) {
-        fetch_box<kTcThreads>(to, mat + k0, a.k, n_pad, rank, 8, left, m_wide);
+        for (int r = r0; r < n_pad; r += kTcThreads / 8, to += kTcThreads / 8 * 128) {
+          const int there = r < rank ? bytes : 0;
+          copy_piece(to, there ? mat + (int64_t)r * a.k + k0 + 8 * c : mat, there, m_wide);
+        }
       } else {
-        for (int b = 0; b < tc_blocks(rank); ++b)
-          fetch_box<kTcThreads>(to + b * kTcK * 128, mat + (int64_t)k0 * rank + 64 * b, rank, kTcK, left, min(8, (n_pad - 64 * b) / 8), rank - 64 * b,
-                                m_wide);
+        for (int b = 8 * c; b < n_pad; b += 64, to += kTcK * 128) {
+          const int there = max(0, min(rank - b, 8)) * 2;
+#pragma unroll
+          for (int u = 0; u < kTcK / (kTcThreads / 8); ++u) {
+            const int k = r0 + u * (kTcThreads / 8);
+            copy_piece(to + u * (kTcThreads / 8) * 128, there && k < left ? mat + (int64_t)(k0 + k) * rank + b : mat, k < left ? there : 0, m_wide);
+          }
+        }
       }
     }
     fetch_commit();
