@@ -316,6 +316,20 @@ __device__ __forceinline__ void turn_pairs(float (&v)[16], int lane) {
   }
 }
 
+// up to eight elements at the end of a row
+__device__ __noinline__ uint4 read_some(const uint16_t *p, int left) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = (2 * j < left ? p[2 * j] : 0u) | (2 * j + 1 < left ? (uint32_t)p[2 * j + 1] << 16 : 0u);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __noinline__ void write_some(uint16_t *p, uint4 v, int left) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < left) p[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+}
+
 // Units of a tile of 128 rows and 128 columns: h in its two parts (A, K-major) against the matrix's columns (B).  A block
 // has runs of units; all blocks' runs one beside the other, so that what is read and written at a time are some tiles'
 // rows.  One warp fetches the matrix, one issues the products into two sets of sums in turn, eight add the base, which
@@ -369,31 +383,33 @@ __global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a,
     if (none && a.base == a.out) continue;
     if (warp < kTcUpEpi / 32) {
       const int first_row = 32 * (warp & 3), q = lane & 3, col = col0 + 64 * (warp >> 2) + 8 * q;
-      int32_t token[4];
+      const uint16_t *from[4];  // this lane's rows, from its first eight columns on
+      uint16_t *to[4];
+      bool in[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = first_row + 8 * i + (lane >> 2);
-        token[i] = t < tile.count ? __ldg(a.order + tile.first + t) : -1;
+      for (int r = 0; r < 4; ++r) {
+        const int t = first_row + 8 * r + (lane >> 2);
+        in[r] = t < tile.count;
+        const int64_t token = __ldg(a.order + tile.first + (in[r] ? t : 0));
+        from[r] = reinterpret_cast<const uint16_t *>(a.base) + token * a.base_ld + col;
+        to[r] = reinterpret_cast<uint16_t *>(a.out) + token * a.out_ld + col;
       }
       uint4 base[2][4];
-      auto read = [&](int c, uint4 (&to)[4]) {
+      auto read = [&](int past, bool whole, uint4 (&v)[4]) {  // columns `past` behind the first ones
+        if (a.base && whole) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          to[i] = make_uint4(0, 0, 0, 0);
-          if (!a.base || token[i] < 0 || c >= a.cols) continue;
-          const uint16_t *from = reinterpret_cast<const uint16_t *>(a.base) + token[i] * a.base_ld + c;
-          if (c + 8 <= a.cols) {
-            to[i] = *reinterpret_cast<const uint4 *>(from);
-          } else {
-            uint16_t v[8];
+          for (int r = 0; r < 4; ++r)
+            if (in[r]) v[r] = *reinterpret_cast<const uint4 *>(from[r] + past);
+        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = c + e < a.cols ? from[e] : (uint16_t)0;
-            to[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-          }
+          for (int r = 0; r < 4; ++r) v[r] = read_some(from[r] + past, a.base && in[r] ? a.cols - col - past : 0);
         }
       };
-      read(col, base[0]);
-      read(col + 32, base[1]);
+      const bool whole_first = !a.base || col0 + kTcUpCols <= a.cols;
+      if (a.base) {
+        read(0, whole_first, base[0]);
+        read(32, whole_first, base[1]);
+      }
       if (!none) {  // h, when no product reads the tile's before any more: two threads have a row, eight ranks at a time; zeros
                     // past the tile's rows and the rank
         const float scale = a.scales ? a.scales[tile.adapter] : 1.f;
@@ -431,12 +447,17 @@ __global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a,
         }
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
-          const int c = col + i * kTcUpCols + 32 * sub;
+          const int past = i * kTcUpCols + 32 * sub;
+          const bool whole = col0 + (i + 1) * kTcUpCols <= a.cols;
+          if (!a.base) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) base[sub][r] = make_uint4(0, 0, 0, 0);
+          }
           float v[2][16];
           if (!none) {
-            const uint32_t from = tmem + ((uint32_t)first_row << 16) + (g & 1) * kTcUpCols + 64 * (warp >> 2) + 32 * sub;
-            tmem_ld_rows(from, v[0]);
-            tmem_ld_rows(from + (16u << 16), v[1]);
+            const uint32_t at_sums = tmem + ((uint32_t)first_row << 16) + (g & 1) * kTcUpCols + 64 * (warp >> 2) + 32 * sub;
+            tmem_ld_rows(at_sums, v[0]);
+            tmem_ld_rows(at_sums + (16u << 16), v[1]);
             tmem_wait(v[0], v[1]);
             if (sub == 1) {
               tc_fence_before();
@@ -447,28 +468,24 @@ __global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a,
               turn_pairs(v[0], lane);
               turn_pairs(v[1], lane);
             }
+            if (!ok) v[0][0] = v[0][2] = v[1][0] = v[1][2] = NAN;  // a wait gave up: no row without a NaN
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const float *x = &v[r >> 1][2 * (r & 1)];
               uint32_t(&o)[4] = reinterpret_cast<uint32_t(&)[4]>(base[sub][r]);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) o[j] = ok ? pack_pair(bf16_lo(o[j]) + x[4 * j], bf16_hi(o[j]) + x[4 * j + 1]) : 0x7FFF7FFFu;
+              for (int j = 0; j < 4; ++j) o[j] = pack_pair(bf16_lo(o[j]) + x[4 * j], bf16_hi(o[j]) + x[4 * j + 1]);
             }
           }
+          if (whole) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (token[r] >= 0 && c < a.cols) {
-              uint16_t *to = reinterpret_cast<uint16_t *>(a.out) + token[r] * a.out_ld + c;
-              if (c + 8 <= a.cols) {
-                *reinterpret_cast<uint4 *>(to) = base[sub][r];
-              } else {
-                const uint32_t w[4] = {base[sub][r].x, base[sub][r].y, base[sub][r].z, base[sub][r].w};
+            for (int r = 0; r < 4; ++r)
+              if (in[r]) *reinterpret_cast<uint4 *>(to[r] + past) = base[sub][r];
+          } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  if (c + e < a.cols) to[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-              }
-            }
-          if (i + 1 < items) read(c + kTcUpCols, base[sub]);
+            for (int r = 0; r < 4; ++r) write_some(to[r] + past, base[sub][r], in[r] ? a.cols - col - past : 0);
+          }
+          if (a.base && i + 1 < items) read(past + kTcUpCols, col0 + (i + 2) * kTcUpCols <= a.cols, base[sub]);
         }
         if (!none) ++g;
       }
@@ -481,14 +498,23 @@ __global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a,
         uint8_t *to = ring + s * stage_bytes;
         const int col = col0 + i * kTcUpCols, left = a.cols - col;
         if constexpr (kAlong) {  // eight lanes have 128 bytes of a row, four rows at a time
-          const int c = lane & 7, r0 = lane >> 3;
+          // row r = 4 u + r0 of the tile is column 32 (u / 8) + 16 (u % 2) + 2 (u / 2 % 4) + 8 (r0 / 2) + r0 % 2: a fragment's
+          const int c = lane & 7, r0 = lane >> 3, n0 = 8 * (r0 >> 1) + (r0 & 1);
           for (int b = 0; b < k_blocks; ++b, to += kTcUpCols * 128) {
             if (64 * b + 8 * c >= 16 * steps) break;
             const int bytes = max(0, min(rank - 64 * b - 8 * c, 8)) * 2;
-#pragma unroll 8
-            for (int u = 0; u < kTcUpCols / 4; ++u) {
-              const int r = r0 + 4 * u, n = (r & ~31) + 8 * ((r >> 1) & 3) + 2 * ((r >> 3) & 3) + (r & 1), there = n < left ? bytes : 0;
-              copy_piece(to + r * 128 + ((c ^ (r & 7)) << 4), there ? mat + (int64_t)(col + n) * rank + 64 * b + 8 * c : mat, there, m_wide);
+            const bf16 *p = mat + (int64_t)(col + n0) * rank + 64 * b + 8 * c;
+            uint8_t *even = to + r0 * 128 + ((c ^ r0) << 4), *odd = to + (r0 + 4) * 128 + ((c ^ (r0 + 4)) << 4) - 512;
+            if (left >= kTcUpCols && bytes == 16 && m_wide) {
+#pragma unroll
+              for (int u = 0; u < kTcUpCols / 4; ++u)
+                copy_whole<16>((u & 1 ? odd : even) + u * 512, p + (32 * (u >> 3) + 16 * (u & 1) + 2 * ((u >> 1) & 3)) * rank);
+            } else {
+#pragma unroll 4
+              for (int u = 0; u < kTcUpCols / 4; ++u) {
+                const int n = 32 * (u >> 3) + 16 * (u & 1) + 2 * ((u >> 1) & 3), there = n0 + n < left ? bytes : 0;
+                copy_piece((u & 1 ? odd : even) + u * 512, there ? p + n * rank : mat, there, m_wide);
+              }
             }
           }
         } else {  // 16 lanes have the 256 bytes of a row
