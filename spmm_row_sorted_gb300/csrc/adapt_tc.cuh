@@ -705,24 +705,26 @@ __global__ void __launch_bounds__(kTcThreads, 3) k_adapt_outer_tc(const OuterPai
   // v: four ranks of a row at a time
   constexpr int kQuads = kRanks / 4, kJobs = kTcRows * kQuads / kTcThreads;
   static_assert(kJobs * kTcThreads == kTcRows * kQuads, "whole jobs");
-  Pack<float, 16> held[kJobs];
-  auto read_v = [&](int tokens) {
+  struct Held {
+    Pack<float, 16> v[kJobs];
+  };
+  auto read_v = [&](int tokens, Held &held) {
 #pragma unroll
     for (int u = 0; u < kJobs; ++u) {
       const int job = threadIdx.x + u * kTcThreads, k = job / kQuads, r = r0 + job % kQuads * 4;
       const int token = __shfl_sync(0xffffffffu, tokens, k);
       const bool in = token >= 0 && r < a.rank;
-      held[u] = load_vec<float, 4>(a.v + (in ? (int64_t)token * a.rank + r : 0), in ? a.rank - r : 0, a.v_wide);
+      held.v[u] = load_vec<float, 4>(a.v + (in ? (int64_t)token * a.rank + r : 0), in ? a.rank - r : 0, a.v_wide);
     }
   };
-  auto put_v = [&](int i) {
+  auto put_v = [&](int i, const Held &held) {
     uint8_t *to = ring + (i % kTcStages) * kStage + kTcCols / 64 * kTcBox;
 #pragma unroll
     for (int u = 0; u < kJobs; ++u) {
       const int job = threadIdx.x + u * kTcThreads, k = job / kQuads, r = job % kQuads * 4;
       uint32_t w[2][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) cut_pair<2>(held[u].get(2 * h), held[u].get(2 * h + 1), w[h]);
+      for (int h = 0; h < 2; ++h) cut_pair<2>(held.v[u].get(2 * h), held.v[u].get(2 * h + 1), w[h]);
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const int c = p * kRanks + r;
@@ -734,17 +736,19 @@ __global__ void __launch_bounds__(kTcThreads, 3) k_adapt_outer_tc(const OuterPai
   if (steps) {
     constexpr uint32_t kInst = tc_inst(128, kRanks, true, true);
     int ahead[kTcStages];  // the rows of steps i + 1, ..., i + kTcStages
+    Held even, odd;        // v of the step in hand and of the next one
     {
       const int now = tokens_at(0);
 #pragma unroll
       for (int s = 0; s < kTcStages; ++s) ahead[s] = tokens_at(s + 1);
       fetch(0, now);
-      read_v(now);
+      read_v(now, even);
+      read_v(ahead[0], odd);
 #pragma unroll
       for (int s = 1; s < kTcStages - 1; ++s) fetch(s, ahead[s - 1]);
     }
-    for (int i = 0; i < steps; ++i) {
-      put_v(i);
+    auto step_on = [&](int i, Held &held) {
+      put_v(i, held);
       fetch_wait<kTcStages - 2>();
       fence_async_shared();
       __syncthreads();
@@ -764,10 +768,14 @@ __global__ void __launch_bounds__(kTcThreads, 3) k_adapt_outer_tc(const OuterPai
       // the stage that step i - 1 has read is filled for step i + kTcStages - 1
       if (i > 0) ok = mbar_wait(&done[(i - 1) % kTcStages], ((i - 1) / kTcStages) & 1) && ok;
       fetch(i + kTcStages - 1, ahead[kTcStages - 2]);
-      read_v(ahead[0]);
+      read_v(ahead[1], held);
 #pragma unroll
       for (int s = 0; s + 1 < kTcStages; ++s) ahead[s] = ahead[s + 1];
       ahead[kTcStages - 1] = tokens_at(i + kTcStages + 1);
+    };
+    for (int i = 0; i < steps; i += 2) {
+      step_on(i, even);
+      if (i + 1 < steps) step_on(i + 1, odd);
     }
     fetch_wait<0>();
     ok = mbar_wait(&done[(steps - 1) % kTcStages], ((steps - 1) / kTcStages) & 1) && ok;
@@ -824,8 +832,8 @@ cudaError_t launch_outer_tc(OuterPair p, int64_t n, int32_t adapters, int sms, c
   p.slices = p.a[0].out ? (int32_t)ceil_div(p.a[0].cols, kTcCols) : 0;
   const int64_t slices = p.slices + (p.a[1].out ? ceil_div(p.a[1].cols, kTcCols) : 0);
   const int64_t ranks = ceil_div(p.a[0].rank, kRanks);
-  // three blocks of an SM at a time; two rounds of them even out adapters that have more rows than others (8192 rows, 64 of
-  // 4096 to 16384, four adapters: 161 us in 320 blocks, 104 in 640, 113 in 1280)
+  // three blocks of an SM at a time; two rounds of them even out adapters that have more rows than others (8192 rows, rank 64,
+  // 4096 to 16384, four adapters: 161 us in 320 blocks, 104 in 640, 113 in 1280; 95 with v read two steps ahead)
   const unsigned c = cluster_for(slices * ranks * adapters, ceil_div(n, (int64_t)adapters * kTcRows), 5 * sms);
   return launch_cluster(c, kernel, dim3((unsigned)(slices * c), (unsigned)adapters, (unsigned)ranks), kTcThreads, smem, s,
                         (const OuterPair)p);
