@@ -1233,13 +1233,11 @@ cudaError_t down_by(DownArgs a, int64_t n, int tile_cap, int sms, cudaStream_t s
                                       : launch_down<T, NT, kHalves, kAlong, false>(a, n, tile_cap, sms, s);
 }
 template <typename T, bool kAlong>
-cudaError_t down(const DownArgs &a, int64_t n, int tile_rows, int tile_cap, int sms, cudaStream_t s) {
+cudaError_t down(const DownArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
   if constexpr (sizeof(T) == 2)
-    if (tile_rows == kTcTile) return launch_down_tc<kAlong>(a, likely_tiles(n, a.adapters, kTcTile), tile_cap, sms, s);
-  if (a.rank <= 16) return down_by<T, 2, 1, kAlong>(a, n, tile_cap, sms, s);
-  if (a.rank <= 32 || sizeof(T) == 4) return down_by<T, 2, 2, kAlong>(a, n, tile_cap, sms, s);
-  if constexpr (sizeof(T) == 2) return down_by<T, 4, 2, kAlong>(a, n, tile_cap, sms, s);
-  return cudaErrorInvalidValue;
+    return down_tc<kAlong>(a, likely_tiles(n, a.adapters, kTcTile), tile_cap, sms, s);
+  else
+    return a.rank <= 16 ? down_by<T, 2, 1, kAlong>(a, n, tile_cap, sms, s) : down_by<T, 2, 2, kAlong>(a, n, tile_cap, sms, s);
 }
 
 template <typename T, bool kAlong, int kSteps, bool kWide>
@@ -1268,15 +1266,11 @@ cudaError_t up_by(UpArgs a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
   return up_wide<T, kAlong>(&a) ? launch_up<T, kAlong, kSteps, true>(a, n, tile_cap, sms, s) : launch_up<T, kAlong, kSteps, false>(a, n, tile_cap, sms, s);
 }
 template <typename T, bool kAlong>
-cudaError_t up(const UpArgs &a, int64_t n, int tile_rows, int tile_cap, int sms, cudaStream_t s) {
+cudaError_t up(const UpArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
   if constexpr (sizeof(T) == 2)
-    if (tile_rows == kTcTile) return launch_up_tc<kAlong>(a, tile_cap, sms, s);
-  if (a.rank <= 16 || sizeof(T) == 4) return up_by<T, kAlong, 1>(a, n, tile_cap, sms, s);
-  if constexpr (sizeof(T) == 2) {
-    if (a.rank > 32 && a.rank <= 64) return up_by<T, kAlong, 4>(a, n, tile_cap, sms, s);
-    return up_by<T, kAlong, 2>(a, n, tile_cap, sms, s);
-  }
-  return cudaErrorInvalidValue;
+    return up_tc<kAlong>(a, tile_cap, sms, s);
+  else
+    return up_by<T, kAlong, 1>(a, n, tile_cap, sms, s);
 }
 
 template <typename T, int NT, int kSteps, bool kWide>
@@ -1286,7 +1280,8 @@ cudaError_t launch_few(const DownArgs &d, UpArgs u, const TokenSrc &which, int n
   const auto kernel = k_adapt_few<T, NT, kSteps, kWide>;
   cudaError_t e = raise_smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
-  const unsigned c = cluster_for(std::min<int64_t>(n, (int64_t)d.adapters + 1), ceil_div(d.k, Op<T>::kGroup * kDownParts), sms);
+  const int64_t shares = std::max(ceil_div(d.k, Op<T>::kGroup * kDownParts), ceil_div(u.cols, kUpWarps * kUpCols));
+  const unsigned c = cluster_for(std::min<int64_t>(n, (int64_t)d.adapters + 1), shares, sms);
   u.groups = (int)ceil_div(u.cols, (int64_t)c * kUpWarps * kUpCols);
   return launch_cluster(c, kernel, dim3((unsigned)n * c), kFewThreads, smem, s, d, (const UpArgs)u, which, n);
 }
@@ -1318,15 +1313,13 @@ cudaError_t outer(const OuterPair &p, int32_t rank, int64_t n, int32_t adapters,
   const auto aligned = [](const OuterArgs &a) { return !a.out || row_wide(a.x, a.x_ld, sizeof(T)); };
   const bool wide = aligned(p.a[0]) && aligned(p.a[1]);
   if constexpr (sizeof(T) == 2) {
-    if (wide) return rank <= 32 ? launch_outer_tc<32>(p, n, adapters, sms, s) : launch_outer_tc<64>(p, n, adapters, sms, s);
-  } else if (wide) {
-    return rank <= 16   ? launch_outer<T, 1, true>(p, n, adapters, sms, s)
-           : rank <= 32 ? launch_outer<T, 2, true>(p, n, adapters, sms, s)
-                        : launch_outer<T, 4, true>(p, n, adapters, sms, s);
+    if (rank <= 32) return wide ? launch_outer_tc<32, true>(p, n, adapters, sms, s) : launch_outer_tc<32, false>(p, n, adapters, sms, s);
+    return wide ? launch_outer_tc<64, true>(p, n, adapters, sms, s) : launch_outer_tc<64, false>(p, n, adapters, sms, s);
+  } else {
+    if (rank <= 16) return wide ? launch_outer<T, 1, true>(p, n, adapters, sms, s) : launch_outer<T, 1, false>(p, n, adapters, sms, s);
+    if (rank <= 32) return wide ? launch_outer<T, 2, true>(p, n, adapters, sms, s) : launch_outer<T, 2, false>(p, n, adapters, sms, s);
+    return wide ? launch_outer<T, 4, true>(p, n, adapters, sms, s) : launch_outer<T, 4, false>(p, n, adapters, sms, s);
   }
-  return rank <= 16   ? launch_outer<T, 1, false>(p, n, adapters, sms, s)
-         : rank <= 32 ? launch_outer<T, 2, false>(p, n, adapters, sms, s)
-                      : launch_outer<T, 4, false>(p, n, adapters, sms, s);
 }
 
 snack_status adapt_check(int64_t n, int32_t adapters, int32_t rank, int32_t in_f, int32_t out_f, snack_dtype t) {
@@ -1342,19 +1335,12 @@ struct Span {
 };
 bool overlaps(const Span &a, const Span &b) { return spans_overlap(a.p, a.bytes, b.p, b.bytes); }
 
-// Rows of a tile: of bf16 whose rows lie on 16 bytes, and the matrices' on 8, those of TMEM.
-bool on8(const void *m, int32_t ld) { return ptr_aligned(m, 8) && ld % 4 == 0; }
-int down_tile_rows(const DownArgs &d, int32_t m_ld, snack_dtype t) {
-  return t == SNACK_BF16 && row_wide(d.x, d.x_ld, 2) && on8(d.m, m_ld) ? kTcTile : kTile;
-}
-int up_tile_rows(const UpArgs &u, int32_t m_ld, snack_dtype t) {
-  return t == SNACK_BF16 && row_wide(u.base, u.base_ld, 2) && row_wide(u.out, u.out_ld, 2) && on8(u.m, m_ld) ? kTcTile : kTile;
-}
+int tile_rows(snack_dtype t) { return t == SNACK_BF16 ? kTcTile : kTile; }
 
 template <typename T>
-cudaError_t run_fwd(const DownArgs &d, const UpArgs &u, int64_t n, int tile_rows, const AdaptWs &W, int sms, cudaStream_t s) {
-  cudaError_t e = down<T, true>(d, n, tile_rows, W.tile_cap, sms, s);
-  return e != cudaSuccess ? e : up<T, true>(u, n, tile_rows, W.tile_cap, sms, s);
+cudaError_t run_fwd(const DownArgs &d, const UpArgs &u, int64_t n, const AdaptWs &W, int sms, cudaStream_t s) {
+  cudaError_t e = down<T, true>(d, n, W.tile_cap, sms, s);
+  return e != cudaSuccess ? e : up<T, true>(u, n, W.tile_cap, sms, s);
 }
 
 int sms_here() {
@@ -1443,9 +1429,8 @@ snack_status snack_adapt_fwd(const void *x, int64_t x_ld, int64_t n, const void 
     ADAPT_CUDA(t == SNACK_F32 ? few<float>(d, u, ids, (int)n, sms, s) : few<bf16>(d, u, ids, (int)n, sms, s));
     return SNACK_OK;
   }
-  const int rows = std::min(down_tile_rows(d, in_f, t), up_tile_rows(u, rank, t));
-  ADAPT_CUDA(launch_group(ids, (int)n, rows, w, W, s));
-  ADAPT_CUDA(t == SNACK_F32 ? run_fwd<float>(d, u, n, rows, W, sms, s) : run_fwd<bf16>(d, u, n, rows, W, sms, s));
+  ADAPT_CUDA(launch_group(ids, (int)n, tile_rows(t), w, W, s));
+  ADAPT_CUDA(t == SNACK_F32 ? run_fwd<float>(d, u, n, W, sms, s) : run_fwd<bf16>(d, u, n, W, sms, s));
   return SNACK_OK;
 } catch (...) {  // a host allocation failed
   return SNACK_ERR_CUDA;
@@ -1520,11 +1505,10 @@ snack_status snack_adapt_bwd(const void *x, int64_t x_ld, int64_t n, const void 
   u.out = dx;
   u.out_ld = dx_ld;
   u.h_wide = rank % 4 == 0;
-  const int rows = dx ? std::min(down_tile_rows(d, rank, t), up_tile_rows(u, in_f, t)) : down_tile_rows(d, rank, t);
-  ADAPT_CUDA(launch_group(TokenSrc{which, which_t == SNACK_I64, (uint32_t)n_adapters}, (int)n, rows, w, W, s));
+  ADAPT_CUDA(launch_group(TokenSrc{which, which_t == SNACK_I64, (uint32_t)n_adapters}, (int)n, tile_rows(t), w, W, s));
   if (dx || da)
-    ADAPT_CUDA(wide32 ? down<float, false>(d, n, rows, W.tile_cap, sms, s) : down<bf16, false>(d, n, rows, W.tile_cap, sms, s));
-  if (dx) ADAPT_CUDA(wide32 ? up<float, false>(u, n, rows, W.tile_cap, sms, s) : up<bf16, false>(u, n, rows, W.tile_cap, sms, s));
+    ADAPT_CUDA(wide32 ? down<float, false>(d, n, W.tile_cap, sms, s) : down<bf16, false>(d, n, W.tile_cap, sms, s));
+  if (dx) ADAPT_CUDA(wide32 ? up<float, false>(u, n, W.tile_cap, sms, s) : up<bf16, false>(u, n, W.tile_cap, sms, s));
   if (da || db) {
     OuterPair p = {};
     for (OuterArgs &o : p.a) {

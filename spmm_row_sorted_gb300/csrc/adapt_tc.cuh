@@ -107,7 +107,68 @@ __host__ __device__ constexpr size_t tc_down_smem(int rank) {
   return (ring > sums ? ring : sums) + 1024;
 }
 
-// A pieces of 16 bytes as 16 or, where the rows lie on 8, twice 8 of them; `bytes` of them are there.
+// How a matrix's or the rows' pieces of eight elements lie in memory
+enum { kLoose = 0, kOn8 = 1, kOn16 = 2 };
+__host__ inline int lies_on(const void *p, int64_t ld) {
+  return ptr_aligned(p, 16) && ld % 8 == 0 ? kOn16 : ptr_aligned(p, 8) && ld % 4 == 0 ? kOn8 : kLoose;
+}
+
+// Eight elements from anywhere, `left` of them there, the others zeros: the two aligned pieces that hold them, shifted.
+// kKept: read only while the kernel runs.
+template <bool kKept>
+__device__ __forceinline__ uint4 load_loose(const void *p, int left) {
+  if (left <= 0) return make_uint4(0, 0, 0, 0);
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const int skip = (int)(at & 15), bytes = min(left, 8) * 2;
+  const uint4 *from = reinterpret_cast<const uint4 *>(at - skip);
+  uint4 lo, hi = make_uint4(0, 0, 0, 0);
+  if constexpr (kKept) {
+    lo = __ldg(from);
+    if (skip + bytes > 16) hi = __ldg(from + 1);
+  } else {
+    lo = *from;
+    if (skip + bytes > 16) hi = from[1];
+  }
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (skip & 8)
+#pragma unroll
+    for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+  if (skip & 4)
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+  uint32_t v[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[k] = skip & 2 ? __byte_perm(w[k], w[k + 1], 0x5432) : w[k];
+    v[k] = 2 * k + 1 < left ? v[k] : 2 * k < left ? v[k] & 0xFFFFu : 0u;
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+// and to anywhere, by words where they are aligned
+__device__ __forceinline__ void store_loose(uint16_t *p, uint4 v, int left) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if ((reinterpret_cast<uintptr_t>(p) & 2) == 0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (2 * k + 1 < left)
+        *reinterpret_cast<uint32_t *>(p + 2 * k) = w[k];
+      else if (2 * k < left)
+        p[2 * k] = (uint16_t)w[k];
+    }
+  } else {
+    if (left > 0) p[0] = (uint16_t)w[0];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t pair = k < 3 ? __byte_perm(w[k], w[k + 1 < 4 ? k + 1 : 3], 0x5432) : w[k] >> 16;
+      if (k < 3 && 2 * k + 2 < left)
+        *reinterpret_cast<uint32_t *>(p + 2 * k + 1) = pair;
+      else if (2 * k + 1 < left)
+        p[2 * k + 1] = (uint16_t)pair;
+    }
+  }
+}
+
+// A piece of 16 bytes as 16 or, where it lies on 8, twice 8 of them; `bytes` of them are there.
 __device__ __forceinline__ void copy_piece(void *to, const void *from, int bytes, bool wide) {
   if (wide) {
     copy_async<16>(to, from, bytes);
@@ -116,10 +177,41 @@ __device__ __forceinline__ void copy_piece(void *to, const void *from, int bytes
     copy_async<8>(reinterpret_cast<uint8_t *>(to) + 8, reinterpret_cast<const uint8_t *>(from) + (bytes > 8 ? 8 : 0), max(bytes - 8, 0));
   }
 }
+// Pieces of a matrix, place(k, to, from, bytes) naming the k-th of n: on their way, or, where they lie anywhere, read two at
+// a time and there.
+template <typename F>
+__device__ __forceinline__ void copy_pieces(int n, int on, F place) {
+  if (on != kLoose) {
+#pragma unroll 2
+    for (int k = 0; k < n; ++k) {
+      uint8_t *to;
+      const bf16 *from;
+      int bytes;
+      place(k, to, from, bytes);
+      copy_piece(to, from, bytes, on == kOn16);
+    }
+    return;
+  }
+#pragma unroll 1
+  for (int k = 0; k < n; k += 2) {
+    uint8_t *to[2];
+    uint4 v[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const bf16 *from;
+      int bytes = 0;
+      place(min(k + u, n - 1), to[u], from, bytes);
+      v[u] = load_loose<true>(from, bytes / 2);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) *reinterpret_cast<uint4 *>(to[u]) = v[u];
+  }
+}
 
 // A tile of 128 rows against an adapter's matrix, all of its ranks (N); the cluster's blocks have every so many 64 of K.
-template <bool kAlong>
-__global__ void __launch_bounds__(kTcThreads, 2) k_adapt_down_tc(const DownArgs a, int m_wide) {
+// kWide: the rows lie on 16 bytes.
+template <bool kAlong, bool kWide>
+__global__ void __launch_bounds__(kTcThreads, 2) k_adapt_down_tc(const DownArgs a, int m_on) {
   pdl_wait();
   const uint32_t block = cluster_rank(), blocks = cluster_blocks();
   const Tile tile = a.tiles[blockIdx.x / blocks];
@@ -156,29 +248,38 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_adapt_down_tc(const DownArgs 
       const int k0 = (i * (int)blocks + (int)block) * kTcK;
       uint8_t *to = ring + (i % kTcDownStages) * stage_bytes;
       const int left = a.k - k0, bytes = max(0, min(left - 8 * (lane & 7), 8)) * 2;
+      auto place = [&](int u) { return to + (threadIdx.x / 8 + u * (kTcThreads / 8)) * 128 + (((lane & 7) ^ ((threadIdx.x / 8) & 7)) << 4); };
+      if constexpr (kWide) {
 #pragma unroll
-      for (int u = 0; u < kPasses; ++u) {
-        const int t = threadIdx.x / 8 + u * (kTcThreads / 8);
-        if (t < tile.count) copy_async<16>(to + t * 128 + (((lane & 7) ^ (t & 7)) << 4), bytes ? row[u] + k0 : row[u], bytes);
+        for (int u = 0; u < kPasses; ++u)
+          if (threadIdx.x / 8 + u * (kTcThreads / 8) < tile.count) copy_async<16>(place(u), bytes ? row[u] + k0 : row[u], bytes);
+      } else {
+        uint4 v[kPasses];
+#pragma unroll
+        for (int u = 0; u < kPasses; ++u)
+          v[u] = load_loose<true>(row[u] + k0, threadIdx.x / 8 + u * (kTcThreads / 8) < tile.count ? bytes / 2 : 0);
+#pragma unroll
+        for (int u = 0; u < kPasses; ++u) *reinterpret_cast<uint4 *>(place(u)) = v[u];
       }
-      to += kTcRowBox;
       // the matrix: eight threads have 128 bytes of every 32nd row; zeros past the end
       const int c = lane & 7, r0 = threadIdx.x >> 3;
-      to += r0 * 128 + ((c ^ (r0 & 7)) << 4);
+      uint8_t *box = to + kTcRowBox + r0 * 128 + ((c ^ (r0 & 7)) << 4);
+      constexpr int kEvery = kTcThreads / 8;
       if constexpr (kAlong) {
-        for (int r = r0; r < n_pad; r += kTcThreads / 8, to += kTcThreads / 8 * 128) {
-          const int there = r < rank ? bytes : 0;
-          copy_piece(to, there ? mat + (int64_t)r * a.k + k0 + 8 * c : mat, there, m_wide);
-        }
+        copy_pieces((n_pad - r0 + kEvery - 1) / kEvery, m_on, [&](int k, uint8_t *&at, const bf16 *&from, int &n) {
+          const int r = r0 + k * kEvery;
+          at = box + k * kEvery * 128;
+          n = r < rank ? bytes : 0;
+          from = n ? mat + (int64_t)r * a.k + k0 + 8 * c : mat;
+        });
       } else {
-        for (int b = 8 * c; b < n_pad; b += 64, to += kTcK * 128) {
-          const int there = max(0, min(rank - b, 8)) * 2;
-#pragma unroll
-          for (int u = 0; u < kTcK / (kTcThreads / 8); ++u) {
-            const int k = r0 + u * (kTcThreads / 8);
-            copy_piece(to + u * (kTcThreads / 8) * 128, there && k < left ? mat + (int64_t)(k0 + k) * rank + b : mat, k < left ? there : 0, m_wide);
-          }
-        }
+        copy_pieces(8 * c < n_pad ? 2 * ((n_pad - 8 * c + 63) / 64) : 0, m_on, [&](int k, uint8_t *&at, const bf16 *&from, int &n) {
+          static_assert(kTcK == 2 * kEvery, "two rows of each 64");
+          const int b = 8 * c + 64 * (k >> 1), r = r0 + (k & 1) * kEvery;
+          at = box + (k >> 1) * kTcK * 128 + (k & 1) * kEvery * 128;
+          n = r < left ? max(0, min(rank - b, 8)) * 2 : 0;
+          from = n ? mat + (int64_t)(k0 + r) * rank + b : mat;
+        });
       }
     }
     fetch_commit();
@@ -256,15 +357,19 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_adapt_down_tc(const DownArgs 
   if (blocks > 1) cluster_sync();  // no block's memory is read any more
 }
 
-template <bool kAlong>
+template <bool kAlong, bool kWide>
 cudaError_t launch_down_tc(const DownArgs &a, int64_t tiles, int tile_cap, int sms, cudaStream_t s) {
   const size_t smem = tc_down_smem(a.rank);
-  const auto kernel = k_adapt_down_tc<kAlong>;
+  const auto kernel = k_adapt_down_tc<kAlong, kWide>;
   cudaError_t e = raise_smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
-  const int m_wide = ptr_aligned(a.m, 16) && (kAlong ? a.k : a.rank) % 8 == 0;
   const unsigned c = cluster_for(tiles, ceil_div(a.k, 2 * kTcK), 2 * sms);
-  return launch_cluster(c, kernel, dim3((unsigned)tile_cap * c), kTcThreads, smem, s, a, m_wide);
+  return launch_cluster(c, kernel, dim3((unsigned)tile_cap * c), kTcThreads, smem, s, a, lies_on(a.m, kAlong ? a.k : a.rank));
+}
+template <bool kAlong>
+cudaError_t down_tc(const DownArgs &a, int64_t tiles, int tile_cap, int sms, cudaStream_t s) {
+  return lies_on(a.x, a.x_ld) == kOn16 ? launch_down_tc<kAlong, true>(a, tiles, tile_cap, sms, s)
+                                       : launch_down_tc<kAlong, false>(a, tiles, tile_cap, sms, s);
 }
 
 // ------------------------------------------------------------ y and dx
@@ -337,8 +442,9 @@ __device__ __noinline__ void write_some(uint16_t *p, uint4 v, int left) {
 // For that the matrix's rows lie in the order of a fragment's columns (kAlong), or pairs change lanes.
 // (Base and result through shared memory, 64 columns at a time: 143 us for y of 8192 x 16384 of rank 64, 41 % of shared
 // memory's cycles; eight warps doing everything in turn 190, of a step's 3700 cycles 1200 waiting for the products.)
-template <bool kAlong>
-__global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a, int m_wide) {
+// kWide: the base's and the result's rows lie on 16 bytes.
+template <bool kAlong, bool kWide>
+__global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a, int m_on) {
   pdl_wait();
   extern __shared__ uint8_t tc_raw[];
   __shared__ uint64_t full[kTcUpMostStages], empty[kTcUpMostStages], done[2], taken[2];
@@ -396,13 +502,16 @@ __global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a,
       }
       uint4 base[2][4];
       auto read = [&](int past, bool whole, uint4 (&v)[4]) {  // columns `past` behind the first ones
-        if (a.base && whole) {
+        if (kWide && a.base && whole) {
 #pragma unroll
           for (int r = 0; r < 4; ++r)
             if (in[r]) v[r] = *reinterpret_cast<const uint4 *>(from[r] + past);
         } else {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] = read_some(from[r] + past, a.base && in[r] ? a.cols - col - past : 0);
+          for (int r = 0; r < 4; ++r) {
+            const int left = a.base && in[r] ? a.cols - col - past : 0;
+            v[r] = kWide ? read_some(from[r] + past, left) : load_loose<false>(from[r] + past, left);
+          }
         }
       };
       const bool whole_first = !a.base || col0 + kTcUpCols <= a.cols;
@@ -477,13 +586,19 @@ __global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a,
               for (int j = 0; j < 4; ++j) o[j] = pack_pair(bf16_lo(o[j]) + x[4 * j], bf16_hi(o[j]) + x[4 * j + 1]);
             }
           }
-          if (whole) {
+          if (kWide && whole) {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
               if (in[r]) *reinterpret_cast<uint4 *>(to[r] + past) = base[sub][r];
           } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) write_some(to[r] + past, base[sub][r], in[r] ? a.cols - col - past : 0);
+            for (int r = 0; r < 4; ++r) {
+              const int left = in[r] ? a.cols - col - past : 0;
+              if constexpr (kWide)
+                write_some(to[r] + past, base[sub][r], left);
+              else
+                store_loose(to[r] + past, base[sub][r], left);
+            }
           }
           if (a.base && i + 1 < items) read(past + kTcUpCols, col0 + (i + 2) * kTcUpCols <= a.cols, base[sub]);
         }
@@ -505,25 +620,39 @@ __global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a,
             const int bytes = max(0, min(rank - 64 * b - 8 * c, 8)) * 2;
             const bf16 *p = mat + (int64_t)(col + n0) * rank + 64 * b + 8 * c;
             uint8_t *even = to + r0 * 128 + ((c ^ r0) << 4), *odd = to + (r0 + 4) * 128 + ((c ^ (r0 + 4)) << 4) - 512;
-            if (left >= kTcUpCols && bytes == 16 && m_wide) {
+            if (left >= kTcUpCols && bytes == 16 && m_on == kOn16) {
 #pragma unroll
               for (int u = 0; u < kTcUpCols / 4; ++u)
                 copy_whole<16>((u & 1 ? odd : even) + u * 512, p + (32 * (u >> 3) + 16 * (u & 1) + 2 * ((u >> 1) & 3)) * rank);
             } else {
-#pragma unroll 4
-              for (int u = 0; u < kTcUpCols / 4; ++u) {
-                const int n = 32 * (u >> 3) + 16 * (u & 1) + 2 * ((u >> 1) & 3), there = n0 + n < left ? bytes : 0;
-                copy_piece((u & 1 ? odd : even) + u * 512, there ? p + n * rank : mat, there, m_wide);
-              }
+              copy_pieces(kTcUpCols / 4, m_on, [&](int u, uint8_t *&at, const bf16 *&piece, int &there) {
+                const int n = 32 * (u >> 3) + 16 * (u & 1) + 2 * ((u >> 1) & 3);
+                at = (u & 1 ? odd : even) + u * 512;
+                there = n0 + n < left ? bytes : 0;
+                piece = there ? p + n * rank : mat;
+              });
             }
           }
         } else {  // 16 lanes have the 256 bytes of a row
           const int c = lane & 15, r0 = lane >> 4, bytes = max(0, min(left - 8 * c, 8)) * 2;
           to += (c >> 3) * k_blocks * 64 * 128;
+          auto place = [&](int u, uint8_t *&at, const bf16 *&piece, int &there) {
+            const int k = r0 + 2 * u;
+            at = to + k * 128 + (((c & 7) ^ (k & 7)) << 4);
+            there = k < rank ? bytes : 0;
+            piece = there ? mat + (int64_t)k * a.cols + col + 8 * c : mat;
+          };
+          if (left >= kTcUpCols && rank % 16 == 0 && m_on == kOn16) {
 #pragma unroll 8
-          for (int k = r0; k < 16 * steps; k += 2) {
-            const int there = k < rank ? bytes : 0;
-            copy_piece(to + k * 128 + (((c & 7) ^ (k & 7)) << 4), there ? mat + (int64_t)k * a.cols + col + 8 * c : mat, there, m_wide);
+            for (int u = 0; u < 8 * steps; ++u) {
+              uint8_t *at;
+              const bf16 *piece;
+              int there;
+              place(u, at, piece, there);
+              copy_whole<16>(at, mat + (int64_t)(r0 + 2 * u) * a.cols + col + 8 * c);
+            }
+          } else {
+            copy_pieces(8 * steps, m_on, place);
           }
         }
         fetch_commit();
@@ -578,15 +707,19 @@ __global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a,
   }
 }
 
-template <bool kAlong>
+template <bool kAlong, bool kWide>
 cudaError_t launch_up_tc(const UpArgs &a, int tile_cap, int sms, cudaStream_t s) {
   const size_t smem = tc_up_smem(a.rank);
-  const auto kernel = k_adapt_up_tc<kAlong>;
+  const auto kernel = k_adapt_up_tc<kAlong, kWide>;
   cudaError_t e = raise_smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
-  const int m_wide = ptr_aligned(a.m, 16) && (kAlong ? a.rank : a.cols) % 8 == 0;
   const int64_t most = tile_cap * ceil_div(a.cols, kTcUpCols), room = (int64_t)sms * (smem <= 113 * 1024 ? 2 : 1);
-  return launch_pdl(kernel, (unsigned)std::min(most, room), kTcUpThreads, smem, s, a, m_wide);
+  return launch_pdl(kernel, (unsigned)std::min(most, room), kTcUpThreads, smem, s, a, lies_on(a.m, kAlong ? a.rank : a.cols));
+}
+template <bool kAlong>
+cudaError_t up_tc(const UpArgs &a, int tile_cap, int sms, cudaStream_t s) {
+  return (!a.base || lies_on(a.base, a.base_ld) == kOn16) && lies_on(a.out, a.out_ld) == kOn16 ? launch_up_tc<kAlong, true>(a, tile_cap, sms, s)
+                                                                                              : launch_up_tc<kAlong, false>(a, tile_cap, sms, s);
 }
 
 // ------------------------------------------------------------ dA and dB
@@ -651,8 +784,9 @@ __device__ __forceinline__ void tc_outer_write(const OuterArgs &a, const float *
 
 // An adapter's sums over its rows for 256 columns of x (A, as it lies) and kRanks of v
 // (B: its second parts, then its first ones, into the same sums).
-template <int kRanks>
-__global__ void __launch_bounds__(kTcThreads, 3) k_adapt_outer_tc(const OuterPair pair) {
+// kWide: the rows of x lie on 16 bytes.
+template <int kRanks, bool kWide>
+__global__ void __launch_bounds__(kTcThreads, kWide ? 3 : 2) k_adapt_outer_tc(const OuterPair pair) {
   pdl_wait();
   const uint32_t block = cluster_rank(), blocks = cluster_blocks();
   const int slices = (int)(blockIdx.x / blocks), second = slices >= pair.slices ? 1 : 0;
@@ -694,10 +828,22 @@ __global__ void __launch_bounds__(kTcThreads, 3) k_adapt_outer_tc(const OuterPai
   auto fetch = [&](int i, int tokens) {
     if (i < steps) {
       uint8_t *to = ring + (i % kTcStages) * kStage + (lane >> 3) * kTcBox;
+      uint4 v[kTcRows / 8];
 #pragma unroll
       for (int u = 0; u < kTcRows / 8; ++u) {
         const int k = warp + 8 * u, token = __shfl_sync(0xffffffffu, tokens, k);
-        copy_async<16>(to + k * 128 + (((lane & 7) ^ (k & 7)) << 4), x + max(token, 0) * a.x_ld, token >= 0 ? bytes : 0);
+        const bf16 *from = x + max(token, 0) * a.x_ld;
+        if constexpr (kWide)
+          copy_async<16>(to + k * 128 + (((lane & 7) ^ (k & 7)) << 4), from, token >= 0 ? bytes : 0);
+        else
+          v[u] = load_loose<true>(from, token >= 0 ? bytes / 2 : 0);
+      }
+      if constexpr (!kWide) {
+#pragma unroll
+        for (int u = 0; u < kTcRows / 8; ++u) {
+          const int k = warp + 8 * u;
+          *reinterpret_cast<uint4 *>(to + k * 128 + (((lane & 7) ^ (k & 7)) << 4)) = v[u];
+        }
       }
     }
     fetch_commit();
@@ -823,10 +969,10 @@ __global__ void __launch_bounds__(kTcThreads, 3) k_adapt_outer_tc(const OuterPai
   if (blocks > 1) cluster_sync();
 }
 
-template <int kRanks>
+template <int kRanks, bool kWide>
 cudaError_t launch_outer_tc(OuterPair p, int64_t n, int32_t adapters, int sms, cudaStream_t s) {
   const size_t smem = tc_outer_smem(kRanks);
-  const auto kernel = k_adapt_outer_tc<kRanks>;
+  const auto kernel = k_adapt_outer_tc<kRanks, kWide>;
   cudaError_t e = raise_smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
   p.slices = p.a[0].out ? (int32_t)ceil_div(p.a[0].cols, kTcCols) : 0;

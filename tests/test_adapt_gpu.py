@@ -367,3 +367,22 @@ def test_adapt_of_many_rows_matches_definition(n, adapters, rank, width, out, dt
     snack.adapt_grad(c.x, c.dy, *c.args(), h, c.scales, dx=into)
     check(into, val[1] + start.double(), mag[1] + start.double().abs(), rel[1], "dx added")
     assert torch.equal(into[outside], start[outside])
+
+
+@pytest.mark.parametrize("lead", [1, 2, 3, 4, 5, 6, 7])
+def test_adapt_of_rows_that_lie_anywhere(lead):
+    """Starts at every element of an access, rows of odd and even steps, matrices too."""
+    for n, rank, width, out, gap in ((300, 9, 133, 141, 0), (270, 33, 65, 130, 1), (290, 3, 130, 71, 2)):
+        c = Case(n, 3, rank, width, out, "bf16", "runs", gap, lead, seed=lead)
+        val, mag = c.want()
+        rel = bounds(c)
+        y, h = snack.adapt(c.x, c.base, *c.args(), c.scales, keep=True)
+        grads = snack.adapt_grad(c.x, c.dy, *c.args(), h, c.scales)
+        for got, i, what in ((y, 0, "y"), (grads[0], 1, "dx"), (grads[1], 2, "da"), (grads[2], 3, "db")):
+            check(got, val[i], mag[i], rel[i], what)
+        buf = torch.full((n * (out + gap) + lead + 9,), 7.0, device="cuda", dtype=torch.bfloat16)
+        into = buf[lead:lead + n * (out + gap)].view(n, out + gap)[:, :out]
+        snack.adapt(c.x, c.base, *c.args(), c.scales, out=into)
+        assert torch.equal(into, y)
+        into.fill_(7.0)
+        assert bool((buf == 7).all())  # nothing beside the rows was written
