@@ -9,24 +9,24 @@
 //   dB_a = s_a sum_i dy_i h_i^T
 //
 // All of it is bound by memory for the ranks that adapters have: x, base and y
-// (dy, dx) go over the bus once each, an adapter's matrices once per 64 rows,
-// out of L2.  One block first files the rows by adapter, stably, into tiles of up
-// to 64 rows of one adapter (k_adapt_group).  Three kernels do the products:
-//   down   h, dh: a tile against one adapter's matrix, K split over a block's
-//          warps and a cluster's blocks, whose sums meet in shared memory;
-//   up     y, dx: rank is the K, so a tile's h stays in shared memory and each
-//          warp has 32 columns; the product is added to the base and rounded once;
+// (dy, dx) go over the bus once each, an adapter's matrices once per tile, out of
+// L2.  One block first files the rows by adapter, stably, into tiles of rows of one
+// adapter (k_adapt_group).  Three kernels do the products:
+//   down   h, dh: a tile against one adapter's matrix, K split over a cluster's
+//          blocks, whose sums meet in shared memory;
+//   up     y, dx: rank is the K, so a tile's h stays in shared memory for all
+//          columns; the product is added to the base and rounded once;
 //   outer  dA, dB: sums over an adapter's rows, in their order.
-// The products run on the tensor cores by mma.sync, operands straight from global
-// memory: which columns of a group a lane holds does not matter to a sum as long as
-// both operands agree, so every lane reads 16 consecutive bytes of a row.  (tcgen05
-// would want 128 rows of one adapter and a rank of 64 at least, and both operands
-// laid out in shared memory, to save arithmetic that is not the bound.)  fp32
-// operands are cut into three bf16 parts in registers, six part products down to
-// 2^-16 of the leading one, 16 of K on the tensor core at a time: its sums round
-// towards zero.  h and dh are fp32 in memory and go into products as two bf16 parts
-// (bf16 operands: 2^-17 of an entry, far below the output's rounding) or three.
-// Every sum has one order: results repeat bit for bit.
+// bf16 goes through tcgen05 in tiles of 128 rows (adapt_tc.cuh).  fp32, in tiles of
+// 64, and few rows of either type (down and up in one launch, k_adapt_few) through
+// mma.sync, operands as they lie: which columns of a group a lane holds does not
+// matter to a sum as long as both operands agree, so every lane reads 16
+// consecutive bytes of a row.  fp32 operands are cut into three bf16 parts in
+// registers, six part products down to 2^-16 of the leading one, 16 of K on the
+// tensor core at a time: its sums round towards zero.  h and dh are fp32 in memory
+// and go into products as two bf16 parts (bf16 operands: 2^-17 of an entry, far
+// below the output's rounding) or three.  Every sum has one order: results repeat
+// bit for bit.
 #include <math.h>
 #include <stdint.h>
 
@@ -392,12 +392,10 @@ struct DownArgs {
   int x_wide, m_wide;   // the rows, the matrices are aligned to whole accesses
 };
 
-constexpr int kDownParts = 8;  // shares of K in a block: a warp each, or a pair that shares the rows' part and has half the
-                               // ranks each (one warp with all 64: 128 sums, eight warps on an SM; dh of 8192 x 16384 130 us)
-// groups of K a pair has on their way or in hand, so that an SM has 130 to 190 KB
-__host__ __device__ constexpr int down_stages(int cols) { return cols >= 64 ? 3 : 4; }
+constexpr int kDownParts = 8;   // shares of K in a block: a warp each, or a pair that shares the rows' part and has half of the ranks each
+constexpr int kDownStages = 4;  // groups of K that are on their way or in hand
 __host__ __device__ constexpr int down_smem(int cols) {
-  const int ring = kDownParts * down_stages(cols) * (kTile / 8 + cols / 8) * 512, sums = 4 * kTile * cols * 4;
+  const int ring = kDownParts * kDownStages * (kTile / 8 + cols / 8) * 512, sums = 4 * kTile * cols * 4;
   return ring > sums ? ring : sums;
 }
 
@@ -405,7 +403,7 @@ __host__ __device__ constexpr int down_smem(int cols) {
 template <typename T, int MT, int NT, int kHalves, bool kAlong, bool kWide>
 __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, int slice, float *smem) {
   typedef Op<T> O;
-  constexpr int kRows = 16 * MT, kCols = 8 * NT * kHalves, kStages = down_stages(kCols), kSlots = kTile / 8 + NT * kHalves;
+  constexpr int kRows = 16 * MT, kCols = 8 * NT * kHalves, kStages = kDownStages, kSlots = kTile / 8 + NT * kHalves;
   constexpr int kThreads = kDownParts * kHalves * 32;
   typedef Pack<T, NT * (int)sizeof(T)> Cross;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -597,8 +595,7 @@ __host__ __device__ constexpr int up_stage_bytes() { return up_base_bytes<T>() +
 template <typename T>
 __host__ __device__ constexpr int up_stages() { return sizeof(T) == 2 ? 3 : 2; }
 
-static_assert(kUpWarps * up_stages<bf16>() * up_stage_bytes<bf16, 4>() * 32 + up_h_bytes<bf16>(64) <= 232448 &&
-                  kUpWarps * up_stages<bf16>() * up_stage_bytes<bf16, 2>() * 32 + up_h_bytes<bf16>(kMostRank) <= 232448 &&
+static_assert(kUpWarps * up_stages<bf16>() * up_stage_bytes<bf16, 2>() * 32 + up_h_bytes<bf16>(kMostRank) <= 232448 &&
                   kUpWarps * up_stages<float>() * up_stage_bytes<float, 1>() * 32 + up_h_bytes<float>(kMostRank) <= 232448,
               "shared memory of one block");
 
@@ -638,7 +635,7 @@ __device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, int s
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pair = warp >> 1, half = warp & 1;
   const int g = lane >> 2, q = lane & 3;
   const int ld = up_ld<T>(a.rank) / 2, plane = kTile * ld;  // in words
-  const int steps = none ? 1 : (a.rank + 15) / 16, turns = kWhole && kSteps == 4 ? 1 : (steps + kSteps - 1) / kSteps;
+  const int steps = none ? 1 : (a.rank + 15) / 16, turns = (steps + kSteps - 1) / kSteps;
   const int first_row = 32 * half, m_tiles = kWhole ? MT : max(0, min(MT, (tile.count - first_row + 15) / 16));
   uint8_t *ring = up_ring + pair * kStages * kStage;
   uint32_t *hs = reinterpret_cast<uint32_t *>(up_ring + kUpWarps * kStages * kStage);
