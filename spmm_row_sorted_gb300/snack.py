@@ -989,23 +989,27 @@ _adapt_ws = functools.lru_cache(maxsize=256)(snack_adapt_workspace_size)
 def _adapt_args(x, a, b, which, scales):
     """What both calls take of x and the adapters, and a workspace; and what to keep alive."""
     x, xa, n, width, x_ld = _matrix(x)
-    if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2] or a.shape[2] != width:
+    kind, shape_a, shape_b = x.dtype, a.shape, b.shape
+    if len(shape_a) != 3 or len(shape_b) != 3:
         raise ValueError("a must be [adapters, rank, width of x] and b [adapters, width of the output, rank]")
-    kind = x.dtype
+    adapters, rank, in_f = shape_a
+    if shape_b[0] != adapters or shape_b[2] != rank or in_f != width:
+        raise ValueError("a must be [adapters, rank, width of x] and b [adapters, width of the output, rank]")
     if a.dtype != kind or b.dtype != kind:
         raise ValueError("x, a and b must have one type")
     if which.numel() != n:
         raise ValueError("which needs one entry per row of x")
-    adapters, rank, _ = a.shape
+    scales_addr = None
     if scales is not None:
         if scales.dtype != torch.float32 or scales.numel() != adapters:
             raise ValueError("scales must hold one float32 value per adapter")
         scales = scales.contiguous()
+        scales_addr = scales.data_ptr()
     a, b, which = a.contiguous(), b.contiguous(), which.contiguous()
-    nbytes = max(256, _adapt_ws(n, adapters, rank))
+    nbytes = _adapt_ws(n, adapters, rank) or 256
     ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-    args = (xa, x_ld, n, a.data_ptr(), b.data_ptr(), adapters, rank, width, b.shape[1], _code(_DTYPES, kind),
-            which.data_ptr(), _code(_INDICES, which.dtype), _addr(scales))
+    args = (xa, x_ld, n, a.data_ptr(), b.data_ptr(), adapters, rank, width, shape_b[1], _code(_DTYPES, kind), which.data_ptr(),
+            _code(_INDICES, which.dtype), scales_addr)
     return args, ws, nbytes, (x, a, b, which, scales)
 
 
@@ -1025,7 +1029,7 @@ def adapt(x: torch.Tensor, base: Optional[torch.Tensor], a: torch.Tensor, b: tor
     n, rank, out_f, kind = args[2], args[6], args[8], kept[0].dtype
     base_addr, base_ld = None, 0
     if base is not None:
-        if base.dtype != kind or tuple(base.shape) != (n, out_f):
+        if base.dtype != kind or base.shape != (n, out_f):
             raise ValueError(f"base must be a {kind} matrix [{n}, {out_f}]")
         if out is not base:
             base, base_addr, _, _, base_ld = _matrix(base)
@@ -1056,21 +1060,21 @@ def adapt_grad(x: torch.Tensor, dy: torch.Tensor, a: torch.Tensor, b: torch.Tens
             return adapt_grad(x, dy, a, b, which, h, scales, dx, want_dx, want_da, want_db)
     args, ws, nbytes, kept = _adapt_args(x, a, b, which, scales)
     n, adapters, rank, width, out_f, kind = args[2], args[5], args[6], args[7], args[8], kept[0].dtype
-    if dy.dtype != kind or tuple(dy.shape) != (n, out_f):
+    if dy.dtype != kind or dy.shape != (n, out_f):
         raise ValueError(f"dy must be a {kind} matrix [{n}, {out_f}]")
     dy, dy_addr, _, _, dy_ld = _matrix(dy)
     if h is None:
         if want_db:
             raise ValueError("the gradient of b needs h")
-    elif h.dtype != torch.float32 or tuple(h.shape) != (n, rank) or not h.is_contiguous():
+    elif h.dtype != torch.float32 or h.shape != (n, rank) or not h.is_contiguous():
         raise ValueError("h must be what adapt kept for these arguments")
     add = dx is not None
     if add:
         _out_rows(dx, n, width, kind)
     elif want_dx:
         dx = torch.empty((n, width), dtype=kind, device=x.device)
-    da = torch.empty((adapters, rank, width), dtype=kind, device=x.device) if want_da else None
-    db = torch.empty((adapters, out_f, rank), dtype=kind, device=x.device) if want_db else None
+    da = torch.empty_like(kept[1]) if want_da else None
+    db = torch.empty_like(kept[2]) if want_db else None
     dx_ld = 0 if dx is None else width if n < 2 else dx.stride(0)
     st = (_lib or load()).snack_adapt_bwd(*args, _addr(h), dy_addr, dy_ld, 1 if add else 0, _addr(dx), dx_ld, _addr(da),
                                           _addr(db), ws.data_ptr(), nbytes, _raw_stream(None))
