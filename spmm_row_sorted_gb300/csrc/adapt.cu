@@ -583,7 +583,7 @@ constexpr int kUpCols = 32;  // columns of a pair at a time
 // highest ranks of fp32 have no room for that.
 template <typename T>
 __host__ __device__ constexpr int up_ld(int rank) {
-  return sizeof(T) == 2 ? (rank + 63) / 64 * 64 + 8 : rank > 240 ? kMostRank + 8 : (rank + 63) / 64 * 64 + 16;
+  return sizeof(T) == 2 ? (rank + 63) / 64 * 64 + 8 : rank > 192 ? kMostRank + 8 : (rank + 63) / 64 * 64 + 16;
 }
 template <typename T>
 constexpr size_t up_h_bytes(int rank) { return (size_t)kTile * up_ld<T>(rank) * 4; }
@@ -596,7 +596,9 @@ template <typename T>
 __host__ __device__ constexpr int up_stages() { return sizeof(T) == 2 ? 3 : 2; }
 
 static_assert(kUpWarps * up_stages<bf16>() * up_stage_bytes<bf16, 2>() * 32 + up_h_bytes<bf16>(kMostRank) <= 232448 &&
-                  kUpWarps * up_stages<float>() * up_stage_bytes<float, 1>() * 32 + up_h_bytes<float>(kMostRank) <= 232448,
+                  kUpWarps * up_stages<float>() * up_stage_bytes<float, 1>() * 32 + up_h_bytes<float>(kMostRank) <= 232448 &&
+                  kUpWarps * up_stages<float>() * up_stage_bytes<float, 1>() * 32 + up_h_bytes<float>(193) <= 232448 &&
+                  kUpWarps * up_stages<float>() * up_stage_bytes<float, 1>() * 32 + up_h_bytes<float>(192) <= 232448,
               "shared memory of one block");
 
 // four values of h, which another block of the cluster may have written

@@ -386,3 +386,15 @@ def test_adapt_of_rows_that_lie_anywhere(lead):
         assert torch.equal(into, y)
         into.fill_(7.0)
         assert bool((buf == 7).all())  # nothing beside the rows was written
+
+
+@pytest.mark.parametrize("rank", [192, 193, 208, 240, 241, 255])
+@pytest.mark.parametrize("n", [3, 70, 300])
+def test_adapt_of_the_highest_ranks(n, rank):
+    for dtype in ("f32", "bf16"):
+        c = Case(n, 2, rank, 72, 80, dtype, "runs", 0, 0, seed=n)
+        val, mag = c.want()
+        rel = bounds(c)
+        y, h = snack.adapt(c.x, c.base, *c.args(), c.scales, keep=True)
+        for got, i, what in zip((y, *snack.adapt_grad(c.x, c.dy, *c.args(), h, c.scales)), range(4), ("y", "dx", "da", "db")):
+            check(got, val[i], mag[i], rel[i], what)
