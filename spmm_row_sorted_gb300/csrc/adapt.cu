@@ -194,6 +194,104 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
   pass(true);
 }
 
+// Some rows are filed by every block of the first kernel for itself, which saves a launch; one block writes down what the
+// others need (1023 rows of 768, rank 8, fp32, with gradients: 59 and 50 us,
+// seven launches and five).
+constexpr int kFileRows = 1024, kFileAdapters = 255;
+struct FileArgs {
+  TokenSrc which;  // ids null: the rows are filed already
+  int32_t n, tile_rows, tile_cap;
+  int32_t *order, *start;
+  Tile *tiles;
+};
+
+// Tile `b` of the rows, its rows in `rows`; scratch: kThreads / 32 x (adapters + 1) words.  All of a block.
+template <int kThreads>
+__device__ __forceinline__ Tile file_tile(const FileArgs &f, int b, bool writer, int32_t *scratch, int32_t *rows) {
+  constexpr int kWarps = kThreads / 32, kRounds = kFileRows / kThreads;
+  static_assert(kFileAdapters < kThreads, "a group per thread");
+  __shared__ int2 warp_sum[kWarps];
+  __shared__ Tile found;
+  const int groups = (int)f.which.vocab + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rounds = (f.n + kThreads - 1) / kThreads, first = warp * rounds * 32 + lane;
+  const unsigned below = (1u << lane) - 1u;
+  uint32_t key[kRounds];
+  int place[kRounds];
+#pragma unroll
+  for (int u = 0; u < kRounds; ++u) key[u] = u < rounds && first + 32 * u < f.n ? f.which.key(first + 32 * u) : 0xFFFFFFFFu;
+  for (int i = threadIdx.x; i < kWarps * groups; i += kThreads) scratch[i] = 0;
+  if (threadIdx.x == 0) found = Tile{-1, 0, 0, 0};
+  __syncthreads();
+  int32_t *mine = scratch + warp * groups;
+#pragma unroll
+  for (int u = 0; u < kRounds; ++u) {
+    if (u >= rounds) break;
+    const unsigned peers = __match_any_sync(0xffffffffu, key[u]);
+    const bool here = key[u] != 0xFFFFFFFFu;
+    const int at = here ? mine[key[u]] : 0;
+    __syncwarp();
+    if (here && (peers & below) == 0) mine[key[u]] = at + __popc(peers);
+    place[u] = at + __popc(peers & below);
+    __syncwarp();
+  }
+  __syncthreads();
+  const int g = threadIdx.x;
+  int before_warp[kWarps], count = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    before_warp[w] = count;
+    count += g < groups ? scratch[w * groups + g] : 0;
+  }
+  const int own = (count + f.tile_rows - 1) / f.tile_rows;
+  int2 inc = make_int2(count, own);
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int r = __shfl_up_sync(0xffffffffu, inc.x, d), t = __shfl_up_sync(0xffffffffu, inc.y, d);
+    if (lane >= d) {
+      inc.x += r;
+      inc.y += t;
+    }
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  int from = inc.x - count, tile = inc.y - own, tiles = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) {
+      from += warp_sum[w].x;
+      tile += warp_sum[w].y;
+    }
+    tiles += warp_sum[w].y;
+  }
+  if (g < groups) {
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) scratch[w * groups + g] = from + before_warp[w];
+    if (b >= tile && b < tile + own) found = Tile{g, from + (b - tile) * f.tile_rows, min(f.tile_rows, count - (b - tile) * f.tile_rows), 0};
+    if (writer) {
+      f.start[g] = from;
+      for (int t = 0; t < own; ++t) f.tiles[tile + t] = Tile{g, from + t * f.tile_rows, min(f.tile_rows, count - t * f.tile_rows), 0};
+    }
+  }
+  if (writer) {
+    if (threadIdx.x == 0) {
+      f.start[groups] = f.n;
+      f.start[groups + 1] = tiles;
+    }
+    for (int t = tiles + threadIdx.x; t < f.tile_cap; t += kThreads) f.tiles[t] = Tile{-1, 0, 0, 0};
+  }
+  __syncthreads();
+  const Tile t = found;
+#pragma unroll
+  for (int u = 0; u < kRounds; ++u) {
+    if (key[u] == 0xFFFFFFFFu) continue;
+    const int at = mine[key[u]] + place[u], d = at - t.first;
+    if (d >= 0 && d < t.count) rows[d] = first + 32 * u;
+    if (writer) f.order[at] = first + 32 * u;
+  }
+  __syncthreads();
+  return Tile{t.adapter, 0, t.count, 0};
+}
+
 // ------------------------------------------------------------ operands
 
 // What of a group of K a lane holds: 16 bytes of a row that runs along K, four
@@ -545,10 +643,19 @@ __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, i
 }
 
 template <typename T, int NT, int kHalves, bool kAlong, bool kWide>
-__global__ void __launch_bounds__(kDownParts * kHalves * 32, 1) k_adapt_down(const DownArgs a) {
+__global__ void __launch_bounds__(kDownParts * kHalves * 32, 1) k_adapt_down(const DownArgs args, const FileArgs f) {
   pdl_wait();
   extern __shared__ __align__(16) float down_ring[];
-  const Tile tile = a.tiles[blockIdx.x / cluster_blocks()];
+  __shared__ int32_t rows[kTile];
+  DownArgs a = args;
+  const int b = (int)(blockIdx.x / cluster_blocks());
+  Tile tile;
+  if (f.which.ids) {
+    tile = file_tile<kDownParts * kHalves * 32>(f, b, blockIdx.x == 0 && blockIdx.y == 0, reinterpret_cast<int32_t *>(down_ring), rows);
+    a.order = rows;
+  } else {
+    tile = a.tiles[b];
+  }
   if (tile.adapter < 0 || tile.adapter >= a.adapters) return;  // the whole cluster's
   if (tile.count <= 16)
     down_tile<T, 1, NT, kHalves, kAlong, kWide>(a, tile, blockIdx.y, down_ring);
@@ -1208,7 +1315,7 @@ namespace snack {
 namespace {
 
 template <typename T, int NT, int kHalves, bool kAlong, bool kWide>
-cudaError_t launch_down(const DownArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
+cudaError_t launch_down(const DownArgs &a, const FileArgs &f, int64_t n, int tile_cap, int sms, cudaStream_t s) {
   constexpr int kCols = 8 * NT * kHalves;
   const size_t smem = down_smem(kCols);
   const auto kernel = k_adapt_down<T, NT, kHalves, kAlong, kWide>;
@@ -1216,7 +1323,7 @@ cudaError_t launch_down(const DownArgs &a, int64_t n, int tile_cap, int sms, cud
   if (e != cudaSuccess) return e;
   const unsigned slices = (unsigned)ceil_div(a.rank, kCols);
   const unsigned c = cluster_for(likely_tiles(n, a.adapters, kTile) * slices, ceil_div(a.k, Op<T>::kGroup * kDownParts), sms);
-  return launch_cluster(c, kernel, dim3((unsigned)tile_cap * c, slices), kDownParts * kHalves * 32, smem, s, a);
+  return launch_cluster(c, kernel, dim3((unsigned)tile_cap * c, slices), kDownParts * kHalves * 32, smem, s, a, f);
 }
 // whole accesses of 16 bytes of the rows and of a matrix that runs along K, of `across` elements of one that does not
 template <typename T, bool kAlong>
@@ -1227,16 +1334,16 @@ bool down_wide(DownArgs *a, int across) {
   return a->x_wide && a->m_wide;
 }
 template <typename T, int NT, int kHalves, bool kAlong>
-cudaError_t down_by(DownArgs a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
-  return down_wide<T, kAlong>(&a, NT) ? launch_down<T, NT, kHalves, kAlong, true>(a, n, tile_cap, sms, s)
-                                      : launch_down<T, NT, kHalves, kAlong, false>(a, n, tile_cap, sms, s);
+cudaError_t down_by(DownArgs a, const FileArgs &f, int64_t n, int tile_cap, int sms, cudaStream_t s) {
+  return down_wide<T, kAlong>(&a, NT) ? launch_down<T, NT, kHalves, kAlong, true>(a, f, n, tile_cap, sms, s)
+                                      : launch_down<T, NT, kHalves, kAlong, false>(a, f, n, tile_cap, sms, s);
 }
 template <typename T, bool kAlong>
-cudaError_t down(const DownArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
+cudaError_t down(const DownArgs &a, const FileArgs &f, int64_t n, int tile_cap, int sms, cudaStream_t s) {
   if constexpr (sizeof(T) == 2)
-    return down_tc<kAlong>(a, likely_tiles(n, a.adapters, kTcTile), tile_cap, sms, s);
+    return down_tc<kAlong>(a, f, likely_tiles(n, a.adapters, kTcTile), tile_cap, sms, s);
   else
-    return a.rank <= 16 ? down_by<T, 2, 1, kAlong>(a, n, tile_cap, sms, s) : down_by<T, 2, 2, kAlong>(a, n, tile_cap, sms, s);
+    return a.rank <= 16 ? down_by<T, 2, 1, kAlong>(a, f, n, tile_cap, sms, s) : down_by<T, 2, 2, kAlong>(a, f, n, tile_cap, sms, s);
 }
 
 template <typename T, bool kAlong, int kSteps, bool kWide>
@@ -1335,10 +1442,23 @@ struct Span {
 bool overlaps(const Span &a, const Span &b) { return spans_overlap(a.p, a.bytes, b.p, b.bytes); }
 
 int tile_rows(snack_dtype t) { return t == SNACK_BF16 ? kTcTile : kTile; }
+// how the first kernel files the rows itself; without ids where they are too many
+FileArgs file_args(const TokenSrc &which, int n, snack_dtype t, uint8_t *ws, const AdaptWs &W) {
+  FileArgs f = {};
+  if (n > kFileRows || which.vocab > (uint32_t)kFileAdapters) return f;
+  f.which = which;
+  f.n = n;
+  f.tile_rows = tile_rows(t);
+  f.tile_cap = W.tile_cap;
+  f.order = reinterpret_cast<int32_t *>(ws + W.order);
+  f.start = reinterpret_cast<int32_t *>(ws + W.start);
+  f.tiles = reinterpret_cast<Tile *>(ws + W.tiles);
+  return f;
+}
 
 template <typename T>
-cudaError_t run_fwd(const DownArgs &d, const UpArgs &u, int64_t n, const AdaptWs &W, int sms, cudaStream_t s) {
-  cudaError_t e = down<T, true>(d, n, W.tile_cap, sms, s);
+cudaError_t run_fwd(const DownArgs &d, const UpArgs &u, const FileArgs &f, int64_t n, const AdaptWs &W, int sms, cudaStream_t s) {
+  cudaError_t e = down<T, true>(d, f, n, W.tile_cap, sms, s);
   return e != cudaSuccess ? e : up<T, true>(u, n, W.tile_cap, sms, s);
 }
 
@@ -1428,8 +1548,9 @@ snack_status snack_adapt_fwd(const void *x, int64_t x_ld, int64_t n, const void 
     ADAPT_CUDA(t == SNACK_F32 ? few<float>(d, u, ids, (int)n, sms, s) : few<bf16>(d, u, ids, (int)n, sms, s));
     return SNACK_OK;
   }
-  ADAPT_CUDA(launch_group(ids, (int)n, tile_rows(t), w, W, s));
-  ADAPT_CUDA(t == SNACK_F32 ? run_fwd<float>(d, u, n, W, sms, s) : run_fwd<bf16>(d, u, n, W, sms, s));
+  const FileArgs f = file_args(ids, (int)n, t, w, W);
+  if (!f.which.ids) ADAPT_CUDA(launch_group(ids, (int)n, tile_rows(t), w, W, s));
+  ADAPT_CUDA(t == SNACK_F32 ? run_fwd<float>(d, u, f, n, W, sms, s) : run_fwd<bf16>(d, u, f, n, W, sms, s));
   return SNACK_OK;
 } catch (...) {  // a host allocation failed
   return SNACK_ERR_CUDA;
@@ -1504,9 +1625,11 @@ snack_status snack_adapt_bwd(const void *x, int64_t x_ld, int64_t n, const void 
   u.out = dx;
   u.out_ld = dx_ld;
   u.h_wide = rank % 4 == 0;
-  ADAPT_CUDA(launch_group(TokenSrc{which, which_t == SNACK_I64, (uint32_t)n_adapters}, (int)n, tile_rows(t), w, W, s));
+  const TokenSrc ids{which, which_t == SNACK_I64, (uint32_t)n_adapters};
+  const FileArgs f = dx || da ? file_args(ids, (int)n, t, w, W) : FileArgs{};
+  if (!f.which.ids) ADAPT_CUDA(launch_group(ids, (int)n, tile_rows(t), w, W, s));
   if (dx || da)
-    ADAPT_CUDA(wide32 ? down<float, false>(d, n, W.tile_cap, sms, s) : down<bf16, false>(d, n, W.tile_cap, sms, s));
+    ADAPT_CUDA(wide32 ? down<float, false>(d, f, n, W.tile_cap, sms, s) : down<bf16, false>(d, f, n, W.tile_cap, sms, s));
   if (dx) ADAPT_CUDA(wide32 ? up<float, false>(u, n, W.tile_cap, sms, s) : up<bf16, false>(u, n, W.tile_cap, sms, s));
   if (da || db) {
     OuterPair p = {};

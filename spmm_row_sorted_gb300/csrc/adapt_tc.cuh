@@ -211,12 +211,20 @@ __device__ __forceinline__ void copy_pieces(int n, int on, F place) {
 // A tile of 128 rows against an adapter's matrix, all of its ranks (N); the cluster's blocks have every so many 64 of K.
 // kWide: the rows lie on 16 bytes.
 template <bool kAlong, bool kWide>
-__global__ void __launch_bounds__(kTcThreads, 2) k_adapt_down_tc(const DownArgs a, int m_on) {
+__global__ void __launch_bounds__(kTcThreads, 2) k_adapt_down_tc(const DownArgs args, const FileArgs f, int m_on) {
   pdl_wait();
   const uint32_t block = cluster_rank(), blocks = cluster_blocks();
-  const Tile tile = a.tiles[blockIdx.x / blocks];
-  if (tile.adapter < 0 || tile.adapter >= a.adapters) return;  // the whole cluster's
   extern __shared__ uint8_t tc_raw[];
+  __shared__ int32_t rows[kTcTile];
+  DownArgs a = args;
+  Tile tile;
+  if (f.which.ids) {
+    tile = file_tile<kTcThreads>(f, (int)(blockIdx.x / blocks), blockIdx.x == 0, reinterpret_cast<int32_t *>(tc_raw + (16 - (su32(tc_raw) & 15) & 15)), rows);
+    a.order = rows;
+  } else {
+    tile = a.tiles[blockIdx.x / blocks];
+  }
+  if (tile.adapter < 0 || tile.adapter >= a.adapters) return;  // the whole cluster's
   __shared__ uint64_t done[kTcDownStages];
   __shared__ uint32_t tmem_at;
   uint8_t *ring = tc_raw + ((1024 - (su32(tc_raw) & 1023)) & 1023);
@@ -240,7 +248,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_adapt_down_tc(const DownArgs 
 #pragma unroll
   for (int u = 0; u < kPasses; ++u) {
     const int t = threadIdx.x / 8 + u * (kTcThreads / 8);
-    row[u] = reinterpret_cast<const bf16 *>(a.x) + (int64_t)__ldg(a.order + tile.first + min(t, tile.count - 1)) * a.x_ld + 8 * (lane & 7);
+    row[u] = reinterpret_cast<const bf16 *>(a.x) + (int64_t)a.order[tile.first + min(t, tile.count - 1)] * a.x_ld + 8 * (lane & 7);
   }
   const bf16 *mat = reinterpret_cast<const bf16 *>(a.m) + (int64_t)tile.adapter * rank * a.k;
   auto fetch = [&](int i) {
@@ -358,18 +366,18 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_adapt_down_tc(const DownArgs 
 }
 
 template <bool kAlong, bool kWide>
-cudaError_t launch_down_tc(const DownArgs &a, int64_t tiles, int tile_cap, int sms, cudaStream_t s) {
+cudaError_t launch_down_tc(const DownArgs &a, const FileArgs &f, int64_t tiles, int tile_cap, int sms, cudaStream_t s) {
   const size_t smem = tc_down_smem(a.rank);
   const auto kernel = k_adapt_down_tc<kAlong, kWide>;
   cudaError_t e = raise_smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
   const unsigned c = cluster_for(tiles, ceil_div(a.k, 2 * kTcK), 2 * sms);
-  return launch_cluster(c, kernel, dim3((unsigned)tile_cap * c), kTcThreads, smem, s, a, lies_on(a.m, kAlong ? a.k : a.rank));
+  return launch_cluster(c, kernel, dim3((unsigned)tile_cap * c), kTcThreads, smem, s, a, f, lies_on(a.m, kAlong ? a.k : a.rank));
 }
 template <bool kAlong>
-cudaError_t down_tc(const DownArgs &a, int64_t tiles, int tile_cap, int sms, cudaStream_t s) {
-  return lies_on(a.x, a.x_ld) == kOn16 ? launch_down_tc<kAlong, true>(a, tiles, tile_cap, sms, s)
-                                       : launch_down_tc<kAlong, false>(a, tiles, tile_cap, sms, s);
+cudaError_t down_tc(const DownArgs &a, const FileArgs &f, int64_t tiles, int tile_cap, int sms, cudaStream_t s) {
+  return lies_on(a.x, a.x_ld) == kOn16 ? launch_down_tc<kAlong, true>(a, f, tiles, tile_cap, sms, s)
+                                       : launch_down_tc<kAlong, false>(a, f, tiles, tile_cap, sms, s);
 }
 
 // ------------------------------------------------------------ y and dx
