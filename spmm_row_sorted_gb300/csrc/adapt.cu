@@ -195,9 +195,9 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
 }
 
 // Some rows are filed by every block of the first kernel for itself, which saves a launch; one block writes down what the
-// others need (1023 rows of 768, rank 8, fp32, with gradients: 59 and 50 us,
-// seven launches and five).
-constexpr int kFileRows = 1024, kFileAdapters = 255;
+// others need (1023 rows of 768, rank 8, fp32, with gradients: seven launches 59 us, five 50; 2048 rows of 6208 to 1024,
+// rank 16, bf16: 72 and 70).
+constexpr int kFileRows = 2048, kFileAdapters = 255;
 struct FileArgs {
   TokenSrc which;  // ids null: the rows are filed already
   int32_t n, tile_rows, tile_cap;

@@ -398,3 +398,18 @@ def test_adapt_of_the_highest_ranks(n, rank):
         y, h = snack.adapt(c.x, c.base, *c.args(), c.scales, keep=True)
         for got, i, what in zip((y, *snack.adapt_grad(c.x, c.dy, *c.args(), h, c.scales)), range(4), ("y", "dx", "da", "db")):
             check(got, val[i], mag[i], rel[i], what)
+
+
+@pytest.mark.parametrize("n,adapters", [(257, 255), (257, 256), (511, 1), (1024, 9), (2047, 255), (2048, 40), (2049, 40), (2049, 3)])
+@pytest.mark.parametrize("kind", ["mixed", "runs", "one"])
+def test_adapt_files_rows_by_every_way(n, adapters, kind):
+    """Around the sizes up to which the first product's blocks file the rows themselves."""
+    for dtype, rank in (("f32", 3), ("bf16", 8), ("f32", 40)):
+        c = Case(n, adapters, rank, 40, 24, dtype, kind, 0, 0, seed=n, itype=torch.int32 if n % 2 else torch.int64)
+        val, mag = c.want()
+        rel = bounds(c)
+        y, h = snack.adapt(c.x, c.base, *c.args(), c.scales, keep=True)
+        for got, i, what in zip((y, *snack.adapt_grad(c.x, c.dy, *c.args(), h, c.scales)), range(4), ("y", "dx", "da", "db")):
+            check(got, val[i], mag[i], rel[i], what)
+        only = snack.adapt_grad(c.x, c.dy, *c.args(), h, c.scales, want_dx=False, want_da=False)[2]
+        check(only, val[3], mag[3], rel[3], "db alone")
