@@ -515,8 +515,9 @@ snack_status snack_clip_grad_norm(int32_t n_tensors, const void *const *grads, v
  * values, rows without an adapter untouched) is kept for the gradient, or NULL.
  * n < 2^24, rank <= 256, n_adapters <= 32768, in_f, out_f < 2^20.  The workspace
  * takes n * (rank + 1) * 4 bytes and some per adapter.
- * fp32 products are sums over parts of their operands: one with an infinite or NaN
- * operand is NaN, and so is its row.
+ * Products of fp32 operands, and those of h and dh, are sums over parts of their
+ * operands: one with an infinite or NaN operand may be NaN where fp32 arithmetic has
+ * an infinity, and so may its row; no other row is touched by it.
  */
 snack_status snack_adapt_workspace_size(int64_t n, int32_t n_adapters, int32_t rank, size_t *bytes);
 snack_status snack_adapt_fwd(const void *x, int64_t x_ld, int64_t n, const void *a, const void *b, int32_t n_adapters,
