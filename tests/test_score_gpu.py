@@ -7,7 +7,8 @@ the sums (2^-17 over thousands of terms): |err logp| <= 2 A T + 2^-16 + 2^-22 |l
 within e of itself.  H = log S - sum e^(z - M) (z - M) / S: the second part is at most H and a sum of terms of one sign, each
 within e of itself; dH/dz_v = -p (log p + H), the sum of which over v is at most 2 H: |err H| <= e (1 + 4 H).
 dz = g [v = t] - p (g + h (log p + H)) is within e of the magnitude of each part, p |h| (err logp + err H) and its rounding,
-2^-8 of it (bf16; not of the target's entry, which goes unrounded into both products) or 2^-22 (fp32 parts).  A product's sum adds A of its magnitudes, a bf16 output half an ulp.
+2^-8 of it (bf16; not of the target's entry where g is not 0, which goes unrounded into both products: with g = 0 it is
+an entry like the others, -p h (log p + H) rounded to bf16, by half an ulp and so up to 2^-8 of it) or 2^-22 (fp32 parts).  A product's sum adds A of its magnitudes, a bf16 output half an ulp.
 Ids: where the logits' order is not clear in fp32 the products are summed in twice its precision, so ids are equal to the
 order of the 64-bit logits, whose differences are far above 2^-45 of them here.
 """
@@ -87,7 +88,8 @@ class Want:
         if hasattr(self, "at"):
             dz.scatter_add_(1, self.at[:, None], g)
             if bf:  # its own part of p, too
-                mag.scatter_(1, self.at[:, None], mag.gather(1, self.at[:, None]) * (rel + 2.0 ** -22) / (rel + 2.0 ** -8))
+                own = mag.gather(1, self.at[:, None])
+                mag.scatter_(1, self.at[:, None], torch.where(g != 0, own * (rel + 2.0 ** -22) / (rel + 2.0 ** -8), own))
             mag.scatter_add_(1, self.at[:, None], g.abs() * (rel + 2.0 ** -22))
         for got, want, tol in ((dx, dz @ self.w, mag @ self.w.abs()), (dw, dz.T @ self.x, mag.T @ self.x.abs())):
             tol = tol + HALF_ULP[got.dtype] * (want.abs() + tol) + 2.0 ** -133
