@@ -241,4 +241,13 @@ snack_status dense_dx(snack_layer *h, const void *val, const void *dy, int32_t b
                       size_t ws_bytes, cudaStream_t s);
 snack_status dense_dw(snack_layer *h, const void *x, const void *dy, int32_t batch, float *dw, float *db, void *ws,
                       size_t ws_bytes, cudaStream_t s);
+// Whether a call that needs a context (the encoding of a tensor map) succeeds: a host
+// thread that has made no other CUDA call yet has none, and gets the current device's.
+template <typename F>
+bool with_context(F call) {
+  if (call()) return true;
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && call();
+}
+
 }  // namespace snack

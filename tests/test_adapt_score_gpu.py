@@ -6,6 +6,8 @@ tens of times the result's: gradients agree to 1e-3 of the largest of their tens
 would change.
 """
 
+import threading
+
 import pytest
 import torch
 
@@ -95,3 +97,41 @@ def test_serving_picks_the_likeliest_tokens_and_replays(dtype):
     graph.replay()
     assert all(torch.equal(p, q) for p, q in zip(held, step()))
     m.layer.close()
+
+
+def in_a_new_thread(call):
+    out = []
+
+    def run():
+        try:
+            out.append(call())
+        except Exception as e:  # handed on to the test
+            out.append(e)
+
+    t = threading.Thread(target=run)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    if isinstance(out[0], Exception):
+        raise out[0]
+    return out[0]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_calls_from_a_host_thread_of_their_own(dtype):
+    """A thread's first call of CUDA, too: a server's threads start with any of them."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, w = (torch.randn(r, 96, device="cuda", generator=g).to(dtype) for r in (200, 3000))
+    t = torch.randint(0, 3000, (200,), device="cuda", generator=g)
+    a, b = torch.randn(3, 8, 96, device="cuda", generator=g).to(dtype), torch.randn(3, 96, 8, device="cuda", generator=g).to(dtype)
+    which = torch.randint(0, 3, (200,), device="cuda", generator=g)  # rows without one leave their h as it was
+    up = torch.randn(200, device="cuda", generator=g)
+    y, h = snack.adapt(x, x, a, b, which, keep=True)
+    scored = snack.score(x, w, t, top=3)
+    kept = snack.xent(x, w, t)
+    calls = (lambda: snack.adapt(x, x, a, b, which, keep=True), lambda: snack.adapt_grad(x, x, a, b, which, h),
+             lambda: snack.score(x, w, t, top=3), lambda: snack.score_grad(x, w, t, scored[4], up, up),
+             lambda: snack.xent(x, w, t), lambda: snack.xent_grad(x, w, t, kept[1]))
+    for call in calls:
+        for p, q in zip(in_a_new_thread(call), call()):
+            assert torch.equal(p, q)
