@@ -195,8 +195,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
 }
 
 // Some rows are filed by every block of the first kernel for itself, which saves a launch; one block writes down what the
-// others need (1023 rows of 768, rank 8, fp32, with gradients: seven launches 59 us, five 50; 2048 rows of 6208 to 1024,
-// rank 16, bf16: 72 and 70).
+// others need (1023 rows of 768, rank 8, fp32, with gradients, from cold caches: seven launches 54 us, five 49; 2048 rows
+// of 6208 to 1024, rank 16, bf16: 80 and 77).
 constexpr int kFileRows = 2048, kFileAdapters = 255;
 struct FileArgs {
   TokenSrc which;  // ids null: the rows are filed already
