@@ -510,9 +510,10 @@ snack_status snack_clip_grad_norm(int32_t n_tensors, const void *const *grads, v
  * type t as x [n, in_f], base and y [n, out_f] are; scales holds n_adapters fp32
  * values, or is NULL (1).  A row whose which[i] is outside [0, n_adapters) has no
  * adapter: y[i] is base[i], and nothing is computed of it.  Rows may come in any
- * order.  base may be y itself (in place, with the same row step) or NULL (0: the
- * adapters' part alone); otherwise y overlaps no other argument.  h (n * rank fp32
- * values, rows without an adapter untouched) is kept for the gradient, or NULL.
+ * order.  base may be y itself (in place; the row step has to be the same where
+ * there are several rows) or NULL (0: the adapters' part alone); otherwise y
+ * overlaps no other argument.  h (n * rank fp32 values, rows without an adapter
+ * untouched) is kept for the gradient, or NULL.
  * n < 2^24, rank <= 256, n_adapters <= 32768, in_f, out_f < 2^20.  The workspace
  * takes n * (rank + 1) * 4 bytes and some per adapter.
  * Products of fp32 operands, and those of h and dh, are sums over parts of their

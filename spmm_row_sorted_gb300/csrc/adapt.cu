@@ -1510,7 +1510,7 @@ snack_status snack_adapt_fwd(const void *x, int64_t x_ld, int64_t n, const void 
                        {scales, scales ? (size_t)n_adapters * 4 : 0}};
   for (const Span &r : read)
     if (overlaps(sy, r) || overlaps(sh, r) || overlaps(sw, r)) return SNACK_ERR_INVALID_ARG;
-  const bool in_place = base == y && base_ld == y_ld;
+  const bool in_place = base == y && (n == 1 || base_ld == y_ld);  // of one row the step means nothing
   if ((!in_place && overlaps(sy, sbase)) || overlaps(sh, sbase) || overlaps(sw, sbase) || overlaps(sy, sh) || overlaps(sy, sw) ||
       overlaps(sh, sw))
     return SNACK_ERR_INVALID_ARG;

@@ -413,3 +413,19 @@ def test_adapt_files_rows_by_every_way(n, adapters, kind):
             check(got, val[i], mag[i], rel[i], what)
         only = snack.adapt_grad(c.x, c.dy, *c.args(), h, c.scales, want_dx=False, want_da=False)[2]
         check(only, val[3], mag[3], rel[3], "db alone")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_one_row_in_place_by_another_tensor(dtype):
+    """Of one row the step means nothing: a view of a wider buffer is the same row, whatever its step."""
+    c = Case(1, 2, 12, 90, 51, dtype, "one", gap=3, seed=4)
+    y = snack.adapt(c.x, c.base, *c.args(), c.scales)
+    buf = c.base.new_full((1, 60), 7.0)
+    out, view = buf[:, 4:55], buf[:, 4:55]
+    out.copy_(c.base)
+    snack.adapt(c.x, out, *c.args(), c.scales, out=view)
+    assert torch.equal(out, y) and bool((buf[:, :4] == 7).all()) and bool((buf[:, 55:] == 7).all())
+    out.copy_(c.base)
+    without = torch.full_like(c.which, -1)  # no adapter: the base stays
+    snack.adapt(c.x, out, c.a, c.b, without, c.scales, out=view)
+    assert torch.equal(out, c.base) and bool((buf[:, 55:] == 7).all())
