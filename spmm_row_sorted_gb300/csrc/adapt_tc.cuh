@@ -736,6 +736,12 @@ constexpr int kTcCols = 256;     // columns of a block: two tiles of 128, the la
 constexpr int kTcRows = 32;      // rows (of K) per stage
 constexpr int kTcStages = 3;
 constexpr int kTcBox = kTcRows * 128;  // bytes of 64 columns of a stage
+// Steps summed on the tensor core, which cuts off what does not fit (of terms of one sign 5e-8 of the sum at each of a step's
+// four additions; 2^21 rows of one adapter were off by 1.7e-3), before their sum is added in fp32: 528 additions, 2.7e-5 or
+// a 72nd of half a step of bf16, 4096 rows and a bit.  An even number of rounds of the stages: the barriers' phases begin
+// again with each run.
+constexpr int kTcRun = 132;
+static_assert(kTcRun % (2 * kTcStages) == 0, "whole phases");
 __host__ __device__ constexpr int tc_outer_stage(int ranks) { return (kTcCols + 2 * ranks) / 64 * kTcBox; }
 constexpr size_t tc_outer_smem(int ranks) {
   const size_t ring = (size_t)kTcStages * tc_outer_stage(ranks), sums = std::max((size_t)ranks * (kTcCols + 4), (size_t)kTcCols * (ranks + 4)) * 4;
@@ -792,8 +798,9 @@ __device__ __forceinline__ void tc_outer_write(const OuterArgs &a, const float *
 
 // An adapter's sums over its rows for 256 columns of x (A, as it lies) and kRanks of v
 // (B: its second parts, then its first ones, into the same sums).
-// kWide: the rows of x lie on 16 bytes.
-template <int kRanks, bool kWide>
+// kWide: the rows of x lie on 16 bytes.  kLong: a block may have more than a run of steps (8192 rows, rank 64, 4096 to 16384,
+// four adapters, both calls: 331 us without, 339 with it, where no block has more).
+template <int kRanks, bool kWide, bool kLong>
 __global__ void __launch_bounds__(kTcThreads, kWide ? 3 : 2) k_adapt_outer_tc(const OuterPair pair) {
   pdl_wait();
   const uint32_t block = cluster_rank(), blocks = cluster_blocks();
@@ -811,8 +818,10 @@ __global__ void __launch_bounds__(kTcThreads, kWide ? 3 : 2) k_adapt_outer_tc(co
   const int adapter = blockIdx.y, r0 = blockIdx.z * kRanks;
   const int b0 = (slices - second * pair.slices) * kTcCols;
   const int first = a.start[adapter], end = a.start[adapter + 1];
-  const int step = (int)blocks * kTcRows, p_first = first + (int)block * kTcRows;
-  const int steps = p_first < end ? (end - p_first + step - 1) / step : 0;
+  const int step = (int)blocks * kTcRows;
+  int p_first = first + (int)block * kTcRows;
+  const int all_steps = p_first < end ? (end - p_first + step - 1) / step : 0;
+  int steps = kLong ? min(all_steps, kTcRun) : all_steps, left_steps = all_steps;  // of the run, and from it on
   if (warp == 0) tmem_alloc(&tmem_at, kTmem);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kTcStages; ++s) mbar_init(&done[s], 1);
@@ -823,6 +832,9 @@ __global__ void __launch_bounds__(kTcThreads, kWide ? 3 : 2) k_adapt_outer_tc(co
   tc_fence_after();
   const uint32_t tmem = tmem_at;
   bool ok = true;
+  // this warp's sums: column 32 (warp % 4) + lane of tile warp / 4
+  const uint32_t own_sums = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (warp >> 2) * kRanks;
+  float before[kLong ? kRanks : 1];  // of the runs before: in local memory, for registers would cost the SM's third block (360)
 
   // lane l: the row at place l of a step's 32 (-1 past the end)
   auto tokens_at = [&](int i) {
@@ -887,7 +899,7 @@ __global__ void __launch_bounds__(kTcThreads, kWide ? 3 : 2) k_adapt_outer_tc(co
       }
     }
   };
-  if (steps) {
+  while (steps) {
     constexpr uint32_t kInst = tc_inst(128, kRanks, true, true);
     int ahead[kTcStages];  // the rows of steps i + 1, ..., i + kTcStages
     Held even, odd;        // v of the step in hand and of the next one
@@ -934,22 +946,35 @@ __global__ void __launch_bounds__(kTcThreads, kWide ? 3 : 2) k_adapt_outer_tc(co
     fetch_wait<0>();
     ok = mbar_wait(&done[(steps - 1) % kTcStages], ((steps - 1) / kTcStages) & 1) && ok;
     tc_fence_after();
+    if (!kLong || left_steps <= kTcRun) break;
+    // read before the next step's barrier, behind which the next run begins
+#pragma unroll 1
+    for (int r = 0; r < kRanks; r += 16) {
+      float v[16];
+      tmem_ld16(own_sums + r, v);
+      tmem_wait(v, v);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) before[kLong ? r + e : 0] = left_steps < all_steps ? before[kLong ? r + e : 0] + v[e] : v[e];
+    }
+    tc_fence_before();
+    left_steps -= kTcRun;
+    steps = min(left_steps, kTcRun);
+    p_first += kTcRun * step;
   }
   __syncthreads();  // the ring becomes the sums
   float *sums = reinterpret_cast<float *>(ring);
   {
-    const int tile = warp >> 2, c = 128 * tile + 32 * (warp & 3) + lane;
-    const uint32_t from = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + tile * kRanks;
+    const int c = 32 * warp + lane;
 #pragma unroll
     for (int r = 0; r < kRanks; r += 32) {
       float v[2][16];
-      if (steps) {
-        tmem_ld16(from + r, v[0]);
-        tmem_ld16(from + r + 16, v[1]);
+      if (all_steps) {
+        tmem_ld16(own_sums + r, v[0]);
+        tmem_ld16(own_sums + r + 16, v[1]);
         tmem_wait(v[0], v[1]);
       }
 #pragma unroll
-      for (int e = 0; e < 32; ++e) v[e >> 4][e & 15] = !ok ? NAN : steps ? v[e >> 4][e & 15] : 0.f;
+      for (int e = 0; e < 32; ++e) v[e >> 4][e & 15] = !ok ? NAN : all_steps ? v[e >> 4][e & 15] : 0.f;
       if (a.turned) {
 #pragma unroll
         for (int e = 0; e < 32; e += 4)
@@ -959,6 +984,10 @@ __global__ void __launch_bounds__(kTcThreads, kWide ? 3 : 2) k_adapt_outer_tc(co
 #pragma unroll
         for (int e = 0; e < 32; ++e) sums[(r + e) * (kTcCols + 4) + c] = v[e >> 4][e & 15];
       }
+    }
+    if (kLong && all_steps > kTcRun) {  // a loop of its own: otherwise `before` is read in any case
+#pragma unroll 1
+      for (int r = 0; r < kRanks; ++r) sums[a.turned ? c * (kRanks + 4) + r : r * (kTcCols + 4) + c] += before[kLong ? r : 0];
     }
   }
   tc_fence_before();
@@ -980,15 +1009,16 @@ __global__ void __launch_bounds__(kTcThreads, kWide ? 3 : 2) k_adapt_outer_tc(co
 template <int kRanks, bool kWide>
 cudaError_t launch_outer_tc(OuterPair p, int64_t n, int32_t adapters, int sms, cudaStream_t s) {
   const size_t smem = tc_outer_smem(kRanks);
-  const auto kernel = k_adapt_outer_tc<kRanks, kWide>;
-  cudaError_t e = raise_smem_limit(kernel, smem);
-  if (e != cudaSuccess) return e;
   p.slices = p.a[0].out ? (int32_t)ceil_div(p.a[0].cols, kTcCols) : 0;
   const int64_t slices = p.slices + (p.a[1].out ? ceil_div(p.a[1].cols, kTcCols) : 0);
   const int64_t ranks = ceil_div(p.a[0].rank, kRanks);
   // three blocks of an SM at a time; two rounds of them even out adapters that have more rows than others (8192 rows, rank 64,
   // 4096 to 16384, four adapters: 161 us in 320 blocks, 104 in 640, 113 in 1280; 95 with v read two steps ahead)
   const unsigned c = cluster_for(slices * ranks * adapters, ceil_div(n, (int64_t)adapters * kTcRows), 5 * sms);
+  // all rows may be one adapter's
+  const auto kernel = ceil_div(n, (int64_t)c * kTcRows) > kTcRun ? k_adapt_outer_tc<kRanks, kWide, true> : k_adapt_outer_tc<kRanks, kWide, false>;
+  cudaError_t e = raise_smem_limit(kernel, smem);
+  if (e != cudaSuccess) return e;
   return launch_cluster(c, kernel, dim3((unsigned)(slices * c), (unsigned)adapters, (unsigned)ranks), kTcThreads, smem, s,
                         (const OuterPair)p);
 }

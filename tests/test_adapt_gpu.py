@@ -429,3 +429,58 @@ def test_one_row_in_place_by_another_tensor(dtype):
     without = torch.full_like(c.which, -1)  # no adapter: the base stays
     snack.adapt(c.x, out, c.a, c.b, without, c.scales, out=view)
     assert torch.equal(out, c.base) and bool((buf[:, 55:] == 7).all())
+
+
+def positive(rows, width, seed, dtype=torch.bfloat16):
+    """Values from 1/2 to 3/2, of one sign: truncated sums of them are all off to the same side."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    out = torch.empty(rows, width, device="cuda", dtype=dtype)
+    for part in out.split(max(1, (1 << 26) // width)):
+        part.copy_(torch.rand(part.shape, device="cuda", generator=g) + 0.5)
+    return out
+
+
+# additions of a run on the tensor core: its sum is added, rounded to nearest, to what came before
+RUN_OUTER = 528
+
+
+@pytest.mark.parametrize("rank", [32, 64])
+def test_matrices_gradients_over_millions_of_rows_are_sums_in_fp32(rank):
+    """dA and dB of one adapter over 2^21 rows of one sign, bf16.  Their mean relative error has none of the roundings to
+    bf16 in it: those of m entries, independent (every row and column has a scale of its own) and at most 2^-8 each, add up
+    to a mean above 2^-8 sqrt(2 ln(2e12) / m) once in 10^12 (Hoeffding).  What is left is off to one side: a run's additions,
+    2^-22 each at most, the second parts of h and dh (2^-17), and h and dh themselves (20 additions of 2^-22)."""
+    n, width, out = 1 << 21, 512, 256
+    g = torch.Generator(device="cuda").manual_seed(5)
+
+    def scales(k):
+        return 1 + torch.rand(k, device="cuda", generator=g)
+
+    x, dy = positive(n, width, 1).mul_(scales(width)), positive(n, out, 2).mul_(scales(out))
+    a, b = positive(rank, width, 3).mul_(scales(rank)[:, None]).view(1, rank, width), positive(out, rank, 4).mul_(scales(rank)).view(1, out, rank)
+    which = torch.zeros(n, device="cuda", dtype=torch.int64)
+    h = snack.adapt(x, dy, a, b, which, keep=True)[1]
+    _, da, db = snack.adapt_grad(x, dy, a, b, which, h, want_dx=False)
+    want_a, want_b = torch.zeros(rank, width, device="cuda", dtype=torch.float64), torch.zeros(out, rank, device="cuda", dtype=torch.float64)
+    for i in range(0, n, 1 << 17):
+        xs, gs = x[i:i + (1 << 17)].double(), dy[i:i + (1 << 17)].double()
+        want_a += (gs @ b[0].double()).T @ xs
+        want_b += gs.T @ (xs @ a[0].double().T)
+    for got, want in ((da[0], want_a), (db[0], want_b)):
+        chance = 2.0 ** -8 * (2 * 28.33 / want.numel()) ** 0.5
+        assert abs(float(((got - want) / want).mean())) <= chance + RUN_OUTER * 2.0 ** -22 + 2.0 ** -17 + 20 * 2.0 ** -22
+
+
+@pytest.mark.parametrize("n,adapters,rank,gap,kind", [(33792, 1, 64, 0, "one"), (33793, 1, 20, 0, "one"), (33856, 1, 64, 1, "one"), (70001, 2, 32, 3, "mixed"),
+                                                      (70001, 2, 65, 0, "runs"), (101377, 3, 8, 0, "one")])
+def test_matrices_gradients_around_the_ends_of_runs(n, adapters, rank, gap, kind):
+    """A cluster of eight blocks has 33792 rows in whole runs: one more run with no, one or a few rows, and several."""
+    c = Case(n, adapters, rank, 40, 24, "bf16", kind, gap, 0, seed=n)
+    val, mag = c.want()
+    rel = bounds(c)
+    h = snack.adapt(c.x, c.base, *c.args(), c.scales, keep=True)[1]
+    _, da, db = snack.adapt_grad(c.x, c.dy, *c.args(), h, c.scales, want_dx=False)
+    check(da, val[2], mag[2], rel[2], "da")
+    check(db, val[3], mag[3], rel[3], "db")
+    again = snack.adapt_grad(c.x, c.dy, *c.args(), h, c.scales, want_dx=False)
+    assert torch.equal(again[1], da) and torch.equal(again[2], db)
