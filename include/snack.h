@@ -531,7 +531,7 @@ snack_status snack_adapt_fwd(const void *x, int64_t x_ld, int64_t n, const void 
  *   dh[i] = scales[k] * B_k^T dy[i]
  *   dx[i] = A_k^T dh[i]                      (+ what is there, with accumulate != 0)
  *   da[k] = sum_i dh[i] x[i]^T,   db[k] = scales[k] * sum_i dy[i] h[i]^T
- * summed in fp32 over the adapter's rows (of bf16 operands within 3e-5 of the sum of
+ * summed in fp32 over the adapter's rows (of bf16 operands within 5e-5 of the sum of
  * magnitudes, however many they are) and rounded once to t.  dx is the
  * adapters' part alone: accumulate adds it to the projection's own input
  * gradient.  Rows without an adapter have dx = 0 (or stay, with accumulate) and

@@ -416,43 +416,35 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
 }
 
 // acc[i] += a[i] b[i] over 16 of K for kN independent sums: rows g (lo) and g + 8 (hi)
-// of a, in parts; the small products first, and those of fp32 operands summed apart
-// from what is there.  One part after the other for all sums: none waits for its own.
+// of a, in parts; the small products first, summed apart from what is there, which the
+// tensor core would cut off at the same side each time (nearly 2^20 terms of one sign
+// were off by 3e-4).  One part after the other for all sums: none waits for its own.
 template <int kN, int kA, int kB, typename FA, typename FB, typename FAcc>
 __device__ __forceinline__ void mma_all(FAcc acc, FA a, FB b) {
   typedef const uint32_t(&Rows)[2][2][kA];  // [row half][pair of K][part]
   typedef const uint32_t(&Cols)[2][kB];     // [pair of K][part]
-  if constexpr (kA == 3 && kB == 3) {
-    float d[kN][4];
+  static_assert(kB == 1 || kA == kB, "parts");
+  float d[kN][4];
 #pragma unroll
-    for (int n = 0; n < kN; ++n)
+  for (int n = 0; n < kN; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) d[n][e] = 0.f;
+    for (int e = 0; e < 4; ++e) d[n][e] = 0.f;
 #pragma unroll
-    for (int sum = 2; sum >= 0; --sum)
+  for (int sum = kA - 1; sum >= 0; --sum)
 #pragma unroll
-      for (int i = sum; i >= 0; --i)
-#pragma unroll
-        for (int n = 0; n < kN; ++n) {
-          Rows w = a(n);
-          Cols v = b(n);
-          mma(d[n], w[0][0][i], w[1][0][i], w[0][1][i], w[1][1][i], v[0][sum - i], v[1][sum - i]);
-        }
-#pragma unroll
-    for (int n = 0; n < kN; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc(n)[e] += d[n][e];
-  } else {
-    static_assert(kB == 1, "one part");
-#pragma unroll
-    for (int i = kA - 1; i >= 0; --i)
+    for (int i = sum; i >= 0; --i) {
+      if (sum - i >= kB) break;
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
         Rows w = a(n);
         Cols v = b(n);
-        mma(acc(n), w[0][0][i], w[1][0][i], w[0][1][i], w[1][1][i], v[0][0], v[1][0]);
+        mma(d[n], w[0][0][i], w[1][0][i], w[0][1][i], w[1][1][i], v[0][sum - i], v[1][sum - i]);
       }
-  }
+    }
+#pragma unroll
+  for (int n = 0; n < kN; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc(n)[e] += d[n][e];
 }
 
 // a lane's words of four consecutive elements of a row along K: [pair][part]

@@ -101,10 +101,18 @@ __host__ __device__ constexpr int tc_blocks(int rank) { return (rank + 63) / 64;
 __host__ __device__ constexpr uint32_t tc_tmem_cols(int cols) { return cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256; }
 
 constexpr int kTcDownStages = 4;
+// Steps summed on the tensor core, which cuts off what does not fit (of terms of one sign 9e-8 of the sum at each of a step's
+// four additions; nearly 2^20 of K were off by 7e-4), before their sum is added in fp32: 64 additions, 6e-6, less than
+// the 2^-17 that h and dh are held to in the products after.  Runs have the two halves of a block's tensor memory in turn; the
+// one before is read when its last step has been waited for anyway (8192 rows of 16384, rank 64, both calls of a pass: 331 us
+// without runs, 335 with these, 341 with runs of 8).
+constexpr int kTcDownRun = 16;
 __host__ __device__ constexpr int tc_down_stage(int rank) { return kTcRowBox + tc_blocks(rank) * kTcK * 128; }
 __host__ __device__ constexpr size_t tc_down_smem(int rank) {
   const size_t ring = (size_t)kTcDownStages * tc_down_stage(rank), sums = (size_t)kTcTile * (16 * tc_steps(rank) + 4) * 4;
-  return (ring > sums ? ring : sums) + 1024;
+  const size_t all = (ring > sums ? ring : sums) + 1024;
+  // all of the tensor memory above a rank of 128: no room beside it for another kernel that wants some
+  return rank > 128 && all < 200 * 1024 ? 200 * 1024 : all;
 }
 
 // How a matrix's or the rows' pieces of eight elements lie in memory
@@ -209,8 +217,8 @@ __device__ __forceinline__ void copy_pieces(int n, int on, F place) {
 }
 
 // A tile of 128 rows against an adapter's matrix, all of its ranks (N); the cluster's blocks have every so many 64 of K.
-// kWide: the rows lie on 16 bytes.
-template <bool kAlong, bool kWide>
+// kWide: the rows lie on 16 bytes.  kLong: a block may have more than a run of steps.
+template <bool kAlong, bool kWide, bool kLong>
 __global__ void __launch_bounds__(kTcThreads, 2) k_adapt_down_tc(const DownArgs args, const FileArgs f, int m_on) {
   pdl_wait();
   const uint32_t block = cluster_rank(), blocks = cluster_blocks();
@@ -230,7 +238,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_adapt_down_tc(const DownArgs 
   uint8_t *ring = tc_raw + ((1024 - (su32(tc_raw) & 1023)) & 1023);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = a.rank, n_pad = 16 * tc_steps(rank), stage_bytes = tc_down_stage(rank);
-  const uint32_t tmem_cols = tc_tmem_cols(n_pad);
+  const uint32_t half = tc_tmem_cols(n_pad), tmem_cols = kLong ? 2 * half : half;
   if (warp == 0) tmem_alloc(&tmem_at, tmem_cols);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kTcDownStages; ++s) mbar_init(&done[s], 1);
@@ -292,6 +300,25 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_adapt_down_tc(const DownArgs 
     }
     fetch_commit();
   };
+  // this warp's sums: rows 32 (warp % 4) + lane, 16 columns in 32
+  const uint32_t own_sums = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+  const int own_c = 16 * (warp >> 2);
+  float before[kLong ? kMostRank / 2 : 1];  // of the runs before the one before, in local memory
+  auto keep = [&](int run) {
+    tc_fence_after();
+#pragma unroll 1
+    for (int c = own_c; c < n_pad; c += 32) {
+      float v[16];
+      tmem_ld16(own_sums + (run & 1) * half + c, v);
+      tmem_wait(v, v);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float &to = before[kLong ? (c >> 5) * 16 + e : 0];
+        to = run ? to + v[e] : v[e];
+      }
+    }
+    tc_fence_before();
+  };
   // the rows past the tile's end stay as they are: a row's sums are its own
   if (steps) {
     const uint32_t inst = tc_inst(kTcTile, n_pad, false, !kAlong);
@@ -303,13 +330,16 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_adapt_down_tc(const DownArgs 
       if (threadIdx.x == 0) {
         tc_fence_after();
         const uint32_t at = su32(ring) + (i % kTcDownStages) * stage_bytes, b = at + kTcRowBox;
+        const uint32_t d = kLong ? tmem + (i / kTcDownRun & 1) * half : tmem;
 #pragma unroll
         for (int s = 0; s < kTcK / 16; ++s)
-          tc_mma(tmem, tc_desc(at + s * 32, 16), kAlong ? tc_desc(b + s * 32, 16) : tc_desc(b + s * 2048, kTcK * 128), inst, i > 0 || s > 0);
+          tc_mma(d, tc_desc(at + s * 32, 16), kAlong ? tc_desc(b + s * 32, 16) : tc_desc(b + s * 2048, kTcK * 128), inst,
+                 (kLong ? i % kTcDownRun : i) > 0 || s > 0);
         tc_commit(&done[i % kTcDownStages]);
       }
       if (i > 0) ok = mbar_wait(&done[(i - 1) % kTcDownStages], ((i - 1) / kTcDownStages) & 1) && ok;
       fetch(i + kTcDownStages - 1);
+      if (kLong && i > 0 && i % kTcDownRun == 0) keep(i / kTcDownRun - 1);
     }
     fetch_wait<0>();
     ok = mbar_wait(&done[(steps - 1) % kTcDownStages], ((steps - 1) / kTcDownStages) & 1) && ok;
@@ -318,13 +348,16 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_adapt_down_tc(const DownArgs 
   __syncthreads();  // the ring becomes the sums
   float *sums = reinterpret_cast<float *>(ring);
   const int pitch = n_pad + 4;
-  for (int c = 16 * (warp >> 2); c < n_pad; c += 32) {
+  for (int c = own_c; c < n_pad; c += 32) {
     float v[16];
     if (steps) {
-      tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + c, v);
+      tmem_ld16(own_sums + (kLong ? ((steps - 1) / kTcDownRun & 1) * half : 0) + c, v);
       tmem_wait(v, v);
     }
     float *to = sums + (32 * (warp & 3) + lane) * pitch + c;
+    if (kLong && steps > kTcDownRun)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] += before[kLong ? (c >> 5) * 16 + e : 0];
 #pragma unroll
     for (int e = 0; e < 16; ++e) v[e] = !ok ? NAN : steps ? v[e] : 0.f;
 #pragma unroll
@@ -368,10 +401,10 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_adapt_down_tc(const DownArgs 
 template <bool kAlong, bool kWide>
 cudaError_t launch_down_tc(const DownArgs &a, const FileArgs &f, int64_t tiles, int tile_cap, int sms, cudaStream_t s) {
   const size_t smem = tc_down_smem(a.rank);
-  const auto kernel = k_adapt_down_tc<kAlong, kWide>;
+  const unsigned c = cluster_for(tiles, ceil_div(a.k, 2 * kTcK), 2 * sms);
+  const auto kernel = ceil_div(a.k, (int64_t)c * kTcK) > kTcDownRun ? k_adapt_down_tc<kAlong, kWide, true> : k_adapt_down_tc<kAlong, kWide, false>;
   cudaError_t e = raise_smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
-  const unsigned c = cluster_for(tiles, ceil_div(a.k, 2 * kTcK), 2 * sms);
   return launch_cluster(c, kernel, dim3((unsigned)tile_cap * c), kTcThreads, smem, s, a, f, lies_on(a.m, kAlong ? a.k : a.rank));
 }
 template <bool kAlong>

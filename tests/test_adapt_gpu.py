@@ -484,3 +484,42 @@ def test_matrices_gradients_around_the_ends_of_runs(n, adapters, rank, gap, kind
     check(db, val[3], mag[3], rel[3], "db")
     again = snack.adapt_grad(c.x, c.dy, *c.args(), h, c.scales, want_dx=False)
     assert torch.equal(again[1], da) and torch.equal(again[2], db)
+
+
+@pytest.mark.parametrize("n,adapters,rank,run,chain", [(300, 1, 16, 64, 1 << 13), (300, 2, 160, 64, 1 << 13), (100, 64, 2, 1, 1 << 12), (3, 1, 16, 1, 1 << 10)])
+def test_h_of_the_widest_rows_is_a_sum_in_fp32(n, adapters, rank, run, chain):
+    """Nearly 2^20 terms of one sign per entry, bf16, 16 of them at a time: `chain` such additions one after the other by a
+    cluster's block (of eight, by 128 rows) or a warp (eight in each of two or eight blocks, by few rows).  Of each `run` of
+    them the tensor core cuts off at most 2^-22 per addition; the runs, and the sums of warps and blocks (16), are added in
+    fp32, 2^-24 each."""
+    width = (1 << 20) - 8
+    x, a = positive(n, width, 1), positive(adapters * rank, width, 2).view(adapters, rank, width)
+    b = torch.zeros(adapters, 1, rank, device="cuda", dtype=torch.bfloat16)
+    which = torch.arange(n, device="cuda") % adapters
+    h = snack.adapt(x, None, a, b, which, keep=True)[1]
+    want = torch.zeros(n, rank, device="cuda", dtype=torch.float64)
+    for c in range(0, width, 1 << 16):
+        for k in range(adapters):
+            want[which == k] += x[which == k, c:c + (1 << 16)].double() @ a[k, :, c:c + (1 << 16)].double().T
+    assert float(((h - want) / want).abs().max()) <= run * 2.0 ** -22 + (chain / run + 17) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("n,adapters,rank,width", [(*c, w) for c in ((257, 1, 20), (600, 40, 64), (300, 2, 130), (300, 1, 256))
+                                                   for w in (8128, 8192, 8256, 16400, 33001)] + [(20000, 2, 16, 2112), (9000, 3, 100, 4097)])
+def test_h_around_the_ends_of_runs(n, adapters, rank, width):
+    """Clusters of eight, one and two blocks with steps of 64 in runs of sixteen: the last run full, with one step, alone."""
+    c = Case(n, adapters, rank, width, 24, "bf16", "mixed", seed=n)
+    val, mag = c.want()
+    rel = bounds(c)
+    y, h = snack.adapt(c.x, c.base, *c.args(), c.scales, keep=True)
+    check(y, val[0], mag[0], rel[0], "y")
+    own = (c.which >= 0) & (c.which < adapters)
+    x, a = c.x[own].double(), c.a.double()[c.which[own].long()]
+    tol = sums(width, torch.bfloat16) * torch.einsum("ni,nri->nr", x.abs(), a.abs()) if n * rank * width < 1 << 28 else None
+    if tol is not None:
+        assert bool(((h[own] - torch.einsum("ni,nri->nr", x, a)).abs() <= tol).all())
+    c = Case(n, adapters, rank, 24, width, "bf16", "mixed", seed=n)  # dh
+    val, mag = c.want()
+    dx, da, _ = snack.adapt_grad(c.x, c.dy, *c.args(), None, c.scales, want_db=False)
+    check(dx, val[1], mag[1], bounds(c)[1], "dx")
+    check(da, val[2], mag[2], bounds(c)[2], "da")
