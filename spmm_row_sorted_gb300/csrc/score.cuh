@@ -16,10 +16,12 @@
 // with the largest maxima (of equal ones the first): each of those has a logit that
 // comes before any of another group.  So the product writes the maxima, and the logits
 // themselves for a piece of the vocabulary; a block per row then reads V / 32 maxima and
-// `keep` lines of logits, whatever the data.  Eight more than asked for are kept: where
-// neighbours in the order are within 2^-12 of the largest magnitude, some hundred times
-// what the logits are off by, they are ranked by their products summed again in twice
-// fp32's precision.  Equal logits rank by their ids.  Included by xent.cu.
+// `keep` lines of logits, whatever the data.  Eight more than asked for are kept, and
+// neighbours in the order that are too close are ranked by their products summed again
+// in twice fp32's precision.  What a logit is off by goes with the size of its terms, not
+// with its own, where terms cancel: too close are two that are within 2^-15 of the largest
+// sum |x w| of those kept (each is within 10^-5 of its own), or, where the rows are few or
+// fp32, any two.  Equal logits rank by their ids.  Included by xent.cu.
 #pragma once
 
 namespace snack {
@@ -27,10 +29,10 @@ namespace {
 
 constexpr int kMostTop = 24;
 constexpr int kKeepMore = 8;
-// of a block: four warps, or where the rows are few four for the likeliest tokens, four for the statistics beside them and
-// one for the target's logit (8 rows of 32768, 20 tokens: the call 39 and 35 us; 2048 rows of 65536, 8: 62 and 74 us)
+// of a block: four warps, or where the rows are few four for the likeliest tokens, four for the statistics beside them, one
+// for the target's logit and as many for what is summed again
 constexpr int kTopWarps = 4, kTopThreads = kTopWarps * 32;
-constexpr int kFinishThreads = (2 * kTopWarps + 1) * 32;
+constexpr int kFinishThreads = 1024;
 constexpr int kFoundFew = 256;  // keys that are ranked by counting
 constexpr int kNoId = 0x7FFFFFFF;
 constexpr int kFound = (kMostTop + kKeepMore) * 32;  // all logits of the groups that are looked at
@@ -180,11 +182,13 @@ __device__ __noinline__ void choose(const Key *keys, int n, Key *chosen, int kee
   }
 }
 
-// hi + lo += a * b, to about twice fp32's precision
+// hi + lo += a * b, to about twice fp32's precision; kExact: the product fits fp32, as that of two bf16 does
+template <bool kExact>
 __device__ __forceinline__ void add_product(float &hi, float &lo, float a, float b) {
-  const float p = __fmul_rn(a, b), e = __fmaf_rn(a, b, -p);
+  const float p = __fmul_rn(a, b);
   const float s = __fadd_rn(hi, p), t = __fsub_rn(s, hi);
-  lo = __fadd_rn(lo, __fadd_rn(e, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(p, t))));
+  const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(p, t));
+  lo = __fadd_rn(lo, kExact ? e : __fadd_rn(__fmaf_rn(a, b, -p), e));
   hi = s;
 }
 // a number in the order of hi + lo, an integer (double's own comparisons and sums are slow here)
@@ -192,7 +196,7 @@ __device__ __forceinline__ long long order_of(float hi, float lo) {
   const long long bits = __double_as_longlong((double)(hi + 0.f) + (double)lo);  // -0 as 0
   return bits < 0 ? bits ^ 0x7FFFFFFFFFFFFFFFLL : bits;
 }
-// hi + lo = a + b, exactly
+// hi + lo += b, to about twice fp32's precision
 __device__ __forceinline__ void add_two(float &hi, float &lo, float b_hi, float b_lo) {
   const float s = __fadd_rn(hi, b_hi), t = __fsub_rn(s, hi);
   const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(b_hi, t));
@@ -210,7 +214,7 @@ __device__ __noinline__ float2 long_logit(const TargetLogit &at, int64_t row, in
   for (int g = lane; g < groups; g += 32) {
     const Pack<T, 16> p = TargetLogit::some(a, g, at.width, at.x_wide), q = TargetLogit::some(b, g, at.width, at.w_wide);
 #pragma unroll
-    for (int e = 0; e < kN; ++e) add_product(hi, lo, p.get(e), q.get(e));
+    for (int e = 0; e < kN; ++e) add_product<sizeof(T) == 2>(hi, lo, p.get(e), q.get(e));
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) {
@@ -220,8 +224,35 @@ __device__ __noinline__ float2 long_logit(const TargetLogit &at, int64_t row, in
   return make_float2(hi, lo);
 }
 
-// A block per row.
-__global__ void __launch_bounds__(kFinishThreads) k_score_finish(const FinishArgs a) {
+// Of a row and kept tokens i0 .. i0 + 15 of bf16: a warp's share of their sums of |x w|, in .x of token i0 + lane / 4 and in .y
+// of the eighth after it.  Tokens are the rows of mma.sync; which columns of 32 a lane holds does not matter to a sum.
+__device__ __noinline__ float2 term_sizes(const TargetLogit &at, int64_t row, const Key *chosen, int keep, int i0, int warp, int lane) {
+  constexpr uint32_t kNoSigns = 0x7FFF7FFFu;
+  const int q = lane & 3, groups = (at.width + 7) / 8;
+  const bf16 *x = reinterpret_cast<const bf16 *>(at.x) + row * at.x_ld, *w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = i0 + 8 * h + (lane >> 2);
+    const Key k = i < keep && chosen[i] ? chosen[i] : chosen[0];
+    w[h] = reinterpret_cast<const bf16 *>(at.w) + (int64_t)key_id(k) * at.w_ld;
+  }
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int g0 = 4 * warp; g0 < groups; g0 += 4 * kTopWarps) {
+    const Pack<bf16, 16> b = TargetLogit::some(x, g0 + q, at.width, at.x_wide), lo = TargetLogit::some(w[0], g0 + q, at.width, at.w_wide),
+                         hi = TargetLogit::some(w[1], g0 + q, at.width, at.w_wide);
+#pragma unroll
+    for (int s = 0; s < 4; s += 2) {
+      const uint32_t a[4] = {lo.w[s] & kNoSigns, hi.w[s] & kNoSigns, lo.w[s + 1] & kNoSigns, hi.w[s + 1] & kNoSigns};
+      mma16816(acc, a, b.w[s] & kNoSigns, b.w[s + 1] & kNoSigns);
+    }
+  }
+  return make_float2(acc[0], acc[2]);
+}
+
+// A block per row.  kFew: few rows, a large block each.
+template <bool kFew>
+__global__ void __launch_bounds__(kFew ? kFinishThreads : kTopThreads) k_score_finish(const FinishArgs a) {
   pdl_wait();
   __shared__ Key chosen[32];
   __shared__ __align__(16) uint32_t bests[kTopThreads];
@@ -229,12 +260,12 @@ __global__ void __launch_bounds__(kFinishThreads) k_score_finish(const FinishArg
   __shared__ __align__(16) Key found[kFound + 32];
   __shared__ float4 sums[kTopWarps];
   __shared__ float2 exact[32];
-  __shared__ unsigned again;
+  __shared__ float sizes[kTopWarps][32];
   __shared__ float target_z;
   __shared__ int n_found;
   const int64_t row = blockIdx.x;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const bool wide = warps > kTopWarps;
+  constexpr int warps = (kFew ? kFinishThreads : kTopThreads) / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool bad = a.last && any_error(a.err);
   const uint32_t target = a.targets.ids ? a.targets.key(row) : a.targets.vocab;
   const bool given = target < a.targets.vocab;
@@ -335,22 +366,10 @@ __global__ void __launch_bounds__(kFinishThreads) k_score_finish(const FinishArg
     if (warp == 0) {
       list = chosen[lane];
       if (!a.last) a.list[row * 32 + lane] = list;
-      // which of them are too close to tell
-      const float mine = list ? key_value(list) : -INFINITY, above = __shfl_up_sync(0xffffffffu, mine, 1);
-      float size = lane < a.keep && isfinite(mine) ? fabsf(mine) : 0.f;
-#pragma unroll
-      for (int d = 16; d; d >>= 1) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, d));
-      const bool close = lane > 0 && lane < a.keep && list && above - mine <= size * 0x1p-12f;  // not of two infinities
-      const unsigned with = __ballot_sync(0xffffffffu, close);  // bit l: l goes with l - 1
-      // a run of them that begins before place `top`
-      const int begin = 31 - __clz(~with & (0xffffffffu >> (31 - lane)));
-      const bool run = close || (lane < 31 && (with >> (lane + 1)) & 1);
-      const unsigned m = __ballot_sync(0xffffffffu, run && begin < a.top);
-      if (lane == 0) again = m;
     }
   }
   if (!a.last) return;
-  if (const int mine = warp - (wide ? kTopWarps : 0); mine >= 0 && mine < kTopWarps) {  // the row's statistics
+  if (const int mine = warp - (kFew ? kTopWarps : 0); mine >= 0 && mine < kTopWarps) {  // the row's statistics
     float4 s = make_float4(-INFINITY, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int i = 32 * mine + lane; i < a.slots; i += kTopThreads) s = join_stats(s, a.stats[row * a.stats_ld + i]);
@@ -370,7 +389,33 @@ __global__ void __launch_bounds__(kFinishThreads) k_score_finish(const FinishArg
     if (lane == 0) target_z = z;
   }
   __syncthreads();
+  unsigned again = 0;  // what is summed again
   if (a.top) {
+    float slack = INFINITY;
+    if (!kFew && a.at.bf) {
+      for (int i0 = 0; i0 < a.keep; i0 += 16) {
+        const float2 size = term_sizes(a.at, row, chosen, a.keep, i0, warp, lane);
+        if ((lane & 3) == 0) {
+          sizes[warp][i0 + (lane >> 2)] = size.x;
+          sizes[warp][i0 + 8 + (lane >> 2)] = size.y;
+        }
+      }
+      __syncthreads();
+      float size = 0.f;
+#pragma unroll
+      for (int w = 0; w < kTopWarps; ++w) size += lane < a.keep ? sizes[w][lane] : 0.f;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, d));
+      slack = size * 0x1p-15f;
+    }
+    const Key own = chosen[lane];
+    const float mine = own ? key_value(own) : -INFINITY, above = __shfl_up_sync(0xffffffffu, mine, 1);
+    const bool close = lane > 0 && own && !(above - mine > slack);
+    const unsigned with = __ballot_sync(0xffffffffu, close);  // bit l: l goes with l - 1
+    // a run of them that begins before place `top`
+    const int begin = 31 - __clz(~with & (0xffffffffu >> (31 - lane)));
+    const bool run = close || (lane < 31 && (with >> (lane + 1)) & 1);
+    again = __ballot_sync(0xffffffffu, run && begin < a.top);
     int k = 0;
     for (unsigned m = again; m; m &= m - 1, ++k) {
       if (k % warps != warp) continue;
@@ -416,10 +461,14 @@ __global__ void __launch_bounds__(kFinishThreads) k_score_finish(const FinishArg
     const int ij = __shfl_sync(0xffffffffu, id, j);
     place += other > mine || (other == mine && ij < id) ? 1 : 0;
   }
+  // the first one's log probability by the statistics' own logits, whose errors it shares; the others' by what is between them
+  const int best = __ffs(__ballot_sync(0xffffffffu, lane < a.keep && place == 0)) - 1;
+  const bool of_target = given && id == (int)target;
+  const float first = __shfl_sync(0xffffffffu, of_target ? logp : (key_value(list) - high) - log_sum, best);
+  const float2 top_l = make_float2(__shfl_sync(0xffffffffu, l.x, best), __shfl_sync(0xffffffffu, l.y, best));
   if (lane < a.keep && place < a.top) {
-    const float own = given && id == (int)target ? logp : (l.x - high) - log_sum;
     a.top_ids[row * a.top + place] = id;
-    a.top_logp[row * a.top + place] = own;
+    a.top_logp[row * a.top + place] = of_target ? logp : place ? ((l.x - top_l.x) + (l.y - top_l.y)) + first : first;
   }
 }
 
@@ -596,7 +645,10 @@ snack_status snack_score_fwd(const void *x, int64_t x_ld, int32_t n, const void 
   f.top_ids = top_ids;
   f.lse = state;
   f.kept_entropy = state + n;
-  auto finish = [&] { return launch_pdl(k_score_finish, (unsigned)n, n <= S.sms ? kFinishThreads : kTopThreads, 0, s, (const FinishArgs)f); };
+  auto finish = [&] {
+    return n <= S.sms ? launch_pdl(k_score_finish<true>, (unsigned)n, kFinishThreads, 0, s, (const FinishArgs)f)
+                      : launch_pdl(k_score_finish<false>, (unsigned)n, kTopThreads, 0, s, (const FinishArgs)f);
+  };
   if (W.tokens) {
     f.groups = f.slots = (int32_t)W.slots;
     f.rows = (int32_t)vocab;

@@ -366,3 +366,36 @@ def test_score_without_rows_and_refusals():
         with pytest.raises(snack.SnackError) as e:
             snack.score(x, w, t, top)
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [2, 40, 200])
+def test_order_of_logits_that_are_small_against_their_terms(n, dtype):
+    """Terms whose sums reach 2^13 or so cancel: a rounding of such a sum to fp32 (2^-11) is larger than the steps between the
+    fourteen largest logits (2^-12, near 2^-3), which differ by far more than roundings of numbers of their own size would.
+    The products are multiples of 2^-14 and 64-bit sums of them exact."""
+    vocab, width = 5000, 512
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    half = width // 2 - 2
+    x, w = torch.zeros(n, width, device="cuda"), torch.zeros(vocab, width, device="cuda")
+
+    def eight_bits(*shape):  # from 1 to 16
+        return torch.randint(128, 256, shape, generator=gen, device="cuda") / 2.0 ** torch.randint(4, 8, shape, generator=gen, device="cuda")
+
+    big, terms = eight_bits(half), eight_bits(vocab, half)
+    turn = torch.randperm(half, generator=gen, device="cuda")
+    sign = 1 - 2 * torch.randint(0, 2, (n, 1), generator=gen, device="cuda")
+    x[:, :half], x[:, half:2 * half] = sign * big, sign * big[turn]
+    w[:, :half], w[:, half:2 * half] = terms, -terms[:, turn]
+    x[:, -1] = 2.0 ** -6
+    x[:, -2] = 2.0 ** -3
+    near = torch.randperm(vocab, generator=gen, device="cuda")[:14]
+    w[:, -2] = -8.0  # the others: -1
+    w[near, -2] = 1.0
+    w[near, -1] = torch.randperm(14, generator=gen, device="cuda").float() * 2.0 ** -6
+    x, w = x.to(DTYPES[dtype]), w.to(DTYPES[dtype])
+    want = Want(x, w, None, 6)
+    assert torch.equal(want.ids[0], near[w[near, -1].float().argsort(descending=True)][:6])
+    got = snack.score(x, w, top=6)
+    assert torch.equal(got[2], want.ids)
+    assert bool((got[3][:, 1:] <= got[3][:, :-1]).all())
