@@ -13,10 +13,10 @@ __device__ __forceinline__ uint32_t su32(const void *p) { return static_cast<uin
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(bar)), "r"(count) : "memory");
 }
-constexpr int kSpinLimit = 1 << 20;  // far above any real wait
-__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
+constexpr int kSpinLimit = 1 << 20;  // about four seconds, far above any real wait
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, int limit = kSpinLimit) {
   const uint32_t at = su32(bar);
-  for (int i = 0; i < kSpinLimit; ++i) {
+  for (int i = 0; i < limit; ++i) {
     uint32_t done;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_adapt_down_tc(const DownArgs 
     ok = mbar_wait(&done[(steps - 1) % kTcDownStages], ((steps - 1) / kTcDownStages) & 1) && ok;
     tc_fence_after();
   }
-  __syncthreads();  // the ring becomes the sums
+  ok = __syncthreads_and(ok);  // the ring becomes the sums; of a wait that gave up all of the block's are NaN
   float *sums = reinterpret_cast<float *>(ring);
   const int pitch = n_pad + 4;
   for (int c = own_c; c < n_pad; c += 32) {
@@ -429,8 +429,22 @@ static_assert(tc_up_smem(kMostRank) <= 232448 - 1024 && tc_up_smem(192) <= 23244
                   tc_down_smem(kMostRank) <= 232448 - 1024,
               "shared memory of one block");
 
-// the warps that lay out h and the one that issues products
-__device__ __forceinline__ void tc_rows_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kTcUpEpi + 32) : "memory"); }
+// how often the warp that fetches, and those that issue and write, look for what they wait for: a test builds with fewer
+#ifndef SNACK_UP_FETCH_WAITS
+#define SNACK_UP_FETCH_WAITS kSpinLimit
+#define SNACK_UP_WAITS kSpinLimit
+#endif
+constexpr int kFetchWaits = SNACK_UP_FETCH_WAITS, kUpWaits = SNACK_UP_WAITS;
+
+// the warps that lay out h and the one that issues products: whether all are well
+__device__ __forceinline__ bool tc_rows_sync(bool ok) {
+  uint32_t all;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.and.pred p, 1, %2, q;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(all)
+               : "r"(ok ? 1u : 0u), "n"(kTcUpEpi + 32)
+               : "memory");
+  return all != 0;
+}
 
 // 32 columns of 16 lanes of TMEM as a product's fragments: v[4 j + 2 h + e] is row 8 h + lane / 4, column 8 j + 2 (lane % 4) + e
 __device__ __forceinline__ void tmem_ld_rows(uint32_t at, float (&v)[16]) {
@@ -481,6 +495,7 @@ __device__ __noinline__ void write_some(uint16_t *p, uint4 v, int left) {
 // rows.  One warp fetches the matrix, one issues the products into two sets of sums in turn, eight add the base, which
 // they have read ahead, and write the result: 32 rows and 64 columns each, 64 bytes of a row from four lanes together.
 // For that the matrix's rows lie in the order of a fragment's columns (kAlong), or pairs change lanes.
+// A warp whose wait gives up hands on nothing more, so that the others' waits give up as well: a result is right or NaN.
 // (Base and result through shared memory, 64 columns at a time: 143 us for y of 8192 x 16384 of rank 64, 41 % of shared
 // memory's cycles; eight warps doing everything in turn 190, of a step's 3700 cycles 1200 waiting for the products.)
 // kWide: the base's and the result's rows lie on 16 bytes.
@@ -516,7 +531,7 @@ __global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a,
   const uint32_t tmem = tmem_at;
   bool ok = true;
   int s = 0, turn = 0;       // the stage in hand and how often the ring has been round, modulo 2
-  uint32_t g = 0;            // units with products so far
+  uint32_t g = 0;            // units with products so far; of the warp that issues them those issued
   while (u0 < units) {
     const int at = (int)(u0 / across), first = (int)(u0 - (int64_t)at * across);
     const int items = (int)min((int64_t)(across - first), u_end - u0), col0 = first * kTcUpCols;
@@ -565,7 +580,7 @@ __global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a,
         const float scale = a.scales ? a.scales[tile.adapter] : 1.f;
         const int t = threadIdx.x >> 1;
         const float *from = a.h + (int64_t)__ldg(a.order + tile.first + (t < tile.count ? t : 0)) * rank;
-        for (int e0 = threadIdx.x & 1; e0 < 2 * steps; e0 += 4) {
+        for (int e0 = threadIdx.x & 1; ok && e0 < 2 * steps; e0 += 4) {
           Pack<float, 16> v[2][2];
 #pragma unroll
           for (int u = 0; u < 2; ++u)
@@ -588,11 +603,11 @@ __global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a,
           }
         }
         fence_async_shared();
-        tc_rows_sync();
+        ok = tc_rows_sync(ok);
       }
       for (int i = 0; i < items; ++i) {
         if (!none) {
-          ok = ok && mbar_wait(&done[g & 1], (g >> 1) & 1);
+          ok = ok && mbar_wait(&done[g & 1], (g >> 1) & 1, kUpWaits);
           tc_fence_after();
         }
 #pragma unroll
@@ -612,13 +627,15 @@ __global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a,
             if (sub == 1) {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&taken[g & 1]);
+              if (lane == 0 && ok) mbar_arrive(&taken[g & 1]);
             }
             if constexpr (!kAlong) {
               turn_pairs(v[0], lane);
               turn_pairs(v[1], lane);
             }
-            if (!ok) v[0][0] = v[0][2] = v[1][0] = v[1][2] = NAN;  // a wait gave up: no row without a NaN
+            if (!ok)  // a wait gave up
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[0][e] = v[1][e] = NAN;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const float *x = &v[r >> 1][2 * (r & 1)];
@@ -650,7 +667,10 @@ __global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a,
     } else if (warp == kTcUpEpi / 32) {
       const bf16 *mat = reinterpret_cast<const bf16 *>(a.m) + (int64_t)tile.adapter * rank * a.cols;
       for (int i = 0; i < items; ++i, ++g) {
-        if (g >= (uint32_t)stages) ok = ok && mbar_wait(&empty[s], turn ^ 1);
+        if (g >= (uint32_t)stages) {
+          ok = __all_sync(0xffffffffu, ok && mbar_wait(&empty[s], turn ^ 1, kFetchWaits));
+          if (!ok) continue;
+        }
         uint8_t *to = ring + s * stage_bytes;
         const int col = col0 + i * kTcUpCols, left = a.cols - col;
         if constexpr (kAlong) {  // eight lanes have 128 bytes of a row, four rows at a time
@@ -712,10 +732,12 @@ __global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a,
         }
       }
     } else {
-      tc_rows_sync();
+      ok = tc_rows_sync(ok);
       constexpr uint32_t kInst = tc_inst(kTcTile, kTcUpCols, false, !kAlong);
-      for (int i = 0; i < items; ++i, ++g) {
-        ok = ok && mbar_wait(&full[s], turn) && (g < 2 || mbar_wait(&taken[g & 1], ((g >> 1) & 1) ^ 1));
+      for (int i = 0; i < items; ++i) {
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(&full[s], turn, kUpWaits) &&
+                                         (g < 2 || mbar_wait(&taken[g & 1], ((g >> 1) & 1) ^ 1, kUpWaits)));
+        if (!ok) break;
         tc_fence_after();
         if (lane == 0) {
           const uint32_t h_at = su32(hs), b = su32(ring) + s * stage_bytes, d = tmem + (g & 1) * kTcUpCols;
@@ -728,6 +750,7 @@ __global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a,
           tc_commit(&done[g & 1]);
         }
         __syncwarp();
+        ++g;
         if (++s == stages) {
           s = 0;
           turn ^= 1;
@@ -738,8 +761,10 @@ __global__ void __launch_bounds__(kTcUpThreads, 2) k_adapt_up_tc(const UpArgs a,
   if (warp == kTcUpEpi / 32 && g > 0 && stages > 1) {
     fetch_wait<0>();
     fence_async_shared();
-    mbar_arrive(&full[s == 0 ? stages - 1 : s - 1]);
+    if (ok) mbar_arrive(&full[s == 0 ? stages - 1 : s - 1]);
   }
+  // no product is under way any more, also where the warps that write have given up
+  if (warp == kTcUpThreads / 32 - 1 && g > 0) mbar_wait(&done[(g - 1) & 1], ((g - 1) >> 1) & 1, kUpWaits);
   tc_fence_before();
   __syncthreads();
   if (warp == kTcUpThreads / 32 - 1) {
@@ -979,22 +1004,26 @@ __global__ void __launch_bounds__(kTcThreads, kWide ? 3 : 2) k_adapt_outer_tc(co
     fetch_wait<0>();
     ok = mbar_wait(&done[(steps - 1) % kTcStages], ((steps - 1) / kTcStages) & 1) && ok;
     tc_fence_after();
-    if (!kLong || left_steps <= kTcRun) break;
-    // read before the next step's barrier, behind which the next run begins
+    if constexpr (!kLong) {
+      break;
+    } else {
+      if (left_steps <= kTcRun) break;
+      // read before the next step's barrier, behind which the next run begins
 #pragma unroll 1
-    for (int r = 0; r < kRanks; r += 16) {
-      float v[16];
-      tmem_ld16(own_sums + r, v);
-      tmem_wait(v, v);
+      for (int r = 0; r < kRanks; r += 16) {
+        float v[16];
+        tmem_ld16(own_sums + r, v);
+        tmem_wait(v, v);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) before[kLong ? r + e : 0] = left_steps < all_steps ? before[kLong ? r + e : 0] + v[e] : v[e];
+        for (int e = 0; e < 16; ++e) before[r + e] = left_steps < all_steps ? before[r + e] + v[e] : v[e];
+      }
+      tc_fence_before();
+      left_steps -= kTcRun;
+      steps = min(left_steps, kTcRun);
+      p_first += kTcRun * step;
     }
-    tc_fence_before();
-    left_steps -= kTcRun;
-    steps = min(left_steps, kTcRun);
-    p_first += kTcRun * step;
   }
-  __syncthreads();  // the ring becomes the sums
+  ok = __syncthreads_and(ok);  // the ring becomes the sums; of a wait that gave up all of the block's are NaN
   float *sums = reinterpret_cast<float *>(ring);
   {
     const int c = 32 * warp + lane;
