@@ -1103,5 +1103,7 @@ class _AdaptFn(torch.autograd.Function):
 
 def adapted(x: torch.Tensor, base: torch.Tensor, a: torch.Tensor, b: torch.Tensor, which: torch.Tensor,
             scales: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """Autograd-aware adapt; gradients flow to x, base, a and b (not to scales)."""
+    """Autograd-aware adapt; gradients flow to x, base, a and b.  scales that want one are refused: they get none."""
+    if scales is not None and scales.requires_grad and torch.is_grad_enabled():
+        raise ValueError("adapted gives scales no gradient: detach them")
     return _AdaptFn.apply(x, base, a, b, which, scales)

@@ -95,3 +95,17 @@ def test_adapt_python_refusals():
         snack.adapt(x, base, a, b, which)
     with pytest.raises(ValueError, match="CUDA"):
         snack.adapt_grad(x, base, a, b, which, torch.zeros(4, 3))
+
+
+def test_adapted_refuses_scales_that_want_a_gradient():
+    """Before it looks at anything else, so that this runs without a GPU."""
+    x, base = torch.zeros(4, 8), torch.zeros(4, 6)
+    a, b, which = torch.zeros(2, 3, 8), torch.zeros(2, 6, 3), torch.zeros(4, dtype=torch.int64)
+    scales = torch.ones(2, requires_grad=True)
+    with pytest.raises(ValueError, match="scales"):
+        snack.adapted(x, base, a, b, which, scales)
+    for held in (scales.detach(), None):
+        with pytest.raises(ValueError, match="CUDA"):
+            snack.adapted(x, base, a, b, which, held)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+        snack.adapted(x, base, a, b, which, scales)
