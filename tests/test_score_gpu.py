@@ -399,3 +399,48 @@ def test_order_of_logits_that_are_small_against_their_terms(n, dtype):
     got = snack.score(x, w, top=6)
     assert torch.equal(got[2], want.ids)
     assert bool((got[3][:, 1:] <= got[3][:, :-1]).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,vocab", [(1, 9000), (5, 40000), (40, 9000), (70, 40000), (200, 9000), (200, 40000)])
+def test_equal_logits_of_many_groups_rank_by_id(n, vocab, dtype):
+    """More groups of 32 equal logits than are ranked by counting (256), and than there is room for (1024)."""
+    x, w, _ = make(n, vocab, 64, dtype, seed=1)
+    x[0] = 0  # every logit 0
+    got = snack.score(x, w, top=24)
+    assert torch.equal(got[2][0], torch.arange(24, device="cuda"))
+    assert bool(((got[3][0] + torch.log(torch.tensor(float(vocab)))).abs() <= 2.0 ** -15).all())
+    Want(x, w, None, 24).check(got)
+    w[:] = w[5]  # all of them, in every row
+    w[vocab - 3:] *= 2  # and three beside, the largest or the lowest
+    Want(x, w, None, 10).check(snack.score(x, w, top=10))
+
+
+def test_equal_logits_in_pieces_of_the_vocabulary_rank_by_id():
+    n, vocab = 8200, 50000  # 1.6 GB of logits
+    x, w, _ = make(n, vocab, 64, "bf16", seed=2)
+    x[::7] = 0
+    w[:] = w[torch.arange(vocab, device="cuda") % 20000]
+    ids = snack.score(x, w, top=24)[2]
+    assert torch.equal(ids[::7], torch.arange(24, device="cuda").expand(len(ids[::7]), 24))
+    for rows in (slice(0, 600), slice(n - 600, n)):
+        assert torch.equal(ids[rows], Want(x[rows], w, None, 24).ids)
+
+
+def test_gradients_where_logits_are_the_lowest():
+    """Tokens with -inf logits get no probability: their rows of dw are 0, the others' as if they were not there.  dx is dz w, a
+    product with their rows in it: 0 times -inf, NaN, in the column that has them, and the others' sum elsewhere."""
+    x, w, t = make(70, 300, 64, "bf16", seed=7, ignored=0)
+    x[:, 0], w[:, 0] = 1, 0
+    gone = torch.arange(300, device="cuda") % 3 == 0
+    t = torch.where(t % 3 == 0, (t + 1) % 300, t)
+    kept = (~gone).nonzero()[:, 0]
+    back = torch.full((300,), -1, device="cuda")
+    back[kept] = torch.arange(len(kept), device="cuda")
+    want = Want(x, w[kept].contiguous(), back[t])
+    w[gone, 0] = float("-inf")
+    g, h = (torch.randn(70, device="cuda", generator=torch.Generator(device="cuda").manual_seed(s)) for s in (1, 2))
+    dx, dw = snack.score_grad(x, w, t, snack.score(x, w, t)[4], g, h)
+    assert bool(torch.isnan(dx[:, 0]).all()) and bool((dw[gone] == 0).all())
+    dx[:, 0] = 0  # w's kept entries of the column are 0
+    want.check_grads(dx, dw[kept], g, h)
