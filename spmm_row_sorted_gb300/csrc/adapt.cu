@@ -22,11 +22,11 @@
 // mma.sync, operands as they lie: which columns of a group a lane holds does not
 // matter to a sum as long as both operands agree, so every lane reads 16
 // consecutive bytes of a row.  fp32 operands are cut into three bf16 parts in
-// registers, six part products down to 2^-16 of the leading one, 16 of K on the
-// tensor core at a time: its sums round towards zero.  h and dh are fp32 in memory
-// and go into products as two bf16 parts (bf16 operands: 2^-17 of an entry, far
-// below the output's rounding) or three.  Every sum has one order: results repeat
-// bit for bit.
+// registers, six part products down to 2^-16 of the leading one.  The tensor core's
+// sums round towards zero: 16 of K at a time here, runs of them by tcgen05, are added
+// in fp32.  h and dh are fp32 in memory and go into products as two bf16 parts (bf16
+// operands: 2^-17 of an entry, far below the output's rounding) or three.  Every sum
+// has one order: results repeat bit for bit.
 #include <math.h>
 #include <stdint.h>
 
@@ -84,7 +84,8 @@ int group_warps(int groups, int n) {
 }
 
 // Each warp counts a stretch of the rows by adapter; the counts, added up over
-// adapters and warps, say where its rows go.  8192 rows: see adapt_fwd's figures.
+// adapters and warps, say where its rows go.  8192 rows, 16 adapters: 6 us, a chain of
+// latencies on one SM.
 __global__ void __launch_bounds__(kGroupThreads, 1)
     k_adapt_group(TokenSrc which, int n, int warps, int32_t *__restrict__ order, int32_t *__restrict__ start,
                   Tile *__restrict__ tiles, int tile_cap, int tile_rows) {
@@ -458,13 +459,10 @@ __device__ __forceinline__ void along(const Pack<T, B> &v, int s, uint32_t (&w)[
       cut_pair<3>(v.get(4 * s + 2 * h), v.get(4 * s + 2 * h + 1), w[h]);
   }
 }
-// the pair of elements j of two rows that follow one another along K
-template <typename T, int B>
-__device__ __forceinline__ void across(const Pack<T, B> &a, const Pack<T, B> &b, int j, uint32_t (&w)[Op<T>::kParts]) {
-  if constexpr (sizeof(T) == 2)
-    w[0] = __byte_perm(a.w[j >> 1], b.w[j >> 1], j & 1 ? 0x7632 : 0x5410);
-  else
-    cut_pair<3>(a.get(j), b.get(j), w);
+// the pair of elements j of two rows that follow one another along K; bf16 matrices that lie so go through tcgen05
+template <int B>
+__device__ __forceinline__ void across(const Pack<float, B> &a, const Pack<float, B> &b, int j, uint32_t (&w)[3]) {
+  cut_pair<3>(a.get(j), b.get(j), w);
 }
 
 // ------------------------------------------------------------ h and dh
@@ -586,7 +584,7 @@ __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, i
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) across<T>(v[2 * h], v[2 * h + 1], j, bw[s][j][h]);
+          for (int h = 0; h < 2; ++h) across(v[2 * h], v[2 * h + 1], j, bw[s][j][h]);
       }
 #pragma unroll
       for (int j = 0; j < NT; ++j)
@@ -634,7 +632,7 @@ __device__ __forceinline__ void down_tile(const DownArgs &a, const Tile &tile, i
   if (blocks > 1) cluster_sync();  // no block's memory is read any more
 }
 
-template <typename T, int NT, int kHalves, bool kAlong, bool kWide>
+template <int NT, int kHalves, bool kAlong, bool kWide>
 __global__ void __launch_bounds__(kDownParts * kHalves * 32, 1) k_adapt_down(const DownArgs args, const FileArgs f) {
   pdl_wait();
   extern __shared__ __align__(16) float down_ring[];
@@ -650,9 +648,9 @@ __global__ void __launch_bounds__(kDownParts * kHalves * 32, 1) k_adapt_down(con
   }
   if (tile.adapter < 0 || tile.adapter >= a.adapters) return;  // the whole cluster's
   if (tile.count <= 16)
-    down_tile<T, 1, NT, kHalves, kAlong, kWide>(a, tile, blockIdx.y, down_ring);
+    down_tile<float, 1, NT, kHalves, kAlong, kWide>(a, tile, blockIdx.y, down_ring);
   else
-    down_tile<T, 4, NT, kHalves, kAlong, kWide>(a, tile, blockIdx.y, down_ring);
+    down_tile<float, 4, NT, kHalves, kAlong, kWide>(a, tile, blockIdx.y, down_ring);
 }
 
 // ------------------------------------------------------------ y and dx
@@ -894,7 +892,7 @@ __device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, int s
             along<T>(mv[j], 0, b[j]);
           } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) across<T>(mv[2 * h], mv[2 * h + 1], j, b[j][h]);
+            for (int h = 0; h < 2; ++h) across(mv[2 * h], mv[2 * h + 1], j, b[j][h]);
           }
         }
 #pragma unroll
@@ -976,7 +974,7 @@ __device__ __forceinline__ void up_tile(const UpArgs &a, const Tile &tile, int s
   }
 }
 
-template <typename T, bool kAlong, int kSteps, bool kWide>
+template <bool kAlong, bool kWide>
 __global__ void __launch_bounds__(kUpWarps * 64, 1) k_adapt_up(const UpArgs a) {
   pdl_wait();
   extern __shared__ __align__(16) uint8_t up_ring[];
@@ -985,12 +983,12 @@ __global__ void __launch_bounds__(kUpWarps * 64, 1) k_adapt_up(const UpArgs a) {
   const bool none = tile.adapter >= a.adapters;
   if (none && a.base == a.out) return;
   if constexpr (kWide) {
-    if (!none && tile.count == kTile && a.cols % kUpCols == 0 && a.rank % (16 * kSteps) == 0) {
-      up_tile<T, kAlong, kSteps, true, true>(a, tile, blockIdx.y, up_ring);
+    if (!none && tile.count == kTile && a.cols % kUpCols == 0 && a.rank % 16 == 0) {
+      up_tile<float, kAlong, 1, true, true>(a, tile, blockIdx.y, up_ring);
       return;
     }
   }
-  up_tile<T, kAlong, kSteps, kWide, false>(a, tile, blockIdx.y, up_ring);
+  up_tile<float, kAlong, 1, kWide, false>(a, tile, blockIdx.y, up_ring);
 }
 
 // ------------------------------------------------------------ few rows
@@ -1067,21 +1065,21 @@ constexpr int kOuterWarps = 8;
 constexpr int kOuterRows = 32;    // rows of v in shared memory at a time: two steps of 16
 constexpr int kOuterStages = 4;   // of x, on its way
 __host__ __device__ constexpr int outer_cols(int lane) { return kOuterWarps * 8 * lane; }  // of a block
-template <typename T, int MT>
-constexpr int outer_v_words() { return Op<T>::kOwnParts * 2 * MT * 128; }  // a fragment: 4 words of 32 lanes
-template <typename T, int MT>
+template <int MT>
+constexpr int outer_v_words() { return Op<float>::kOwnParts * 2 * MT * 128; }  // a fragment: 4 words of 32 lanes
+template <int MT>
 constexpr size_t outer_smem() {
-  const size_t ring = (size_t)kOuterWarps * kOuterStages * 8 * 512 + 2 * (size_t)outer_v_words<T, MT>() * 4;
-  const size_t sums = (size_t)16 * MT * (outer_cols(Op<T>::kLane) + 1) * 4;
+  const size_t ring = (size_t)kOuterWarps * kOuterStages * 8 * 512 + 2 * (size_t)outer_v_words<MT>() * 4;
+  const size_t sums = (size_t)16 * MT * (outer_cols(Op<float>::kLane) + 1) * 4;
   return ring > sums ? ring : sums;
 }
 
 // The cluster's sums [kRank][kCols] to the output, this block's share of them.
-template <typename T, int kRank, int kCols, int kThreads>
+template <int kRank, int kCols, int kThreads>
 __device__ __forceinline__ void outer_write(const OuterArgs &a, const float *sums, int pitch, uint32_t block, uint32_t blocks, int adapter,
                                             int r0, int b0, bool empty) {
   const float scale = a.scales ? a.scales[adapter] : 1.f;
-  T *out = reinterpret_cast<T *>(a.out) + (int64_t)adapter * a.rank * a.cols;
+  float *out = reinterpret_cast<float *>(a.out) + (int64_t)adapter * a.rank * a.cols;
   for (int i = (int)block * kThreads + threadIdx.x; i < kCols * kRank; i += (int)blocks * kThreads) {
     int r, c;  // of the block's
     if (a.turned) {
@@ -1099,23 +1097,23 @@ __device__ __forceinline__ void outer_write(const OuterArgs &a, const float *sum
       for (uint32_t b = 1; b < blocks; ++b) s += ld_cluster(at, b);
     }
     // an adapter without rows has no gradient, whatever its scale
-    const float v = empty ? 0.f : s * scale;
-    out[a.turned ? (int64_t)(b0 + c) * a.rank + r0 + r : (int64_t)(r0 + r) * a.cols + b0 + c] = from_f32<T>(v);
+    out[a.turned ? (int64_t)(b0 + c) * a.rank + r0 + r : (int64_t)(r0 + r) * a.cols + b0 + c] = empty ? 0.f : s * scale;
   }
 }
 
 // An adapter's sums over its rows, 32 at a time, for 16 MT of the rank: a warp has 8
 // kLane columns, the cluster's blocks have every so many of the rows.  The block's
 // warps share the rows' v, cut into parts and laid out as mma.sync reads it.
-template <typename T, int MT, bool kWide>
+template <int MT, bool kWide>
 __global__ void __launch_bounds__(kOuterWarps * 32, 1) k_adapt_outer(const OuterPair pair) {
   pdl_wait();
   const uint32_t block = cluster_rank(), blocks = cluster_blocks();
   const int slice = (int)(blockIdx.x / blocks), second = slice >= pair.slices ? 1 : 0;
   const OuterArgs &a = pair.a[second];
+  typedef float T;
   typedef Op<T> O;
   constexpr int NT = O::kLane, kCols = 8 * NT, kRank = 16 * MT, kVp = O::kOwnParts, kThreads = kOuterWarps * 32;
-  constexpr int kVWords = outer_v_words<T, MT>(), kPitch = outer_cols(NT) + 1;
+  constexpr int kVWords = outer_v_words<MT>(), kPitch = outer_cols(NT) + 1;
   extern __shared__ __align__(16) uint32_t outer_ring[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, q = lane & 3;
@@ -1222,7 +1220,7 @@ __global__ void __launch_bounds__(kOuterWarps * 32, 1) k_adapt_outer(const Outer
         for (int j = 0; j < NT; ++j) {
           uint32_t b[2][O::kParts];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) across<T>(xv[2 * k], xv[2 * k + 1], j, b[k]);
+          for (int k = 0; k < 2; ++k) across(xv[2 * k], xv[2 * k + 1], j, b[k]);
           mma_all<MT, kVp, O::kParts>([&](int m) -> float(&)[4] { return acc[m][j]; },
                                       [&](int m) -> const uint32_t(&)[2][2][kVp] { return w[m]; },
                                       [&](int) -> const uint32_t(&)[2][O::kParts] { return b; });
@@ -1245,7 +1243,7 @@ __global__ void __launch_bounds__(kOuterWarps * 32, 1) k_adapt_outer(const Outer
     cluster_sync();
   else
     __syncthreads();
-  outer_write<T, kRank, outer_cols(NT), kThreads>(a, sums, kPitch, block, blocks, adapter, r0, b0, first == end);
+  outer_write<kRank, outer_cols(NT), kThreads>(a, sums, kPitch, block, blocks, adapter, r0, b0, first == end);
   if (blocks > 1) cluster_sync();
 }
 
@@ -1306,15 +1304,15 @@ unsigned cluster_for(int64_t blocks, int64_t shares, int sms) {
 namespace snack {
 namespace {
 
-template <typename T, int NT, int kHalves, bool kAlong, bool kWide>
+template <int NT, int kHalves, bool kAlong, bool kWide>
 cudaError_t launch_down(const DownArgs &a, const FileArgs &f, int64_t n, int tile_cap, int sms, cudaStream_t s) {
   constexpr int kCols = 8 * NT * kHalves;
   const size_t smem = down_smem(kCols);
-  const auto kernel = k_adapt_down<T, NT, kHalves, kAlong, kWide>;
+  const auto kernel = k_adapt_down<NT, kHalves, kAlong, kWide>;
   cudaError_t e = raise_smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
   const unsigned slices = (unsigned)ceil_div(a.rank, kCols);
-  const unsigned c = cluster_for(likely_tiles(n, a.adapters, kTile) * slices, ceil_div(a.k, Op<T>::kGroup * kDownParts), sms);
+  const unsigned c = cluster_for(likely_tiles(n, a.adapters, kTile) * slices, ceil_div(a.k, Op<float>::kGroup * kDownParts), sms);
   return launch_cluster(c, kernel, dim3((unsigned)tile_cap * c, slices), kDownParts * kHalves * 32, smem, s, a, f);
 }
 // whole accesses of 16 bytes of the rows and of a matrix that runs along K, of `across` elements of one that does not
@@ -1325,23 +1323,23 @@ bool down_wide(DownArgs *a, int across) {
   a->m_wide = kAlong ? row_wide(a->m, a->k, es) : ptr_aligned(a->m, across * es) && a->rank % across == 0;
   return a->x_wide && a->m_wide;
 }
-template <typename T, int NT, int kHalves, bool kAlong>
+template <int NT, int kHalves, bool kAlong>
 cudaError_t down_by(DownArgs a, const FileArgs &f, int64_t n, int tile_cap, int sms, cudaStream_t s) {
-  return down_wide<T, kAlong>(&a, NT) ? launch_down<T, NT, kHalves, kAlong, true>(a, f, n, tile_cap, sms, s)
-                                      : launch_down<T, NT, kHalves, kAlong, false>(a, f, n, tile_cap, sms, s);
+  return down_wide<float, kAlong>(&a, NT) ? launch_down<NT, kHalves, kAlong, true>(a, f, n, tile_cap, sms, s)
+                                          : launch_down<NT, kHalves, kAlong, false>(a, f, n, tile_cap, sms, s);
 }
 template <typename T, bool kAlong>
 cudaError_t down(const DownArgs &a, const FileArgs &f, int64_t n, int tile_cap, int sms, cudaStream_t s) {
   if constexpr (sizeof(T) == 2)
     return down_tc<kAlong>(a, f, likely_tiles(n, a.adapters, kTcTile), tile_cap, sms, s);
   else
-    return a.rank <= 16 ? down_by<T, 2, 1, kAlong>(a, f, n, tile_cap, sms, s) : down_by<T, 2, 2, kAlong>(a, f, n, tile_cap, sms, s);
+    return a.rank <= 16 ? down_by<2, 1, kAlong>(a, f, n, tile_cap, sms, s) : down_by<2, 2, kAlong>(a, f, n, tile_cap, sms, s);
 }
 
-template <typename T, bool kAlong, int kSteps, bool kWide>
+template <bool kAlong, bool kWide>
 cudaError_t launch_up(UpArgs a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
-  const size_t smem = (size_t)kUpWarps * up_stages<T>() * up_stage_bytes<T, kSteps>() * 32 + up_h_bytes<T>(a.rank);
-  const auto kernel = k_adapt_up<T, kAlong, kSteps, kWide>;
+  const size_t smem = (size_t)kUpWarps * up_stages<float>() * up_stage_bytes<float, 1>() * 32 + up_h_bytes<float>(a.rank);
+  const auto kernel = k_adapt_up<kAlong, kWide>;
   cudaError_t e = raise_smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
   const int64_t all = ceil_div(a.cols, kUpWarps * kUpCols);
@@ -1359,16 +1357,16 @@ bool up_wide(UpArgs *a) {
   a->m_wide = ptr_aligned(a->m, 4 * es) && (kAlong ? a->rank : a->cols) % 4 == 0;
   return row_wide(a->base, a->base_ld, es) && row_wide(a->out, a->out_ld, es) && a->m_wide;
 }
-template <typename T, bool kAlong, int kSteps>
+template <bool kAlong>
 cudaError_t up_by(UpArgs a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
-  return up_wide<T, kAlong>(&a) ? launch_up<T, kAlong, kSteps, true>(a, n, tile_cap, sms, s) : launch_up<T, kAlong, kSteps, false>(a, n, tile_cap, sms, s);
+  return up_wide<float, kAlong>(&a) ? launch_up<kAlong, true>(a, n, tile_cap, sms, s) : launch_up<kAlong, false>(a, n, tile_cap, sms, s);
 }
 template <typename T, bool kAlong>
 cudaError_t up(const UpArgs &a, int64_t n, int tile_cap, int sms, cudaStream_t s) {
   if constexpr (sizeof(T) == 2)
     return up_tc<kAlong>(a, tile_cap, sms, s);
   else
-    return up_by<T, kAlong, 1>(a, n, tile_cap, sms, s);
+    return up_by<kAlong>(a, n, tile_cap, sms, s);
 }
 
 template <typename T, int NT, int kSteps, bool kWide>
@@ -1391,13 +1389,13 @@ cudaError_t few(DownArgs d, UpArgs u, const TokenSrc &which, int n, int sms, cud
   return wide ? launch_few<T, 2, kSteps, true>(d, u, which, n, sms, s) : launch_few<T, 2, kSteps, false>(d, u, which, n, sms, s);
 }
 
-template <typename T, int MT, bool kWide>
+template <int MT, bool kWide>
 cudaError_t launch_outer(OuterPair p, int64_t n, int32_t adapters, int sms, cudaStream_t s) {
-  const size_t smem = outer_smem<T, MT>();
-  const auto kernel = k_adapt_outer<T, MT, kWide>;
+  const size_t smem = outer_smem<MT>();
+  const auto kernel = k_adapt_outer<MT, kWide>;
   cudaError_t e = raise_smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
-  constexpr int kCols = outer_cols(Op<T>::kLane);
+  constexpr int kCols = outer_cols(Op<float>::kLane);
   p.slices = p.a[0].out ? (int32_t)ceil_div(p.a[0].cols, kCols) : 0;
   const int64_t slices = p.slices + (p.a[1].out ? ceil_div(p.a[1].cols, kCols) : 0);
   const int32_t rank = p.a[p.slices ? 0 : 1].rank;
@@ -1414,9 +1412,9 @@ cudaError_t outer(const OuterPair &p, int32_t rank, int64_t n, int32_t adapters,
     if (rank <= 32) return wide ? launch_outer_tc<32, true>(p, n, adapters, sms, s) : launch_outer_tc<32, false>(p, n, adapters, sms, s);
     return wide ? launch_outer_tc<64, true>(p, n, adapters, sms, s) : launch_outer_tc<64, false>(p, n, adapters, sms, s);
   } else {
-    if (rank <= 16) return wide ? launch_outer<T, 1, true>(p, n, adapters, sms, s) : launch_outer<T, 1, false>(p, n, adapters, sms, s);
-    if (rank <= 32) return wide ? launch_outer<T, 2, true>(p, n, adapters, sms, s) : launch_outer<T, 2, false>(p, n, adapters, sms, s);
-    return wide ? launch_outer<T, 4, true>(p, n, adapters, sms, s) : launch_outer<T, 4, false>(p, n, adapters, sms, s);
+    if (rank <= 16) return wide ? launch_outer<1, true>(p, n, adapters, sms, s) : launch_outer<1, false>(p, n, adapters, sms, s);
+    if (rank <= 32) return wide ? launch_outer<2, true>(p, n, adapters, sms, s) : launch_outer<2, false>(p, n, adapters, sms, s);
+    return wide ? launch_outer<4, true>(p, n, adapters, sms, s) : launch_outer<4, false>(p, n, adapters, sms, s);
   }
 }
 
