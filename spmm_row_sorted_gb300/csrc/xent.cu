@@ -1515,7 +1515,10 @@ XentShape xent_shape(const void *x, int64_t x_ld, int32_t n, const void *wt, int
 // of the reads: 1024 x 16384 x 768, 5 us of 92).  What is rounded to bf16 (dz, dx
 // and dw of bf16 operands) is far below half its ulp with long ones; dz at the
 // target, p - 1, is not, and does not come from them: one accumulator over 4096 of K
-// would make it wrong by 2e-4 at logits of 40, where 1 - p was 2e-3.
+// would make it wrong by 2e-4 at logits of 40, where 1 - p was 2e-3.  The entropy's
+// gradient has log p + H, which is small where the logits are alike: there dz takes the
+// units of the statistics, whose error is then common to both (1021 x 50001 x 1000 370
+// and 374 us, 4096 x 131072 x 2048 5420 and 5545).
 // Measured, relative error of logits of 40 (width 4096) on average, and the loss of
 // 2048 x 65536 x 4096 bf16 and of 67 x 119598 x 2176 fp32, us:
 //   unit   random    positive  nine of ten zero    bf16   fp32
@@ -1533,7 +1536,8 @@ cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtens
     else
       return k_xent<kMode>;
   }();
-  constexpr bool kLogits = kMode == kStats || kMode == kScore;
+  // the entropy's gradient has what a logit is above the row's mean: its logits have to be the statistics' own, to the bit
+  const bool logits = kMode == kStats || kMode == kScore || (kMode == kDlog && g.ent.weight);
   cudaError_t e = raise_smem_limit(kernel, kSmem);
   if (e != cudaSuccess) return e;
   // the register split draws on what the launch gives: a kernel built with fewer would wait for ever
@@ -1545,7 +1549,7 @@ cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtens
   if (!enough) return cudaErrorInvalidDeviceFunction;
   g.m_tiles = (int32_t)ceil_div(g.m, kM);
   g.n_tiles = (int32_t)ceil_div(g.n, g.nt);
-  g.unit = unit_of((int)ceil_div(g.k_blocks, g.n_split), g.products > 1 ? (kLogits ? 4 : 8) : kLogits ? 8 : 64);
+  g.unit = unit_of((int)ceil_div(g.k_blocks, g.n_split), g.products > 1 ? (logits ? 4 : 8) : logits ? 8 : 64);
   g.a_rows = kMode == kDw || g.m >= kMCta ? kMCta : (int32_t)align_up((size_t)g.m, 8);
   g.stages = kRing / ((g.a_rows + g.nt / 2) * kKb * 2);
   if (g.stages > kMaxStages) g.stages = kMaxStages;

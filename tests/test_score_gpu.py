@@ -444,3 +444,25 @@ def test_gradients_where_logits_are_the_lowest():
     assert bool(torch.isnan(dx[:, 0]).all()) and bool((dw[gone] == 0).all())
     dx[:, 0] = 0  # w's kept entries of the column are 0
     want.check_grads(dx, dw[kept], g, h)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [3, 12, 30, 130, 300])
+def test_the_entropy_s_gradient_adds_up_to_nothing(n, dtype):
+    """sum_v dz = -sum_v p (log p + H) = 0: dx in a column where every token has 1.  Logits near 640 that differ by 0.2: what
+    log p + H is off by is common to all of a row, so logits that the gradient sums in another way than the statistics did (off
+    by 10^-7 of themselves for each truncated addition) would show.  What may be left: the roundings of lse and H (2^-24 of each),
+    H's own error (2^-17 of its two parts), dz's (2^-8 of each entry, or 2^-22) and dx's."""
+    vocab, width = 8192, 4096
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    x = (torch.rand(n, width, device="cuda", generator=gen) + 0.5) * 0.4
+    w = (0.75 + 0.5 * torch.rand(1, width, device="cuda", generator=gen)) * 0.4 + torch.randn(vocab, width, device="cuda", generator=gen) * 0.008
+    x[:, 0], w[:, 0] = 0, 1
+    x, w = x.to(DTYPES[dtype]), w.to(DTYPES[dtype])
+    state = snack.score(x, w)[4]
+    dx = snack.score_grad(x, w, None, state, dentropy=torch.ones(n, device="cuda"), want_dw=False)[0]
+    want = Want(x, w, None)
+    size = (want.p * (want.log_p + want.H[:, None]).abs()).sum(1)
+    tol = 2.0 ** -24 * (want.lse + want.H) + 2.0 ** -17 * 2 * (1 + want.H) + size * (2.0 ** -8 if dtype == "bf16" else 2.0 ** -22)
+    assert float(want.lse.min()) > 400 and 0.05 < float(size.mean()) < 0.5
+    assert bool((dx[:, 0].abs().double() <= tol * (1 + HALF_ULP[dx.dtype])).all()), float((dx[:, 0].abs().double() / tol).max())
