@@ -448,15 +448,17 @@ snack_status snack_xent_bwd(const void *x, int64_t x_ld, int32_t n, const void *
  * row that is not scored: its results are 0, and its ids -1, whatever its row of x
  * holds.  targets may be NULL: then every row is scored, and logp has to be NULL.
  * logp, entropy (n values each), and top_ids and top_logp (n * top) where top is 0,
- * may be NULL.  0 <= top <= 24 (SNACK_ERR_UNSUPPORTED above) and top <= vocab.  Logits
- * are formed as the loss's are, within 10^-5 of the sum of their terms' magnitudes; where
- * neighbours in the order of the likeliest tokens are too close for that, however their
- * terms cancel, their products are summed again in about twice fp32's precision (so the
- * order is that of the exact logits unless more than eight beyond the
- * last one asked for are that close to it).  A row with a NaN or an infinite largest
- * logit has NaN results; its ids are some of the vocabulary.  state (2 n values: each
- * row's lse and entropy) is kept for the gradient.  With top the workspace holds up to
- * a gigabyte of logits at a time (1024 columns at least); the other sizes are as for
+ * may be NULL.  0 <= top <= 24 (SNACK_ERR_UNSUPPORTED above: a warp ranks 32, eight
+ * more than are asked for) and top <= vocab.  Logits are formed as the loss's are, within
+ * 10^-5 of the sum of their terms' magnitudes; where neighbours in the order of the
+ * likeliest tokens are too close for that, however their terms cancel, their products are
+ * summed again in about twice fp32's precision (so the order is that of the exact logits
+ * unless more than eight beyond the last one asked for are that close to it).  A row with
+ * a NaN or an infinite largest logit has NaN results; its ids are some of the vocabulary.
+ * state (2 n values: each row's lse and entropy) is kept for the gradient.  With top the
+ * workspace holds up to
+ * a gigabyte of logits at a time (1024 columns at least), and 16 bytes per row and some
+ * hundred columns for the statistics, twice the loss's; the other sizes are as for
  * snack_xent_workspace_size.
  */
 snack_status snack_score_workspace_size(const void *x, int64_t x_ld, int32_t n, const void *w, int64_t w_ld,

@@ -1,9 +1,10 @@
-// The adapters' products on the fifth generation tensor cores (bf16 whose rows lie on
-// 16 bytes).  Included by adapt.cu.
+// The adapters' products of bf16 on the fifth generation tensor cores; few rows are
+// k_adapt_few's.  Included by adapt.cu.
 //
-// Operands are gathered row by row with cp.async into tiles with the 128-byte swizzle,
-// the fp32 one cut into two bf16 parts on its way; one thread issues tcgen05.mma, the
-// sums stay in tensor memory until the block's share of K is done.
+// Operands are gathered row by row into tiles with the 128-byte swizzle, by cp.async, or
+// where they lie on no such access as the aligned pieces that hold them, shifted; the fp32
+// one is cut into two bf16 parts on its way.  One thread issues tcgen05.mma.  The sums stay
+// in tensor memory for a run of steps, whose sums are added in fp32 where there are several.
 #pragma once
 
 namespace snack {
