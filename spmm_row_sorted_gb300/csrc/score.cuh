@@ -30,7 +30,8 @@ namespace {
 constexpr int kMostTop = 24;
 constexpr int kKeepMore = 8;
 // of a block: four warps, or where the rows are few four for the likeliest tokens, four for the statistics beside them, one
-// for the target's logit and as many for what is summed again
+// for the target's logit, and all 32 for what is summed again (8 rows of 32768, 20 tokens: the call 38.3 us, 40.4 with 17 warps;
+// 2048 rows of 65536, 8 tokens: blocks of eight warps 841 us where those of four took 834)
 constexpr int kTopWarps = 4, kTopThreads = kTopWarps * 32;
 constexpr int kFinishThreads = 1024;
 constexpr int kFoundFew = 256;  // keys that are ranked by counting
